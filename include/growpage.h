@@ -374,9 +374,90 @@ gp_status gp_decode_attention(gp_ctx* ctx, int32_t layer, int32_t n, const gp_re
                               const int32_t* num_tokens, const void* q_dev, const uint8_t* first_dev,
                               float* out_dev);
 
+/* ---- eviction by accumulated attention weight ---------------------------------
+ * The common alternative to the demand estimate: keep the tokens that received
+ * the most attention so far, and a recent window.  Four calls carry it from
+ * the prompt on: gp_append_tokens writes new tokens, gp_chunk_attention (a
+ * prompt, or a few drafted tokens) and gp_decode_attention_weighted (one token)
+ * attend and add the weights they give, gp_evict_weighted evicts by them.
+ *
+ * Accumulated weights ("weights_dev"): device fp32
+ * [L][max_slots][Hkv][max_pages_per_req * 256], owned by the caller, 4-byte
+ * aligned, indexed by request slot and logical token -- not by page, so
+ * requests that share prefix pages gather weights of their own.  Entry i of
+ * (layer, slot, h) is the sum over the queries so far of the softmax weights
+ * of token i, summed over the query heads of KV head h.  gp_append_tokens
+ * clears the entries of the tokens it writes, so the array needs no clearing
+ * of its own; entries past a request's tokens are never read or written.
+ * The sums are fp32, each entry has one writer per call and a fixed order:
+ * the same calls give the same bits.
+ *
+ * The calls share these rules.  Requests need a bound slot, listed once per
+ * call.  Arguments are checked before anything happens (GP_ERR_INVALID,
+ * nothing changed).  The device current at gp_create must be current
+ * (GP_ERR_INVALID), and the engine stream must not be capturing a graph
+ * (GP_ERR_UNSUPPORTED: a replay would not see a later call's tables and
+ * lengths).  They run on the engine stream, asynchronously, and wait there
+ * for a pending side-stream compaction only if a request holds one of its
+ * pages.  Two contexts share no scratch and may run at the same time.
+ *
+ * gp_append_tokens: new tokens of one layer into the cache.  Request r appends
+ * num_new[r] >= 0 tokens after its num_cached[r] >= 0 cached ones; the rows of
+ * q, k and v are packed, request after request.  Token t goes to logical slot
+ * num_cached[r] + t of the request's pages with its key rotated (rotate-half
+ * RoPE at position reqs[r].pos + t, rope_theta; angles in fp64, one rounding
+ * to kv_dtype) and its value copied; q_rot gets the rotated queries, rounded
+ * to q_dtype, as gp_chunk_attention takes them.  q_dev, q_rot_dev: device
+ * [rows][Hq][d] q_dtype, both or neither NULL, may be the same buffer;
+ * k_dev, v_dev: device [rows][Hkv][d] kv_dtype; weights_dev may be NULL.
+ * All but weights_dev 16-byte aligned, as the caches.  num_cached and num_new:
+ * HOST int32 [n]; the tokens must fit the request's pages, and a page written
+ * must have one reference and be written by one request of the call
+ * (GP_ERR_INVALID: copy a shared page first).  A gp_boundary_demand result of
+ * the slots is stale afterwards (GP_ERR_STATE in gp_compress_hold). */
+gp_status gp_append_tokens(gp_ctx* ctx, int32_t layer, int32_t n, const gp_request* reqs,
+                           const int32_t* num_cached, const int32_t* num_new, const void* q_dev,
+                           const void* k_dev, const void* v_dev, void* q_rot_dev, float* weights_dev);
+
+/* gp_decode_attention_weighted: gp_decode_attention (same arguments, same
+ * outputs) that also adds its softmax weights: entry i
+ * < num_tokens[r] of (layer, slot, h) grows by the sum over the G query heads
+ * of a_i.  first_dev may be NULL: the summaries are then left as they are. */
+gp_status gp_decode_attention_weighted(gp_ctx* ctx, int32_t layer, int32_t n, const gp_request* reqs,
+                                       const int32_t* num_tokens, const void* q_dev, const uint8_t* first_dev,
+                                       float* out_dev, float* weights_dev);
+
+/* gp_chunk_attention: causal attention of one layer for num_new[r] >= 0 tokens
+ * of each request that are already in the cache behind num_cached[r] others
+ * (gp_append_tokens): token t attends to the logical slots
+ * [0, num_cached[r] + t + 1), z = q . k / sqrt(d), a = softmax(z),
+ * out = sum a v.  q_dev: device [rows][Hq][d] q_dtype, ROTATED, packed as in
+ * gp_append_tokens; out_dev: the same shape and type; both 16-byte aligned.
+ * With weights_dev, the weights of every token are added; NULL leaves that
+ * out.  The rows of K and V of the attended tokens must be finite; cache slots
+ * past num_cached[r] + num_new[r] may hold any bits. */
+gp_status gp_chunk_attention(gp_ctx* ctx, int32_t layer, int32_t n, const gp_request* reqs,
+                             const int32_t* num_cached, const int32_t* num_new, const void* q_dev,
+                             void* out_dev, float* weights_dev);
+
+/* gp_evict_weighted: evict request r's num_tokens[r] tokens down to
+ * keep_tokens[r] >= 1, per (layer, KV head): the min(recent_window, keep) most
+ * recent tokens stay, and of the others the keep - that many of largest
+ * accumulated weight (equal weights: the lower slot; NaN counts as larger than
+ * any number).  K, V and the weights of the kept tokens move, in order, to
+ * the logical slots [0, keep); num_pages is unchanged and the slots from keep
+ * on become free, their contents unspecified.  A request with num_tokens <=
+ * keep_tokens is left as it is.  Copy-on-write as in gp_compress_hold for the
+ * requests that evict (GP_ERR_NO_PAGES: nothing changed).  num_tokens and
+ * keep_tokens: HOST int32 [n].  Runs on the compaction stream if one is set,
+ * with gp_compress_hold's rules; a gp_boundary_demand result of the slots is
+ * stale afterwards.  gp_debug_keep_mask gives the kept sets. */
+gp_status gp_evict_weighted(gp_ctx* ctx, int32_t n, gp_request* reqs, const int32_t* num_tokens,
+                            const int32_t* keep_tokens, float* weights_dev);
+
 /* ---- asynchronous compaction (App. E.3: compaction overlapped with decoding)
  * gp_set_compaction_stream: from now on the compaction of gp_compress_hold,
- * gp_shrink, gp_compress_fill and gp_compact_kv runs on `stream` (a caller
+ * gp_shrink, gp_compress_fill, gp_compact_kv and gp_evict_weighted runs on `stream` (a caller
  * CUDA stream; NULL: the engine stream again).  Each such call makes the
  * side stream wait for the work the engine stream holds at that point, then
  * returns without waiting for the compaction; the block tables and the page
@@ -401,7 +482,7 @@ gp_status gp_wait_compaction(gp_ctx* ctx, void* stream);
 /* ---- inspection (tests, benchmarks) ---------------------------------------
  * All of these synchronise the stream.  req_idx indexes the request list of
  * the last gp_boundary_demand (k, probabilities, scores) or of the last
- * gp_compress_hold (keep masks). */
+ * gp_compress_hold or gp_evict_weighted (keep masks). */
 
 /* K^S, K^L per unit: k_out host int32[L * Hkv * 2] ([unit][x]). */
 gp_status gp_debug_demand_k(gp_ctx* ctx, int32_t req_idx, int32_t* k_out);
@@ -443,7 +524,8 @@ gp_status gp_debug_attention_plan(gp_ctx* ctx, int32_t n, const int32_t* num_tok
 /* ---- test hooks -------------------------------------------------------------
  * gp_debug_set_wait_limit: the limit, in SM clock cycles, of the bounded copy
  * waits of later launches of `kernel` (GP_KERNEL_COMPRESS: the compaction;
- * GP_KERNEL_SELECT: the speculative selection); 0 makes each such wait give
+ * GP_KERNEL_SELECT: the speculative selection; GP_KERNEL_EVICT: the eviction's
+ * waits for rows still to be read); 0 makes each such wait give
  * up at once, a negative value restores the default of 2^31 (about one
  * second).  A wait that gives up makes its CTA wait for the copies it already
  * issued (always with the default limit), record a timeout and return;
@@ -495,7 +577,12 @@ gp_status gp_set_selection_mode(gp_ctx* ctx, int32_t mode);
 #define GP_KERNEL_ATTENTION 4
 #define GP_KERNEL_SELECT 5
 #define GP_KERNEL_ENTROPY 6
-#define GP_KERNEL_COUNT 7
+#define GP_KERNEL_APPEND 7
+#define GP_KERNEL_CHUNK 8
+#define GP_KERNEL_WEIGHTS 9        /* the weights of a decode step or a chunk */
+#define GP_KERNEL_EVICT_SELECT 10
+#define GP_KERNEL_EVICT 11
+#define GP_KERNEL_COUNT 12
 gp_status gp_set_timing(gp_ctx* ctx, int32_t enabled);
 gp_status gp_kernel_time(gp_ctx* ctx, int32_t kernel, double* ms, int64_t* launches);
 gp_status gp_reset_timing(gp_ctx* ctx);

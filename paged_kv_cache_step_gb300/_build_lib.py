@@ -19,7 +19,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libgrowpage.so")
 
 SOURCES = ["growpage.cpp", "k_summaries.cu", "k_demand.cu", "k_demand_tc.cu", "k_compress.cu", "k_attention.cu",
-           "k_attention_tc.cu", "k_entropy.cu", "noalloc.cu"]
+           "k_attention_tc.cu", "k_entropy.cu", "noalloc.cu", "weighted.cpp", "k_append.cu", "k_weights.cu", "k_chunk.cu",
+           "k_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -41,7 +42,8 @@ def _stale(obj: str, src: str) -> bool:
     t = os.path.getmtime(obj)
     deps = [src, os.path.join(CSRC, "gp_kernels.h"), os.path.join(CSRC, "gp_internal.h"),
             os.path.join(CSRC, "demand_common.cuh"), os.path.join(CSRC, "engine.h"),
-            os.path.join(CSRC, "attn_kernels.h"), os.path.join(CSRC, "tc_ptx.cuh"), os.path.join(INCLUDE, "growpage.h")]
+            os.path.join(CSRC, "attn_kernels.h"), os.path.join(CSRC, "tc_ptx.cuh"),
+            os.path.join(CSRC, "weighted_kernels.h"), os.path.join(INCLUDE, "growpage.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -31,8 +31,10 @@ GP_SCAN_AUTO, GP_SCAN_CUDA_CORE, GP_SCAN_TENSOR_CORE = 0, 1, 2
 GP_SELECT_AUTO, GP_SELECT_SPECULATIVE, GP_SELECT_IN_COMPACTION = 0, 1, 2
 GP_KERNEL_EMA, GP_KERNEL_PREP, GP_KERNEL_DEMAND, GP_KERNEL_COMPRESS, GP_KERNEL_ATTENTION = 0, 1, 2, 3, 4
 GP_KERNEL_SELECT, GP_KERNEL_ENTROPY = 5, 6
+GP_KERNEL_APPEND, GP_KERNEL_CHUNK, GP_KERNEL_WEIGHTS, GP_KERNEL_EVICT_SELECT, GP_KERNEL_EVICT = 7, 8, 9, 10, 11
 KERNEL_NAMES = {0: "ema_update", 1: "prep_queries", 2: "boundary_demand", 3: "compress_hold",
-                4: "decode_attention", 5: "select", 6: "entropy"}
+                4: "decode_attention", 5: "select", 6: "entropy", 7: "append_tokens", 8: "chunk_attention",
+                9: "weights", 10: "evict_select", 11: "evict_move"}
 
 EXPORTS = [
     "gp_config_default", "gp_create", "gp_destroy", "gp_last_error", "gp_status_string",
@@ -46,6 +48,7 @@ EXPORTS = [
     "gp_debug_attention_plan",
     "gp_set_compaction_stream", "gp_wait_compaction", "gp_decode_attention",
     "gp_synchronize", "gp_debug_set_wait_limit", "gp_debug_fail_next_launch", "gp_set_selection_mode",
+    "gp_append_tokens", "gp_decode_attention_weighted", "gp_chunk_attention", "gp_evict_weighted",
 ]
 
 
@@ -152,6 +155,10 @@ def load(build_if_missing: bool = True):
         "gp_debug_set_wait_limit": (I32, [P, I32, I64]),
         "gp_debug_fail_next_launch": (I32, [P, I32]),
         "gp_set_selection_mode": (I32, [P, I32]),
+        "gp_append_tokens": (I32, [P, I32, I32, C.POINTER(GpRequest), P, P, P, P, P, P, P]),
+        "gp_decode_attention_weighted": (I32, [P, I32, I32, C.POINTER(GpRequest), P, P, P, P, P]),
+        "gp_chunk_attention": (I32, [P, I32, I32, C.POINTER(GpRequest), P, P, P, P, P]),
+        "gp_evict_weighted": (I32, [P, I32, C.POINTER(GpRequest), P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -401,6 +408,54 @@ def gp_decode_attention(ctx, layer: int, reqs, num_tokens, q_dev, first_dev, out
     nt = np.ascontiguousarray(np.asarray(num_tokens, dtype=np.int32))
     _check(ctx, load().gp_decode_attention(ctx, layer, len(reqs), arr, nt.ctypes.data, _ptr(q_dev),
                                            _ptr(first_dev), _ptr(out_dev)))
+
+
+def _counts(reqs, *lists):
+    """Host int32 arrays of per-request counts, one entry a request."""
+    out = []
+    for x in lists:
+        a = np.ascontiguousarray(np.asarray(x, dtype=np.int32))
+        if a.shape != (len(reqs),):
+            raise GrowPageError(GP_ERR_INVALID, f"{len(reqs)} requests, counts of shape {a.shape}")
+        out.append(a)
+    return out
+
+
+def gp_append_tokens(ctx, layer: int, reqs, num_cached, num_new, q_dev, k_dev, v_dev, q_rot_dev, weights_dev=None):
+    """New tokens of one layer into the cache: rotated keys, values, rotated
+    queries, cleared weights.  num_cached, num_new: host int32 per request;
+    q_dev, q_rot_dev [rows][Hq][d] (both None: keys and values alone);
+    k_dev, v_dev [rows][Hkv][d], rows packed request after request."""
+    nc, nn = _counts(reqs, num_cached, num_new)
+    _check(ctx, load().gp_append_tokens(ctx, layer, len(reqs), _marshal(reqs), nc.ctypes.data, nn.ctypes.data,
+                                        _ptr(q_dev), _ptr(k_dev), _ptr(v_dev), _ptr(q_rot_dev), _ptr(weights_dev)))
+
+
+def gp_decode_attention_weighted(ctx, layer: int, reqs, num_tokens, q_dev, first_dev, out_dev, weights_dev):
+    """gp_decode_attention that adds its softmax weights to weights_dev
+    (fp32 [L][max_slots][Hkv][max_pages_per_req * 256]); first_dev may be None."""
+    nt, = _counts(reqs, num_tokens)
+    _check(ctx, load().gp_decode_attention_weighted(ctx, layer, len(reqs), _marshal(reqs), nt.ctypes.data,
+                                                    _ptr(q_dev), _ptr(first_dev), _ptr(out_dev), _ptr(weights_dev)))
+
+
+def gp_chunk_attention(ctx, layer: int, reqs, num_cached, num_new, q_dev, out_dev, weights_dev=None):
+    """Causal attention of each request's num_new last tokens over its cache;
+    q_dev (rotated) and out_dev [rows][Hq][d] of q_dtype, packed."""
+    nc, nn = _counts(reqs, num_cached, num_new)
+    _check(ctx, load().gp_chunk_attention(ctx, layer, len(reqs), _marshal(reqs), nc.ctypes.data, nn.ctypes.data,
+                                          _ptr(q_dev), _ptr(out_dev), _ptr(weights_dev)))
+
+
+def gp_evict_weighted(ctx, reqs, num_tokens, keep_tokens, weights_dev):
+    """Keep each request's recent window and its tokens of most accumulated
+    weight, keep_tokens in all, per (layer, KV head); K, V and weights are
+    compacted in order.  Rewrites the requests' tables (copy-on-write)."""
+    nt, nk = _counts(reqs, num_tokens, keep_tokens)
+    arr = _marshal(reqs)
+    st = load().gp_evict_weighted(ctx, len(reqs), arr, nt.ctypes.data, nk.ctypes.data, _ptr(weights_dev))
+    _unmarshal(arr, reqs)
+    _check(ctx, st)
 
 
 def gp_compact_kv(ctx, reqs, keep_masks_dev):

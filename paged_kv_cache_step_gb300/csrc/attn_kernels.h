@@ -35,7 +35,8 @@ struct AttnArgs {
   const int32_t* ntok;     // [n] cached tokens attended to
   const void* q;           // [n][Hq][D] pre-RoPE query of this layer
   int q_f32;
-  const uint8_t* first;    // [n] 1: the slot's first step (summaries initialised)
+  const uint8_t* first;    // [n] 1: the slot's first step (summaries initialised);
+                           // null: the summaries are left as they are
   double* pool;            // summary pool [L][M][2][Hq][D]
   double beta_s, beta_l;
   const double* inv_freq;  // [D/2]
@@ -53,6 +54,12 @@ struct AttnArgs {
   const int32_t* cta_begin;//   [cta_begin[c], cta_begin[c + 1]) ([grid + 1]); a pair's
                            //   items are consecutive, its partials part_first + split
   int* err;
+  // for the accumulated weights (all null otherwise): the base-2 logits of the
+  // attended tokens, those of request r at logit_off[r], [Hkv][pages * 256][G],
+  // and the softmax's (maximum, 1 / sum) per (request, query head)
+  float* logits;
+  const int64_t* logit_off;
+  float2* stat;
 };
 cudaError_t launch_decode_attention(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_decode_attention_tc(const AttnArgs& a, cudaStream_t s);

@@ -48,6 +48,16 @@ struct CompressRec {
   int64_t mask_off = 0;
 };
 
+// A call's descriptors on their way to the device: pinned memory, its device
+// mirror, and the event after which both may be written again.
+struct StagingSlot {
+  void* pinned = nullptr;
+  size_t pinned_cap = 0;
+  DevBuf dev;
+  cudaEvent_t free = nullptr;
+};
+constexpr int kStagingSlots = 8;
+
 struct TimedEvent {
   int kernel;
   cudaEvent_t start, stop;
@@ -79,6 +89,12 @@ struct gp_ctx {
   int* err_dev = nullptr;          // kernel error bits
   unsigned long long* moved_dev = nullptr;
   gp::DevBuf upload, bt2, qt, bq, scores, aval, tickets, kout, ksum, masks, xstat, attn, spec_masks, ent;
+  // the accumulated-weight operators: descriptor staging (calls in turn, so
+  // that a call waits on the host only for the one kStagingSlots before it) and scratch
+  gp::StagingSlot staging[gp::kStagingSlots];
+  int staging_next = 0;
+  gp::DevBuf logits, wstat, evict;
+  int device = 0;                  // the device current at gp_create
   gp::DevBuf upload_attn;              // decode attention's own descriptors (it may overlap a compaction)
   // speculative selection: the Eq. 10 keep masks of every request of the last
   // demand call, computed on an engine-owned stream while the host decides
@@ -120,6 +136,7 @@ struct gp_ctx {
   // and a launch to fail without running (-1: none)
   long long wait_limit_select = gp::kDefaultWaitLimit;
   long long wait_limit_compress = gp::kDefaultWaitLimit;
+  long long wait_limit_evict = gp::kDefaultWaitLimit;
   int inject_fail = -1;
 };
 
@@ -253,6 +270,62 @@ inline gp_status need_device(gp_ctx* c) {
   return GP_OK;
 }
 
+// What the accumulated-weight operators check first: their descriptors are
+// host data of the call, which a graph's replay would not see again, and their
+// launches go to the current device.
+inline gp_status ready_call(gp_ctx* c) {
+  gp_status st = need_device(c);
+  if (st != GP_OK) return st;
+  int dev = -1;
+  GP_CUDA(c, cudaGetDevice(&dev));
+  if (dev != c->device)
+    return fail(c, GP_ERR_INVALID, "device %d is current, the engine was created on device %d", dev, c->device);
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  GP_CUDA(c, cudaStreamIsCapturing(c->stream, &cap));
+  if (cap != cudaStreamCaptureStatusNone)
+    return fail(c, GP_ERR_UNSUPPORTED, "the engine stream is being captured: the call reads host data at every launch");
+  return GP_OK;
+}
+
+// A staging slot of at least `bytes`, free to be written.
+inline gp_status staging_take(gp_ctx* c, size_t bytes, StagingSlot** out) {
+  StagingSlot& s = c->staging[c->staging_next];
+  if (!s.free) GP_CUDA(c, cudaEventCreateWithFlags(&s.free, cudaEventDisableTiming));
+  GP_CUDA(c, cudaEventSynchronize(s.free));
+  if (bytes > s.pinned_cap) {
+    const size_t cap = (std::max(bytes, 2 * s.pinned_cap) + 65535) & ~size_t(65535);
+    if (s.pinned) GP_CUDA(c, cudaFreeHost(s.pinned));
+    s.pinned = nullptr;
+    s.pinned_cap = 0;
+    GP_CUDA(c, cudaHostAlloc(&s.pinned, cap, cudaHostAllocDefault));
+    s.pinned_cap = cap;
+  }
+  const gp_status st = ensure(c, s.dev, s.pinned_cap);
+  if (st != GP_OK) return st;
+  c->staging_next = (c->staging_next + 1) % kStagingSlots;
+  *out = &s;
+  return GP_OK;
+}
+
+inline gp_status staging_upload(gp_ctx* c, StagingSlot& s, size_t bytes) {
+  GP_CUDA(c, cudaMemcpyAsync(s.dev.p, s.pinned, bytes, cudaMemcpyHostToDevice, c->stream));
+  GP_CUDA(c, cudaEventRecord(s.free, c->stream));
+  return GP_OK;
+}
+
+// The engine stream waits for a compaction pending on the side stream if a
+// request holds a page it reads or writes (App. E.3).
+inline gp_status wait_shared_pages(gp_ctx* c, int n, const gp_request* reqs) {
+  if (!c->compaction_pending) return GP_OK;
+  for (int r = 0; r < n; ++r)
+    for (int j = 0; j < reqs[r].num_pages; ++j)
+      if (c->pending_pages.count(reqs[r].block_table[j])) {
+        GP_CUDA(c, cudaStreamWaitEvent(c->stream, c->ev_done, 0));
+        return GP_OK;
+      }
+  return GP_OK;
+}
+
 // Read and clear the kernels' error word (synchronises the stream).  A word
 // holding only ERR_TIMEOUT (bounded waits gave up) is GP_ERR_TIMEOUT; any
 // failed device-side check makes it GP_ERR_INVALID.
@@ -278,6 +351,14 @@ inline gp_status kernel_error_status(gp_ctx* c, int e) {
   return GP_OK;
 }
 
+// Starts a check that marks pages as it meets them (page_seen == check).
+inline void begin_page_check(gp_ctx* c) {
+  if (c->page_seen.size() != c->refcnt.size() || ++c->check == 0) {
+    c->page_seen.assign(c->refcnt.size(), 0);
+    c->check = 1;
+  }
+}
+
 inline gp_status validate_request(gp_ctx* c, const gp_request& r, int idx, bool need_slot) {
   const gp_config& g = c->cfg;
   if (need_slot && (r.slot < 0 || r.slot >= g.max_slots || !c->slot_bound[r.slot]))
@@ -288,10 +369,7 @@ inline gp_status validate_request(gp_ctx* c, const gp_request& r, int idx, bool 
   if (!r.block_table) return fail(c, GP_ERR_INVALID, "request %d: null block table", idx);
   if (r.pos < 0) return fail(c, GP_ERR_INVALID, "request %d: negative position", idx);
   // a page is marked with the number of the check that meets it: no set to build
-  if (c->page_seen.size() != c->refcnt.size() || ++c->check == 0) {
-    c->page_seen.assign(c->refcnt.size(), 0);
-    c->check = 1;
-  }
+  begin_page_check(c);
   for (int j = 0; j < r.num_pages; ++j) {
     const int32_t pg = r.block_table[j];
     if (pg < 0 || pg >= g.num_pages || c->refcnt[pg] <= 0)

@@ -24,6 +24,7 @@
 #include "attn_kernels.h"
 #include "engine.h"
 #include "gp_kernels.h"
+#include "weighted_kernels.h"
 
 using namespace gp;
 
@@ -225,6 +226,7 @@ gp_status gp_create(const gp_config* cfg, void* k_cache, void* v_cache, void* st
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && sms > 0) {
       c->spec_units_max = 4 * (int64_t)sms;
       c->sms = sms;
+      c->device = dev;
     }
   }
   *out = c;
@@ -245,8 +247,13 @@ gp_status gp_destroy(gp_ctx* c) {
     if (c->ev_ready) cudaEventDestroy(c->ev_ready);
     if (c->ev_done) cudaEventDestroy(c->ev_done);
     for (DevBuf* b : {&c->upload, &c->bt2, &c->qt, &c->bq, &c->scores, &c->aval, &c->tickets, &c->kout, &c->ksum, &c->ent,
-                      &c->masks, &c->xstat, &c->attn, &c->spec_masks, &c->upload_attn})
+                      &c->masks, &c->xstat, &c->attn, &c->spec_masks, &c->upload_attn, &c->logits, &c->wstat, &c->evict})
       if (b->p) cudaFree(b->p);
+    for (StagingSlot& s : c->staging) {
+      if (s.pinned) cudaFreeHost(s.pinned);
+      if (s.dev.p) cudaFree(s.dev.p);
+      if (s.free) cudaEventDestroy(s.free);
+    }
     if (c->inv_freq) cudaFree(c->inv_freq);
     if (c->pool) cudaFree(c->pool);
     if (c->err_dev) cudaFree(c->err_dev);
@@ -1153,6 +1160,8 @@ gp_status gp_debug_set_wait_limit(gp_ctx* c, int32_t kernel, int64_t cycles) {
     c->wait_limit_compress = v;
   } else if (kernel == GP_KERNEL_SELECT) {
     c->wait_limit_select = v;
+  } else if (kernel == GP_KERNEL_EVICT) {
+    c->wait_limit_evict = v;
   } else {
     return fail(c, GP_ERR_UNSUPPORTED, "kernel %d has no settable wait limit", kernel);
   }
@@ -1183,16 +1192,17 @@ gp_status gp_stats(const gp_ctx* c, gp_stats_t* out) {
 
 // ---- decode attention with the summary update fused in --------------------------
 
-gp_status gp_decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_request* reqs,
-                              const int32_t* num_tokens, const void* q_dev, const uint8_t* first_dev,
-                              float* out_dev) {
-  gp_status st = need_device(c);
-  if (st != GP_OK) return st;
+namespace {
+
+// The argument checks of the decode attention calls.
+gp_status check_decode(gp_ctx* c, int32_t layer, int32_t n, const gp_request* reqs, const int32_t* num_tokens,
+                       bool null_argument) {
+  gp_status st;
   const gp_config& g = c->cfg;
   if (layer < 0 || layer >= g.num_layers) return fail(c, GP_ERR_INVALID, "layer %d", layer);
   if (n < 0 || n > g.max_slots) return fail(c, GP_ERR_INVALID, "n = %d outside [0, max_slots]", n);
   if (n == 0) return GP_OK;
-  if (!reqs || !num_tokens || !q_dev || !first_dev || !out_dev) return fail(c, GP_ERR_INVALID, "null argument");
+  if (!reqs || !num_tokens || null_argument) return fail(c, GP_ERR_INVALID, "null argument");
   std::unordered_set<int32_t> slots;
   for (int r = 0; r < n; ++r) {
     if ((st = validate_request(c, reqs[r], r, true)) != GP_OK) return st;
@@ -1201,6 +1211,17 @@ gp_status gp_decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_requ
       return fail(c, GP_ERR_INVALID, "request %d: num_tokens %d outside [0, %d]", r, num_tokens[r],
                   reqs[r].num_pages * kPage);
   }
+  return GP_OK;
+}
+
+// gp_decode_attention, and with `weights` gp_decode_attention_weighted: the
+// attention kernel keeps its logits and statistics, a second kernel adds the
+// weights they give.
+gp_status decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_request* reqs, const int32_t* num_tokens,
+                           const void* q_dev, const uint8_t* first_dev, float* out_dev, float* weights) {
+  gp_status st;
+  const gp_config& g = c->cfg;
+  if (n == 0) return GP_OK;
   // A compaction pending on the side stream (App. E.3) runs on: this call
   // waits for it on the device only if one of its requests holds a page the
   // compaction reads or writes.  The call uploads its descriptors to its own
@@ -1218,6 +1239,22 @@ gp_status gp_decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_requ
   if (c->scan_kernel == GP_SCAN_TENSOR_CORE && !tc)
     return fail(c, GP_ERR_UNSUPPORTED, "the tensor-core attention kernel cannot take this cache or shape");
   if (overlap) GP_CUDA(c, cudaStreamWaitEvent(c->stream, c->ev_done, 0));
+  // the accumulated weights: where each request's logits start
+  std::vector<gp::WeightReq> wreqs(weights ? n : 0);
+  std::vector<int64_t> logit_off(weights ? n : 0);
+  int64_t logit_floats = 0;
+  int wpages = 0;
+  if (weights) {
+    for (int r = 0; r < n; ++r) {
+      const int held = (num_tokens[r] + kPage - 1) / kPage;
+      logit_off[r] = logit_floats;
+      wreqs[r] = {logit_floats, wpages, num_tokens[r], reqs[r].slot, 0};
+      wpages += held;
+      logit_floats += (int64_t)held * kPage * g.num_q_heads;
+    }
+    if ((st = ensure(c, c->logits, sizeof(float) * (size_t)logit_floats)) != GP_OK) return st;
+    if ((st = ensure(c, c->wstat, sizeof(float2) * (size_t)n * g.num_q_heads)) != GP_OK) return st;
+  }
   const int maxp = g.max_pages_per_req;
   const int Hkv = g.num_kv_heads;
   std::vector<int> npg(n), order(n), nsp(n);
@@ -1254,9 +1291,15 @@ gp_status gp_decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_requ
   const size_t tick_off = (part_floats * sizeof(float) + 255) & ~size_t(255);
   if ((st = ensure(c, c->attn, tick_off + sizeof(unsigned) * (size_t)n * Hkv)) != GP_OK) return st;
   const size_t items_bytes = sizeof(gp::AttnItem) * items.size();
+  const size_t weights_at = (items_bytes + sizeof(int32_t) * cta_begin.size() + 15) & ~size_t(15);
+  const size_t wreq_bytes = sizeof(gp::WeightReq) * wreqs.size();
   Staged s{};
-  if ((st = stage(c, n, false, &s, &c->upload_attn, items_bytes + sizeof(int32_t) * cta_begin.size())) != GP_OK)
+  if ((st = stage(c, n, false, &s, &c->upload_attn, weights_at + wreq_bytes + sizeof(int64_t) * wreqs.size())) != GP_OK)
     return st;
+  if (weights) {
+    std::memcpy(static_cast<char*>(s.extra) + weights_at, wreqs.data(), wreq_bytes);
+    std::memcpy(static_cast<char*>(s.extra) + weights_at + wreq_bytes, logit_off.data(), sizeof(int64_t) * n);
+  }
   s.part_base[0] = 0;
   for (int i = 0; i < n; ++i) {
     s.sel[i] = order[i];
@@ -1319,8 +1362,49 @@ gp_status gp_decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_requ
   a.items = tc ? dev_at<gp::AttnItem>(s, s.off_extra) : nullptr;
   a.cta_begin = tc ? dev_at<int32_t>(s, s.off_extra + items_bytes) : nullptr;
   a.err = c->err_dev;
-  return timed_launch(c, GP_KERNEL_ATTENTION, "decode_attention",
-                      [&] { return gp::launch_decode_attention(a, c->stream); });
+  if (weights) {
+    a.logits = static_cast<float*>(c->logits.p);
+    a.logit_off = dev_at<int64_t>(s, s.off_extra + weights_at + wreq_bytes);
+    a.stat = static_cast<float2*>(c->wstat.p);
+  }
+  st = timed_launch(c, GP_KERNEL_ATTENTION, "decode_attention",
+                    [&] { return gp::launch_decode_attention(a, c->stream); });
+  if (st != GP_OK || !weights) return st;
+  gp::WeightArgs w{};
+  w.reqs = dev_at<gp::WeightReq>(s, s.off_extra + weights_at);
+  w.n = n;
+  w.pages = wpages;
+  w.layer = layer;
+  w.Hq = g.num_q_heads;
+  w.Hkv = g.num_kv_heads;
+  w.G = G;
+  w.M = g.max_slots;
+  w.cap = (int64_t)g.max_pages_per_req * kPage;
+  w.logits = a.logits;
+  w.stat = a.stat;
+  w.weights = weights;
+  w.err = c->err_dev;
+  return timed_launch(c, GP_KERNEL_WEIGHTS, "decode_weights", [&] { return gp::launch_decode_weights(w, c->stream); });
+}
+
+}  // namespace
+
+gp_status gp_decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_request* reqs,
+                              const int32_t* num_tokens, const void* q_dev, const uint8_t* first_dev,
+                              float* out_dev) {
+  gp_status st = need_device(c);
+  if (st != GP_OK) return st;
+  if ((st = check_decode(c, layer, n, reqs, num_tokens, !q_dev || !first_dev || !out_dev)) != GP_OK) return st;
+  return decode_attention(c, layer, n, reqs, num_tokens, q_dev, first_dev, out_dev, nullptr);
+}
+
+gp_status gp_decode_attention_weighted(gp_ctx* c, int32_t layer, int32_t n, const gp_request* reqs,
+                                       const int32_t* num_tokens, const void* q_dev, const uint8_t* first_dev,
+                                       float* out_dev, float* weights_dev) {
+  if (!c) return GP_ERR_INVALID;
+  gp_status st = check_decode(c, layer, n, reqs, num_tokens, !q_dev || !out_dev || !weights_dev);
+  if (st != GP_OK || (st = ready_call(c)) != GP_OK) return st;
+  return decode_attention(c, layer, n, reqs, num_tokens, q_dev, first_dev, out_dev, weights_dev);
 }
 
 // ---- asynchronous compaction (side stream) ------------------------------------

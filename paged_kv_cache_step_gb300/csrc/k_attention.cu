@@ -94,7 +94,8 @@ __device__ __forceinline__ void load_row(const unsigned char* row, int c, float 
   }
 }
 
-template <int D, int G, bool F32>
+// W: keep the logits and the softmax's statistics for the accumulated weights.
+template <int D, int G, bool F32, bool W>
 __global__ void __launch_bounds__(NT, 2) k_decode_attn(AttnArgs a) {
   constexpr int RB = F32 ? 4 * D : 2 * D;  // bytes of a cached row
   constexpr int SR = TBYTES / RB;          // rows of a stage
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(NT, 2) k_decode_attn(AttnArgs a) {
     const size_t qi = ((size_t)r * a.Hq + g) * D + d;
     const double qv = a.q_f32 ? (double)static_cast<const float*>(a.q)[qi]
                               : (double)__bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[qi]);
-    if (split == 0) {
+    if (split == 0 && a.first) {
       double* row = a.pool + (((size_t)a.layer * a.M + slot) * 2) * ((size_t)a.Hq * D) + (size_t)g * D + d;
       double* row_l = row + (size_t)a.Hq * D;
       if (a.first[r]) {
@@ -265,6 +266,16 @@ __global__ void __launch_bounds__(NT, 2) k_decode_attn(AttnArgs a) {
       for (int u = 0; u < UK; ++u)
 #pragma unroll
         for (int g = 0; g < G; ++g) z[u][g] += __shfl_xor_sync(0xffffffffu, z[u][g], o);
+    if constexpr (W) {
+      if (c == 0)
+#pragma unroll
+        for (int u = 0; u < UK; ++u)
+          if (grp + KG * u < nval) {
+            const size_t i = (size_t)h * npg * PAGE + (size_t)(p0 * PAGE + k * SR + grp + KG * u);
+#pragma unroll
+            for (int g = 0; g < G; ++g) a.logits[a.logit_off[r] + i * G + g] = z[u][g];
+          }
+    }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       float mx = NEGF;
@@ -362,20 +373,26 @@ __global__ void __launch_bounds__(NT, 2) k_decode_attn(AttnArgs a) {
       den = fmaf(w, __ldcg(q + D + 1), den);
     }
     a.out[((size_t)r * a.Hq + h * G + gi) * D + d] = den > 0.f ? num / den : 0.f;
+    if constexpr (W)
+      if (d == 0) a.stat[(size_t)r * a.Hq + h * G + gi] = make_float2(M, den > 0.f ? 1.f / den : 0.f);
   }
 }
 
-template <int D, int G, bool F32>
-cudaError_t launch_t(const AttnArgs& a, cudaStream_t s) {
+template <int D, int G, bool F32, bool W>
+cudaError_t launch_w(const AttnArgs& a, cudaStream_t s) {
   constexpr int smem = NSTAGE * STAGE;
   static bool attr = false;
   if (!attr) {
-    const cudaError_t e = cudaFuncSetAttribute(k_decode_attn<D, G, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(k_decode_attn<D, G, F32, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     attr = true;
   }
-  k_decode_attn<D, G, F32><<<dim3(a.n_ctas), NT, smem, s>>>(a);
+  k_decode_attn<D, G, F32, W><<<dim3(a.n_ctas), NT, smem, s>>>(a);
   return cudaGetLastError();
+}
+template <int D, int G, bool F32>
+cudaError_t launch_t(const AttnArgs& a, cudaStream_t s) {
+  return a.logits ? launch_w<D, G, F32, true>(a, s) : launch_w<D, G, F32, false>(a, s);
 }
 
 }  // namespace

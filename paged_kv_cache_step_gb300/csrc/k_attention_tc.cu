@@ -164,6 +164,13 @@ __device__ __forceinline__ Item load_item(const AttnArgs& a, int i) {
   return it;
 }
 
+// A key's logits, for the pass over the accumulated weights.
+template <int G>
+__device__ __forceinline__ void store_logits(float* dst, const float* z) {
+  if constexpr (G == 4) *reinterpret_cast<float4*>(dst) = make_float4(z[0], z[1], z[2], z[3]);
+  else *reinterpret_cast<float2*>(dst) = make_float2(z[0], z[1]);
+}
+
 // A partial of the tensor-core kernel: [G][D] outputs, then [G] maxima and
 // [G] sums (the same G (D + 2) floats as the CUDA-core kernel's, laid out so
 // that the outputs of every partial start on a 16-byte boundary).
@@ -175,7 +182,7 @@ constexpr int kPartFloats = G * (D + 2);
 // 2^(m_split - m) are computed once (into mw, [nsp][G] in shared memory);
 // then each lane owns float4 pieces of the G x D outputs and keeps one load
 // per split in flight for each.
-template <int G>
+template <int G, bool W>
 __device__ __forceinline__ void merge_splits(const AttnArgs& a, const AttnItem& it, float* mw, int lane) {
   const float* base = a.part + (size_t)it.part_first * kPartFloats<G>;
   float M[G], den[G];
@@ -232,6 +239,11 @@ __device__ __forceinline__ void merge_splits(const AttnArgs& a, const AttnItem& 
       acc[c].w = fmaf(w1, v1[c].w, fmaf(w0, v0[c].w, acc[c].w));
     }
   }
+  if constexpr (W)
+#pragma unroll
+    for (int gg = 0; gg < G; ++gg)
+      if (lane == gg)
+        a.stat[(size_t)it.r * a.Hq + it.h * G + gg] = make_float2(M[gg], den[gg] > 0.f ? 1.f / den[gg] : 0.f);
   const bool vec = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;  // the caller's buffer may be offset
 #pragma unroll
   for (int c = 0; c < PIECES; ++c) {
@@ -253,7 +265,8 @@ __device__ __forceinline__ void merge_splits(const AttnArgs& a, const AttnItem& 
   }
 }
 
-template <int G>
+// W: keep the logits and the softmax's statistics for the accumulated weights.
+template <int G, bool W>
 __global__ void __launch_bounds__(NT, 1) k_decode_attn_tc(const __grid_constant__ AttnArgs a) {
   using L = Sm<G>;
   static_assert(3 * G <= NB, "three parts per head fit the MMA N");
@@ -452,7 +465,7 @@ __global__ void __launch_bounds__(NT, 1) k_decode_attn_tc(const __grid_constant_
         const size_t qi = ((size_t)it.r * a.Hq + g) * D + d;
         const double qv = a.q_f32 ? (double)static_cast<const float*>(a.q)[qi]
                                   : (double)__bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[qi]);
-        if (it.split == 0) {
+        if (it.split == 0 && a.first) {
           double* row =
               a.pool + (((size_t)a.layer * a.M + it.slot) * 2) * ((size_t)a.Hq * D) + (size_t)g * D + d;
           double* row_l = row + (size_t)a.Hq * D;
@@ -505,6 +518,9 @@ __global__ void __launch_bounds__(NT, 1) k_decode_attn_tc(const __grid_constant_
       float m[G];
 #pragma unroll
       for (int gg = 0; gg < G; ++gg) m[gg] = NEG;
+      float* lg = nullptr;  // the pair's logits
+      if constexpr (W)
+        lg = a.logits + a.logit_off[it.r] + (size_t)it.h * ((it.ntok + PAGE - 1) / PAGE * PAGE) * G;
       for (int t = 0; t < it.T; ++t, ++g) {
         const int j = g % NS;
         const bool ok = __all_sync(0xffffffffu, wait_bar(sready(j), (uint32_t)((g / NS) & 1), abort));
@@ -543,6 +559,8 @@ __global__ void __launch_bounds__(NT, 1) k_decode_attn_tc(const __grid_constant_
           z[gg] = valid ? v[gg] + (v[G + gg] + v[2 * G + gg]) : NEG;
           wm[gg] = z[gg];
         }
+        if constexpr (W)
+          if (valid) store_logits<G>(lg + (size_t)(it.p0 * PAGE + t * TK + key) * G, z);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
@@ -642,6 +660,13 @@ __global__ void __launch_bounds__(NT, 1) k_decode_attn_tc(const __grid_constant_
 #pragma unroll
         for (int gg = 0; gg < G; ++gg)
           a.out[((size_t)it.r * a.Hq + it.h * G + gg) * D + d] = den[gg] > 0.f ? acc[gg] / den[gg] : 0.f;
+        if constexpr (W)
+          if (warp == W_CR0)
+#pragma unroll
+            for (int gg = 0; gg < G; ++gg)
+              if (lane == gg)
+                a.stat[(size_t)it.r * a.Hq + it.h * G + gg] =
+                    make_float2(mx[gg], den[gg] > 0.f ? 1.f / den[gg] : 0.f);
         if (it.T == 0)  // warp 8 alone (the other warps skipped the item): every d of the pair
           for (int e = lane; e < G * D; e += 32) a.out[((size_t)it.r * a.Hq + it.h * G) * D + e] = 0.f;
         return true;
@@ -684,7 +709,7 @@ __global__ void __launch_bounds__(NT, 1) k_decode_attn_tc(const __grid_constant_
           last = old == (unsigned)(it.nsp - 1) ? 1u : 0u;
           if (last) __threadfence();
         }
-        if (__shfl_sync(0xffffffffu, last, 0)) merge_splits<G>(a, it, reinterpret_cast<float*>(sm + L::MW), lane);
+        if (__shfl_sync(0xffffffffu, last, 0)) merge_splits<G, W>(a, it, reinterpret_cast<float*>(sm + L::MW), lane);
       }
       if (it.T > 0) ++ke;
       return true;
@@ -700,17 +725,17 @@ __global__ void __launch_bounds__(NT, 1) k_decode_attn_tc(const __grid_constant_
   }
 }
 
-template <int G>
+template <int G, bool W>
 cudaError_t launch_tc(const AttnArgs& a, cudaStream_t s) {
   constexpr size_t smem = Sm<G>::BYTES;
   static bool attr = false;
   if (!attr) {
     const cudaError_t e =
-        cudaFuncSetAttribute(k_decode_attn_tc<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(k_decode_attn_tc<G, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     attr = true;
   }
-  k_decode_attn_tc<G><<<dim3((unsigned)a.grid), NT, smem, s>>>(a);
+  k_decode_attn_tc<G, W><<<dim3((unsigned)a.grid), NT, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -720,7 +745,8 @@ cudaError_t launch_decode_attention_tc(const AttnArgs& a, cudaStream_t s) {
   if (a.n == 0) return cudaSuccess;
   if (a.n_ctas < a.n * a.Hkv || a.grid < 1 || a.grid > a.n_ctas || !a.tc || a.kv_f32 || !attention_tc_shape(a.D, a.G))
     return cudaErrorInvalidValue;
-  return a.G == 4 ? launch_tc<4>(a, s) : launch_tc<2>(a, s);
+  if (a.logits) return a.G == 4 ? launch_tc<4, true>(a, s) : launch_tc<2, true>(a, s);
+  return a.G == 4 ? launch_tc<4, false>(a, s) : launch_tc<2, false>(a, s);
 }
 
 }  // namespace gp

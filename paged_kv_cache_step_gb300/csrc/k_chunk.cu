@@ -1,0 +1,313 @@
+// Causal attention of several new tokens a request over the paged cache, and
+// the accumulated weights of it, on the CUDA cores (fp32 FMA): fp32 caches or
+// queries, and every shape when it is asked for.  k_chunk_tc.cu has the
+// tensor-core kernels.
+//
+// Token t of request r (query rows rotated, packed) sees the logical slots
+// [0, cached + t + 1):  z = q . k / sqrt(d), a = softmax(z), out = sum a v,
+// and W_i += sum over the tokens and the group's heads of a_i.
+//
+// A query row here is a (token, head of the group) pair: the G heads of a KV
+// head share its keys, so a tile of 64 rows is 64 / G tokens.
+//   attention  one CTA a tile: key tiles of 64 through shared memory, S by
+//              4 x 4 register tiles, softmax in base 2 with a running maximum
+//              and sum, out += P V.  Slots past the last token may hold any
+//              bits; their V rows are zeroed as they are read.
+//   weights    the sums over a column need every row's final maximum and sum,
+//              so S is formed again, one CTA a tile of 64 keys, over the query
+//              tiles that see it: a weight has one writer, and the sum's order
+//              is fixed.
+// Bounded by the fp32 pipe: 2 d (2 + 1) flops a (row, key) pair.
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "weighted_kernels.h"
+
+namespace gp {
+namespace {
+
+constexpr int NT = 256;  // 16 x 16 threads
+constexpr int PAGE = 256;
+constexpr int BR = CHUNK_ROWS, BK = CHUNK_KEYS;
+constexpr float NEG = -1.0e30f;
+static_assert(BR == 64 && BK == 64 && PAGE % BK == 0, "4 x 4 outputs a thread");
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int D>
+struct Smem {
+  static constexpr int LD = D + 4;  // floats of a staged row: rows 4 banks apart
+  float q[BR][LD];
+  float kv[BK][LD];
+  float p[BR][BK + 4];
+  float m[BR], l[BR], f[BR];  // maximum, sum, the tile's rescale factor
+};
+
+template <bool F32>
+__device__ __forceinline__ float4 load4(const void* base, size_t elt) {
+  if constexpr (F32) {
+    return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + elt);
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + elt);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xffff0000u));
+  }
+}
+
+// 64 query rows from token t0, scaled to base 2; rows past the request are 0.
+template <int D>
+__device__ __forceinline__ void load_rows(const ChunkArgs& a, const ChunkReq& rq, int h, int t0, Smem<D>& sm) {
+  const float sc = 1.4426950408889634f / sqrtf((float)D);
+  for (int e = threadIdx.x; e < BR * D / 4; e += NT) {
+    const int row = e / (D / 4), d = e % (D / 4) * 4;
+    const int t = t0 + row / a.G;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t < rq.nnew) {
+      const size_t at = ((size_t)(rq.row0 + t) * a.Hq + h * a.G + row % a.G) * D + d;
+      x = a.q_f32 ? load4<true>(a.q, at) : load4<false>(a.q, at);
+    }
+    *reinterpret_cast<float4*>(&sm.q[row][d]) = make_float4(sc * x.x, sc * x.y, sc * x.z, sc * x.w);
+  }
+}
+
+// 64 rows of K or V from logical slot s0; rows from `total` on are 0.
+template <int D>
+__device__ __forceinline__ void load_keys(const ChunkArgs& a, const ChunkReq& rq, const void* cache, int h, int s0,
+                                          int total, Smem<D>& sm) {
+  int page = a.bt[rq.bt_off + s0 / PAGE];
+  if (page < 0 || page >= a.num_pages_total) {
+    if (threadIdx.x == 0) atomicOr(a.err, ERR_BAD_PAGE);
+    page = 0;
+  }
+  const size_t base = ((((size_t)a.layer * a.num_pages_total + page) * a.Hkv + h) * PAGE + s0 % PAGE) * D;
+  for (int e = threadIdx.x; e < BK * D / 4; e += NT) {
+    const int row = e / (D / 4), d = e % (D / 4) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (s0 + row < total) {
+      const size_t at = base + (size_t)row * D + d;
+      x = a.kv_f32 ? load4<true>(cache, at) : load4<false>(cache, at);
+    }
+    *reinterpret_cast<float4*>(&sm.kv[row][d]) = x;
+  }
+}
+
+// s[i][j] = q row 4 ty + i . key tx + 16 j
+template <int D>
+__device__ __forceinline__ void scores(const Smem<D>& sm, int ty, int tx, float s[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+  for (int d = 0; d < D; d += 4) {
+    float4 q[4], k[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(&sm.q[4 * ty + i][d]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4*>(&sm.kv[tx + 16 * j][d]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = fmaf(q[i].x, k[j].x, s[i][j]);
+        s[i][j] = fmaf(q[i].y, k[j].y, s[i][j]);
+        s[i][j] = fmaf(q[i].z, k[j].z, s[i][j]);
+        s[i][j] = fmaf(q[i].w, k[j].w, s[i][j]);
+      }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(NT) k_chunk(const __grid_constant__ ChunkArgs a) {
+  extern __shared__ __align__(16) unsigned char raw[];
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
+  constexpr int DC = D / 64;  // float4 columns of the output a thread owns
+  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+  const ChunkTile tile = a.tiles[blockIdx.x];
+  const ChunkReq rq = a.reqs[tile.r];
+  const int total = rq.cached + rq.nnew;
+  const int tokens = BR / a.G;
+  const int last = min(tile.first + tokens, rq.nnew) - 1;  // last token of the tile
+  const int end = rq.cached + last + 1;                    // slots it sees
+  load_rows<D>(a, rq, tile.h, tile.first, sm);
+  if (tid < BR) {
+    sm.m[tid] = NEG;
+    sm.l[tid] = 0.f;
+  }
+  float acc[4][DC][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < DC; ++c)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) acc[i][c][x] = 0.f;
+  for (int s0 = 0; s0 < end; s0 += BK) {
+    __syncthreads();  // the last tile's V and P are used
+    load_keys<D>(a, rq, a.k_cache, tile.h, s0, total, sm);
+    __syncthreads();
+    float s[4][4];
+    scores<D>(sm, ty, tx, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 4 * ty + i;
+      const int sees = rq.cached + tile.first + row / a.G;  // last slot the row sees
+      float mx = NEG;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (s0 + tx + 16 * j > sees) s[i][j] = -INFINITY;
+        mx = fmaxf(mx, s[i][j]);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float old = sm.m[row], mn = fmaxf(old, mx);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = ex2f(s[i][j] - mn);
+        sm.p[row][tx + 16 * j] = p;
+        sum += p;
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      __syncwarp();  // the row's old maximum has been read by its 16 threads
+      if (tx == 0) {
+        const float f = ex2f(old - mn);
+        sm.f[row] = f;
+        sm.m[row] = mn;
+        sm.l[row] = fmaf(sm.l[row], f, sum);
+      }
+    }
+    __syncthreads();  // K is used, P and the factors are written
+    load_keys<D>(a, rq, a.v_cache, tile.h, s0, total, sm);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = sm.f[4 * ty + i];
+#pragma unroll
+      for (int c = 0; c < DC; ++c)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[i][c][x] *= f;
+    }
+#pragma unroll 4
+    for (int k = 0; k < BK; ++k) {
+      float p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = sm.p[4 * ty + i][k];
+#pragma unroll
+      for (int c = 0; c < DC; ++c) {
+        const float4 v = *reinterpret_cast<const float4*>(&sm.kv[k][64 * c + 4 * tx]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[i][c][0] = fmaf(p[i], v.x, acc[i][c][0]);
+          acc[i][c][1] = fmaf(p[i], v.y, acc[i][c][1]);
+          acc[i][c][2] = fmaf(p[i], v.z, acc[i][c][2]);
+          acc[i][c][3] = fmaf(p[i], v.w, acc[i][c][3]);
+        }
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 4 * ty + i, t = tile.first + row / a.G;
+    if (t >= rq.nnew) continue;
+    const int g = tile.h * a.G + row % a.G;
+    const size_t at = (size_t)(rq.row0 + t) * a.Hq + g;
+    const float inv = 1.f / sm.l[row];
+    if (tx == 0 && a.stat) a.stat[at] = make_float2(sm.m[row], inv);
+#pragma unroll
+    for (int c = 0; c < DC; ++c) {
+      float o[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[x] = acc[i][c][x] * inv;
+      const size_t e = at * D + 64 * c + 4 * tx;
+      if (a.q_f32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + e) = make_float4(o[0], o[1], o[2], o[3]);
+      } else {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(o[0], o[1]), hi = __floats2bfloat162_rn(o[2], o[3]);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + e) =
+            make_uint2(*reinterpret_cast<const unsigned*>(&lo), *reinterpret_cast<const unsigned*>(&hi));
+      }
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(NT) k_chunk_weights(const __grid_constant__ ChunkArgs a) {
+  extern __shared__ __align__(16) unsigned char raw[];
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
+  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+  const ChunkTile tile = a.wtiles[blockIdx.x];
+  const ChunkReq rq = a.reqs[tile.r];
+  const int total = rq.cached + rq.nnew;
+  const int tokens = BR / a.G, s0 = tile.first;
+  if (rq.slot < 0 || rq.slot >= a.M) return;
+  load_keys<D>(a, rq, a.k_cache, tile.h, s0, total, sm);
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
+  // the first token that sees slot s0, rounded down to a tile
+  for (int t0 = max(0, s0 - rq.cached) / tokens * tokens; t0 < rq.nnew; t0 += tokens) {
+    __syncthreads();  // the last tile's rows are used
+    load_rows<D>(a, rq, tile.h, t0, sm);
+    if (tid < BR) {
+      const int t = t0 + tid / a.G;
+      const float2 st = t < rq.nnew ? a.stat[(size_t)(rq.row0 + t) * a.Hq + tile.h * a.G + tid % a.G]
+                                    : make_float2(0.f, 0.f);
+      sm.m[tid] = st.x;
+      sm.l[tid] = st.y;
+    }
+    __syncthreads();
+    float s[4][4];
+    scores<D>(sm, ty, tx, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 4 * ty + i, t = t0 + row / a.G;
+      const float m = sm.m[row], inv = sm.l[row];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (t < rq.nnew && s0 + tx + 16 * j <= rq.cached + t) w[j] = fmaf(ex2f(s[i][j] - m), inv, w[j]);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sm.p[ty][tx + 16 * j] = w[j];
+  __syncthreads();
+  if (tid < BK && s0 + tid < total) {
+    float sum = 0.f;
+#pragma unroll
+    for (int y = 0; y < 16; ++y) sum += sm.p[y][tid];
+    a.weights[(((size_t)a.layer * a.M + rq.slot) * a.Hkv + tile.h) * a.cap + s0 + tid] += sum;
+  }
+}
+
+template <typename K>
+cudaError_t launch_k(K kernel, size_t smem, int grid, const ChunkArgs& a, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<dim3((unsigned)grid), NT, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t s) {
+  if (a.n_tiles == 0) return cudaSuccess;
+  if (a.G < 1 || BR % a.G) return cudaErrorInvalidValue;
+  if (a.D == 128) return launch_k(k_chunk<128>, sizeof(Smem<128>), a.n_tiles, a, s);
+  if (a.D == 64) return launch_k(k_chunk<64>, sizeof(Smem<64>), a.n_tiles, a, s);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_chunk_weights(const ChunkArgs& a, cudaStream_t s) {
+  if (a.n_wtiles == 0) return cudaSuccess;
+  if (a.G < 1 || BR % a.G) return cudaErrorInvalidValue;
+  if (a.D == 128) return launch_k(k_chunk_weights<128>, sizeof(Smem<128>), a.n_wtiles, a, s);
+  if (a.D == 64) return launch_k(k_chunk_weights<64>, sizeof(Smem<64>), a.n_wtiles, a, s);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace gp

@@ -1,0 +1,148 @@
+// Internal interface between the host side of the accumulated-weight
+// operators (weighted.cpp) and their kernels (k_append.cu, k_weights.cu,
+// k_chunk.cu, k_chunk_tc.cu, k_evict.cu).  Plain structs of device pointers
+// and sizes; no torch types.
+//
+// The accumulated weights are the caller's: fp32 [L][M][Hkv][cap], by request
+// slot and logical token, cap = max_pages_per_req * 256.
+#pragma once
+
+#include "gp_kernels.h"
+
+namespace gp {
+
+// ---- new tokens into the cache (RoPE, pages, weights cleared) ---------------
+struct AppendReq {
+  int64_t pos;     // RoPE position of the first new token
+  int64_t row0;    // its row in the packed inputs
+  int32_t cached;  // its logical slot
+  int32_t nnew;    // tokens, at least one
+  int32_t slot;    // request slot (row of the weights)
+  int32_t bt_off;  // pages of the logical blocks cached / 256, ...
+};
+
+struct AppendArgs {
+  void* k_cache;
+  void* v_cache;
+  int kv_f32, q_f32;
+  int num_pages_total;
+  int layer, Hq, Hkv, D, M;
+  int64_t cap;               // tokens of a row of the weights
+  const AppendReq* reqs;     // [n], row0 ascending
+  const int32_t* bt;
+  int n;
+  int rows;                  // packed rows
+  const void* q;             // [rows][Hq][D] or null
+  const void* k;             // [rows][Hkv][D]
+  const void* v;             // [rows][Hkv][D]
+  void* q_rot;               // [rows][Hq][D], may be q
+  float* weights;            // or null
+  const double* inv_freq;    // [D / 2]
+  int* err;
+};
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
+
+// ---- one decode step's weights from the logits the attention kernel kept ----
+struct WeightReq {
+  int64_t logit_off;  // float offset of the request's logits [Hkv][pages * 256][G]
+  int32_t page0;      // pages of the requests before it
+  int32_t ntok;
+  int32_t slot;
+  int32_t pad;
+};
+static_assert(sizeof(WeightReq) == 24, "uploaded as it is");
+
+struct WeightArgs {
+  const WeightReq* reqs;  // [n], page0 ascending
+  int n;
+  int pages;              // of all requests
+  int layer, Hq, Hkv, G, M;
+  int64_t cap;
+  const float* logits;    // base 2
+  const float2* stat;     // [n][Hq] (maximum, 1 / sum)
+  float* weights;
+  int* err;
+};
+cudaError_t launch_decode_weights(const WeightArgs& a, cudaStream_t s);
+
+// ---- eviction by accumulated weight -----------------------------------------
+struct EvictReq {
+  int32_t slot;
+  int32_t T, keep, recent;  // tokens, tokens kept, of them the most recent
+  int32_t bt_off;
+  int32_t words;            // of the keep mask, num_pages * 8
+  int32_t items;            // move items of a unit: ceil(keep / rows of an item), 0 when T <= keep
+  int32_t pad;
+  int64_t mask_off;         // word offset of the masks [units][words]
+  int64_t idx_off;          // offset of the kept slots [units][keep]
+  int64_t item0;            // items of the requests before it (all units)
+  int64_t pre_off;          // offset of the kept-slot counts [units][items + 1]
+};
+
+struct EvictArgs {
+  void* k_cache;
+  void* v_cache;
+  int num_pages_total;
+  int L, Hkv, M, row_bytes;
+  int64_t cap;
+  const EvictReq* reqs;       // [n]
+  int n;
+  const int32_t* old_bt;
+  const int32_t* new_bt;
+  float* weights;
+  uint32_t* masks;
+  uint16_t* idx;              // kept slot of each rank
+  int32_t* pre;               // kept slots below every item's first slot
+  unsigned* flags;            // [items of all units], 1: the item's rows are read
+  unsigned long long* ticket; // next item
+  int64_t items;              // of all requests
+  int sms;
+  unsigned long long* moved;
+  int* err;
+  long long wait_limit;
+};
+// Rows of a move item: K rows of 16 KB.
+__host__ __device__ constexpr int evict_rows(int row_bytes) { return 16384 / row_bytes; }
+cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t s);
+cudaError_t launch_evict_move(const EvictArgs& a, cudaStream_t s);
+
+// ---- causal attention of several new tokens a request -----------------------
+struct ChunkReq {
+  int64_t row0;    // packed row of the first new token
+  int32_t cached;  // tokens before it
+  int32_t nnew;
+  int32_t slot;
+  int32_t bt_off;
+};
+
+// CUDA-core kernels: a tile of 64 query rows (64 / G tokens of the G heads of
+// a KV head), a tile of 64 keys.
+struct ChunkTile {
+  int32_t r, h, first, pad;  // request, KV head, first token of the rows (or first key)
+};
+constexpr int CHUNK_ROWS = 64, CHUNK_KEYS = 64;
+
+struct ChunkArgs {
+  const void* k_cache;
+  const void* v_cache;
+  int kv_f32, q_f32;
+  int num_pages_total;
+  int layer, Hq, Hkv, D, G, M;
+  int64_t cap;
+  const ChunkReq* reqs;
+  int n;
+  const int32_t* bt;
+  const ChunkTile* tiles;   // of the attention
+  int n_tiles;
+  const ChunkTile* wtiles;  // of the weights
+  int n_wtiles;
+  const void* q;            // [rows][Hq][D], rotated
+  void* out;                // [rows][Hq][D] in q's type
+  float2* stat;             // [rows][Hq] (maximum, 1 / sum) of the base-2 logits
+  float* weights;           // or null
+  int* err;
+};
+cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t s);
+cudaError_t launch_chunk_weights(const ChunkArgs& a, cudaStream_t s);
+
+}  // namespace gp
