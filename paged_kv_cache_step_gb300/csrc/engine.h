@@ -8,6 +8,7 @@
 #include "growpage.h"
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -93,7 +94,7 @@ struct gp_ctx {
   // that a call waits on the host only for the one kStagingSlots before it) and scratch
   gp::StagingSlot staging[gp::kStagingSlots];
   int staging_next = 0;
-  gp::DevBuf logits, wstat, evict;
+  gp::DevBuf logits, wstat, evict, chunk;
   int device = 0;                  // the device current at gp_create
   gp::DevBuf upload_attn;              // decode attention's own descriptors (it may overlap a compaction)
   // speculative selection: the Eq. 10 keep masks of every request of the last
@@ -378,6 +379,22 @@ inline gp_status validate_request(gp_ctx* c, const gp_request& r, int idx, bool 
       return fail(c, GP_ERR_INVALID, "request %d: page %d appears twice in the block table", idx, pg);
   }
   return GP_OK;
+}
+
+// A tiled bf16 tensor map with the 128-byte swizzle; false if it cannot be made.
+inline bool encode_bf16_map(CUtensorMap* map, uint32_t rank, const void* base, const cuuint64_t* dims,
+                            const cuuint64_t* strides, const cuuint32_t* box) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
+                        cudaSuccess && q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn) : nullptr;
+  }();
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box,
+                          ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 inline int units_of(const gp_ctx* c) { return c->cfg.num_layers * c->cfg.num_kv_heads; }

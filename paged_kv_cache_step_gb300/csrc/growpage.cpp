@@ -6,7 +6,6 @@
 #include "growpage.h"
 
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -41,20 +40,10 @@ bool make_map(gp_ctx* c, void* cache, CUtensorMap* map) {
   if (reinterpret_cast<uintptr_t>(cache) & 15u) return false;
   const uint64_t rows = (uint64_t)g.num_layers * (uint64_t)g.num_pages * (uint64_t)g.num_kv_heads * kPage;
   if (rows + 128 >= (1ull << 31)) return false;
-  void* fn = nullptr;
-  cudaDriverEntryPointQueryResult q{};
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-      q != cudaDriverEntryPointSuccess || !fn)
-    return false;
-  auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  cuuint64_t dims[2] = {(cuuint64_t)g.head_dim, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)g.head_dim * 2};
-  cuuint32_t box[2] = {64, 128};
-  cuuint32_t estr[2] = {1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, cache, dims, strides, box, estr,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  const cuuint64_t dims[2] = {(cuuint64_t)g.head_dim, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)g.head_dim * 2};
+  const cuuint32_t box[2] = {64, 128};
+  return encode_bf16_map(map, 2, cache, dims, strides, box);
 }
 
 // Work of the tensor-core attention kernel (persistent, one CTA per SM):
@@ -247,7 +236,7 @@ gp_status gp_destroy(gp_ctx* c) {
     if (c->ev_ready) cudaEventDestroy(c->ev_ready);
     if (c->ev_done) cudaEventDestroy(c->ev_done);
     for (DevBuf* b : {&c->upload, &c->bt2, &c->qt, &c->bq, &c->scores, &c->aval, &c->tickets, &c->kout, &c->ksum, &c->ent,
-                      &c->masks, &c->xstat, &c->attn, &c->spec_masks, &c->upload_attn, &c->logits, &c->wstat, &c->evict})
+                      &c->masks, &c->xstat, &c->attn, &c->spec_masks, &c->upload_attn, &c->logits, &c->wstat, &c->evict, &c->chunk})
       if (b->p) cudaFree(b->p);
     for (StagingSlot& s : c->staging) {
       if (s.pinned) cudaFreeHost(s.pinned);

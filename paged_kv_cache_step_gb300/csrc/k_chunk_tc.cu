@@ -1,0 +1,918 @@
+// Causal attention of several new tokens a request over the paged cache, and
+// the accumulated weights of it, on the tensor cores (tcgen05, sm_103a): bf16
+// caches and queries.  The formulas are k_chunk.cu's.
+//
+// Attention.  A query tile is 128 rows, 128 / G tokens of the G heads of a KV
+// head (they share its keys).  Per key tile of 128 slots
+//   S = Q K^T        128 x 128, K = d, fp32 in TMEM
+//   P = 2^(S c - m)  c = log2(e) / sqrt(d), rounded to bf16 over S in TMEM
+//   O += P V         128 x d, K = 128, P from TMEM, V MN-major as TMA left it
+// with the running maximum m moved only when a row's maximum has grown by
+// more than 8 (a factor 256, which fp32 and the bf16 exponent hold easily):
+// O is then rescaled in TMEM by the warp that found it, between two products.
+// Rounding P to bf16 costs 2^-9 relative a weight at random signs, about what
+// rounding the output to bf16 costs; keeping it exact would double the second
+// product.  The sum l is of the unrounded fp32 weights.
+//
+// One CTA per SM walks a list of items that the host cut into even shares.
+// Two softmax groups of 128 threads (thread = row = TMEM lane) alternate on
+// the tensor core: while one computes P, the other's products run.  They hold
+// two query tiles (the K and V tiles then serve 256 rows), or, when a request
+// has one tile left, the even and odd key tiles of that one.  A query tile in
+// several parts leaves partials (O, m, l) that a second kernel joins.
+//   warp 0       producer: Q tiles, and the K and V tiles through a ring
+//   warp 1       MMA issuer
+//   warps 4-7    softmax of group 0, then its epilogue;  warps 8-11 group 1
+// TMEM: S0 S1 (128 columns each, P over the first 64 of them), O0 O1.
+//
+// Weights.  W_i += sum over rows of 2^(S_ri c - m_r) / l_r needs the final m and
+// l of every row, so S is formed again, transposed: S^T = K Q^T, so that a
+// thread (TMEM lane) owns a key and adds up its row in a register: no
+// reduction over threads, no atomics, one writer a weight.  An item is a page
+// (two key tiles, one a group) against a range of query tiles, S^T double
+// buffered, K tiles kept and the next item's loaded meanwhile.  The statistics
+// of a query tile go through shared memory (warp 2).
+//
+// Every wait is bounded: on expiry the CTA records ERR_TIMEOUT, raises an
+// abort flag that ends every role's loop, waits (bounded) for its copies and
+// products in flight, frees its TMEM and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "tc_ptx.cuh"
+#include "weighted_kernels.h"
+
+namespace gp {
+namespace {
+
+using namespace tc;
+
+constexpr int PAGE = 256;
+constexpr int NT = 384;
+constexpr int TK = 128;
+constexpr int TMEM_COLS = 512;
+constexpr float NEG = -1.0e30f;
+constexpr float LAZY = 8.f;                  // base-2 growth of a maximum that is not followed
+constexpr long long kWaitLimit = 1ll << 31;  // clock cycles (about one second)
+
+// bf16 A and B, fp32 accumulator, M = 128, N; bit 16: B is MN-major.
+__host__ __device__ constexpr uint32_t idesc(int n, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+        "l"(reinterpret_cast<const uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
+}
+
+// D (TMEM) [+]= A (TMEM, bf16 pairs) . B for one K = 16 step.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bd, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bd), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// 32 columns of this thread's lane; the values may be used after tmem_arrived.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Ties a load's registers to the wait before it, so that no use moves above.
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile(""
+                 : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                   "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Bounded wait; gives up when the limit passes or *abort is set.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const volatile int* abort) {
+  if (mbar_try(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_try(bar, parity)) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitLimit) return false;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ T load_item(const T* p) {
+  static_assert(sizeof(T) == 32, "two 16-byte loads");
+  union {
+    int4 v[2];
+    T t;
+  } u;
+  u.v[0] = __ldg(reinterpret_cast<const int4*>(p));
+  u.v[1] = __ldg(reinterpret_cast<const int4*>(p) + 1);
+  return u.t;
+}
+__device__ __forceinline__ ChunkReq load_req(const ChunkReq* p) {
+  static_assert(sizeof(ChunkReq) == 24, "row0, four ints");
+  ChunkReq q;
+  const int2* s = reinterpret_cast<const int2*>(p);
+  const int2 a = __ldg(s), b = __ldg(s + 1), c = __ldg(s + 2);
+  q.row0 = (int64_t)(((uint64_t)(uint32_t)a.y << 32) | (uint32_t)a.x);
+  q.cached = b.x;
+  q.nnew = b.y;
+  q.slot = c.x;
+  q.bt_off = c.y;
+  return q;
+}
+
+// The key row of tile `t` of a request in the cache's tensor map.
+__device__ __forceinline__ int key_row(const ChunkTcArgs& a, const ChunkReq& rq, int h, int t) {
+  int pg = __ldg(a.bt + rq.bt_off + (t >> 1));
+  if (pg < 0 || pg >= a.num_pages_total) {
+    atomicOr(a.err, ERR_BAD_PAGE);
+    pg = 0;
+  }
+  return (int)((((size_t)a.layer * a.num_pages_total + pg) * a.Hkv + h) * PAGE + (t & 1) * TK);
+}
+
+// What an item's groups do: `n` key tiles, of which group x takes cnt[x].
+struct Work {
+  int n, cnt[2];
+};
+template <int G>
+__device__ __forceinline__ Work work_of(const ChunkItem& it, const ChunkReq& rq) {
+  constexpr int TOK = 128 / G;
+  Work w;
+  w.n = it.ke - it.kb;
+  if (it.keys) {
+    w.cnt[0] = (w.n + 1) / 2;
+    w.cnt[1] = w.n / 2;
+  } else {
+    // the first tile's last token sees fewer slots than the second's
+    const int see = (rq.cached + min(it.t0 + TOK, rq.nnew) + TK - 1) / TK;
+    w.cnt[0] = min(max(see - it.kb, 0), w.n);
+    w.cnt[1] = w.n;
+  }
+  return w;
+}
+
+template <int D>
+struct Sm {
+  static constexpr int TILE = TK * D * 2;             // a Q, K or V tile
+  static constexpr int HALF = TK * 128;               // its span of 64 columns
+  static constexpr int NST = D == 128 ? 5 : 8;        // K and V tiles in flight
+  static constexpr size_t Q = 0;                      // two query tiles
+  static constexpr size_t ST = 2 * (size_t)TILE;
+  static constexpr size_t BARS = ST + (size_t)NST * TILE;
+  // full[NST], empty[NST], q_full, q_empty, s_ready[2], p_ready[2], o_done[2], o_free[2], mma_done
+  static constexpr int NBARS = 2 * NST + 11;
+  static constexpr size_t MISC = BARS + 8 * NBARS;
+  static constexpr size_t BYTES = MISC + 64 + 1024;   // + alignment slack
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ ChunkTcArgs a) {
+  using L = Sm<D>;
+  constexpr int NST = L::NST, TOK = 128 / G;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
+  int* misc = reinterpret_cast<int*>(sm + L::MISC);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc);
+  volatile int* abort = misc + 1;
+  const uint32_t bar0 = sb + (uint32_t)L::BARS;
+  auto full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
+  auto empty = [&](int s) { return bar0 + 8u * (uint32_t)(NST + s); };
+  const uint32_t q_full = bar0 + 8u * (uint32_t)(2 * NST), q_empty = q_full + 8u;
+  auto s_ready = [&](int x) { return q_full + 8u * (uint32_t)(2 + x); };
+  auto p_ready = [&](int x) { return q_full + 8u * (uint32_t)(4 + x); };
+  auto o_done = [&](int x) { return q_full + 8u * (uint32_t)(6 + x); };
+  auto o_free = [&](int x) { return q_full + 8u * (uint32_t)(8 + x); };
+  const uint32_t mma_done = q_full + 80u;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int i0 = a.begin[blockIdx.x], i1 = a.begin[blockIdx.x + 1];
+  if (tid == 0) {
+    for (int i = 0; i < L::NBARS; ++i) {
+      const int b = i - 2 * NST;  // p_ready and o_free: the group's four warps; else one arrival
+      mbar_init(bar0 + 8u * (uint32_t)i, b == 4 || b == 5 || b == 8 || b == 9 ? 4 : 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    *abort = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(tmem_holder))),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  auto timed_out = [&] {
+    atomicOr(a.err, ERR_TIMEOUT);
+    *abort = 1;
+  };
+
+  if (warp == 0) {
+    // ---- producer ----------------------------------------------------------
+    if (lane == 0) {
+      int c = 0, nq = 0;  // tiles and items issued
+      bool ok = true;
+      for (int i = i0; i < i1 && ok; ++i) {
+        const ChunkItem it = load_item(a.items + i);
+        const ChunkReq rq = load_req(a.reqs + it.r);
+        const Work w = work_of<G>(it, rq);
+        auto tile = [&](const CUtensorMap* map, int t) {
+          if (!ok) return;
+          const int s = c % NST;
+          if (c >= NST && !(ok = wait_bar(empty(s), (uint32_t)((c / NST - 1) & 1), abort))) return;
+          const int y = key_row(a, rq, it.h, t);
+          const uint32_t dst = sb + (uint32_t)(L::ST + (size_t)s * L::TILE);
+          mbar_expect_tx(full(s), L::TILE);
+#pragma unroll
+          for (int x = 0; x < D; x += 64) tma_load_2d(dst + (uint32_t)(x / 64 * L::HALF), map, x, y, full(s));
+          ++c;
+        };
+        if (nq > 0 && !(ok = wait_bar(q_empty, (uint32_t)((nq - 1) & 1), abort))) break;
+        mbar_expect_tx(q_full, (it.keys ? 1 : 2) * L::TILE);
+        for (int x = 0; x < (it.keys ? 1 : 2); ++x)
+#pragma unroll
+          for (int d = 0; d < D; d += 64)
+            tma_load_3d(sb + (uint32_t)(L::Q + (size_t)x * L::TILE + d / 64 * L::HALF), &a.qmap, d, it.h * G,
+                        (int)rq.row0 + it.t0 + x * TOK, q_full);
+        ++nq;
+        if (it.keys) {
+          tile(&a.kmap, it.kb);
+          if (w.cnt[1] > 0) tile(&a.kmap, it.kb + 1);
+          for (int j = 0; j < w.cnt[0]; ++j) {
+            tile(&a.vmap, it.kb + 2 * j);
+            if (j + 1 < w.cnt[0]) tile(&a.kmap, it.kb + 2 * j + 2);
+            if (j < w.cnt[1]) tile(&a.vmap, it.kb + 2 * j + 1);
+            if (j + 1 < w.cnt[1]) tile(&a.kmap, it.kb + 2 * j + 3);
+          }
+        } else {
+          for (int j = it.kb; j < it.ke; ++j) {
+            tile(&a.kmap, j);
+            tile(&a.vmap, j);
+          }
+        }
+      }
+      if (!ok) timed_out();
+      // every copy issued has landed before the CTA moves on (bounded)
+      const int zero = 0;
+      for (int x = c > NST ? c - NST : 0; x < c; ++x) wait_bar(full(x % NST), (uint32_t)((x / NST) & 1), &zero);
+      if (nq > 0) wait_bar(q_full, (uint32_t)((nq - 1) & 1), &zero);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- MMA issuer ----------------------------------------------------------
+    if (lane == 0) {
+      int c = 0, nq = 0;          // tiles consumed, items
+      int ns[2] = {0, 0};         // products P V issued per group
+      int no[2] = {0, 0};         // items per group
+      bool ok = true;
+      auto wait = [&](uint32_t bar, int phase) { ok = ok && wait_bar(bar, (uint32_t)(phase & 1), abort); };
+      auto stage = [&](int k) { return sb + (uint32_t)(L::ST + (size_t)(k % NST) * L::TILE); };
+      auto score = [&](int x, int k, int qt) {  // S of group x from the K tile k and query tile qt
+        wait(full(k % NST), k / NST);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t q0 = sb + (uint32_t)(L::Q + (size_t)qt * L::TILE), k0 = stage(k);
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) {
+          const uint32_t off = (uint32_t)((e >> 2) * L::HALF + (e & 3) * 32);
+          mma_f16(tmem + (uint32_t)(x * 128), sw128_desc(q0 + off), sw128_desc(k0 + off), idesc(TK, false),
+                  e > 0 ? 1u : 0u);
+        }
+        mma_commit(s_ready(x));
+      };
+      auto value = [&](int x, int k, bool first) {  // O of group x from its P and the V tile k
+        wait(p_ready(x), ns[x]);
+        wait(full(k % NST), k / NST);
+        if (first && no[x] > 0) wait(o_free(x), no[x] - 1);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t v0 = stage(k);
+#pragma unroll
+        for (int e = 0; e < TK / 16; ++e)
+          mma_f16_ts(tmem + (uint32_t)(256 + x * 128), tmem + (uint32_t)(x * 128 + e * 8),
+                     sw128_mn_desc(v0 + (uint32_t)e * 2048u, L::HALF), idesc(D, true), first && e == 0 ? 0u : 1u);
+        ++ns[x];
+      };
+      for (int i = i0; i < i1 && ok; ++i) {
+        const ChunkItem it = load_item(a.items + i);
+        const Work w = work_of<G>(it, load_req(a.reqs + it.r));
+        wait(q_full, nq++);
+        if (it.keys) {
+          // every tile serves one group; consumed in the order of the loads
+          auto S = [&](int x, bool last) {
+            score(x, c, 0);
+            if (!ok) return;
+            mma_commit(empty(c++ % NST));
+            if (last) mma_commit(q_empty);
+          };
+          auto V = [&](int x, int j) {
+            value(x, c, j == 0);
+            if (!ok) return;
+            mma_commit(empty(c++ % NST));
+            if (j + 1 == w.cnt[x]) {
+              mma_commit(o_done(x));
+              ++no[x];
+            }
+          };
+          S(0, w.n == 1);
+          if (w.cnt[1] > 0 && ok) S(1, w.n == 2);
+          for (int j = 0; j < w.cnt[0] && ok; ++j) {
+            V(0, j);
+            if (j + 1 < w.cnt[0] && ok) S(0, 2 * j + 3 == w.n);
+            if (j < w.cnt[1] && ok) V(1, j);
+            if (j + 1 < w.cnt[1] && ok) S(1, 2 * j + 4 == w.n);
+          }
+        } else {
+          const int k0 = c;  // K tile j is k0 + 2 j, V tile j the one after it
+          if (w.cnt[0] > 0) score(0, k0, 0);
+          score(1, k0, 1);
+          if (ok) mma_commit(empty(k0 % NST));
+          if (ok && w.n == 1) mma_commit(q_empty);
+          for (int j = 0; j < w.n && ok; ++j) {
+            const int kv = k0 + 2 * j + 1;
+            if (j < w.cnt[0]) {
+              value(0, kv, j == 0);
+              if (ok && j + 1 == w.cnt[0]) {
+                mma_commit(o_done(0));
+                ++no[0];
+              }
+              if (j + 1 < w.cnt[0]) score(0, kv + 1, 0);
+            }
+            value(1, kv, j == 0);
+            if (!ok) break;
+            mma_commit(empty(kv % NST));
+            if (j + 1 == w.n) {
+              mma_commit(o_done(1));
+              ++no[1];
+            } else {
+              score(1, kv + 1, 1);
+              if (!ok) break;
+              mma_commit(empty((kv + 1) % NST));
+              if (j + 2 == w.n) mma_commit(q_empty);
+            }
+          }
+          c += 2 * w.n;
+        }
+      }
+      if (!ok) timed_out();
+      // every product issued has completed before TMEM is released (bounded)
+      mma_commit(mma_done);
+      const int zero = 0;
+      wait_bar(mma_done, 0u, &zero);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---- softmax and epilogue: thread = row ------------------------------------
+    const int x = (warp - 4) >> 2, quad = warp & 3, row = 32 * quad + lane;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const uint32_t ts = tmem + lanes + (uint32_t)(x * 128), to = tmem + lanes + (uint32_t)(256 + x * 128);
+    const float sc = 1.4426950408889634f / sqrtf((float)D);
+    int ns = 0, no = 0;  // tiles and items of this group
+    int c = 0;           // tiles of all items (the ring's)
+    bool ok = true;
+    for (int i = i0; i < i1 && ok; ++i) {
+      const ChunkItem it = load_item(a.items + i);
+      const ChunkReq rq = load_req(a.reqs + it.r);
+      const Work w = work_of<G>(it, rq);
+      const int total = rq.cached + rq.nnew;
+      const int cnt = w.cnt[x];
+      const int first = it.t0 + (it.keys ? 0 : x * TOK);  // the tile's first token
+      const int t = first + row / G;
+      const int sees = rq.cached + t;                     // last slot the row sees
+      float m = NEG, l = 0.f;
+      for (int j = 0; j < cnt; ++j) {
+        const int kt = it.kb + (it.keys ? 2 * j + x : j);  // key tile
+        ok = __all_sync(0xffffffffu, wait_bar(s_ready(x), (uint32_t)(ns & 1), abort));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t r[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_load32(ts + (uint32_t)(32 * q), r[q]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_arrived(r[q]);
+        if (kt * TK + TK - 1 > rq.cached + first) {  // some row of the tile does not see all of these keys
+          const int keep = sees - kt * TK;           // columns 0 .. keep are seen
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * q + e > keep) r[q][e] = 0xff800000u;  // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          mx[q] = __uint_as_float(r[q][0]);
+#pragma unroll
+          for (int e = 1; e < 32; ++e) mx[q] = fmaxf(mx[q], __uint_as_float(r[q][e]));
+        }
+        const float top = sc * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (j == 0) {
+          m = fmaxf(m, top);
+        } else {
+          const bool grow = top > m + LAZY;
+          if (__any_sync(0xffffffffu, grow)) {
+            // the products issued before this S have completed: O is at rest
+            const float mn = grow ? top : m, f = ex2f(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+              uint32_t o[32];
+              tmem_load32(to + (uint32_t)d, o);
+              tmem_wait_ld();
+              tmem_arrived(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_store32(to + (uint32_t)d, o);
+            }
+          }
+        }
+        const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m, -m);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 z = fma2(make_float2(__uint_as_float(r[q][2 * e]), __uint_as_float(r[q][2 * e + 1])), sc2, nm2);
+            z.x = ex2f(z.x);
+            z.y = ex2f(z.y);
+            sum[e & 1] = add2(sum[e & 1], z);
+            p[e] = pack_bf16(z.x, z.y);
+          }
+          tmem_store16(ts + (uint32_t)(16 * q), p);
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        // the last key tile may hold slots past the request's tokens: their
+        // weights are 0, but 0 x inf or NaN would reach O; their V rows are
+        // zeroed by the group that takes the tile first
+        const bool last_tile = kt + 1 == it.ke && kt * TK + TK > total;
+        const bool mine = it.keys || (x == 0 ? true : w.cnt[0] < w.n);
+        if (last_tile && mine) {
+          const int k = c + 2 * w.n - 1;  // the item's last load
+          ok = __all_sync(0xffffffffu, wait_bar(full(k % NST), (uint32_t)((k / NST) & 1), abort));
+          if (!ok) break;
+          if (kt * TK + row >= total) {
+            unsigned char* v = sm + L::ST + (size_t)(k % NST) * L::TILE + (size_t)row * 128;
+#pragma unroll
+            for (int d = 0; d < D / 64; ++d)
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                reinterpret_cast<uint4*>(v + (size_t)d * L::HALF)[e] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready(x));
+        ++ns;
+      }
+      if (!ok) break;
+      // ---- epilogue ----
+      const int part = x == 0 ? it.part_a : it.part_b;
+      const bool valid = t < rq.nnew;
+      if (cnt == 0) {  // nothing of this range is seen by the tile, or there is no second part
+        if (!it.keys && part >= 0) {
+          float* po = a.part + (size_t)part * chunk_part_floats(D) + 128 * D;
+          po[row] = NEG;
+          po[128 + row] = 0.f;
+        }
+      } else {
+        ok = __all_sync(0xffffffffu, wait_bar(o_done(x), (uint32_t)(no & 1), abort));
+        if (!ok) break;
+        tc_fence_after();
+        const size_t at = (size_t)(rq.row0 + t) * a.Hq + it.h * G + row % G;
+        const float inv = 1.f / l;
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          uint32_t o[32];
+          tmem_load32(to + (uint32_t)d, o);
+          tmem_wait_ld();
+          tmem_arrived(o);
+          if (valid && part < 0) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * D + d);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t u[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                u[k] = pack_bf16(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+              dst[e] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+          } else if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(a.part + (size_t)part * chunk_part_floats(D)) + (size_t)(d / 4) * 128 + row;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[(size_t)e * 128] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free(x));
+        ++no;
+        if (valid && part < 0 && a.stat) a.stat[at] = make_float2(m, inv);
+        if (part >= 0) {
+          float* po = a.part + (size_t)part * chunk_part_floats(D) + 128 * D;
+          po[row] = m;
+          po[128 + row] = l;
+        }
+      }
+      c += 2 * w.n;
+    }
+    if (!ok && lane == 0) timed_out();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+  }
+}
+
+// Joins the partials of a query tile: thread = (row, slice of d).
+template <int D, int G>
+__global__ void __launch_bounds__(256) k_chunk_join(const __grid_constant__ ChunkTcArgs a) {
+  const ChunkJoin jn = load_item(a.joins + blockIdx.x);
+  const ChunkReq rq = load_req(a.reqs + jn.r);
+  const int row = threadIdx.x & 127, half = threadIdx.x >> 7;
+  const int t = jn.t0 + row / G;
+  if (t >= rq.nnew) return;
+  const float* base = a.part + (size_t)jn.first * chunk_part_floats(D);
+  float M = NEG;
+  for (int p = 0; p < jn.n; ++p) M = fmaxf(M, __ldg(base + p * chunk_part_floats(D) + 128 * D + row));
+  float l = 0.f;
+  float4 acc[2] = {};
+  const int d0 = (blockIdx.y * 2 + half) * 8;  // eight dimensions
+  for (int p = 0; p < jn.n; ++p) {
+    const float* q = base + p * chunk_part_floats(D);
+    const float lp = __ldg(q + 128 * D + 128 + row);
+    if (lp == 0.f) continue;  // a part that the row does not see
+    const float f = ex2f(__ldg(q + 128 * D + row) - M);
+    l = fmaf(f, lp, l);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float4 o = __ldg(reinterpret_cast<const float4*>(q) + (size_t)(d0 / 4 + e) * 128 + row);
+      acc[e].x = fmaf(f, o.x, acc[e].x);
+      acc[e].y = fmaf(f, o.y, acc[e].y);
+      acc[e].z = fmaf(f, o.z, acc[e].z);
+      acc[e].w = fmaf(f, o.w, acc[e].w);
+    }
+  }
+  const float inv = 1.f / l;
+  const size_t at = (size_t)(rq.row0 + t) * a.Hq + jn.h * G + row % G;
+  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * D + d0) =
+      make_uint4(pack_bf16(acc[0].x * inv, acc[0].y * inv), pack_bf16(acc[0].z * inv, acc[0].w * inv),
+                 pack_bf16(acc[1].x * inv, acc[1].y * inv), pack_bf16(acc[1].z * inv, acc[1].w * inv));
+  if (d0 == 0 && a.stat) a.stat[at] = make_float2(M, inv);
+}
+
+// ---- weights -----------------------------------------------------------------
+
+template <int D>
+struct SmW {
+  static constexpr int TILE = TK * D * 2;
+  static constexpr int HALF = TK * 128;
+  static constexpr int NQ = D == 128 ? 3 : 6;          // query tiles in flight
+  static constexpr size_t K = 0;                       // two pages, two tiles each
+  static constexpr size_t Q = 4 * (size_t)TILE;
+  static constexpr size_t STAT = Q + (size_t)NQ * TILE;  // [2][128] (-maximum, 1 / sum)
+  static constexpr size_t BARS = STAT + 2 * 128 * 8;
+  // k_full[2], k_empty[2], q_full[NQ], q_empty[NQ], t_full[2], t_empty[2], s_ready[2][2], s_free[2][2], mma_done
+  static constexpr int NBARS = 8 + 2 * NQ + 8 + 1;
+  static constexpr size_t MISC = BARS + 8 * NBARS;
+  static constexpr size_t BYTES = MISC + 64;           // the base is aligned to 1 KiB by its declaration
+  static_assert(BYTES <= 232448, "227 KiB a CTA");
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(NT, 1) k_chunk_weights_tc(const __grid_constant__ ChunkTcArgs a) {
+  using L = SmW<D>;
+  constexpr int NQ = L::NQ, TOK = 128 / G;
+  extern __shared__ __align__(1024) unsigned char smem_base[];
+  unsigned char* sm = smem_base;
+  const uint32_t sb = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
+  if (sb & 1023u) {  // the swizzled tiles need it; there is no room to align here
+    if (threadIdx.x == 0) atomicOr(a.err, ERR_BAD_COUNT);
+    return;
+  }
+  int* misc = reinterpret_cast<int*>(sm + L::MISC);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc);
+  volatile int* abort = misc + 1;
+  const uint32_t bar0 = sb + (uint32_t)L::BARS;
+  auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+  auto k_full = [&](int b) { return bar(b); };
+  auto k_empty = [&](int b) { return bar(2 + b); };
+  auto q_full = [&](int s) { return bar(4 + s); };
+  auto q_empty = [&](int s) { return bar(4 + NQ + s); };
+  auto t_full = [&](int b) { return bar(4 + 2 * NQ + b); };
+  auto t_empty = [&](int b) { return bar(6 + 2 * NQ + b); };
+  auto s_ready = [&](int x, int b) { return bar(8 + 2 * NQ + 2 * x + b); };
+  auto s_free = [&](int x, int b) { return bar(12 + 2 * NQ + 2 * x + b); };
+  const uint32_t mma_done = bar(16 + 2 * NQ);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int i0 = a.wbegin[blockIdx.x], i1 = a.wbegin[blockIdx.x + 1];
+  if (tid == 0) {
+    for (int i = 0; i < L::NBARS; ++i) {
+      int n = 1;
+      if (i >= 6 + 2 * NQ && i < 8 + 2 * NQ) n = 8;    // t_empty: both groups' warps
+      if (i >= 12 + 2 * NQ && i < 16 + 2 * NQ) n = 4;  // s_free: a group's warps
+      mbar_init(bar(i), (uint32_t)n);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    *abort = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(tmem_holder))),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  auto timed_out = [&] {
+    atomicOr(a.err, ERR_TIMEOUT);
+    *abort = 1;
+  };
+
+  if (warp == 0) {
+    // ---- producer: an item's two K tiles, then its query tiles -------------------
+    if (lane == 0) {
+      int c = 0, n = 0;  // query tiles and items issued
+      bool ok = true;
+      for (int i = i0; i < i1 && ok; ++i, ++n) {
+        const WeightItem it = load_item(a.witems + i);
+        const ChunkReq rq = load_req(a.reqs + it.r);
+        const int b = n & 1;
+        if (n >= 2 && !(ok = wait_bar(k_empty(b), (uint32_t)((n / 2 - 1) & 1), abort))) break;
+        const int y = key_row(a, rq, it.h, 2 * it.page);
+        mbar_expect_tx(k_full(b), 2 * L::TILE);
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int d = 0; d < D; d += 64)
+            tma_load_2d(sb + (uint32_t)(L::K + (size_t)(2 * b + x) * L::TILE + d / 64 * L::HALF), &a.kmap, d, y + x * TK,
+                        k_full(b));
+        for (int q = it.qb; q < it.qe; ++q, ++c) {
+          const int s = c % NQ;
+          if (c >= NQ && !(ok = wait_bar(q_empty(s), (uint32_t)((c / NQ - 1) & 1), abort))) break;
+          mbar_expect_tx(q_full(s), L::TILE);
+#pragma unroll
+          for (int d = 0; d < D; d += 64)
+            tma_load_3d(sb + (uint32_t)(L::Q + (size_t)s * L::TILE + d / 64 * L::HALF), &a.qmap, d, it.h * G,
+                        (int)rq.row0 + q * TOK, q_full(s));
+        }
+      }
+      if (!ok) timed_out();
+      const int zero = 0;
+      for (int x = c > NQ ? c - NQ : 0; x < c; ++x) wait_bar(q_full(x % NQ), (uint32_t)((x / NQ) & 1), &zero);
+      for (int x = n > 2 ? n - 2 : 0; x < n; ++x) wait_bar(k_full(x & 1), (uint32_t)((x / 2) & 1), &zero);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- MMA issuer ----------------------------------------------------------
+    if (lane == 0) {
+      int c = 0, n = 0;
+      bool ok = true;
+      auto wait = [&](uint32_t b, int phase) { ok = ok && wait_bar(b, (uint32_t)(phase & 1), abort); };
+      for (int i = i0; i < i1 && ok; ++i, ++n) {
+        const WeightItem it = load_item(a.witems + i);
+        const int b = n & 1;
+        wait(k_full(b), n / 2);
+        for (int q = it.qb; q < it.qe && ok; ++q, ++c) {
+          const int s = c % NQ, z = c & 1;
+          wait(q_full(s), c / NQ);
+          const uint32_t q0 = sb + (uint32_t)(L::Q + (size_t)s * L::TILE);
+          for (int x = 0; x < 2 && ok; ++x) {
+            if (c >= 2) wait(s_free(x, z), c / 2 - 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t k0 = sb + (uint32_t)(L::K + (size_t)(2 * b + x) * L::TILE);
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e) {
+              const uint32_t off = (uint32_t)((e >> 2) * L::HALF + (e & 3) * 32);
+              mma_f16(tmem + (uint32_t)(x * 256 + z * 128), sw128_desc(k0 + off), sw128_desc(q0 + off),
+                      idesc(128, false), e > 0 ? 1u : 0u);
+            }
+            mma_commit(s_ready(x, z));
+          }
+          if (ok) mma_commit(q_empty(s));
+        }
+        if (ok) mma_commit(k_empty(b));
+      }
+      if (!ok) timed_out();
+      mma_commit(mma_done);
+      const int zero = 0;
+      wait_bar(mma_done, 0u, &zero);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---- statistics of the query tiles -------------------------------------------
+    int c = 0;
+    bool ok = true;
+    for (int i = i0; i < i1 && ok; ++i) {
+      const WeightItem it = load_item(a.witems + i);
+      const ChunkReq rq = load_req(a.reqs + it.r);
+      for (int q = it.qb; q < it.qe; ++q, ++c) {
+        const int b = c & 1;
+        if (c >= 2) ok = __all_sync(0xffffffffu, wait_bar(t_empty(b), (uint32_t)((c / 2 - 1) & 1), abort));
+        if (!ok) break;
+        float2* dst = reinterpret_cast<float2*>(sm + L::STAT) + b * 128;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = 32 * k + lane, t = q * TOK + row / G;
+          float2 st = make_float2(0.f, 0.f);
+          if (t < rq.nnew) st = __ldg(a.stat + (size_t)(rq.row0 + t) * a.Hq + it.h * G + row % G);
+          dst[row] = make_float2(-st.x, st.y);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(t_full(b));
+      }
+    }
+    if (!ok && lane == 0) timed_out();
+  } else if (warp >= 4) {
+    // ---- sums: thread = key ---------------------------------------------------------
+    const int x = (warp - 4) >> 2, quad = warp & 3, key = 32 * quad + lane;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const float sc = 1.4426950408889634f / sqrtf((float)D);
+    const float2 sc2 = make_float2(sc, sc);
+    int c = 0;
+    bool ok = true;
+    for (int i = i0; i < i1 && ok; ++i) {
+      const WeightItem it = load_item(a.witems + i);
+      const ChunkReq rq = load_req(a.reqs + it.r);
+      const int slot_i = it.page * PAGE + x * TK + key;  // this thread's logical slot
+      float2 w[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      for (int q = it.qb; q < it.qe; ++q, ++c) {
+        const int z = c & 1;
+        ok = __all_sync(0xffffffffu, wait_bar(t_full(z), (uint32_t)((c / 2) & 1), abort)) &&
+             __all_sync(0xffffffffu, wait_bar(s_ready(x, z), (uint32_t)((c / 2) & 1), abort));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t ts = tmem + lanes + (uint32_t)(x * 256 + z * 128);
+        const float4* st = reinterpret_cast<const float4*>(sm + L::STAT) + z * 64;
+        // columns lo .. hi - 1 count: the rows of tokens that see the slot and exist
+        const int lo = (slot_i - rq.cached - q * TOK) * G, hi = (rq.nnew - q * TOK) * G;
+        const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= 128);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t r[32];
+          tmem_load32(ts + (uint32_t)(32 * h), r);
+          tmem_wait_ld();
+          tmem_arrived(r);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float4 t2 = st[16 * h + e];  // (-m, 1/l) of two columns
+            float2 v = fma2(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), sc2,
+                            make_float2(t2.x, t2.z));
+            v.x = ex2f(v.x);
+            v.y = ex2f(v.y);
+            if (!whole) {
+              const int col = 32 * h + 2 * e;
+              v.x = col >= lo && col < hi ? v.x : 0.f;
+              v.y = col + 1 >= lo && col + 1 < hi ? v.y : 0.f;
+            }
+            w[e & 1] = fma2(v, make_float2(t2.y, t2.w), w[e & 1]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(s_free(x, z));
+          mbar_arrive(t_empty(z));
+        }
+      }
+      if (!ok) break;
+      const float sum = (w[0].x + w[0].y) + (w[1].x + w[1].y);
+      if (it.part >= 0) {
+        a.wpart[(size_t)it.part * PAGE + x * TK + key] = sum;
+      } else if (slot_i < rq.cached + rq.nnew && rq.slot >= 0 && rq.slot < a.M) {
+        a.weights[(((size_t)a.layer * a.M + rq.slot) * a.Hkv + it.h) * a.cap + slot_i] += sum;
+      }
+    }
+    if (!ok && lane == 0) timed_out();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+  }
+}
+
+// Adds the partial sums of a page, in the order of its parts.
+__global__ void __launch_bounds__(PAGE) k_chunk_weights_join(const __grid_constant__ ChunkTcArgs a) {
+  const WeightJoin jn = load_item(a.wjoins + blockIdx.x);
+  const ChunkReq rq = load_req(a.reqs + jn.r);
+  const int i = jn.page * PAGE + (int)threadIdx.x;
+  if (i >= rq.cached + rq.nnew || rq.slot < 0 || rq.slot >= a.M) return;
+  float w = 0.f;
+  for (int p = 0; p < jn.n; ++p) w += __ldg(a.wpart + (size_t)(jn.first + p) * PAGE + threadIdx.x);
+  a.weights[(((size_t)a.layer * a.M + rq.slot) * a.Hkv + jn.h) * a.cap + i] += w;
+}
+
+template <int D, int G>
+cudaError_t attention(const ChunkTcArgs& a, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(k_chunk_tc<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sm<D>::BYTES);
+  if (e != cudaSuccess) return e;
+  k_chunk_tc<D, G><<<dim3((unsigned)a.grid), NT, Sm<D>::BYTES, s>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess || a.n_joins == 0) return e;
+  k_chunk_join<D, G><<<dim3((unsigned)a.n_joins, D / 16), 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+template <int D, int G>
+cudaError_t weights(const ChunkTcArgs& a, cudaStream_t s) {
+  cudaError_t e =
+      cudaFuncSetAttribute(k_chunk_weights_tc<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SmW<D>::BYTES);
+  if (e != cudaSuccess) return e;
+  k_chunk_weights_tc<D, G><<<dim3((unsigned)a.wgrid), NT, SmW<D>::BYTES, s>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess || a.n_wjoins == 0) return e;
+  k_chunk_weights_join<<<dim3((unsigned)a.n_wjoins), PAGE, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_tc(const ChunkTcArgs& a, cudaStream_t s) {
+  if (a.grid < 1 || !chunk_tc_shape(a.D, a.G)) return cudaErrorInvalidValue;
+  if (a.D == 128) return a.G == 4 ? attention<128, 4>(a, s) : attention<128, 2>(a, s);
+  return a.G == 4 ? attention<64, 4>(a, s) : attention<64, 2>(a, s);
+}
+cudaError_t launch_chunk_weights_tc(const ChunkTcArgs& a, cudaStream_t s) {
+  if (a.wgrid < 1 || !chunk_tc_shape(a.D, a.G)) return cudaErrorInvalidValue;
+  if (a.D == 128) return a.G == 4 ? weights<128, 4>(a, s) : weights<128, 2>(a, s);
+  return a.G == 4 ? weights<64, 4>(a, s) : weights<64, 2>(a, s);
+}
+
+}  // namespace gp

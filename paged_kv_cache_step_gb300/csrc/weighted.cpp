@@ -54,6 +54,152 @@ gp_status check_new_tokens(gp_ctx* c, int32_t layer, int32_t n, const gp_request
   return GP_OK;
 }
 
+// ---- work of the tensor-core chunk kernels --------------------------------------
+
+// Work laid end to end and cut into one even share a CTA, of at least `least`.
+// A job is `n` tiles that cost `cost` each, and every piece of it `fixed` more.
+// begin: the first piece of every CTA, and the number of pieces.
+struct Job {
+  int n, cost;
+};
+struct Piece {
+  int job, from, to;
+};
+void cut_even(const std::vector<Job>& jobs, int ctas, int fixed, int least, std::vector<Piece>& pieces,
+              std::vector<int32_t>& begin) {
+  int64_t total = 0;
+  for (const Job& j : jobs) total += fixed + (int64_t)j.n * j.cost;
+  // pieces add their fixed cost and are not slivers, so an exact share may need
+  // one CTA too many: the share grows until it does not
+  for (int64_t share = std::max<int64_t>(least, (total + ctas - 1) / ctas);; share += std::max<int64_t>(1, share / 64)) {
+    pieces.clear();
+    begin.assign(1, 0);
+    int64_t room = share;
+    for (int k = 0; k < (int)jobs.size(); ++k) {
+      const Job& j = jobs[k];
+      for (int at = 0; at < j.n;) {
+        if (room < share && room < fixed + (int64_t)j.cost * std::min(j.n - at, 2)) {
+          begin.push_back((int32_t)pieces.size());
+          room = share;
+        }
+        int take = (int)std::min<int64_t>(j.n - at, std::max<int64_t>(1, (room - fixed) / j.cost));
+        if (j.n - at - take == 1) ++take;  // no sliver of one tile
+        pieces.push_back({k, at, at + take});
+        at += take;
+        room -= fixed + (int64_t)j.cost * take;
+      }
+    }
+    begin.push_back((int32_t)pieces.size());
+    if ((int)begin.size() - 1 <= ctas) return;
+  }
+}
+
+struct ChunkPlan {
+  std::vector<ChunkItem> items;
+  std::vector<ChunkJoin> joins;
+  std::vector<int32_t> begin;
+  int parts = 0;
+  std::vector<WeightItem> witems;
+  std::vector<WeightJoin> wjoins;
+  std::vector<int32_t> wbegin;
+  int wparts = 0;
+};
+
+// Attention: pairs of query tiles that follow each other (a key tile costs two
+// products' time), or the last tile alone with its key tiles split between
+// the groups (one).  A piece's fixed cost is the time to load Q and to empty
+// the pipeline, about two tiles.
+void plan_chunk(int n, const int32_t* cached, const int32_t* fresh, int Hkv, int G, int ctas, bool weights,
+                ChunkPlan* p) {
+  const int tok = 128 / G;
+  std::vector<Job> jobs;
+  std::vector<ChunkItem> of;
+  for (int r = 0; r < n; ++r) {
+    const int tiles = (fresh[r] + tok - 1) / tok;
+    for (int h = 0; h < Hkv; ++h)
+      for (int t = 0; t < tiles; t += 2) {
+        const bool alone = t + 1 == tiles;
+        const int last = std::min((t + (alone ? 1 : 2)) * tok, fresh[r]);
+        jobs.push_back({(cached[r] + last + 127) / 128, alone ? 1 : 2});
+        of.push_back({r, h, t * tok, alone, 0, 0, -1, -1});
+      }
+  }
+  std::vector<Piece> pieces;
+  cut_even(jobs, ctas, 2, 6, pieces, p->begin);
+  for (size_t k = 0; k < pieces.size();) {
+    size_t e = k;
+    while (e < pieces.size() && pieces[e].job == pieces[k].job) ++e;
+    const ChunkItem& job = of[pieces[k].job];
+    const int count = (int)(e - k), first = p->parts;
+    if (job.keys) {
+      int parts = 0;
+      for (size_t i = k; i < e; ++i) parts += pieces[i].to - pieces[i].from > 1 ? 2 : 1;
+      int part = first;
+      for (size_t i = k; i < e; ++i) {
+        ChunkItem it = job;
+        it.kb = pieces[i].from;
+        it.ke = pieces[i].to;
+        if (parts > 1) {
+          it.part_a = part++;
+          if (it.ke - it.kb > 1) it.part_b = part++;
+        }
+        p->items.push_back(it);
+      }
+      if (parts > 1) {
+        p->joins.push_back({job.r, job.h, job.t0, first, parts, {}});
+        p->parts += parts;
+      }
+    } else {
+      for (size_t i = k; i < e; ++i) {
+        ChunkItem it = job;
+        it.kb = pieces[i].from;
+        it.ke = pieces[i].to;
+        if (count > 1) {
+          it.part_a = first + (int)(i - k);
+          it.part_b = first + count + (int)(i - k);
+        }
+        p->items.push_back(it);
+      }
+      if (count > 1) {
+        p->joins.push_back({job.r, job.h, job.t0, first, count, {}});
+        p->joins.push_back({job.r, job.h, job.t0 + tok, first + count, count, {}});
+        p->parts += 2 * count;
+      }
+    }
+    k = e;
+  }
+  if (!weights) return;
+  // Weights: a page against the query tiles that see it; loading the page
+  // costs about two query tiles' products.
+  jobs.clear();
+  std::vector<WeightItem> wof;
+  for (int r = 0; r < n; ++r) {
+    const int tiles = (fresh[r] + tok - 1) / tok, pages = (cached[r] + fresh[r] + kPage - 1) / kPage;
+    if (fresh[r] == 0) continue;
+    for (int h = 0; h < Hkv; ++h)
+      for (int pg = 0; pg < pages; ++pg) {
+        const int q0 = std::max(0, pg * kPage - cached[r]) / tok;
+        jobs.push_back({tiles - q0, 1});
+        wof.push_back({r, h, pg, q0, tiles, -1, {}});
+      }
+  }
+  cut_even(jobs, ctas, 2, 6, pieces, p->wbegin);
+  for (size_t k = 0; k < pieces.size();) {
+    size_t e = k;
+    while (e < pieces.size() && pieces[e].job == pieces[k].job) ++e;
+    const WeightItem& job = wof[pieces[k].job];
+    for (size_t i = k; i < e; ++i) {
+      WeightItem it = job;
+      it.qb = job.qb + pieces[i].from;
+      it.qe = job.qb + pieces[i].to;
+      it.part = e - k > 1 ? p->wparts++ : -1;
+      p->witems.push_back(it);
+    }
+    if (e - k > 1) p->wjoins.push_back({job.r, job.h, job.page, p->wparts - (int)(e - k), (int)(e - k), {}});
+    k = e;
+  }
+}
+
 }  // namespace
 
 gp_status gp_append_tokens(gp_ctx* c, int32_t layer, int32_t n, const gp_request* reqs, const int32_t* num_cached,
@@ -150,23 +296,44 @@ gp_status gp_chunk_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_reque
   if (misaligned(q_dev) || misaligned(out_dev) || misaligned(c->k_cache) || misaligned(c->v_cache))
     return fail(c, GP_ERR_INVALID, "queries, outputs and caches must be 16-byte aligned");
   if ((st = ready_call(c)) != GP_OK) return st;
+  // The tensor-core kernels take bf16 caches and queries (AUTO and
+  // TENSOR_CORE), the CUDA-core ones everything.
+  const bool tc = c->attn_tc_ok && c->scan_kernel != GP_SCAN_CUDA_CORE && g.q_dtype == GP_DTYPE_BF16 &&
+                  chunk_tc_shape(g.head_dim, G) && rows < (1ll << 31) - 256;
+  if (c->scan_kernel == GP_SCAN_TENSOR_CORE && !tc)
+    return fail(c, GP_ERR_UNSUPPORTED, "the tensor-core chunk kernels cannot take this cache, shape or query type");
   if ((st = wait_shared_pages(c, n, reqs)) != GP_OK) return st;
   const int maxp = g.max_pages_per_req, tokens = CHUNK_ROWS / G;
-  // query tiles, those that see most first; key tiles, the first (seen by most) first
   std::vector<ChunkTile> tiles, wtiles;
-  for (int r = 0; r < n; ++r) {
-    if (num_new[r] == 0) continue;
-    for (int t = (num_new[r] - 1) / tokens * tokens; t >= 0; t -= tokens)
-      for (int h = 0; h < Hkv; ++h) tiles.push_back({r, h, t, 0});
-    if (weights_dev)
-      for (int s = 0; s < num_cached[r] + num_new[r]; s += CHUNK_KEYS)
-        for (int h = 0; h < Hkv; ++h) wtiles.push_back({r, h, s, 0});
+  ChunkPlan plan;
+  if (tc) {
+    plan_chunk(n, num_cached, num_new, Hkv, G, c->sms, weights_dev != nullptr, &plan);
+  } else {
+    // query tiles, those that see most first; key tiles, the first (seen by most) first
+    for (int r = 0; r < n; ++r) {
+      if (num_new[r] == 0) continue;
+      for (int t = (num_new[r] - 1) / tokens * tokens; t >= 0; t -= tokens)
+        for (int h = 0; h < Hkv; ++h) tiles.push_back({r, h, t, 0});
+      if (weights_dev)
+        for (int s = 0; s < num_cached[r] + num_new[r]; s += CHUNK_KEYS)
+          for (int h = 0; h < Hkv; ++h) wtiles.push_back({r, h, s, 0});
+    }
   }
-  Layout lay;
+  Layout lay, scratch;
   const size_t at_req = lay.take(sizeof(ChunkReq) * (size_t)n), at_bt = lay.take(sizeof(int32_t) * (size_t)n * maxp);
-  const size_t at_tiles = lay.take(sizeof(ChunkTile) * tiles.size());
-  const size_t at_wtiles = lay.take(sizeof(ChunkTile) * wtiles.size());
+  std::vector<std::pair<size_t, std::pair<const void*, size_t>>> tables;
+  auto table = [&](const auto& v) {
+    const size_t bytes = sizeof(v[0]) * v.size(), at = lay.take(bytes);
+    tables.push_back({at, {v.data(), bytes}});
+    return at;
+  };
+  const size_t at_tiles = table(tiles), at_wtiles = table(wtiles);
+  const size_t at_items = table(plan.items), at_begin = table(plan.begin), at_joins = table(plan.joins);
+  const size_t at_witems = table(plan.witems), at_wbegin = table(plan.wbegin), at_wjoins = table(plan.wjoins);
+  const size_t at_part = scratch.take(sizeof(float) * chunk_part_floats(g.head_dim) * (size_t)plan.parts);
+  const size_t at_wpart = scratch.take(sizeof(float) * kPage * (size_t)plan.wparts);
   if (weights_dev && (st = ensure(c, c->wstat, sizeof(float2) * (size_t)rows * g.num_q_heads)) != GP_OK) return st;
+  if ((st = ensure(c, c->chunk, scratch.bytes)) != GP_OK) return st;
   StagingSlot* slot = nullptr;
   if ((st = staging_take(c, lay.bytes, &slot)) != GP_OK) return st;
   char* host = static_cast<char*>(slot->pinned);
@@ -177,10 +344,52 @@ gp_status gp_chunk_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_reque
     std::memcpy(host + at_bt + sizeof(int32_t) * (size_t)r * maxp, reqs[r].block_table,
                 sizeof(int32_t) * reqs[r].num_pages);
   }
-  std::memcpy(host + at_tiles, tiles.data(), sizeof(ChunkTile) * tiles.size());
-  std::memcpy(host + at_wtiles, wtiles.data(), sizeof(ChunkTile) * wtiles.size());
+  for (const auto& t : tables)
+    if (t.second.second) std::memcpy(host + t.first, t.second.first, t.second.second);
   if ((st = staging_upload(c, *slot, lay.bytes)) != GP_OK) return st;
   const char* dev = static_cast<char*>(slot->dev.p);
+  const ChunkReq* dreqs = reinterpret_cast<const ChunkReq*>(dev + at_req);
+  const int32_t* dbt = reinterpret_cast<const int32_t*>(dev + at_bt);
+  float2* stat = weights_dev ? static_cast<float2*>(c->wstat.p) : nullptr;
+  if (tc) {
+    ChunkTcArgs a{};
+    a.kmap = c->kmap;
+    a.vmap = c->vmap;
+    const cuuint64_t dims[3] = {(cuuint64_t)g.head_dim, (cuuint64_t)g.num_q_heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)g.head_dim * 2, (cuuint64_t)g.head_dim * 2 * g.num_q_heads};
+    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+    if (!encode_bf16_map(&a.qmap, 3, q_dev, dims, strides, box))
+      return fail(c, GP_ERR_CUDA, "no tensor map for the queries");
+    a.num_pages_total = g.num_pages;
+    a.layer = layer;
+    a.Hq = g.num_q_heads;
+    a.Hkv = Hkv;
+    a.D = g.head_dim;
+    a.G = G;
+    a.M = g.max_slots;
+    a.cap = (int64_t)maxp * kPage;
+    a.reqs = dreqs;
+    a.bt = dbt;
+    a.items = reinterpret_cast<const ChunkItem*>(dev + at_items);
+    a.begin = reinterpret_cast<const int32_t*>(dev + at_begin);
+    a.grid = (int)plan.begin.size() - 1;
+    a.joins = reinterpret_cast<const ChunkJoin*>(dev + at_joins);
+    a.n_joins = (int)plan.joins.size();
+    a.witems = reinterpret_cast<const WeightItem*>(dev + at_witems);
+    a.wbegin = reinterpret_cast<const int32_t*>(dev + at_wbegin);
+    a.wgrid = (int)plan.wbegin.size() - 1;
+    a.wjoins = reinterpret_cast<const WeightJoin*>(dev + at_wjoins);
+    a.n_wjoins = (int)plan.wjoins.size();
+    a.out = out_dev;
+    a.stat = stat;
+    a.weights = weights_dev;
+    a.part = reinterpret_cast<float*>(static_cast<char*>(c->chunk.p) + at_part);
+    a.wpart = reinterpret_cast<float*>(static_cast<char*>(c->chunk.p) + at_wpart);
+    a.err = c->err_dev;
+    st = timed_launch(c, GP_KERNEL_CHUNK, "chunk_attention", [&] { return launch_chunk_tc(a, c->stream); });
+    if (st != GP_OK || !weights_dev) return st;
+    return timed_launch(c, GP_KERNEL_WEIGHTS, "chunk_weights", [&] { return launch_chunk_weights_tc(a, c->stream); });
+  }
   ChunkArgs a{};
   a.k_cache = c->k_cache;
   a.v_cache = c->v_cache;
@@ -194,16 +403,16 @@ gp_status gp_chunk_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_reque
   a.G = G;
   a.M = g.max_slots;
   a.cap = (int64_t)maxp * kPage;
-  a.reqs = reinterpret_cast<const ChunkReq*>(dev + at_req);
+  a.reqs = dreqs;
   a.n = n;
-  a.bt = reinterpret_cast<const int32_t*>(dev + at_bt);
+  a.bt = dbt;
   a.tiles = reinterpret_cast<const ChunkTile*>(dev + at_tiles);
   a.n_tiles = (int)tiles.size();
   a.wtiles = reinterpret_cast<const ChunkTile*>(dev + at_wtiles);
   a.n_wtiles = (int)wtiles.size();
   a.q = q_dev;
   a.out = out_dev;
-  a.stat = weights_dev ? static_cast<float2*>(c->wstat.p) : nullptr;
+  a.stat = stat;
   a.weights = weights_dev;
   a.err = c->err_dev;
   st = timed_launch(c, GP_KERNEL_CHUNK, "chunk_attention", [&] { return launch_chunk(a, c->stream); });

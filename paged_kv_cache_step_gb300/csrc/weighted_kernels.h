@@ -145,4 +145,63 @@ struct ChunkArgs {
 cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t s);
 cudaError_t launch_chunk_weights(const ChunkArgs& a, cudaStream_t s);
 
+// Tensor-core kernels (bf16 caches and queries).  A query tile is 128 rows,
+// 128 / G tokens of the G heads; a key tile 128 slots.
+//
+// Attention: an item is a range of key tiles for either two query tiles that
+// follow each other (pair = 0), or one query tile whose even key tiles go to
+// the first softmax group and odd ones to the second (pair = 1).
+struct ChunkItem {
+  int32_t r, h, t0;      // request, KV head, first token
+  int32_t keys;          // 1: one query tile, the key tiles split between the groups
+  int32_t kb, ke;        // key tiles
+  int32_t part_a, part_b;// partial of each group, -1: its output directly
+};
+static_assert(sizeof(ChunkItem) == 32, "two 16-byte loads");
+// A query tile whose partials are joined.
+struct ChunkJoin {
+  int32_t r, h, t0, first, n, pad[3];
+};
+// Weights: an item is 256 keys (a page) against a range of query tiles.
+struct WeightItem {
+  int32_t r, h, page;
+  int32_t qb, qe;        // query tiles
+  int32_t part;          // partial, -1: added to the weights directly
+  int32_t pad[2];
+};
+struct WeightJoin {
+  int32_t r, h, page, first, n, pad[3];
+};
+
+struct ChunkTcArgs {
+  CUtensorMap kmap, vmap;  // caches as [rows][D], box 64 x 128, 128-byte swizzle
+  CUtensorMap qmap;        // queries as [rows][Hq][D], box 64 x G x 128 / G
+  int num_pages_total;
+  int layer, Hq, Hkv, D, G, M;
+  int64_t cap;
+  const ChunkReq* reqs;
+  const int32_t* bt;
+  const ChunkItem* items;      // CTA c takes [begin[c], begin[c + 1])
+  const int32_t* begin;
+  int grid;
+  const ChunkJoin* joins;
+  int n_joins;
+  const WeightItem* witems;
+  const int32_t* wbegin;
+  int wgrid;
+  const WeightJoin* wjoins;
+  int n_wjoins;
+  void* out;                   // [rows][Hq][D] bf16
+  float2* stat;                // [rows][Hq], or null
+  float* weights;
+  float* part;                 // partial outputs, chunk_part_floats(D) each
+  float* wpart;                // partial weights, 256 each
+  int* err;
+};
+// A partial: outputs [D / 4][128 rows][4], then 128 maxima, then 128 sums.
+__host__ __device__ constexpr size_t chunk_part_floats(int D) { return (size_t)128 * (D + 2); }
+inline bool chunk_tc_shape(int D, int G) { return (D == 64 || D == 128) && (G == 2 || G == 4); }
+cudaError_t launch_chunk_tc(const ChunkTcArgs& a, cudaStream_t s);
+cudaError_t launch_chunk_weights_tc(const ChunkTcArgs& a, cudaStream_t s);
+
 }  // namespace gp
