@@ -25,13 +25,13 @@
 //   warps 4-7    softmax of group 0, then its epilogue;  warps 8-11 group 1
 // TMEM: S0 S1 (128 columns each, P over the first 64 of them), O0 O1.
 //
-// Weights.  W_i += sum over rows of 2^(S_ri c - m_r) / l_r needs the final m and
-// l of every row, so S is formed again, transposed: S^T = K Q^T, so that a
-// thread (TMEM lane) owns a key and adds up its row in a register: no
-// reduction over threads, no atomics, one writer a weight.  An item is a page
-// (two key tiles, one a group) against a range of query tiles, S^T double
-// buffered, K tiles kept and the next item's loaded meanwhile.  The statistics
-// of a query tile go through shared memory (warp 2).
+// Weights.  W_i += sum over rows of 2^(S_ri c - L_r) needs the final
+// L_r = m_r + log2 l_r of every row (rounded to fp32 once, as the logit is), so S
+// is formed again, transposed: S^T = K Q^T, so that a thread (TMEM lane) owns
+// a key and adds up half of its columns in registers: no atomics, one writer a
+// weight.  An item is a page (two key tiles) against a range of query tiles,
+// S^T double buffered, K tiles kept and the next item's loaded meanwhile.  L
+// of a query tile goes through shared memory (warp 2).
 //
 // Every wait is bounded: on expiry the CTA records ERR_TIMEOUT, raises an
 // abort flag that ends every role's loop, waits (bounded) for its copies and
@@ -50,7 +50,8 @@ namespace {
 using namespace tc;
 
 constexpr int PAGE = 256;
-constexpr int NT = 384;
+constexpr int NT = 384;   // attention: four warps of the pipeline, two softmax groups of four
+constexpr int WNT = 640;  // weights: four warps of the pipeline, four summing groups
 constexpr int TK = 128;
 constexpr int TMEM_COLS = 512;
 constexpr float NEG = -1.0e30f;
@@ -85,12 +86,32 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-// D (TMEM) [+]= A (TMEM, bf16 pairs) . B for one K = 16 step.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t bd, uint32_t id, uint32_t acc) {
+// The products are issued by a whole warp, whose leader executes them: with the
+// loop and the descriptors uniform an instruction takes about 25 clocks to
+// issue, under a branch of one lane about 60, just the 64 that a 128 x 128 x 16
+// product takes (measured on a loop of products alone: 257 and 459 clocks
+// for eight 128 x 64 x 16 ones).
+// D (TMEM) [+]= A (shared memory) . B for one K = 16 step.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(id), "r"(acc)
+      : "memory");
+}
+// D (TMEM) [+]= A (TMEM, bf16 pairs) . B.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bd, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(bd), "r"(id), "r"(acc)
+      : "memory");
+}
+// The barrier is arrived at when the leader's products so far have completed.
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -143,6 +164,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// Registers of the calling warpgroup (all of its warps call it).  The shares add
+// up to what the block was launched with.
+template <int N>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Bounded wait; gives up when the limit passes or *abort is set.
@@ -219,8 +251,8 @@ struct Sm {
   static constexpr size_t Q = 0;                      // two query tiles
   static constexpr size_t ST = 2 * (size_t)TILE;
   static constexpr size_t BARS = ST + (size_t)NST * TILE;
-  // full[NST], empty[NST], q_full, q_empty, s_ready[2], p_ready[2], o_done[2], o_free[2], mma_done
-  static constexpr int NBARS = 2 * NST + 11;
+  // full[NST], empty[NST], q_full, q_empty, s_ready[2], p_ready[2], o_done[2], o_free[2], p_half[2], mma_done
+  static constexpr int NBARS = 2 * NST + 13;
   static constexpr size_t MISC = BARS + 8 * NBARS;
   static constexpr size_t BYTES = MISC + 64 + 1024;   // + alignment slack
 };
@@ -244,14 +276,15 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
   auto p_ready = [&](int x) { return q_full + 8u * (uint32_t)(4 + x); };
   auto o_done = [&](int x) { return q_full + 8u * (uint32_t)(6 + x); };
   auto o_free = [&](int x) { return q_full + 8u * (uint32_t)(8 + x); };
-  const uint32_t mma_done = q_full + 80u;
+  auto p_half = [&](int x) { return q_full + 8u * (uint32_t)(10 + x); };
+  const uint32_t mma_done = q_full + 96u;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int i0 = a.begin[blockIdx.x], i1 = a.begin[blockIdx.x + 1];
   if (tid == 0) {
     for (int i = 0; i < L::NBARS; ++i) {
-      const int b = i - 2 * NST;  // p_ready and o_free: the group's four warps; else one arrival
-      mbar_init(bar0 + 8u * (uint32_t)i, b == 4 || b == 5 || b == 8 || b == 9 ? 4 : 1);
+      const int b = i - 2 * NST;  // p_ready, o_free, p_half: the group's four warps; else one arrival
+      mbar_init(bar0 + 8u * (uint32_t)i, b == 4 || b == 5 || (b >= 8 && b <= 11) ? 4 : 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     *abort = 0;
@@ -272,6 +305,9 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
     *abort = 1;
   };
 
+  // 128 x 88 + 256 x 208 registers = the 384 x 168 of the launch
+  if (warp < 4) {
+  registers_down<88>();
   if (warp == 0) {
     // ---- producer ----------------------------------------------------------
     if (lane == 0) {
@@ -325,37 +361,42 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
     __syncwarp();
   } else if (warp == 1) {
     // ---- MMA issuer ----------------------------------------------------------
-    if (lane == 0) {
+    {
       int c = 0, nq = 0;          // tiles consumed, items
       int ns[2] = {0, 0};         // products P V issued per group
       int no[2] = {0, 0};         // items per group
       bool ok = true;
-      auto wait = [&](uint32_t bar, int phase) { ok = ok && wait_bar(bar, (uint32_t)(phase & 1), abort); };
+      auto wait = [&](uint32_t bar, int phase) { ok = ok && __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(phase & 1), abort)); };
       auto stage = [&](int k) { return sb + (uint32_t)(L::ST + (size_t)(k % NST) * L::TILE); };
       auto score = [&](int x, int k, int qt) {  // S of group x from the K tile k and query tile qt
         wait(full(k % NST), k / NST);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t q0 = sb + (uint32_t)(L::Q + (size_t)qt * L::TILE), k0 = stage(k);
+        const uint64_t q0 = sw128_desc(sb + (uint32_t)(L::Q + (size_t)qt * L::TILE)), k0 = sw128_desc(stage(k));
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) {
-          const uint32_t off = (uint32_t)((e >> 2) * L::HALF + (e & 3) * 32);
-          mma_f16(tmem + (uint32_t)(x * 128), sw128_desc(q0 + off), sw128_desc(k0 + off), idesc(TK, false),
-                  e > 0 ? 1u : 0u);
+          const uint64_t off = (uint64_t)(((e >> 2) * L::HALF + (e & 3) * 32) >> 4);
+          mma_ss(tmem + (uint32_t)(x * 128), q0 + off, k0 + off, idesc(TK, false), e > 0 ? 1u : 0u);
         }
-        mma_commit(s_ready(x));
+        commit(s_ready(x));
       };
       auto value = [&](int x, int k, bool first) {  // O of group x from its P and the V tile k
-        wait(p_ready(x), ns[x]);
+        // in two steps: the second half of P is still being computed when the
+        // first 64 keys' product starts
+        wait(p_half(x), ns[x]);
         wait(full(k % NST), k / NST);
         if (first && no[x] > 0) wait(o_free(x), no[x] - 1);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t v0 = stage(k);
+        const uint64_t v0 = sw128_mn_desc(stage(k), L::HALF);
 #pragma unroll
-        for (int e = 0; e < TK / 16; ++e)
-          mma_f16_ts(tmem + (uint32_t)(256 + x * 128), tmem + (uint32_t)(x * 128 + e * 8),
-                     sw128_mn_desc(v0 + (uint32_t)e * 2048u, L::HALF), idesc(D, true), first && e == 0 ? 0u : 1u);
+        for (int half = 0; half < 2; ++half) {
+          if (half) wait(p_ready(x), ns[x]);
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll
+          for (int e = 4 * half; e < 4 * half + 4; ++e)
+            mma_ts(tmem + (uint32_t)(256 + x * 128), tmem + (uint32_t)(x * 128 + e * 8), v0 + (uint64_t)(e * 2048 >> 4),
+                   idesc(D, true), first && e == 0 ? 0u : 1u);
+        }
         ++ns[x];
       };
       for (int i = i0; i < i1 && ok; ++i) {
@@ -367,15 +408,15 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
           auto S = [&](int x, bool last) {
             score(x, c, 0);
             if (!ok) return;
-            mma_commit(empty(c++ % NST));
-            if (last) mma_commit(q_empty);
+            commit(empty(c++ % NST));
+            if (last) commit(q_empty);
           };
           auto V = [&](int x, int j) {
             value(x, c, j == 0);
             if (!ok) return;
-            mma_commit(empty(c++ % NST));
+            commit(empty(c++ % NST));
             if (j + 1 == w.cnt[x]) {
-              mma_commit(o_done(x));
+              commit(o_done(x));
               ++no[x];
             }
           };
@@ -391,42 +432,44 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
           const int k0 = c;  // K tile j is k0 + 2 j, V tile j the one after it
           if (w.cnt[0] > 0) score(0, k0, 0);
           score(1, k0, 1);
-          if (ok) mma_commit(empty(k0 % NST));
-          if (ok && w.n == 1) mma_commit(q_empty);
+          if (ok) commit(empty(k0 % NST));
+          if (ok && w.n == 1) commit(q_empty);
           for (int j = 0; j < w.n && ok; ++j) {
             const int kv = k0 + 2 * j + 1;
             if (j < w.cnt[0]) {
               value(0, kv, j == 0);
               if (ok && j + 1 == w.cnt[0]) {
-                mma_commit(o_done(0));
+                commit(o_done(0));
                 ++no[0];
               }
               if (j + 1 < w.cnt[0]) score(0, kv + 1, 0);
             }
             value(1, kv, j == 0);
             if (!ok) break;
-            mma_commit(empty(kv % NST));
+            commit(empty(kv % NST));
             if (j + 1 == w.n) {
-              mma_commit(o_done(1));
+              commit(o_done(1));
               ++no[1];
             } else {
               score(1, kv + 1, 1);
               if (!ok) break;
-              mma_commit(empty((kv + 1) % NST));
-              if (j + 2 == w.n) mma_commit(q_empty);
+              commit(empty((kv + 1) % NST));
+              if (j + 2 == w.n) commit(q_empty);
             }
           }
           c += 2 * w.n;
         }
       }
-      if (!ok) timed_out();
+      if (!ok && lane == 0) timed_out();
       // every product issued has completed before TMEM is released (bounded)
-      mma_commit(mma_done);
+      commit(mma_done);
       const int zero = 0;
       wait_bar(mma_done, 0u, &zero);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  }
+  } else {
+    registers_up<208>();
     // ---- softmax and epilogue: thread = row ------------------------------------
     const int x = (warp - 4) >> 2, quad = warp & 3, row = 32 * quad + lane;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
@@ -493,22 +536,6 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
             }
           }
         }
-        const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m, -m);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t p[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float2 z = fma2(make_float2(__uint_as_float(r[q][2 * e]), __uint_as_float(r[q][2 * e + 1])), sc2, nm2);
-            z.x = ex2f(z.x);
-            z.y = ex2f(z.y);
-            sum[e & 1] = add2(sum[e & 1], z);
-            p[e] = pack_bf16(z.x, z.y);
-          }
-          tmem_store16(ts + (uint32_t)(16 * q), p);
-        }
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         // the last key tile may hold slots past the request's tokens: their
         // weights are 0, but 0 x inf or NaN would reach O; their V rows are
         // zeroed by the group that takes the tile first
@@ -528,6 +555,28 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
+        const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m, -m);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 z = fma2(make_float2(__uint_as_float(r[q][2 * e]), __uint_as_float(r[q][2 * e + 1])), sc2, nm2);
+            z.x = ex2f(z.x);
+            z.y = ex2f(z.y);
+            sum[e & 1] = add2(sum[e & 1], z);
+            p[e] = pack_bf16(z.x, z.y);
+          }
+          tmem_store16(ts + (uint32_t)(16 * q), p);
+          if (q == 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_half(x));
+          }
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -577,7 +626,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
         __syncwarp();
         if (lane == 0) mbar_arrive(o_free(x));
         ++no;
-        if (valid && part < 0 && a.stat) a.stat[at] = make_float2(m, inv);
+        if (valid && part < 0 && a.lse) a.lse[at] = m + log2f(l);
         if (part >= 0) {
           float* po = a.part + (size_t)part * chunk_part_floats(D) + 128 * D;
           po[row] = m;
@@ -631,7 +680,7 @@ __global__ void __launch_bounds__(256) k_chunk_join(const __grid_constant__ Chun
   *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * D + d0) =
       make_uint4(pack_bf16(acc[0].x * inv, acc[0].y * inv), pack_bf16(acc[0].z * inv, acc[0].w * inv),
                  pack_bf16(acc[1].x * inv, acc[1].y * inv), pack_bf16(acc[1].z * inv, acc[1].w * inv));
-  if (d0 == 0 && a.stat) a.stat[at] = make_float2(M, inv);
+  if (d0 == 0 && a.lse) a.lse[at] = M + log2f(l);
 }
 
 // ---- weights -----------------------------------------------------------------
@@ -643,8 +692,9 @@ struct SmW {
   static constexpr int NQ = D == 128 ? 3 : 6;          // query tiles in flight
   static constexpr size_t K = 0;                       // two pages, two tiles each
   static constexpr size_t Q = 4 * (size_t)TILE;
-  static constexpr size_t STAT = Q + (size_t)NQ * TILE;  // [2][128] (-maximum, 1 / sum)
-  static constexpr size_t BARS = STAT + 2 * 128 * 8;
+  static constexpr size_t STAT = Q + (size_t)NQ * TILE;  // float [2][128], negated
+  static constexpr size_t HALVES = STAT + 2 * 128 * 4;   // float [2][128]
+  static constexpr size_t BARS = HALVES + 2 * 128 * 4;
   // k_full[2], k_empty[2], q_full[NQ], q_empty[NQ], t_full[2], t_empty[2], s_ready[2][2], s_free[2][2], mma_done
   static constexpr int NBARS = 8 + 2 * NQ + 8 + 1;
   static constexpr size_t MISC = BARS + 8 * NBARS;
@@ -653,7 +703,7 @@ struct SmW {
 };
 
 template <int D, int G>
-__global__ void __launch_bounds__(NT, 1) k_chunk_weights_tc(const __grid_constant__ ChunkTcArgs a) {
+__global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_constant__ ChunkTcArgs a) {
   using L = SmW<D>;
   constexpr int NQ = L::NQ, TOK = 128 / G;
   extern __shared__ __align__(1024) unsigned char smem_base[];
@@ -666,6 +716,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_weights_tc(const __grid_constan
   int* misc = reinterpret_cast<int*>(sm + L::MISC);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort = misc + 1;
+  volatile int* fail = misc + 2;  // [2] a wait of a key tile's threads gave up
   const uint32_t bar0 = sb + (uint32_t)L::BARS;
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   auto k_full = [&](int b) { return bar(b); };
@@ -683,12 +734,14 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_weights_tc(const __grid_constan
   if (tid == 0) {
     for (int i = 0; i < L::NBARS; ++i) {
       int n = 1;
-      if (i >= 6 + 2 * NQ && i < 8 + 2 * NQ) n = 8;    // t_empty: both groups' warps
-      if (i >= 12 + 2 * NQ && i < 16 + 2 * NQ) n = 4;  // s_free: a group's warps
+      if (i >= 6 + 2 * NQ && i < 8 + 2 * NQ) n = 16;   // t_empty: all groups' warps
+      if (i >= 12 + 2 * NQ && i < 16 + 2 * NQ) n = 8;  // s_free: the warps of a key tile
       mbar_init(bar(i), (uint32_t)n);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     *abort = 0;
+    fail[0] = 0;
+    fail[1] = 0;
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -741,10 +794,10 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_weights_tc(const __grid_constan
     __syncwarp();
   } else if (warp == 1) {
     // ---- MMA issuer ----------------------------------------------------------
-    if (lane == 0) {
+    {
       int c = 0, n = 0;
       bool ok = true;
-      auto wait = [&](uint32_t b, int phase) { ok = ok && wait_bar(b, (uint32_t)(phase & 1), abort); };
+      auto wait = [&](uint32_t b, int phase) { ok = ok && __all_sync(0xffffffffu, wait_bar(b, (uint32_t)(phase & 1), abort)); };
       for (int i = i0; i < i1 && ok; ++i, ++n) {
         const WeightItem it = load_item(a.witems + i);
         const int b = n & 1;
@@ -752,26 +805,25 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_weights_tc(const __grid_constan
         for (int q = it.qb; q < it.qe && ok; ++q, ++c) {
           const int s = c % NQ, z = c & 1;
           wait(q_full(s), c / NQ);
-          const uint32_t q0 = sb + (uint32_t)(L::Q + (size_t)s * L::TILE);
+          const uint64_t q0 = sw128_desc(sb + (uint32_t)(L::Q + (size_t)s * L::TILE));
           for (int x = 0; x < 2 && ok; ++x) {
             if (c >= 2) wait(s_free(x, z), c / 2 - 1);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t k0 = sb + (uint32_t)(L::K + (size_t)(2 * b + x) * L::TILE);
+            const uint64_t k0 = sw128_desc(sb + (uint32_t)(L::K + (size_t)(2 * b + x) * L::TILE));
 #pragma unroll
             for (int e = 0; e < D / 16; ++e) {
-              const uint32_t off = (uint32_t)((e >> 2) * L::HALF + (e & 3) * 32);
-              mma_f16(tmem + (uint32_t)(x * 256 + z * 128), sw128_desc(k0 + off), sw128_desc(q0 + off),
-                      idesc(128, false), e > 0 ? 1u : 0u);
+              const uint64_t off = (uint64_t)(((e >> 2) * L::HALF + (e & 3) * 32) >> 4);
+              mma_ss(tmem + (uint32_t)(x * 256 + z * 128), k0 + off, q0 + off, idesc(128, false), e > 0 ? 1u : 0u);
             }
-            mma_commit(s_ready(x, z));
+            commit(s_ready(x, z));
           }
-          if (ok) mma_commit(q_empty(s));
+          if (ok) commit(q_empty(s));
         }
-        if (ok) mma_commit(k_empty(b));
+        if (ok) commit(k_empty(b));
       }
-      if (!ok) timed_out();
-      mma_commit(mma_done);
+      if (!ok && lane == 0) timed_out();
+      commit(mma_done);
       const int zero = 0;
       wait_bar(mma_done, 0u, &zero);
     }
@@ -787,13 +839,11 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_weights_tc(const __grid_constan
         const int b = c & 1;
         if (c >= 2) ok = __all_sync(0xffffffffu, wait_bar(t_empty(b), (uint32_t)((c / 2 - 1) & 1), abort));
         if (!ok) break;
-        float2* dst = reinterpret_cast<float2*>(sm + L::STAT) + b * 128;
+        float* dst = reinterpret_cast<float*>(sm + L::STAT) + b * 128;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int row = 32 * k + lane, t = q * TOK + row / G;
-          float2 st = make_float2(0.f, 0.f);
-          if (t < rq.nnew) st = __ldg(a.stat + (size_t)(rq.row0 + t) * a.Hq + it.h * G + row % G);
-          dst[row] = make_float2(-st.x, st.y);
+          dst[row] = t < rq.nnew ? -__ldg(a.lse + (size_t)(rq.row0 + t) * a.Hq + it.h * G + row % G) : 0.f;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(t_full(b));
@@ -801,50 +851,58 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_weights_tc(const __grid_constan
     }
     if (!ok && lane == 0) timed_out();
   } else if (warp >= 4) {
-    // ---- sums: thread = key ---------------------------------------------------------
-    const int x = (warp - 4) >> 2, quad = warp & 3, key = 32 * quad + lane;
+    // ---- sums: thread = (key, half of the columns) ---------------------------------
+    const int x = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quad = warp & 3, key = 32 * quad + lane;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     const float sc = 1.4426950408889634f / sqrtf((float)D);
     const float2 sc2 = make_float2(sc, sc);
+    float* other = reinterpret_cast<float*>(sm + L::HALVES) + x * 128 + key;  // the upper half's sum
     int c = 0;
     bool ok = true;
     for (int i = i0; i < i1 && ok; ++i) {
       const WeightItem it = load_item(a.witems + i);
       const ChunkReq rq = load_req(a.reqs + it.r);
       const int slot_i = it.page * PAGE + x * TK + key;  // this thread's logical slot
-      float2 w[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      float2 w[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       for (int q = it.qb; q < it.qe; ++q, ++c) {
         const int z = c & 1;
         ok = __all_sync(0xffffffffu, wait_bar(t_full(z), (uint32_t)((c / 2) & 1), abort)) &&
              __all_sync(0xffffffffu, wait_bar(s_ready(x, z), (uint32_t)((c / 2) & 1), abort));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t ts = tmem + lanes + (uint32_t)(x * 256 + z * 128);
-        const float4* st = reinterpret_cast<const float4*>(sm + L::STAT) + z * 64;
-        // columns lo .. hi - 1 count: the rows of tokens that see the slot and exist
-        const int lo = (slot_i - rq.cached - q * TOK) * G, hi = (rq.nnew - q * TOK) * G;
-        const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= 128);
+        uint32_t r[2][32];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t r[32];
-          tmem_load32(ts + (uint32_t)(32 * h), r);
-          tmem_wait_ld();
-          tmem_arrived(r);
+        for (int h = 0; h < 2; ++h)
+          tmem_load32(tmem + lanes + (uint32_t)(x * 256 + z * 128 + half * 64 + h * 32), r[h]);
+        const float4* st = reinterpret_cast<const float4*>(sm + L::STAT) + z * 32 + half * 16;
+        // of this half's columns lo .. hi - 1 count: rows of tokens that see the slot and exist
+        const int lo = (slot_i - rq.cached - q * TOK) * G - half * 64, hi = (rq.nnew - q * TOK) * G - half * 64;
+        tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float4 t2 = st[16 * h + e];  // (-m, 1/l) of two columns
-            float2 v = fma2(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), sc2,
-                            make_float2(t2.x, t2.z));
+        for (int h = 0; h < 2; ++h) tmem_arrived(r[h]);
+        if (__any_sync(0xffffffffu, lo > 0 || hi < 64)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * h + e < lo || 32 * h + e >= hi) r[h][e] = 0xff800000u;  // -inf
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 nm = st[8 * h + e];
+            float2 u = fma2(make_float2(__uint_as_float(r[h][4 * e]), __uint_as_float(r[h][4 * e + 1])), sc2,
+                            make_float2(nm.x, nm.y));
+            float2 v = fma2(make_float2(__uint_as_float(r[h][4 * e + 2]), __uint_as_float(r[h][4 * e + 3])), sc2,
+                            make_float2(nm.z, nm.w));
+            u.x = ex2f(u.x);
+            u.y = ex2f(u.y);
             v.x = ex2f(v.x);
             v.y = ex2f(v.y);
-            if (!whole) {
-              const int col = 32 * h + 2 * e;
-              v.x = col >= lo && col < hi ? v.x : 0.f;
-              v.y = col + 1 >= lo && col + 1 < hi ? v.y : 0.f;
-            }
-            w[e & 1] = fma2(v, make_float2(t2.y, t2.w), w[e & 1]);
+            w[e & 1] = add2(w[e & 1], u);
+            w[2 + (e & 1)] = add2(w[2 + (e & 1)], v);
           }
-        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -852,8 +910,17 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_weights_tc(const __grid_constan
           mbar_arrive(t_empty(z));
         }
       }
+      // the two halves of a key's sum meet (both groups of threads come here,
+      // whether a wait gave up or not)
+      float sum = ((w[0].x + w[0].y) + (w[1].x + w[1].y)) + ((w[2].x + w[2].y) + (w[3].x + w[3].y));
+      if (half) *other = sum;
+      if (!ok) fail[x] = 1;  // written only before the barrier: all of the key tile's threads agree
+      asm volatile("bar.sync %0, 256;" ::"r"(1 + x) : "memory");
+      ok = !fail[x];
+      if (!half) sum += *other;
+      asm volatile("bar.sync %0, 256;" ::"r"(1 + x) : "memory");
       if (!ok) break;
-      const float sum = (w[0].x + w[0].y) + (w[1].x + w[1].y);
+      if (half) continue;
       if (it.part >= 0) {
         a.wpart[(size_t)it.part * PAGE + x * TK + key] = sum;
       } else if (slot_i < rq.cached + rq.nnew && rq.slot >= 0 && rq.slot < a.M) {
@@ -896,7 +963,7 @@ cudaError_t weights(const ChunkTcArgs& a, cudaStream_t s) {
   cudaError_t e =
       cudaFuncSetAttribute(k_chunk_weights_tc<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SmW<D>::BYTES);
   if (e != cudaSuccess) return e;
-  k_chunk_weights_tc<D, G><<<dim3((unsigned)a.wgrid), NT, SmW<D>::BYTES, s>>>(a);
+  k_chunk_weights_tc<D, G><<<dim3((unsigned)a.wgrid), WNT, SmW<D>::BYTES, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.n_wjoins == 0) return e;
   k_chunk_weights_join<<<dim3((unsigned)a.n_wjoins), PAGE, 0, s>>>(a);
   return cudaGetLastError();

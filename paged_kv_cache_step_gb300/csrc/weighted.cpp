@@ -381,7 +381,7 @@ gp_status gp_chunk_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_reque
     a.wjoins = reinterpret_cast<const WeightJoin*>(dev + at_wjoins);
     a.n_wjoins = (int)plan.wjoins.size();
     a.out = out_dev;
-    a.stat = stat;
+    a.lse = reinterpret_cast<float*>(stat);
     a.weights = weights_dev;
     a.part = reinterpret_cast<float*>(static_cast<char*>(c->chunk.p) + at_part);
     a.wpart = reinterpret_cast<float*>(static_cast<char*>(c->chunk.p) + at_wpart);

@@ -192,7 +192,7 @@ struct ChunkTcArgs {
   const WeightJoin* wjoins;
   int n_wjoins;
   void* out;                   // [rows][Hq][D] bf16
-  float2* stat;                // [rows][Hq], or null
+  float* lse;                  // [rows][Hq] base-2 log of the softmax's sum, or null
   float* weights;
   float* part;                 // partial outputs, chunk_part_floats(D) each
   float* wpart;                // partial weights, 256 each
