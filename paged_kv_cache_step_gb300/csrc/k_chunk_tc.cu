@@ -7,9 +7,10 @@
 //   S = Q K^T        128 x 128, K = d, fp32 in TMEM
 //   P = 2^(S c - m)  c = log2(e) / sqrt(d), rounded to bf16 over S in TMEM
 //   O += P V         128 x d, K = 128, P from TMEM, V MN-major as TMA left it
-// with the running maximum m moved only when a row's maximum has grown by
-// more than 8 (a factor 256, which fp32 and the bf16 exponent hold easily):
-// O is then rescaled in TMEM by the warp that found it, between two products.
+// with the maximum m of the first tile, moved only when a row's has grown by
+// more than 24 (a factor 2^24, which the exponents of fp32 and bf16 hold
+// easily): O is then rescaled in TMEM by the warp that found it, between two
+// products.
 // Rounding P to bf16 costs 2^-9 relative a weight at random signs, about what
 // rounding the output to bf16 costs; keeping it exact would double the second
 // product.  The sum l is of the unrounded fp32 weights.
@@ -55,7 +56,7 @@ constexpr int WNT = 640;  // weights: four warps of the pipeline, four summing g
 constexpr int TK = 128;
 constexpr int TMEM_COLS = 512;
 constexpr float NEG = -1.0e30f;
-constexpr float LAZY = 8.f;                  // base-2 growth of a maximum that is not followed
+constexpr float LAZY = 24.f;                 // base-2 growth of a maximum that is not followed
 constexpr long long kWaitLimit = 1ll << 31;  // clock cycles (about one second)
 
 // bf16 A and B, fp32 accumulator, M = 128, N; bit 16: B is MN-major.
@@ -68,6 +69,11 @@ __device__ __forceinline__ float ex2f(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -475,6 +481,16 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     const uint32_t ts = tmem + lanes + (uint32_t)(x * 128), to = tmem + lanes + (uint32_t)(256 + x * 128);
     const float sc = 1.4426950408889634f / sqrtf((float)D);
+    auto zero_rows = [&](int k, bool past) {  // this thread's row of the V tile k
+      if (past) {
+        unsigned char* v = sm + L::ST + (size_t)(k % NST) * L::TILE + (size_t)row * 128;
+#pragma unroll
+        for (int d = 0; d < D / 64; ++d)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) reinterpret_cast<uint4*>(v + (size_t)d * L::HALF)[e] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    };
     int ns = 0, no = 0;  // tiles and items of this group
     int c = 0;           // tiles of all items (the ring's)
     bool ok = true;
@@ -487,12 +503,35 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
       const int first = it.t0 + (it.keys ? 0 : x * TOK);  // the tile's first token
       const int t = first + row / G;
       const int sees = rq.cached + t;                     // last slot the row sees
+      // the last key tile may hold slots past the request's tokens: their weights
+      // are 0, but 0 x inf or NaN would reach O; their V rows are zeroed by the
+      // group that takes the tile first
+      const bool mine = it.keys || x == 0 || w.cnt[0] < w.n;
+      auto last_of = [&](int kt) { return mine && kt + 1 == it.ke && kt * TK + TK > total; };
+      // a warp whose rows are all past the request's tokens computes nothing: its
+      // rows of P hold any bits, and spoil only its rows of O
+      const bool live = first + 32 * quad / G < rq.nnew;
       float m = NEG, l = 0.f;
       for (int j = 0; j < cnt; ++j) {
         const int kt = it.kb + (it.keys ? 2 * j + x : j);  // key tile
         ok = __all_sync(0xffffffffu, wait_bar(s_ready(x), (uint32_t)(ns & 1), abort));
         if (!ok) break;
         tc_fence_after();
+        if (!live) {
+          if (last_of(kt)) {
+            const int k = c + 2 * w.n - 1;
+            ok = __all_sync(0xffffffffu, wait_bar(full(k % NST), (uint32_t)((k / NST) & 1), abort));
+            if (!ok) break;
+            zero_rows(k, kt * TK + row >= total);
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(p_half(x));
+            mbar_arrive(p_ready(x));
+          }
+          ++ns;
+          continue;
+        }
         uint32_t r[4][32];
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_load32(ts + (uint32_t)(32 * q), r[q]);
@@ -510,9 +549,10 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
         float mx[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          mx[q] = __uint_as_float(r[q][0]);
+          mx[q] = max3(__uint_as_float(r[q][0]), __uint_as_float(r[q][1]), __uint_as_float(r[q][2]));
 #pragma unroll
-          for (int e = 1; e < 32; ++e) mx[q] = fmaxf(mx[q], __uint_as_float(r[q][e]));
+          for (int e = 3; e < 31; e += 2) mx[q] = max3(mx[q], __uint_as_float(r[q][e]), __uint_as_float(r[q][e + 1]));
+          mx[q] = fmaxf(mx[q], __uint_as_float(r[q][31]));
         }
         const float top = sc * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         if (j == 0) {
@@ -536,29 +576,9 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
             }
           }
         }
-        // the last key tile may hold slots past the request's tokens: their
-        // weights are 0, but 0 x inf or NaN would reach O; their V rows are
-        // zeroed by the group that takes the tile first
-        const bool last_tile = kt + 1 == it.ke && kt * TK + TK > total;
-        const bool mine = it.keys || (x == 0 ? true : w.cnt[0] < w.n);
-        if (last_tile && mine) {
-          const int k = c + 2 * w.n - 1;  // the item's last load
-          ok = __all_sync(0xffffffffu, wait_bar(full(k % NST), (uint32_t)((k / NST) & 1), abort));
-          if (!ok) break;
-          if (kt * TK + row >= total) {
-            unsigned char* v = sm + L::ST + (size_t)(k % NST) * L::TILE + (size_t)row * 128;
-#pragma unroll
-            for (int d = 0; d < D / 64; ++d)
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                reinterpret_cast<uint4*>(v + (size_t)d * L::HALF)[e] = make_uint4(0u, 0u, 0u, 0u);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
         const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m, -m);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        auto weigh = [&](int q) {  // 32 keys' weights, over their logits
           uint32_t p[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -569,13 +589,21 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
             p[e] = pack_bf16(z.x, z.y);
           }
           tmem_store16(ts + (uint32_t)(16 * q), p);
-          if (q == 1) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_half(x));
-          }
+        };
+        weigh(0);
+        weigh(1);
+        if (last_of(kt)) {
+          const int k = c + 2 * w.n - 1;  // the item's last load
+          ok = __all_sync(0xffffffffu, wait_bar(full(k % NST), (uint32_t)((k / NST) & 1), abort));
+          if (!ok) break;
+          zero_rows(k, kt * TK + row >= total);
         }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_half(x));
+        weigh(2);
+        weigh(3);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
         tc_fence_before();
@@ -656,19 +684,22 @@ __global__ void __launch_bounds__(256) k_chunk_join(const __grid_constant__ Chun
   if (t >= rq.nnew) return;
   const float* base = a.part + (size_t)jn.first * chunk_part_floats(D);
   float M = NEG;
+#pragma unroll 8
   for (int p = 0; p < jn.n; ++p) M = fmaxf(M, __ldg(base + p * chunk_part_floats(D) + 128 * D + row));
   float l = 0.f;
   float4 acc[2] = {};
   const int d0 = (blockIdx.y * 2 + half) * 8;  // eight dimensions
+#pragma unroll 4
   for (int p = 0; p < jn.n; ++p) {
     const float* q = base + p * chunk_part_floats(D);
     const float lp = __ldg(q + 128 * D + 128 + row);
-    if (lp == 0.f) continue;  // a part that the row does not see
-    const float f = ex2f(__ldg(q + 128 * D + row) - M);
+    // a part that the row does not see has no sum, and its O may not be there
+    const float f = lp > 0.f ? ex2f(__ldg(q + 128 * D + row) - M) : 0.f;
     l = fmaf(f, lp, l);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float4 o = __ldg(reinterpret_cast<const float4*>(q) + (size_t)(d0 / 4 + e) * 128 + row);
+      float4 o = __ldg(reinterpret_cast<const float4*>(q) + (size_t)(d0 / 4 + e) * 128 + row);
+      if (f == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
       acc[e].x = fmaf(f, o.x, acc[e].x);
       acc[e].y = fmaf(f, o.y, acc[e].y);
       acc[e].z = fmaf(f, o.z, acc[e].z);
