@@ -18,9 +18,10 @@
 // One CTA per SM walks a list of items that the host cut into even shares.
 // Two softmax groups of 128 threads (thread = row = TMEM lane) alternate on
 // the tensor core: while one computes P, the other's products run.  They hold
-// two query tiles (the K and V tiles then serve 256 rows), or, when a request
-// has one tile left, the even and odd key tiles of that one.  A query tile in
-// several parts leaves partials (O, m, l) that a second kernel joins.
+// two query tiles (the K and V tiles then serve 256 rows), or, where a request
+// has one tile left, the even and odd key tiles of that one (a launch of its
+// own).  A query tile in several parts leaves partials (O, m, l) that another
+// kernel joins.
 //   warp 0       producer: Q tiles, and the K and V tiles through a ring
 //   warp 1       MMA issuer
 //   warps 4-7    softmax of group 0, then its epilogue;  warps 8-11 group 1
@@ -32,7 +33,7 @@
 // a key and adds up half of its columns in registers: no atomics, one writer a
 // weight.  An item is a page (two key tiles) against a range of query tiles,
 // S^T double buffered, K tiles kept and the next item's loaded meanwhile.  L
-// of a query tile goes through shared memory (warp 2).
+// of a query tile goes through shared memory (warp 3).
 //
 // Every wait is bounded: on expiry the CTA records ERR_TIMEOUT, raises an
 // abort flag that ends every role's loop, waits (bounded) for its copies and
@@ -228,16 +229,21 @@ __device__ __forceinline__ int key_row(const ChunkTcArgs& a, const ChunkReq& rq,
   return (int)((((size_t)a.layer * a.num_pages_total + pg) * a.Hkv + h) * PAGE + (t & 1) * TK);
 }
 
+// The same value in every lane, in a form that the compiler knows as uniform:
+// the descriptors made of it then live in uniform registers, from which the
+// products take them.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // What an item's groups do: `n` key tiles, of which group x takes cnt[x].
 struct Work {
   int n, cnt[2];
 };
-template <int G>
+template <int G, bool KEYS>
 __device__ __forceinline__ Work work_of(const ChunkItem& it, const ChunkReq& rq) {
   constexpr int TOK = 128 / G;
   Work w;
   w.n = it.ke - it.kb;
-  if (it.keys) {
+  if (KEYS) {
     w.cnt[0] = (w.n + 1) / 2;
     w.cnt[1] = w.n / 2;
   } else {
@@ -249,13 +255,16 @@ __device__ __forceinline__ Work work_of(const ChunkItem& it, const ChunkReq& rq)
   return w;
 }
 
-template <int D>
+// KEYS: one query tile, its even key tiles the first group's and the odd ones
+// the second's; else two query tiles, every key tile for both.
+template <int D, bool KEYS>
 struct Sm {
   static constexpr int TILE = TK * D * 2;             // a Q, K or V tile
   static constexpr int HALF = TK * 128;               // its span of 64 columns
-  static constexpr int NST = D == 128 ? 5 : 8;        // K and V tiles in flight
-  static constexpr size_t Q = 0;                      // two query tiles
-  static constexpr size_t ST = 2 * (size_t)TILE;
+  static constexpr int NQT = KEYS ? 1 : 2;            // query tiles
+  static constexpr int NST = (D == 128 ? 7 : 12) - NQT;  // K and V tiles in flight
+  static constexpr size_t Q = 0;
+  static constexpr size_t ST = NQT * (size_t)TILE;
   static constexpr size_t BARS = ST + (size_t)NST * TILE;
   // full[NST], empty[NST], q_full, q_empty, s_ready[2], p_ready[2], o_done[2], o_free[2], p_half[2], mma_done
   static constexpr int NBARS = 2 * NST + 13;
@@ -263,9 +272,9 @@ struct Sm {
   static constexpr size_t BYTES = MISC + 64 + 1024;   // + alignment slack
 };
 
-template <int D, int G>
+template <int D, int G, bool KEYS>
 __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ ChunkTcArgs a) {
-  using L = Sm<D>;
+  using L = Sm<D, KEYS>;
   constexpr int NST = L::NST, TOK = 128 / G;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm =
@@ -285,12 +294,15 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
   auto p_half = [&](int x) { return q_full + 8u * (uint32_t)(10 + x); };
   const uint32_t mma_done = q_full + 96u;
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int i0 = a.begin[blockIdx.x], i1 = a.begin[blockIdx.x + 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
+  const ChunkItem* items = KEYS ? a.kitems : a.items;
+  const int32_t* begin = KEYS ? a.kbegin : a.begin;
+  const int i0 = uniform(begin[blockIdx.x]), i1 = uniform(begin[blockIdx.x + 1]);
   if (tid == 0) {
     for (int i = 0; i < L::NBARS; ++i) {
       const int b = i - 2 * NST;  // p_ready, o_free, p_half: the group's four warps; else one arrival
-      mbar_init(bar0 + 8u * (uint32_t)i, b == 4 || b == 5 || (b >= 8 && b <= 11) ? 4 : 1);
+      const int n = b == 4 || b == 5 || (b >= 8 && b <= 11) ? 4 : 1;
+      mbar_init(bar0 + 8u * (uint32_t)i, (uint32_t)n);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     *abort = 0;
@@ -305,7 +317,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
+  const uint32_t tmem = (uint32_t)uniform((int)*tmem_holder);
   auto timed_out = [&] {
     atomicOr(a.err, ERR_TIMEOUT);
     *abort = 1;
@@ -320,9 +332,9 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
       int c = 0, nq = 0;  // tiles and items issued
       bool ok = true;
       for (int i = i0; i < i1 && ok; ++i) {
-        const ChunkItem it = load_item(a.items + i);
+        const ChunkItem it = load_item(items + i);
         const ChunkReq rq = load_req(a.reqs + it.r);
-        const Work w = work_of<G>(it, rq);
+        const Work w = work_of<G, KEYS>(it, rq);
         auto tile = [&](const CUtensorMap* map, int t) {
           if (!ok) return;
           const int s = c % NST;
@@ -335,14 +347,15 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
           ++c;
         };
         if (nq > 0 && !(ok = wait_bar(q_empty, (uint32_t)((nq - 1) & 1), abort))) break;
-        mbar_expect_tx(q_full, (it.keys ? 1 : 2) * L::TILE);
-        for (int x = 0; x < (it.keys ? 1 : 2); ++x)
+        mbar_expect_tx(q_full, L::NQT * L::TILE);
+#pragma unroll
+        for (int x = 0; x < L::NQT; ++x)
 #pragma unroll
           for (int d = 0; d < D; d += 64)
             tma_load_3d(sb + (uint32_t)(L::Q + (size_t)x * L::TILE + d / 64 * L::HALF), &a.qmap, d, it.h * G,
                         (int)rq.row0 + it.t0 + x * TOK, q_full);
         ++nq;
-        if (it.keys) {
+        if (KEYS) {
           tile(&a.kmap, it.kb);
           if (w.cnt[1] > 0) tile(&a.kmap, it.kb + 1);
           for (int j = 0; j < w.cnt[0]; ++j) {
@@ -366,112 +379,111 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---- MMA issuer ----------------------------------------------------------
-    {
-      int c = 0, nq = 0;          // tiles consumed, items
-      int ns[2] = {0, 0};         // products P V issued per group
-      int no[2] = {0, 0};         // items per group
-      bool ok = true;
-      auto wait = [&](uint32_t bar, int phase) { ok = ok && __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(phase & 1), abort)); };
-      auto stage = [&](int k) { return sb + (uint32_t)(L::ST + (size_t)(k % NST) * L::TILE); };
-      auto score = [&](int x, int k, int qt) {  // S of group x from the K tile k and query tile qt
-        wait(full(k % NST), k / NST);
+    // ---- MMA issuer --------------------------------------------------------------
+    int c = 0, nq = 0;      // tiles of the ring, items
+    int ns[2] = {0, 0};     // products P V per group
+    int no[2] = {0, 0};     // items per group
+    bool ok = true;
+    auto wait = [&](uint32_t bar, int phase) {
+      ok = ok && __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(phase & 1), abort));
+    };
+    auto stage = [&](int k) { return sb + (uint32_t)(L::ST + (size_t)(k % NST) * L::TILE); };
+    auto arrived = [&](int k) { wait(full(k % NST), k / NST); };
+    auto score = [&](int x, int k) {  // S of group x from the K tile k
+      arrived(k);
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t q0 = sw128_desc(sb + (uint32_t)(L::Q + (KEYS ? 0 : (size_t)x * L::TILE)));
+      const uint64_t k0 = sw128_desc(stage(k));
+#pragma unroll
+      for (int e = 0; e < D / 16; ++e) {
+        const uint64_t off = (uint64_t)(((e >> 2) * L::HALF + (e & 3) * 32) >> 4);
+        mma_ss(tmem + (uint32_t)(x * 128), q0 + off, k0 + off, idesc(TK, false), e > 0 ? 1u : 0u);
+      }
+      commit(s_ready(x));
+    };
+    // O of group x from its P and the V tile k, in two steps: the second half of
+    // P is still being computed when the first 64 keys' product starts
+    auto value = [&](int x, int k, bool first, bool last, int& n, int& items_done) {
+      arrived(k);
+      if (first && items_done > 0) wait(o_free(x), items_done - 1);
+      wait(p_half(x), n);
+      const uint64_t v0 = sw128_mn_desc(stage(k), L::HALF);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (half) wait(p_ready(x), n);
         if (!ok) return;
         tc_fence_after();
-        const uint64_t q0 = sw128_desc(sb + (uint32_t)(L::Q + (size_t)qt * L::TILE)), k0 = sw128_desc(stage(k));
 #pragma unroll
-        for (int e = 0; e < D / 16; ++e) {
-          const uint64_t off = (uint64_t)(((e >> 2) * L::HALF + (e & 3) * 32) >> 4);
-          mma_ss(tmem + (uint32_t)(x * 128), q0 + off, k0 + off, idesc(TK, false), e > 0 ? 1u : 0u);
-        }
-        commit(s_ready(x));
-      };
-      auto value = [&](int x, int k, bool first) {  // O of group x from its P and the V tile k
-        // in two steps: the second half of P is still being computed when the
-        // first 64 keys' product starts
-        wait(p_half(x), ns[x]);
-        wait(full(k % NST), k / NST);
-        if (first && no[x] > 0) wait(o_free(x), no[x] - 1);
-        const uint64_t v0 = sw128_mn_desc(stage(k), L::HALF);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (half) wait(p_ready(x), ns[x]);
+        for (int e = 4 * half; e < 4 * half + 4; ++e)
+          mma_ts(tmem + (uint32_t)(256 + x * 128), tmem + (uint32_t)(x * 128 + e * 8), v0 + (uint64_t)(e * 2048 >> 4),
+                 idesc(D, true), first && e == 0 ? 0u : 1u);
+      }
+      ++n;
+      if (last) {
+        commit(o_done(x));
+        ++items_done;
+      }
+    };
+    for (int i = i0; i < i1 && ok; ++i) {
+      const ChunkItem it = load_item(items + i);
+      Work w = work_of<G, KEYS>(it, load_req(a.reqs + it.r));
+      w.n = uniform(w.n);
+      w.cnt[0] = uniform(w.cnt[0]);
+      w.cnt[1] = uniform(w.cnt[1]);
+      wait(q_full, nq++);
+      if constexpr (KEYS) {
+        int at = c;  // every tile serves one group; used in the order of the loads
+        auto S = [&](int x, bool last) {
+          score(x, at);
           if (!ok) return;
-          tc_fence_after();
-#pragma unroll
-          for (int e = 4 * half; e < 4 * half + 4; ++e)
-            mma_ts(tmem + (uint32_t)(256 + x * 128), tmem + (uint32_t)(x * 128 + e * 8), v0 + (uint64_t)(e * 2048 >> 4),
-                   idesc(D, true), first && e == 0 ? 0u : 1u);
+          commit(empty(at++ % NST));
+          if (last) commit(q_empty);
+        };
+        auto V = [&](int x, int j) {
+          value(x, at, j == 0, j + 1 == w.cnt[x], ns[x], no[x]);
+          if (ok) commit(empty(at++ % NST));
+        };
+        S(0, w.n == 1);
+        if (w.cnt[1] > 0 && ok) S(1, w.n == 2);
+        for (int j = 0; j < w.cnt[0] && ok; ++j) {
+          V(0, j);
+          if (j + 1 < w.cnt[0] && ok) S(0, 2 * j + 3 == w.n);
+          if (j < w.cnt[1] && ok) V(1, j);
+          if (j + 1 < w.cnt[1] && ok) S(1, 2 * j + 4 == w.n);
         }
-        ++ns[x];
-      };
-      for (int i = i0; i < i1 && ok; ++i) {
-        const ChunkItem it = load_item(a.items + i);
-        const Work w = work_of<G>(it, load_req(a.reqs + it.r));
-        wait(q_full, nq++);
-        if (it.keys) {
-          // every tile serves one group; consumed in the order of the loads
-          auto S = [&](int x, bool last) {
-            score(x, c, 0);
-            if (!ok) return;
-            commit(empty(c++ % NST));
-            if (last) commit(q_empty);
-          };
-          auto V = [&](int x, int j) {
-            value(x, c, j == 0);
-            if (!ok) return;
-            commit(empty(c++ % NST));
-            if (j + 1 == w.cnt[x]) {
-              commit(o_done(x));
-              ++no[x];
-            }
-          };
-          S(0, w.n == 1);
-          if (w.cnt[1] > 0 && ok) S(1, w.n == 2);
-          for (int j = 0; j < w.cnt[0] && ok; ++j) {
-            V(0, j);
-            if (j + 1 < w.cnt[0] && ok) S(0, 2 * j + 3 == w.n);
-            if (j < w.cnt[1] && ok) V(1, j);
-            if (j + 1 < w.cnt[1] && ok) S(1, 2 * j + 4 == w.n);
+      } else {
+        // K tile j is c + 2 j, V tile j the one after it; the first group may see
+        // fewer tiles
+        if (w.cnt[0] > 0) score(0, c);
+        score(1, c);
+        if (!ok) break;
+        commit(empty(c % NST));
+        if (w.n == 1) commit(q_empty);
+        for (int j = 0; j < w.n && ok; ++j) {
+          const int kv = c + 2 * j + 1;
+          if (j < w.cnt[0]) {
+            value(0, kv, j == 0, j + 1 == w.cnt[0], ns[0], no[0]);
+            if (ok && j + 1 < w.cnt[0]) score(0, kv + 1);
           }
-        } else {
-          const int k0 = c;  // K tile j is k0 + 2 j, V tile j the one after it
-          if (w.cnt[0] > 0) score(0, k0, 0);
-          score(1, k0, 1);
-          if (ok) commit(empty(k0 % NST));
-          if (ok && w.n == 1) commit(q_empty);
-          for (int j = 0; j < w.n && ok; ++j) {
-            const int kv = k0 + 2 * j + 1;
-            if (j < w.cnt[0]) {
-              value(0, kv, j == 0);
-              if (ok && j + 1 == w.cnt[0]) {
-                commit(o_done(0));
-                ++no[0];
-              }
-              if (j + 1 < w.cnt[0]) score(0, kv + 1, 0);
-            }
-            value(1, kv, j == 0);
+          value(1, kv, j == 0, j + 1 == w.n, ns[1], no[1]);
+          if (!ok) break;
+          commit(empty(kv % NST));
+          if (j + 1 < w.n) {
+            score(1, kv + 1);
             if (!ok) break;
-            commit(empty(kv % NST));
-            if (j + 1 == w.n) {
-              commit(o_done(1));
-              ++no[1];
-            } else {
-              score(1, kv + 1, 1);
-              if (!ok) break;
-              commit(empty((kv + 1) % NST));
-              if (j + 2 == w.n) commit(q_empty);
-            }
+            commit(empty((kv + 1) % NST));
+            if (j + 2 == w.n) commit(q_empty);
           }
-          c += 2 * w.n;
         }
       }
-      if (!ok && lane == 0) timed_out();
-      // every product issued has completed before TMEM is released (bounded)
-      commit(mma_done);
-      const int zero = 0;
-      wait_bar(mma_done, 0u, &zero);
+      c += 2 * w.n;
     }
+    if (!ok && lane == 0) timed_out();
+    // every product issued has completed before TMEM is released (bounded)
+    commit(mma_done);
+    const int zero = 0;
+    wait_bar(mma_done, 0u, &zero);
     __syncwarp();
   }
   } else {
@@ -495,25 +507,24 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
     int c = 0;           // tiles of all items (the ring's)
     bool ok = true;
     for (int i = i0; i < i1 && ok; ++i) {
-      const ChunkItem it = load_item(a.items + i);
+      const ChunkItem it = load_item(items + i);
       const ChunkReq rq = load_req(a.reqs + it.r);
-      const Work w = work_of<G>(it, rq);
+      const Work w = work_of<G, KEYS>(it, rq);
       const int total = rq.cached + rq.nnew;
       const int cnt = w.cnt[x];
-      const int first = it.t0 + (it.keys ? 0 : x * TOK);  // the tile's first token
+      const int first = it.t0 + (KEYS ? 0 : x * TOK);  // the tile's first token
       const int t = first + row / G;
       const int sees = rq.cached + t;                     // last slot the row sees
       // the last key tile may hold slots past the request's tokens: their weights
-      // are 0, but 0 x inf or NaN would reach O; their V rows are zeroed by the
-      // group that takes the tile first
-      const bool mine = it.keys || x == 0 || w.cnt[0] < w.n;
-      auto last_of = [&](int kt) { return mine && kt + 1 == it.ke && kt * TK + TK > total; };
+      // are 0, but 0 x inf or NaN would reach O; their V rows are zeroed (by both
+      // groups when both take the tile: neither waits for the other)
+      auto last_of = [&](int kt) { return kt + 1 == it.ke && kt * TK + TK > total; };
       // a warp whose rows are all past the request's tokens computes nothing: its
       // rows of P hold any bits, and spoil only its rows of O
       const bool live = first + 32 * quad / G < rq.nnew;
       float m = NEG, l = 0.f;
       for (int j = 0; j < cnt; ++j) {
-        const int kt = it.kb + (it.keys ? 2 * j + x : j);  // key tile
+        const int kt = it.kb + (KEYS ? 2 * j + x : j);  // key tile
         ok = __all_sync(0xffffffffu, wait_bar(s_ready(x), (uint32_t)(ns & 1), abort));
         if (!ok) break;
         tc_fence_after();
@@ -616,7 +627,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
       const int part = x == 0 ? it.part_a : it.part_b;
       const bool valid = t < rq.nnew;
       if (cnt == 0) {  // nothing of this range is seen by the tile, or there is no second part
-        if (!it.keys && part >= 0) {
+        if (!KEYS && part >= 0) {
           float* po = a.part + (size_t)part * chunk_part_floats(D) + 128 * D;
           po[row] = NEG;
           po[128 + row] = 0.f;
@@ -726,8 +737,8 @@ struct SmW {
   static constexpr size_t STAT = Q + (size_t)NQ * TILE;  // float [2][128], negated
   static constexpr size_t HALVES = STAT + 2 * 128 * 4;   // float [2][128]
   static constexpr size_t BARS = HALVES + 2 * 128 * 4;
-  // k_full[2], k_empty[2], q_full[NQ], q_empty[NQ], t_full[2], t_empty[2], s_ready[2][2], s_free[2][2], mma_done
-  static constexpr int NBARS = 8 + 2 * NQ + 8 + 1;
+  // k_full[2], k_empty[2], q_full[NQ], q_empty[NQ], t_full[2], t_empty[2], s_ready[2][2], s_free[2][2], mma_done[2]
+  static constexpr int NBARS = 8 + 2 * NQ + 8 + 2;
   static constexpr size_t MISC = BARS + 8 * NBARS;
   static constexpr size_t BYTES = MISC + 64;           // the base is aligned to 1 KiB by its declaration
   static_assert(BYTES <= 232448, "227 KiB a CTA");
@@ -758,13 +769,13 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
   auto t_empty = [&](int b) { return bar(6 + 2 * NQ + b); };
   auto s_ready = [&](int x, int b) { return bar(8 + 2 * NQ + 2 * x + b); };
   auto s_free = [&](int x, int b) { return bar(12 + 2 * NQ + 2 * x + b); };
-  const uint32_t mma_done = bar(16 + 2 * NQ);
+  auto mma_done = [&](int x) { return bar(16 + 2 * NQ + x); };
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int i0 = a.wbegin[blockIdx.x], i1 = a.wbegin[blockIdx.x + 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
+  const int i0 = uniform(a.wbegin[blockIdx.x]), i1 = uniform(a.wbegin[blockIdx.x + 1]);
   if (tid == 0) {
     for (int i = 0; i < L::NBARS; ++i) {
-      int n = 1;
+      int n = i == 2 || i == 3 || (i >= 4 + NQ && i < 4 + 2 * NQ) ? 2 : 1;  // k_empty, q_empty: both issuers
       if (i >= 6 + 2 * NQ && i < 8 + 2 * NQ) n = 16;   // t_empty: all groups' warps
       if (i >= 12 + 2 * NQ && i < 16 + 2 * NQ) n = 8;  // s_free: the warps of a key tile
       mbar_init(bar(i), (uint32_t)n);
@@ -784,7 +795,7 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
+  const uint32_t tmem = (uint32_t)uniform((int)*tmem_holder);
   auto timed_out = [&] {
     atomicOr(a.err, ERR_TIMEOUT);
     *abort = 1;
@@ -795,12 +806,13 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
     if (lane == 0) {
       int c = 0, n = 0;  // query tiles and items issued
       bool ok = true;
-      for (int i = i0; i < i1 && ok; ++i, ++n) {
-        const WeightItem it = load_item(a.witems + i);
-        const ChunkReq rq = load_req(a.reqs + it.r);
+      for (int i = i0; i < i1 && ok; ++i) {
+       const WeightItem it = load_item(a.witems + i);
+       const ChunkReq rq = load_req(a.reqs + it.r);
+       for (int pg = it.page; pg < it.page + it.pages; ++pg, ++n) {
         const int b = n & 1;
         if (n >= 2 && !(ok = wait_bar(k_empty(b), (uint32_t)((n / 2 - 1) & 1), abort))) break;
-        const int y = key_row(a, rq, it.h, 2 * it.page);
+        const int y = key_row(a, rq, it.h, 2 * pg);
         mbar_expect_tx(k_full(b), 2 * L::TILE);
         for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -816,6 +828,8 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
             tma_load_3d(sb + (uint32_t)(L::Q + (size_t)s * L::TILE + d / 64 * L::HALF), &a.qmap, d, it.h * G,
                         (int)rq.row0 + q * TOK, q_full(s));
         }
+        if (!ok) break;
+       }
       }
       if (!ok) timed_out();
       const int zero = 0;
@@ -823,50 +837,53 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
       for (int x = n > 2 ? n - 2 : 0; x < n; ++x) wait_bar(k_full(x & 1), (uint32_t)((x / 2) & 1), &zero);
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ---- MMA issuer ----------------------------------------------------------
-    {
-      int c = 0, n = 0;
-      bool ok = true;
-      auto wait = [&](uint32_t b, int phase) { ok = ok && __all_sync(0xffffffffu, wait_bar(b, (uint32_t)(phase & 1), abort)); };
-      for (int i = i0; i < i1 && ok; ++i, ++n) {
-        const WeightItem it = load_item(a.witems + i);
+  } else if (warp < 3) {
+    // ---- MMA issuers, one a key tile -----------------------------------------------
+    const int x = warp - 1;
+    int c = 0, n = 0;
+    bool ok = true;
+    auto wait = [&](uint32_t b, int phase) {
+      ok = ok && __all_sync(0xffffffffu, wait_bar(b, (uint32_t)(phase & 1), abort));
+    };
+    for (int i = i0; i < i1 && ok; ++i) {
+      const WeightItem it = load_item(a.witems + i);
+      const int pages = uniform(it.pages), tiles = uniform(it.qe - it.qb);
+      for (int pg = 0; pg < pages && ok; ++pg, ++n) {
         const int b = n & 1;
         wait(k_full(b), n / 2);
-        for (int q = it.qb; q < it.qe && ok; ++q, ++c) {
+        const uint64_t k0 = sw128_desc(sb + (uint32_t)(L::K + (size_t)(2 * b + x) * L::TILE));
+        for (int q = 0; q < tiles && ok; ++q, ++c) {
           const int s = c % NQ, z = c & 1;
           wait(q_full(s), c / NQ);
+          if (c >= 2) wait(s_free(x, z), c / 2 - 1);
+          if (!ok) break;
+          tc_fence_after();
           const uint64_t q0 = sw128_desc(sb + (uint32_t)(L::Q + (size_t)s * L::TILE));
-          for (int x = 0; x < 2 && ok; ++x) {
-            if (c >= 2) wait(s_free(x, z), c / 2 - 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t k0 = sw128_desc(sb + (uint32_t)(L::K + (size_t)(2 * b + x) * L::TILE));
 #pragma unroll
-            for (int e = 0; e < D / 16; ++e) {
-              const uint64_t off = (uint64_t)(((e >> 2) * L::HALF + (e & 3) * 32) >> 4);
-              mma_ss(tmem + (uint32_t)(x * 256 + z * 128), k0 + off, q0 + off, idesc(128, false), e > 0 ? 1u : 0u);
-            }
-            commit(s_ready(x, z));
+          for (int e = 0; e < D / 16; ++e) {
+            const uint64_t off = (uint64_t)(((e >> 2) * L::HALF + (e & 3) * 32) >> 4);
+            mma_ss(tmem + (uint32_t)(x * 256 + z * 128), k0 + off, q0 + off, idesc(128, false), e > 0 ? 1u : 0u);
           }
-          if (ok) commit(q_empty(s));
+          commit(s_ready(x, z));
+          commit(q_empty(s));
         }
         if (ok) commit(k_empty(b));
       }
-      if (!ok && lane == 0) timed_out();
-      commit(mma_done);
-      const int zero = 0;
-      wait_bar(mma_done, 0u, &zero);
     }
+    if (!ok && lane == 0) timed_out();
+    commit(mma_done(x));
+    const int zero = 0;
+    wait_bar(mma_done(x), 0u, &zero);
     __syncwarp();
-  } else if (warp == 2) {
+  } else if (warp == 3) {
     // ---- statistics of the query tiles -------------------------------------------
     int c = 0;
     bool ok = true;
     for (int i = i0; i < i1 && ok; ++i) {
       const WeightItem it = load_item(a.witems + i);
       const ChunkReq rq = load_req(a.reqs + it.r);
-      for (int q = it.qb; q < it.qe; ++q, ++c) {
+      for (int pg = 0; pg < it.pages && ok; ++pg)
+       for (int q = it.qb; q < it.qe; ++q, ++c) {
         const int b = c & 1;
         if (c >= 2) ok = __all_sync(0xffffffffu, wait_bar(t_empty(b), (uint32_t)((c / 2 - 1) & 1), abort));
         if (!ok) break;
@@ -893,7 +910,8 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
     for (int i = i0; i < i1 && ok; ++i) {
       const WeightItem it = load_item(a.witems + i);
       const ChunkReq rq = load_req(a.reqs + it.r);
-      const int slot_i = it.page * PAGE + x * TK + key;  // this thread's logical slot
+     for (int pg = it.page; pg < it.page + it.pages && ok; ++pg) {
+      const int slot_i = pg * PAGE + x * TK + key;  // this thread's logical slot
       float2 w[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       for (int q = it.qb; q < it.qe; ++q, ++c) {
         const int z = c & 1;
@@ -901,39 +919,41 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
              __all_sync(0xffffffffu, wait_bar(s_ready(x, z), (uint32_t)((c / 2) & 1), abort));
         if (!ok) break;
         tc_fence_after();
-        uint32_t r[2][32];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          tmem_load32(tmem + lanes + (uint32_t)(x * 256 + z * 128 + half * 64 + h * 32), r[h]);
-        const float4* st = reinterpret_cast<const float4*>(sm + L::STAT) + z * 32 + half * 16;
         // of this half's columns lo .. hi - 1 count: rows of tokens that see the slot and exist
         const int lo = (slot_i - rq.cached - q * TOK) * G - half * 64, hi = (rq.nnew - q * TOK) * G - half * 64;
-        tmem_wait_ld();
+        if (hi > 0) {
+          uint32_t r[2][32];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) tmem_arrived(r[h]);
-        if (__any_sync(0xffffffffu, lo > 0 || hi < 64)) {
+          for (int h = 0; h < 2; ++h)
+            tmem_load32(tmem + lanes + (uint32_t)(x * 256 + z * 128 + half * 64 + h * 32), r[h]);
+          const float4* st = reinterpret_cast<const float4*>(sm + L::STAT) + z * 32 + half * 16;
+          tmem_wait_ld();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) tmem_arrived(r[h]);
+          if (__any_sync(0xffffffffu, lo > 0 || hi < 64)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (32 * h + e < lo || 32 * h + e >= hi) r[h][e] = 0xff800000u;  // -inf
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * h + e < lo || 32 * h + e >= hi) r[h][e] = 0xff800000u;  // -inf
+            for (int e = 0; e < 8; ++e) {
+              const float4 nm = st[8 * h + e];
+              float2 u = fma2(make_float2(__uint_as_float(r[h][4 * e]), __uint_as_float(r[h][4 * e + 1])), sc2,
+                              make_float2(nm.x, nm.y));
+              float2 v = fma2(make_float2(__uint_as_float(r[h][4 * e + 2]), __uint_as_float(r[h][4 * e + 3])), sc2,
+                              make_float2(nm.z, nm.w));
+              u.x = ex2f(u.x);
+              u.y = ex2f(u.y);
+              v.x = ex2f(v.x);
+              v.y = ex2f(v.y);
+              w[e & 1] = add2(w[e & 1], u);
+              w[2 + (e & 1)] = add2(w[2 + (e & 1)], v);
+            }
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 nm = st[8 * h + e];
-            float2 u = fma2(make_float2(__uint_as_float(r[h][4 * e]), __uint_as_float(r[h][4 * e + 1])), sc2,
-                            make_float2(nm.x, nm.y));
-            float2 v = fma2(make_float2(__uint_as_float(r[h][4 * e + 2]), __uint_as_float(r[h][4 * e + 3])), sc2,
-                            make_float2(nm.z, nm.w));
-            u.x = ex2f(u.x);
-            u.y = ex2f(u.y);
-            v.x = ex2f(v.x);
-            v.y = ex2f(v.y);
-            w[e & 1] = add2(w[e & 1], u);
-            w[2 + (e & 1)] = add2(w[2 + (e & 1)], v);
-          }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -957,6 +977,7 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
       } else if (slot_i < rq.cached + rq.nnew && rq.slot >= 0 && rq.slot < a.M) {
         a.weights[(((size_t)a.layer * a.M + rq.slot) * a.Hkv + it.h) * a.cap + slot_i] += sum;
       }
+     }
     }
     if (!ok && lane == 0) timed_out();
   }
@@ -980,12 +1001,20 @@ __global__ void __launch_bounds__(PAGE) k_chunk_weights_join(const __grid_consta
   a.weights[(((size_t)a.layer * a.M + rq.slot) * a.Hkv + jn.h) * a.cap + i] += w;
 }
 
+template <int D, int G, bool KEYS>
+cudaError_t attention_launch(const ChunkTcArgs& a, int grid, cudaStream_t s) {
+  if (grid == 0) return cudaSuccess;
+  constexpr int smem = (int)Sm<D, KEYS>::BYTES;
+  const cudaError_t e = cudaFuncSetAttribute(k_chunk_tc<D, G, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  k_chunk_tc<D, G, KEYS><<<dim3((unsigned)grid), NT, smem, s>>>(a);
+  return cudaGetLastError();
+}
 template <int D, int G>
 cudaError_t attention(const ChunkTcArgs& a, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(k_chunk_tc<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sm<D>::BYTES);
-  if (e != cudaSuccess) return e;
-  k_chunk_tc<D, G><<<dim3((unsigned)a.grid), NT, Sm<D>::BYTES, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess || a.n_joins == 0) return e;
+  cudaError_t e = attention_launch<D, G, false>(a, a.grid, s);
+  if (e == cudaSuccess) e = attention_launch<D, G, true>(a, a.kgrid, s);
+  if (e != cudaSuccess || a.n_joins == 0) return e;
   k_chunk_join<D, G><<<dim3((unsigned)a.n_joins, D / 16), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
@@ -1003,7 +1032,7 @@ cudaError_t weights(const ChunkTcArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_chunk_tc(const ChunkTcArgs& a, cudaStream_t s) {
-  if (a.grid < 1 || !chunk_tc_shape(a.D, a.G)) return cudaErrorInvalidValue;
+  if (a.grid + a.kgrid < 1 || !chunk_tc_shape(a.D, a.G)) return cudaErrorInvalidValue;
   if (a.D == 128) return a.G == 4 ? attention<128, 4>(a, s) : attention<128, 2>(a, s);
   return a.G == 4 ? attention<64, 4>(a, s) : attention<64, 2>(a, s);
 }

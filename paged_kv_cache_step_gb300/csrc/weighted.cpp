@@ -57,47 +57,79 @@ gp_status check_new_tokens(gp_ctx* c, int32_t layer, int32_t n, const gp_request
 // ---- work of the tensor-core chunk kernels --------------------------------------
 
 // Work laid end to end and cut into one even share a CTA, of at least `least`.
-// A job is `n` tiles that cost `cost` each, and every piece of it `fixed` more.
-// begin: the first piece of every CTA, and the number of pieces.
+// A job is `n` tiles that cost `cost` each, `times` of them alike one after the
+// other; every piece of a job costs `fixed` more.  A piece is tiles [from, to)
+// of one job, or `times` whole ones.  begin: the first piece of every CTA, and
+// the number of pieces.
 struct Job {
-  int n, cost;
+  int n, cost, times;
 };
 struct Piece {
-  int job, from, to;
+  int job, at, times;  // `times` jobs from the `at`-th of the run
+  int from, to;        // tiles (all of them when times > 1)
 };
+int lay_out(const std::vector<Job>& jobs, int64_t share, int fixed, std::vector<Piece>* pieces,
+            std::vector<int32_t>* begin) {
+  int ctas = 1, count = 0;
+  int64_t room = share;
+  auto put = [&](const Piece& p) {
+    ++count;
+    if (pieces) pieces->push_back(p);
+  };
+  auto next_cta = [&] {
+    ++ctas;
+    if (begin) begin->push_back(count);
+    room = share;
+  };
+  for (int k = 0; k < (int)jobs.size(); ++k) {
+    const Job& j = jobs[k];
+    const int64_t whole = fixed + (int64_t)j.n * j.cost;
+    for (int at = 0; at < j.times;) {
+      if (whole <= room) {
+        const int take = (int)std::min<int64_t>(j.times - at, room / whole);
+        put({k, at, take, 0, j.n});
+        at += take;
+        room -= take * whole;
+        continue;
+      }
+      for (int from = 0; from < j.n;) {
+        if (room < share && room < fixed + (int64_t)j.cost * std::min(j.n - from, 2)) next_cta();
+        int take = (int)std::min<int64_t>(j.n - from, std::max<int64_t>(1, (room - fixed) / j.cost));
+        if (j.n - from - take == 1) ++take;  // no sliver of one tile
+        put({k, at, 1, from, from + take});
+        from += take;
+        room -= fixed + (int64_t)j.cost * take;
+      }
+      ++at;
+    }
+  }
+  if (begin) begin->push_back(count);
+  return ctas;
+}
 void cut_even(const std::vector<Job>& jobs, int ctas, int fixed, int least, std::vector<Piece>& pieces,
               std::vector<int32_t>& begin) {
   int64_t total = 0;
-  for (const Job& j : jobs) total += fixed + (int64_t)j.n * j.cost;
-  // pieces add their fixed cost and are not slivers, so an exact share may need
-  // one CTA too many: the share grows until it does not
-  for (int64_t share = std::max<int64_t>(least, (total + ctas - 1) / ctas);; share += std::max<int64_t>(1, share / 64)) {
-    pieces.clear();
-    begin.assign(1, 0);
-    int64_t room = share;
-    for (int k = 0; k < (int)jobs.size(); ++k) {
-      const Job& j = jobs[k];
-      for (int at = 0; at < j.n;) {
-        if (room < share && room < fixed + (int64_t)j.cost * std::min(j.n - at, 2)) {
-          begin.push_back((int32_t)pieces.size());
-          room = share;
-        }
-        int take = (int)std::min<int64_t>(j.n - at, std::max<int64_t>(1, (room - fixed) / j.cost));
-        if (j.n - at - take == 1) ++take;  // no sliver of one tile
-        pieces.push_back({k, at, at + take});
-        at += take;
-        room -= fixed + (int64_t)j.cost * take;
-      }
-    }
-    begin.push_back((int32_t)pieces.size());
-    if ((int)begin.size() - 1 <= ctas) return;
+  int most = 1;
+  for (const Job& j : jobs) {
+    total += (fixed + (int64_t)j.n * j.cost) * j.times;
+    most = std::max(most, j.cost);
   }
+  // cut pieces add their fixed cost, and a share ends early or late by a few
+  // tiles, so an exact share may need more CTAs: it grows in steps up to one
+  // that cannot
+  const int64_t slack = 2 * fixed + 4 * most;
+  int64_t share = std::max<int64_t>(least, (total + ctas - 1) / ctas);
+  for (int64_t step = std::max<int64_t>(1, slack / 4); lay_out(jobs, share, fixed, nullptr, nullptr) > ctas;)
+    share += step;
+  pieces.clear();
+  begin.assign(1, 0);
+  lay_out(jobs, share, fixed, &pieces, &begin);
 }
 
 struct ChunkPlan {
-  std::vector<ChunkItem> items;
+  std::vector<ChunkItem> items, kitems;
   std::vector<ChunkJoin> joins;
-  std::vector<int32_t> begin;
+  std::vector<int32_t> begin, kbegin;
   int parts = 0;
   std::vector<WeightItem> witems;
   std::vector<WeightJoin> wjoins;
@@ -106,97 +138,111 @@ struct ChunkPlan {
 };
 
 // Attention: pairs of query tiles that follow each other (a key tile costs two
-// products' time), or the last tile alone with its key tiles split between
-// the groups (one).  A piece's fixed cost is the time to load Q and to empty
-// the pipeline, about two tiles.
+// products' time), and the last tiles alone, their key tiles split between the
+// groups (one).  A piece's fixed cost is the time to load Q and to empty the
+// pipeline, about two tiles.
 void plan_chunk(int n, const int32_t* cached, const int32_t* fresh, int Hkv, int G, int ctas, bool weights,
                 ChunkPlan* p) {
   const int tok = 128 / G;
   std::vector<Job> jobs;
   std::vector<ChunkItem> of;
-  for (int r = 0; r < n; ++r) {
-    const int tiles = (fresh[r] + tok - 1) / tok;
-    for (int h = 0; h < Hkv; ++h)
-      for (int t = 0; t < tiles; t += 2) {
-        const bool alone = t + 1 == tiles;
-        const int last = std::min((t + (alone ? 1 : 2)) * tok, fresh[r]);
-        jobs.push_back({(cached[r] + last + 127) / 128, alone ? 1 : 2});
-        of.push_back({r, h, t * tok, alone, 0, 0, -1, -1});
-      }
-  }
   std::vector<Piece> pieces;
-  cut_even(jobs, ctas, 2, 6, pieces, p->begin);
-  for (size_t k = 0; k < pieces.size();) {
-    size_t e = k;
-    while (e < pieces.size() && pieces[e].job == pieces[k].job) ++e;
+  // pairs
+  for (int r = 0; r < n; ++r)
+    for (int h = 0; h < Hkv; ++h)
+      for (int t = 0; t + tok < fresh[r]; t += 2 * tok) {
+        jobs.push_back({(cached[r] + std::min(t + 2 * tok, fresh[r]) + 127) / 128, 2, 1});
+        of.push_back({r, h, t, 0, 0, 0, -1, -1});
+      }
+  if (!jobs.empty()) cut_even(jobs, ctas, 2, 6, pieces, p->begin);
+  for (size_t k = 0, e; k < pieces.size(); k = e) {
+    for (e = k; e < pieces.size() && pieces[e].job == pieces[k].job;) ++e;
     const ChunkItem& job = of[pieces[k].job];
     const int count = (int)(e - k), first = p->parts;
-    if (job.keys) {
-      int parts = 0;
-      for (size_t i = k; i < e; ++i) parts += pieces[i].to - pieces[i].from > 1 ? 2 : 1;
-      int part = first;
-      for (size_t i = k; i < e; ++i) {
-        ChunkItem it = job;
-        it.kb = pieces[i].from;
-        it.ke = pieces[i].to;
-        if (parts > 1) {
-          it.part_a = part++;
-          if (it.ke - it.kb > 1) it.part_b = part++;
-        }
-        p->items.push_back(it);
-      }
-      if (parts > 1) {
-        p->joins.push_back({job.r, job.h, job.t0, first, parts, {}});
-        p->parts += parts;
-      }
-    } else {
-      for (size_t i = k; i < e; ++i) {
-        ChunkItem it = job;
-        it.kb = pieces[i].from;
-        it.ke = pieces[i].to;
-        if (count > 1) {
-          it.part_a = first + (int)(i - k);
-          it.part_b = first + count + (int)(i - k);
-        }
-        p->items.push_back(it);
-      }
+    for (size_t i = k; i < e; ++i) {
+      ChunkItem it = job;
+      it.kb = pieces[i].from;
+      it.ke = pieces[i].to;
       if (count > 1) {
-        p->joins.push_back({job.r, job.h, job.t0, first, count, {}});
-        p->joins.push_back({job.r, job.h, job.t0 + tok, first + count, count, {}});
-        p->parts += 2 * count;
+        it.part_a = first + (int)(i - k);
+        it.part_b = first + count + (int)(i - k);
       }
+      p->items.push_back(it);
     }
-    k = e;
+    if (count > 1) {
+      p->joins.push_back({job.r, job.h, job.t0, first, count, {}});
+      p->joins.push_back({job.r, job.h, job.t0 + tok, first + count, count, {}});
+      p->parts += 2 * count;
+    }
+  }
+  // last tiles alone
+  jobs.clear();
+  of.clear();
+  pieces.clear();
+  for (int r = 0; r < n; ++r) {
+    const int tiles = (fresh[r] + tok - 1) / tok;
+    if (tiles % 2 == 0) continue;
+    for (int h = 0; h < Hkv; ++h) {
+      jobs.push_back({(cached[r] + fresh[r] + 127) / 128, 1, 1});
+      of.push_back({r, h, (tiles - 1) * tok, 0, 0, 0, -1, -1});
+    }
+  }
+  if (!jobs.empty()) cut_even(jobs, ctas, 2, 6, pieces, p->kbegin);
+  for (size_t k = 0, e; k < pieces.size(); k = e) {
+    int parts = 0;
+    for (e = k; e < pieces.size() && pieces[e].job == pieces[k].job; ++e) parts += pieces[e].to - pieces[e].from > 1 ? 2 : 1;
+    const ChunkItem& job = of[pieces[k].job];
+    int part = p->parts;
+    for (size_t i = k; i < e; ++i) {
+      ChunkItem it = job;
+      it.kb = pieces[i].from;
+      it.ke = pieces[i].to;
+      if (parts > 1) {
+        it.part_a = part++;
+        if (it.ke - it.kb > 1) it.part_b = part++;
+      }
+      p->kitems.push_back(it);
+    }
+    if (parts > 1) {
+      p->joins.push_back({job.r, job.h, job.t0, p->parts, parts, {}});
+      p->parts += parts;
+    }
   }
   if (!weights) return;
   // Weights: a page against the query tiles that see it; loading the page
-  // costs about two query tiles' products.
+  // costs about two query tiles' products.  The pages that every token sees
+  // are alike.
   jobs.clear();
   std::vector<WeightItem> wof;
   for (int r = 0; r < n; ++r) {
     const int tiles = (fresh[r] + tok - 1) / tok, pages = (cached[r] + fresh[r] + kPage - 1) / kPage;
     if (fresh[r] == 0) continue;
-    for (int h = 0; h < Hkv; ++h)
-      for (int pg = 0; pg < pages; ++pg) {
-        const int q0 = std::max(0, pg * kPage - cached[r]) / tok;
-        jobs.push_back({tiles - q0, 1});
-        wof.push_back({r, h, pg, q0, tiles, -1, {}});
+    const int seen = std::min(pages, (cached[r] + tok - 1) / kPage + 1);  // pages that the first query tile sees some of
+    for (int h = 0; h < Hkv; ++h) {
+      jobs.push_back({tiles, 1, seen});
+      wof.push_back({r, h, 0, 0, 0, tiles, -1, 0});
+      for (int pg = seen; pg < pages; ++pg) {
+        const int q0 = (pg * kPage - cached[r]) / tok;
+        jobs.push_back({tiles - q0, 1, 1});
+        wof.push_back({r, h, pg, 0, q0, tiles, -1, 0});
       }
-  }
-  cut_even(jobs, ctas, 2, 6, pieces, p->wbegin);
-  for (size_t k = 0; k < pieces.size();) {
-    size_t e = k;
-    while (e < pieces.size() && pieces[e].job == pieces[k].job) ++e;
-    const WeightItem& job = wof[pieces[k].job];
-    for (size_t i = k; i < e; ++i) {
-      WeightItem it = job;
-      it.qb = job.qb + pieces[i].from;
-      it.qe = job.qb + pieces[i].to;
-      it.part = e - k > 1 ? p->wparts++ : -1;
-      p->witems.push_back(it);
     }
-    if (e - k > 1) p->wjoins.push_back({job.r, job.h, job.page, p->wparts - (int)(e - k), (int)(e - k), {}});
-    k = e;
+  }
+  pieces.clear();
+  cut_even(jobs, ctas, 2, 6, pieces, p->wbegin);
+  for (size_t k = 0; k < pieces.size(); ++k) {
+    const Piece& pc = pieces[k];
+    WeightItem it = wof[pc.job];
+    it.page += pc.at;
+    it.pages = pc.times;
+    if (pc.to - pc.from < jobs[pc.job].n) {  // a part of a page's query tiles
+      if (pc.from == 0) p->wjoins.push_back({it.r, it.h, it.page, p->wparts, 0, {}});
+      ++p->wjoins.back().n;
+      it.part = p->wparts++;
+    }
+    it.qe = it.qb + pc.to;
+    it.qb += pc.from;
+    p->witems.push_back(it);
   }
 }
 
@@ -329,6 +375,7 @@ gp_status gp_chunk_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_reque
   };
   const size_t at_tiles = table(tiles), at_wtiles = table(wtiles);
   const size_t at_items = table(plan.items), at_begin = table(plan.begin), at_joins = table(plan.joins);
+  const size_t at_kitems = table(plan.kitems), at_kbegin = table(plan.kbegin);
   const size_t at_witems = table(plan.witems), at_wbegin = table(plan.wbegin), at_wjoins = table(plan.wjoins);
   const size_t at_part = scratch.take(sizeof(float) * chunk_part_floats(g.head_dim) * (size_t)plan.parts);
   const size_t at_wpart = scratch.take(sizeof(float) * kPage * (size_t)plan.wparts);
@@ -372,7 +419,10 @@ gp_status gp_chunk_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_reque
     a.bt = dbt;
     a.items = reinterpret_cast<const ChunkItem*>(dev + at_items);
     a.begin = reinterpret_cast<const int32_t*>(dev + at_begin);
-    a.grid = (int)plan.begin.size() - 1;
+    a.grid = std::max(0, (int)plan.begin.size() - 1);
+    a.kitems = reinterpret_cast<const ChunkItem*>(dev + at_kitems);
+    a.kbegin = reinterpret_cast<const int32_t*>(dev + at_kbegin);
+    a.kgrid = std::max(0, (int)plan.kbegin.size() - 1);
     a.joins = reinterpret_cast<const ChunkJoin*>(dev + at_joins);
     a.n_joins = (int)plan.joins.size();
     a.witems = reinterpret_cast<const WeightItem*>(dev + at_witems);

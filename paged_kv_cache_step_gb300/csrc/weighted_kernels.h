@@ -149,11 +149,11 @@ cudaError_t launch_chunk_weights(const ChunkArgs& a, cudaStream_t s);
 // 128 / G tokens of the G heads; a key tile 128 slots.
 //
 // Attention: an item is a range of key tiles for either two query tiles that
-// follow each other (pair = 0), or one query tile whose even key tiles go to
-// the first softmax group and odd ones to the second (pair = 1).
+// follow each other, or (kitems) one query tile whose even key tiles go to the
+// first softmax group and the odd ones to the second.
 struct ChunkItem {
   int32_t r, h, t0;      // request, KV head, first token
-  int32_t keys;          // 1: one query tile, the key tiles split between the groups
+  int32_t pad;
   int32_t kb, ke;        // key tiles
   int32_t part_a, part_b;// partial of each group, -1: its output directly
 };
@@ -162,12 +162,13 @@ static_assert(sizeof(ChunkItem) == 32, "two 16-byte loads");
 struct ChunkJoin {
   int32_t r, h, t0, first, n, pad[3];
 };
-// Weights: an item is 256 keys (a page) against a range of query tiles.
+// Weights: an item is one or more pages (256 keys each), one after the other,
+// against a range of query tiles.
 struct WeightItem {
-  int32_t r, h, page;
+  int32_t r, h, page, pages;
   int32_t qb, qe;        // query tiles
-  int32_t part;          // partial, -1: added to the weights directly
-  int32_t pad[2];
+  int32_t part;          // partial (of a single page), -1: added to the weights directly
+  int32_t pad;
 };
 struct WeightJoin {
   int32_t r, h, page, first, n, pad[3];
@@ -184,6 +185,9 @@ struct ChunkTcArgs {
   const ChunkItem* items;      // CTA c takes [begin[c], begin[c + 1])
   const int32_t* begin;
   int grid;
+  const ChunkItem* kitems;     // the same of the items of one query tile
+  const int32_t* kbegin;
+  int kgrid;
   const ChunkJoin* joins;
   int n_joins;
   const WeightItem* witems;
