@@ -250,7 +250,7 @@ __device__ __forceinline__ Work work_of(const ChunkItem& it, const ChunkReq& rq)
     // the first tile's last token sees fewer slots than the second's
     const int see = (rq.cached + min(it.t0 + TOK, rq.nnew) + TK - 1) / TK;
     w.cnt[0] = min(max(see - it.kb, 0), w.n);
-    w.cnt[1] = w.n;
+    w.cnt[1] = it.alone ? 0 : w.n;
   }
   return w;
 }
@@ -347,9 +347,9 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
           ++c;
         };
         if (nq > 0 && !(ok = wait_bar(q_empty, (uint32_t)((nq - 1) & 1), abort))) break;
-        mbar_expect_tx(q_full, L::NQT * L::TILE);
-#pragma unroll
-        for (int x = 0; x < L::NQT; ++x)
+        const int nqt = KEYS || it.alone ? 1 : 2;
+        mbar_expect_tx(q_full, (uint32_t)(nqt * L::TILE));
+        for (int x = 0; x < nqt; ++x)
 #pragma unroll
           for (int d = 0; d < D; d += 64)
             tma_load_3d(sb + (uint32_t)(L::Q + (size_t)x * L::TILE + d / 64 * L::HALF), &a.qmap, d, it.h * G,
@@ -454,9 +454,10 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
         }
       } else {
         // K tile j is c + 2 j, V tile j the one after it; the first group may see
-        // fewer tiles
+        // fewer tiles, the second have no query tile
+        const bool two = w.cnt[1] > 0;
         if (w.cnt[0] > 0) score(0, c);
-        score(1, c);
+        if (two) score(1, c);
         if (!ok) break;
         commit(empty(c % NST));
         if (w.n == 1) commit(q_empty);
@@ -466,11 +467,11 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
             value(0, kv, j == 0, j + 1 == w.cnt[0], ns[0], no[0]);
             if (ok && j + 1 < w.cnt[0]) score(0, kv + 1);
           }
-          value(1, kv, j == 0, j + 1 == w.n, ns[1], no[1]);
+          if (two) value(1, kv, j == 0, j + 1 == w.n, ns[1], no[1]);
           if (!ok) break;
           commit(empty(kv % NST));
           if (j + 1 < w.n) {
-            score(1, kv + 1);
+            if (two) score(1, kv + 1);
             if (!ok) break;
             commit(empty((kv + 1) % NST));
             if (j + 2 == w.n) commit(q_empty);

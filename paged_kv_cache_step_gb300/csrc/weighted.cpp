@@ -140,19 +140,30 @@ struct ChunkPlan {
 // Attention: pairs of query tiles that follow each other (a key tile costs two
 // products' time), and the last tiles alone, their key tiles split between the
 // groups (one).  A piece's fixed cost is the time to load Q and to empty the
-// pipeline, about two tiles.
+// pipeline, about two tiles.  The last tiles need a launch of their own, about
+// 8 us; beside pairs, up to 12 key tiles of them a CTA (about 0.6 us each) go
+// along as pairs without a second tile instead, at twice the cost (five ragged
+// prompts, d = 64: 47 us in one launch, 55 in two).
 void plan_chunk(int n, const int32_t* cached, const int32_t* fresh, int Hkv, int G, int ctas, bool weights,
                 ChunkPlan* p) {
   const int tok = 128 / G;
   std::vector<Job> jobs;
   std::vector<ChunkItem> of;
   std::vector<Piece> pieces;
-  // pairs
+  int64_t odd = 0;  // key tiles of the last tiles alone
+  bool pairs = false;
+  for (int r = 0; r < n; ++r) {
+    pairs |= fresh[r] > tok;
+    if ((fresh[r] + tok - 1) / tok % 2) odd += (int64_t)Hkv * ((cached[r] + fresh[r] + 127) / 128);
+  }
+  const bool along = pairs && odd <= 12ll * ctas;
   for (int r = 0; r < n; ++r)
     for (int h = 0; h < Hkv; ++h)
-      for (int t = 0; t + tok < fresh[r]; t += 2 * tok) {
+      for (int t = 0; t < fresh[r]; t += 2 * tok) {
+        const bool alone = t + tok >= fresh[r];
+        if (alone && !along) continue;
         jobs.push_back({(cached[r] + std::min(t + 2 * tok, fresh[r]) + 127) / 128, 2, 1});
-        of.push_back({r, h, t, 0, 0, 0, -1, -1});
+        of.push_back({r, h, t, alone, 0, 0, -1, -1});
       }
   if (!jobs.empty()) cut_even(jobs, ctas, 2, 6, pieces, p->begin);
   for (size_t k = 0, e; k < pieces.size(); k = e) {
@@ -165,14 +176,14 @@ void plan_chunk(int n, const int32_t* cached, const int32_t* fresh, int Hkv, int
       it.ke = pieces[i].to;
       if (count > 1) {
         it.part_a = first + (int)(i - k);
-        it.part_b = first + count + (int)(i - k);
+        if (!job.alone) it.part_b = first + count + (int)(i - k);
       }
       p->items.push_back(it);
     }
     if (count > 1) {
       p->joins.push_back({job.r, job.h, job.t0, first, count, {}});
-      p->joins.push_back({job.r, job.h, job.t0 + tok, first + count, count, {}});
-      p->parts += 2 * count;
+      if (!job.alone) p->joins.push_back({job.r, job.h, job.t0 + tok, first + count, count, {}});
+      p->parts += job.alone ? count : 2 * count;
     }
   }
   // last tiles alone
@@ -181,7 +192,7 @@ void plan_chunk(int n, const int32_t* cached, const int32_t* fresh, int Hkv, int
   pieces.clear();
   for (int r = 0; r < n; ++r) {
     const int tiles = (fresh[r] + tok - 1) / tok;
-    if (tiles % 2 == 0) continue;
+    if (tiles % 2 == 0 || along) continue;
     for (int h = 0; h < Hkv; ++h) {
       jobs.push_back({(cached[r] + fresh[r] + 127) / 128, 1, 1});
       of.push_back({r, h, (tiles - 1) * tok, 0, 0, 0, -1, -1});

@@ -149,11 +149,12 @@ cudaError_t launch_chunk_weights(const ChunkArgs& a, cudaStream_t s);
 // 128 / G tokens of the G heads; a key tile 128 slots.
 //
 // Attention: an item is a range of key tiles for either two query tiles that
-// follow each other, or (kitems) one query tile whose even key tiles go to the
-// first softmax group and the odd ones to the second.
+// follow each other (the second may be missing), or (kitems) one query tile
+// whose even key tiles go to the first softmax group and the odd ones to the
+// second.
 struct ChunkItem {
   int32_t r, h, t0;      // request, KV head, first token
-  int32_t pad;
+  int32_t alone;         // of a pair: there is no second query tile
   int32_t kb, ke;        // key tiles
   int32_t part_a, part_b;// partial of each group, -1: its output directly
 };
