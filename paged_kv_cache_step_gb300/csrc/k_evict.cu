@@ -8,17 +8,19 @@
 //           order-preserving key) of the threshold, then one ordered pass that
 //           writes the keep mask, the kept slot of every rank, and how many
 //           slots are kept below the first slot of every move item.
-//   move    in place, many CTAs a unit.  An item is evict_rows consecutive
-//           ranks -- target slots [kR, (k+1)R) -- so its rows are always all
-//           wanted, and its 32 KB of K and V pass through registers.
+//   move    in place, many warps a unit.  An item is evict_rows consecutive
+//           ranks -- target slots [kR, (k+1)R), consecutive rows of one page --
+//           so its rows are always all wanted, and its K and V pass through
+//           16 KB of shared memory: asynchronous copies in, a bulk copy out.
 //           Writing item k destroys the rows that live in those slots; the
 //           kept ones among them have ranks <= their slots, so they belong
-//           to items <= k.  CTAs take the items in order (a ticket), read
+//           to items <= k.  Warps take the items in order (a ticket), read
 //           their rows at once, raise the item's flag, and only then wait for
 //           the flags of the (at most two) items whose rows they will
 //           overwrite: a reader never waits, so the lowest item not yet read
 //           is always read, and every wait ends.  Waits are bounded all the
-//           same.
+//           same.  Fourteen warps an SM keep 224 KB of items on their way, each
+//           at a step of its own (ticket, kept slots, pages, rows, flags).
 // Bounded by HBM: kept rows are read and written once.
 #include <cstdint>
 
@@ -28,10 +30,10 @@ namespace gp {
 namespace {
 
 constexpr int PAGE = 256;
-constexpr int SNT = 512;  // select
-constexpr int SWARP = SNT / 32;
-constexpr int BINS = 2048;
-constexpr int MNT = 256;  // move
+constexpr int SNT = 512;    // select
+constexpr int BINS = 2048;  // a digit of 11 bits
+constexpr int MWARPS = 14;         // move: warps of a CTA, one CTA per SM,
+constexpr int STAGE = 16 * 1024;   // each with an item's K and V rows
 
 // Order-preserving key of a weight; -0 counts as 0, NaN as the largest.
 __device__ __forceinline__ unsigned okey(float v) {
@@ -40,7 +42,14 @@ __device__ __forceinline__ unsigned okey(float v) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// A warp has consecutive words (32 slots each) of the unit.  STAGED: the keys
+// are formed once and stay in shared memory for the five passes over them, else
+// the weights are read again.  (In registers, 16 a thread, they left one CTA an
+// SM: 96 us against 70 for 1024 units of 8192 slots, read again each pass.)
+template <bool STAGED>
 __global__ void __launch_bounds__(SNT) k_evict_select(const __grid_constant__ EvictArgs a) {
+  constexpr int SWARP = SNT / 32, PER_BIN = BINS / SNT;
+  extern __shared__ unsigned staged[];
   __shared__ unsigned hist[BINS];
   __shared__ unsigned wsum[SWARP], weq[SWARP];
   __shared__ unsigned s_bin, s_above;
@@ -56,11 +65,42 @@ __global__ void __launch_bounds__(SNT) k_evict_select(const __grid_constant__ Ev
     for (int w = tid; w < nw; w += SNT) mask[w] = rq.T - 32 * w >= 32 ? 0xffffffffu : (1u << (rq.T - 32 * w)) - 1u;
     return;
   }
-  unsigned* flags = a.flags + rq.item0 + (size_t)unit * rq.items;
-  for (int k = tid; k < rq.items; k += SNT) flags[k] = 0u;
   const float* w0 = a.weights + (((size_t)(unit / a.Hkv) * a.M + rq.slot) * a.Hkv + unit % a.Hkv) * a.cap;
   const int ncand = rq.T - rq.recent;
   const unsigned need = (unsigned)(rq.keep - rq.recent);  // 0 <= need < ncand
+  const int per = (nw + SWARP - 1) / SWARP, wa = min(nw, warp * per), wb = min(nw, wa + per);
+  if constexpr (STAGED) {
+    for (int i = tid; i < ncand; i += 8 * SNT) {  // eight loads in flight
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = i + j * SNT < ncand ? w0[i + j * SNT] : 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j * SNT < ncand) staged[i + j * SNT] = okey(v[j]);
+    }
+  }
+  unsigned* flags = a.flags + rq.item0 + (size_t)unit * rq.items;
+  for (int k = tid; k < rq.items; k += SNT) flags[k] = 0u;
+  // f(word, key) for this warp's words in order; the key counts where slot < ncand
+  auto each_word = [&](auto&& f) {
+    if constexpr (STAGED) {
+#pragma unroll 4
+      for (int w = wa; w < wb; ++w) f(w, 32 * w + lane < ncand ? staged[32 * w + lane] : 0u);
+    } else {
+      for (int w = wa; w < wb; w += 8) {  // eight loads in flight
+        unsigned k[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int s = 32 * (w + j) + lane;
+          k[j] = w + j < wb && s < ncand ? okey(w0[s]) : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (w + j < wb) f(w + j, k[j]);
+      }
+    }
+  };
+  if (need == 0) __syncthreads();  // the keys are staged (the passes below begin with a barrier)
 
   // ---- the need-th largest key: prefix, and how many keys lie above it ----
   unsigned prefix = 0u, mask_bits = 0u, above = 0u;
@@ -71,16 +111,15 @@ __global__ void __launch_bounds__(SNT) k_evict_select(const __grid_constant__ Ev
       const unsigned digit = pass == 2 ? 1023u : 2047u;
       for (int b = tid; b < BINS; b += SNT) hist[b] = 0u;
       __syncthreads();
-      for (int i = tid; i < ncand; i += SNT) {
-        const unsigned k = okey(w0[i]);
-        if ((k & mask_bits) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1u);
-      }
+      each_word([&](int w, unsigned k) {
+        if (32 * w + lane < ncand && (k & mask_bits) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1u);
+      });
       __syncthreads();
-      // thread t owns the four bins from BINS - 1 - 4 t down
-      unsigned c[4], own = 0u;
+      // thread t owns the PER_BIN bins from BINS - 1 - PER_BIN t down
+      unsigned c[PER_BIN], own = 0u;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        c[j] = hist[BINS - 1 - 4 * tid - j];
+      for (int j = 0; j < PER_BIN; ++j) {
+        c[j] = hist[BINS - 1 - PER_BIN * tid - j];
         own += c[j];
       }
       unsigned inc = own;
@@ -95,30 +134,33 @@ __global__ void __launch_bounds__(SNT) k_evict_select(const __grid_constant__ Ev
       for (int w = 0; w < warp; ++w) cum += wsum[w];
       const unsigned want = need - above;
       if (cum < want && want <= cum + own) {  // one thread: the bins' counts sum to at least `want`
-        int j = 0;
-        while (j < 3 && cum + c[j] < want) cum += c[j++];
-        s_bin = (unsigned)(BINS - 1 - 4 * tid - j);
+        int bin = BINS - 1 - PER_BIN * tid;
+#pragma unroll
+        for (int j = 0; j < PER_BIN - 1; ++j)
+          if (bin == BINS - 1 - PER_BIN * tid - j && cum + c[j] < want) {
+            cum += c[j];
+            --bin;
+          }
+        s_bin = (unsigned)bin;
         s_above = cum;
       }
       __syncthreads();
       prefix |= s_bin << shift;
       mask_bits |= digit << shift;
       above += s_above;
-      __syncthreads();
     }
   }
   const unsigned thr = prefix, take_eq = need - above;  // of the keys equal to thr, the first take_eq
 
-  // ---- the ordered pass: a warp has consecutive words ------------------------
-  const int per = (nw + SWARP - 1) / SWARP, wa = min(nw, warp * per), wb = min(nw, wa + per);
+  // ---- the ordered pass ------------------------------------------------------
+  auto sure_of = [&](int s, unsigned k) { return (s >= ncand && s < rq.T) || (s < ncand && need > 0 && k > thr); };
+  auto tie_of = [&](int s, unsigned k) { return s < ncand && need > 0 && k == thr; };
   unsigned cnt = 0u, eqs = 0u;  // kept whatever the ties, and ties
-  for (int w = wa; w < wb; ++w) {
-    const int s = 32 * w + lane;
-    const unsigned k = s < ncand && need > 0 ? okey(w0[s]) : 0u;
-    const bool sure = (s >= ncand && s < rq.T) || (s < ncand && need > 0 && k > thr);
-    cnt += __popc(__ballot_sync(0xffffffffu, sure));
-    eqs += __popc(__ballot_sync(0xffffffffu, s < ncand && need > 0 && k == thr));
-  }
+  each_word([&](int w, unsigned k) {
+    cnt += __popc(__ballot_sync(0xffffffffu, sure_of(32 * w + lane, k)));
+    eqs += __popc(__ballot_sync(0xffffffffu, tie_of(32 * w + lane, k)));
+  });
+  __syncthreads();  // wsum is read above
   if (lane == 0) {
     wsum[warp] = cnt;
     weq[warp] = eqs;
@@ -132,11 +174,9 @@ __global__ void __launch_bounds__(SNT) k_evict_select(const __grid_constant__ Ev
   const int R = evict_rows(a.row_bytes);
   uint16_t* idx = a.idx + rq.idx_off + (size_t)unit * rq.keep;
   int32_t* pre = a.pre + rq.pre_off + (size_t)unit * (rq.items + 1);
-  for (int w = wa; w < wb; ++w) {
+  each_word([&](int w, unsigned k) {
     const int s = 32 * w + lane;
-    const unsigned k = s < ncand && need > 0 ? okey(w0[s]) : 0u;
-    const bool sure = (s >= ncand && s < rq.T) || (s < ncand && need > 0 && k > thr);
-    const bool tie = s < ncand && need > 0 && k == thr;
+    const bool sure = sure_of(s, k), tie = tie_of(s, k);
     const unsigned below = (1u << lane) - 1u;
     const unsigned bt = __ballot_sync(0xffffffffu, tie);
     const bool kept = sure || (tie && eq_before + __popc(bt & below) < take_eq);
@@ -145,11 +185,16 @@ __global__ void __launch_bounds__(SNT) k_evict_select(const __grid_constant__ Ev
     if (kept) idx[rank + __popc(bk & below)] = (uint16_t)s;
     if (lane == 0) {
       mask[w] = bk;
-      if ((32 * w) % R == 0 && 32 * w / R <= rq.items) pre[32 * w / R] = (int32_t)rank;
+      if (R < 32) {  // two items a word
+        if (2 * w <= rq.items) pre[2 * w] = (int32_t)rank;
+        if (2 * w + 1 <= rq.items) pre[2 * w + 1] = (int32_t)(rank + __popc(bk & 0xffffu));
+      } else if ((32 * w) % R == 0 && 32 * w / R <= rq.items) {
+        pre[32 * w / R] = (int32_t)rank;
+      }
     }
     sure_before += __popc(__ballot_sync(0xffffffffu, sure));
     eq_before += __popc(bt);
-  }
+  });
   if (tid == 0 && rq.items * R >= 32 * nw) pre[rq.items] = rq.keep;
 }
 
@@ -158,118 +203,183 @@ __device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ void st_release(unsigned* p, unsigned v) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ void st_relaxed(unsigned* p, unsigned v) {
+  asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
 template <int RB>
-__global__ void __launch_bounds__(MNT) k_evict_move(const __grid_constant__ EvictArgs a) {
-  constexpr int R = evict_rows(RB);   // rows of an item
-  constexpr int PIECES = RB / 16;     // 16-byte pieces of a row
-  constexpr int PER = R * PIECES / MNT;  // pieces of K (and of V) a thread carries
-  static_assert(PER * MNT == R * PIECES && R <= MNT && R % 32 == 0 && PAGE % R == 0, "item shape");
-  __shared__ unsigned long long s_item;
-  __shared__ int s_src[R];  // source slot, -1: the row stays where it is
-  __shared__ int s_fail;
-  const int tid = threadIdx.x;
+__global__ void __launch_bounds__(32 * MWARPS, 1) k_evict_move(const __grid_constant__ EvictArgs a) {
+  constexpr int R = evict_rows(RB);        // rows of an item
+  constexpr int PIECES = RB / 16;          // 16-byte pieces of a row
+  constexpr int LOADS = R * PIECES / 32;   // pieces of K (and of V) a lane copies
+  constexpr int OWN = (R + 31) / 32;       // rows a lane looks up
+  static_assert((R % 32 == 0 || R == 16) && PAGE % R == 0 && 2 * R * RB == STAGE, "item shape");
+  extern __shared__ __align__(128) unsigned char stages[];
+  const int lane = threadIdx.x & 31;
+  unsigned char* stage = stages + (size_t)(threadIdx.x >> 5) * STAGE;  // this warp's K rows, then V rows
+  const uint32_t st = static_cast<uint32_t>(__cvta_generic_to_shared(stage));
   unsigned char* kc = static_cast<unsigned char*>(a.k_cache);
   unsigned char* vc = static_cast<unsigned char*>(a.v_cache);
   unsigned moved = 0u;
-  if (tid == 0) s_fail = 0;
-  for (;;) {
-    if (tid == 0) s_item = atomicAdd(a.ticket, 1ull);
-    __syncthreads();
-    const int64_t item = (int64_t)s_item;
-    if (item >= a.items) break;
-    int lo = 0, hi = a.n;  // reqs[lo].item0 <= item < reqs[hi].item0
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.reqs[mid].item0 <= item) lo = mid;
-      else hi = mid;
+  bool fail = false, stored = false;
+  uint64_t once;  // L2 policy of rows that are not read again
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+  auto take = [&] {  // the next item, in every lane
+    unsigned long long t = 0ull;
+    if (lane == 0) t = atomicAdd(a.ticket, 1ull);
+    return (int64_t)__shfl_sync(0xffffffffu, t, 0);
+  };
+  struct Item {
+    int64_t id;
+    int k, rows;
+    bool any, clear;      // some row moves; the target slots' rows are known to be read
+    int wait0, wait1;     // items whose flags that takes, -1: none
+    size_t dst;           // byte offset of the targets in K (and V)
+    float* wrow;
+    unsigned* flags;
+    int src[OWN];         // the lane's rows lane, lane + 32, ...: slot,
+    long long off[OWN];   // byte offset, -1: no row,
+    float wv[OWN];        // weight
+    unsigned stay;        // bit o: the row stays where it is
+  };
+  EvictReq rq{};
+  int64_t rq_end = -1;  // first item past rq's
+  auto look_up = [&](int64_t id) {
+    Item it;
+    it.id = id;
+    it.any = false;
+    if (id >= a.items) return it;
+    if (id >= rq_end) {  // items come in order: mostly the request of the last one
+      int lo = 0, hi = a.n;  // reqs[lo].item0 <= id < reqs[hi].item0
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.reqs[mid].item0 <= id) lo = mid;
+        else hi = mid;
+      }
+      rq = a.reqs[lo];
+      rq_end = rq.item0 + (int64_t)rq.items * a.L * a.Hkv;
     }
-    const EvictReq rq = a.reqs[lo];
-    const int unit = (int)((item - rq.item0) / rq.items), k = (int)((item - rq.item0) % rq.items);
+    const int units = a.L * a.Hkv;
+    const int unit = (int)((id - rq.item0) % units), k = (int)((id - rq.item0) / units);
     const int layer = unit / a.Hkv, h = unit % a.Hkv;
-    const int rows = min(R, rq.keep - k * R);
     const int32_t* ob = a.old_bt + rq.bt_off;
-    const int32_t* nb = a.new_bt + rq.bt_off;
-    const int dpage = nb[k * R / PAGE];  // an item's targets share a page
-    const bool same_page = ob[k * R / PAGE] == dpage;
-    if (tid < rows) {
-      const int s = a.idx[rq.idx_off + (size_t)unit * rq.keep + k * R + tid];
-      s_src[tid] = s == k * R + tid && same_page ? -1 : s;
-    }
-    __syncthreads();
-    const size_t lbase = (size_t)layer * a.num_pages_total;
-    float* wrow = a.weights + (((size_t)layer * a.M + rq.slot) * a.Hkv + h) * a.cap;
-    // ---- read ----
-    uint4 kv[PER], vv[PER];
-    float wv = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int p = tid + i * MNT, row = p / PIECES, q = p % PIECES;
-      const int s = row < rows ? s_src[row] : -1;
-      if (s >= 0) {
-        const size_t off = ((lbase + ob[s / PAGE]) * a.Hkv + h) * (size_t)(PAGE * RB) + (size_t)(s % PAGE) * RB + q * 16;
-        kv[i] = *reinterpret_cast<const uint4*>(kc + off);
-        vv[i] = *reinterpret_cast<const uint4*>(vc + off);
-      }
-    }
-    const bool wmove = tid < rows && s_src[tid] >= 0;
-    if (wmove) wv = wrow[s_src[tid]];
-    // the block's reads come before the flag: barrier, then a release at GPU scope
-    __syncthreads();
     const int32_t* pre = a.pre + rq.pre_off + (size_t)unit * (rq.items + 1);
-    unsigned* flags = a.flags + rq.item0 + (size_t)unit * rq.items;
-    if (tid == 0) {
-      __threadfence();
-      st_release(flags + k, 1u);
-    }
-    // ---- the rows that live in the target slots have been read ----
-    if (tid < 2) {
-      const int p0 = pre[k], p1 = pre[k + 1];
-      const int j = p0 / R + tid;  // items p0 / R .. (p1 - 1) / R, two at most, none above k
-      if (p1 > p0 && j <= (p1 - 1) / R && j < k) {
-        const long long t0 = clock64();
-        bool ok = a.wait_limit > 0 && ld_acquire(flags + j) != 0u;
-        while (!ok) {
-          if (clock64() - t0 >= a.wait_limit) break;
-          ok = ld_acquire(flags + j) != 0u;
-        }
-        if (!ok) atomicOr(&s_fail, 1);
-      }
-    }
-    __syncthreads();
-    if (s_fail) break;  // read after the barrier: all threads leave together
-    // ---- write ----
-    const size_t dbase = ((lbase + dpage) * a.Hkv + h) * (size_t)(PAGE * RB) + (size_t)(k * R % PAGE) * RB;
+    const size_t lbase = (size_t)layer * a.num_pages_total;
+    it.k = k;
+    it.rows = min(R, rq.keep - k * R);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int p = tid + i * MNT, row = p / PIECES;
-      if (row < rows && s_src[row] >= 0) {
-        *reinterpret_cast<uint4*>(kc + dbase + (size_t)p * 16) = kv[i];
-        *reinterpret_cast<uint4*>(vc + dbase + (size_t)p * 16) = vv[i];
+    for (int o = 0; o < OWN; ++o) {
+      const int r = lane + 32 * o;
+      it.src[o] = r < it.rows ? (int)a.idx[rq.idx_off + (size_t)unit * rq.keep + k * R + r] : -1;
+    }
+    const int p0 = pre[k], p1 = pre[k + 1];
+    const int dpage = a.new_bt[rq.bt_off + k * R / PAGE];  // an item's targets share a page
+    const bool same_page = ob[k * R / PAGE] == dpage;
+    it.dst = ((lbase + dpage) * a.Hkv + h) * (size_t)(PAGE * RB) + (size_t)(k * R % PAGE) * RB;
+    it.wrow = a.weights + (((size_t)layer * a.M + rq.slot) * a.Hkv + h) * a.cap;
+    it.flags = a.flags + rq.item0 + (size_t)unit * rq.items;
+    // the kept rows in the target slots have ranks p0 .. p1 - 1: two items at most, none above k
+    it.wait0 = p1 > p0 && p0 / R < k ? p0 / R : -1;
+    it.wait1 = p1 > p0 && (p1 - 1) / R != p0 / R && (p1 - 1) / R < k ? (p1 - 1) / R : -1;
+    const int mine = lane == 0 ? it.wait0 : lane == 1 ? it.wait1 : -1;
+    it.clear = __all_sync(0xffffffffu, mine < 0 || (a.wait_limit > 0 && ld_acquire(it.flags + max(mine, 0)) != 0u));
+    it.stay = 0u;
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+      if (it.src[o] < 0 || (same_page && it.src[o] == k * R + lane + 32 * o)) it.stay |= 1u << o;
+      it.off[o] = -1;
+      it.wv[o] = 0.f;
+      if (it.src[o] >= 0) {
+        it.off[o] = (long long)(((lbase + ob[it.src[o] / PAGE]) * a.Hkv + h) * (size_t)(PAGE * RB) +
+                                (size_t)(it.src[o] % PAGE) * RB);
+        it.wv[o] = it.wrow[it.src[o]];
       }
     }
-    if (wmove) {
-      wrow[k * R + tid] = wv;
-      ++moved;
+    it.any = __any_sync(0xffffffffu, it.stay != (1u << OWN) - 1u);
+    return it;
+  };
+  Item it = look_up(take());
+  while (it.id < a.items && !fail) {
+    // ---- read: consecutive lanes copy consecutive pieces of a row ----
+    if (it.any) {
+      if (stored && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the stage is free
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const int row = (32 * i + lane) / PIECES, q = (32 * i + lane) % PIECES;
+        const long long at = __shfl_sync(0xffffffffu, it.off[i / PIECES], row & 31);
+        if (at >= 0) {
+          const uint32_t d = st + (uint32_t)(row * RB + q * 16);
+          asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(d), "l"(kc + at + q * 16),
+                       "l"(once)
+                       : "memory");
+          asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(d + (uint32_t)(R * RB)),
+                       "l"(vc + at + q * 16), "l"(once)
+                       : "memory");
+        }
+      }
     }
-    __syncthreads();  // s_src and s_item are rewritten
+    // the next item's ticket, slots and pages come with the rows.  The items
+    // before it are read all the same: this warp reads its own before it waits.
+    const Item next = look_up(take());
+    if (it.any) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the rows are stored from there by a bulk copy
+    }
+    __threadfence();  // every lane's reads come before the flag
+    __syncwarp();
+    if (lane == 0) st_relaxed(it.flags + it.k, 1u);  // a release, with the fence
+    if (it.any) {
+      // ---- the rows that live in the target slots have been read ----
+      if (!it.clear) {
+        const int mine = lane == 0 ? it.wait0 : lane == 1 ? it.wait1 : -1;
+        if (mine >= 0) {
+          const long long t0 = clock64();
+          bool ok = false;
+          while (!ok) {
+            if (clock64() - t0 >= a.wait_limit) break;
+            ok = ld_acquire(it.flags + mine) != 0u;
+          }
+          fail = !ok;
+        }
+        fail = __any_sync(0xffffffffu, fail);
+        if (fail) break;
+      }
+      // ---- write: the targets are consecutive ----
+      if (lane == 0) {
+        const uint32_t bytes = (uint32_t)(it.rows * RB);
+        asm volatile("fence.proxy.async;" ::: "memory");  // after what the flags told
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(kc + it.dst), "r"(st), "r"(bytes)
+                     : "memory");
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(vc + it.dst),
+                     "r"(st + (uint32_t)(R * RB)), "r"(bytes)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+      stored = true;
+#pragma unroll
+      for (int o = 0; o < OWN; ++o)
+        if (!((it.stay >> o) & 1u)) {
+          it.wrow[it.k * R + lane + 32 * o] = it.wv[o];
+          ++moved;
+        }
+    }
+    it = next;
   }
-  if (tid == 0 && s_fail) atomicOr(a.err, ERR_TIMEOUT);
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  if (fail && lane == 0) atomicOr(a.err, ERR_TIMEOUT);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) moved += __shfl_xor_sync(0xffffffffu, moved, o);
-  if ((tid & 31) == 0 && moved) atomicAdd(a.moved, (unsigned long long)moved);
+  if (lane == 0 && moved) atomicAdd(a.moved, (unsigned long long)moved);
 }
 
 template <int RB>
 cudaError_t launch_rb(const EvictArgs& a, cudaStream_t s) {
-  int per_sm = 0;
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_evict_move<RB>, MNT, 0);
+  constexpr int smem = MWARPS * STAGE;
+  const cudaError_t e = cudaFuncSetAttribute(k_evict_move<RB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t grid = a.items < (int64_t)per_sm * a.sms ? a.items : (int64_t)per_sm * a.sms;
-  k_evict_move<RB><<<dim3((unsigned)grid), MNT, 0, s>>>(a);
+  const int64_t grid = a.items < (int64_t)a.sms ? a.items : (int64_t)a.sms;
+  k_evict_move<RB><<<dim3((unsigned)grid), 32 * MWARPS, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -279,7 +389,14 @@ cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t s) {
   if (a.n == 0) return cudaSuccess;
   const int64_t grid = (int64_t)a.n * a.L * a.Hkv;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  k_evict_select<<<dim3((unsigned)grid), SNT, 0, s>>>(a);
+  const size_t smem = sizeof(unsigned) * (size_t)a.longest;
+  if (smem > 200 * 1024) {  // over 51 200 slots
+    k_evict_select<false><<<dim3((unsigned)grid), SNT, 0, s>>>(a);
+  } else {
+    const cudaError_t e = cudaFuncSetAttribute(k_evict_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    k_evict_select<true><<<dim3((unsigned)grid), SNT, smem, s>>>(a);
+  }
   return cudaGetLastError();
 }
 

@@ -495,6 +495,7 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
   const int row_bytes = g.head_dim * elt_bytes(g.kv_dtype), R = evict_rows(row_bytes);
   std::vector<uint8_t> bound(g.max_slots, 0);
   size_t cow = 0;
+  int longest = 0;
   int64_t mask_words = 0, idx_count = 0, items = 0, pre_count = 0;
   std::vector<EvictReq> er(n);
   for (int r = 0; r < n; ++r) {
@@ -523,6 +524,7 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
     idx_count += (int64_t)units * keep;
     items += (int64_t)units * e.items;
     pre_count += (int64_t)units * (e.items + 1);
+    longest = std::max(longest, T);
     for (int j = 0; j < reqs[r].num_pages; ++j) cow += c->refcnt[reqs[r].block_table[j]] > 1;
   }
   if ((st = ready_call(c)) != GP_OK) return st;
@@ -584,6 +586,7 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
   a.flags = reinterpret_cast<unsigned*>(scr + at_flags);
   a.ticket = reinterpret_cast<unsigned long long*>(scr + at_ticket);
   a.items = items;
+  a.longest = longest;
   a.sms = c->sms;
   a.moved = c->moved_dev;
   a.err = c->err_dev;

@@ -96,13 +96,14 @@ struct EvictArgs {
   unsigned* flags;            // [items of all units], 1: the item's rows are read
   unsigned long long* ticket; // next item
   int64_t items;              // of all requests
+  int longest;                // most tokens of a request that evicts
   int sms;
   unsigned long long* moved;
   int* err;
   long long wait_limit;
 };
-// Rows of a move item: K rows of 16 KB.
-__host__ __device__ constexpr int evict_rows(int row_bytes) { return 16384 / row_bytes; }
+// Rows of a move item: K rows of 8 KB.
+__host__ __device__ constexpr int evict_rows(int row_bytes) { return 8192 / row_bytes; }
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t s);
 cudaError_t launch_evict_move(const EvictArgs& a, cudaStream_t s);
 
