@@ -47,6 +47,9 @@ struct CompressRec {
   bool spec = false;      // masks in the speculative buffer (at mask_off), else in `masks`
   int32_t num_pages = 0;
   int64_t mask_off = 0;
+  // gp_evict_weighted: lists of kept slots instead of masks, at mask_off
+  bool evict = false;
+  int32_t tokens = 0, kept = 0, pitch = 0;  // kept 0: all of the tokens
 };
 
 // A call's descriptors on their way to the device: pinned memory, its device

@@ -1027,6 +1027,22 @@ gp_status gp_debug_keep_mask(gp_ctx* c, int32_t req_idx, uint32_t* out) {
     return fail(c, GP_ERR_INVALID, "no compress result %d", req_idx);
   const CompressRec& rec = c->last_compress[req_idx];
   const size_t count = (size_t)units_of(c) * (rec.num_pages * kPage / 32);
+  if (rec.evict) {  // kept slots: made into masks here
+    std::vector<uint16_t> kept((size_t)units_of(c) * rec.pitch);
+    if (rec.kept) {
+      GP_CUDA(c, cudaMemcpyAsync(kept.data(), static_cast<const uint16_t*>(c->evict.p) + rec.mask_off,
+                                 sizeof(uint16_t) * kept.size(), cudaMemcpyDeviceToHost, c->stream));
+      if ((st = check_kernel_errors(c)) != GP_OK) return st;
+    }
+    std::fill(out, out + count, 0u);
+    const size_t words = rec.num_pages * kPage / 32;
+    for (int u = 0; u < units_of(c); ++u)
+      for (int i = 0; i < (rec.kept ? rec.kept : rec.tokens); ++i) {
+        const int slot = rec.kept ? kept[(size_t)u * rec.pitch + i] : i;
+        out[u * words + slot / 32] |= 1u << (slot % 32);
+      }
+    return check_kernel_errors(c);
+  }
   const uint32_t* src = static_cast<const uint32_t*>(rec.spec ? c->spec_masks.p : c->masks.p);
   GP_CUDA(c, cudaMemcpyAsync(out, src + rec.mask_off, sizeof(uint32_t) * count, cudaMemcpyDeviceToHost, c->stream));
   return check_kernel_errors(c);

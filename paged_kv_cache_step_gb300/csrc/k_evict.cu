@@ -5,9 +5,10 @@
 //
 // Two kernels:
 //   select  one CTA a unit: radix select (11 + 11 + 10 bits of an
-//           order-preserving key) of the threshold, then one ordered pass that
-//           writes the keep mask, the kept slot of every rank, and how many
-//           slots are kept below the first slot of every move item.
+//           order-preserving key, fewer when a bin is kept whole) of the
+//           threshold, then one ordered pass that writes the kept slot of every
+//           rank, and how many slots are kept below the first slot of every
+//           move item.
 //   move    in place, many warps a unit.  An item is evict_rows consecutive
 //           ranks -- target slots [kR, (k+1)R), consecutive rows of one page --
 //           so its rows are always all wanted, and its K and V pass through
@@ -53,18 +54,14 @@ __global__ void __launch_bounds__(SNT) k_evict_select(const __grid_constant__ Ev
   __shared__ unsigned hist[BINS];
   __shared__ unsigned wsum[SWARP], weq[SWARP];
   __shared__ unsigned s_bin, s_above;
+  __shared__ bool s_whole;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int units = a.L * a.Hkv;
   const int r = blockIdx.x / units, unit = blockIdx.x % units;
   const EvictReq rq = a.reqs[r];
   if (blockIdx.x == 0 && tid == 0) *a.ticket = 0ull;
-  uint32_t* mask = a.masks + rq.mask_off + (size_t)unit * rq.words;
+  if (rq.items == 0) return;  // nothing to evict
   const int nw = (rq.T + 31) / 32;
-  for (int w = nw + tid; w < rq.words; w += SNT) mask[w] = 0u;
-  if (rq.items == 0) {  // nothing to evict
-    for (int w = tid; w < nw; w += SNT) mask[w] = rq.T - 32 * w >= 32 ? 0xffffffffu : (1u << (rq.T - 32 * w)) - 1u;
-    return;
-  }
   const float* w0 = a.weights + (((size_t)(unit / a.Hkv) * a.M + rq.slot) * a.Hkv + unit % a.Hkv) * a.cap;
   const int ncand = rq.T - rq.recent;
   const unsigned need = (unsigned)(rq.keep - rq.recent);  // 0 <= need < ncand
@@ -103,10 +100,13 @@ __global__ void __launch_bounds__(SNT) k_evict_select(const __grid_constant__ Ev
   if (need == 0) __syncthreads();  // the keys are staged (the passes below begin with a barrier)
 
   // ---- the need-th largest key: prefix, and how many keys lie above it ----
+  // `whole`: the keys of the prefix's last bin are just as many as still wanted,
+  // so all of them are kept and the digits left need not be known
   unsigned prefix = 0u, mask_bits = 0u, above = 0u;
+  bool whole = false;
   if (need > 0) {
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
+    for (int pass = 0; pass < 3 && !whole; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const unsigned digit = pass == 2 ? 1023u : 2047u;
       for (int b = tid; b < BINS; b += SNT) hist[b] = 0u;
@@ -134,68 +134,113 @@ __global__ void __launch_bounds__(SNT) k_evict_select(const __grid_constant__ Ev
       for (int w = 0; w < warp; ++w) cum += wsum[w];
       const unsigned want = need - above;
       if (cum < want && want <= cum + own) {  // one thread: the bins' counts sum to at least `want`
-        int bin = BINS - 1 - PER_BIN * tid;
+        bool found = false;
 #pragma unroll
-        for (int j = 0; j < PER_BIN - 1; ++j)
-          if (bin == BINS - 1 - PER_BIN * tid - j && cum + c[j] < want) {
-            cum += c[j];
-            --bin;
+        for (int j = 0; j < PER_BIN; ++j) {
+          if (!found && want <= cum + c[j]) {
+            found = true;
+            s_bin = (unsigned)(BINS - 1 - PER_BIN * tid - j);
+            s_above = cum;
+            s_whole = want == cum + c[j];
           }
-        s_bin = (unsigned)bin;
-        s_above = cum;
+          cum += c[j];
+        }
       }
       __syncthreads();
       prefix |= s_bin << shift;
       mask_bits |= digit << shift;
       above += s_above;
+      whole = s_whole;
     }
   }
-  const unsigned thr = prefix, take_eq = need - above;  // of the keys equal to thr, the first take_eq
+  const unsigned thr = prefix, take_eq = whole ? 0u : need - above;  // of the keys equal to thr, the first take_eq
 
   // ---- the ordered pass ------------------------------------------------------
-  auto sure_of = [&](int s, unsigned k) { return (s >= ncand && s < rq.T) || (s < ncand && need > 0 && k > thr); };
-  auto tie_of = [&](int s, unsigned k) { return s < ncand && need > 0 && k == thr; };
-  unsigned cnt = 0u, eqs = 0u;  // kept whatever the ties, and ties
+  // lane j holds the bits of the warp's words j, j + 32, ...: the slots kept
+  // whatever the ties, and the ties
+  constexpr int BLOCKS = 65536 / 32 / SWARP / 32;  // of 32 words a warp, at most
+  unsigned sure[BLOCKS], tie[BLOCKS];
+#pragma unroll
+  for (int b = 0; b < BLOCKS; ++b) sure[b] = tie[b] = 0u;
   each_word([&](int w, unsigned k) {
-    cnt += __popc(__ballot_sync(0xffffffffu, sure_of(32 * w + lane, k)));
-    eqs += __popc(__ballot_sync(0xffffffffu, tie_of(32 * w + lane, k)));
+    const int s = 32 * w + lane, j = w - wa;
+    const bool cand = s < ncand && need > 0;
+    const unsigned bs = __ballot_sync(0xffffffffu, cand ? (whole ? k >= thr : k > thr) : s >= ncand && s < rq.T);
+    const unsigned bt = __ballot_sync(0xffffffffu, cand && !whole && k == thr);
+#pragma unroll
+    for (int b = 0; b < BLOCKS; ++b)
+      if (j == 32 * b + lane) {
+        sure[b] = bs;
+        tie[b] = bt;
+      }
   });
-  __syncthreads();  // wsum is read above
+  unsigned cnt = 0u, eqs = 0u;
+#pragma unroll
+  for (int b = 0; b < BLOCKS; ++b) {
+    cnt += __popc(sure[b]);
+    eqs += __popc(tie[b]);
+  }
+  cnt = __reduce_add_sync(0xffffffffu, cnt);
+  eqs = __reduce_add_sync(0xffffffffu, eqs);
+  __syncthreads();  // wsum has been read above
   if (lane == 0) {
     wsum[warp] = cnt;
     weq[warp] = eqs;
   }
   __syncthreads();
-  unsigned sure_before = 0u, eq_before = 0u;
+  unsigned before = 0u, eq_before = 0u;  // kept slots and ties before this warp's words
   for (int w = 0; w < warp; ++w) {
-    sure_before += wsum[w];
+    before += wsum[w];
     eq_before += weq[w];
   }
-  const int R = evict_rows(a.row_bytes);
-  uint16_t* idx = a.idx + rq.idx_off + (size_t)unit * rq.keep;
+  before += min(eq_before, take_eq);
+  const int rlog = 31 - __clz(evict_rows(a.row_bytes));  // rows of an item, a power of two
+  uint16_t* idx = a.idx + rq.idx_off + (size_t)unit * rq.idx_pitch;
   int32_t* pre = a.pre + rq.pre_off + (size_t)unit * (rq.items + 1);
-  each_word([&](int w, unsigned k) {
-    const int s = 32 * w + lane;
-    const bool sure = sure_of(s, k), tie = tie_of(s, k);
-    const unsigned below = (1u << lane) - 1u;
-    const unsigned bt = __ballot_sync(0xffffffffu, tie);
-    const bool kept = sure || (tie && eq_before + __popc(bt & below) < take_eq);
-    const unsigned bk = __ballot_sync(0xffffffffu, kept);
-    const unsigned rank = sure_before + min(eq_before, take_eq);  // kept slots before this word
-    if (kept) idx[rank + __popc(bk & below)] = (uint16_t)s;
-    if (lane == 0) {
-      mask[w] = bk;
-      if (R < 32) {  // two items a word
+  // the kept slots go out through shared memory, in whole lines
+  uint16_t* list = STAGED ? reinterpret_cast<uint16_t*>(staged + (ncand + 3) / 4 * 4) : idx;
+#pragma unroll
+  for (int b = 0; b < BLOCKS; ++b) {
+    if (wa + 32 * b >= wb) break;
+    const int w = wa + 32 * b + lane;
+    // ties before this lane's word, then the ties of it that are kept: its first ones
+    unsigned eq = __popc(tie[b]), inc = eq;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const unsigned eq_mine = eq_before + inc - eq, room = take_eq > eq_mine ? take_eq - eq_mine : 0u;
+    unsigned t = tie[b];
+    for (; eq > room; --eq) t &= ~(0x80000000u >> __clz(t));
+    eq_before += __shfl_sync(0xffffffffu, inc, 31);
+    unsigned kept = sure[b] | t;
+    const unsigned n = __popc(kept);
+    inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    unsigned rank = before + inc - n;  // kept slots before this lane's word
+    before += __shfl_sync(0xffffffffu, inc, 31);
+    if (w < wb) {
+      if (rlog < 5) {  // 16 rows an item: two items a word
         if (2 * w <= rq.items) pre[2 * w] = (int32_t)rank;
-        if (2 * w + 1 <= rq.items) pre[2 * w + 1] = (int32_t)(rank + __popc(bk & 0xffffu));
-      } else if ((32 * w) % R == 0 && 32 * w / R <= rq.items) {
-        pre[32 * w / R] = (int32_t)rank;
+        if (2 * w + 1 <= rq.items) pre[2 * w + 1] = (int32_t)(rank + __popc(kept & 0xffffu));
+      } else if (((32 * w) & ((1 << rlog) - 1)) == 0 && (32 * w) >> rlog <= rq.items) {
+        pre[(32 * w) >> rlog] = (int32_t)rank;
       }
     }
-    sure_before += __popc(__ballot_sync(0xffffffffu, sure));
-    eq_before += __popc(bt);
-  });
-  if (tid == 0 && rq.items * R >= 32 * nw) pre[rq.items] = rq.keep;
+    for (; kept; kept &= kept - 1u) list[rank++] = (uint16_t)(32 * w + __ffs(kept) - 1);
+  }
+  if (tid == 0 && rq.items << rlog >= 32 * nw) pre[rq.items] = rq.keep;
+  if constexpr (STAGED) {
+    __syncthreads();
+    uint4* dst = reinterpret_cast<uint4*>(idx);  // every unit's list starts on 16 bytes
+    const uint4* src = reinterpret_cast<const uint4*>(list);
+    for (int i = tid; i < (rq.keep + 7) / 8; i += SNT) dst[i] = src[i];
+  }
 }
 
 __device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
@@ -270,7 +315,7 @@ __global__ void __launch_bounds__(32 * MWARPS, 1) k_evict_move(const __grid_cons
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
       const int r = lane + 32 * o;
-      it.src[o] = r < it.rows ? (int)a.idx[rq.idx_off + (size_t)unit * rq.keep + k * R + r] : -1;
+      it.src[o] = r < it.rows ? (int)a.idx[rq.idx_off + (size_t)unit * rq.idx_pitch + k * R + r] : -1;
     }
     const int p0 = pre[k], p1 = pre[k + 1];
     const int dpage = a.new_bt[rq.bt_off + k * R / PAGE];  // an item's targets share a page
@@ -389,8 +434,9 @@ cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t s) {
   if (a.n == 0) return cudaSuccess;
   const int64_t grid = (int64_t)a.n * a.L * a.Hkv;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  const size_t smem = sizeof(unsigned) * (size_t)a.longest;
-  if (smem > 200 * 1024) {  // over 51 200 slots
+  // a key and a place in the list of kept slots each, and the list's last piece
+  const size_t smem = (sizeof(unsigned) + sizeof(uint16_t)) * (size_t)a.longest + 64;
+  if (smem > 208 * 1024) {  // over 35 488 slots
     k_evict_select<false><<<dim3((unsigned)grid), SNT, 0, s>>>(a);
   } else {
     const cudaError_t e = cudaFuncSetAttribute(k_evict_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -496,7 +496,7 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
   std::vector<uint8_t> bound(g.max_slots, 0);
   size_t cow = 0;
   int longest = 0;
-  int64_t mask_words = 0, idx_count = 0, items = 0, pre_count = 0;
+  int64_t idx_count = 0, items = 0, pre_count = 0;
   std::vector<EvictReq> er(n);
   for (int r = 0; r < n; ++r) {
     if ((st = validate_request(c, reqs[r], r, true)) != GP_OK) return st;
@@ -513,15 +513,13 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
     e.keep = keep;
     e.recent = std::min(g.recent_window, keep);
     e.bt_off = r * maxp;
-    e.words = reqs[r].num_pages * (kPage / 32);
-    e.mask_off = mask_words;
-    mask_words += (int64_t)units * e.words;
+    e.idx_pitch = (keep + 7) / 8 * 8;
     e.idx_off = idx_count;
     e.item0 = items;
     e.pre_off = pre_count;
     if (T <= keep) continue;  // nothing to evict: its tables and rows stay as they are
     e.items = (keep + R - 1) / R;
-    idx_count += (int64_t)units * keep;
+    idx_count += (int64_t)units * e.idx_pitch;
     items += (int64_t)units * e.items;
     pre_count += (int64_t)units * (e.items + 1);
     longest = std::max(longest, T);
@@ -539,7 +537,6 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
   const size_t at_idx = scratch.take(sizeof(uint16_t) * (size_t)idx_count);
   const size_t at_pre = scratch.take(sizeof(int32_t) * (size_t)pre_count);
   const size_t at_flags = scratch.take(sizeof(unsigned) * (size_t)items), at_ticket = scratch.take(sizeof(unsigned long long));
-  if ((st = ensure(c, c->masks, sizeof(uint32_t) * (size_t)mask_words)) != GP_OK) return st;
   if ((st = ensure(c, c->evict, scratch.bytes)) != GP_OK) return st;
   StagingSlot* slot = nullptr;
   if ((st = staging_take(c, lay.bytes, &slot)) != GP_OK) return st;
@@ -580,7 +577,6 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
   a.old_bt = reinterpret_cast<const int32_t*>(dev + at_old);
   a.new_bt = reinterpret_cast<const int32_t*>(dev + at_new);
   a.weights = weights_dev;
-  a.masks = static_cast<uint32_t*>(c->masks.p);
   a.idx = reinterpret_cast<uint16_t*>(scr + at_idx);
   a.pre = reinterpret_cast<int32_t*>(scr + at_pre);
   a.flags = reinterpret_cast<unsigned*>(scr + at_flags);
@@ -625,8 +621,13 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
       ++c->stats.cow_pages;
     }
     if (er[r].items) ++c->slot_gen[reqs[r].slot];
-    c->last_compress[r].num_pages = reqs[r].num_pages;
-    c->last_compress[r].mask_off = er[r].mask_off;
+    CompressRec& rec = c->last_compress[r];
+    rec.num_pages = reqs[r].num_pages;
+    rec.evict = true;
+    rec.tokens = er[r].T;
+    rec.kept = er[r].items ? er[r].keep : 0;
+    rec.pitch = er[r].idx_pitch;
+    rec.mask_off = er[r].idx_off;  // c->evict starts with the kept slots
   }
   return GP_OK;
 }

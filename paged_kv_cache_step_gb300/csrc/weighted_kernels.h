@@ -70,11 +70,9 @@ struct EvictReq {
   int32_t slot;
   int32_t T, keep, recent;  // tokens, tokens kept, of them the most recent
   int32_t bt_off;
-  int32_t words;            // of the keep mask, num_pages * 8
   int32_t items;            // move items of a unit: ceil(keep / rows of an item), 0 when T <= keep
-  int32_t pad;
-  int64_t mask_off;         // word offset of the masks [units][words]
-  int64_t idx_off;          // offset of the kept slots [units][keep]
+  int32_t idx_pitch;        // keep, rounded up to 8
+  int64_t idx_off;          // offset of the kept slots [units][idx_pitch]
   int64_t item0;            // items of the requests before it (all units)
   int64_t pre_off;          // offset of the kept-slot counts [units][items + 1]
 };
@@ -90,7 +88,6 @@ struct EvictArgs {
   const int32_t* old_bt;
   const int32_t* new_bt;
   float* weights;
-  uint32_t* masks;
   uint16_t* idx;              // kept slot of each rank
   int32_t* pre;               // kept slots below every item's first slot
   unsigned* flags;            // [items of all units], 1: the item's rows are read
