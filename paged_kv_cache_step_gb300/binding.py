@@ -12,6 +12,7 @@ device memory and streams.
 
 from __future__ import annotations
 
+import array
 import ctypes as C
 import struct
 import os
@@ -190,16 +191,54 @@ def _ptr(t) -> int:
 # requests
 # ---------------------------------------------------------------------------
 
+# gp_request packed field by field: {int32 slot, int32 num_pages, pointer
+# block_table, int64 pos}, checked against the ctypes layout at import.
+_REQ_PACK = struct.Struct("=iiQq")
+assert (_REQ_PACK.size == C.sizeof(GpRequest) and GpRequest.slot.offset == 0 and GpRequest.num_pages.offset == 4
+        and GpRequest.block_table.offset == 8 and GpRequest.pos.offset == 16), "gp_request layout"
+
+
 class Request:
-    """A request as the scheduler holds it: slot, block table (host), position."""
+    """A request as the scheduler holds it: slot, block table (host), position.
+    Its gp_request record is packed when a field changes, not on every call."""
 
     def __init__(self, slot: int, pages, pos: int, capacity: int):
-        self.slot = int(slot)
-        self.table = np.zeros(capacity, dtype=np.int32)
+        self._slot, self._pos = int(slot), int(pos)
         pages = list(pages)
-        self.table[:len(pages)] = pages
-        self.num_pages = len(pages)
-        self.pos = int(pos)
+        self._num_pages = len(pages)
+        table = np.zeros(capacity, dtype=np.int32)
+        table[:len(pages)] = pages
+        self.table = table
+
+    def _pack(self):
+        self._raw = _REQ_PACK.pack(self._slot, self._num_pages, self._bt, self._pos)
+
+    @property
+    def slot(self):
+        return self._slot
+
+    @slot.setter
+    def slot(self, v):
+        self._slot = v
+        self._pack()
+
+    @property
+    def num_pages(self):
+        return self._num_pages
+
+    @num_pages.setter
+    def num_pages(self, v):
+        self._num_pages = v
+        self._pack()
+
+    @property
+    def pos(self):
+        return self._pos
+
+    @pos.setter
+    def pos(self, v):
+        self._pos = v
+        self._pack()
 
     @property
     def table(self):
@@ -209,6 +248,7 @@ class Request:
     def table(self, t):
         self._table = np.ascontiguousarray(t, dtype=np.int32)
         self._bt = self._table.ctypes.data  # the C side reads and extends it in place
+        self._pack()
 
     @property
     def pages(self):
@@ -223,31 +263,24 @@ _REQ_DTYPE = np.dtype({"names": ["slot", "num_pages", "block_table", "pos"],
                                    GpRequest.block_table.offset, GpRequest.pos.offset],
                        "itemsize": C.sizeof(GpRequest)})
 
-
-# gp_request packed field by field: {int32 slot, int32 num_pages, pointer
-# block_table, int64 pos}, checked against the ctypes layout at import.
-_REQ_PACK = struct.Struct("=iiQq")
-assert (_REQ_PACK.size == C.sizeof(GpRequest) and GpRequest.slot.offset == 0 and GpRequest.num_pages.offset == 4
-        and GpRequest.block_table.offset == 8 and GpRequest.pos.offset == 16), "gp_request layout"
 _NUM_PAGES = struct.Struct("=i")
 
 
 def _marshal(reqs):
     arr = (GpRequest * max(1, len(reqs)))()
-    pack, size = _REQ_PACK.pack_into, _REQ_PACK.size
-    for i, r in enumerate(reqs):
-        pack(arr, i * size, r.slot, r.num_pages, r._bt, r.pos)
+    if len(reqs):
+        C.memmove(arr, b"".join([r._raw for r in reqs]), len(reqs) * _REQ_PACK.size)
     return arr
 
 
 def _unmarshal(arr, reqs):
     if len(reqs) <= 8:
         get, size = _NUM_PAGES.unpack_from, _REQ_PACK.size
-        for i, r in enumerate(reqs):
-            r.num_pages = get(arr, i * size + 4)[0]
+        counts = [get(arr, i * size + 4)[0] for i in range(len(reqs))]
     else:
         counts = np.frombuffer(arr, dtype=_REQ_DTYPE, count=len(reqs))["num_pages"].tolist()
-        for r, p in zip(reqs, counts):
+    for r, p in zip(reqs, counts):
+        if p != r._num_pages:
             r.num_pages = p
 
 
@@ -414,11 +447,21 @@ def _counts(reqs, *lists):
     """Host int32 arrays of per-request counts, one entry a request."""
     out = []
     for x in lists:
-        a = np.ascontiguousarray(np.asarray(x, dtype=np.int32))
-        if a.shape != (len(reqs),):
-            raise GrowPageError(GP_ERR_INVALID, f"{len(reqs)} requests, counts of shape {a.shape}")
+        if type(x) is list or type(x) is tuple:
+            a = array.array("i", x)
+            n = len(a)
+        else:
+            a = np.ascontiguousarray(np.asarray(x, dtype=np.int32))
+            n = len(a) if a.ndim == 1 else -1
+        if n != len(reqs):
+            raise GrowPageError(GP_ERR_INVALID, f"{len(reqs)} requests, {n} counts")
         out.append(a)
     return out
+
+
+def _host(a) -> int:
+    """Host address of a counts array."""
+    return a.buffer_info()[0] if type(a) is array.array else a.ctypes.data
 
 
 def gp_append_tokens(ctx, layer: int, reqs, num_cached, num_new, q_dev, k_dev, v_dev, q_rot_dev, weights_dev=None):
@@ -427,7 +470,7 @@ def gp_append_tokens(ctx, layer: int, reqs, num_cached, num_new, q_dev, k_dev, v
     q_dev, q_rot_dev [rows][Hq][d] (both None: keys and values alone);
     k_dev, v_dev [rows][Hkv][d], rows packed request after request."""
     nc, nn = _counts(reqs, num_cached, num_new)
-    _check(ctx, load().gp_append_tokens(ctx, layer, len(reqs), _marshal(reqs), nc.ctypes.data, nn.ctypes.data,
+    _check(ctx, load().gp_append_tokens(ctx, layer, len(reqs), _marshal(reqs), _host(nc), _host(nn),
                                         _ptr(q_dev), _ptr(k_dev), _ptr(v_dev), _ptr(q_rot_dev), _ptr(weights_dev)))
 
 
@@ -435,7 +478,7 @@ def gp_decode_attention_weighted(ctx, layer: int, reqs, num_tokens, q_dev, first
     """gp_decode_attention that adds its softmax weights to weights_dev
     (fp32 [L][max_slots][Hkv][max_pages_per_req * 256]); first_dev may be None."""
     nt, = _counts(reqs, num_tokens)
-    _check(ctx, load().gp_decode_attention_weighted(ctx, layer, len(reqs), _marshal(reqs), nt.ctypes.data,
+    _check(ctx, load().gp_decode_attention_weighted(ctx, layer, len(reqs), _marshal(reqs), _host(nt),
                                                     _ptr(q_dev), _ptr(first_dev), _ptr(out_dev), _ptr(weights_dev)))
 
 
@@ -443,7 +486,7 @@ def gp_chunk_attention(ctx, layer: int, reqs, num_cached, num_new, q_dev, out_de
     """Causal attention of each request's num_new last tokens over its cache;
     q_dev (rotated) and out_dev [rows][Hq][d] of q_dtype, packed."""
     nc, nn = _counts(reqs, num_cached, num_new)
-    _check(ctx, load().gp_chunk_attention(ctx, layer, len(reqs), _marshal(reqs), nc.ctypes.data, nn.ctypes.data,
+    _check(ctx, load().gp_chunk_attention(ctx, layer, len(reqs), _marshal(reqs), _host(nc), _host(nn),
                                           _ptr(q_dev), _ptr(out_dev), _ptr(weights_dev)))
 
 
@@ -453,7 +496,7 @@ def gp_evict_weighted(ctx, reqs, num_tokens, keep_tokens, weights_dev):
     compacted in order.  Rewrites the requests' tables (copy-on-write)."""
     nt, nk = _counts(reqs, num_tokens, keep_tokens)
     arr = _marshal(reqs)
-    st = load().gp_evict_weighted(ctx, len(reqs), arr, nt.ctypes.data, nk.ctypes.data, _ptr(weights_dev))
+    st = load().gp_evict_weighted(ctx, len(reqs), arr, _host(nt), _host(nk), _ptr(weights_dev))
     _unmarshal(arr, reqs)
     _check(ctx, st)
 

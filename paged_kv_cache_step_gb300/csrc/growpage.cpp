@@ -1293,14 +1293,16 @@ gp_status decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_request
   }
   if (tc) n_ctas = (long long)items.size();
   const size_t part_floats = (size_t)n_ctas * G * (g.head_dim + 2);
-  const size_t tick_off = (part_floats * sizeof(float) + 255) & ~size_t(255);
-  if ((st = ensure(c, c->attn, tick_off + sizeof(unsigned) * (size_t)n * Hkv)) != GP_OK) return st;
+  if ((st = ensure(c, c->attn, part_floats * sizeof(float))) != GP_OK) return st;
   const size_t items_bytes = sizeof(gp::AttnItem) * items.size();
   const size_t weights_at = (items_bytes + sizeof(int32_t) * cta_begin.size() + 15) & ~size_t(15);
   const size_t wreq_bytes = sizeof(gp::WeightReq) * wreqs.size();
+  // the pairs' tickets, zero, travel with the descriptors
+  const size_t tick_at = (weights_at + wreq_bytes + sizeof(int64_t) * wreqs.size() + 15) & ~size_t(15);
+  const size_t tick_bytes = sizeof(unsigned) * (size_t)n * Hkv;
   Staged s{};
-  if ((st = stage(c, n, false, &s, &c->upload_attn, weights_at + wreq_bytes + sizeof(int64_t) * wreqs.size())) != GP_OK)
-    return st;
+  if ((st = stage(c, n, false, &s, &c->upload_attn, tick_at + tick_bytes)) != GP_OK) return st;
+  std::memset(static_cast<char*>(s.extra) + tick_at, 0, tick_bytes);
   if (weights) {
     std::memcpy(static_cast<char*>(s.extra) + weights_at, wreqs.data(), wreq_bytes);
     std::memcpy(static_cast<char*>(s.extra) + weights_at + wreq_bytes, logit_off.data(), sizeof(int64_t) * n);
@@ -1329,7 +1331,6 @@ gp_status decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_request
   }
   if ((st = upload(c, s)) != GP_OK) return st;
   char* base = static_cast<char*>(c->attn.p);
-  GP_CUDA(c, cudaMemsetAsync(base + tick_off, 0, sizeof(unsigned) * (size_t)n * g.num_kv_heads, c->stream));
   gp::AttnArgs a{};
   a.tc = tc ? 1 : 0;
   if (tc) {
@@ -1358,7 +1359,7 @@ gp_status decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_request
   a.inv_freq = c->inv_freq;
   a.out = out_dev;
   a.part = reinterpret_cast<float*>(base);
-  a.tickets = reinterpret_cast<unsigned*>(base + tick_off);
+  a.tickets = dev_at<unsigned>(s, s.off_extra + tick_at);
   a.split_base = dev_at<int32_t>(s, s.off_pb);
   a.order = dev_at<int32_t>(s, s.off_sel);
   a.n = n;

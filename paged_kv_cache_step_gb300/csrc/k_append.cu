@@ -88,16 +88,21 @@ __global__ void __launch_bounds__(NT) k_append(const __grid_constant__ AppendArg
   __shared__ __align__(16) float sn[D / 2];
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
-  int lo = 0, hi = a.n;  // reqs[lo].row0 <= row < reqs[hi].row0
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.reqs[mid].row0 <= row) lo = mid;
-    else hi = mid;
+  int lo = 0, hi = a.n;  // request lo: its row0 <= row < request hi's row0
+  if (a.n == a.rows) {   // one token each
+    lo = (int)row;
+  } else {
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((a.reqs ? a.reqs[mid].row0 : a.few[mid].row0) <= row) lo = mid;
+      else hi = mid;
+    }
   }
-  const AppendReq rq = a.reqs[lo];
+  const AppendReq rq = a.reqs ? a.reqs[lo] : a.few[lo];
   const int t = (int)(row - rq.row0);
   const int tok = rq.cached + t;
-  const int page = a.bt[rq.bt_off + (tok / PAGE - rq.cached / PAGE)];
+  const int at = rq.bt_off + (tok / PAGE - rq.cached / PAGE);
+  const int page = a.reqs ? a.bt[at] : a.few_bt[at];
   if (page < 0 || page >= a.num_pages_total || rq.slot < 0 || rq.slot >= a.M) {  // the host checked both
     if (tid == 0) atomicOr(a.err, ERR_BAD_PAGE);
     return;

@@ -30,6 +30,7 @@
 #include <cstdint>
 
 #include "attn_kernels.h"
+#include "chained.cuh"
 #include "gp_kernels.h"
 
 namespace gp {
@@ -110,6 +111,7 @@ __global__ void __launch_bounds__(NT, 2) k_decode_attn(AttnArgs a) {
   extern __shared__ __align__(128) unsigned char ring[];  // NSTAGE x (K rows, V rows)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if constexpr (W) let_next_in();
   // ---- this CTA's (request, KV head, split); requests in the host's order ----
   int lo = 0, hi = a.n;  // split_base[lo] <= blockIdx.x < split_base[hi]
   while (hi - lo > 1) {

@@ -48,6 +48,7 @@
 #include <cstdint>
 
 #include "attn_kernels.h"
+#include "chained.cuh"
 #include "gp_kernels.h"
 #include "tc_ptx.cuh"
 
@@ -298,6 +299,7 @@ __global__ void __launch_bounds__(NT, 1) k_decode_attn_tc(const __grid_constant_
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = (int)blockIdx.x;
+  if constexpr (W) let_next_in();
   // Every role walks the same items, this CTA's list from the host; the
   // next item's record is loaded while f runs on this one.  Items whose slot
   // is out of range are skipped (the first query thread records the error).

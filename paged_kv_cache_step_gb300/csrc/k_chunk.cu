@@ -22,6 +22,7 @@
 
 #include <cstdint>
 
+#include "chained.cuh"
 #include "weighted_kernels.h"
 
 namespace gp {
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(NT) k_chunk(const __grid_constant__ ChunkArgs 
   constexpr int DC = D / 64;  // float4 columns of the output a thread owns
   const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
   const ChunkTile tile = a.tiles[blockIdx.x];
+  let_next_in();
   const ChunkReq rq = a.reqs[tile.r];
   const int total = rq.cached + rq.nnew;
   const int tokens = BR / a.G;
@@ -247,6 +249,7 @@ __global__ void __launch_bounds__(NT) k_chunk_weights(const __grid_constant__ Ch
   const int total = rq.cached + rq.nnew;
   const int tokens = BR / a.G, s0 = tile.first;
   if (rq.slot < 0 || rq.slot >= a.M) return;
+  wait_for_previous();
   load_keys<D>(a, rq, a.k_cache, tile.h, s0, total, sm);
   float w[4] = {0.f, 0.f, 0.f, 0.f};
   // the first token that sees slot s0, rounded down to a tile
@@ -284,10 +287,10 @@ __global__ void __launch_bounds__(NT) k_chunk_weights(const __grid_constant__ Ch
   }
 }
 
-template <typename K>
-cudaError_t launch_k(K kernel, size_t smem, int grid, const ChunkArgs& a, cudaStream_t s) {
+cudaError_t launch_k(void (*kernel)(ChunkArgs), size_t smem, int grid, bool chained, const ChunkArgs& a, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
+  if (chained) return launch_chained(kernel, dim3((unsigned)grid), NT, smem, s, a);
   kernel<<<dim3((unsigned)grid), NT, smem, s>>>(a);
   return cudaGetLastError();
 }
@@ -297,16 +300,16 @@ cudaError_t launch_k(K kernel, size_t smem, int grid, const ChunkArgs& a, cudaSt
 cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t s) {
   if (a.n_tiles == 0) return cudaSuccess;
   if (a.G < 1 || BR % a.G) return cudaErrorInvalidValue;
-  if (a.D == 128) return launch_k(k_chunk<128>, sizeof(Smem<128>), a.n_tiles, a, s);
-  if (a.D == 64) return launch_k(k_chunk<64>, sizeof(Smem<64>), a.n_tiles, a, s);
+  if (a.D == 128) return launch_k(k_chunk<128>, sizeof(Smem<128>), a.n_tiles, false, a, s);
+  if (a.D == 64) return launch_k(k_chunk<64>, sizeof(Smem<64>), a.n_tiles, false, a, s);
   return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_chunk_weights(const ChunkArgs& a, cudaStream_t s) {
   if (a.n_wtiles == 0) return cudaSuccess;
   if (a.G < 1 || BR % a.G) return cudaErrorInvalidValue;
-  if (a.D == 128) return launch_k(k_chunk_weights<128>, sizeof(Smem<128>), a.n_wtiles, a, s);
-  if (a.D == 64) return launch_k(k_chunk_weights<64>, sizeof(Smem<64>), a.n_wtiles, a, s);
+  if (a.D == 128) return launch_k(k_chunk_weights<128>, sizeof(Smem<128>), a.n_wtiles, true, a, s);
+  if (a.D == 64) return launch_k(k_chunk_weights<64>, sizeof(Smem<64>), a.n_wtiles, true, a, s);
   return cudaErrorInvalidValue;
 }
 

@@ -43,6 +43,7 @@
 
 #include <cstdint>
 
+#include "chained.cuh"
 #include "tc_ptx.cuh"
 #include "weighted_kernels.h"
 
@@ -298,6 +299,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
   const ChunkItem* items = KEYS ? a.kitems : a.items;
   const int32_t* begin = KEYS ? a.kbegin : a.begin;
   const int i0 = uniform(begin[blockIdx.x]), i1 = uniform(begin[blockIdx.x + 1]);
+  let_next_in();
   if (tid == 0) {
     for (int i = 0; i < L::NBARS; ++i) {
       const int b = i - 2 * NST;  // p_ready, o_free, p_half: the group's four warps; else one arrival
@@ -318,6 +320,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_holder);
+  wait_for_previous();  // (of two attention launches the second is chained)
   auto timed_out = [&] {
     atomicOr(a.err, ERR_TIMEOUT);
     *abort = 1;
@@ -690,6 +693,8 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
 template <int D, int G>
 __global__ void __launch_bounds__(256) k_chunk_join(const __grid_constant__ ChunkTcArgs a) {
   const ChunkJoin jn = load_item(a.joins + blockIdx.x);
+  let_next_in();
+  wait_for_previous();
   const ChunkReq rq = load_req(a.reqs + jn.r);
   const int row = threadIdx.x & 127, half = threadIdx.x >> 7;
   const int t = jn.t0 + row / G;
@@ -774,6 +779,7 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
 
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const int i0 = uniform(a.wbegin[blockIdx.x]), i1 = uniform(a.wbegin[blockIdx.x + 1]);
+  let_next_in();
   if (tid == 0) {
     for (int i = 0; i < L::NBARS; ++i) {
       int n = i == 2 || i == 3 || (i >= 4 + NQ && i < 4 + 2 * NQ) ? 2 : 1;  // k_empty, q_empty: both issuers
@@ -797,6 +803,7 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_holder);
+  wait_for_previous();  // the statistics are the attention's; the weights may be an earlier call's
   auto timed_out = [&] {
     atomicOr(a.err, ERR_TIMEOUT);
     *abort = 1;
@@ -994,6 +1001,7 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
 // Adds the partial sums of a page, in the order of its parts.
 __global__ void __launch_bounds__(PAGE) k_chunk_weights_join(const __grid_constant__ ChunkTcArgs a) {
   const WeightJoin jn = load_item(a.wjoins + blockIdx.x);
+  wait_for_previous();
   const ChunkReq rq = load_req(a.reqs + jn.r);
   const int i = jn.page * PAGE + (int)threadIdx.x;
   if (i >= rq.cached + rq.nnew || rq.slot < 0 || rq.slot >= a.M) return;
@@ -1003,31 +1011,30 @@ __global__ void __launch_bounds__(PAGE) k_chunk_weights_join(const __grid_consta
 }
 
 template <int D, int G, bool KEYS>
-cudaError_t attention_launch(const ChunkTcArgs& a, int grid, cudaStream_t s) {
+cudaError_t attention_launch(const ChunkTcArgs& a, int grid, bool chained, cudaStream_t s) {
   if (grid == 0) return cudaSuccess;
   constexpr int smem = (int)Sm<D, KEYS>::BYTES;
   const cudaError_t e = cudaFuncSetAttribute(k_chunk_tc<D, G, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  if (chained) return launch_chained(k_chunk_tc<D, G, KEYS>, dim3((unsigned)grid), NT, smem, s, a);
   k_chunk_tc<D, G, KEYS><<<dim3((unsigned)grid), NT, smem, s>>>(a);
   return cudaGetLastError();
 }
 template <int D, int G>
 cudaError_t attention(const ChunkTcArgs& a, cudaStream_t s) {
-  cudaError_t e = attention_launch<D, G, false>(a, a.grid, s);
-  if (e == cudaSuccess) e = attention_launch<D, G, true>(a, a.kgrid, s);
+  cudaError_t e = attention_launch<D, G, false>(a, a.grid, false, s);
+  if (e == cudaSuccess) e = attention_launch<D, G, true>(a, a.kgrid, a.grid > 0, s);
   if (e != cudaSuccess || a.n_joins == 0) return e;
-  k_chunk_join<D, G><<<dim3((unsigned)a.n_joins, D / 16), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_chained(k_chunk_join<D, G>, dim3((unsigned)a.n_joins, D / 16), 256, 0, s, a);
 }
 template <int D, int G>
 cudaError_t weights(const ChunkTcArgs& a, cudaStream_t s) {
   cudaError_t e =
       cudaFuncSetAttribute(k_chunk_weights_tc<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SmW<D>::BYTES);
   if (e != cudaSuccess) return e;
-  k_chunk_weights_tc<D, G><<<dim3((unsigned)a.wgrid), WNT, SmW<D>::BYTES, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess || a.n_wjoins == 0) return e;
-  k_chunk_weights_join<<<dim3((unsigned)a.n_wjoins), PAGE, 0, s>>>(a);
-  return cudaGetLastError();
+  e = launch_chained(k_chunk_weights_tc<D, G>, dim3((unsigned)a.wgrid), WNT, SmW<D>::BYTES, s, a);
+  if (e != cudaSuccess || a.n_wjoins == 0) return e;
+  return launch_chained(k_chunk_weights_join, dim3((unsigned)a.n_wjoins), PAGE, 0, s, a);
 }
 
 }  // namespace

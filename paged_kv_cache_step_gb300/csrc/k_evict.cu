@@ -25,6 +25,7 @@
 // Bounded by HBM: kept rows are read and written once.
 #include <cstdint>
 
+#include "chained.cuh"
 #include "weighted_kernels.h"
 
 namespace gp {
@@ -59,6 +60,7 @@ __global__ void __launch_bounds__(SNT) k_evict_select(const __grid_constant__ Ev
   const int units = a.L * a.Hkv;
   const int r = blockIdx.x / units, unit = blockIdx.x % units;
   const EvictReq rq = a.reqs[r];
+  let_next_in();
   if (blockIdx.x == 0 && tid == 0) *a.ticket = 0ull;
   if (rq.items == 0) return;  // nothing to evict
   const int nw = (rq.T + 31) / 32;
@@ -343,6 +345,7 @@ __global__ void __launch_bounds__(32 * MWARPS, 1) k_evict_move(const __grid_cons
     it.any = __any_sync(0xffffffffu, it.stay != (1u << OWN) - 1u);
     return it;
   };
+  wait_for_previous();
   Item it = look_up(take());
   while (it.id < a.items && !fail) {
     // ---- read: consecutive lanes copy consecutive pieces of a row ----
@@ -424,8 +427,7 @@ cudaError_t launch_rb(const EvictArgs& a, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(k_evict_move<RB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t grid = a.items < (int64_t)a.sms ? a.items : (int64_t)a.sms;
-  k_evict_move<RB><<<dim3((unsigned)grid), 32 * MWARPS, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_chained(k_evict_move<RB>, dim3((unsigned)grid), 32 * MWARPS, smem, s, a);
 }
 
 }  // namespace

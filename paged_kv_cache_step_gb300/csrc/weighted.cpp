@@ -293,13 +293,21 @@ gp_status gp_append_tokens(gp_ctx* c, int32_t layer, int32_t n, const gp_request
   }
   if ((st = ready_call(c)) != GP_OK) return st;
   if ((st = wait_shared_pages(c, n, reqs)) != GP_OK) return st;
+  AppendArgs a{};
+  AppendReq* hr = a.few;
+  int32_t* hb = a.few_bt;
+  const bool few = live <= AppendArgs::FEW_REQS && pages <= AppendArgs::FEW_PAGES;
   Layout lay;
-  const size_t at_req = lay.take(sizeof(AppendReq) * (size_t)live), at_bt = lay.take(sizeof(int32_t) * (size_t)pages);
   StagingSlot* slot = nullptr;
-  if ((st = staging_take(c, lay.bytes, &slot)) != GP_OK) return st;
-  char* host = static_cast<char*>(slot->pinned);
-  AppendReq* hr = reinterpret_cast<AppendReq*>(host + at_req);
-  int32_t* hb = reinterpret_cast<int32_t*>(host + at_bt);
+  if (!few) {
+    const size_t at_req = lay.take(sizeof(AppendReq) * (size_t)live), at_bt = lay.take(sizeof(int32_t) * (size_t)pages);
+    if ((st = staging_take(c, lay.bytes, &slot)) != GP_OK) return st;
+    char *host = static_cast<char*>(slot->pinned), *dev = static_cast<char*>(slot->dev.p);
+    hr = reinterpret_cast<AppendReq*>(host + at_req);
+    hb = reinterpret_cast<int32_t*>(host + at_bt);
+    a.reqs = reinterpret_cast<const AppendReq*>(dev + at_req);
+    a.bt = reinterpret_cast<const int32_t*>(dev + at_bt);
+  }
   int64_t row = 0;
   int at = 0, k = 0;
   for (int r = 0; r < n; ++r) {
@@ -309,8 +317,7 @@ gp_status gp_append_tokens(gp_ctx* c, int32_t layer, int32_t n, const gp_request
     for (int j = num_cached[r] / kPage; j <= (num_cached[r] + num_new[r] - 1) / kPage; ++j)
       hb[at++] = reqs[r].block_table[j];
   }
-  if ((st = staging_upload(c, *slot, lay.bytes)) != GP_OK) return st;
-  AppendArgs a{};
+  if (!few && (st = staging_upload(c, *slot, lay.bytes)) != GP_OK) return st;
   a.k_cache = c->k_cache;
   a.v_cache = c->v_cache;
   a.kv_f32 = g.kv_dtype == GP_DTYPE_F32;
@@ -322,8 +329,6 @@ gp_status gp_append_tokens(gp_ctx* c, int32_t layer, int32_t n, const gp_request
   a.D = g.head_dim;
   a.M = g.max_slots;
   a.cap = (int64_t)g.max_pages_per_req * kPage;
-  a.reqs = reinterpret_cast<const AppendReq*>(static_cast<char*>(slot->dev.p) + at_req);
-  a.bt = reinterpret_cast<const int32_t*>(static_cast<char*>(slot->dev.p) + at_bt);
   a.n = live;
   a.rows = (int)rows;
   a.q = q_dev;

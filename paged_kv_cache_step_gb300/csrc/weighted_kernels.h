@@ -28,7 +28,7 @@ struct AppendArgs {
   int num_pages_total;
   int layer, Hq, Hkv, D, M;
   int64_t cap;               // tokens of a row of the weights
-  const AppendReq* reqs;     // [n], row0 ascending
+  const AppendReq* reqs;     // [n], row0 ascending; null: `few`
   const int32_t* bt;
   int n;
   int rows;                  // packed rows
@@ -39,6 +39,11 @@ struct AppendArgs {
   float* weights;            // or null
   const double* inv_freq;    // [D / 2]
   int* err;
+  // the descriptors of a small call travel with the launch: no copy before it,
+  // and constant-bank reads instead of dependent trips to L2
+  static constexpr int FEW_REQS = 64, FEW_PAGES = 128;
+  AppendReq few[FEW_REQS];
+  int32_t few_bt[FEW_PAGES];
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
 
