@@ -349,20 +349,25 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
           for (int x = 0; x < D; x += 64) tma_load_2d(dst + (uint32_t)(x / 64 * L::HALF), map, x, y, full(s));
           ++c;
         };
-        if (nq > 0 && !(ok = wait_bar(q_empty, (uint32_t)((nq - 1) & 1), abort))) break;
-        const int nqt = KEYS || it.alone ? 1 : 2;
-        mbar_expect_tx(q_full, (uint32_t)(nqt * L::TILE));
-        for (int x = 0; x < nqt; ++x)
+        // the query tiles' place is free only when the item before has formed its
+        // last S: the first key tiles are on their way before
+        auto queries = [&] {
+          if (!ok || (nq > 0 && !(ok = wait_bar(q_empty, (uint32_t)((nq - 1) & 1), abort)))) return;
+          const int nqt = KEYS || it.alone ? 1 : 2;
+          mbar_expect_tx(q_full, (uint32_t)(nqt * L::TILE));
+          for (int x = 0; x < nqt; ++x)
 #pragma unroll
-          for (int d = 0; d < D; d += 64)
-            tma_load_3d(sb + (uint32_t)(L::Q + (size_t)x * L::TILE + d / 64 * L::HALF), &a.qmap, d, it.h * G,
-                        (int)rq.row0 + it.t0 + x * TOK, q_full);
-        ++nq;
+            for (int d = 0; d < D; d += 64)
+              tma_load_3d(sb + (uint32_t)(L::Q + (size_t)x * L::TILE + d / 64 * L::HALF), &a.qmap, d, it.h * G,
+                          (int)rq.row0 + it.t0 + x * TOK, q_full);
+          ++nq;
+        };
         if (KEYS) {
           tile(&a.kmap, it.kb);
           if (w.cnt[1] > 0) tile(&a.kmap, it.kb + 1);
           for (int j = 0; j < w.cnt[0]; ++j) {
             tile(&a.vmap, it.kb + 2 * j);
+            if (j == 0) queries();
             if (j + 1 < w.cnt[0]) tile(&a.kmap, it.kb + 2 * j + 2);
             if (j < w.cnt[1]) tile(&a.vmap, it.kb + 2 * j + 1);
             if (j + 1 < w.cnt[1]) tile(&a.kmap, it.kb + 2 * j + 3);
@@ -371,6 +376,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
           for (int j = it.kb; j < it.ke; ++j) {
             tile(&a.kmap, j);
             tile(&a.vmap, j);
+            if (j == it.kb) queries();
           }
         }
       }
