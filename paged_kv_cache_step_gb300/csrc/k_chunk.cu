@@ -17,6 +17,8 @@
 //              so S is formed again, one CTA a tile of 64 keys, over the query
 //              tiles that see it: a weight has one writer, and the sum's order
 //              is fixed.
+// Few tiles are cut into several items each, over the keys (weights: over the
+// query tiles), for about four a SM; their partials are joined by a kernel more.
 // Bounded by the fp32 pipe: 2 d (2 + 1) flops a (row, key) pair.
 #include <cuda_bf16.h>
 
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(NT) k_chunk(const __grid_constant__ ChunkArgs 
   const int total = rq.cached + rq.nnew;
   const int tokens = BR / a.G;
   const int last = min(tile.first + tokens, rq.nnew) - 1;  // last token of the tile
-  const int end = rq.cached + last + 1;                    // slots it sees
+  const int end = min(rq.cached + last + 1, tile.to * BK);  // slots it sees, of this item
   load_rows<D>(a, rq, tile.h, tile.first, sm);
   if (tid < BR) {
     sm.m[tid] = NEG;
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(NT) k_chunk(const __grid_constant__ ChunkArgs 
     for (int c = 0; c < DC; ++c)
 #pragma unroll
       for (int x = 0; x < 4; ++x) acc[i][c][x] = 0.f;
-  for (int s0 = 0; s0 < end; s0 += BK) {
+  for (int s0 = tile.from * BK; s0 < end; s0 += BK) {
     __syncthreads();  // the last tile's V and P are used
     load_keys<D>(a, rq, a.k_cache, tile.h, s0, total, sm);
     __syncthreads();
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(NT) k_chunk(const __grid_constant__ ChunkArgs 
       }
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float old = sm.m[row], mn = fmaxf(old, mx);
+      const float old = sm.m[row], mn = fmaxf(old, mx);  // NEG while the row has seen no slot: its P is 0
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -218,6 +220,18 @@ __global__ void __launch_bounds__(NT) k_chunk(const __grid_constant__ ChunkArgs 
   for (int i = 0; i < 4; ++i) {
     const int row = 4 * ty + i, t = tile.first + row / a.G;
     if (t >= rq.nnew) continue;
+    if (tile.part >= 0) {
+      float* po = a.part + (size_t)tile.part * chunk_tile_part_floats(D);
+#pragma unroll
+      for (int c = 0; c < DC; ++c)
+        *reinterpret_cast<float4*>(po + (size_t)row * D + 64 * c + 4 * tx) =
+            make_float4(acc[i][c][0], acc[i][c][1], acc[i][c][2], acc[i][c][3]);
+      if (tx == 0) {
+        po[BR * D + row] = sm.m[row];
+        po[BR * D + BR + row] = sm.l[row];
+      }
+      continue;
+    }
     const int g = tile.h * a.G + row % a.G;
     const size_t at = (size_t)(rq.row0 + t) * a.Hq + g;
     const float inv = 1.f / sm.l[row];
@@ -245,6 +259,7 @@ __global__ void __launch_bounds__(NT) k_chunk_weights(const __grid_constant__ Ch
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
   const ChunkTile tile = a.wtiles[blockIdx.x];
+  let_next_in();
   const ChunkReq rq = a.reqs[tile.r];
   const int total = rq.cached + rq.nnew;
   const int tokens = BR / a.G, s0 = tile.first;
@@ -252,8 +267,7 @@ __global__ void __launch_bounds__(NT) k_chunk_weights(const __grid_constant__ Ch
   wait_for_previous();
   load_keys<D>(a, rq, a.k_cache, tile.h, s0, total, sm);
   float w[4] = {0.f, 0.f, 0.f, 0.f};
-  // the first token that sees slot s0, rounded down to a tile
-  for (int t0 = max(0, s0 - rq.cached) / tokens * tokens; t0 < rq.nnew; t0 += tokens) {
+  for (int t0 = tile.from * tokens; t0 < min(tile.to * tokens, rq.nnew); t0 += tokens) {
     __syncthreads();  // the last tile's rows are used
     load_rows<D>(a, rq, tile.h, t0, sm);
     if (tid < BR) {
@@ -283,8 +297,58 @@ __global__ void __launch_bounds__(NT) k_chunk_weights(const __grid_constant__ Ch
     float sum = 0.f;
 #pragma unroll
     for (int y = 0; y < 16; ++y) sum += sm.p[y][tid];
-    a.weights[(((size_t)a.layer * a.M + rq.slot) * a.Hkv + tile.h) * a.cap + s0 + tid] += sum;
+    if (tile.part >= 0) a.wpart[(size_t)tile.part * BK + tid] = sum;
+    else a.weights[(((size_t)a.layer * a.M + rq.slot) * a.Hkv + tile.h) * a.cap + s0 + tid] += sum;
   }
+}
+
+// Joins the partials of a query tile: thread = four dimensions of a row.
+template <int D>
+__global__ void __launch_bounds__(D / 4) k_chunk_tile_join(const __grid_constant__ ChunkArgs a) {
+  const ChunkTileJoin jn = a.joins[blockIdx.x];
+  let_next_in();
+  wait_for_previous();
+  const ChunkReq rq = a.reqs[jn.r];
+  const int row = blockIdx.y, t = jn.first + row / a.G;
+  if (t >= rq.nnew) return;
+  const float* base = a.part + (size_t)jn.part * chunk_tile_part_floats(D);
+  float M = NEG;
+#pragma unroll 8
+  for (int p = 0; p < jn.n; ++p) M = fmaxf(M, __ldg(base + p * chunk_tile_part_floats(D) + BR * D + row));
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = 0; p < jn.n; ++p) {
+    const float* q = base + p * chunk_tile_part_floats(D);
+    const float f = ex2f(__ldg(q + BR * D + row) - M);  // 0 for a part of which the row sees nothing
+    const float4 x = __ldg(reinterpret_cast<const float4*>(q + (size_t)row * D) + threadIdx.x);
+    l = fmaf(f, __ldg(q + BR * D + BR + row), l);
+    o = make_float4(fmaf(f, x.x, o.x), fmaf(f, x.y, o.y), fmaf(f, x.z, o.z), fmaf(f, x.w, o.w));
+  }
+  const float inv = 1.f / l;
+  const size_t at = (size_t)(rq.row0 + t) * a.Hq + jn.h * a.G + row % a.G;
+  if (threadIdx.x == 0 && a.stat) a.stat[at] = make_float2(M, inv);
+  const size_t e = at * D + 4 * threadIdx.x;
+  if (a.q_f32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + e) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  } else {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + e) =
+        make_uint2(*reinterpret_cast<const unsigned*>(&lo), *reinterpret_cast<const unsigned*>(&hi));
+  }
+}
+
+// Adds the partial sums of a key tile, in the order of its parts.
+__global__ void __launch_bounds__(BK) k_chunk_tile_weights_join(const __grid_constant__ ChunkArgs a) {
+  const ChunkTileJoin jn = a.wjoins[blockIdx.x];
+  wait_for_previous();
+  const ChunkReq rq = a.reqs[jn.r];
+  const int i = jn.first + (int)threadIdx.x;
+  if (i >= rq.cached + rq.nnew || rq.slot < 0 || rq.slot >= a.M) return;
+  float w = 0.f;
+#pragma unroll 8
+  for (int p = 0; p < jn.n; ++p) w += __ldg(a.wpart + (size_t)(jn.part + p) * BK + threadIdx.x);
+  a.weights[(((size_t)a.layer * a.M + rq.slot) * a.Hkv + jn.h) * a.cap + i] += w;
 }
 
 cudaError_t launch_k(void (*kernel)(ChunkArgs), size_t smem, int grid, bool chained, const ChunkArgs& a, cudaStream_t s) {
@@ -299,18 +363,22 @@ cudaError_t launch_k(void (*kernel)(ChunkArgs), size_t smem, int grid, bool chai
 
 cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t s) {
   if (a.n_tiles == 0) return cudaSuccess;
-  if (a.G < 1 || BR % a.G) return cudaErrorInvalidValue;
-  if (a.D == 128) return launch_k(k_chunk<128>, sizeof(Smem<128>), a.n_tiles, false, a, s);
-  if (a.D == 64) return launch_k(k_chunk<64>, sizeof(Smem<64>), a.n_tiles, false, a, s);
-  return cudaErrorInvalidValue;
+  if (a.G < 1 || BR % a.G || (a.D != 64 && a.D != 128)) return cudaErrorInvalidValue;
+  const cudaError_t e = a.D == 128 ? launch_k(k_chunk<128>, sizeof(Smem<128>), a.n_tiles, false, a, s)
+                                   : launch_k(k_chunk<64>, sizeof(Smem<64>), a.n_tiles, false, a, s);
+  if (e != cudaSuccess || a.n_joins == 0) return e;
+  const dim3 grid((unsigned)a.n_joins, BR);
+  return a.D == 128 ? launch_chained(k_chunk_tile_join<128>, grid, 32, 0, s, a)
+                    : launch_chained(k_chunk_tile_join<64>, grid, 16, 0, s, a);
 }
 
 cudaError_t launch_chunk_weights(const ChunkArgs& a, cudaStream_t s) {
   if (a.n_wtiles == 0) return cudaSuccess;
-  if (a.G < 1 || BR % a.G) return cudaErrorInvalidValue;
-  if (a.D == 128) return launch_k(k_chunk_weights<128>, sizeof(Smem<128>), a.n_wtiles, true, a, s);
-  if (a.D == 64) return launch_k(k_chunk_weights<64>, sizeof(Smem<64>), a.n_wtiles, true, a, s);
-  return cudaErrorInvalidValue;
+  if (a.G < 1 || BR % a.G || (a.D != 64 && a.D != 128)) return cudaErrorInvalidValue;
+  const cudaError_t e = a.D == 128 ? launch_k(k_chunk_weights<128>, sizeof(Smem<128>), a.n_wtiles, true, a, s)
+                                   : launch_k(k_chunk_weights<64>, sizeof(Smem<64>), a.n_wtiles, true, a, s);
+  if (e != cudaSuccess || a.n_wjoins == 0) return e;
+  return launch_chained(k_chunk_tile_weights_join, dim3((unsigned)a.n_wjoins), BK, 0, s, a);
 }
 
 }  // namespace gp

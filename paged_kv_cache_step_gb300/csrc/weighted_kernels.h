@@ -119,9 +119,18 @@ struct ChunkReq {
 };
 
 // CUDA-core kernels: a tile of 64 query rows (64 / G tokens of the G heads of
-// a KV head), a tile of 64 keys.
+// a KV head), a tile of 64 keys.  An item is a query tile and key tiles
+// [from, to) of it, or (weights) a key tile and query tiles [from, to).
 struct ChunkTile {
-  int32_t r, h, first, pad;  // request, KV head, first token of the rows (or first key)
+  int32_t r, h, first;  // request, KV head, first token of the rows (or first key)
+  int32_t from, to;
+  int32_t part;         // partial, -1: the result directly
+  int32_t pad[2];
+};
+struct ChunkTileJoin {
+  int32_t r, h, first;  // as above
+  int32_t part, n;      // its partials
+  int32_t pad[3];
 };
 constexpr int CHUNK_ROWS = 64, CHUNK_KEYS = 64;
 
@@ -137,14 +146,21 @@ struct ChunkArgs {
   const int32_t* bt;
   const ChunkTile* tiles;   // of the attention
   int n_tiles;
+  const ChunkTileJoin* joins;
+  int n_joins;
   const ChunkTile* wtiles;  // of the weights
   int n_wtiles;
+  const ChunkTileJoin* wjoins;
+  int n_wjoins;
+  float* part;              // partial outputs [64][D], 64 maxima, 64 sums each
+  float* wpart;             // partial weights [64] each
   const void* q;            // [rows][Hq][D], rotated
   void* out;                // [rows][Hq][D] in q's type
   float2* stat;             // [rows][Hq] (maximum, 1 / sum) of the base-2 logits
   float* weights;           // or null
   int* err;
 };
+__host__ __device__ constexpr size_t chunk_tile_part_floats(int D) { return (size_t)CHUNK_ROWS * (D + 2); }
 cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t s);
 cudaError_t launch_chunk_weights(const ChunkArgs& a, cudaStream_t s);
 
