@@ -93,13 +93,13 @@ struct gp_ctx {
   int* err_dev = nullptr;          // kernel error bits
   unsigned long long* moved_dev = nullptr;
   gp::DevBuf upload, bt2, qt, bq, scores, aval, tickets, kout, ksum, masks, xstat, attn, spec_masks, ent;
-  // the accumulated-weight operators: descriptor staging (calls in turn, so
-  // that a call waits on the host only for the one kStagingSlots before it) and scratch
+  // decode attention and the accumulated-weight operators: descriptor staging
+  // (calls in turn, so that a call waits on the host only for the one
+  // kStagingSlots before it, and none disturbs a compaction's) and scratch
   gp::StagingSlot staging[gp::kStagingSlots];
   int staging_next = 0;
   gp::DevBuf logits, wstat, evict, chunk;
   int device = 0;                  // the device current at gp_create
-  gp::DevBuf upload_attn;              // decode attention's own descriptors (it may overlap a compaction)
   // speculative selection: the Eq. 10 keep masks of every request of the last
   // demand call, computed on an engine-owned stream while the host decides
   cudaStream_t sel_stream = nullptr;

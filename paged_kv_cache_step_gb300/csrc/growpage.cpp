@@ -236,7 +236,7 @@ gp_status gp_destroy(gp_ctx* c) {
     if (c->ev_ready) cudaEventDestroy(c->ev_ready);
     if (c->ev_done) cudaEventDestroy(c->ev_done);
     for (DevBuf* b : {&c->upload, &c->bt2, &c->qt, &c->bq, &c->scores, &c->aval, &c->tickets, &c->kout, &c->ksum, &c->ent,
-                      &c->masks, &c->xstat, &c->attn, &c->spec_masks, &c->upload_attn, &c->logits, &c->wstat, &c->evict, &c->chunk})
+                      &c->masks, &c->xstat, &c->attn, &c->spec_masks, &c->logits, &c->wstat, &c->evict, &c->chunk})
       if (b->p) cudaFree(b->p);
     for (StagingSlot& s : c->staging) {
       if (s.pinned) cudaFreeHost(s.pinned);
@@ -367,10 +367,9 @@ struct Staged {
 };
 
 // Pinned layout [DevReq n][bt n*maxP][bt_new n*maxP][work n][part_base n+1]
-// [sel n][extra bytes], mirrored in `dev` (the engine's upload buffer unless
-// another is given).
-gp_status stage(gp_ctx* c, int n, bool with_new, Staged* s, DevBuf* dev = nullptr, size_t extra = 0) {
-  s->dev = dev ? dev : &c->upload;
+// [sel n][extra bytes], mirrored in the engine's upload buffer, or in a staging
+// slot of its own (*own).
+gp_status stage(gp_ctx* c, int n, bool with_new, Staged* s, StagingSlot** own = nullptr, size_t extra = 0) {
   const int maxp = c->cfg.max_pages_per_req;
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t r = o; o += (bytes + 255) & ~size_t(255); return r; };
@@ -382,11 +381,18 @@ gp_status stage(gp_ctx* c, int n, bool with_new, Staged* s, DevBuf* dev = nullpt
   s->off_sel = take(sizeof(int32_t) * n);
   s->off_extra = take(extra);
   s->bytes = o;
-  gp_status st = ensure_pinned(c, o);
-  if (st != GP_OK) return st;
-  st = ensure(c, *s->dev, o);
-  if (st != GP_OK) return st;
-  char* p = static_cast<char*>(c->pinned);
+  gp_status st;
+  char* p = nullptr;
+  if (own) {
+    if ((st = staging_take(c, o, own)) != GP_OK) return st;
+    s->dev = &(*own)->dev;
+    p = static_cast<char*>((*own)->pinned);
+  } else {
+    s->dev = &c->upload;
+    if ((st = ensure_pinned(c, o)) != GP_OK) return st;
+    if ((st = ensure(c, *s->dev, o)) != GP_OK) return st;
+    p = static_cast<char*>(c->pinned);
+  }
   s->reqs = reinterpret_cast<gp::DevReq*>(p + off_req);
   s->bt = reinterpret_cast<int32_t*>(p + s->off_bt);
   s->bt_new = reinterpret_cast<int32_t*>(p + s->off_bt_new);
@@ -1229,8 +1235,8 @@ gp_status decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_request
   if (n == 0) return GP_OK;
   // A compaction pending on the side stream (App. E.3) runs on: this call
   // waits for it on the device only if one of its requests holds a page the
-  // compaction reads or writes.  The call uploads its descriptors to its own
-  // buffer, so neither the compaction nor the speculative selection, which
+  // compaction reads or writes.  The call uploads its descriptors to a staging
+  // slot, so neither the compaction nor the speculative selection, which
   // read the engine's upload buffer, is disturbed.
   bool overlap = false;
   if (c->compaction_pending)
@@ -1301,7 +1307,8 @@ gp_status decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_request
   const size_t tick_at = (weights_at + wreq_bytes + sizeof(int64_t) * wreqs.size() + 15) & ~size_t(15);
   const size_t tick_bytes = sizeof(unsigned) * (size_t)n * Hkv;
   Staged s{};
-  if ((st = stage(c, n, false, &s, &c->upload_attn, tick_at + tick_bytes)) != GP_OK) return st;
+  StagingSlot* slot = nullptr;
+  if ((st = stage(c, n, false, &s, &slot, tick_at + tick_bytes)) != GP_OK) return st;
   std::memset(static_cast<char*>(s.extra) + tick_at, 0, tick_bytes);
   if (weights) {
     std::memcpy(static_cast<char*>(s.extra) + weights_at, wreqs.data(), wreq_bytes);
@@ -1329,7 +1336,7 @@ gp_status decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_request
     std::memcpy(s.bt + (size_t)r * maxp, reqs[r].block_table, sizeof(int32_t) * reqs[r].num_pages);
     s.work[r] = num_tokens[r];  // the staged work array carries the token counts here
   }
-  if ((st = upload(c, s)) != GP_OK) return st;
+  if ((st = staging_upload(c, *slot, s.bytes)) != GP_OK) return st;
   char* base = static_cast<char*>(c->attn.p);
   gp::AttnArgs a{};
   a.tc = tc ? 1 : 0;

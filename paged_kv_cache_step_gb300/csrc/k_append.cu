@@ -12,7 +12,9 @@
 //
 // Bounded by HBM: every element is read and written once in 16-byte pieces,
 // a pair's two halves by the same thread (so q_rot may be q).  One block a
-// token: the d / 2 angles are shared by all its heads.
+// token: the d / 2 angles are shared by all its heads, and formed while the
+// rows are on their way.  16 884 tokens of 32 + 8 heads, d = 128, bf16: 64 us,
+// 96 % of the copy rate (76 us with the loads after the angles).
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -61,12 +63,10 @@ struct Piece<false> {
 };
 
 // One piece of each half of a head's row, rotated.
-template <int D, bool F32>
-__device__ __forceinline__ void rotate_piece(const unsigned char* src, unsigned char* dst, int piece, const float* cs,
-                                             const float* sn) {
+template <bool F32>
+__device__ __forceinline__ void rotate_piece(const uint4& lo, const uint4& hi, uint4* dst_lo, uint4* dst_hi, int piece,
+                                             const float* cs, const float* sn) {
   using P = Piece<F32>;
-  constexpr int HALF = D / 2 / P::N;  // pieces of a half row
-  const uint4 lo = reinterpret_cast<const uint4*>(src)[piece], hi = reinterpret_cast<const uint4*>(src)[piece + HALF];
   float a[P::N], b[P::N], x[P::N], y[P::N];
   P::get(lo, a);
   P::get(hi, b);
@@ -76,14 +76,15 @@ __device__ __forceinline__ void rotate_piece(const unsigned char* src, unsigned 
     x[i] = fmaf(a[i], c, -b[i] * s);
     y[i] = fmaf(b[i], c, a[i] * s);
   }
-  reinterpret_cast<uint4*>(dst)[piece] = P::put(x);
-  reinterpret_cast<uint4*>(dst)[piece + HALF] = P::put(y);
+  *dst_lo = P::put(x);
+  *dst_hi = P::put(y);
 }
 
 template <int D, bool QF32, bool KF32>
 __global__ void __launch_bounds__(NT) k_append(const __grid_constant__ AppendArgs a) {
   constexpr int QB = QF32 ? 4 * D : 2 * D, KB = KF32 ? 4 * D : 2 * D;  // bytes of a row
-  constexpr int UQ = D / 2 / Piece<QF32>::N, UK = D / 2 / Piece<KF32>::N, UV = KB / 16;
+  constexpr int UQ = D / 2 / Piece<QF32>::N, UK = D / 2 / Piece<KF32>::N, UV = KB / 16;  // units of a head
+  constexpr int AHEAD = 2;  // units a thread loads before the angles are known
   __shared__ __align__(16) float cs[D / 2];
   __shared__ __align__(16) float sn[D / 2];
   const int tid = threadIdx.x;
@@ -107,6 +108,41 @@ __global__ void __launch_bounds__(NT) k_append(const __grid_constant__ AppendArg
     if (tid == 0) atomicOr(a.err, ERR_BAD_PAGE);
     return;
   }
+  const size_t head0 = ((size_t)a.layer * a.num_pages_total + page) * a.Hkv;  // (layer, page)'s first KV head
+  const size_t in_page = (size_t)(tok % PAGE) * KB;
+  const int nq = a.q ? a.Hq * UQ : 0, nk = nq + a.Hkv * UK, nv = nk + a.Hkv * UV;
+  // unit u: a piece of each half of a query or key row, or a piece of a value row
+  auto load = [&](int u, uint4& lo, uint4& hi) {
+    if (u < nq) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.q) + ((size_t)row * a.Hq + u / UQ) * QB);
+      lo = src[u % UQ];
+      hi = src[u % UQ + UQ];
+    } else if (u < nk) {
+      const int h = (u - nq) / UK, p = (u - nq) % UK;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.k) + ((size_t)row * a.Hkv + h) * KB);
+      lo = src[p];
+      hi = src[p + UK];
+    } else if (u < nv) {
+      const int h = (u - nk) / UV, p = (u - nk) % UV;
+      lo = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.v) + ((size_t)row * a.Hkv + h) * KB)[p];
+    }
+  };
+  auto store = [&](int u, const uint4& lo, const uint4& hi) {
+    if (u < nq) {
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<unsigned char*>(a.q_rot) + ((size_t)row * a.Hq + u / UQ) * QB) + u % UQ;
+      rotate_piece<QF32>(lo, hi, dst, dst + UQ, u % UQ, cs, sn);
+    } else if (u < nk) {
+      const int h = (u - nq) / UK, p = (u - nq) % UK;
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<unsigned char*>(a.k_cache) + (head0 + h) * (size_t)PAGE * KB + in_page) + p;
+      rotate_piece<KF32>(lo, hi, dst, dst + UK, p, cs, sn);
+    } else if (u < nv) {
+      const int h = (u - nk) / UV, p = (u - nk) % UV;
+      reinterpret_cast<uint4*>(static_cast<unsigned char*>(a.v_cache) + (head0 + h) * (size_t)PAGE * KB + in_page)[p] = lo;
+    }
+  };
+  uint4 first[AHEAD], second[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) load(tid + i * NT, first[i], second[i]);
   if (tid < D / 2) {
     const double ang = (double)(rq.pos + t) * a.inv_freq[tid];
     const double k = rint(ang * 0.15915494309189535);  // 1 / (2 pi)
@@ -118,25 +154,11 @@ __global__ void __launch_bounds__(NT) k_append(const __grid_constant__ AppendArg
     sn[tid] = s;
   }
   __syncthreads();
-  const size_t head0 = ((size_t)a.layer * a.num_pages_total + page) * a.Hkv;  // (layer, page)'s first KV head
-  const size_t in_page = (size_t)(tok % PAGE) * KB;
-  unsigned char* kc = static_cast<unsigned char*>(a.k_cache);
-  unsigned char* vc = static_cast<unsigned char*>(a.v_cache);
-  const int nq = a.q ? a.Hq * UQ : 0, nk = nq + a.Hkv * UK, nv = nk + a.Hkv * UV;
-  for (int u = tid; u < nv; u += NT) {
-    if (u < nq) {
-      const size_t off = ((size_t)row * a.Hq + u / UQ) * QB;
-      rotate_piece<D, QF32>(static_cast<const unsigned char*>(a.q) + off, static_cast<unsigned char*>(a.q_rot) + off,
-                            u % UQ, cs, sn);
-    } else if (u < nk) {
-      const int h = (u - nq) / UK;
-      rotate_piece<D, KF32>(static_cast<const unsigned char*>(a.k) + ((size_t)row * a.Hkv + h) * KB,
-                            kc + (head0 + h) * (size_t)PAGE * KB + in_page, (u - nq) % UK, cs, sn);
-    } else {
-      const int h = (u - nk) / UV, p = (u - nk) % UV;
-      reinterpret_cast<uint4*>(vc + (head0 + h) * (size_t)PAGE * KB + in_page)[p] =
-          reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.v) + ((size_t)row * a.Hkv + h) * KB)[p];
-    }
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) store(tid + i * NT, first[i], second[i]);
+  for (int u = tid + AHEAD * NT; u < nv; u += NT) {
+    load(u, first[0], second[0]);
+    store(u, first[0], second[0]);
   }
   if (a.weights)
     for (int h = tid; h < a.Hkv; h += NT)
