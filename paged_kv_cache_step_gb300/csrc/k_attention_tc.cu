@@ -461,42 +461,53 @@ __global__ void __launch_bounds__(NT, 1) k_decode_attn_tc(const __grid_constant_
       }
       asm volatile("bar.sync %0, %1;" ::"n"(BAR_Q), "n"(NQ_THR) : "memory");
       if (*q_fail) return false;  // written only before the barrier: both query warps agree
-      for (int e = qt; e < G * D; e += NQ_THR) {
-        const int gi = e / D, d = e % D;
-        const int g = it.h * G + gi;
-        const size_t qi = ((size_t)it.r * a.Hq + g) * D + d;
-        const double qv = a.q_f32 ? (double)static_cast<const float*>(a.q)[qi]
-                                  : (double)__bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[qi]);
-        if (it.split == 0 && a.first) {
-          double* row =
-              a.pool + (((size_t)a.layer * a.M + it.slot) * 2) * ((size_t)a.Hq * D) + (size_t)g * D + d;
+      // every element's load is on its way before the first is used
+      constexpr int QN = G * D / NQ_THR;
+      double qv[QN];
+#pragma unroll
+      for (int u = 0; u < QN; ++u) {
+        const size_t qi = ((size_t)it.r * a.Hq + it.h * G) * D + qt + u * NQ_THR;
+        qv[u] = a.q_f32 ? (double)static_cast<const float*>(a.q)[qi]
+                        : (double)__bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[qi]);
+      }
+      if (it.split == 0 && a.first) {
+        const bool first = a.first[it.r];
+#pragma unroll
+        for (int u = 0; u < QN; ++u) {
+          double* row = a.pool + (((size_t)a.layer * a.M + it.slot) * 2) * ((size_t)a.Hq * D) + (size_t)it.h * G * D + qt +
+                        u * NQ_THR;
           double* row_l = row + (size_t)a.Hq * D;
-          if (a.first[it.r]) {
-            *row = qv;
-            *row_l = qv;
+          if (first) {
+            *row = qv[u];
+            *row_l = qv[u];
           } else {
-            *row = fma(a.beta_s, *row, (1.0 - a.beta_s) * qv);
-            *row_l = fma(a.beta_l, *row_l, (1.0 - a.beta_l) * qv);
+            *row = fma(a.beta_s, *row, (1.0 - a.beta_s) * qv[u]);
+            *row_l = fma(a.beta_l, *row_l, (1.0 - a.beta_l) * qv[u]);
           }
         }
-        qs[gi * D + d] = (float)qv;
       }
-      asm volatile("bar.sync %0, %1;" ::"n"(BAR_Q), "n"(NQ_THR) : "memory");
-      // rotate-half RoPE at the request's position (pairs (i, i + D/2)) and the
-      // log2(e)/sqrt(d) scale, then the three bf16 parts: rows gi, G + gi, 2G + gi
-      for (int e = qt; e < G * (D / 2); e += NQ_THR) {
-        const int gi = e / (D / 2), i = e % (D / 2);
-        const double ang = (double)it.pos * a.inv_freq[i];
+#pragma unroll
+      for (int u = 0; u < QN; ++u) qs[qt + u * NQ_THR] = (float)qv[u];
+      // rotate-half RoPE at the request's position (pairs (i, i + D/2), an angle
+      // per thread for the G heads) and the log2(e)/sqrt(d) scale, then the three
+      // bf16 parts: rows gi, G + gi, 2G + gi
+      static_assert(NQ_THR == D / 2, "one pair of dimensions a thread");
+      float sn, cs;
+      {
+        const double ang = (double)it.pos * a.inv_freq[qt];
         const double kk = rint(ang * 0.15915494309189535);  // 1 / (2 pi)
         double red2 = fma(-kk, 6.283185307179586, ang);     // 2 pi, high part
         red2 = fma(-kk, 2.4492935982947064e-16, red2);      // 2 pi, low part
-        float sn, cs;
         sincosf((float)red2, &sn, &cs);
-        const float x1 = qs[gi * D + i], x2 = qs[gi * D + i + D / 2];
+      }
+      asm volatile("bar.sync %0, %1;" ::"n"(BAR_Q), "n"(NQ_THR) : "memory");
+#pragma unroll
+      for (int gi = 0; gi < G; ++gi) {
+        const float x1 = qs[gi * D + qt], x2 = qs[gi * D + qt + D / 2];
         const float o[2] = {sc * fmaf(x1, cs, -x2 * sn), sc * fmaf(x2, cs, x1 * sn)};
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const int d = i + hf * (D / 2);
+          const int d = qt + hf * (D / 2);
           __nv_bfloat16 h1, h2, h3;
           split3(o[hf], h1, h2, h3);
           st_bf16(qb, op_off(d, gi), h1);
