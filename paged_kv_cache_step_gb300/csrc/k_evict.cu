@@ -80,22 +80,22 @@ __global__ void __launch_bounds__(SNT) k_evict_select(const __grid_constant__ Ev
   }
   unsigned* flags = a.flags + rq.item0 + (size_t)unit * rq.items;
   for (int k = tid; k < rq.items; k += SNT) flags[k] = 0u;
-  // f(word, key) for this warp's words in order; the key counts where slot < ncand
-  auto each_word = [&](auto&& f) {
+  // f(word, key) for words [from, to) in order; the key counts where slot < ncand
+  auto each_word = [&](int from, int to, auto&& f) {
     if constexpr (STAGED) {
 #pragma unroll 4
-      for (int w = wa; w < wb; ++w) f(w, 32 * w + lane < ncand ? staged[32 * w + lane] : 0u);
+      for (int w = from; w < to; ++w) f(w, 32 * w + lane < ncand ? staged[32 * w + lane] : 0u);
     } else {
-      for (int w = wa; w < wb; w += 8) {  // eight loads in flight
+      for (int w = from; w < to; w += 8) {  // eight loads in flight
         unsigned k[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int s = 32 * (w + j) + lane;
-          k[j] = w + j < wb && s < ncand ? okey(w0[s]) : 0u;
+          k[j] = w + j < to && s < ncand ? okey(w0[s]) : 0u;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (w + j < wb) f(w + j, k[j]);
+          if (w + j < to) f(w + j, k[j]);
       }
     }
   };
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(SNT) k_evict_select(const __grid_constant__ Ev
       const unsigned digit = pass == 2 ? 1023u : 2047u;
       for (int b = tid; b < BINS; b += SNT) hist[b] = 0u;
       __syncthreads();
-      each_word([&](int w, unsigned k) {
+      each_word(wa, wb, [&](int w, unsigned k) {
         if (32 * w + lane < ncand && (k & mask_bits) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1u);
       });
       __syncthreads();
@@ -163,19 +163,20 @@ __global__ void __launch_bounds__(SNT) k_evict_select(const __grid_constant__ Ev
   constexpr int BLOCKS = 65536 / 32 / SWARP / 32;  // of 32 words a warp, at most
   unsigned sure[BLOCKS], tie[BLOCKS];
 #pragma unroll
-  for (int b = 0; b < BLOCKS; ++b) sure[b] = tie[b] = 0u;
-  each_word([&](int w, unsigned k) {
-    const int s = 32 * w + lane, j = w - wa;
-    const bool cand = s < ncand && need > 0;
-    const unsigned bs = __ballot_sync(0xffffffffu, cand ? (whole ? k >= thr : k > thr) : s >= ncand && s < rq.T);
-    const unsigned bt = __ballot_sync(0xffffffffu, cand && !whole && k == thr);
-#pragma unroll
-    for (int b = 0; b < BLOCKS; ++b)
-      if (j == 32 * b + lane) {
+  for (int b = 0; b < BLOCKS; ++b) {
+    sure[b] = tie[b] = 0u;
+    const int first = wa + 32 * b;
+    each_word(first, min(first + 32, wb), [&](int w, unsigned k) {
+      const int s = 32 * w + lane;
+      const bool cand = s < ncand && need > 0;
+      const unsigned bs = __ballot_sync(0xffffffffu, cand ? (whole ? k >= thr : k > thr) : s >= ncand && s < rq.T);
+      const unsigned bt = __ballot_sync(0xffffffffu, cand && !whole && k == thr);
+      if (w - first == lane) {
         sure[b] = bs;
         tie[b] = bt;
       }
-  });
+    });
+  }
   unsigned cnt = 0u, eqs = 0u;
 #pragma unroll
   for (int b = 0; b < BLOCKS; ++b) {
