@@ -926,6 +926,10 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
       const ChunkReq rq = load_req(a.reqs + it.r);
      for (int pg = it.page; pg < it.page + it.pages && ok; ++pg) {
       const int slot_i = pg * PAGE + x * TK + key;  // this thread's logical slot
+      // the weight so far is on its way while the products run
+      auto mine = [&] { return half == 0 && slot_i < rq.cached + rq.nnew && rq.slot >= 0 && rq.slot < a.M; };
+      auto weight = [&] { return a.weights + (((size_t)a.layer * a.M + rq.slot) * a.Hkv + it.h) * a.cap + slot_i; };
+      const float so_far = it.part < 0 && mine() ? *weight() : 0.f;
       float2 w[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       for (int q = it.qb; q < it.qe; ++q, ++c) {
         const int z = c & 1;
@@ -986,11 +990,8 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
       asm volatile("bar.sync %0, 256;" ::"r"(1 + x) : "memory");
       if (!ok) break;
       if (half) continue;
-      if (it.part >= 0) {
-        a.wpart[(size_t)it.part * PAGE + x * TK + key] = sum;
-      } else if (slot_i < rq.cached + rq.nnew && rq.slot >= 0 && rq.slot < a.M) {
-        a.weights[(((size_t)a.layer * a.M + rq.slot) * a.Hkv + it.h) * a.cap + slot_i] += sum;
-      }
+      if (it.part >= 0) a.wpart[(size_t)it.part * PAGE + x * TK + key] = sum;
+      else if (mine()) *weight() = so_far + sum;
      }
     }
     if (!ok && lane == 0) timed_out();
