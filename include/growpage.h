@@ -408,7 +408,7 @@ gp_status gp_decode_attention(gp_ctx* ctx, int32_t layer, int32_t n, const gp_re
  * RoPE at position reqs[r].pos + t, rope_theta; angles in fp64, one rounding
  * to kv_dtype) and its value copied; q_rot gets the rotated queries, rounded
  * to q_dtype, as gp_chunk_attention takes them.  q_dev, q_rot_dev: device
- * [rows][Hq][d] q_dtype, both or neither NULL, may be the same buffer;
+ * [rows][Hq][d] q_dtype, both or neither NULL, the same buffer or disjoint ones;
  * k_dev, v_dev: device [rows][Hkv][d] kv_dtype; weights_dev may be NULL.
  * All but weights_dev 16-byte aligned, as the caches.  num_cached and num_new:
  * HOST int32 [n]; the tokens must fit the request's pages, and a page written
@@ -435,7 +435,11 @@ gp_status gp_decode_attention_weighted(gp_ctx* ctx, int32_t layer, int32_t n, co
  * gp_append_tokens; out_dev: the same shape and type; both 16-byte aligned.
  * With weights_dev, the weights of every token are added; NULL leaves that
  * out.  The rows of K and V of the attended tokens must be finite; cache slots
- * past num_cached[r] + num_new[r] may hold any bits. */
+ * past num_cached[r] + num_new[r] may hold any bits.  out_dev must not overlap
+ * q_dev.  bf16 caches and queries run on the tensor-core kernels, which round
+ * the softmax weights to bf16 for the product with V (out is bf16 too; the
+ * accumulated weights are not rounded); the rest, or everything under
+ * gp_set_scan_kernel(CUDA_CORE), on CUDA-core ones in fp32. */
 gp_status gp_chunk_attention(gp_ctx* ctx, int32_t layer, int32_t n, const gp_request* reqs,
                              const int32_t* num_cached, const int32_t* num_new, const void* q_dev,
                              void* out_dev, float* weights_dev);
@@ -450,8 +454,9 @@ gp_status gp_chunk_attention(gp_ctx* ctx, int32_t layer, int32_t n, const gp_req
  * keep_tokens is left as it is.  Copy-on-write as in gp_compress_hold for the
  * requests that evict (GP_ERR_NO_PAGES: nothing changed).  num_tokens and
  * keep_tokens: HOST int32 [n].  Runs on the compaction stream if one is set,
- * with gp_compress_hold's rules; a gp_boundary_demand result of the slots is
- * stale afterwards.  gp_debug_keep_mask gives the kept sets. */
+ * with gp_compress_hold's rules, which hold for the weights of the evicted
+ * requests as for their K/V; a gp_boundary_demand result of the slots is stale
+ * afterwards.  gp_debug_keep_mask gives the kept sets. */
 gp_status gp_evict_weighted(gp_ctx* ctx, int32_t n, gp_request* reqs, const int32_t* num_tokens,
                             const int32_t* keep_tokens, float* weights_dev);
 
@@ -539,7 +544,8 @@ gp_status gp_debug_fail_next_launch(gp_ctx* ctx, int32_t kernel);
 
 /* Which kernels do the cache-wide contractions: the scan of
  * gp_boundary_demand and the scores and weighted values of
- * gp_decode_attention.  AUTO (default): the tensor-core (tcgen05) kernels
+ * gp_decode_attention(_weighted) and gp_chunk_attention (which takes bf16
+ * queries and caches on the tensor cores).  AUTO (default): the tensor-core (tcgen05) kernels
  * where they apply -- the scan for bf16 caches (every request length up to
  * the 256-page block-table limit), attention for bf16 caches with d = 128
  * and 2 or 4 query heads per KV head -- and the CUDA-core (fp32 FMA)

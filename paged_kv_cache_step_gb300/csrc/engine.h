@@ -161,8 +161,10 @@ inline gp_status fail(gp_ctx* c, gp_status st, const char* fmt, ...) {
 #define GP_CUDA(ctx, call)                                                              \
   do {                                                                                  \
     cudaError_t e_ = (call);                                                            \
-    if (e_ != cudaSuccess)                                                              \
+    if (e_ != cudaSuccess) {                                                            \
+      cudaGetLastError(); /* else the next launch's check would meet it again */        \
       return fail((ctx), GP_ERR_CUDA, "%s failed: %s", #call, cudaGetErrorString(e_)); \
+    }                                                                                   \
   } while (0)
 
 inline int elt_bytes(int dtype) { return dtype == GP_DTYPE_F32 ? 4 : 2; }

@@ -1416,6 +1416,8 @@ gp_status gp_decode_attention_weighted(gp_ctx* c, int32_t layer, int32_t n, cons
                                        float* out_dev, float* weights_dev) {
   if (!c) return GP_ERR_INVALID;
   gp_status st = check_decode(c, layer, n, reqs, num_tokens, !q_dev || !out_dev || !weights_dev);
+  if (st == GP_OK && (reinterpret_cast<uintptr_t>(weights_dev) & 3u))
+    return fail(c, GP_ERR_INVALID, "the weights must be 4-byte aligned");
   if (st != GP_OK || (st = ready_call(c)) != GP_OK) return st;
   return decode_attention(c, layer, n, reqs, num_tokens, q_dev, first_dev, out_dev, weights_dev);
 }

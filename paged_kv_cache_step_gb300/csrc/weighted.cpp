@@ -27,7 +27,13 @@ struct Layout {
   }
 };
 
-bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool misaligned(const void* p, unsigned to = 16) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+
+// Whether two buffers of `bytes` share any.
+bool overlap(const void* p, const void* q, size_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + bytes && b < a + bytes;
+}
 
 // The checks that the calls over new tokens share: every request bound and
 // listed once, its cached and new tokens inside its pages.  *rows: packed rows.
@@ -318,6 +324,10 @@ gp_status gp_append_tokens(gp_ctx* c, int32_t layer, int32_t n, const gp_request
   if (misaligned(q_dev) || misaligned(k_dev) || misaligned(v_dev) || misaligned(q_rot_dev) ||
       misaligned(c->k_cache) || misaligned(c->v_cache))
     return fail(c, GP_ERR_INVALID, "queries, keys, values and caches must be 16-byte aligned");
+  if (misaligned(weights_dev, 4)) return fail(c, GP_ERR_INVALID, "the weights must be 4-byte aligned");
+  if (q_dev && q_rot_dev != q_dev &&
+      overlap(q_dev, q_rot_dev, (size_t)rows * g.num_q_heads * g.head_dim * elt_bytes(g.q_dtype)))
+    return fail(c, GP_ERR_INVALID, "q_rot overlaps q without being it");
   // the pages written: private, and each in one request only
   int64_t pages = 0;
   int live = 0;
@@ -402,6 +412,9 @@ gp_status gp_chunk_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_reque
   if (!q_dev || !out_dev) return fail(c, GP_ERR_INVALID, "null argument");
   if (misaligned(q_dev) || misaligned(out_dev) || misaligned(c->k_cache) || misaligned(c->v_cache))
     return fail(c, GP_ERR_INVALID, "queries, outputs and caches must be 16-byte aligned");
+  if (misaligned(weights_dev, 4)) return fail(c, GP_ERR_INVALID, "the weights must be 4-byte aligned");
+  if (overlap(q_dev, out_dev, (size_t)rows * g.num_q_heads * g.head_dim * elt_bytes(g.q_dtype)))
+    return fail(c, GP_ERR_INVALID, "the outputs overlap the queries");
   if ((st = ready_call(c)) != GP_OK) return st;
   // The tensor-core kernels take bf16 caches and queries (AUTO and
   // TENSOR_CORE), the CUDA-core ones everything.
@@ -537,8 +550,8 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
   if (n < 0 || n > g.max_slots) return fail(c, GP_ERR_INVALID, "n = %d outside [0, max_slots]", n);
   if (n == 0) return ready_call(c);
   if (!reqs || !num_tokens || !keep_tokens || !weights_dev) return fail(c, GP_ERR_INVALID, "null argument");
-  if (misaligned(c->k_cache) || misaligned(c->v_cache))
-    return fail(c, GP_ERR_INVALID, "the caches must be 16-byte aligned");
+  if (misaligned(c->k_cache) || misaligned(c->v_cache) || misaligned(weights_dev, 4))
+    return fail(c, GP_ERR_INVALID, "the caches must be 16-byte aligned, the weights 4-byte");
   const int units = units_of(c), maxp = g.max_pages_per_req;
   const int row_bytes = g.head_dim * elt_bytes(g.kv_dtype), R = evict_rows(row_bytes);
   std::vector<uint8_t> bound(g.max_slots, 0);
@@ -588,6 +601,7 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
   if ((st = ensure(c, c->evict, scratch.bytes)) != GP_OK) return st;
   StagingSlot* slot = nullptr;
   if ((st = staging_take(c, lay.bytes, &slot)) != GP_OK) return st;
+  c->last_compress.clear();  // its lists may be in the scratch
   char* host = static_cast<char*>(slot->pinned);
   std::memcpy(host + at_req, er.data(), sizeof(EvictReq) * (size_t)n);
   int32_t* old_bt = reinterpret_cast<int32_t*>(host + at_old);

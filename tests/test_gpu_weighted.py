@@ -363,6 +363,58 @@ def test_chunk_attention_concentrated(kernel):
         e.close()
 
 
+@pytest.mark.parametrize("shape", ["bf16_g2_d64", "bf16_g4_d128"])
+def test_chunk_attention_long_beside_short(shape):
+    """One drafted token chunk over a cache long enough that single query tiles
+    get a launch of their own, beside prompts of pairs and of odd tiles; rows
+    of the weights longer than any request."""
+    cached, new = [33000, 0, 130, 0], [5, 300, 2, 1]
+    d = SHAPES[shape].get("d", 128)
+    e = Engine([130, 2, 1, 1], L=1, hq=16 if d == 64 else 32, hkv=8, d=d, seed=14, cap=140)
+    try:
+        e.fill([33005, 300, 132, 1])
+        q = e.randn(sum(new), e.hq, e.d).bfloat16()
+        out, w = torch.full_like(q, math.nan), e.w.clone()
+        gp.gp_chunk_attention(e.ctx, 0, e.reqs, cached, new, q, out, w)
+        gp.gp_synchronize(e.ctx)
+        check_chunk(e, 0, cached, new, q, out, e.w, w, True)
+    finally:
+        e.close()
+
+
+def test_the_longest_request():
+    """256 pages, 65 536 tokens: appended to, attended to by a chunk and a step,
+    evicted by one and by half (over the length that the selection stages)."""
+    T = 65536
+    e = Engine([256], L=1, hq=2, hkv=1, d=64, seed=15)
+    try:
+        e.fill([T - 40])
+        e.reqs[0].pos = 1_000_000
+        qx, kx, vx = (e.randn(40, h, 64).bfloat16() for h in (2, 1, 1))
+        rot = torch.empty_like(qx)
+        gp.gp_append_tokens(e.ctx, 0, e.reqs, [T - 40], [40], qx, kx, vx, rot, e.w)
+        out, w = torch.empty_like(rot), e.w.clone()
+        gp.gp_chunk_attention(e.ctx, 0, e.reqs, [T - 40], [40], rot, out, w)
+        gp.gp_synchronize(e.ctx)
+        check_chunk(e, 0, [T - 40], [40], rot, out, e.w, w, True)
+        e.w.copy_(w)
+        one, w1 = torch.empty(1, 2, 64, device="cuda"), e.w.clone()
+        gp.gp_decode_attention_weighted(e.ctx, 0, e.reqs, [T], qx[:1].contiguous(), None, one, w1)
+        gp.gp_synchronize(e.ctx)
+        qr = e.rope(qx[:1], torch.tensor([1_000_000], device="cuda"))
+        ref, mag, ws, rel = softmax_reference(qr, e.rows(e.k, 0, 0, 0, T), e.rows(e.v, 0, 0, 0, T), T)
+        assert torch.all((one[0].double() - ref[0]).abs() <= 2 * rel * mag[0])
+        want = e.w[0, 0, 0].double() + ws
+        assert torch.all((w1[0, 0, 0].double() - want).abs() <= rel * ws + 4 * 2.0 ** -23 * want)
+        for tokens, keep in ((T, T - 1), (T - 1, 30001)):
+            k0, v0, w0, t0 = e.k.clone(), e.v.clone(), e.w.clone(), [e.reqs[0].pages]
+            gp.gp_evict_weighted(e.ctx, e.reqs, [tokens], [keep], e.w)
+            gp.gp_synchronize(e.ctx)
+            check_evict(e, [tokens], [keep], k0, v0, w0, t0)
+    finally:
+        e.close()
+
+
 # ---- gp_evict_weighted ---------------------------------------------------------
 
 def order_key(w):

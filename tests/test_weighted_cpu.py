@@ -29,7 +29,7 @@ def _append(ctx, reqs, cached=(0, 5, 256), new=(1, 0, 256), layer=0, q=DEV, k=DE
     gp.gp_append_tokens(ctx, layer, reqs, cached, new, q, k, v, rot, w)
 
 
-def _chunk(ctx, reqs, cached=(0, 5, 256), new=(1, 0, 256), layer=0, q=DEV, out=DEV, w=DEV):
+def _chunk(ctx, reqs, cached=(0, 5, 256), new=(1, 0, 256), layer=0, q=DEV, out=DEV << 4, w=DEV):
     gp.gp_chunk_attention(ctx, layer, reqs, cached, new, q, out, w)
 
 
@@ -95,7 +95,7 @@ def test_new_tokens_outside_the_pages(eng, call):
 def test_append_pointers_and_shared_pages(eng):
     ctx, reqs = eng
     for kw in (dict(k=None), dict(v=None), dict(q=None), dict(rot=None), dict(q=DEV + 2), dict(k=DEV + 8),
-               dict(v=DEV + 4), dict(rot=DEV + 8)):
+               dict(v=DEV + 4), dict(rot=DEV + 8), dict(rot=DEV + 16), dict(q=DEV + 16), dict(w=DEV + 2)):
         assert _status(_append, ctx, reqs, **kw) == gp.GP_ERR_INVALID
     assert _status(_append, ctx, reqs, q=None, rot=None) == gp.GP_ERR_STATE
     assert _status(_append, ctx, reqs, w=None) == gp.GP_ERR_STATE
@@ -111,17 +111,21 @@ def test_append_pointers_and_shared_pages(eng):
 
 def test_attention_pointers_and_lengths(eng):
     ctx, reqs = eng
-    for kw in (dict(q=None), dict(out=None), dict(q=DEV + 8), dict(out=DEV + 4)):
-        assert _status(_chunk, ctx, reqs, **kw) == gp.GP_ERR_INVALID
+    bytes_ = 257 * 8 * 128 * 2  # rows x heads x d, bf16
+    far = DEV + 2 * bytes_
+    for kw in (dict(q=None), dict(out=None), dict(q=DEV + 8), dict(out=far + 4), dict(out=DEV), dict(w=DEV + 2),
+               dict(out=DEV + bytes_ - 16), dict(q=DEV + bytes_ - 16, out=DEV)):
+        assert _status(_chunk, ctx, reqs, **dict(dict(out=far), **kw)) == gp.GP_ERR_INVALID
+    assert _status(_chunk, ctx, reqs, out=DEV + bytes_) == gp.GP_ERR_STATE
     assert _status(_chunk, ctx, reqs, w=None) == gp.GP_ERR_STATE
-    for kw in (dict(q=None), dict(out=None), dict(w=None), dict(tokens=(0, -1, 0)), dict(tokens=(0, 513, 0)),
+    for kw in (dict(q=None), dict(out=None), dict(w=None), dict(w=DEV + 1), dict(tokens=(0, -1, 0)), dict(tokens=(0, 513, 0)),
                dict(layer=2), dict(layer=-1)):
         assert _status(_decode, ctx, reqs, **kw) == gp.GP_ERR_INVALID
 
 
 def test_evict_lengths(eng):
     ctx, reqs = eng
-    for kw in (dict(w=None), dict(tokens=(0, -1, 0)), dict(tokens=(0, 0, 513)), dict(keep=(0, 1, 1)),
+    for kw in (dict(w=None), dict(w=DEV + 2), dict(tokens=(0, -1, 0)), dict(tokens=(0, 0, 513)), dict(keep=(0, 1, 1)),
                dict(keep=(-5, 1, 1))):
         assert _status(_evict, ctx, reqs, **kw) == gp.GP_ERR_INVALID
     assert _status(_evict, ctx, reqs, (1, 2), (1, 2)) == gp.GP_ERR_INVALID
