@@ -31,9 +31,23 @@
 // L_r = m_r + log2 l_r of every row (rounded to fp32 once, as the logit is), so S
 // is formed again, transposed: S^T = K Q^T, so that a thread (TMEM lane) owns
 // a key and adds up half of its columns in registers: no atomics, one writer a
-// weight.  An item is a page (two key tiles) against a range of query tiles,
-// S^T double buffered, K tiles kept and the next item's loaded meanwhile.  L
-// of a query tile goes through shared memory (warp 3).
+// weight.  -L / c joins S^T as one more K = 16 step, ones times its three bf16
+// parts (24 bits): read from shared memory by every thread instead, it took
+// four times its bytes of the bandwidth that the products need there (291 us
+// against 272 for 6007 tokens behind 4099, 32 heads, d = 128).  An item is a
+// page (two key tiles) against a range of query tiles, S^T double buffered, K
+// tiles kept and the next item's loaded meanwhile.
+//   warp 0       producer;  warps 1, 2  MMA issuers, one a key tile
+//   warp 3       L of the query tiles;  warps 4-19  sums
+//
+// Measured (bf16, d = 128, 32 query and 8 KV heads): those 6007 tokens take 520
+// us of attention (1340 TFLOP/s of its 4 d flops a pair, 70 % of the measured
+// bf16 rate) and 272 us of weights; 106 drafted tokens of 16 requests over
+// 85 831 cached ones 72 and 34 us, where reading K and V once takes 52 us and K
+// again 26.  What bounds the attention is the chain S - softmax - O of a group
+// (about 3200 clocks for two tiles of 1024 clocks of products each); tried and
+// slower: two threads a row (583 us), an issuer a group (554 us), weights under
+// the old maximum while the new one is found (562 us).
 //
 // Every wait is bounded: on expiry the CTA records ERR_TIMEOUT, raises an
 // abort flag that ends every role's loop, waits (bounded) for its copies and
@@ -84,6 +98,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "=l"(reinterpret_cast<uint64_t&>(d))
       : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
         "l"(reinterpret_cast<const uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
   return d;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -743,11 +764,13 @@ template <int D>
 struct SmW {
   static constexpr int TILE = TK * D * 2;
   static constexpr int HALF = TK * 128;
-  static constexpr int NQ = D == 128 ? 3 : 6;          // query tiles in flight
+  static constexpr int NQ = D == 128 ? 2 : 6;          // query tiles in flight
+  static constexpr int ROW16 = 128 * 32;               // an operand of 128 rows of 16
   static constexpr size_t K = 0;                       // two pages, two tiles each
   static constexpr size_t Q = 4 * (size_t)TILE;
-  static constexpr size_t STAT = Q + (size_t)NQ * TILE;  // float [2][128], negated
-  static constexpr size_t HALVES = STAT + 2 * 128 * 4;   // float [2][128]
+  static constexpr size_t ONES = Q + (size_t)NQ * TILE;
+  static constexpr size_t LSE = ONES + ROW16;          // [2]
+  static constexpr size_t HALVES = LSE + 2 * ROW16;    // float [2][128]
   static constexpr size_t BARS = HALVES + 2 * 128 * 4;
   // k_full[2], k_empty[2], q_full[NQ], q_empty[NQ], t_full[2], t_empty[2], s_ready[2][2], s_free[2][2], mma_done[2]
   static constexpr int NBARS = 8 + 2 * NQ + 8 + 2;
@@ -755,6 +778,14 @@ struct SmW {
   static constexpr size_t BYTES = MISC + 64;           // the base is aligned to 1 KiB by its declaration
   static_assert(BYTES <= 232448, "227 KiB a CTA");
 };
+
+// An operand of 128 rows of 16 without swizzle: 8 x 16-byte blocks, the two of a
+// row's halves 128 bytes apart, the next eight rows 256.
+__device__ __forceinline__ int row16(int row) { return (row >> 3) * 256 + (row & 7) * 16; }
+__device__ __forceinline__ uint64_t row16_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(256 >> 4) << 32) |
+         ((uint64_t)1 << 46);
+}
 
 template <int D, int G>
 __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_constant__ ChunkTcArgs a) {
@@ -789,7 +820,7 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
   if (tid == 0) {
     for (int i = 0; i < L::NBARS; ++i) {
       int n = i == 2 || i == 3 || (i >= 4 + NQ && i < 4 + 2 * NQ) ? 2 : 1;  // k_empty, q_empty: both issuers
-      if (i >= 6 + 2 * NQ && i < 8 + 2 * NQ) n = 16;   // t_empty: all groups' warps
+      if (i >= 6 + 2 * NQ && i < 8 + 2 * NQ) n = 2;    // t_empty: both issuers
       if (i >= 12 + 2 * NQ && i < 16 + 2 * NQ) n = 8;  // s_free: the warps of a key tile
       mbar_init(bar(i), (uint32_t)n);
     }
@@ -798,6 +829,14 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
     fail[0] = 0;
     fail[1] = 0;
   }
+  // the constant parts of the operands that carry L (see ROW16's layout below)
+  for (int row = tid; row < 128; row += WNT) {
+    unsigned char* at = sm + row16(row);
+    *reinterpret_cast<uint4*>(at + L::ONES) = make_uint4(0x3f803f80u, 0x00003f80u, 0u, 0u);  // 1, 1, 1, 0, ...
+    *reinterpret_cast<uint4*>(at + L::ONES + 128) = make_uint4(0u, 0u, 0u, 0u);
+    for (int b = 0; b < 2; ++b) *reinterpret_cast<uint4*>(at + L::LSE + b * L::ROW16 + 128) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      static_cast<uint32_t>(__cvta_generic_to_shared(tmem_holder))),
@@ -873,11 +912,16 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
           if (!ok) break;
           tc_fence_after();
           const uint64_t q0 = sw128_desc(sb + (uint32_t)(L::Q + (size_t)s * L::TILE));
+          wait(t_full(z), c / 2);
+          if (!ok) break;
 #pragma unroll
           for (int e = 0; e < D / 16; ++e) {
             const uint64_t off = (uint64_t)(((e >> 2) * L::HALF + (e & 3) * 32) >> 4);
             mma_ss(tmem + (uint32_t)(x * 256 + z * 128), k0 + off, q0 + off, idesc(128, false), e > 0 ? 1u : 0u);
           }
+          mma_ss(tmem + (uint32_t)(x * 256 + z * 128), row16_desc(sb + (uint32_t)L::ONES),
+                 row16_desc(sb + (uint32_t)(L::LSE + z * L::ROW16)), idesc(128, false), 1u);
+          commit(t_empty(z));
           commit(s_ready(x, z));
           commit(q_empty(s));
         }
@@ -890,26 +934,35 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
     wait_bar(mma_done(x), 0u, &zero);
     __syncwarp();
   } else if (warp == 3) {
-    // ---- statistics of the query tiles -------------------------------------------
+    // ---- -L / c of the query tiles, in three bf16 parts ---------------------------
+    const float inv_sc = sqrtf((float)D) / 1.4426950408889634f;
     int c = 0;
     bool ok = true;
     for (int i = i0; i < i1 && ok; ++i) {
       const WeightItem it = load_item(a.witems + i);
       const ChunkReq rq = load_req(a.reqs + it.r);
       for (int pg = 0; pg < it.pages && ok; ++pg)
-       for (int q = it.qb; q < it.qe; ++q, ++c) {
-        const int b = c & 1;
-        if (c >= 2) ok = __all_sync(0xffffffffu, wait_bar(t_empty(b), (uint32_t)((c / 2 - 1) & 1), abort));
-        if (!ok) break;
-        float* dst = reinterpret_cast<float*>(sm + L::STAT) + b * 128;
+        for (int q = it.qb; q < it.qe; ++q, ++c) {
+          const int b = c & 1;
+          float v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = 32 * k + lane, t = q * TOK + row / G;
-          dst[row] = t < rq.nnew ? -__ldg(a.lse + (size_t)(rq.row0 + t) * a.Hq + it.h * G + row % G) : 0.f;
+          for (int k = 0; k < 4; ++k) {
+            const int row = 32 * k + lane, t = q * TOK + row / G;
+            v[k] = t < rq.nnew ? -inv_sc * __ldg(a.lse + (size_t)(rq.row0 + t) * a.Hq + it.h * G + row % G) : 0.f;
+          }
+          if (c >= 2) ok = __all_sync(0xffffffffu, wait_bar(t_empty(b), (uint32_t)((c / 2 - 1) & 1), abort));
+          if (!ok) break;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float h1 = __bfloat162float(__float2bfloat16_rn(v[k]));
+            const float h2 = __bfloat162float(__float2bfloat16_rn(v[k] - h1));
+            *reinterpret_cast<uint4*>(sm + L::LSE + b * L::ROW16 + row16(32 * k + lane)) =
+                make_uint4(pack_bf16(h1, h2), pack_bf16(v[k] - h1 - h2, 0.f), 0u, 0u);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(t_full(b));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(t_full(b));
-      }
     }
     if (!ok && lane == 0) timed_out();
   } else if (warp >= 4) {
@@ -933,8 +986,7 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
       float2 w[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       for (int q = it.qb; q < it.qe; ++q, ++c) {
         const int z = c & 1;
-        ok = __all_sync(0xffffffffu, wait_bar(t_full(z), (uint32_t)((c / 2) & 1), abort)) &&
-             __all_sync(0xffffffffu, wait_bar(s_ready(x, z), (uint32_t)((c / 2) & 1), abort));
+        ok = __all_sync(0xffffffffu, wait_bar(s_ready(x, z), (uint32_t)((c / 2) & 1), abort));
         if (!ok) break;
         tc_fence_after();
         // of this half's columns lo .. hi - 1 count: rows of tokens that see the slot and exist
@@ -944,7 +996,6 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             tmem_load32(tmem + lanes + (uint32_t)(x * 256 + z * 128 + half * 64 + h * 32), r[h]);
-          const float4* st = reinterpret_cast<const float4*>(sm + L::STAT) + z * 32 + half * 16;
           tmem_wait_ld();
 #pragma unroll
           for (int h = 0; h < 2; ++h) tmem_arrived(r[h]);
@@ -959,11 +1010,8 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float4 nm = st[8 * h + e];
-              float2 u = fma2(make_float2(__uint_as_float(r[h][4 * e]), __uint_as_float(r[h][4 * e + 1])), sc2,
-                              make_float2(nm.x, nm.y));
-              float2 v = fma2(make_float2(__uint_as_float(r[h][4 * e + 2]), __uint_as_float(r[h][4 * e + 3])), sc2,
-                              make_float2(nm.z, nm.w));
+              float2 u = mul2(make_float2(__uint_as_float(r[h][4 * e]), __uint_as_float(r[h][4 * e + 1])), sc2);
+              float2 v = mul2(make_float2(__uint_as_float(r[h][4 * e + 2]), __uint_as_float(r[h][4 * e + 3])), sc2);
               u.x = ex2f(u.x);
               u.y = ex2f(u.y);
               v.x = ex2f(v.x);
@@ -976,7 +1024,6 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(s_free(x, z));
-          mbar_arrive(t_empty(z));
         }
       }
       // the two halves of a key's sum meet (both groups of threads come here,
