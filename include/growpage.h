@@ -395,11 +395,11 @@ gp_status gp_decode_attention(gp_ctx* ctx, int32_t layer, int32_t n, const gp_re
  * The calls share these rules.  Requests need a bound slot, listed once per
  * call.  Arguments are checked before anything happens (GP_ERR_INVALID,
  * nothing changed).  The device current at gp_create must be current
- * (GP_ERR_INVALID), and the engine stream must not be capturing a graph
- * (GP_ERR_UNSUPPORTED: a replay would not see a later call's tables and
+ * (GP_ERR_INVALID), and neither the engine stream nor the compaction stream may
+ * be capturing a graph (GP_ERR_UNSUPPORTED: a replay would not see a later call's tables and
  * lengths).  They run on the engine stream, asynchronously, and wait there
  * for a pending side-stream compaction only if a request holds one of its
- * pages.  Two contexts share no scratch and may run at the same time.
+ * pages or a slot whose weights it moves.  Two contexts share no scratch and may run at the same time.
  *
  * gp_append_tokens: new tokens of one layer into the cache.  Request r appends
  * num_new[r] >= 0 tokens after its num_cached[r] >= 0 cached ones; the rows of

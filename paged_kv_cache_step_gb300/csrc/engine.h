@@ -125,6 +125,7 @@ struct gp_ctx {
   cudaEvent_t ev_ready = nullptr, ev_done = nullptr;
   bool compaction_pending = false;
   std::unordered_set<int32_t> pending_pages;  // old and new pages of the pending compaction
+  std::unordered_set<int32_t> pending_slots;  // slots whose accumulated weights it moves
 
   std::vector<gp::DemandRec> last_demand;
   std::vector<gp::CompressRec> last_compress;
@@ -266,6 +267,7 @@ inline gp_status join_compaction(gp_ctx* c) {
     GP_CUDA(c, cudaEventSynchronize(c->ev_done));
     c->compaction_pending = false;
     c->pending_pages.clear();
+    c->pending_slots.clear();
   }
   return GP_OK;
 }
@@ -286,10 +288,12 @@ inline gp_status ready_call(gp_ctx* c) {
   GP_CUDA(c, cudaGetDevice(&dev));
   if (dev != c->device)
     return fail(c, GP_ERR_INVALID, "device %d is current, the engine was created on device %d", dev, c->device);
-  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  GP_CUDA(c, cudaStreamIsCapturing(c->stream, &cap));
-  if (cap != cudaStreamCaptureStatusNone)
-    return fail(c, GP_ERR_UNSUPPORTED, "the engine stream is being captured: the call reads host data at every launch");
+  for (cudaStream_t s : {c->stream, c->cstream ? c->cstream : c->stream}) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    GP_CUDA(c, cudaStreamIsCapturing(s, &cap));
+    if (cap != cudaStreamCaptureStatusNone)
+      return fail(c, GP_ERR_UNSUPPORTED, "a stream of the engine is being captured: the call reads host data at every launch");
+  }
   return GP_OK;
 }
 
@@ -320,15 +324,16 @@ inline gp_status staging_upload(gp_ctx* c, StagingSlot& s, size_t bytes) {
 }
 
 // The engine stream waits for a compaction pending on the side stream if a
-// request holds a page it reads or writes (App. E.3).
-inline gp_status wait_shared_pages(gp_ctx* c, int n, const gp_request* reqs) {
+// request holds a page it reads or writes (App. E.3), or a slot whose weights it
+// moves: the slot of a finished request may be another's by now, on other pages.
+inline gp_status wait_pending(gp_ctx* c, int n, const gp_request* reqs) {
   if (!c->compaction_pending) return GP_OK;
-  for (int r = 0; r < n; ++r)
-    for (int j = 0; j < reqs[r].num_pages; ++j)
-      if (c->pending_pages.count(reqs[r].block_table[j])) {
-        GP_CUDA(c, cudaStreamWaitEvent(c->stream, c->ev_done, 0));
-        return GP_OK;
-      }
+  bool shared = false;
+  for (int r = 0; r < n && !shared; ++r) {
+    shared = c->pending_slots.count(reqs[r].slot) != 0;
+    for (int j = 0; j < reqs[r].num_pages && !shared; ++j) shared = c->pending_pages.count(reqs[r].block_table[j]) != 0;
+  }
+  if (shared) GP_CUDA(c, cudaStreamWaitEvent(c->stream, c->ev_done, 0));
   return GP_OK;
 }
 

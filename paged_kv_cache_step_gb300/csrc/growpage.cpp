@@ -1238,18 +1238,13 @@ gp_status decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_request
   // compaction reads or writes.  The call uploads its descriptors to a staging
   // slot, so neither the compaction nor the speculative selection, which
   // read the engine's upload buffer, is disturbed.
-  bool overlap = false;
-  if (c->compaction_pending)
-    for (int r = 0; r < n && !overlap; ++r)
-      for (int j = 0; j < reqs[r].num_pages && !overlap; ++j)
-        overlap = c->pending_pages.count(reqs[r].block_table[j]) != 0;
   const int G = g.num_q_heads / g.num_kv_heads;
   // The tensor-core kernel takes bf16 caches with d = 128 and G = 2 or 4
   // (AUTO and TENSOR_CORE); the CUDA-core kernel everything else.
   const bool tc = c->attn_tc_ok && c->scan_kernel != GP_SCAN_CUDA_CORE && gp::attention_tc_shape(g.head_dim, G);
   if (c->scan_kernel == GP_SCAN_TENSOR_CORE && !tc)
     return fail(c, GP_ERR_UNSUPPORTED, "the tensor-core attention kernel cannot take this cache or shape");
-  if (overlap) GP_CUDA(c, cudaStreamWaitEvent(c->stream, c->ev_done, 0));
+  if ((st = wait_pending(c, n, reqs)) != GP_OK) return st;
   // the accumulated weights: where each request's logits start
   std::vector<gp::WeightReq> wreqs(weights ? n : 0);
   std::vector<int64_t> logit_off(weights ? n : 0);

@@ -347,7 +347,7 @@ gp_status gp_append_tokens(gp_ctx* c, int32_t layer, int32_t n, const gp_request
     }
   }
   if ((st = ready_call(c)) != GP_OK) return st;
-  if ((st = wait_shared_pages(c, n, reqs)) != GP_OK) return st;
+  if ((st = wait_pending(c, n, reqs)) != GP_OK) return st;
   AppendArgs a{};
   AppendReq* hr = a.few;
   int32_t* hb = a.few_bt;
@@ -422,7 +422,7 @@ gp_status gp_chunk_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_reque
                   chunk_tc_shape(g.head_dim, G) && rows < (1ll << 31) - 256;
   if (c->scan_kernel == GP_SCAN_TENSOR_CORE && !tc)
     return fail(c, GP_ERR_UNSUPPORTED, "the tensor-core chunk kernels cannot take this cache, shape or query type");
-  if ((st = wait_shared_pages(c, n, reqs)) != GP_OK) return st;
+  if ((st = wait_pending(c, n, reqs)) != GP_OK) return st;
   const int maxp = g.max_pages_per_req;
   ChunkPlan plan;
   TilePlan tiles;
@@ -667,11 +667,14 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
     GP_CUDA(c, cudaEventRecord(c->ev_done, ks));
     c->compaction_pending = true;
     c->pending_pages.clear();
-    for (int r = 0; r < n; ++r)
+    c->pending_slots.clear();
+    for (int r = 0; r < n; ++r) {
+      c->pending_slots.insert(reqs[r].slot);
       for (int j = 0; j < reqs[r].num_pages; ++j) {
         c->pending_pages.insert(old_bt[(size_t)r * maxp + j]);
         c->pending_pages.insert(new_bt[(size_t)r * maxp + j]);
       }
+    }
   }
   c->last_compress.assign(n, CompressRec{});
   for (int r = 0; r < n; ++r) {

@@ -538,6 +538,35 @@ def test_evict_copies_shared_pages(side):
         e.close()
 
 
+def test_a_slot_taken_again_while_its_eviction_is_pending():
+    """A request is finished while its eviction waits on the side stream; its slot
+    goes to another, on a page that the eviction does not touch.  The new one's
+    append clears the slot's weights after the eviction has moved them."""
+    e = Engine([4], spare=1, seed=26, L=1)
+    side = torch.cuda.Stream()
+    try:
+        e.fill([900])
+        gp.gp_set_compaction_stream(e.ctx, side)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)  # the eviction starts well after the append has been issued
+        gp.gp_evict_weighted(e.ctx, e.reqs, [900], [300], e.w)
+        old = e.reqs[0]
+        gp.gp_slot_release(e.ctx, old.slot)
+        slot, page = gp.gp_slot_acquire(e.ctx), gp.gp_page_alloc(e.ctx)
+        assert slot == old.slot and page not in old.pages
+        k = e.randn(200, 2, 128).bfloat16()
+        new = gp.Request(slot, np.array([page]), 0, 4)
+        gp.gp_append_tokens(e.ctx, 0, [new], [0], [200], None, k, k, None, e.w)
+        gp.gp_wait_compaction(e.ctx)
+        gp.gp_synchronize(e.ctx)
+        torch.cuda.synchronize()
+        assert not e.w[0, slot, :, :200].any() and bool((e.w[0, slot, :, 200:300] > 0).all())
+    finally:
+        gp.gp_set_compaction_stream(e.ctx, None)
+        e.close()
+
+
 def test_evict_without_pages_or_launch_changes_nothing():
     tokens, keep = [900, 1000], [300, 700]
     e = Engine([4, 4], spare=2, seed=24, L=1)
@@ -709,6 +738,31 @@ def test_refused_while_the_stream_is_captured():
             call()
         gp.gp_synchronize(e.ctx)
     finally:
+        e.close()
+
+
+def test_eviction_refused_while_the_side_stream_is_captured():
+    side = torch.cuda.Stream()
+    e = Engine([2], L=1, seed=43)
+    try:
+        e.fill([300])
+        gp.gp_set_compaction_stream(e.ctx, side)
+        x, w0 = torch.ones(8, device="cuda"), e.w.clone()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side, capture_error_mode="relaxed"):
+            x.mul_(2)
+            with pytest.raises(gp.GrowPageError) as err:
+                gp.gp_evict_weighted(e.ctx, e.reqs, [300], [100], e.w)
+        assert err.value.status == gp.GP_ERR_UNSUPPORTED
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bits(e.w), bits(w0)) and x[0] == 2
+        gp.gp_evict_weighted(e.ctx, e.reqs, [300], [100], e.w)  # and the context works on
+        gp.gp_wait_compaction(e.ctx)
+        gp.gp_synchronize(e.ctx)
+    finally:
+        gp.gp_set_compaction_stream(e.ctx, None)
         e.close()
 
 
