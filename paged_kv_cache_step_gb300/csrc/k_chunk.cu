@@ -18,13 +18,19 @@
 //              tiles that see it: a weight has one writer, and the sum's order
 //              is fixed.
 // Few tiles are cut into several items each, over the keys (weights: over the
-// query tiles), for about four a SM; their partials are joined by a kernel more.
-// Bounded by the fp32 pipe: 2 d (2 + 1) flops a (row, key) pair.
+// query tiles), to fill the SMs; their partials are joined by a kernel more.
+// Bounded by the fp32 pipe: 2 d (2 + 1) flops a (row, key) pair.  The next K, V
+// or query tile is on its way, in registers, while one is at work, and the FMAs
+// are issued two at a time: 8000 tokens, 32 query and 8 KV heads, d = 128, fp32
+// take 12.5 ms of attention (42 TFLOP/s) and 6.6 ms of weights (8.0 ms without),
+// two requests of 1000 tokens behind 300, 16 and 8 heads, d = 64, 229 and 131 us
+// (317 and 146).
 #include <cuda_bf16.h>
 
 #include <cstdint>
 
 #include "chained.cuh"
+#include "math2.cuh"
 #include "weighted_kernels.h"
 
 namespace gp {
@@ -35,12 +41,6 @@ constexpr int PAGE = 256;
 constexpr int BR = CHUNK_ROWS, BK = CHUNK_KEYS;
 constexpr float NEG = -1.0e30f;
 static_assert(BR == 64 && BK == 64 && PAGE % BK == 0, "4 x 4 outputs a thread");
-
-__device__ __forceinline__ float ex2f(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 template <int D>
 struct Smem {
@@ -62,71 +62,90 @@ __device__ __forceinline__ float4 load4(const void* base, size_t elt) {
   }
 }
 
+// A thread's pieces of 64 rows of queries, K or V: fetched while the tile before
+// is at work, put into shared memory when that is done.
+template <int D>
+struct Pieces {
+  static constexpr int N = 64 * D / 4 / NT;
+  float4 x[N];
+  static __device__ __forceinline__ int row(int i) { return (threadIdx.x + i * NT) / (D / 4); }
+  static __device__ __forceinline__ int col(int i) { return (threadIdx.x + i * NT) % (D / 4) * 4; }
+  __device__ __forceinline__ void put(float (*dst)[D + 4]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<float4*>(&dst[row(i)][col(i)]) = x[i];
+  }
+};
+
 // 64 query rows from token t0, scaled to base 2; rows past the request are 0.
 template <int D>
-__device__ __forceinline__ void load_rows(const ChunkArgs& a, const ChunkReq& rq, int h, int t0, Smem<D>& sm) {
+__device__ __forceinline__ void fetch_rows(const ChunkArgs& a, const ChunkReq& rq, int h, int t0, Pieces<D>& to) {
   const float sc = 1.4426950408889634f / sqrtf((float)D);
-  for (int e = threadIdx.x; e < BR * D / 4; e += NT) {
-    const int row = e / (D / 4), d = e % (D / 4) * 4;
-    const int t = t0 + row / a.G;
+#pragma unroll
+  for (int i = 0; i < Pieces<D>::N; ++i) {
+    const int row = Pieces<D>::row(i), t = t0 + row / a.G;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (t < rq.nnew) {
-      const size_t at = ((size_t)(rq.row0 + t) * a.Hq + h * a.G + row % a.G) * D + d;
+      const size_t at = ((size_t)(rq.row0 + t) * a.Hq + h * a.G + row % a.G) * D + Pieces<D>::col(i);
       x = a.q_f32 ? load4<true>(a.q, at) : load4<false>(a.q, at);
     }
-    *reinterpret_cast<float4*>(&sm.q[row][d]) = make_float4(sc * x.x, sc * x.y, sc * x.z, sc * x.w);
+    to.x[i] = make_float4(sc * x.x, sc * x.y, sc * x.z, sc * x.w);
   }
 }
 
 // 64 rows of K or V from logical slot s0; rows from `total` on are 0.
 template <int D>
-__device__ __forceinline__ void load_keys(const ChunkArgs& a, const ChunkReq& rq, const void* cache, int h, int s0,
-                                          int total, Smem<D>& sm) {
+__device__ __forceinline__ void fetch_keys(const ChunkArgs& a, const ChunkReq& rq, const void* cache, int h, int s0,
+                                           int total, Pieces<D>& to) {
   int page = a.bt[rq.bt_off + s0 / PAGE];
   if (page < 0 || page >= a.num_pages_total) {
     if (threadIdx.x == 0) atomicOr(a.err, ERR_BAD_PAGE);
     page = 0;
   }
   const size_t base = ((((size_t)a.layer * a.num_pages_total + page) * a.Hkv + h) * PAGE + s0 % PAGE) * D;
-  for (int e = threadIdx.x; e < BK * D / 4; e += NT) {
-    const int row = e / (D / 4), d = e % (D / 4) * 4;
+#pragma unroll
+  for (int i = 0; i < Pieces<D>::N; ++i) {
+    const int row = Pieces<D>::row(i);
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (s0 + row < total) {
-      const size_t at = base + (size_t)row * D + d;
+      const size_t at = base + (size_t)row * D + Pieces<D>::col(i);
       x = a.kv_f32 ? load4<true>(cache, at) : load4<false>(cache, at);
     }
-    *reinterpret_cast<float4*>(&sm.kv[row][d]) = x;
+    to.x[i] = x;
   }
 }
 
-// s[i][j] = q row 4 ty + i . key tx + 16 j
+// s[i][j] = q row 4 ty + i . key tx + 16 j: the even and the odd products apart,
+// two a step
 template <int D>
 __device__ __forceinline__ void scores(const Smem<D>& sm, int ty, int tx, float s[4][4]) {
+  float2 z[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) z[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
   for (int d = 0; d < D; d += 4) {
-    float4 q[4], k[4];
+    float4 q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(&sm.q[4 * ty + i][d]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4*>(&sm.kv[tx + 16 * j][d]);
+    for (int j = 0; j < 4; ++j) {
+      const float4 k = *reinterpret_cast<const float4*>(&sm.kv[tx + 16 * j][d]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[i][j] = fmaf(q[i].x, k[j].x, s[i][j]);
-        s[i][j] = fmaf(q[i].y, k[j].y, s[i][j]);
-        s[i][j] = fmaf(q[i].z, k[j].z, s[i][j]);
-        s[i][j] = fmaf(q[i].w, k[j].w, s[i][j]);
+      for (int i = 0; i < 4; ++i) {
+        z[i][j] = fma2(make_float2(q[i].x, q[i].y), make_float2(k.x, k.y), z[i][j]);
+        z[i][j] = fma2(make_float2(q[i].z, q[i].w), make_float2(k.z, k.w), z[i][j]);
       }
+    }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = z[i][j].x + z[i][j].y;
 }
 
 template <int D>
-__global__ void __launch_bounds__(NT) k_chunk(const __grid_constant__ ChunkArgs a) {
+__global__ void __launch_bounds__(NT, 2) k_chunk(const __grid_constant__ ChunkArgs a) {
   extern __shared__ __align__(16) unsigned char raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   constexpr int DC = D / 64;  // float4 columns of the output a thread owns
@@ -138,22 +157,24 @@ __global__ void __launch_bounds__(NT) k_chunk(const __grid_constant__ ChunkArgs 
   const int tokens = BR / a.G;
   const int last = min(tile.first + tokens, rq.nnew) - 1;  // last token of the tile
   const int end = min(rq.cached + last + 1, tile.to * BK);  // slots it sees, of this item
-  load_rows<D>(a, rq, tile.h, tile.first, sm);
+  Pieces<D> next, rows;
+  fetch_keys<D>(a, rq, a.k_cache, tile.h, tile.from * BK, total, next);
+  fetch_rows<D>(a, rq, tile.h, tile.first, rows);
+  rows.put(sm.q);
   if (tid < BR) {
     sm.m[tid] = NEG;
     sm.l[tid] = 0.f;
   }
-  float acc[4][DC][4];
+  float2 acc[4][DC][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int c = 0; c < DC; ++c)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) acc[i][c][x] = 0.f;
+    for (int c = 0; c < DC; ++c) acc[i][c][0] = acc[i][c][1] = make_float2(0.f, 0.f);
   for (int s0 = tile.from * BK; s0 < end; s0 += BK) {
     __syncthreads();  // the last tile's V and P are used
-    load_keys<D>(a, rq, a.k_cache, tile.h, s0, total, sm);
+    next.put(sm.kv);
     __syncthreads();
+    fetch_keys<D>(a, rq, a.v_cache, tile.h, s0, total, next);
     float s[4][4];
     scores<D>(sm, ty, tx, s);
 #pragma unroll
@@ -187,32 +208,39 @@ __global__ void __launch_bounds__(NT) k_chunk(const __grid_constant__ ChunkArgs 
       }
     }
     __syncthreads();  // K is used, P and the factors are written
-    load_keys<D>(a, rq, a.v_cache, tile.h, s0, total, sm);
+    next.put(sm.kv);
     __syncthreads();
+    if (s0 + BK < end) fetch_keys<D>(a, rq, a.k_cache, tile.h, s0 + BK, total, next);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float f = sm.f[4 * ty + i];
 #pragma unroll
       for (int c = 0; c < DC; ++c)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) acc[i][c][x] *= f;
+        for (int x = 0; x < 2; ++x) acc[i][c][x] = mul2(acc[i][c][x], make_float2(f, f));
     }
-#pragma unroll 4
-    for (int k = 0; k < BK; ++k) {
-      float p[4];
+    // four keys' weights a load: one at a time the reads of P alone took as long
+    // as the FMAs
+#pragma unroll 2
+    for (int k = 0; k < BK; k += 4) {
+      float p[4][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = sm.p[4 * ty + i][k];
-#pragma unroll
-      for (int c = 0; c < DC; ++c) {
-        const float4 v = *reinterpret_cast<const float4*>(&sm.kv[k][64 * c + 4 * tx]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[i][c][0] = fmaf(p[i], v.x, acc[i][c][0]);
-          acc[i][c][1] = fmaf(p[i], v.y, acc[i][c][1]);
-          acc[i][c][2] = fmaf(p[i], v.z, acc[i][c][2]);
-          acc[i][c][3] = fmaf(p[i], v.w, acc[i][c][3]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float4 x = *reinterpret_cast<const float4*>(&sm.p[4 * ty + i][k]);
+        p[i][0] = x.x; p[i][1] = x.y; p[i][2] = x.z; p[i][3] = x.w;
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int c = 0; c < DC; ++c) {
+          const float4 v = *reinterpret_cast<const float4*>(&sm.kv[k + e][64 * c + 4 * tx]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 w = make_float2(p[i][e], p[i][e]);
+            acc[i][c][0] = fma2(w, make_float2(v.x, v.y), acc[i][c][0]);
+            acc[i][c][1] = fma2(w, make_float2(v.z, v.w), acc[i][c][1]);
+          }
+        }
     }
   }
   __syncthreads();
@@ -225,7 +253,7 @@ __global__ void __launch_bounds__(NT) k_chunk(const __grid_constant__ ChunkArgs 
 #pragma unroll
       for (int c = 0; c < DC; ++c)
         *reinterpret_cast<float4*>(po + (size_t)row * D + 64 * c + 4 * tx) =
-            make_float4(acc[i][c][0], acc[i][c][1], acc[i][c][2], acc[i][c][3]);
+            make_float4(acc[i][c][0].x, acc[i][c][0].y, acc[i][c][1].x, acc[i][c][1].y);
       if (tx == 0) {
         po[BR * D + row] = sm.m[row];
         po[BR * D + BR + row] = sm.l[row];
@@ -238,9 +266,7 @@ __global__ void __launch_bounds__(NT) k_chunk(const __grid_constant__ ChunkArgs 
     if (tx == 0 && a.stat) a.stat[at] = make_float2(sm.m[row], inv);
 #pragma unroll
     for (int c = 0; c < DC; ++c) {
-      float o[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) o[x] = acc[i][c][x] * inv;
+      const float o[4] = {acc[i][c][0].x * inv, acc[i][c][0].y * inv, acc[i][c][1].x * inv, acc[i][c][1].y * inv};
       const size_t e = at * D + 64 * c + 4 * tx;
       if (a.q_f32) {
         *reinterpret_cast<float4*>(static_cast<float*>(a.out) + e) = make_float4(o[0], o[1], o[2], o[3]);
@@ -265,19 +291,27 @@ __global__ void __launch_bounds__(NT) k_chunk_weights(const __grid_constant__ Ch
   const int tokens = BR / a.G, s0 = tile.first;
   if (rq.slot < 0 || rq.slot >= a.M) return;
   wait_for_previous();
-  load_keys<D>(a, rq, a.k_cache, tile.h, s0, total, sm);
+  Pieces<D> rows;
+  fetch_keys<D>(a, rq, a.k_cache, tile.h, s0, total, rows);
+  rows.put(sm.kv);
   float w[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int t0 = tile.from * tokens; t0 < min(tile.to * tokens, rq.nnew); t0 += tokens) {
+  const int end = min(tile.to * tokens, rq.nnew);
+  float2 st = make_float2(0.f, 0.f);
+  auto fetch = [&](int t0) {
+    fetch_rows<D>(a, rq, tile.h, t0, rows);
+    const int t = t0 + tid / a.G;
+    if (tid < BR) st = t < rq.nnew ? a.stat[(size_t)(rq.row0 + t) * a.Hq + tile.h * a.G + tid % a.G] : make_float2(0.f, 0.f);
+  };
+  fetch(tile.from * tokens);
+  for (int t0 = tile.from * tokens; t0 < end; t0 += tokens) {
     __syncthreads();  // the last tile's rows are used
-    load_rows<D>(a, rq, tile.h, t0, sm);
+    rows.put(sm.q);
     if (tid < BR) {
-      const int t = t0 + tid / a.G;
-      const float2 st = t < rq.nnew ? a.stat[(size_t)(rq.row0 + t) * a.Hq + tile.h * a.G + tid % a.G]
-                                    : make_float2(0.f, 0.f);
       sm.m[tid] = st.x;
       sm.l[tid] = st.y;
     }
     __syncthreads();
+    if (t0 + tokens < end) fetch(t0 + tokens);
     float s[4][4];
     scores<D>(sm, ty, tx, s);
 #pragma unroll

@@ -13,18 +13,13 @@
 #include <cstdint>
 
 #include "chained.cuh"
+#include "math2.cuh"
 #include "weighted_kernels.h"
 
 namespace gp {
 namespace {
 
 constexpr int PAGE = 256;
-
-__device__ __forceinline__ float ex2f(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 constexpr int NT = 256;
 constexpr int SPAN = 128;  // tokens of a warp

@@ -272,17 +272,31 @@ struct TilePlan {
 };
 
 // Query tiles (weights: key tiles), those with most work first, each cut into
-// equal items of at most `most` key tiles (query tiles): a quarter of an SM's
-// share, so that about four items run beside each other on it, and two at
-// least.  Two requests of about 500 tokens, two KV heads, d = 64, fp32: attention
-// 110 us and weights 66 us uncut, 51 and 24 us cut.
+// equal items of at most `most` key tiles (query tiles).  Two CTAs fit on an SM;
+// `most` is between a half and a whole of what a place of these has to do, where
+// the rounds over all places cost least, an item counting 1.5 tiles more for its
+// start and end.  Two requests of about 500 tokens, two KV heads, d = 64, fp32:
+// attention 110 us and weights 66 us uncut, 42 and 23 us cut.
 void plan_tiles(int n, const int32_t* cached, const int32_t* fresh, int Hkv, int G, int sms, bool weights, TilePlan* p) {
   const int tok = CHUNK_ROWS / G;
   std::vector<ChunkTile> whole;
   auto cut = [&](std::vector<ChunkTile>& tiles, std::vector<ChunkTileJoin>& joins, int& parts) {
     int64_t total = 0;
     for (const ChunkTile& t : whole) total += t.to - t.from;
-    const int most = (int)std::max<int64_t>(2, (total + 4 * sms - 1) / (4 * sms));
+    const int64_t places = 2 * (int64_t)sms;
+    int most = 0;
+    double least = 0.;
+    const int64_t half = std::max<int64_t>(1, (total + 2 * places - 1) / (2 * places));
+    const int64_t full = std::max<int64_t>(1, (total + places - 1) / places);
+    for (int64_t m = half; m <= full; m += std::max<int64_t>(1, (full - half) / 12)) {  // some thirteen tries
+      int64_t items = 0;
+      for (const ChunkTile& t : whole) items += (t.to - t.from + m - 1) / m;
+      const double cost = (double)((items + places - 1) / places) * (m + 1.5);
+      if (most == 0 || cost < least) {
+        most = (int)m;
+        least = cost;
+      }
+    }
     for (ChunkTile t : whole) {
       const int from = t.from, len = t.to - t.from, count = (len + most - 1) / most;
       if (count > 1) joins.push_back({t.r, t.h, t.first, parts, count, {}});
