@@ -322,174 +322,174 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
 
   // 128 x 88 + 256 x 208 registers = the 384 x 168 of the launch
   if (warp < 4) {
-  registers_down<88>();
-  if (warp == 0) {
-    // ---- producer ----------------------------------------------------------
-    if (lane == 0) {
-      int c = 0, nq = 0;  // tiles and items issued
-      bool ok = true;
-      for (int i = i0; i < i1 && ok; ++i) {
-        const ChunkItem it = load_item(items + i);
-        const ChunkReq rq = load_req(a.reqs + it.r);
-        const Work w = work_of<G, KEYS>(it, rq);
-        auto tile = [&](const CUtensorMap* map, int t) {
-          if (!ok) return;
-          const int s = c % NST;
-          if (c >= NST && !(ok = wait_bar(empty(s), (uint32_t)((c / NST - 1) & 1), abort))) return;
-          const int y = key_row(a, rq, it.h, t);
-          const uint32_t dst = sb + (uint32_t)(L::ST + (size_t)s * L::TILE);
-          mbar_expect_tx(full(s), L::TILE);
-#pragma unroll
-          for (int x = 0; x < D; x += 64) tma_load_2d(dst + (uint32_t)(x / 64 * L::HALF), map, x, y, full(s));
-          ++c;
-        };
-        // the query tiles' place is free only when the item before has formed its
-        // last S: the first key tiles are on their way before
-        auto queries = [&] {
-          if (!ok || (nq > 0 && !(ok = wait_bar(q_empty, (uint32_t)((nq - 1) & 1), abort)))) return;
-          const int nqt = KEYS || it.alone ? 1 : 2;
-          mbar_expect_tx(q_full, (uint32_t)(nqt * L::TILE));
-          for (int x = 0; x < nqt; ++x)
-#pragma unroll
-            for (int d = 0; d < D; d += 64)
-              tma_load_3d(sb + (uint32_t)(L::Q + (size_t)x * L::TILE + d / 64 * L::HALF), &a.qmap, d, it.h * G,
-                          (int)rq.row0 + it.t0 + x * TOK, q_full);
-          ++nq;
-        };
-        if (KEYS) {
-          tile(&a.kmap, it.kb);
-          if (w.cnt[1] > 0) tile(&a.kmap, it.kb + 1);
-          for (int j = 0; j < w.cnt[0]; ++j) {
-            tile(&a.vmap, it.kb + 2 * j);
-            if (j == 0) queries();
-            if (j + 1 < w.cnt[0]) tile(&a.kmap, it.kb + 2 * j + 2);
-            if (j < w.cnt[1]) tile(&a.vmap, it.kb + 2 * j + 1);
-            if (j + 1 < w.cnt[1]) tile(&a.kmap, it.kb + 2 * j + 3);
-          }
-        } else {
-          for (int j = it.kb; j < it.ke; ++j) {
-            tile(&a.kmap, j);
-            tile(&a.vmap, j);
-            if (j == it.kb) queries();
+    registers_down<88>();
+    if (warp == 0) {
+      // ---- producer ----------------------------------------------------------
+      if (lane == 0) {
+        int c = 0, nq = 0;  // tiles and items issued
+        bool ok = true;
+        for (int i = i0; i < i1 && ok; ++i) {
+          const ChunkItem it = load_item(items + i);
+          const ChunkReq rq = load_req(a.reqs + it.r);
+          const Work w = work_of<G, KEYS>(it, rq);
+          auto tile = [&](const CUtensorMap* map, int t) {
+            if (!ok) return;
+            const int s = c % NST;
+            if (c >= NST && !(ok = wait_bar(empty(s), (uint32_t)((c / NST - 1) & 1), abort))) return;
+            const int y = key_row(a, rq, it.h, t);
+            const uint32_t dst = sb + (uint32_t)(L::ST + (size_t)s * L::TILE);
+            mbar_expect_tx(full(s), L::TILE);
+  #pragma unroll
+            for (int x = 0; x < D; x += 64) tma_load_2d(dst + (uint32_t)(x / 64 * L::HALF), map, x, y, full(s));
+            ++c;
+          };
+          // the query tiles' place is free only when the item before has formed its
+          // last S: the first key tiles are on their way before
+          auto queries = [&] {
+            if (!ok || (nq > 0 && !(ok = wait_bar(q_empty, (uint32_t)((nq - 1) & 1), abort)))) return;
+            const int nqt = KEYS || it.alone ? 1 : 2;
+            mbar_expect_tx(q_full, (uint32_t)(nqt * L::TILE));
+            for (int x = 0; x < nqt; ++x)
+  #pragma unroll
+              for (int d = 0; d < D; d += 64)
+                tma_load_3d(sb + (uint32_t)(L::Q + (size_t)x * L::TILE + d / 64 * L::HALF), &a.qmap, d, it.h * G,
+                            (int)rq.row0 + it.t0 + x * TOK, q_full);
+            ++nq;
+          };
+          if (KEYS) {
+            tile(&a.kmap, it.kb);
+            if (w.cnt[1] > 0) tile(&a.kmap, it.kb + 1);
+            for (int j = 0; j < w.cnt[0]; ++j) {
+              tile(&a.vmap, it.kb + 2 * j);
+              if (j == 0) queries();
+              if (j + 1 < w.cnt[0]) tile(&a.kmap, it.kb + 2 * j + 2);
+              if (j < w.cnt[1]) tile(&a.vmap, it.kb + 2 * j + 1);
+              if (j + 1 < w.cnt[1]) tile(&a.kmap, it.kb + 2 * j + 3);
+            }
+          } else {
+            for (int j = it.kb; j < it.ke; ++j) {
+              tile(&a.kmap, j);
+              tile(&a.vmap, j);
+              if (j == it.kb) queries();
+            }
           }
         }
+        if (!ok) timed_out();
+        // every copy issued has landed before the CTA moves on (bounded)
+        const int zero = 0;
+        for (int x = c > NST ? c - NST : 0; x < c; ++x) wait_bar(full(x % NST), (uint32_t)((x / NST) & 1), &zero);
+        if (nq > 0) wait_bar(q_full, (uint32_t)((nq - 1) & 1), &zero);
       }
-      if (!ok) timed_out();
-      // every copy issued has landed before the CTA moves on (bounded)
-      const int zero = 0;
-      for (int x = c > NST ? c - NST : 0; x < c; ++x) wait_bar(full(x % NST), (uint32_t)((x / NST) & 1), &zero);
-      if (nq > 0) wait_bar(q_full, (uint32_t)((nq - 1) & 1), &zero);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ---- MMA issuer --------------------------------------------------------------
-    int c = 0, nq = 0;      // tiles of the ring, items
-    int ns[2] = {0, 0};     // products P V per group
-    int no[2] = {0, 0};     // items per group
-    bool ok = true;
-    auto wait = [&](uint32_t bar, int phase) {
-      ok = ok && __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(phase & 1), abort));
-    };
-    auto stage = [&](int k) { return sb + (uint32_t)(L::ST + (size_t)(k % NST) * L::TILE); };
-    auto arrived = [&](int k) { wait(full(k % NST), k / NST); };
-    auto score = [&](int x, int k) {  // S of group x from the K tile k
-      arrived(k);
-      if (!ok) return;
-      tc_fence_after();
-      const uint64_t q0 = sw128_desc(sb + (uint32_t)(L::Q + (KEYS ? 0 : (size_t)x * L::TILE)));
-      const uint64_t k0 = sw128_desc(stage(k));
-#pragma unroll
-      for (int e = 0; e < D / 16; ++e) {
-        const uint64_t off = (uint64_t)(((e >> 2) * L::HALF + (e & 3) * 32) >> 4);
-        mma_ss(tmem + (uint32_t)(x * 128), q0 + off, k0 + off, idesc(TK, false), e > 0 ? 1u : 0u);
-      }
-      commit(s_ready(x));
-    };
-    // O of group x from its P and the V tile k, in two steps: the second half of
-    // P is still being computed when the first 64 keys' product starts
-    auto value = [&](int x, int k, bool first, bool last, int& n, int& items_done) {
-      arrived(k);
-      if (first && items_done > 0) wait(o_free(x), items_done - 1);
-      wait(p_half(x), n);
-      const uint64_t v0 = sw128_mn_desc(stage(k), L::HALF);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (half) wait(p_ready(x), n);
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---- MMA issuer --------------------------------------------------------------
+      int c = 0, nq = 0;      // tiles of the ring, items
+      int ns[2] = {0, 0};     // products P V per group
+      int no[2] = {0, 0};     // items per group
+      bool ok = true;
+      auto wait = [&](uint32_t bar, int phase) {
+        ok = ok && __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(phase & 1), abort));
+      };
+      auto stage = [&](int k) { return sb + (uint32_t)(L::ST + (size_t)(k % NST) * L::TILE); };
+      auto arrived = [&](int k) { wait(full(k % NST), k / NST); };
+      auto score = [&](int x, int k) {  // S of group x from the K tile k
+        arrived(k);
         if (!ok) return;
         tc_fence_after();
-#pragma unroll
-        for (int e = 4 * half; e < 4 * half + 4; ++e)
-          mma_ts(tmem + (uint32_t)(256 + x * 128), tmem + (uint32_t)(x * 128 + e * 8), v0 + (uint64_t)(e * 2048 >> 4),
-                 idesc(D, true), first && e == 0 ? 0u : 1u);
-      }
-      ++n;
-      if (last) {
-        commit(o_done(x));
-        ++items_done;
-      }
-    };
-    for (int i = i0; i < i1 && ok; ++i) {
-      const ChunkItem it = load_item(items + i);
-      Work w = work_of<G, KEYS>(it, load_req(a.reqs + it.r));
-      w.n = uniform(w.n);
-      w.cnt[0] = uniform(w.cnt[0]);
-      w.cnt[1] = uniform(w.cnt[1]);
-      wait(q_full, nq++);
-      if constexpr (KEYS) {
-        int at = c;  // every tile serves one group; used in the order of the loads
-        auto S = [&](int x, bool last) {
-          score(x, at);
+        const uint64_t q0 = sw128_desc(sb + (uint32_t)(L::Q + (KEYS ? 0 : (size_t)x * L::TILE)));
+        const uint64_t k0 = sw128_desc(stage(k));
+  #pragma unroll
+        for (int e = 0; e < D / 16; ++e) {
+          const uint64_t off = (uint64_t)(((e >> 2) * L::HALF + (e & 3) * 32) >> 4);
+          mma_ss(tmem + (uint32_t)(x * 128), q0 + off, k0 + off, idesc(TK, false), e > 0 ? 1u : 0u);
+        }
+        commit(s_ready(x));
+      };
+      // O of group x from its P and the V tile k, in two steps: the second half of
+      // P is still being computed when the first 64 keys' product starts
+      auto value = [&](int x, int k, bool first, bool last, int& n, int& items_done) {
+        arrived(k);
+        if (first && items_done > 0) wait(o_free(x), items_done - 1);
+        wait(p_half(x), n);
+        const uint64_t v0 = sw128_mn_desc(stage(k), L::HALF);
+  #pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (half) wait(p_ready(x), n);
           if (!ok) return;
-          commit(empty(at++ % NST));
-          if (last) commit(q_empty);
-        };
-        auto V = [&](int x, int j) {
-          value(x, at, j == 0, j + 1 == w.cnt[x], ns[x], no[x]);
-          if (ok) commit(empty(at++ % NST));
-        };
-        S(0, w.n == 1);
-        if (w.cnt[1] > 0 && ok) S(1, w.n == 2);
-        for (int j = 0; j < w.cnt[0] && ok; ++j) {
-          V(0, j);
-          if (j + 1 < w.cnt[0] && ok) S(0, 2 * j + 3 == w.n);
-          if (j < w.cnt[1] && ok) V(1, j);
-          if (j + 1 < w.cnt[1] && ok) S(1, 2 * j + 4 == w.n);
+          tc_fence_after();
+  #pragma unroll
+          for (int e = 4 * half; e < 4 * half + 4; ++e)
+            mma_ts(tmem + (uint32_t)(256 + x * 128), tmem + (uint32_t)(x * 128 + e * 8), v0 + (uint64_t)(e * 2048 >> 4),
+                   idesc(D, true), first && e == 0 ? 0u : 1u);
         }
-      } else {
-        // K tile j is c + 2 j, V tile j the one after it; the first group may see
-        // fewer tiles, the second have no query tile
-        const bool two = w.cnt[1] > 0;
-        if (w.cnt[0] > 0) score(0, c);
-        if (two) score(1, c);
-        if (!ok) break;
-        commit(empty(c % NST));
-        if (w.n == 1) commit(q_empty);
-        for (int j = 0; j < w.n && ok; ++j) {
-          const int kv = c + 2 * j + 1;
-          if (j < w.cnt[0]) {
-            value(0, kv, j == 0, j + 1 == w.cnt[0], ns[0], no[0]);
-            if (ok && j + 1 < w.cnt[0]) score(0, kv + 1);
+        ++n;
+        if (last) {
+          commit(o_done(x));
+          ++items_done;
+        }
+      };
+      for (int i = i0; i < i1 && ok; ++i) {
+        const ChunkItem it = load_item(items + i);
+        Work w = work_of<G, KEYS>(it, load_req(a.reqs + it.r));
+        w.n = uniform(w.n);
+        w.cnt[0] = uniform(w.cnt[0]);
+        w.cnt[1] = uniform(w.cnt[1]);
+        wait(q_full, nq++);
+        if constexpr (KEYS) {
+          int at = c;  // every tile serves one group; used in the order of the loads
+          auto S = [&](int x, bool last) {
+            score(x, at);
+            if (!ok) return;
+            commit(empty(at++ % NST));
+            if (last) commit(q_empty);
+          };
+          auto V = [&](int x, int j) {
+            value(x, at, j == 0, j + 1 == w.cnt[x], ns[x], no[x]);
+            if (ok) commit(empty(at++ % NST));
+          };
+          S(0, w.n == 1);
+          if (w.cnt[1] > 0 && ok) S(1, w.n == 2);
+          for (int j = 0; j < w.cnt[0] && ok; ++j) {
+            V(0, j);
+            if (j + 1 < w.cnt[0] && ok) S(0, 2 * j + 3 == w.n);
+            if (j < w.cnt[1] && ok) V(1, j);
+            if (j + 1 < w.cnt[1] && ok) S(1, 2 * j + 4 == w.n);
           }
-          if (two) value(1, kv, j == 0, j + 1 == w.n, ns[1], no[1]);
+        } else {
+          // K tile j is c + 2 j, V tile j the one after it; the first group may see
+          // fewer tiles, the second have no query tile
+          const bool two = w.cnt[1] > 0;
+          if (w.cnt[0] > 0) score(0, c);
+          if (two) score(1, c);
           if (!ok) break;
-          commit(empty(kv % NST));
-          if (j + 1 < w.n) {
-            if (two) score(1, kv + 1);
+          commit(empty(c % NST));
+          if (w.n == 1) commit(q_empty);
+          for (int j = 0; j < w.n && ok; ++j) {
+            const int kv = c + 2 * j + 1;
+            if (j < w.cnt[0]) {
+              value(0, kv, j == 0, j + 1 == w.cnt[0], ns[0], no[0]);
+              if (ok && j + 1 < w.cnt[0]) score(0, kv + 1);
+            }
+            if (two) value(1, kv, j == 0, j + 1 == w.n, ns[1], no[1]);
             if (!ok) break;
-            commit(empty((kv + 1) % NST));
-            if (j + 2 == w.n) commit(q_empty);
+            commit(empty(kv % NST));
+            if (j + 1 < w.n) {
+              if (two) score(1, kv + 1);
+              if (!ok) break;
+              commit(empty((kv + 1) % NST));
+              if (j + 2 == w.n) commit(q_empty);
+            }
           }
         }
+        c += 2 * w.n;
       }
-      c += 2 * w.n;
+      if (!ok && lane == 0) timed_out();
+      // every product issued has completed before TMEM is released (bounded)
+      commit(mma_done);
+      const int zero = 0;
+      wait_bar(mma_done, 0u, &zero);
+      __syncwarp();
     }
-    if (!ok && lane == 0) timed_out();
-    // every product issued has completed before TMEM is released (bounded)
-    commit(mma_done);
-    const int zero = 0;
-    wait_bar(mma_done, 0u, &zero);
-    __syncwarp();
-  }
   } else {
     registers_up<208>();
     // ---- softmax and epilogue: thread = row ------------------------------------
@@ -833,29 +833,29 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
       int c = 0, n = 0;  // query tiles and items issued
       bool ok = true;
       for (int i = i0; i < i1 && ok; ++i) {
-       const WeightItem it = load_item(a.witems + i);
-       const ChunkReq rq = load_req(a.reqs + it.r);
-       for (int pg = it.page; pg < it.page + it.pages; ++pg, ++n) {
-        const int b = n & 1;
-        if (n >= 2 && !(ok = wait_bar(k_empty(b), (uint32_t)((n / 2 - 1) & 1), abort))) break;
-        const int y = key_row(a, rq, it.h, 2 * pg);
-        mbar_expect_tx(k_full(b), 2 * L::TILE);
-        for (int x = 0; x < 2; ++x)
+        const WeightItem it = load_item(a.witems + i);
+        const ChunkReq rq = load_req(a.reqs + it.r);
+        for (int pg = it.page; pg < it.page + it.pages; ++pg, ++n) {
+          const int b = n & 1;
+          if (n >= 2 && !(ok = wait_bar(k_empty(b), (uint32_t)((n / 2 - 1) & 1), abort))) break;
+          const int y = key_row(a, rq, it.h, 2 * pg);
+          mbar_expect_tx(k_full(b), 2 * L::TILE);
+          for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int d = 0; d < D; d += 64)
-            tma_load_2d(sb + (uint32_t)(L::K + (size_t)(2 * b + x) * L::TILE + d / 64 * L::HALF), &a.kmap, d, y + x * TK,
-                        k_full(b));
-        for (int q = it.qb; q < it.qe; ++q, ++c) {
-          const int s = c % NQ;
-          if (c >= NQ && !(ok = wait_bar(q_empty(s), (uint32_t)((c / NQ - 1) & 1), abort))) break;
-          mbar_expect_tx(q_full(s), L::TILE);
+            for (int d = 0; d < D; d += 64)
+              tma_load_2d(sb + (uint32_t)(L::K + (size_t)(2 * b + x) * L::TILE + d / 64 * L::HALF), &a.kmap, d, y + x * TK,
+                          k_full(b));
+          for (int q = it.qb; q < it.qe; ++q, ++c) {
+            const int s = c % NQ;
+            if (c >= NQ && !(ok = wait_bar(q_empty(s), (uint32_t)((c / NQ - 1) & 1), abort))) break;
+            mbar_expect_tx(q_full(s), L::TILE);
 #pragma unroll
-          for (int d = 0; d < D; d += 64)
-            tma_load_3d(sb + (uint32_t)(L::Q + (size_t)s * L::TILE + d / 64 * L::HALF), &a.qmap, d, it.h * G,
-                        (int)rq.row0 + q * TOK, q_full(s));
+            for (int d = 0; d < D; d += 64)
+              tma_load_3d(sb + (uint32_t)(L::Q + (size_t)s * L::TILE + d / 64 * L::HALF), &a.qmap, d, it.h * G,
+                          (int)rq.row0 + q * TOK, q_full(s));
+          }
+          if (!ok) break;
         }
-        if (!ok) break;
-       }
       }
       if (!ok) timed_out();
       const int zero = 0;
@@ -950,69 +950,69 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
     for (int i = i0; i < i1 && ok; ++i) {
       const WeightItem it = load_item(a.witems + i);
       const ChunkReq rq = load_req(a.reqs + it.r);
-     for (int pg = it.page; pg < it.page + it.pages && ok; ++pg) {
-      const int slot_i = pg * PAGE + x * TK + key;  // this thread's logical slot
-      // the weight so far is on its way while the products run
-      auto mine = [&] { return half == 0 && slot_i < rq.cached + rq.nnew && rq.slot >= 0 && rq.slot < a.M; };
-      auto weight = [&] { return a.weights + (((size_t)a.layer * a.M + rq.slot) * a.Hkv + it.h) * a.cap + slot_i; };
-      const float so_far = it.part < 0 && mine() ? *weight() : 0.f;
-      float2 w[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      for (int q = it.qb; q < it.qe; ++q, ++c) {
-        const int z = c & 1;
-        ok = __all_sync(0xffffffffu, wait_bar(s_ready(x, z), (uint32_t)((c / 2) & 1), abort));
-        if (!ok) break;
-        tc_fence_after();
-        // of this half's columns lo .. hi - 1 count: rows of tokens that see the slot and exist
-        const int lo = (slot_i - rq.cached - q * TOK) * G - half * 64, hi = (rq.nnew - q * TOK) * G - half * 64;
-        if (hi > 0) {
-          uint32_t r[2][32];
+      for (int pg = it.page; pg < it.page + it.pages && ok; ++pg) {
+        const int slot_i = pg * PAGE + x * TK + key;  // this thread's logical slot
+        // the weight so far is on its way while the products run
+        auto mine = [&] { return half == 0 && slot_i < rq.cached + rq.nnew && rq.slot >= 0 && rq.slot < a.M; };
+        auto weight = [&] { return a.weights + (((size_t)a.layer * a.M + rq.slot) * a.Hkv + it.h) * a.cap + slot_i; };
+        const float so_far = it.part < 0 && mine() ? *weight() : 0.f;
+        float2 w[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        for (int q = it.qb; q < it.qe; ++q, ++c) {
+          const int z = c & 1;
+          ok = __all_sync(0xffffffffu, wait_bar(s_ready(x, z), (uint32_t)((c / 2) & 1), abort));
+          if (!ok) break;
+          tc_fence_after();
+          // of this half's columns lo .. hi - 1 count: rows of tokens that see the slot and exist
+          const int lo = (slot_i - rq.cached - q * TOK) * G - half * 64, hi = (rq.nnew - q * TOK) * G - half * 64;
+          if (hi > 0) {
+            uint32_t r[2][32];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            tmem_load32(tmem + lanes + (uint32_t)(x * 256 + z * 128 + half * 64 + h * 32), r[h]);
-          tmem_wait_ld();
+            for (int h = 0; h < 2; ++h)
+              tmem_load32(tmem + lanes + (uint32_t)(x * 256 + z * 128 + half * 64 + h * 32), r[h]);
+            tmem_wait_ld();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) tmem_arrived(r[h]);
-          if (__any_sync(0xffffffffu, lo > 0 || hi < 64)) {
+            for (int h = 0; h < 2; ++h) tmem_arrived(r[h]);
+            if (__any_sync(0xffffffffu, lo > 0 || hi < 64)) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (32 * h + e < lo || 32 * h + e >= hi) r[h][e] = 0xff800000u;  // -inf
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (32 * h + e < lo || 32 * h + e >= hi) r[h][e] = 0xff800000u;  // -inf
+              for (int e = 0; e < 8; ++e) {
+                float2 u = mul2(make_float2(__uint_as_float(r[h][4 * e]), __uint_as_float(r[h][4 * e + 1])), sc2);
+                float2 v = mul2(make_float2(__uint_as_float(r[h][4 * e + 2]), __uint_as_float(r[h][4 * e + 3])), sc2);
+                u.x = ex2f(u.x);
+                u.y = ex2f(u.y);
+                v.x = ex2f(v.x);
+                v.y = ex2f(v.y);
+                w[e & 1] = add2(w[e & 1], u);
+                w[2 + (e & 1)] = add2(w[2 + (e & 1)], v);
+              }
           }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float2 u = mul2(make_float2(__uint_as_float(r[h][4 * e]), __uint_as_float(r[h][4 * e + 1])), sc2);
-              float2 v = mul2(make_float2(__uint_as_float(r[h][4 * e + 2]), __uint_as_float(r[h][4 * e + 3])), sc2);
-              u.x = ex2f(u.x);
-              u.y = ex2f(u.y);
-              v.x = ex2f(v.x);
-              v.y = ex2f(v.y);
-              w[e & 1] = add2(w[e & 1], u);
-              w[2 + (e & 1)] = add2(w[2 + (e & 1)], v);
-            }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(s_free(x, z));
+          }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(s_free(x, z));
-        }
+        // the two halves of a key's sum meet (both groups of threads come here,
+        // whether a wait gave up or not)
+        float sum = ((w[0].x + w[0].y) + (w[1].x + w[1].y)) + ((w[2].x + w[2].y) + (w[3].x + w[3].y));
+        if (half) *other = sum;
+        if (!ok) fail[x] = 1;  // written only before the barrier: all of the key tile's threads agree
+        asm volatile("bar.sync %0, 256;" ::"r"(1 + x) : "memory");
+        ok = !fail[x];
+        if (!half) sum += *other;
+        asm volatile("bar.sync %0, 256;" ::"r"(1 + x) : "memory");
+        if (!ok) break;
+        if (half) continue;
+        if (it.part >= 0) a.wpart[(size_t)it.part * PAGE + x * TK + key] = sum;
+        else if (mine()) *weight() = so_far + sum;
       }
-      // the two halves of a key's sum meet (both groups of threads come here,
-      // whether a wait gave up or not)
-      float sum = ((w[0].x + w[0].y) + (w[1].x + w[1].y)) + ((w[2].x + w[2].y) + (w[3].x + w[3].y));
-      if (half) *other = sum;
-      if (!ok) fail[x] = 1;  // written only before the barrier: all of the key tile's threads agree
-      asm volatile("bar.sync %0, 256;" ::"r"(1 + x) : "memory");
-      ok = !fail[x];
-      if (!half) sum += *other;
-      asm volatile("bar.sync %0, 256;" ::"r"(1 + x) : "memory");
-      if (!ok) break;
-      if (half) continue;
-      if (it.part >= 0) a.wpart[(size_t)it.part * PAGE + x * TK + key] = sum;
-      else if (mine()) *weight() = so_far + sum;
-     }
     }
     if (!ok && lane == 0) timed_out();
   }
