@@ -156,9 +156,9 @@ def load(build_if_missing: bool = True):
         "gp_debug_set_wait_limit": (I32, [P, I32, I64]),
         "gp_debug_fail_next_launch": (I32, [P, I32]),
         "gp_set_selection_mode": (I32, [P, I32]),
-        "gp_append_tokens": (I32, [P, I32, I32, C.POINTER(GpRequest), P, P, P, P, P, P, P]),
-        "gp_decode_attention_weighted": (I32, [P, I32, I32, C.POINTER(GpRequest), P, P, P, P, P]),
-        "gp_chunk_attention": (I32, [P, I32, I32, C.POINTER(GpRequest), P, P, P, P, P]),
+        "gp_append_tokens": (I32, [P, I32, I32, P, P, P, P, P, P, P, P]),
+        "gp_decode_attention_weighted": (I32, [P, I32, I32, P, P, P, P, P, P]),
+        "gp_chunk_attention": (I32, [P, I32, I32, P, P, P, P, P, P]),
         "gp_evict_weighted": (I32, [P, I32, C.POINTER(GpRequest), P, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -269,8 +269,13 @@ _NUM_PAGES = struct.Struct("=i")
 def _marshal(reqs):
     arr = (GpRequest * max(1, len(reqs)))()
     if len(reqs):
-        C.memmove(arr, b"".join([r._raw for r in reqs]), len(reqs) * _REQ_PACK.size)
+        C.memmove(arr, _records(reqs), len(reqs) * _REQ_PACK.size)
     return arr
+
+
+def _records(reqs) -> bytes:
+    """The requests' records for a call that only reads them."""
+    return b"".join([r._raw for r in reqs])
 
 
 def _unmarshal(arr, reqs):
@@ -470,7 +475,7 @@ def gp_append_tokens(ctx, layer: int, reqs, num_cached, num_new, q_dev, k_dev, v
     q_dev, q_rot_dev [rows][Hq][d] (both None: keys and values alone);
     k_dev, v_dev [rows][Hkv][d], rows packed request after request."""
     nc, nn = _counts(reqs, num_cached, num_new)
-    _check(ctx, load().gp_append_tokens(ctx, layer, len(reqs), _marshal(reqs), _host(nc), _host(nn),
+    _check(ctx, load().gp_append_tokens(ctx, layer, len(reqs), _records(reqs), _host(nc), _host(nn),
                                         _ptr(q_dev), _ptr(k_dev), _ptr(v_dev), _ptr(q_rot_dev), _ptr(weights_dev)))
 
 
@@ -478,7 +483,7 @@ def gp_decode_attention_weighted(ctx, layer: int, reqs, num_tokens, q_dev, first
     """gp_decode_attention that adds its softmax weights to weights_dev
     (fp32 [L][max_slots][Hkv][max_pages_per_req * 256]); first_dev may be None."""
     nt, = _counts(reqs, num_tokens)
-    _check(ctx, load().gp_decode_attention_weighted(ctx, layer, len(reqs), _marshal(reqs), _host(nt),
+    _check(ctx, load().gp_decode_attention_weighted(ctx, layer, len(reqs), _records(reqs), _host(nt),
                                                     _ptr(q_dev), _ptr(first_dev), _ptr(out_dev), _ptr(weights_dev)))
 
 
@@ -486,7 +491,7 @@ def gp_chunk_attention(ctx, layer: int, reqs, num_cached, num_new, q_dev, out_de
     """Causal attention of each request's num_new last tokens over its cache;
     q_dev (rotated) and out_dev [rows][Hq][d] of q_dtype, packed."""
     nc, nn = _counts(reqs, num_cached, num_new)
-    _check(ctx, load().gp_chunk_attention(ctx, layer, len(reqs), _marshal(reqs), _host(nc), _host(nn),
+    _check(ctx, load().gp_chunk_attention(ctx, layer, len(reqs), _records(reqs), _host(nc), _host(nn),
                                           _ptr(q_dev), _ptr(out_dev), _ptr(weights_dev)))
 
 
