@@ -47,7 +47,8 @@
 // again 26.  What bounds the attention is the chain S - softmax - O of a group
 // (about 3200 clocks for two tiles of 1024 clocks of products each); tried and
 // slower: two threads a row (583 us), an issuer a group (554 us), weights under
-// the old maximum while the new one is found (562 us).
+// the old maximum while the new one is found (562 us), S double buffered in steps
+// of 64 keys (717 us: products of 64 columns read A again for half as much).
 //
 // Every wait is bounded: on expiry the CTA records ERR_TIMEOUT, raises an
 // abort flag that ends every role's loop, waits (bounded) for its copies and
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
             const int y = key_row(a, rq, it.h, t);
             const uint32_t dst = sb + (uint32_t)(L::ST + (size_t)s * L::TILE);
             mbar_expect_tx(full(s), L::TILE);
-  #pragma unroll
+#pragma unroll
             for (int x = 0; x < D; x += 64) tma_load_2d(dst + (uint32_t)(x / 64 * L::HALF), map, x, y, full(s));
             ++c;
           };
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
             const int nqt = KEYS || it.alone ? 1 : 2;
             mbar_expect_tx(q_full, (uint32_t)(nqt * L::TILE));
             for (int x = 0; x < nqt; ++x)
-  #pragma unroll
+#pragma unroll
               for (int d = 0; d < D; d += 64)
                 tma_load_3d(sb + (uint32_t)(L::Q + (size_t)x * L::TILE + d / 64 * L::HALF), &a.qmap, d, it.h * G,
                             (int)rq.row0 + it.t0 + x * TOK, q_full);
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
         tc_fence_after();
         const uint64_t q0 = sw128_desc(sb + (uint32_t)(L::Q + (KEYS ? 0 : (size_t)x * L::TILE)));
         const uint64_t k0 = sw128_desc(stage(k));
-  #pragma unroll
+#pragma unroll
         for (int e = 0; e < D / 16; ++e) {
           const uint64_t off = (uint64_t)(((e >> 2) * L::HALF + (e & 3) * 32) >> 4);
           mma_ss(tmem + (uint32_t)(x * 128), q0 + off, k0 + off, idesc(TK, false), e > 0 ? 1u : 0u);
@@ -412,12 +413,12 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
         if (first && items_done > 0) wait(o_free(x), items_done - 1);
         wait(p_half(x), n);
         const uint64_t v0 = sw128_mn_desc(stage(k), L::HALF);
-  #pragma unroll
+#pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (half) wait(p_ready(x), n);
           if (!ok) return;
           tc_fence_after();
-  #pragma unroll
+#pragma unroll
           for (int e = 4 * half; e < 4 * half + 4; ++e)
             mma_ts(tmem + (uint32_t)(256 + x * 128), tmem + (uint32_t)(x * 128 + e * 8), v0 + (uint64_t)(e * 2048 >> 4),
                    idesc(D, true), first && e == 0 ? 0u : 1u);
