@@ -379,10 +379,12 @@ __global__ void __launch_bounds__(BK) k_chunk_tile_weights_join(const __grid_con
   const ChunkReq rq = a.reqs[jn.r];
   const int i = jn.first + (int)threadIdx.x;
   if (i >= rq.cached + rq.nnew || rq.slot < 0 || rq.slot >= a.M) return;
+  float* dst = a.weights + (((size_t)a.layer * a.M + rq.slot) * a.Hkv + jn.h) * a.cap + i;
+  const float so_far = *dst;
   float w = 0.f;
 #pragma unroll 8
   for (int p = 0; p < jn.n; ++p) w += __ldg(a.wpart + (size_t)(jn.part + p) * BK + threadIdx.x);
-  a.weights[(((size_t)a.layer * a.M + rq.slot) * a.Hkv + jn.h) * a.cap + i] += w;
+  *dst = so_far + w;
 }
 
 cudaError_t launch_k(void (*kernel)(ChunkArgs), size_t smem, int grid, bool chained, const ChunkArgs& a, cudaStream_t s) {

@@ -1033,9 +1033,12 @@ __global__ void __launch_bounds__(PAGE) k_chunk_weights_join(const __grid_consta
   const ChunkReq rq = load_req(a.reqs + jn.r);
   const int i = jn.page * PAGE + (int)threadIdx.x;
   if (i >= rq.cached + rq.nnew || rq.slot < 0 || rq.slot >= a.M) return;
+  float* dst = a.weights + (((size_t)a.layer * a.M + rq.slot) * a.Hkv + jn.h) * a.cap + i;
+  const float so_far = *dst;
   float w = 0.f;
+#pragma unroll 8
   for (int p = 0; p < jn.n; ++p) w += __ldg(a.wpart + (size_t)(jn.first + p) * PAGE + threadIdx.x);
-  a.weights[(((size_t)a.layer * a.M + rq.slot) * a.Hkv + jn.h) * a.cap + i] += w;
+  *dst = so_far + w;
 }
 
 template <int D, int G, bool KEYS>

@@ -8,6 +8,9 @@
 // (4 G + 4 G + 8) / 4 d = 8 % of the traffic at d = 128, G = 4.  Forming the
 // logits again from K would add 50 %.
 //
+// 64 requests of 1.05 M tokens in all, 32 query and 8 KV heads: 28 us beside 679 of
+// attention, whose logits of 134 MB are partly still in L2.
+//
 // A thread owns four tokens, a warp half a page of one KV head: every weight has
 // one writer, so the sums do not depend on any order.
 #include <cstdint>
