@@ -34,15 +34,15 @@
 // weight.  -L / c joins S^T as one more K = 16 step, ones times its three bf16
 // parts (24 bits): read from shared memory by every thread instead, it took
 // four times its bytes of the bandwidth that the products need there (291 us
-// against 272 for 6007 tokens behind 4099, 32 heads, d = 128).  An item is a
+// against 272 then for 6007 tokens behind 4099, 32 heads, d = 128).  An item is a
 // page (two key tiles) against a range of query tiles, S^T double buffered, K
 // tiles kept and the next item's loaded meanwhile.
 //   warp 0       producer;  warps 1, 2  MMA issuers, one a key tile
 //   warp 3       L of the query tiles;  warps 4-19  sums
 //
-// Measured (bf16, d = 128, 32 query and 8 KV heads): those 6007 tokens take 520
-// us of attention (1340 TFLOP/s of its 4 d flops a pair, 70 % of the measured
-// bf16 rate) and 272 us of weights; 106 drafted tokens of 16 requests over
+// Measured (bf16, d = 128, 32 query and 8 KV heads): those 6007 tokens take 510
+// us of attention (1365 TFLOP/s of its 4 d flops a pair, 72 % of the measured
+// bf16 rate) and 264 us of weights; 106 drafted tokens of 16 requests over
 // 85 831 cached ones 72 and 34 us, where reading K and V once takes 52 us and K
 // again 26.  What bounds the attention is the chain S - softmax - O of a group
 // (about 3200 clocks for two tiles of 1024 clocks of products each); tried and

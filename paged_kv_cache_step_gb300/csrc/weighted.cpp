@@ -146,7 +146,8 @@ struct ChunkPlan {
 // Attention: pairs of query tiles that follow each other (a key tile costs two
 // products' time), and the last tiles alone, their key tiles split between the
 // groups (one).  A piece's fixed cost is the time to load Q and to empty the
-// pipeline, about two tiles.  The last tiles need a launch of their own, about
+// pipeline, about three tiles (6007 tokens: 517, 515, 509, 513 and 514 us when it
+// is taken as 1, 2, 3, 4 and 6).  The last tiles need a launch of their own, about
 // 8 us; beside pairs, up to 12 key tiles of them a CTA (about 0.6 us each) go
 // along as pairs without a second tile instead, at twice the cost (five ragged
 // prompts, d = 64: 47 us in one launch, 55 in two).
@@ -171,7 +172,7 @@ void plan_chunk(int n, const int32_t* cached, const int32_t* fresh, int Hkv, int
         jobs.push_back({(cached[r] + std::min(t + 2 * tok, fresh[r]) + 127) / 128, 2, 1});
         of.push_back({r, h, t, alone, 0, 0, -1, -1});
       }
-  if (!jobs.empty()) cut_even(jobs, ctas, 2, 6, pieces, p->begin);
+  if (!jobs.empty()) cut_even(jobs, ctas, 3, 6, pieces, p->begin);
   for (size_t k = 0, e; k < pieces.size(); k = e) {
     for (e = k; e < pieces.size() && pieces[e].job == pieces[k].job;) ++e;
     const ChunkItem& job = of[pieces[k].job];
@@ -204,7 +205,7 @@ void plan_chunk(int n, const int32_t* cached, const int32_t* fresh, int Hkv, int
       of.push_back({r, h, (tiles - 1) * tok, 0, 0, 0, -1, -1});
     }
   }
-  if (!jobs.empty()) cut_even(jobs, ctas, 2, 6, pieces, p->kbegin);
+  if (!jobs.empty()) cut_even(jobs, ctas, 3, 6, pieces, p->kbegin);
   for (size_t k = 0, e; k < pieces.size(); k = e) {
     int parts = 0;
     for (e = k; e < pieces.size() && pieces[e].job == pieces[k].job; ++e) parts += pieces[e].to - pieces[e].from > 1 ? 2 : 1;
@@ -227,7 +228,8 @@ void plan_chunk(int n, const int32_t* cached, const int32_t* fresh, int Hkv, int
   }
   if (!weights) return;
   // Weights: a page against the query tiles that see it; loading the page
-  // costs about two query tiles' products.  The pages that every token sees
+  // costs about three query tiles' products (274, 268, 264 and 261 us at 1, 2, 3
+  // and 4 for the 6007 tokens, 28.4, 27.6, 28.3 and 28.9 for ragged prompts).  The pages that every token sees
   // are alike.
   jobs.clear();
   std::vector<WeightItem> wof;
@@ -246,7 +248,7 @@ void plan_chunk(int n, const int32_t* cached, const int32_t* fresh, int Hkv, int
     }
   }
   pieces.clear();
-  cut_even(jobs, ctas, 2, 6, pieces, p->wbegin);
+  cut_even(jobs, ctas, 3, 6, pieces, p->wbegin);
   for (size_t k = 0; k < pieces.size(); ++k) {
     const Piece& pc = pieces[k];
     WeightItem it = wof[pc.job];
