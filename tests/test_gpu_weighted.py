@@ -187,6 +187,33 @@ def test_append_without_queries_or_weights():
         e.close()
 
 
+@pytest.mark.parametrize("pages,new", [([1] * 66, [1] * 66), ([131, 1], [33_100, 200]), ([2] * 64, [300] * 64),
+                                       ([2] * 65, [256] * 65)])
+def test_append_tables_beyond_the_launch_parameters(pages, new):
+    """At and over the 64 requests and 128 pages whose tables travel as launch parameters."""
+    e = Engine(pages, L=1, hq=2, hkv=1, d=64, seed=16)
+    try:
+        cached = [200 if m == 1 else 0 for m in new]
+        for r, req in enumerate(e.reqs):
+            req.pos = 1000 * r
+        n = sum(new)
+        q, k, v = e.randn(n, 2, 64).bfloat16(), e.randn(n, 1, 64).bfloat16(), e.randn(n, 1, 64).bfloat16()
+        rot = torch.empty_like(q)
+        gp.gp_append_tokens(e.ctx, 0, e.reqs, cached, new, q, k, v, rot, e.w)
+        gp.gp_synchronize(e.ctx)
+        pos = torch.cat([1000 * r + torch.arange(m) for r, m in enumerate(new)]).cuda()
+        kr, qr = e.rope(k, pos), e.rope(q, pos)
+        assert torch.all((rot.double() - qr).abs() <= rope_tol(q, qr, EPS["bf16"]))
+        tol, at = rope_tol(k, kr, EPS["bf16"]), 0
+        for r, (c, m) in enumerate(zip(cached, new)):
+            assert torch.all((e.rows(e.k, r, 0, 0, c + m)[c:] - kr[at:at + m, 0]).abs() <= tol[at:at + m, 0])
+            assert torch.equal(e.rows(e.v, r, 0, 0, c + m)[c:], v[at:at + m, 0].double())
+            assert not e.w[0, r, 0, c:c + m].any() and torch.isnan(e.w[0, r, 0, c + m:]).all()
+            at += m
+    finally:
+        e.close()
+
+
 # ---- gp_decode_attention_weighted ---------------------------------------------
 
 SHAPES = {"bf16_g4_d128": dict(hq=8, hkv=2), "bf16_g2_d128": dict(hq=4, hkv=2), "bf16_g2_d64": dict(hq=4, hkv=2, d=64),
@@ -411,6 +438,38 @@ def test_the_longest_request():
             gp.gp_evict_weighted(e.ctx, e.reqs, [tokens], [keep], e.w)
             gp.gp_synchronize(e.ctx)
             check_evict(e, [tokens], [keep], k0, v0, w0, t0)
+    finally:
+        e.close()
+
+
+@pytest.mark.parametrize("kernel", [gp.GP_SCAN_AUTO, gp.GP_SCAN_CUDA_CORE])
+def test_requests_on_shared_pages_gather_their_own_weights(kernel):
+    """Two requests with the same first two pages: chunks and decode steps of both
+    in one call, each with weights of its own."""
+    cached, new = [512, 700], [9, 150]
+    e = Engine([3, 4], L=1, seed=17, kernel=kernel)
+    try:
+        for j in range(2):
+            gp.gp_page_ref(e.ctx, int(e.reqs[0].table[j]))
+            gp.gp_page_unref(e.ctx, int(e.reqs[1].table[j]))
+            e.reqs[1].table[j] = e.reqs[0].table[j]
+        e.fill([521, 850])
+        q = e.randn(159, e.hq, e.d).bfloat16()
+        out, w = torch.full_like(q, math.nan), e.w.clone()
+        gp.gp_chunk_attention(e.ctx, 0, e.reqs, cached, new, q, out, w)
+        gp.gp_synchronize(e.ctx)
+        check_chunk(e, 0, cached, new, q, out, e.w, w, kernel == gp.GP_SCAN_AUTO)
+        one, w1 = torch.empty(2, e.hq, e.d, device="cuda"), w.clone()
+        gp.gp_decode_attention_weighted(e.ctx, 0, e.reqs, [521, 850], q[:2].contiguous(), None, one, w1)
+        gp.gp_synchronize(e.ctx)
+        qr = e.rope(q[:2], torch.zeros(2, device="cuda"))
+        for r, T in enumerate([521, 850]):
+            for h in range(e.hkv):
+                heads = slice(h * e.G, h * e.G + e.G)
+                ref, mag, ws, rel = softmax_reference(qr[r:r + 1, heads], e.rows(e.k, r, 0, h, T), e.rows(e.v, r, 0, h, T), T)
+                assert torch.all((one[r, heads].double() - ref[0]).abs() <= 2 * rel * mag[0])
+                want = w[0, r, h, :T].double() + ws
+                assert torch.all((w1[0, r, h, :T].double() - want).abs() <= rel * ws + (e.G + 2) * 2.0 ** -23 * want)
     finally:
         e.close()
 
