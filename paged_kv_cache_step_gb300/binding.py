@@ -187,6 +187,17 @@ def _ptr(t) -> int:
     return int(t)
 
 
+def _dense(t) -> int:
+    """_ptr of a buffer that kernels read or write as packed rows."""
+    try:
+        if t.is_contiguous() and t.is_cuda:
+            return t.data_ptr()
+    except AttributeError:  # no tensor
+        if not isinstance(t, np.ndarray):
+            return _ptr(t)
+    raise GrowPageError(GP_ERR_INVALID, "a buffer must be a contiguous tensor on a CUDA device, or its address")
+
+
 # ---------------------------------------------------------------------------
 # requests
 # ---------------------------------------------------------------------------
@@ -476,7 +487,7 @@ def gp_append_tokens(ctx, layer: int, reqs, num_cached, num_new, q_dev, k_dev, v
     k_dev, v_dev [rows][Hkv][d], rows packed request after request."""
     nc, nn = _counts(reqs, num_cached, num_new)
     _check(ctx, load().gp_append_tokens(ctx, layer, len(reqs), _records(reqs), _host(nc), _host(nn),
-                                        _ptr(q_dev), _ptr(k_dev), _ptr(v_dev), _ptr(q_rot_dev), _ptr(weights_dev)))
+                                        _dense(q_dev), _dense(k_dev), _dense(v_dev), _dense(q_rot_dev), _dense(weights_dev)))
 
 
 def gp_decode_attention_weighted(ctx, layer: int, reqs, num_tokens, q_dev, first_dev, out_dev, weights_dev):
@@ -484,7 +495,7 @@ def gp_decode_attention_weighted(ctx, layer: int, reqs, num_tokens, q_dev, first
     (fp32 [L][max_slots][Hkv][max_pages_per_req * 256]); first_dev may be None."""
     nt, = _counts(reqs, num_tokens)
     _check(ctx, load().gp_decode_attention_weighted(ctx, layer, len(reqs), _records(reqs), _host(nt),
-                                                    _ptr(q_dev), _ptr(first_dev), _ptr(out_dev), _ptr(weights_dev)))
+                                                    _dense(q_dev), _dense(first_dev), _dense(out_dev), _dense(weights_dev)))
 
 
 def gp_chunk_attention(ctx, layer: int, reqs, num_cached, num_new, q_dev, out_dev, weights_dev=None):
@@ -492,7 +503,7 @@ def gp_chunk_attention(ctx, layer: int, reqs, num_cached, num_new, q_dev, out_de
     q_dev (rotated) and out_dev [rows][Hq][d] of q_dtype, packed."""
     nc, nn = _counts(reqs, num_cached, num_new)
     _check(ctx, load().gp_chunk_attention(ctx, layer, len(reqs), _records(reqs), _host(nc), _host(nn),
-                                          _ptr(q_dev), _ptr(out_dev), _ptr(weights_dev)))
+                                          _dense(q_dev), _dense(out_dev), _dense(weights_dev)))
 
 
 def gp_evict_weighted(ctx, reqs, num_tokens, keep_tokens, weights_dev):
@@ -501,7 +512,7 @@ def gp_evict_weighted(ctx, reqs, num_tokens, keep_tokens, weights_dev):
     compacted in order.  Rewrites the requests' tables (copy-on-write)."""
     nt, nk = _counts(reqs, num_tokens, keep_tokens)
     arr = _marshal(reqs)
-    st = load().gp_evict_weighted(ctx, len(reqs), arr, _host(nt), _host(nk), _ptr(weights_dev))
+    st = load().gp_evict_weighted(ctx, len(reqs), arr, _host(nt), _host(nk), _dense(weights_dev))
     _unmarshal(arr, reqs)
     _check(ctx, st)
 

@@ -769,6 +769,28 @@ def test_appended_tokens_make_a_demand_result_stale():
         e.close()
 
 
+def test_strided_buffers_are_refused():
+    e = Engine([2], L=1, seed=44)
+    try:
+        e.fill([300])
+        q = e.randn(8, 2, 128).bfloat16().transpose(0, 1)  # [2][8][128], not packed
+        kv, out = e.randn(2, 2, 128).bfloat16(), torch.zeros(2, 8, 128, device="cuda", dtype=torch.bfloat16)
+        k0, w0 = e.k.clone(), e.w.clone()
+        for call in (lambda: gp.gp_append_tokens(e.ctx, 0, e.reqs, [300], [2], q, kv, kv, out, e.w),
+                     lambda: gp.gp_append_tokens(e.ctx, 0, e.reqs, [300], [2], None, kv, kv.transpose(0, 1), None, e.w),
+                     lambda: gp.gp_chunk_attention(e.ctx, 0, e.reqs, [298], [2], q, out, e.w),
+                     lambda: gp.gp_chunk_attention(e.ctx, 0, e.reqs, [298], [2], out, q, e.w),
+                     lambda: gp.gp_decode_attention_weighted(e.ctx, 0, e.reqs, [300], q[:1], None, out.float()[:1], e.w),
+                     lambda: gp.gp_evict_weighted(e.ctx, e.reqs, [300], [100], e.w.transpose(2, 3))):
+            with pytest.raises(gp.GrowPageError) as err:
+                call()
+            assert err.value.status == gp.GP_ERR_INVALID
+        gp.gp_synchronize(e.ctx)
+        assert torch.equal(bits(e.k), bits(k0)) and torch.equal(bits(e.w), bits(w0)) and not out.any()
+    finally:
+        e.close()
+
+
 def test_refused_while_the_stream_is_captured():
     stream = torch.cuda.Stream()
     e = Engine([2], L=1, seed=42, stream=stream)

@@ -131,6 +131,19 @@ def test_evict_lengths(eng):
     assert _status(_evict, ctx, reqs, (1, 2), (1, 2)) == gp.GP_ERR_INVALID
 
 
+def test_buffers_on_the_host(eng):
+    torch = pytest.importorskip("torch")
+    ctx, reqs = eng
+    for host in (torch.zeros(4, 4), torch.zeros(4, 4).t(), np.zeros((4, 4), dtype=np.float32)):
+        for name in ("q", "k", "v", "rot", "w"):
+            assert _status(_append, ctx, reqs, **{name: host}) == gp.GP_ERR_INVALID
+        for name in ("q", "out", "w"):
+            assert _status(_chunk, ctx, reqs, **{name: host}) == gp.GP_ERR_INVALID
+            assert _status(_decode, ctx, reqs, **{name: host}) == gp.GP_ERR_INVALID
+        assert _status(_decode, ctx, reqs, first=host) == gp.GP_ERR_INVALID
+        assert _status(_evict, ctx, reqs, w=host) == gp.GP_ERR_INVALID
+
+
 def test_null_context():
     lib = gp.load()
     n = np.zeros(1, dtype=np.int32)
