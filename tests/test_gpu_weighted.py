@@ -604,8 +604,12 @@ def test_a_slot_taken_again_while_its_eviction_is_pending():
     e = Engine([4], spare=1, seed=26, L=1)
     side = torch.cuda.Stream()
     try:
-        e.fill([900])
+        e.fill([901])
+        k = e.randn(200, 2, 128).bfloat16()
         gp.gp_set_compaction_stream(e.ctx, side)
+        # the kernels' first launches load them, which may wait for the device
+        gp.gp_append_tokens(e.ctx, 0, e.reqs, [901], [1], None, k[:1], k[:1], None, None)
+        gp.gp_evict_weighted(e.ctx, e.reqs, [901], [900], e.w)
         torch.cuda.synchronize()
         with torch.cuda.stream(side):
             torch.cuda._sleep(100_000_000)  # the eviction starts well after the append has been issued
@@ -614,7 +618,6 @@ def test_a_slot_taken_again_while_its_eviction_is_pending():
         gp.gp_slot_release(e.ctx, old.slot)
         slot, page = gp.gp_slot_acquire(e.ctx), gp.gp_page_alloc(e.ctx)
         assert slot == old.slot and page not in old.pages
-        k = e.randn(200, 2, 128).bfloat16()
         new = gp.Request(slot, np.array([page]), 0, 4)
         gp.gp_append_tokens(e.ctx, 0, [new], [0], [200], None, k, k, None, e.w)
         gp.gp_wait_compaction(e.ctx)
