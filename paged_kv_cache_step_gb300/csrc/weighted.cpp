@@ -602,6 +602,14 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
     longest = std::max(longest, T);
     for (int j = 0; j < reqs[r].num_pages; ++j) cow += c->refcnt[reqs[r].block_table[j]] > 1;
   }
+  // the pages compacted in place are in one request each
+  begin_page_check(c);
+  for (int r = 0; r < n; ++r)
+    for (int j = 0; er[r].items && j < reqs[r].num_pages; ++j) {
+      const int32_t pg = reqs[r].block_table[j];
+      if (c->refcnt[pg] == 1 && std::exchange(c->page_seen[pg], c->check) == c->check)
+        return fail(c, GP_ERR_INVALID, "page %d is in two requests and has one reference", pg);
+    }
   if ((st = ready_call(c)) != GP_OK) return st;
   if (cow > c->free_pages.size())
     return fail(c, GP_ERR_NO_PAGES, "copy-on-write needs %zu fresh pages, %zu free", cow, c->free_pages.size());

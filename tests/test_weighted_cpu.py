@@ -131,6 +131,17 @@ def test_evict_lengths(eng):
     assert _status(_evict, ctx, reqs, (1, 2), (1, 2)) == gp.GP_ERR_INVALID
 
 
+def test_evict_a_page_of_two_requests(eng):
+    ctx, reqs = eng
+    own, page = int(reqs[1].table[1]), int(reqs[0].table[0])
+    reqs[1].table[1] = page  # without a reference of its own
+    assert _status(_evict, ctx, reqs, (512, 512, 0), (10, 10, 1)) == gp.GP_ERR_INVALID
+    assert _status(_evict, ctx, reqs, (512, 512, 0), (10, 512, 1)) == gp.GP_ERR_STATE  # one of them evicts
+    gp.gp_page_ref(ctx, page)
+    gp.gp_page_unref(ctx, own)
+    assert _status(_evict, ctx, reqs, (512, 512, 0), (10, 10, 1)) == gp.GP_ERR_STATE  # shared: both copy it
+
+
 def test_buffers_on_the_host(eng):
     torch = pytest.importorskip("torch")
     ctx, reqs = eng
