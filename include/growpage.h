@@ -436,9 +436,9 @@ gp_status gp_decode_attention_weighted(gp_ctx* ctx, int32_t layer, int32_t n, co
  * With weights_dev, the weights of every token are added; NULL leaves that
  * out.  The rows of K and V of the attended tokens must be finite; cache slots
  * past num_cached[r] + num_new[r] may hold any bits.  out_dev must not overlap
- * q_dev.  bf16 caches and queries run on the tensor-core kernels, which round
- * the softmax weights to bf16 for the product with V (out is bf16 too; the
- * accumulated weights are not rounded); the rest, or everything under
+ * q_dev.  bf16 caches and queries run on the tensor-core kernels, which hold
+ * the softmax weights to 2^-15 of themselves for the product with V (out is
+ * bf16; the accumulated weights are not rounded); the rest, or everything under
  * gp_set_scan_kernel(CUDA_CORE), on CUDA-core ones in fp32. */
 gp_status gp_chunk_attention(gp_ctx* ctx, int32_t layer, int32_t n, const gp_request* reqs,
                              const int32_t* num_cached, const int32_t* num_new, const void* q_dev,

@@ -5,15 +5,20 @@
 // Attention.  A query tile is 128 rows, 128 / G tokens of the G heads of a KV
 // head (they share its keys).  Per key tile of 128 slots
 //   S = Q K^T        128 x 128, K = d, fp32 in TMEM
-//   P = 2^(S c - m)  c = log2(e) / sqrt(d), rounded to bf16 over S in TMEM
-//   O += P V         128 x d, K = 128, P from TMEM, V MN-major as TMA left it
+//   P = 2^(S c - m)  c = log2(e) / sqrt(d), in two bf16 parts over S in TMEM
+//   O += P V         128 x d, K = 128 for each part, P from TMEM, V MN-major as
+//                    TMA left it
 // with the maximum m of the first tile, moved only when a row's has grown by
 // more than 24 (a factor 2^24, which the exponents of fp32 and bf16 hold
 // easily): O is then rescaled in TMEM by the warp that found it, between two
 // products.
-// Rounding P to bf16 costs 2^-9 relative a weight at random signs, about what
-// rounding the output to bf16 costs; keeping it exact would double the second
-// product.  The sum l is of the unrounded fp32 weights.
+// P's first part is its upper 16 bits, the second the rest rounded to bf16: a
+// weight keeps 2^-15 of itself, where the output's own rounding is 2^-8.  One
+// bf16 part alone takes 522 us instead of the 680 below, and is off by up to 2^-8
+// of sum a |v|: more than the output's rounding where values cancel.  The rest is
+// formed by a mixed-precision FMA of the packed first part (masked out and added
+// instead: 755 us; a rounded first part: 695).  The sum l is of the unrounded fp32
+// weights.
 //
 // One CTA per SM walks a list of items that the host cut into even shares.
 // Two softmax groups of 128 threads (thread = row = TMEM lane) alternate on
@@ -25,7 +30,7 @@
 //   warp 0       producer: Q tiles, and the K and V tiles through a ring
 //   warp 1       MMA issuer
 //   warps 4-7    softmax of group 0, then its epilogue;  warps 8-11 group 1
-// TMEM: S0 S1 (128 columns each, P over the first 64 of them), O0 O1.
+// TMEM: S0 S1 (128 columns each, the parts of P over 64 each), O0 O1.
 //
 // Weights.  W_i += sum over rows of 2^(S_ri c - L_r) needs the final
 // L_r = m_r + log2 l_r of every row (rounded to fp32 once, as the logit is), so S
@@ -40,13 +45,13 @@
 //   warp 0       producer;  warps 1, 2  MMA issuers, one a key tile
 //   warp 3       L of the query tiles;  warps 4-19  sums
 //
-// Measured (bf16, d = 128, 32 query and 8 KV heads): those 6007 tokens take 510
-// us of attention (1365 TFLOP/s of its 4 d flops a pair, 72 % of the measured
-// bf16 rate) and 264 us of weights; 106 drafted tokens of 16 requests over
-// 85 831 cached ones 72 and 34 us, where reading K and V once takes 52 us and K
-// again 26.  What bounds the attention is the chain S - softmax - O of a group
-// (about 3200 clocks for two tiles of 1024 clocks of products each); tried and
-// slower: two threads a row (583 us), an issuer a group (554 us), weights under
+// Measured (bf16, d = 128, 32 query and 8 KV heads): those 6007 tokens take 680
+// us of attention (80 % of the measured bf16 rate, of the 6 d flops a pair that the
+// two parts take) and 270 us of weights; 106 drafted tokens of 16 requests over
+// 85 831 cached ones 80 and 38 us, where reading K and V once takes 52 us and K
+// again 26.  What bounds the attention is the chain S - softmax - O of a group,
+// beside products of 1536 clocks a tile.  Tried when P was one part (510 us then)
+// and slower: two threads a row (583 us), an issuer a group (554 us), weights under
 // the old maximum while the new one is found (562 us), S double buffered in steps
 // of 64 keys (717 us: products of 64 columns read A again for half as much).
 //
@@ -420,8 +425,10 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
           tc_fence_after();
 #pragma unroll
           for (int e = 4 * half; e < 4 * half + 4; ++e)
-            mma_ts(tmem + (uint32_t)(256 + x * 128), tmem + (uint32_t)(x * 128 + e * 8), v0 + (uint64_t)(e * 2048 >> 4),
-                   idesc(D, true), first && e == 0 ? 0u : 1u);
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+              mma_ts(tmem + (uint32_t)(256 + x * 128), tmem + (uint32_t)(x * 128 + part * 64 + e * 8),
+                     v0 + (uint64_t)(e * 2048 >> 4), idesc(D, true), first && e == 0 && part == 0 ? 0u : 1u);
         }
         ++n;
         if (last) {
@@ -594,17 +601,20 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
         }
         const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m, -m);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        auto weigh = [&](int q) {  // 32 keys' weights, over their logits
-          uint32_t p[16];
+        auto weigh = [&](int q) {  // 32 keys' weights, both parts over the logits
+          uint32_t p[16], rest[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float2 z = fma2(make_float2(__uint_as_float(r[q][2 * e]), __uint_as_float(r[q][2 * e + 1])), sc2, nm2);
             z.x = ex2f(z.x);
             z.y = ex2f(z.y);
             sum[e & 1] = add2(sum[e & 1], z);
-            p[e] = pack_bf16(z.x, z.y);
+            p[e] = __byte_perm(__float_as_uint(z.x), __float_as_uint(z.y), 0x7632);  // the upper halves
+            z = less_bf16(z, p[e]);
+            rest[e] = pack_bf16(z.x, z.y);
           }
           tmem_store16(ts + (uint32_t)(16 * q), p);
+          tmem_store16(ts + (uint32_t)(64 + 16 * q), rest);
         };
         weigh(0);
         weigh(1);

@@ -1,4 +1,5 @@
-// Base-2 exponential, and two fp32 operations in one instruction (sm_100 and up).
+// Base-2 exponential, two fp32 operations in one instruction, and fp32 minus bf16
+// (sm_100 and up).
 #pragma once
 
 #include <cstdint>
@@ -31,6 +32,15 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=l"(reinterpret_cast<uint64_t&>(d))
       : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
   return d;
+}
+
+// z minus the two bf16 values packed in p.
+__device__ __forceinline__ float2 less_bf16(float2 z, uint32_t p) {
+  asm("{\n\t.reg .b16 lo, hi, minus;\n\tmov.b16 minus, 0xBF80;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "fma.rn.f32.bf16 %0, lo, minus, %0;\n\tfma.rn.f32.bf16 %1, hi, minus, %1;\n\t}"
+      : "+f"(z.x), "+f"(z.y)
+      : "r"(p));
+  return z;
 }
 
 }  // namespace gp

@@ -1,0 +1,49 @@
+"""The accumulated-weight calls where they once went wrong: precision of the
+softmax weights, evictions at the same time, records kept from call to call,
+lengths and sizes at their ends.  The engine, the formulas in 64 bits and the
+arithmetic behind the tolerances are test_gpu_weighted.py's."""
+
+import math
+
+import pytest
+import torch
+
+import paged_kv_cache_step_gb300 as gp
+from test_gpu_weighted import EPS, Engine, softmax_reference
+
+pytestmark = pytest.mark.gpu
+
+
+# One pair of query tiles, one tile whose keys two groups share, a long cache cut
+# into parts and joined.
+@pytest.mark.parametrize("cached,new", [([300, 0], [130, 260]), ([100, 640], [5, 33]), ([6000], [3])])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (4, 2, 128), (4, 1, 64), (4, 2, 64)])
+def test_chunk_weights_keep_their_bits_for_the_values(cached, new, hq, hkv, d):
+    """Values of either sign that nearly cancel: an output's error shows what the
+    softmax weights were rounded to.  They are held to 2^-15 (two bf16 parts, the
+    first cut off, 2^-7, the second rounded, 2^-8), beside the logits' error and
+    the sum's; a single bf16 part is off by up to 2^-8."""
+    e = Engine([-(-(a + b) // 256) for a, b in zip(cached, new)], L=1, hq=hq, hkv=hkv, d=d, seed=61)
+    try:
+        e.fill([a + b for a, b in zip(cached, new)])
+        for r, (a, b) in enumerate(zip(cached, new)):
+            pages, slots = e.at(r, torch.arange(a + b, device="cuda"))
+            sign = (1 - 2 * (torch.arange(a + b, device="cuda") % 2))[:, None, None]
+            e.v[0, pages, :, slots] = (sign * (1 + torch.arange(d, device="cuda") / d)).to(e.v.dtype).expand(-1, hkv, -1)
+        q = (e.randn(sum(new), hq, d) / 32).bfloat16()  # logits of about 1/32
+        out = torch.full_like(q, math.nan)
+        gp.gp_chunk_attention(e.ctx, 0, e.reqs, cached, new, q, out, None)
+        gp.gp_synchronize(e.ctx)
+        at, worst = 0, 0.0
+        for r, (c, m) in enumerate(zip(cached, new)):
+            for h in range(hkv):
+                heads = slice(h * e.G, h * e.G + e.G)
+                ref, mag, _, rel = softmax_reference(q[at:at + m, heads].double(), e.rows(e.k, r, 0, h, c + m),
+                                                     e.rows(e.v, r, 0, h, c + m), c)
+                tol = (2 * rel + 2.0 ** -15) * mag
+                tol = tol + EPS["bf16"] * (ref.abs() + tol)
+                worst = max(worst, ((out[at:at + m, heads].double() - ref).abs() / tol).max().item())
+            at += m
+        assert worst <= 1.0, worst
+    finally:
+        e.close()
