@@ -2,6 +2,9 @@
 // are placed while the earlier one still runs, and wait on the device for its
 // end (programmatic dependent launch).  The earlier kernel says when with
 // let_next_in, the later one calls wait_for_previous before it touches anything.
+// What an earlier kernel of the chain writes is read after the wait by ordinary
+// loads or __ldcg: __ldg's path is for data that no kernel writes while this one
+// is on the device, the call's descriptors.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -348,15 +348,15 @@ __global__ void __launch_bounds__(D / 4) k_chunk_tile_join(const __grid_constant
   const float* base = a.part + (size_t)jn.part * chunk_tile_part_floats(D);
   float M = NEG;
 #pragma unroll 8
-  for (int p = 0; p < jn.n; ++p) M = fmaxf(M, __ldg(base + p * chunk_tile_part_floats(D) + BR * D + row));
+  for (int p = 0; p < jn.n; ++p) M = fmaxf(M, __ldcg(base + p * chunk_tile_part_floats(D) + BR * D + row));
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int p = 0; p < jn.n; ++p) {
     const float* q = base + p * chunk_tile_part_floats(D);
-    const float f = ex2f(__ldg(q + BR * D + row) - M);  // 0 for a part of which the row sees nothing
-    const float4 x = __ldg(reinterpret_cast<const float4*>(q + (size_t)row * D) + threadIdx.x);
-    l = fmaf(f, __ldg(q + BR * D + BR + row), l);
+    const float f = ex2f(__ldcg(q + BR * D + row) - M);  // 0 for a part of which the row sees nothing
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(q + (size_t)row * D) + threadIdx.x);
+    l = fmaf(f, __ldcg(q + BR * D + BR + row), l);
     o = make_float4(fmaf(f, x.x, o.x), fmaf(f, x.y, o.y), fmaf(f, x.z, o.z), fmaf(f, x.w, o.w));
   }
   const float inv = 1.f / l;
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(BK) k_chunk_tile_weights_join(const __grid_con
   const float so_far = *dst;
   float w = 0.f;
 #pragma unroll 8
-  for (int p = 0; p < jn.n; ++p) w += __ldg(a.wpart + (size_t)(jn.part + p) * BK + threadIdx.x);
+  for (int p = 0; p < jn.n; ++p) w += __ldcg(a.wpart + (size_t)(jn.part + p) * BK + threadIdx.x);
   *dst = so_far + w;
 }
 

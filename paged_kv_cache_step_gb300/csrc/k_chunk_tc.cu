@@ -713,20 +713,20 @@ __global__ void __launch_bounds__(256) k_chunk_join(const __grid_constant__ Chun
   const float* base = a.part + (size_t)jn.first * chunk_part_floats(D);
   float M = NEG;
 #pragma unroll 8
-  for (int p = 0; p < jn.n; ++p) M = fmaxf(M, __ldg(base + p * chunk_part_floats(D) + 128 * D + row));
+  for (int p = 0; p < jn.n; ++p) M = fmaxf(M, __ldcg(base + p * chunk_part_floats(D) + 128 * D + row));
   float l = 0.f;
   float4 acc[2] = {};
   const int d0 = (blockIdx.y * 2 + half) * 8;  // eight dimensions
 #pragma unroll 4
   for (int p = 0; p < jn.n; ++p) {
     const float* q = base + p * chunk_part_floats(D);
-    const float lp = __ldg(q + 128 * D + 128 + row);
+    const float lp = __ldcg(q + 128 * D + 128 + row);
     // a part that the row does not see has no sum, and its O may not be there
-    const float f = lp > 0.f ? ex2f(__ldg(q + 128 * D + row) - M) : 0.f;
+    const float f = lp > 0.f ? ex2f(__ldcg(q + 128 * D + row) - M) : 0.f;
     l = fmaf(f, lp, l);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float4 o = __ldg(reinterpret_cast<const float4*>(q) + (size_t)(d0 / 4 + e) * 128 + row);
+      float4 o = __ldcg(reinterpret_cast<const float4*>(q) + (size_t)(d0 / 4 + e) * 128 + row);
       if (f == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
       acc[e].x = fmaf(f, o.x, acc[e].x);
       acc[e].y = fmaf(f, o.y, acc[e].y);
@@ -932,7 +932,7 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int row = 32 * k + lane, t = q * TOK + row / G;
-            v[k] = t < rq.nnew ? -inv_sc * __ldg(a.lse + (size_t)(rq.row0 + t) * a.Hq + it.h * G + row % G) : 0.f;
+            v[k] = t < rq.nnew ? -inv_sc * __ldcg(a.lse + (size_t)(rq.row0 + t) * a.Hq + it.h * G + row % G) : 0.f;
           }
           if (c >= 2) ok = __all_sync(0xffffffffu, wait_bar(t_empty(b), (uint32_t)((c / 2 - 1) & 1), abort));
           if (!ok) break;
@@ -1047,7 +1047,7 @@ __global__ void __launch_bounds__(PAGE) k_chunk_weights_join(const __grid_consta
   const float so_far = *dst;
   float w = 0.f;
 #pragma unroll 8
-  for (int p = 0; p < jn.n; ++p) w += __ldg(a.wpart + (size_t)(jn.first + p) * PAGE + threadIdx.x);
+  for (int p = 0; p < jn.n; ++p) w += __ldcg(a.wpart + (size_t)(jn.first + p) * PAGE + threadIdx.x);
   *dst = so_far + w;
 }
 

@@ -1,0 +1,41 @@
+"""Faults of the accumulated-weight calls that need no device to show: what the
+sources must not do, and what the calls and the binding refuse."""
+
+import os
+import re
+
+import pytest
+
+import paged_kv_cache_step_gb300 as gp
+
+CSRC = os.path.join(os.path.dirname(gp.__file__), "csrc")
+
+
+def _source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return f.read()
+
+
+def _sources(suffix=(".cu", ".cuh", ".cpp", ".h")):
+    return [f for f in sorted(os.listdir(CSRC)) if f.endswith(suffix)]
+
+
+def _arguments(text, call):
+    """The argument of every `call(...)` in the text, comments left out."""
+    text = re.sub(r"//[^\n]*", "", text)
+    for m in re.finditer(re.escape(call) + r"\(", text):
+        depth, i = 1, m.end()
+        while depth:
+            depth += {"(": 1, ")": -1}.get(text[i], 0)
+            i += 1
+        yield " ".join(text[m.end():i - 1].split())
+
+
+@pytest.mark.parametrize("name", ["k_chunk.cu", "k_chunk_tc.cu", "k_weights.cu", "k_evict.cu", "k_append.cu"])
+def test_the_read_only_path_is_for_descriptors(name):
+    """These kernels are on the device before the one ahead of them has ended: what
+    that one writes (partials, log-sums, weights) is not read-only for their whole
+    life.  Items, requests and block tables are uploaded before the first of them."""
+    descriptor = re.compile(r"reinterpret_cast<const int4\*>\(p\)( \+ 1)?|s( \+ \d)?|a\.bt \+ rq\.bt_off \+ .*")
+    for arg in _arguments(_source(name), "__ldg"):
+        assert descriptor.fullmatch(arg), arg
