@@ -445,10 +445,13 @@ cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t s) {
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   // a key and a place in the list of kept slots each, and the list's last piece
   const size_t smem = (sizeof(unsigned) + sizeof(uint16_t)) * (size_t)a.longest + 64;
-  if (smem > 208 * 1024) {  // over 35 488 slots
+  constexpr size_t most = 208 * 1024;
+  if (smem > most) {  // over 35 488 slots
     k_evict_select<false><<<dim3((unsigned)grid), SNT, 0, s>>>(a);
   } else {
-    const cudaError_t e = cudaFuncSetAttribute(k_evict_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the limit is the function's, whoever launches it: always the same, so that a
+    // thread with a shorter request does not lower it between here and the launch
+    const cudaError_t e = cudaFuncSetAttribute(k_evict_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
     k_evict_select<true><<<dim3((unsigned)grid), SNT, smem, s>>>(a);
   }

@@ -4,6 +4,7 @@ lengths and sizes at their ends.  The engine, the formulas in 64 bits and the
 arithmetic behind the tolerances are test_gpu_weighted.py's."""
 
 import math
+import threading
 
 import pytest
 import torch
@@ -47,3 +48,34 @@ def test_chunk_weights_keep_their_bits_for_the_values(cached, new, hq, hkv, d):
         assert worst <= 1.0, worst
     finally:
         e.close()
+
+
+def test_evictions_of_two_threads():
+    """Two contexts, a host thread each, evict requests of very different lengths at
+    the same time: the limit of shared memory of the selection is one for both."""
+    lengths, errors = [30000, 300], []
+    engines = [Engine([-(-T // 256)], L=1, hq=2, hkv=1, d=64, seed=62, stream=torch.cuda.Stream()) for T in lengths]
+    together = threading.Barrier(2)
+
+    def work(e, T):
+        try:
+            together.wait()
+            for _ in range(600):
+                gp.gp_evict_weighted(e.ctx, e.reqs, [T], [T - 1], e.w)
+            gp.gp_synchronize(e.ctx)
+        except gp.GrowPageError as err:
+            errors.append(str(err))
+
+    try:
+        for e, T in zip(engines, lengths):
+            e.fill([T])
+        torch.cuda.synchronize()
+        threads = [threading.Thread(target=work, args=x) for x in zip(engines, lengths)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not errors
+    finally:
+        for e in engines:
+            e.close()
