@@ -44,7 +44,8 @@ def _stale(obj: str, src: str) -> bool:
             os.path.join(CSRC, "demand_common.cuh"), os.path.join(CSRC, "engine.h"),
             os.path.join(CSRC, "attn_kernels.h"), os.path.join(CSRC, "tc_ptx.cuh"),
             os.path.join(CSRC, "weighted_kernels.h"), os.path.join(CSRC, "chained.cuh"),
-            os.path.join(CSRC, "math2.cuh"), os.path.join(INCLUDE, "growpage.h")]
+            os.path.join(CSRC, "math2.cuh"), os.path.join(CSRC, "shared_limit.cuh"),
+            os.path.join(INCLUDE, "growpage.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -32,6 +32,7 @@
 #include "attn_kernels.h"
 #include "chained.cuh"
 #include "gp_kernels.h"
+#include "shared_limit.cuh"
 
 namespace gp {
 namespace {
@@ -383,12 +384,8 @@ __global__ void __launch_bounds__(NT, 2) k_decode_attn(AttnArgs a) {
 template <int D, int G, bool F32, bool W>
 cudaError_t launch_w(const AttnArgs& a, cudaStream_t s) {
   constexpr int smem = NSTAGE * STAGE;
-  static bool attr = false;
-  if (!attr) {
-    const cudaError_t e = cudaFuncSetAttribute(k_decode_attn<D, G, F32, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+  const cudaError_t e = allow_shared<k_decode_attn<D, G, F32, W>>(smem);
+  if (e != cudaSuccess) return e;
   k_decode_attn<D, G, F32, W><<<dim3(a.n_ctas), NT, smem, s>>>(a);
   return cudaGetLastError();
 }

@@ -50,6 +50,7 @@
 #include "attn_kernels.h"
 #include "chained.cuh"
 #include "gp_kernels.h"
+#include "shared_limit.cuh"
 #include "tc_ptx.cuh"
 
 namespace gp {
@@ -741,13 +742,8 @@ __global__ void __launch_bounds__(NT, 1) k_decode_attn_tc(const __grid_constant_
 template <int G, bool W>
 cudaError_t launch_tc(const AttnArgs& a, cudaStream_t s) {
   constexpr size_t smem = Sm<G>::BYTES;
-  static bool attr = false;
-  if (!attr) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k_decode_attn_tc<G, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+  const cudaError_t e = allow_shared<k_decode_attn_tc<G, W>>((int)smem);
+  if (e != cudaSuccess) return e;
   k_decode_attn_tc<G, W><<<dim3((unsigned)a.grid), NT, smem, s>>>(a);
   return cudaGetLastError();
 }

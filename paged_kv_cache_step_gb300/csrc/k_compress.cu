@@ -32,6 +32,7 @@
 #include <cstdint>
 
 #include "gp_kernels.h"
+#include "shared_limit.cuh"
 
 namespace gp {
 namespace {
@@ -617,13 +618,9 @@ __global__ void __launch_bounds__(NT, 1) k_compress(CompressArgs a) {
 
 template <int RB>
 cudaError_t launch_rb(const CompressArgs& a, cudaStream_t s) {
-  static bool attr = false;
   const int smem = CSTAGES * STAGE_BYTES;
-  if (!attr) {
-    const cudaError_t e = cudaFuncSetAttribute(k_compress<RB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+  const cudaError_t e = allow_shared<k_compress<RB>>(smem);
+  if (e != cudaSuccess) return e;
   k_compress<RB><<<dim3(a.n_work * a.L * a.Hkv), NT, smem, s>>>(a);
   return cudaGetLastError();
 }

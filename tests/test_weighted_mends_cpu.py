@@ -39,3 +39,10 @@ def test_the_read_only_path_is_for_descriptors(name):
     descriptor = re.compile(r"reinterpret_cast<const int4\*>\(p\)( \+ 1)?|s( \+ \d)?|a\.bt \+ rq\.bt_off \+ .*")
     for arg in _arguments(_source(name), "__ldg"):
         assert descriptor.fullmatch(arg), arg
+
+
+@pytest.mark.parametrize("name", _sources((".cu", ".cuh")))
+def test_no_kernel_attribute_hangs_on_a_flag_of_the_process(name):
+    """A kernel's shared memory limit is set per device: a flag that the first launch
+    sets leaves it unset on every other device."""
+    assert not re.search(r"static\s+bool", _source(name))
