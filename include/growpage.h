@@ -452,8 +452,8 @@ gp_status gp_chunk_attention(gp_ctx* ctx, int32_t layer, int32_t n, const gp_req
  * the logical slots [0, keep); num_pages is unchanged and the slots from keep
  * on become free, their contents unspecified.  A request with num_tokens <=
  * keep_tokens is left as it is.  Copy-on-write as in gp_compress_hold for the
- * requests that evict (GP_ERR_NO_PAGES: nothing changed); a page of two of them
- * must have a reference for each (GP_ERR_INVALID).  num_tokens and
+ * requests that evict (GP_ERR_NO_PAGES: nothing changed); a page of several of
+ * them must have a reference for each (GP_ERR_INVALID).  num_tokens and
  * keep_tokens: HOST int32 [n].  Runs on the compaction stream if one is set,
  * with gp_compress_hold's rules, which hold for the weights of the evicted
  * requests as for their K/V; a gp_boundary_demand result of the slots is stale

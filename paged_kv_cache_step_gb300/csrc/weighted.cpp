@@ -602,14 +602,23 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
     longest = std::max(longest, T);
     for (int j = 0; j < reqs[r].num_pages; ++j) cow += c->refcnt[reqs[r].block_table[j]] > 1;
   }
-  // the pages compacted in place are in one request each
+  // a page has a reference for every request that evicts from it: one with a single
+  // reference is compacted in place, a shared one loses a reference to each copy
   begin_page_check(c);
+  std::vector<int32_t> shared;
   for (int r = 0; r < n; ++r)
     for (int j = 0; er[r].items && j < reqs[r].num_pages; ++j) {
       const int32_t pg = reqs[r].block_table[j];
-      if (c->refcnt[pg] == 1 && std::exchange(c->page_seen[pg], c->check) == c->check)
+      if (c->refcnt[pg] > 1) shared.push_back(pg);
+      else if (std::exchange(c->page_seen[pg], c->check) == c->check)
         return fail(c, GP_ERR_INVALID, "page %d is in two requests and has one reference", pg);
     }
+  std::sort(shared.begin(), shared.end());
+  for (size_t i = 0, e; i < shared.size(); i = e) {
+    for (e = i; e < shared.size() && shared[e] == shared[i];) ++e;
+    if ((int64_t)(e - i) > c->refcnt[shared[i]])
+      return fail(c, GP_ERR_INVALID, "page %d is in %zu requests and has %d references", shared[i], e - i, c->refcnt[shared[i]]);
+  }
   if ((st = ready_call(c)) != GP_OK) return st;
   if (cow > c->free_pages.size())
     return fail(c, GP_ERR_NO_PAGES, "copy-on-write needs %zu fresh pages, %zu free", cow, c->free_pages.size());

@@ -7,6 +7,7 @@ import re
 import pytest
 
 import paged_kv_cache_step_gb300 as gp
+from test_weighted_cpu import _evict, _state, _status, eng  # noqa: F401 (a fixture)
 
 CSRC = os.path.join(os.path.dirname(gp.__file__), "csrc")
 
@@ -46,3 +47,19 @@ def test_no_kernel_attribute_hangs_on_a_flag_of_the_process(name):
     """A kernel's shared memory limit is set per device: a flag that the first launch
     sets leaves it unset on every other device."""
     assert not re.search(r"static\s+bool", _source(name))
+
+
+def test_evict_a_page_with_fewer_references_than_requests(eng):  # noqa: F811
+    """Three requests that evict from one page of two references: each would drop one."""
+    ctx, reqs = eng
+    page = int(reqs[0].table[0])
+    for req in reqs[1:]:
+        gp.gp_page_unref(ctx, int(req.table[0]))
+        req.table[0] = page
+    gp.gp_page_ref(ctx, page)
+    before = _state(ctx, reqs)
+    assert _status(_evict, ctx, reqs, (512, 512, 512), (10, 10, 10)) == gp.GP_ERR_INVALID
+    assert _status(_evict, ctx, reqs, (512, 512, 512), (10, 10, 512)) == gp.GP_ERR_STATE  # two of them evict
+    assert _state(ctx, reqs) == before
+    gp.gp_page_ref(ctx, page)
+    assert _status(_evict, ctx, reqs, (512, 512, 512), (10, 10, 10)) == gp.GP_ERR_STATE
