@@ -590,11 +590,11 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
     e.keep = keep;
     e.recent = std::min(g.recent_window, keep);
     e.bt_off = r * maxp;
-    e.idx_pitch = (keep + 7) / 8 * 8;
     e.idx_off = idx_count;
     e.item0 = items;
     e.pre_off = pre_count;
-    if (T <= keep) continue;  // nothing to evict: its tables and rows stay as they are
+    if (T <= keep) continue;  // nothing to evict: its tables and rows stay as they are, and no list is made
+    e.idx_pitch = (keep + 7) / 8 * 8;
     e.items = (keep + R - 1) / R;
     idx_count += (int64_t)units * e.idx_pitch;
     items += (int64_t)units * e.items;

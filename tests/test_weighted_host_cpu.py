@@ -1,0 +1,59 @@
+"""The host side of the accumulated-weight calls over a runtime without a device
+(fake_runtime.cpp): what a failing call leaves behind, what is allocated when, and
+what an inspection call reads."""
+
+import os
+import shutil
+import subprocess
+import types
+
+import numpy as np
+import pytest
+
+import paged_kv_cache_step_gb300 as gp
+from paged_kv_cache_step_gb300 import _build_lib, binding
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+DEV = 1 << 20  # stands for a device address; no kernel runs
+
+
+@pytest.fixture(scope="module")
+def fake_library(tmp_path_factory):
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_build_lib._nvcc()))), "include")
+    if not os.path.exists(os.path.join(cuda, "cuda_runtime.h")) or not shutil.which("g++"):
+        pytest.skip("no CUDA headers or no compiler")
+    _build_lib.build()
+    lib = str(tmp_path_factory.mktemp("fake") / "libfake.so")
+    objs = [os.path.join(_build_lib.BUILD, f + ".o") for f in ("growpage", "weighted")]
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-Wl,-Bsymbolic", "-Wl,--no-undefined", "-I", _build_lib.INCLUDE,
+                    "-I", _build_lib.CSRC, "-I", cuda, os.path.join(HERE, "fake_runtime.cpp"), *objs, "-o", lib], check=True)
+    return lib
+
+
+@pytest.fixture
+def fake(fake_library, monkeypatch):
+    """An engine of two layers over it, and its controls."""
+    monkeypatch.setattr(_build_lib, "LIB", fake_library)
+    monkeypatch.setattr(binding, "_LIB", None)
+    lib = gp.load(build_if_missing=False)
+    lib.fake_reset()
+    cfg = gp.gp_config_default(num_layers=2, num_q_heads=4, num_kv_heads=2, head_dim=64, max_slots=4, num_pages=40,
+                               max_pages_per_req=12)
+    ctx = gp.gp_create(cfg, DEV, DEV, None)
+    reqs = [gp.Request(gp.gp_slot_acquire(ctx), [gp.gp_page_alloc(ctx) for _ in range(p)], 0, 12) for p in (2, 12)]
+    yield types.SimpleNamespace(ctx=ctx, reqs=reqs, calls=lambda name: lib.fake_calls(name.encode()),
+                                fail=lambda name, after=1: lib.fake_fail(name.encode(), after))
+    gp.gp_destroy(ctx)
+
+
+def _masks(ctx, index, num_pages):
+    return gp.unpack_mask(gp.gp_debug_keep_mask(ctx, index, 4, num_pages), num_pages * 256)
+
+
+def test_keep_masks_of_a_budget_that_evicts_nothing(fake):
+    """A budget over the tokens leaves a request as it is, however large it is."""
+    gp.gp_evict_weighted(fake.ctx, fake.reqs, [500, 3000], [2 ** 31 - 1, 700], DEV)
+    mask = _masks(fake.ctx, 0, 2)
+    assert mask[:, :500].all() and not mask[:, 500:].any()
+    mask = _masks(fake.ctx, 1, 12)
+    assert mask[:, :700].all() and not mask[:, 700:].any()
