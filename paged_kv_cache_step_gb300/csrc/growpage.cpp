@@ -1045,6 +1045,7 @@ gp_status gp_debug_keep_mask(gp_ctx* c, int32_t req_idx, uint32_t* out) {
     for (int u = 0; u < units_of(c); ++u)
       for (int i = 0; i < (rec.kept ? rec.kept : rec.tokens); ++i) {
         const int slot = rec.kept ? kept[(size_t)u * rec.pitch + i] : i;
+        if (slot >= rec.tokens) return fail(c, GP_ERR_STATE, "the eviction's selection did not run");
         out[u * words + slot / 32] |= 1u << (slot % 32);
       }
     return check_kernel_errors(c);

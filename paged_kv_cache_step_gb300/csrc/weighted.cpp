@@ -631,10 +631,10 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
   const size_t at_idx = scratch.take(sizeof(uint16_t) * (size_t)idx_count);
   const size_t at_pre = scratch.take(sizeof(int32_t) * (size_t)pre_count);
   const size_t at_flags = scratch.take(sizeof(unsigned) * (size_t)items), at_ticket = scratch.take(sizeof(unsigned long long));
+  c->last_compress.clear();  // its lists may be in the scratch
   if ((st = ensure(c, c->evict, scratch.bytes)) != GP_OK) return st;
   StagingSlot* slot = nullptr;
   if ((st = staging_take(c, lay.bytes, &slot)) != GP_OK) return st;
-  c->last_compress.clear();  // its lists may be in the scratch
   char* host = static_cast<char*>(slot->pinned);
   std::memcpy(host + at_req, er.data(), sizeof(EvictReq) * (size_t)n);
   int32_t* old_bt = reinterpret_cast<int32_t*>(host + at_old);

@@ -17,6 +17,7 @@
 namespace {
 std::map<std::string, long> calls, fail_at;
 std::map<void*, size_t> sizes;
+int skip_select = 0;
 // counts the call; an error when it is the one that is to fail
 cudaError_t called(const char* name) {
   const long n = ++calls[name];
@@ -43,7 +44,9 @@ void fake_fail(const char* name, long after) { fail_at[name] = calls[name] + aft
 void fake_reset() {
   calls.clear();
   fail_at.clear();
+  skip_select = 0;
 }
+void fake_skip_select(int yes) { skip_select = yes; }
 
 cudaError_t cudaMalloc(void** p, size_t n) { return take("cudaMalloc", p, n); }
 cudaError_t cudaHostAlloc(void** p, size_t n, unsigned) { return take("cudaHostAlloc", p, n); }
@@ -123,7 +126,7 @@ FAKE_LAUNCH(launch_prep, PrepArgs)
 // keeps the first slots of every unit
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t) {
   if (called("launch_evict_select") != cudaSuccess) return cudaErrorMemoryAllocation;
-  for (int r = 0; r < a.n; ++r)
+  for (int r = 0; r < a.n && !skip_select; ++r)
     for (int u = 0; u < a.L * a.Hkv && a.reqs[r].items; ++u)
       for (int i = 0; i < a.reqs[r].keep; ++i) a.idx[a.reqs[r].idx_off + (size_t)u * a.reqs[r].idx_pitch + i] = (uint16_t)i;
   return cudaSuccess;

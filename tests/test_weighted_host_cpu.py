@@ -57,3 +57,29 @@ def test_keep_masks_of_a_budget_that_evicts_nothing(fake):
     assert mask[:, :500].all() and not mask[:, 500:].any()
     mask = _masks(fake.ctx, 1, 12)
     assert mask[:, :700].all() and not mask[:, 700:].any()
+
+
+def test_an_eviction_that_fails_half_way_leaves_no_record(fake):
+    """The scratch with the last eviction's lists is given back for a larger one,
+    and then the call fails: the lists are not read any more."""
+    small, large = fake.reqs
+    gp.gp_evict_weighted(fake.ctx, [small], [500], [300], DEV)
+    assert _masks(fake.ctx, 0, 2)[:, :300].all()
+    fake.fail("cudaEventSynchronize")  # the descriptors' place
+    with pytest.raises(gp.GrowPageError) as err:
+        gp.gp_evict_weighted(fake.ctx, [large], [3000], [2500], DEV)
+    assert err.value.status == gp.GP_ERR_CUDA
+    out = np.zeros(4 * 2 * 8 + 8192, dtype=np.uint32)  # room behind the masks, for what should not be written
+    st = gp.load().gp_debug_keep_mask(fake.ctx, 0, out.ctypes.data)
+    assert st == gp.GP_ERR_INVALID and not out.any()
+
+
+def test_lists_that_hold_no_slots_are_not_made_into_masks(fake):
+    """Lists that the selection has not written (its launch went lost): an error, and
+    nothing behind the masks."""
+    small = fake.reqs[0]
+    gp.load().fake_skip_select(1)
+    gp.gp_evict_weighted(fake.ctx, [small], [500], [300], DEV)
+    out = np.zeros(4 * 2 * 8 + 8192, dtype=np.uint32)
+    st = gp.load().gp_debug_keep_mask(fake.ctx, 0, out.ctypes.data)
+    assert st == gp.GP_ERR_STATE and not out[4 * 2 * 8:].any()
