@@ -53,10 +53,10 @@ struct CompressRec {
 };
 
 // A call's descriptors on their way to the device: pinned memory, its device
-// mirror, and the event after which both may be written again.
+// mirror (pieces of the engine's), and the event after which both may be written
+// again.
 struct StagingSlot {
   void* pinned = nullptr;
-  size_t pinned_cap = 0;
   DevBuf dev;
   cudaEvent_t free = nullptr;
 };
@@ -98,6 +98,9 @@ struct gp_ctx {
   // kStagingSlots before it, and none disturbs a compaction's) and scratch
   gp::StagingSlot staging[gp::kStagingSlots];
   int staging_next = 0;
+  void* staging_pinned = nullptr;  // of all slots
+  gp::DevBuf staging_dev;
+  size_t staging_cap = 0;          // bytes of a slot
   gp::DevBuf logits, wstat, evict, chunk;
   int device = 0;                  // the device current at gp_create
   // speculative selection: the Eq. 10 keep masks of every request of the last
@@ -297,21 +300,32 @@ inline gp_status ready_call(gp_ctx* c) {
   return GP_OK;
 }
 
-// A staging slot of at least `bytes`, free to be written.
+// A staging slot of at least `bytes`, free to be written.  The slots are pieces
+// of one allocation, made at the first call and again when a call needs more than
+// any before it: a call that is not the largest so far allocates nothing.
 inline gp_status staging_take(gp_ctx* c, size_t bytes, StagingSlot** out) {
-  StagingSlot& s = c->staging[c->staging_next];
-  if (!s.free) GP_CUDA(c, cudaEventCreateWithFlags(&s.free, cudaEventDisableTiming));
-  GP_CUDA(c, cudaEventSynchronize(s.free));
-  if (bytes > s.pinned_cap) {
-    const size_t cap = (std::max(bytes, 2 * s.pinned_cap) + 65535) & ~size_t(65535);
-    if (s.pinned) GP_CUDA(c, cudaFreeHost(s.pinned));
-    s.pinned = nullptr;
-    s.pinned_cap = 0;
-    GP_CUDA(c, cudaHostAlloc(&s.pinned, cap, cudaHostAllocDefault));
-    s.pinned_cap = cap;
+  if (bytes > c->staging_cap) {
+    for (StagingSlot& s : c->staging) {
+      if (!s.free) GP_CUDA(c, cudaEventCreateWithFlags(&s.free, cudaEventDisableTiming));
+      GP_CUDA(c, cudaEventSynchronize(s.free));  // its copy has read the pinned memory
+    }
+    const size_t cap = (std::max(bytes, 2 * c->staging_cap) + 65535) & ~size_t(65535);
+    c->staging_cap = 0;
+    if (c->staging_pinned) {
+      void* old = std::exchange(c->staging_pinned, nullptr);
+      GP_CUDA(c, cudaFreeHost(old));
+    }
+    GP_CUDA(c, cudaHostAlloc(&c->staging_pinned, kStagingSlots * cap, cudaHostAllocDefault));
+    const gp_status st = ensure(c, c->staging_dev, kStagingSlots * cap);  // (a cudaFree waits for the kernels that read it)
+    if (st != GP_OK) return st;
+    for (int i = 0; i < kStagingSlots; ++i) {
+      c->staging[i].pinned = static_cast<char*>(c->staging_pinned) + i * cap;
+      c->staging[i].dev.p = static_cast<char*>(c->staging_dev.p) + i * cap;
+    }
+    c->staging_cap = cap;
   }
-  const gp_status st = ensure(c, s.dev, s.pinned_cap);
-  if (st != GP_OK) return st;
+  StagingSlot& s = c->staging[c->staging_next];
+  GP_CUDA(c, cudaEventSynchronize(s.free));
   c->staging_next = (c->staging_next + 1) % kStagingSlots;
   *out = &s;
   return GP_OK;

@@ -236,13 +236,11 @@ gp_status gp_destroy(gp_ctx* c) {
     if (c->ev_ready) cudaEventDestroy(c->ev_ready);
     if (c->ev_done) cudaEventDestroy(c->ev_done);
     for (DevBuf* b : {&c->upload, &c->bt2, &c->qt, &c->bq, &c->scores, &c->aval, &c->tickets, &c->kout, &c->ksum, &c->ent,
-                      &c->masks, &c->xstat, &c->attn, &c->spec_masks, &c->logits, &c->wstat, &c->evict, &c->chunk})
+                      &c->masks, &c->xstat, &c->attn, &c->spec_masks, &c->logits, &c->wstat, &c->evict, &c->chunk, &c->staging_dev})
       if (b->p) cudaFree(b->p);
-    for (StagingSlot& s : c->staging) {
-      if (s.pinned) cudaFreeHost(s.pinned);
-      if (s.dev.p) cudaFree(s.dev.p);
+    if (c->staging_pinned) cudaFreeHost(c->staging_pinned);
+    for (StagingSlot& s : c->staging)
       if (s.free) cudaEventDestroy(s.free);
-    }
     if (c->inv_freq) cudaFree(c->inv_freq);
     if (c->pool) cudaFree(c->pool);
     if (c->err_dev) cudaFree(c->err_dev);

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import paged_kv_cache_step_gb300 as gp
-from test_gpu_weighted import EPS, Engine, softmax_reference
+from test_gpu_weighted import EPS, Engine, bits, softmax_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +79,29 @@ def test_evictions_of_two_threads():
     finally:
         for e in engines:
             e.close()
+
+
+def test_descriptors_that_grow_while_calls_are_in_flight():
+    """Calls of few and of many requests in turn, the first ones still waiting on the
+    device when the descriptors' memory grows: the same bits as one call at a time."""
+    n, results = 70, []
+    for held in (False, True):
+        e = Engine([1] * n, L=1, hq=2, hkv=1, d=64, seed=63, cap=256)
+        try:
+            e.fill([200] * n)
+            q = e.randn(n, 2, 64).bfloat16()
+            outs = []
+            torch.cuda.synchronize()
+            if held:
+                torch.cuda._sleep(50_000_000)
+            for i, m in enumerate([2, 3, 1, n, 5, n, 2, n - 1, 4, 1, n, 3]):
+                outs.append(torch.zeros(n, 2, 64, dtype=torch.bfloat16, device="cuda"))
+                gp.gp_chunk_attention(e.ctx, 0, e.reqs[:m], [199 - i] * m, [1] * m, q, outs[-1], e.w)
+                if not held:
+                    gp.gp_synchronize(e.ctx)
+            gp.gp_synchronize(e.ctx)
+            results.append((torch.stack(outs), e.w.clone()))
+        finally:
+            e.close()
+    for a, b in zip(*results):
+        assert torch.equal(bits(a), bits(b))

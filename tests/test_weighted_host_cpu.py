@@ -83,3 +83,56 @@ def test_lists_that_hold_no_slots_are_not_made_into_masks(fake):
     out = np.zeros(4 * 2 * 8 + 8192, dtype=np.uint32)
     st = gp.load().gp_debug_keep_mask(fake.ctx, 0, out.ctypes.data)
     assert st == gp.GP_ERR_STATE and not out[4 * 2 * 8:].any()
+
+
+def _alloc_count(fake):
+    return [fake.calls(x) for x in ("cudaMalloc", "cudaHostAlloc", "cudaFree", "cudaFreeHost", "cudaEventCreate")]
+
+
+@pytest.mark.parametrize("which", ["decode", "weighted decode", "chunk", "evict"])
+def test_only_the_first_call_of_a_size_allocates(fake, which):
+    """Descriptors go through eight slots in turn; they are made together, so the
+    second call is as quick as any later one."""
+    def call():
+        if which == "decode":
+            gp.gp_decode_attention(fake.ctx, 0, fake.reqs, [500, 3000], DEV, DEV, DEV)
+        elif which == "weighted decode":
+            gp.gp_decode_attention_weighted(fake.ctx, 0, fake.reqs, [500, 3000], DEV, None, DEV, DEV)
+        elif which == "chunk":
+            gp.gp_chunk_attention(fake.ctx, 0, fake.reqs, [400, 2000], [100, 50], DEV, DEV << 4, DEV)
+        else:
+            gp.gp_evict_weighted(fake.ctx, fake.reqs, [500, 3000], [300, 2900], DEV)
+
+    call()
+    first = _alloc_count(fake)
+    for _ in range(20):
+        call()
+    assert _alloc_count(fake) == first
+
+
+def test_descriptors_of_many_sizes(fake):
+    """Calls that need more and more room: a slot that grows frees nothing that a copy
+    still reads, and all slots have the new size."""
+    grown = 0
+    for n in (1, 400, 2500, 400, 2500, 1):
+        before, waits = _alloc_count(fake), fake.calls("cudaEventSynchronize")
+        for _ in range(9):
+            gp.gp_chunk_attention(fake.ctx, 0, fake.reqs[1:], [0], [n], DEV, DEV << 4, None)
+        after = _alloc_count(fake)
+        if after[1] > before[1]:
+            grown += 1
+            assert after[1] == before[1] + 1 and fake.calls("cudaEventSynchronize") == waits + 8 + 9
+    assert grown >= 1
+
+
+@pytest.mark.parametrize("name", ["cudaHostAlloc", "cudaMalloc", "cudaEventCreate", "cudaEventSynchronize"])
+def test_a_call_after_one_that_found_no_memory(fake, name):
+    for after in (1, 2, 3):
+        fake.fail(name, after)
+        for _ in range(3):
+            try:
+                gp.gp_chunk_attention(fake.ctx, 0, fake.reqs, [400, 2000], [100, 50], DEV, DEV << 4, None)
+            except gp.GrowPageError as err:
+                assert err.status == gp.GP_ERR_CUDA
+    for _ in range(20):
+        gp.gp_chunk_attention(fake.ctx, 0, fake.reqs, [400, 2000], [100, 50], DEV, DEV << 4, None)
