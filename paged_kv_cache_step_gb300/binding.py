@@ -16,6 +16,7 @@ import array
 import ctypes as C
 import struct
 import os
+import sys
 from dataclasses import dataclass
 
 import numpy as np
@@ -187,15 +188,66 @@ def _ptr(t) -> int:
     return int(t)
 
 
-def _dense(t) -> int:
-    """_ptr of a buffer that kernels read or write as packed rows."""
-    try:
-        if t.is_contiguous() and t.is_cuda:
+class _Buffers:
+    """What the buffers of a context's calls hold: the types of queries and of keys,
+    the elements of a packed row of each and of the accumulated weights."""
+
+    def __init__(self, cfg, device):
+        self._codes = cfg.q_dtype, cfg.kv_dtype
+        self.q_row, self.kv_row = cfg.num_q_heads * cfg.head_dim, cfg.num_kv_heads * cfg.head_dim
+        self.weights = cfg.num_layers * cfg.max_slots * cfg.num_kv_heads * cfg.max_pages_per_req * cfg.page_size
+        self.device = device
+        self.q = self.kv = self.f32 = self.u8 = None  # torch's types, once a tensor is met
+
+    def know_types(self):
+        import torch  # loaded: a tensor of it is being looked at
+        self.f32, self.u8 = torch.float32, torch.uint8
+        self.q, self.kv = (torch.float32 if x == GP_DTYPE_F32 else torch.bfloat16 for x in self._codes)
+
+
+class _Unknown:
+    """_Buffers of a context that gp_create here has not made: nothing is known."""
+    q_row = kv_row = weights = 0
+    device = q = kv = f32 = u8 = None
+
+
+def _held(ctx):
+    held = getattr(ctx, "buffers", _Unknown)
+    if held.f32 is None and held is not _Unknown and "torch" in sys.modules:
+        held.know_types()
+    return held
+
+
+def _dense(held, t, dtype, count) -> int:
+    """_ptr of a buffer that kernels read or write as packed rows: a tensor is
+    contiguous, on the engine's device, of the type that the call takes there and
+    holds the elements of its rows, or more."""
+    if t is None:
+        return 0
+    try:  # in as few looks at the tensor as it takes: half of a small call's time is here
+        if t.dtype is dtype and t.numel() >= count and t.get_device() == held.device and t.is_contiguous():
             return t.data_ptr()
+        placed = t.is_contiguous() and t.is_cuda
     except AttributeError:  # no tensor
         if not isinstance(t, np.ndarray):
             return _ptr(t)
-    raise GrowPageError(GP_ERR_INVALID, "a buffer must be a contiguous tensor on a CUDA device, or its address")
+        placed = False
+    if not placed:
+        raise GrowPageError(GP_ERR_INVALID, "a buffer must be a contiguous tensor on a CUDA device, or its address")
+    if held is not _Unknown:
+        if t.numel() < count or (t.dtype is not dtype and not (dtype is held.u8 and str(t.dtype) == "torch.bool")):
+            raise GrowPageError(GP_ERR_INVALID, f"a buffer of {t.numel()} {t.dtype}, where the call takes {count} {dtype}")
+        if held.device is not None and t.get_device() != held.device:
+            raise GrowPageError(GP_ERR_INVALID, f"a buffer on device {t.get_device()}, the caches are on device {held.device}")
+    return t.data_ptr()
+
+
+def _weights(held, t) -> int:
+    """_dense of the accumulated weights, which have one size."""
+    at = _dense(held, t, held.f32, held.weights)
+    if held.weights and at and hasattr(t, "numel") and t.numel() != held.weights:
+        raise GrowPageError(GP_ERR_INVALID, f"{t.numel()} weights, where the engine has {held.weights}")
+    return at
 
 
 # ---------------------------------------------------------------------------
@@ -333,6 +385,7 @@ def gp_create(cfg: GpConfig, k_cache=None, v_cache=None, stream=None):
     s = 0 if stream is None else (stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
     st = load().gp_create(C.byref(cfg), _ptr(k_cache) or None, _ptr(v_cache) or None, s or None, C.byref(ctx))
     _check(None, st)
+    ctx.buffers = _Buffers(cfg, k_cache.get_device() if hasattr(k_cache, "get_device") else None)
     return ctx
 
 
@@ -480,30 +533,43 @@ def _host(a) -> int:
     return a.buffer_info()[0] if type(a) is array.array else a.ctypes.data
 
 
+def _total(a) -> int:
+    return sum(a) if type(a) is array.array else int(a.sum(dtype=np.int64))
+
+
 def gp_append_tokens(ctx, layer: int, reqs, num_cached, num_new, q_dev, k_dev, v_dev, q_rot_dev, weights_dev=None):
     """New tokens of one layer into the cache: rotated keys, values, rotated
     queries, cleared weights.  num_cached, num_new: host int32 per request;
     q_dev, q_rot_dev [rows][Hq][d] (both None: keys and values alone);
     k_dev, v_dev [rows][Hkv][d], rows packed request after request."""
     nc, nn = _counts(reqs, num_cached, num_new)
+    held, rows = _held(ctx), _total(nn)
+    q, kv = rows * held.q_row, rows * held.kv_row
     _check(ctx, load().gp_append_tokens(ctx, layer, len(reqs), _records(reqs), _host(nc), _host(nn),
-                                        _dense(q_dev), _dense(k_dev), _dense(v_dev), _dense(q_rot_dev), _dense(weights_dev)))
+                                        _dense(held, q_dev, held.q, q), _dense(held, k_dev, held.kv, kv), _dense(held, v_dev, held.kv, kv),
+                                        _dense(held, q_rot_dev, held.q, q), _weights(held, weights_dev)))
 
 
 def gp_decode_attention_weighted(ctx, layer: int, reqs, num_tokens, q_dev, first_dev, out_dev, weights_dev):
     """gp_decode_attention that adds its softmax weights to weights_dev
     (fp32 [L][max_slots][Hkv][max_pages_per_req * 256]); first_dev may be None."""
     nt, = _counts(reqs, num_tokens)
-    _check(ctx, load().gp_decode_attention_weighted(ctx, layer, len(reqs), _records(reqs), _host(nt),
-                                                    _dense(q_dev), _dense(first_dev), _dense(out_dev), _dense(weights_dev)))
+    n = len(reqs)
+    held = _held(ctx)
+    q = n * held.q_row
+    _check(ctx, load().gp_decode_attention_weighted(ctx, layer, n, _records(reqs), _host(nt), _dense(held, q_dev, held.q, q),
+                                                    _dense(held, first_dev, held.u8, n), _dense(held, out_dev, held.f32, q),
+                                                    _weights(held, weights_dev)))
 
 
 def gp_chunk_attention(ctx, layer: int, reqs, num_cached, num_new, q_dev, out_dev, weights_dev=None):
     """Causal attention of each request's num_new last tokens over its cache;
     q_dev (rotated) and out_dev [rows][Hq][d] of q_dtype, packed."""
     nc, nn = _counts(reqs, num_cached, num_new)
+    held = _held(ctx)
+    q = _total(nn) * held.q_row
     _check(ctx, load().gp_chunk_attention(ctx, layer, len(reqs), _records(reqs), _host(nc), _host(nn),
-                                          _dense(q_dev), _dense(out_dev), _dense(weights_dev)))
+                                          _dense(held, q_dev, held.q, q), _dense(held, out_dev, held.q, q), _weights(held, weights_dev)))
 
 
 def gp_evict_weighted(ctx, reqs, num_tokens, keep_tokens, weights_dev):
@@ -512,7 +578,7 @@ def gp_evict_weighted(ctx, reqs, num_tokens, keep_tokens, weights_dev):
     compacted in order.  Rewrites the requests' tables (copy-on-write)."""
     nt, nk = _counts(reqs, num_tokens, keep_tokens)
     arr = _marshal(reqs)
-    st = load().gp_evict_weighted(ctx, len(reqs), arr, _host(nt), _host(nk), _dense(weights_dev))
+    st = load().gp_evict_weighted(ctx, len(reqs), arr, _host(nt), _host(nk), _weights(_held(ctx), weights_dev))
     _unmarshal(arr, reqs)
     _check(ctx, st)
 

@@ -7,7 +7,7 @@ import re
 import pytest
 
 import paged_kv_cache_step_gb300 as gp
-from test_weighted_cpu import _evict, _state, _status, eng  # noqa: F401 (a fixture)
+from test_weighted_cpu import _append, _chunk, _decode, _evict, _state, _status, eng  # noqa: F401 (a fixture)
 
 CSRC = os.path.join(os.path.dirname(gp.__file__), "csrc")
 
@@ -63,3 +63,56 @@ def test_evict_a_page_with_fewer_references_than_requests(eng):  # noqa: F811
     assert _state(ctx, reqs) == before
     gp.gp_page_ref(ctx, page)
     assert _status(_evict, ctx, reqs, (512, 512, 512), (10, 10, 10)) == gp.GP_ERR_STATE
+
+
+class Buffer:
+    """A tensor on a device, as far as the binding looks at it."""
+    is_cuda = True
+
+    def __init__(self, count, dtype, device=0, address=1 << 20):
+        self.count, self.dtype, self.device, self.address = count, dtype, device, address
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self.count
+
+    def get_device(self):
+        return self.device
+
+    def data_ptr(self):
+        return self.address
+
+
+def test_buffers_of_the_wrong_type_or_size(eng):  # noqa: F811
+    """Every buffer of every call, one at a time: too few elements, another type."""
+    torch = pytest.importorskip("torch")
+    bf, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+    ctx, reqs = eng  # 2 layers, 8 and 2 heads of 128, 6 slots, 4 pages a request, bf16
+    weights = Buffer(2 * 6 * 2 * 4 * 256, f32)
+    rows = 257
+    far = 1 << 30
+    calls = [
+        (_append, dict(q=Buffer(rows * 1024, bf), k=Buffer(rows * 256, bf), v=Buffer(rows * 256, bf),
+                       rot=Buffer(rows * 1024, bf, address=far), w=weights)),
+        (_chunk, dict(q=Buffer(rows * 1024, bf), out=Buffer(rows * 1024, bf, address=far), w=weights)),
+        (_decode, dict(q=Buffer(3 * 1024, bf), first=Buffer(3, u8), out=Buffer(3 * 1024, f32), w=weights)),
+        (_evict, dict(w=weights)),
+    ]
+    for call, kw in calls:
+        assert _status(call, ctx, reqs, **kw) == gp.GP_ERR_STATE  # up to the device check
+        for name, b in kw.items():
+            for bad in (Buffer(b.count - 1, b.dtype, address=b.address), Buffer(b.count, torch.float16, address=b.address),
+                        Buffer(b.count, f32 if b.dtype is bf else bf, address=b.address)):
+                assert _status(call, ctx, reqs, **dict(kw, **{name: bad})) == gp.GP_ERR_INVALID, (call, name)
+            more = Buffer(b.count + 1, b.dtype, address=b.address)  # rows behind the last are left alone; weights have one shape
+            assert _status(call, ctx, reqs, **dict(kw, **{name: more})) == (
+                gp.GP_ERR_INVALID if name == "w" else gp.GP_ERR_STATE), (call, name)
+    ctx.buffers.device = 1
+    assert _status(_evict, ctx, reqs, w=weights) == gp.GP_ERR_INVALID
+    ctx.buffers.device = 0
+    assert _status(_evict, ctx, reqs, w=weights) == gp.GP_ERR_STATE
+    assert _status(_decode, ctx, reqs, **dict(calls[2][1], first=Buffer(3, torch.bool))) == gp.GP_ERR_STATE
+    bare = type(ctx)(ctx.value)  # the context's address alone: its shape is not known
+    assert _status(_evict, bare, reqs, w=Buffer(1, bf)) == gp.GP_ERR_STATE
