@@ -516,12 +516,18 @@ def _counts(reqs, *lists):
     """Host int32 arrays of per-request counts, one entry a request."""
     out = []
     for x in lists:
-        if type(x) is list or type(x) is tuple:
-            a = array.array("i", x)
-            n = len(a)
-        else:
-            a = np.ascontiguousarray(np.asarray(x, dtype=np.int32))
-            n = len(a) if a.ndim == 1 else -1
+        try:
+            if type(x) is list or type(x) is tuple:
+                a = array.array("i", x)
+                n = len(a)
+            else:
+                a = np.asarray(x)
+                if a.dtype != np.int32:  # counted one by one: a cast would cut bits off
+                    a = np.asarray(array.array("i", a.ravel().tolist()), dtype=np.int32).reshape(a.shape)
+                a = np.ascontiguousarray(a)
+                n = len(a) if a.ndim == 1 else -1
+        except (OverflowError, TypeError) as err:
+            raise GrowPageError(GP_ERR_INVALID, f"counts must be whole numbers of 32 bits: {err}") from None
         if n != len(reqs):
             raise GrowPageError(GP_ERR_INVALID, f"{len(reqs)} requests, {n} counts")
         out.append(a)

@@ -4,6 +4,7 @@ sources must not do, and what the calls and the binding refuse."""
 import os
 import re
 
+import numpy as np
 import pytest
 
 import paged_kv_cache_step_gb300 as gp
@@ -116,3 +117,17 @@ def test_buffers_of_the_wrong_type_or_size(eng):  # noqa: F811
     assert _status(_decode, ctx, reqs, **dict(calls[2][1], first=Buffer(3, torch.bool))) == gp.GP_ERR_STATE
     bare = type(ctx)(ctx.value)  # the context's address alone: its shape is not known
     assert _status(_evict, bare, reqs, w=Buffer(1, bf)) == gp.GP_ERR_STATE
+
+
+def test_counts_that_32_bits_do_not_hold(eng):  # noqa: F811
+    """A count of 64 bits is not cut to its lower half, nor a fraction to a whole number."""
+    ctx, reqs = eng
+    far = 2 ** 32 + 1  # the lower half is 1
+    for bad in ([1, 1, far], (1, 1, far), np.array([1, 1, far]), np.array([1, 1, -far]), [1, 1, 1.5], np.array([1, 1, 1.5])):
+        assert _status(_append, ctx, reqs, (0, 0, 0), bad) == gp.GP_ERR_INVALID
+        assert _status(_append, ctx, reqs, bad, (0, 0, 0)) == gp.GP_ERR_INVALID
+        assert _status(_decode, ctx, reqs, bad) == gp.GP_ERR_INVALID
+        assert _status(_evict, ctx, reqs, (2, 2, 2), bad) == gp.GP_ERR_INVALID
+    for good in ([1, 1, 1], np.array([1, 1, 1]), np.array([1, 1, 1], dtype=np.uint8), np.array([1, 9, 1, 9, 1, 9], dtype=np.int32)[::2]):
+        assert _status(_append, ctx, reqs, (0, 0, 0), good) == gp.GP_ERR_STATE
+        assert _status(_evict, ctx, reqs, (2, 2, 2), good) == gp.GP_ERR_STATE
