@@ -531,9 +531,10 @@ gp_status gp_debug_attention_plan(gp_ctx* ctx, int32_t n, const int32_t* num_tok
  * gp_debug_set_wait_limit: the limit, in SM clock cycles, of the bounded copy
  * waits of later launches of `kernel` (GP_KERNEL_COMPRESS: the compaction;
  * GP_KERNEL_SELECT: the speculative selection; GP_KERNEL_EVICT: the eviction's
- * waits for rows still to be read); 0 makes each such wait give
- * up at once, a negative value restores the default of 2^31 (about one
- * second).  A wait that gives up makes its CTA wait for the copies it already
+ * waits for rows still to be read; GP_KERNEL_CHUNK, GP_KERNEL_WEIGHTS: the
+ * waits inside the tensor-core chunk attention and its weights); 0 makes each
+ * such wait give up at once (of the last two, those for a free buffer), a
+ * negative value restores the default of 2^31 (about one second).  A wait that gives up makes its CTA wait for the copies it already
  * issued (always with the default limit), record a timeout and return;
  * gp_synchronize then reports GP_ERR_TIMEOUT.  Other kernels:
  * GP_ERR_UNSUPPORTED.  Host only; for tests of the timeout path.

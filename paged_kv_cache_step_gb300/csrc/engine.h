@@ -145,6 +145,8 @@ struct gp_ctx {
   long long wait_limit_select = gp::kDefaultWaitLimit;
   long long wait_limit_compress = gp::kDefaultWaitLimit;
   long long wait_limit_evict = gp::kDefaultWaitLimit;
+  long long wait_limit_chunk = gp::kDefaultWaitLimit;
+  long long wait_limit_weights = gp::kDefaultWaitLimit;
   int inject_fail = -1;
 };
 

@@ -1172,6 +1172,10 @@ gp_status gp_debug_set_wait_limit(gp_ctx* c, int32_t kernel, int64_t cycles) {
     c->wait_limit_select = v;
   } else if (kernel == GP_KERNEL_EVICT) {
     c->wait_limit_evict = v;
+  } else if (kernel == GP_KERNEL_CHUNK) {
+    c->wait_limit_chunk = v;
+  } else if (kernel == GP_KERNEL_WEIGHTS) {
+    c->wait_limit_weights = v;
   } else {
     return fail(c, GP_ERR_UNSUPPORTED, "kernel %d has no settable wait limit", kernel);
   }

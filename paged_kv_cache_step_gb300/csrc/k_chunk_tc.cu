@@ -55,9 +55,10 @@
 // the old maximum while the new one is found (562 us), S double buffered in steps
 // of 64 keys (717 us: products of 64 columns read A again for half as much).
 //
-// Every wait is bounded: on expiry the CTA records ERR_TIMEOUT, raises an
-// abort flag that ends every role's loop, waits (bounded) for its copies and
-// products in flight, frees its TMEM and returns.
+// Every wait is bounded (by the caller's limit, one second of clock cycles unless a
+// test sets less): on expiry the CTA records ERR_TIMEOUT, raises an abort flag that
+// ends every role's loop, waits (bounded by the full second) for its copies, products
+// and TMEM stores in flight, frees its TMEM and returns.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -80,7 +81,6 @@ constexpr int TK = 128;
 constexpr int TMEM_COLS = 512;
 constexpr float NEG = -1.0e30f;
 constexpr float LAZY = 24.f;                 // base-2 growth of a maximum that is not followed
-constexpr long long kWaitLimit = 1ll << 31;  // clock cycles (about one second)
 
 // bf16 A and B, fp32 accumulator, M = 128, N; bit 16: B is MN-major.
 __host__ __device__ constexpr uint32_t idesc(int n, bool b_mn) {
@@ -185,15 +185,20 @@ __device__ __forceinline__ void registers_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Bounded wait; gives up when the limit passes or *abort is set.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const volatile int* abort) {
+// Bounded wait; gives up when the limit passes or *abort is set.  (A try may itself
+// wait for a while; a limit of 0 is looked at by the producers, before they try.)
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const volatile int* abort, long long limit) {
   if (mbar_try(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
+    if (*abort || clock64() - t0 > limit) return false;
     if (mbar_try(bar, parity)) return true;
-    if (*abort) return false;
-    if (clock64() - t0 > kWaitLimit) return false;
   }
+}
+// The wait for what a role has in flight before it ends.
+__device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
+  const int zero = 0;
+  wait_bar(bar, parity, &zero, kDefaultWaitLimit);
 }
 
 template <typename T>
@@ -334,6 +339,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
       if (lane == 0) {
         int c = 0, nq = 0;  // tiles and items issued
         bool ok = true;
+        const bool patient = a.wait_limit != 0;
         for (int i = i0; i < i1 && ok; ++i) {
           const ChunkItem it = load_item(items + i);
           const ChunkReq rq = load_req(a.reqs + it.r);
@@ -341,7 +347,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
           auto tile = [&](const CUtensorMap* map, int t) {
             if (!ok) return;
             const int s = c % NST;
-            if (c >= NST && !(ok = wait_bar(empty(s), (uint32_t)((c / NST - 1) & 1), abort))) return;
+            if (c >= NST && !(ok = patient && wait_bar(empty(s), (uint32_t)((c / NST - 1) & 1), abort, a.wait_limit))) return;
             const int y = key_row(a, rq, it.h, t);
             const uint32_t dst = sb + (uint32_t)(L::ST + (size_t)s * L::TILE);
             mbar_expect_tx(full(s), L::TILE);
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
           // the query tiles' place is free only when the item before has formed its
           // last S: the first key tiles are on their way before
           auto queries = [&] {
-            if (!ok || (nq > 0 && !(ok = wait_bar(q_empty, (uint32_t)((nq - 1) & 1), abort)))) return;
+            if (!ok || (nq > 0 && !(ok = patient && wait_bar(q_empty, (uint32_t)((nq - 1) & 1), abort, a.wait_limit)))) return;
             const int nqt = KEYS || it.alone ? 1 : 2;
             mbar_expect_tx(q_full, (uint32_t)(nqt * L::TILE));
             for (int x = 0; x < nqt; ++x)
@@ -382,9 +388,8 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
         }
         if (!ok) timed_out();
         // every copy issued has landed before the CTA moves on (bounded)
-        const int zero = 0;
-        for (int x = c > NST ? c - NST : 0; x < c; ++x) wait_bar(full(x % NST), (uint32_t)((x / NST) & 1), &zero);
-        if (nq > 0) wait_bar(q_full, (uint32_t)((nq - 1) & 1), &zero);
+        for (int x = c > NST ? c - NST : 0; x < c; ++x) drain_bar(full(x % NST), (uint32_t)((x / NST) & 1));
+        if (nq > 0) drain_bar(q_full, (uint32_t)((nq - 1) & 1));
       }
       __syncwarp();
     } else if (warp == 1) {
@@ -394,7 +399,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
       int no[2] = {0, 0};     // items per group
       bool ok = true;
       auto wait = [&](uint32_t bar, int phase) {
-        ok = ok && __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(phase & 1), abort));
+        ok = ok && __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(phase & 1), abort, a.wait_limit));
       };
       auto stage = [&](int k) { return sb + (uint32_t)(L::ST + (size_t)(k % NST) * L::TILE); };
       auto arrived = [&](int k) { wait(full(k % NST), k / NST); };
@@ -494,8 +499,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
       if (!ok && lane == 0) timed_out();
       // every product issued has completed before TMEM is released (bounded)
       commit(mma_done);
-      const int zero = 0;
-      wait_bar(mma_done, 0u, &zero);
+      drain_bar(mma_done, 0u);
       __syncwarp();
     }
   } else {
@@ -537,13 +541,13 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
       float m = NEG, l = 0.f;
       for (int j = 0; j < cnt; ++j) {
         const int kt = it.kb + (KEYS ? 2 * j + x : j);  // key tile
-        ok = __all_sync(0xffffffffu, wait_bar(s_ready(x), (uint32_t)(ns & 1), abort));
+        ok = __all_sync(0xffffffffu, wait_bar(s_ready(x), (uint32_t)(ns & 1), abort, a.wait_limit));
         if (!ok) break;
         tc_fence_after();
         if (!live) {
           if (last_of(kt)) {
             const int k = c + 2 * w.n - 1;
-            ok = __all_sync(0xffffffffu, wait_bar(full(k % NST), (uint32_t)((k / NST) & 1), abort));
+            ok = __all_sync(0xffffffffu, wait_bar(full(k % NST), (uint32_t)((k / NST) & 1), abort, a.wait_limit));
             if (!ok) break;
             zero_rows(k, kt * TK + row >= total);
           }
@@ -620,7 +624,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
         weigh(1);
         if (last_of(kt)) {
           const int k = c + 2 * w.n - 1;  // the item's last load
-          ok = __all_sync(0xffffffffu, wait_bar(full(k % NST), (uint32_t)((k / NST) & 1), abort));
+          ok = __all_sync(0xffffffffu, wait_bar(full(k % NST), (uint32_t)((k / NST) & 1), abort, a.wait_limit));
           if (!ok) break;
           zero_rows(k, kt * TK + row >= total);
         }
@@ -648,7 +652,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
           po[128 + row] = 0.f;
         }
       } else {
-        ok = __all_sync(0xffffffffu, wait_bar(o_done(x), (uint32_t)(no & 1), abort));
+        ok = __all_sync(0xffffffffu, wait_bar(o_done(x), (uint32_t)(no & 1), abort, a.wait_limit));
         if (!ok) break;
         tc_fence_after();
         const size_t at = (size_t)(rq.row0 + t) * a.Hq + it.h * G + row % G;
@@ -690,6 +694,7 @@ __global__ void __launch_bounds__(NT, 1) k_chunk_tc(const __grid_constant__ Chun
       c += 2 * w.n;
     }
     if (!ok && lane == 0) timed_out();
+    tmem_wait_st();  // a loop that was left between a store and its wait
   }
 
   tc_fence_before();
@@ -841,14 +846,15 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
   if (warp == 0) {
     // ---- producer: an item's two K tiles, then its query tiles -------------------
     if (lane == 0) {
-      int c = 0, n = 0;  // query tiles and items issued
+      int c = 0, n = 0;  // query tiles and pages issued
       bool ok = true;
+      const bool patient = a.wait_limit != 0;
       for (int i = i0; i < i1 && ok; ++i) {
         const WeightItem it = load_item(a.witems + i);
         const ChunkReq rq = load_req(a.reqs + it.r);
-        for (int pg = it.page; pg < it.page + it.pages; ++pg, ++n) {
+        for (int pg = it.page; pg < it.page + it.pages; ++pg) {
           const int b = n & 1;
-          if (n >= 2 && !(ok = wait_bar(k_empty(b), (uint32_t)((n / 2 - 1) & 1), abort))) break;
+          if (n >= 2 && !(ok = patient && wait_bar(k_empty(b), (uint32_t)((n / 2 - 1) & 1), abort, a.wait_limit))) break;
           const int y = key_row(a, rq, it.h, 2 * pg);
           mbar_expect_tx(k_full(b), 2 * L::TILE);
           for (int x = 0; x < 2; ++x)
@@ -856,9 +862,10 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
             for (int d = 0; d < D; d += 64)
               tma_load_2d(sb + (uint32_t)(L::K + (size_t)(2 * b + x) * L::TILE + d / 64 * L::HALF), &a.kmap, d, y + x * TK,
                           k_full(b));
+          ++n;
           for (int q = it.qb; q < it.qe; ++q, ++c) {
             const int s = c % NQ;
-            if (c >= NQ && !(ok = wait_bar(q_empty(s), (uint32_t)((c / NQ - 1) & 1), abort))) break;
+            if (c >= NQ && !(ok = patient && wait_bar(q_empty(s), (uint32_t)((c / NQ - 1) & 1), abort, a.wait_limit))) break;
             mbar_expect_tx(q_full(s), L::TILE);
 #pragma unroll
             for (int d = 0; d < D; d += 64)
@@ -869,9 +876,8 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
         }
       }
       if (!ok) timed_out();
-      const int zero = 0;
-      for (int x = c > NQ ? c - NQ : 0; x < c; ++x) wait_bar(q_full(x % NQ), (uint32_t)((x / NQ) & 1), &zero);
-      for (int x = n > 2 ? n - 2 : 0; x < n; ++x) wait_bar(k_full(x & 1), (uint32_t)((x / 2) & 1), &zero);
+      for (int x = c > NQ ? c - NQ : 0; x < c; ++x) drain_bar(q_full(x % NQ), (uint32_t)((x / NQ) & 1));
+      for (int x = n > 2 ? n - 2 : 0; x < n; ++x) drain_bar(k_full(x & 1), (uint32_t)((x / 2) & 1));
     }
     __syncwarp();
   } else if (warp < 3) {
@@ -880,7 +886,7 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
     int c = 0, n = 0;
     bool ok = true;
     auto wait = [&](uint32_t b, int phase) {
-      ok = ok && __all_sync(0xffffffffu, wait_bar(b, (uint32_t)(phase & 1), abort));
+      ok = ok && __all_sync(0xffffffffu, wait_bar(b, (uint32_t)(phase & 1), abort, a.wait_limit));
     };
     for (int i = i0; i < i1 && ok; ++i) {
       const WeightItem it = load_item(a.witems + i);
@@ -914,8 +920,7 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
     }
     if (!ok && lane == 0) timed_out();
     commit(mma_done(x));
-    const int zero = 0;
-    wait_bar(mma_done(x), 0u, &zero);
+    drain_bar(mma_done(x), 0u);
     __syncwarp();
   } else if (warp == 3) {
     // ---- -L / c of the query tiles, in three bf16 parts ---------------------------
@@ -934,7 +939,7 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
             const int row = 32 * k + lane, t = q * TOK + row / G;
             v[k] = t < rq.nnew ? -inv_sc * __ldcg(a.lse + (size_t)(rq.row0 + t) * a.Hq + it.h * G + row % G) : 0.f;
           }
-          if (c >= 2) ok = __all_sync(0xffffffffu, wait_bar(t_empty(b), (uint32_t)((c / 2 - 1) & 1), abort));
+          if (c >= 2) ok = __all_sync(0xffffffffu, wait_bar(t_empty(b), (uint32_t)((c / 2 - 1) & 1), abort, a.wait_limit));
           if (!ok) break;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -970,7 +975,7 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
         float2 w[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         for (int q = it.qb; q < it.qe; ++q, ++c) {
           const int z = c & 1;
-          ok = __all_sync(0xffffffffu, wait_bar(s_ready(x, z), (uint32_t)((c / 2) & 1), abort));
+          ok = __all_sync(0xffffffffu, wait_bar(s_ready(x, z), (uint32_t)((c / 2) & 1), abort, a.wait_limit));
           if (!ok) break;
           tc_fence_after();
           // of this half's columns lo .. hi - 1 count: rows of tokens that see the slot and exist

@@ -518,8 +518,10 @@ gp_status gp_chunk_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_reque
     a.part = reinterpret_cast<float*>(static_cast<char*>(c->chunk.p) + at_part);
     a.wpart = reinterpret_cast<float*>(static_cast<char*>(c->chunk.p) + at_wpart);
     a.err = c->err_dev;
+    a.wait_limit = c->wait_limit_chunk;
     st = timed_launch(c, GP_KERNEL_CHUNK, "chunk_attention", [&] { return launch_chunk_tc(a, c->stream); });
     if (st != GP_OK || !weights_dev) return st;
+    a.wait_limit = c->wait_limit_weights;
     return timed_launch(c, GP_KERNEL_WEIGHTS, "chunk_weights", [&] { return launch_chunk_weights_tc(a, c->stream); });
   }
   ChunkArgs a{};

@@ -221,6 +221,7 @@ struct ChunkTcArgs {
   float* part;                 // partial outputs, chunk_part_floats(D) each
   float* wpart;                // partial weights, 256 each
   int* err;
+  long long wait_limit;        // clock cycles
 };
 // A partial: outputs [D / 4][128 rows][4], then 128 maxima, then 128 sums.
 __host__ __device__ constexpr size_t chunk_part_floats(int D) { return (size_t)128 * (D + 2); }

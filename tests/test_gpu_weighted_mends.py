@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import paged_kv_cache_step_gb300 as gp
-from test_gpu_weighted import EPS, Engine, bits, softmax_reference
+from test_gpu_weighted import EPS, Engine, bits, check_chunk, softmax_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +105,32 @@ def test_descriptors_that_grow_while_calls_are_in_flight():
             e.close()
     for a, b in zip(*results):
         assert torch.equal(bits(a), bits(b))
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(16, 4, 128), (8, 4, 64)])
+@pytest.mark.parametrize("kernel", [gp.GP_KERNEL_CHUNK, gp.GP_KERNEL_WEIGHTS])
+def test_chunk_waits_that_give_up_are_reported(kernel, hq, hkv, d):
+    """Pairs of query tiles, single ones and joins, more tiles a CTA than its buffers
+    hold.  Without patience every CTA stops with copies and products in flight; with
+    a little some may.  The next call is right."""
+    cached, new = [20000, 0, 52000], [900, 300, 3]
+    e = Engine([82, 2, 204], L=1, hq=hq, hkv=hkv, d=d, seed=64)
+    try:
+        e.fill([a + b for a, b in zip(cached, new)])
+        q = e.randn(sum(new), hq, d).bfloat16()
+        out = torch.empty_like(q)
+        for limit in (0, 1, 300, 3000, 30000, 0):
+            gp.gp_debug_set_wait_limit(e.ctx, kernel, limit)
+            gp.gp_chunk_attention(e.ctx, 0, e.reqs, cached, new, q, out, e.w.clone())
+            try:
+                gp.gp_synchronize(e.ctx)
+                assert limit > 0
+            except gp.GrowPageError as err:
+                assert err.status == gp.GP_ERR_TIMEOUT
+        gp.gp_debug_set_wait_limit(e.ctx, kernel, -1)
+        w = e.w.clone()
+        gp.gp_chunk_attention(e.ctx, 0, e.reqs, cached, new, q, out, w)
+        gp.gp_synchronize(e.ctx)
+        check_chunk(e, 0, cached, new, q, out, e.w, w, True)
+    finally:
+        e.close()
