@@ -434,7 +434,10 @@ gp_status gp_decode_attention_weighted(gp_ctx* ctx, int32_t layer, int32_t n, co
  * out = sum a v.  q_dev: device [rows][Hq][d] q_dtype, ROTATED, packed as in
  * gp_append_tokens; out_dev: the same shape and type; both 16-byte aligned.
  * With weights_dev, the weights of every token are added; NULL leaves that
- * out.  The rows of K and V of the attended tokens must be finite; cache slots
+ * out.  Nothing takes added weights back: for drafted tokens that may yet be
+ * rejected, call with NULL, and once they are settled again with weights_dev and
+ * the accepted count of each request as num_new (their rows of q packed anew).
+ * The rows of K and V of the attended tokens must be finite; cache slots
  * past num_cached[r] + num_new[r] may hold any bits.  out_dev must not overlap
  * q_dev.  bf16 caches and queries run on the tensor-core kernels, which hold
  * the softmax weights to 2^-15 of themselves for the product with V (out is

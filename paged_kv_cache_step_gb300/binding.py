@@ -570,7 +570,8 @@ def gp_decode_attention_weighted(ctx, layer: int, reqs, num_tokens, q_dev, first
 
 def gp_chunk_attention(ctx, layer: int, reqs, num_cached, num_new, q_dev, out_dev, weights_dev=None):
     """Causal attention of each request's num_new last tokens over its cache;
-    q_dev (rotated) and out_dev [rows][Hq][d] of q_dtype, packed."""
+    q_dev (rotated) and out_dev [rows][Hq][d] of q_dtype, packed.  Added weights
+    stay: of drafted tokens, add the accepted ones' in a second call."""
     nc, nn = _counts(reqs, num_cached, num_new)
     held = _held(ctx)
     q = _total(nn) * held.q_row

@@ -134,3 +134,33 @@ def test_chunk_waits_that_give_up_are_reported(kernel, hq, hkv, d):
         check_chunk(e, 0, cached, new, q, out, e.w, w, True)
     finally:
         e.close()
+
+
+def test_only_accepted_drafted_tokens_are_counted():
+    """Drafted tokens attend without weights; the accepted ones' are added by a second
+    call over them, and the next append takes the rejected ones' slots."""
+    cached, drafted, accepted = [700, 255, 40], [5, 6, 3], [2, 6, 0]
+    e = Engine([3, 2, 1], L=1, seed=65)
+    try:
+        e.fill(cached)
+        x = [e.randn(sum(drafted), h, 128).bfloat16() for h in (8, 2, 2)]
+        for r, req in enumerate(e.reqs):
+            req.pos = cached[r]
+        rot = torch.empty_like(x[0])
+        gp.gp_append_tokens(e.ctx, 0, e.reqs, cached, drafted, *x, rot, e.w)
+        before, out = e.w.clone(), torch.empty_like(rot)
+        gp.gp_chunk_attention(e.ctx, 0, e.reqs, cached, drafted, rot, out, None)
+        gp.gp_synchronize(e.ctx)
+        assert torch.equal(bits(e.w), bits(before))
+        taken = torch.cat([torch.arange(sum(drafted[:r]), sum(drafted[:r]) + a) for r, a in enumerate(accepted)]).cuda()
+        q, again = rot[taken].contiguous(), torch.empty_like(rot[taken])
+        gp.gp_chunk_attention(e.ctx, 0, e.reqs, cached, accepted, q, again, e.w)
+        gp.gp_synchronize(e.ctx)
+        check_chunk(e, 0, cached, accepted, q, again, before, e.w, True)
+        now = [c + a for c, a in zip(cached, accepted)]
+        gp.gp_append_tokens(e.ctx, 0, e.reqs, now, [1] * 3, None, x[1][:3], x[2][:3], None, e.w)
+        gp.gp_synchronize(e.ctx)
+        for r, t in enumerate(now):
+            assert not e.w[0, r, :, t].any() and torch.equal(e.rows(e.v, r, 0, 1, t + 1)[t], x[2][r, 1].double())
+    finally:
+        e.close()
