@@ -448,19 +448,23 @@ gp_status gp_chunk_attention(gp_ctx* ctx, int32_t layer, int32_t n, const gp_req
                              void* out_dev, float* weights_dev);
 
 /* gp_evict_weighted: evict request r's num_tokens[r] tokens down to
- * keep_tokens[r] >= 1, per (layer, KV head): the min(recent_window, keep) most
- * recent tokens stay, and of the others the keep - that many of largest
- * accumulated weight (equal weights: the lower slot; NaN counts as larger than
- * any number).  K, V and the weights of the kept tokens move, in order, to
- * the logical slots [0, keep); num_pages is unchanged and the slots from keep
- * on become free, their contents unspecified.  A request with num_tokens <=
- * keep_tokens is left as it is.  Copy-on-write as in gp_compress_hold for the
- * requests that evict (GP_ERR_NO_PAGES: nothing changed); a page of several of
- * them must have a reference for each (GP_ERR_INVALID).  num_tokens and
- * keep_tokens: HOST int32 [n].  Runs on the compaction stream if one is set,
+ * keep_tokens[r] >= 1, per (layer, KV head): the min(recent_window, keep)
+ * most recent tokens stay, and of the others the keep - that many of largest
+ * accumulated weight (equal weights: the lower slot; NaN counts as larger
+ * than any number). K, V and the weights of the kept tokens move, in order,
+ * to the logical slots [0, keep); num_pages is unchanged and the slots from
+ * keep on become free, their contents unspecified. A request with num_tokens
+ * <= keep_tokens is left as it is. Copy-on-write as in gp_compress_hold for
+ * the requests that evict (GP_ERR_NO_PAGES: nothing changed); a page of
+ * several of them must have a reference for each (GP_ERR_INVALID). Shared
+ * pages past keep are replaced too, as they hold the next tokens. A caller
+ * that wants the emptied pages back, [ceil(keep / 256), num_pages), unrefs
+ * each and lowers num_pages, at once also with a side stream: an append to
+ * such a page waits for the eviction that still reads it. num_tokens and
+ * keep_tokens: HOST int32 [n]. Runs on the compaction stream if one is set,
  * with gp_compress_hold's rules, which hold for the weights of the evicted
- * requests as for their K/V; a gp_boundary_demand result of the slots is stale
- * afterwards.  gp_debug_keep_mask gives the kept sets. */
+ * requests as for their K/V; a gp_boundary_demand result of the slots is
+ * stale afterwards. gp_debug_keep_mask gives the kept sets. */
 gp_status gp_evict_weighted(gp_ctx* ctx, int32_t n, gp_request* reqs, const int32_t* num_tokens,
                             const int32_t* keep_tokens, float* weights_dev);
 

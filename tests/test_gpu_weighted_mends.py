@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import paged_kv_cache_step_gb300 as gp
-from test_gpu_weighted import EPS, Engine, bits, check_chunk, softmax_reference
+from test_gpu_weighted import EPS, Engine, bits, check_chunk, kept_slots, softmax_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -163,4 +163,55 @@ def test_only_accepted_drafted_tokens_are_counted():
         for r, t in enumerate(now):
             assert not e.w[0, r, :, t].any() and torch.equal(e.rows(e.v, r, 0, 1, t + 1)[t], x[2][r, 1].double())
     finally:
+        e.close()
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_emptied_pages_go_to_another_request(side):
+    """After an eviction its emptied pages are given back and taken by a request that
+    appends to them at once, while the eviction may not have read them yet."""
+    e = Engine([8, 1], seed=66, spare=1, cap=8)
+    stream = torch.cuda.Stream()
+    try:
+        T, keep = 2000, 300
+        old, new = e.reqs
+        prefix = old.pages[7]  # a shared page past the budget: replaced, and the fresh one given back
+        e.fill([T + 1, 0])
+        # the kernels' first launches load them, which may wait for the device
+        gp.gp_evict_weighted(e.ctx, [old], [T + 1], [T], e.w)
+        gp.gp_append_tokens(e.ctx, 0, [new], [0], [1], None, e.randn(1, 2, 128).bfloat16(), e.randn(1, 2, 128).bfloat16(), None, None)
+        gp.gp_synchronize(e.ctx)
+        gp.gp_page_ref(e.ctx, prefix)
+        k0, v0, w0, t0 = e.k.clone(), e.v.clone(), e.w.clone(), [x.pages for x in e.reqs]
+        rows = [e.randn(1000, 2, 128).bfloat16() for _ in range(2)]
+        if side:
+            gp.gp_set_compaction_stream(e.ctx, stream)
+        torch.cuda.synchronize()
+        if side:
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(50_000_000)
+        gp.gp_evict_weighted(e.ctx, [old], [T], [keep], e.w)
+        assert prefix not in old.pages and gp.gp_page_refcount(e.ctx, prefix) == 1
+        for page in old.pages[2:]:
+            gp.gp_page_unref(e.ctx, page)
+        old.num_pages = 2
+        taken = [gp.gp_page_alloc(e.ctx) for _ in range(3)]
+        assert len(set(taken) & set(t0[0])) >= 2  # pages that the eviction reads
+        new.table[1:4] = taken
+        new.num_pages = 4
+        for layer in range(2):
+            gp.gp_append_tokens(e.ctx, layer, [new], [0], [1000], None, *rows, None, e.w)
+        gp.gp_wait_compaction(e.ctx)
+        gp.gp_synchronize(e.ctx)
+        torch.cuda.synchronize()
+        for layer in range(2):
+            for h in range(2):
+                assert torch.equal(e.rows(e.v, 1, layer, h, 1000), rows[1][:, h].double())
+                idx = torch.as_tensor(kept_slots(w0[layer, 0, h].cpu().numpy(), T, keep, e.recent), device="cuda")
+                src = torch.as_tensor(t0[0], device="cuda")[idx // 256]
+                for cache, was in ((e.k, k0), (e.v, v0)):
+                    assert torch.equal(e.rows(cache, 0, layer, h, keep), was[layer, src, h, idx % 256].double())
+                assert torch.equal(e.w[layer, 0, h, :keep], w0[layer, 0, h, idx])
+    finally:
+        gp.gp_set_compaction_stream(e.ctx, None)
         e.close()
