@@ -818,7 +818,7 @@ __global__ void __launch_bounds__(WNT, 1) k_chunk_weights_tc(const __grid_consta
     fail[0] = 0;
     fail[1] = 0;
   }
-  // the constant parts of the operands that carry L (see ROW16's layout below)
+  // the constant parts of the operands that carry L (row16 has their layout)
   for (int row = tid; row < 128; row += WNT) {
     unsigned char* at = sm + row16(row);
     *reinterpret_cast<uint4*>(at + L::ONES) = make_uint4(0x3f803f80u, 0x00003f80u, 0u, 0u);  // 1, 1, 1, 0, ...

@@ -28,7 +28,8 @@
 // Bounded by HBM: kept rows are read and written once.  Ten requests of 77 671
 // tokens to 37 %, 32 layers of 8 heads, d = 128, bf16: 7.5 GB moved in 1176 us, 6.4
 // TB/s, 94 % of the copy rate, after 99 us of selection (which is bound by the
-// issue of its five passes over the keys in shared memory).
+// issue of its passes over the keys in shared memory: three at most that count
+// digits, and the ordered one).
 #include <cstdint>
 
 #include "chained.cuh"
@@ -51,8 +52,8 @@ __device__ __forceinline__ unsigned okey(float v) {
 }
 
 // A warp has consecutive words (32 slots each) of the unit.  STAGED: the keys
-// are formed once and stay in shared memory for the five passes over them, else
-// the weights are read again.  (In registers, 16 a thread, they left one CTA an
+// are formed once and stay in shared memory for the passes over them, else the
+// weights are read again at each.  (In registers, 16 a thread, they left one CTA an
 // SM: 96 us against 70 for 1024 units of 8192 slots, read again each pass.)
 template <bool STAGED>
 __global__ void __launch_bounds__(SNT) k_evict_select(const __grid_constant__ EvictArgs a) {

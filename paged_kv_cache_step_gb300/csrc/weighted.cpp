@@ -146,11 +146,14 @@ struct ChunkPlan {
 // Attention: pairs of query tiles that follow each other (a key tile costs two
 // products' time), and the last tiles alone, their key tiles split between the
 // groups (one).  A piece's fixed cost is the time to load Q and to empty the
-// pipeline, about three tiles (6007 tokens: 517, 515, 509, 513 and 514 us when it
-// is taken as 1, 2, 3, 4 and 6).  The last tiles need a launch of their own, about
+// pipeline, about three tiles; taken as 1, 2, 3, 4 or 6, ten calls from 40 drafted
+// tokens to 6007 of a prompt differ by 4 % at most, but for one prompt of 2000 tokens
+// (68, 68, 62, 62 and 62 us).  The last tiles need a launch of their own, about
 // 8 us; beside pairs, up to 12 key tiles of them a CTA (about 0.6 us each) go
-// along as pairs without a second tile instead, at twice the cost (five ragged
-// prompts, d = 64: 47 us in one launch, 55 in two).
+// along as pairs without a second tile instead, at twice the cost (in one launch and
+// in two: five ragged prompts, d = 64, 51 and 55 us; eight of about 500 tokens 57 and
+// 66; one of 2000 62 and 71; 64 chunks of 40 to 100 tokens, more than 12 tiles a
+// CTA, 115 and 137).
 void plan_chunk(int n, const int32_t* cached, const int32_t* fresh, int Hkv, int G, int ctas, bool weights,
                 ChunkPlan* p) {
   const int tok = 128 / G;
@@ -228,9 +231,9 @@ void plan_chunk(int n, const int32_t* cached, const int32_t* fresh, int Hkv, int
   }
   if (!weights) return;
   // Weights: a page against the query tiles that see it; loading the page
-  // costs about three query tiles' products (274, 268, 264 and 261 us at 1, 2, 3
-  // and 4 for the 6007 tokens, 28.4, 27.6, 28.3 and 28.9 for ragged prompts).  The pages that every token sees
-  // are alike.
+  // costs about three query tiles' products (278, 273, 268, 266 and 269 us at 1, 2, 3,
+  // 4 and 6 for the 6007 tokens, 28.0, 27.1, 27.4, 27.5 and 29.9 for ragged prompts,
+  // others within 4 %).  The pages that every token sees are alike.
   jobs.clear();
   std::vector<WeightItem> wof;
   for (int r = 0; r < n; ++r) {
