@@ -146,9 +146,9 @@ struct ChunkPlan {
 // Attention: pairs of query tiles that follow each other (a key tile costs two
 // products' time), and the last tiles alone, their key tiles split between the
 // groups (one).  A piece's fixed cost is the time to load Q and to empty the
-// pipeline, about three tiles; taken as 1, 2, 3, 4 or 6, ten calls from 40 drafted
-// tokens to 6007 of a prompt differ by 4 % at most, but for one prompt of 2000 tokens
-// (68, 68, 62, 62 and 62 us).  The last tiles need a launch of their own, about
+// pipeline, about three tiles: of 1, 2, 3, 4 and 6, three keeps each of ten calls
+// (drafted tokens, many short chunks, prompts of 300 to 6007 tokens) within 6 % of
+// its best; the others cost one of them 8 to 10 %.  The last tiles need a launch of their own, about
 // 8 us; beside pairs, up to 12 key tiles of them a CTA (about 0.6 us each) go
 // along as pairs without a second tile instead, at twice the cost (in one launch and
 // in two: five ragged prompts, d = 64, 51 and 55 us; eight of about 500 tokens 57 and
@@ -232,8 +232,8 @@ void plan_chunk(int n, const int32_t* cached, const int32_t* fresh, int Hkv, int
   if (!weights) return;
   // Weights: a page against the query tiles that see it; loading the page
   // costs about three query tiles' products (278, 273, 268, 266 and 269 us at 1, 2, 3,
-  // 4 and 6 for the 6007 tokens, 28.0, 27.1, 27.4, 27.5 and 29.9 for ragged prompts,
-  // others within 4 %).  The pages that every token sees are alike.
+  // 4 and 6 for the 6007 tokens, 28.0, 27.1, 27.4, 27.5 and 29.9 for ragged prompts;
+  // of the ten calls three keeps each within 8 % of its best).  The pages that every token sees are alike.
   jobs.clear();
   std::vector<WeightItem> wof;
   for (int r = 0; r < n; ++r) {
