@@ -62,7 +62,7 @@ typedef enum {
   GP_ERR_INVALID = 1,     /* bad argument; nothing changed */
   GP_ERR_NO_PAGES = 2,    /* the free pool cannot supply the pages; nothing changed */
   GP_ERR_NO_SLOTS = 3,    /* no free summary slot; nothing changed */
-  GP_ERR_CUDA = 4,        /* a CUDA runtime call failed (text in gp_last_error) */
+  GP_ERR_CUDA = 4,        /* a CUDA runtime call failed, or host memory ran out (text in gp_last_error) */
   GP_ERR_TIMEOUT = 5,     /* a bounded device-side wait gave up (about one second of SM
                              clock); the kernel drained its copies and returned, so the
                              context stays usable, but that launch's outputs are

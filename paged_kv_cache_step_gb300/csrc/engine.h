@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <cstdarg>
 #include <cstdio>
+#include <exception>
 #include <set>
 #include <string>
 #include <unordered_set>
@@ -164,6 +165,17 @@ inline gp_status fail(gp_ctx* c, gp_status st, const char* fmt, ...) {
   return st;
 }
 
+// What an entry point returns for an exception, none of which leaves it: the only
+// ones are of allocations, all of which come before the call changes anything.
+inline gp_status no_memory(gp_ctx* c) {
+  try {
+    return fail(c, GP_ERR_CUDA, "out of host memory");
+  } catch (const std::exception&) {
+    if (c) c->err.clear();
+    return GP_ERR_CUDA;
+  }
+}
+
 #define GP_CUDA(ctx, call)                                                              \
   do {                                                                                  \
     cudaError_t e_ = (call);                                                            \
@@ -234,6 +246,7 @@ gp_status timed_launch_on(gp_ctx* c, cudaStream_t s, int kernel, const char* nam
   }
   cudaEvent_t a = nullptr, b = nullptr;
   if (c->timing) {
+    if (c->timed.size() == c->timed.capacity()) c->timed.reserve(2 * c->timed.size() + 16);
     a = take_event(c);
     b = take_event(c);
     cudaEventRecord(a, s);
@@ -242,7 +255,7 @@ gp_status timed_launch_on(gp_ctx* c, cudaStream_t s, int kernel, const char* nam
   if (e != cudaSuccess) return fail(c, GP_ERR_CUDA, "%s launch failed: %s", name, cudaGetErrorString(e));
   if (c->timing) {
     cudaEventRecord(b, s);
-    c->timed.push_back({kernel, a, b});
+    c->timed.push_back({kernel, a, b});  // (room made above)
   }
   return GP_OK;
 }

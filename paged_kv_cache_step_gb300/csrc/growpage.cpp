@@ -1402,22 +1402,26 @@ gp_status decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_request
 
 gp_status gp_decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_request* reqs,
                               const int32_t* num_tokens, const void* q_dev, const uint8_t* first_dev,
-                              float* out_dev) {
+                              float* out_dev) try {
   gp_status st = need_device(c);
   if (st != GP_OK) return st;
   if ((st = check_decode(c, layer, n, reqs, num_tokens, !q_dev || !first_dev || !out_dev)) != GP_OK) return st;
   return decode_attention(c, layer, n, reqs, num_tokens, q_dev, first_dev, out_dev, nullptr);
+} catch (const std::exception&) {
+  return no_memory(c);
 }
 
 gp_status gp_decode_attention_weighted(gp_ctx* c, int32_t layer, int32_t n, const gp_request* reqs,
                                        const int32_t* num_tokens, const void* q_dev, const uint8_t* first_dev,
-                                       float* out_dev, float* weights_dev) {
+                                       float* out_dev, float* weights_dev) try {
   if (!c) return GP_ERR_INVALID;
   gp_status st = check_decode(c, layer, n, reqs, num_tokens, !q_dev || !out_dev || !weights_dev);
   if (st == GP_OK && (reinterpret_cast<uintptr_t>(weights_dev) & 3u))
     return fail(c, GP_ERR_INVALID, "the weights must be 4-byte aligned");
   if (st != GP_OK || (st = ready_call(c)) != GP_OK) return st;
   return decode_attention(c, layer, n, reqs, num_tokens, q_dev, first_dev, out_dev, weights_dev);
+} catch (const std::exception&) {
+  return no_memory(c);
 }
 
 // ---- asynchronous compaction (side stream) ------------------------------------

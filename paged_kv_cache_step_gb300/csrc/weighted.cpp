@@ -331,7 +331,7 @@ void plan_tiles(int n, const int32_t* cached, const int32_t* fresh, int Hkv, int
 
 gp_status gp_append_tokens(gp_ctx* c, int32_t layer, int32_t n, const gp_request* reqs, const int32_t* num_cached,
                            const int32_t* num_new, const void* q_dev, const void* k_dev, const void* v_dev,
-                           void* q_rot_dev, float* weights_dev) {
+                           void* q_rot_dev, float* weights_dev) try {
   if (!c) return GP_ERR_INVALID;
   gp_status st;
   const gp_config& g = c->cfg;
@@ -417,10 +417,12 @@ gp_status gp_append_tokens(gp_ctx* c, int32_t layer, int32_t n, const gp_request
   for (int r = 0; r < n; ++r)  // a demand result over the old rows is stale
     if (num_new[r] > 0) ++c->slot_gen[reqs[r].slot];
   return GP_OK;
+} catch (const std::exception&) {
+  return no_memory(c);
 }
 
 gp_status gp_chunk_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_request* reqs, const int32_t* num_cached,
-                             const int32_t* num_new, const void* q_dev, void* out_dev, float* weights_dev) {
+                             const int32_t* num_new, const void* q_dev, void* out_dev, float* weights_dev) try {
   if (!c) return GP_ERR_INVALID;
   gp_status st;
   const gp_config& g = c->cfg;
@@ -561,10 +563,12 @@ gp_status gp_chunk_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_reque
   st = timed_launch(c, GP_KERNEL_CHUNK, "chunk_attention", [&] { return launch_chunk(a, c->stream); });
   if (st != GP_OK || !weights_dev) return st;
   return timed_launch(c, GP_KERNEL_WEIGHTS, "chunk_weights", [&] { return launch_chunk_weights(a, c->stream); });
+} catch (const std::exception&) {
+  return no_memory(c);
 }
 
 gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_t* num_tokens,
-                            const int32_t* keep_tokens, float* weights_dev) {
+                            const int32_t* keep_tokens, float* weights_dev) try {
   if (!c) return GP_ERR_INVALID;
   gp_status st;
   const gp_config& g = c->cfg;
@@ -644,20 +648,49 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
   std::memcpy(host + at_req, er.data(), sizeof(EvictReq) * (size_t)n);
   int32_t* old_bt = reinterpret_cast<int32_t*>(host + at_old);
   int32_t* new_bt = reinterpret_cast<int32_t*>(host + at_new);
+  // everything that the call leaves behind is allocated before it changes anything
+  std::vector<CompressRec> records(n);
+  for (int r = 0; r < n; ++r) {
+    CompressRec& rec = records[r];
+    rec.num_pages = reqs[r].num_pages;
+    rec.evict = true;
+    rec.tokens = er[r].T;
+    rec.kept = er[r].items ? er[r].keep : 0;
+    rec.pitch = er[r].idx_pitch;
+    rec.mask_off = er[r].idx_off;  // c->evict starts with the kept slots
+  }
+  std::unordered_set<int32_t> pages, slots;  // of a compaction on the side stream
+  if (c->cstream) {
+    size_t most = cow;
+    for (int r = 0; r < n; ++r) most += reqs[r].num_pages;
+    pages.reserve(most);
+    for (int r = 0; r < n; ++r) {
+      slots.insert(reqs[r].slot);
+      pages.insert(reqs[r].block_table, reqs[r].block_table + reqs[r].num_pages);
+    }
+    auto it = c->free_pages.begin();  // those that the copies take
+    for (size_t i = 0; i < cow; ++i) pages.insert(*it++);
+  }
+  std::vector<std::set<int32_t>::node_type> taken;  // free pages, as nodes that the released ones go back by
+  taken.reserve(cow);
   // copy-on-write targets as in Compress & Hold (cannot fail now): lowest id first, ascending logical order
   for (int r = 0; r < n; ++r)
     for (int j = 0; j < reqs[r].num_pages; ++j) {
       const int32_t pg = reqs[r].block_table[j];
       int32_t to = pg;
-      if (er[r].items && c->refcnt[pg] > 1) gp_page_alloc(c, &to);
+      if (er[r].items && c->refcnt[pg] > 1) {
+        taken.push_back(c->free_pages.extract(c->free_pages.begin()));
+        to = taken.back().value();
+        c->refcnt[to] = 1;
+      }
       old_bt[(size_t)r * maxp + j] = pg;
       new_bt[(size_t)r * maxp + j] = to;
     }
   auto roll_back = [&](gp_status why) {
-    for (int r = 0; r < n; ++r)
-      for (int j = 0; j < reqs[r].num_pages; ++j)
-        if (new_bt[(size_t)r * maxp + j] != old_bt[(size_t)r * maxp + j])
-          gp_page_unref(c, new_bt[(size_t)r * maxp + j]);
+    for (auto& node : taken) {
+      c->refcnt[node.value()] = 0;
+      c->free_pages.insert(std::move(node));
+    }
     return why;
   };
   if ((st = staging_upload(c, *slot, lay.bytes)) != GP_OK) return roll_back(st);
@@ -704,33 +737,25 @@ gp_status gp_evict_weighted(gp_ctx* c, int32_t n, gp_request* reqs, const int32_
   if (c->cstream) {
     GP_CUDA(c, cudaEventRecord(c->ev_done, ks));
     c->compaction_pending = true;
-    c->pending_pages.clear();
-    c->pending_slots.clear();
-    for (int r = 0; r < n; ++r) {
-      c->pending_slots.insert(reqs[r].slot);
-      for (int j = 0; j < reqs[r].num_pages; ++j) {
-        c->pending_pages.insert(old_bt[(size_t)r * maxp + j]);
-        c->pending_pages.insert(new_bt[(size_t)r * maxp + j]);
-      }
-    }
+    c->pending_pages.swap(pages);
+    c->pending_slots.swap(slots);
   }
-  c->last_compress.assign(n, CompressRec{});
+  c->last_compress.swap(records);
   for (int r = 0; r < n; ++r) {
     for (int j = 0; j < reqs[r].num_pages; ++j) {
       const int32_t from = old_bt[(size_t)r * maxp + j], to = new_bt[(size_t)r * maxp + j];
       if (to == from) continue;
       reqs[r].block_table[j] = to;
-      gp_page_unref(c, from);
+      if (--c->refcnt[from] == 0) {  // no more of these than pages taken
+        taken.back().value() = from;
+        c->free_pages.insert(std::move(taken.back()));
+        taken.pop_back();
+      }
       ++c->stats.cow_pages;
     }
     if (er[r].items) ++c->slot_gen[reqs[r].slot];
-    CompressRec& rec = c->last_compress[r];
-    rec.num_pages = reqs[r].num_pages;
-    rec.evict = true;
-    rec.tokens = er[r].T;
-    rec.kept = er[r].items ? er[r].keep : 0;
-    rec.pitch = er[r].idx_pitch;
-    rec.mask_off = er[r].idx_off;  // c->evict starts with the kept slots
   }
   return GP_OK;
+} catch (const std::exception&) {
+  return no_memory(c);
 }

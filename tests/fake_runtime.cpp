@@ -7,7 +7,9 @@
 #include <cstdlib>
 #include <cstring>
 #include <map>
+#include <new>
 #include <string>
+#include <utility>
 
 #include "attn_kernels.h"
 #include "gp_internal.h"
@@ -18,8 +20,13 @@ namespace {
 std::map<std::string, long> calls, fail_at;
 std::map<void*, size_t> sizes;
 int skip_select = 0;
+long news = 0, news_until_failure = -1;  // -1: none fails
 // counts the call; an error when it is the one that is to fail
 cudaError_t called(const char* name) {
+  const struct Own {  // the runtime's own allocations do not fail
+    long held = std::exchange(news_until_failure, -1);
+    ~Own() { news_until_failure = held; }
+  } own;
   const long n = ++calls[name];
   const auto it = fail_at.find(name);
   return it != fail_at.end() && it->second == n ? cudaErrorMemoryAllocation : cudaSuccess;
@@ -28,7 +35,9 @@ cudaError_t take(const char* name, void** p, size_t n) {
   if (called(name) != cudaSuccess) return cudaErrorMemoryAllocation;
   *p = std::malloc(n ? n : 1);
   std::memset(*p, 0xff, n);  // what a kernel leaves unwritten is recognised
+  const long held = std::exchange(news_until_failure, -1);
   sizes[*p] = n;
+  news_until_failure = held;
   return cudaSuccess;
 }
 cudaError_t give(const char* name, void* p) {  // the block stays, so that a late use of it does not end the process
@@ -45,7 +54,9 @@ void fake_reset() {
   calls.clear();
   fail_at.clear();
   skip_select = 0;
+  news_until_failure = -1;
 }
+void fake_fail_new(long after) { news_until_failure = after; }  // the after-th allocation from now, -1: none
 void fake_skip_select(int yes) { skip_select = yes; }
 
 cudaError_t cudaMalloc(void** p, size_t n) { return take("cudaMalloc", p, n); }
@@ -105,6 +116,19 @@ gp_status gp_boundary_demand_noalloc(gp_ctx*, int32_t, const gp_request*, const 
   return GP_ERR_UNSUPPORTED;
 }
 }
+
+// The library's own allocations (linked with -Bsymbolic).
+void* operator new(size_t n) {
+  ++news;
+  if (news_until_failure > 0 && --news_until_failure == 0) {
+    news_until_failure = -1;
+    throw std::bad_alloc();
+  }
+  if (void* p = std::malloc(n ? n : 1)) return p;
+  throw std::bad_alloc();
+}
+void operator delete(void* p) noexcept { std::free(p); }
+void operator delete(void* p, size_t) noexcept { std::free(p); }
 
 namespace gp {
 #define FAKE_LAUNCH(name, args) \

@@ -136,3 +136,46 @@ def test_a_call_after_one_that_found_no_memory(fake, name):
                 assert err.status == gp.GP_ERR_CUDA
     for _ in range(20):
         gp.gp_chunk_attention(fake.ctx, 0, fake.reqs, [400, 2000], [100, 50], DEV, DEV << 4, None)
+
+
+def _pool(fake):
+    return ([(r.slot, r.num_pages, r.pages) for r in fake.reqs], gp.gp_free_page_count(fake.ctx),
+            [gp.gp_page_refcount(fake.ctx, p) for p in range(40)])
+
+
+@pytest.mark.parametrize("which", ["append", "decode", "weighted decode", "chunk", "evict", "evict on a side stream"])
+def test_host_memory_that_runs_out_is_an_error(fake, which):
+    """Every allocation of a call fails once: the call says so and changes nothing, no
+    exception leaves the library, and the next call is as ever."""
+    gp.gp_page_ref(fake.ctx, fake.reqs[0].pages[0])  # copied by an eviction
+    if which == "evict on a side stream":
+        gp.gp_set_compaction_stream(fake.ctx, 48)
+
+    def call():
+        if which == "append":
+            gp.gp_append_tokens(fake.ctx, 0, fake.reqs, [500, 2000], [12, 900], DEV, DEV, DEV, DEV, DEV)
+        elif which == "decode":
+            gp.gp_decode_attention(fake.ctx, 0, fake.reqs, [500, 3000], DEV, DEV, DEV)
+        elif which == "weighted decode":
+            gp.gp_decode_attention_weighted(fake.ctx, 0, fake.reqs, [500, 3000], DEV, None, DEV, DEV)
+        elif which == "chunk":
+            gp.gp_chunk_attention(fake.ctx, 0, fake.reqs, [400, 2000], [100, 50], DEV, DEV << 4, DEV)
+        else:
+            gp.gp_evict_weighted(fake.ctx, fake.reqs, [500, 3000], [300, 2900], DEV)
+
+    before, failed = _pool(fake), 0
+    for k in range(1, 2000):
+        gp.load().fake_fail_new(k)
+        try:
+            call()
+            gp.load().fake_fail_new(-1)
+            break
+        except gp.GrowPageError as err:
+            gp.load().fake_fail_new(-1)
+            assert err.status == gp.GP_ERR_CUDA and "host memory" in str(err), (k, err)
+            failed += 1
+            assert _pool(fake) == before, k
+    assert 0 < failed < 1999
+    if "evict" in which:
+        assert gp.gp_free_page_count(fake.ctx) == before[1] - 1
+        gp.gp_set_compaction_stream(fake.ctx, None)
