@@ -368,8 +368,9 @@ gp_status gp_compact_kv(gp_ctx* ctx, int32_t n, gp_request* reqs,
  * results within fp32 tolerances.  With a compaction pending on the side stream (see
  * gp_set_compaction_stream), the call makes the engine stream wait for it
  * only if one of its requests holds a page that compaction reads or writes;
- * otherwise the attention runs concurrently with it (App. E.3).
- * Asynchronous on the engine stream. */
+ * otherwise the attention runs concurrently with it (App. E.3).  out_dev must
+ * not overlap q_dev.  Asynchronous on the engine stream, which must not be
+ * capturing a graph (GP_ERR_UNSUPPORTED, as below). */
 gp_status gp_decode_attention(gp_ctx* ctx, int32_t layer, int32_t n, const gp_request* reqs,
                               const int32_t* num_tokens, const void* q_dev, const uint8_t* first_dev,
                               float* out_dev);
@@ -409,7 +410,8 @@ gp_status gp_decode_attention(gp_ctx* ctx, int32_t layer, int32_t n, const gp_re
  * to kv_dtype) and its value copied; q_rot gets the rotated queries, rounded
  * to q_dtype, as gp_chunk_attention takes them.  q_dev, q_rot_dev: device
  * [rows][Hq][d] q_dtype, both or neither NULL, the same buffer or disjoint ones;
- * k_dev, v_dev: device [rows][Hkv][d] kv_dtype; weights_dev may be NULL.
+ * k_dev, v_dev: device [rows][Hkv][d] kv_dtype, apart from q_rot; weights_dev
+ * may be NULL.
  * All but weights_dev 16-byte aligned, as the caches.  num_cached and num_new:
  * HOST int32 [n]; the tokens must fit the request's pages, and a page written
  * must have one reference and be written by one request of the call

@@ -296,16 +296,10 @@ inline gp_status need_device(gp_ctx* c) {
   return GP_OK;
 }
 
-// What the accumulated-weight operators check first: their descriptors are
-// host data of the call, which a graph's replay would not see again, and their
-// launches go to the current device.
-inline gp_status ready_call(gp_ctx* c) {
-  gp_status st = need_device(c);
-  if (st != GP_OK) return st;
-  int dev = -1;
-  GP_CUDA(c, cudaGetDevice(&dev));
-  if (dev != c->device)
-    return fail(c, GP_ERR_INVALID, "device %d is current, the engine was created on device %d", dev, c->device);
+// Refuses a call while a stream of the engine is being captured: its descriptors
+// are host data of the call, and a replay would copy whatever their memory holds by
+// then.
+inline gp_status refuse_capture(gp_ctx* c) {
   for (cudaStream_t s : {c->stream, c->cstream ? c->cstream : c->stream}) {
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     GP_CUDA(c, cudaStreamIsCapturing(s, &cap));
@@ -313,6 +307,18 @@ inline gp_status ready_call(gp_ctx* c) {
       return fail(c, GP_ERR_UNSUPPORTED, "a stream of the engine is being captured: the call reads host data at every launch");
   }
   return GP_OK;
+}
+
+// What the accumulated-weight operators check first: that, and that their launches
+// go to the engine's device.
+inline gp_status ready_call(gp_ctx* c) {
+  gp_status st = need_device(c);
+  if (st != GP_OK) return st;
+  int dev = -1;
+  GP_CUDA(c, cudaGetDevice(&dev));
+  if (dev != c->device)
+    return fail(c, GP_ERR_INVALID, "device %d is current, the engine was created on device %d", dev, c->device);
+  return refuse_capture(c);
 }
 
 // A staging slot of at least `bytes`, free to be written.  The slots are pieces

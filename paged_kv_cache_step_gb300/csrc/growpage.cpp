@@ -1406,6 +1406,7 @@ gp_status gp_decode_attention(gp_ctx* c, int32_t layer, int32_t n, const gp_requ
   gp_status st = need_device(c);
   if (st != GP_OK) return st;
   if ((st = check_decode(c, layer, n, reqs, num_tokens, !q_dev || !first_dev || !out_dev)) != GP_OK) return st;
+  if ((st = refuse_capture(c)) != GP_OK) return st;
   return decode_attention(c, layer, n, reqs, num_tokens, q_dev, first_dev, out_dev, nullptr);
 } catch (const std::exception&) {
   return no_memory(c);

@@ -215,3 +215,29 @@ def test_emptied_pages_go_to_another_request(side):
     finally:
         gp.gp_set_compaction_stream(e.ctx, None)
         e.close()
+
+
+def test_decode_attention_is_refused_while_the_stream_is_captured():
+    """A replay would read its tables from memory that later calls have written."""
+    stream = torch.cuda.Stream()
+    e = Engine([2], L=1, seed=67, stream=stream)
+    try:
+        e.fill([300])
+        q, out = e.randn(1, 8, 128).bfloat16(), torch.zeros(1, 8, 128, device="cuda")
+        first, x = torch.ones(1, dtype=torch.uint8, device="cuda"), torch.ones(8, device="cuda")
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            x.mul_(2)
+            with pytest.raises(gp.GrowPageError) as err:
+                gp.gp_decode_attention(e.ctx, 0, e.reqs, [300], q, first, out)
+        assert err.value.status == gp.GP_ERR_UNSUPPORTED
+        graph.replay()
+        torch.cuda.synchronize()
+        assert x[0] == 2 and not out.any()
+        for _ in range(10):  # and the context works on, whichever slot a call takes
+            gp.gp_decode_attention(e.ctx, 0, e.reqs, [300], q, first, out)
+        gp.gp_synchronize(e.ctx)
+        assert out.any()
+    finally:
+        e.close()
