@@ -53,6 +53,7 @@
 #include <cuda_bf16.h>
 
 #include "demand_common.cuh"
+#include "shared_limit.cuh"
 #include "tc_ptx.cuh"
 
 namespace gp {
@@ -670,28 +671,22 @@ __global__ void __launch_bounds__(NTHR, 1) k_demand_tc(const __grid_constant__ D
   }
 }
 
-// The kernel's launch attribute (set once) and its dynamic shared memory:
+// The kernel's launch attribute (set once a device) and its dynamic shared memory:
 // the whole opt-in amount, so that one CTA owns an SM, its TMEM (512
 // columns) and the select buffer.  0 if the device cannot hold the layout.
 template <int D, int ROWS>
 size_t prepare_t() {
   using S = TcSmem<D, ROWS>;
-  static size_t smem = 0;
-  if (smem) return smem;
-  int dev = 0, max_optin = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&max_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-      (size_t)max_optin < S::MIN_BYTES) {
+  static std::atomic<int> known{0};  // of the devices that this is built for, all alike
+  int max_optin = known.load(std::memory_order_relaxed), dev = 0;
+  if ((max_optin == 0 && (cudaGetDevice(&dev) != cudaSuccess ||
+                          cudaDeviceGetAttribute(&max_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)) ||
+      (size_t)max_optin < S::MIN_BYTES || allow_shared<k_demand_tc<D, ROWS>>(max_optin) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
-  if (cudaFuncSetAttribute(k_demand_tc<D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, max_optin) !=
-      cudaSuccess) {
-    cudaGetLastError();
-    return 0;
-  }
-  smem = (size_t)max_optin;
-  return smem;
+  known.store(max_optin, std::memory_order_relaxed);
+  return (size_t)max_optin;
 }
 
 // CTAs the device holds at once (one per SM at this shared-memory size).

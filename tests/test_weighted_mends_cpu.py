@@ -131,3 +131,8 @@ def test_counts_that_32_bits_do_not_hold(eng):  # noqa: F811
     for good in ([1, 1, 1], np.array([1, 1, 1]), np.array([1, 1, 1], dtype=np.uint8), np.array([1, 9, 1, 9, 1, 9], dtype=np.int32)[::2]):
         assert _status(_append, ctx, reqs, (0, 0, 0), good) == gp.GP_ERR_STATE
         assert _status(_evict, ctx, reqs, (2, 2, 2), good) == gp.GP_ERR_STATE
+
+
+def test_the_demand_scan_sets_its_shared_memory_limit_on_every_device():
+    body = _source("k_demand_tc.cu").split("size_t prepare_t()")[1].split("\n}\n")[0]
+    assert "allow_shared<" in body and not re.search(r"if \(\w+\) return", body)
