@@ -76,7 +76,7 @@ def _log(rng, lo, hi):
 
 def draw(rng):
     op = rng.choice(["tables", "rotary", "bounds", "select", "attend"])
-    d, group, kv = rng.choice([64, 128]), rng.choice([1, 2, 4, 8]), rng.choice(["bf16", "bf16", "bf16", "f32"])
+    d, group, kv = rng.choice([64, 128]), rng.choice([2, 4]), rng.choice(["bf16", "bf16", "bf16", "f32"])
     hkv = rng.choice([1, 2, 4, 8])
     c = dict(NO_ROPE, op=op, hq=group * hkv, hkv=hkv, d=d, kv=kv, mix=rng.randrange(1 << 20), pad=rng.choice([0, 0, 1, 37]))
     if op == "tables":
