@@ -470,6 +470,180 @@ gp_status gp_chunk_attention(gp_ctx* ctx, int32_t layer, int32_t n, const gp_req
 gp_status gp_evict_weighted(gp_ctx* ctx, int32_t n, gp_request* reqs, const int32_t* num_tokens,
                             const int32_t* keep_tokens, float* weights_dev);
 
+/* ---- a step over device arrays, and attention over selected blocks ---------------
+ * The alternative to eviction: every token stays cached, and a query reads only
+ * the blocks of keys that a cheap score selects for it.  Five calls carry a step:
+ * gp_build_tables lays out its rows, gp_append_mapped writes their keys and
+ * values, gp_block_bounds bounds the keys of the blocks they fall into,
+ * gp_select_blocks lists the blocks of each row, gp_sparse_attention attends to
+ * them.  gp_build_tables is called once a step, the others once a layer.
+ *
+ * They take lengths and block tables from DEVICE arrays (gp_step), which the
+ * host never sees: lengths that only the GPU knows (accepted drafts) need no
+ * way back, and the calls CAN be captured into a CUDA graph and replayed over
+ * other contents of the same arrays.  They use no scratch of the engine: graphs
+ * share nothing but the caller's buffers.
+ *
+ * They share these rules.  Addresses, sizes and options are checked before
+ * anything happens (GP_ERR_INVALID, nothing changed); the device current at
+ * gp_create must be current (GP_ERR_INVALID).  What the device arrays hold is
+ * checked by the kernels: a row whose request, slot, length or page is outside
+ * the engine's sizes is left out (its outputs stay as they were) and
+ * reported by the next synchronising call as GP_ERR_INVALID.  Block sizes are
+ * 16, 32, 64, 128 or 256 tokens.  Rows behind the step's last one
+ * (row_req and slot_map of -1) are left as they were.
+ * All run on the engine stream, asynchronously.  Those that read or write K/V
+ * (gp_append_mapped, gp_block_bounds, gp_sparse_attention) wait there for a
+ * compaction pending on the side stream, whatever its pages; a call that is
+ * being captured is refused while one is (GP_ERR_STATE), and a graph's launches
+ * do not wait: gp_wait_compaction on the launching stream comes first.
+ *
+ * gp_step: the arrays of one step, device memory of the caller, 4-byte (64-bit
+ * ones 8-byte) aligned and apart from one another.  The first four are inputs of
+ * gp_build_tables; tables is read and extended by it; the last four are what it
+ * writes and the others read.  A caller may fill those by other means.
+ *   n          requests, at most max_slots and 4096
+ *   max_rows   rows that the step's buffers have room for (new tokens of all
+ *              requests together)
+ *   slots      int32 [n], the requests' slots (gp_slot_acquire), listed once
+ *   num_cached int32 [n], tokens in the cache before the step
+ *   num_new    int32 [n], tokens of the step
+ *   pos        int64 [n], rotary position of the first new token
+ *   tables     int32 [max_slots][max_pages_per_req], block tables by slot
+ *   row0       int32 [n + 1], first row of each request, and the rows in all
+ *   row_req    int32 [max_rows], a row's request (index below n), -1: none
+ *   slot_map   int64 [max_rows], page * 256 + place in the page, -1: none
+ *   positions  int64 [max_rows], rotary position */
+typedef struct gp_step {
+  int32_t n;
+  int32_t max_rows;
+  const int32_t* slots;
+  const int32_t* num_cached;
+  const int32_t* num_new;
+  const int64_t* pos;
+  int32_t* tables;
+  int32_t* row0;
+  int32_t* row_req;
+  int64_t* slot_map;
+  int64_t* positions;
+} gp_step;
+
+/* What became of a request in gp_build_tables. */
+typedef enum {
+  GP_STEP_GIVEN = 0,    /* its rows are in the step */
+  GP_STEP_NO_PAGES = 1, /* the free list has too few pages */
+  GP_STEP_NO_ROWS = 2,  /* its rows do not fit behind those before it */
+  GP_STEP_INVALID = 3   /* slot out of range or listed twice, a negative length, more tokens
+                           than max_pages_per_req pages, or cached ones without a page */
+} gp_step_state;
+
+/* gp_build_tables: rows, block tables, slot map and positions of a step.
+ * Request i with slot s holds held[s] pages; it needs ceil((num_cached[i] +
+ * num_new[i]) / 256) and takes the ones missing from free_dev, behind those taken
+ * by the requests before it.  A request whose rows or pages do not fit
+ * has no row in this step, takes no page and keeps its table; those after it are
+ * still given what fits.  (Pages: once the list is too short for a request, no
+ * later one takes any.)  free_dev: int32 [num_free], pages that the caller took with
+ * gp_page_alloc, each listed once, of which the first taken_in[0] (NULL: none) are
+ * used up; taken_dev: int32 [1] gets the count after the call, and may be
+ * taken_in.  held_dev: int32 [max_slots]; num_pages_dev: int32 [max_slots] gets the
+ * pages of the listed slots after the call, and may be held_dev: a call repeated
+ * over the same lengths then takes nothing.  state_dev: int32 [n], gp_step_state,
+ * apart from the inputs. */
+gp_status gp_build_tables(gp_ctx* ctx, const gp_step* step, const int32_t* held_dev, int32_t* num_pages_dev,
+                          const int32_t* free_dev, int32_t num_free, const int32_t* taken_in_dev, int32_t* taken_dev,
+                          int32_t* state_dev);
+
+/* Rotary forms.  Pairs of a head's first rotary_dim dimensions are rotated by
+ * position * f_i, the other dimensions copied: (i, i + rotary_dim / 2) in the HALF
+ * layout, (2 i, 2 i + 1) in the INTERLEAVED one.  Before scaling
+ * f_i = theta^(-2 i / rotary_dim).  Scaling for contexts longer than
+ * original_length, by `factor` >= 1:
+ *   LINEAR  f_i / factor
+ *   BANDS   with t_i = original_length f_i / (2 pi), the turns of pair i over the
+ *           original length: f_i / factor where t_i <= low_turns, f_i where
+ *           t_i >= high_turns, between them k f_i + (1 - k) f_i / factor,
+ *           k = (t_i - low_turns) / (high_turns - low_turns)
+ *   RAMP    the same blend by the pair's index: with
+ *           p(t) = rotary_dim ln(original_length / (2 pi t)) / (2 ln theta), a =
+ *           max(0, floor(p(high_turns))), b = min(rotary_dim - 1, ceil(p(low_turns))),
+ *           the part of f_i / factor is (i - a) / (b - a) held to [0, 1] (b - a
+ *           at least 0.001)
+ * Sine and cosine are multiplied by `amplitude`; 0 stands for 0.1 ln(factor) + 1
+ * under RAMP and for 1 otherwise. */
+typedef enum { GP_ROPE_HALF = 0, GP_ROPE_INTERLEAVED = 1 } gp_rope_layout;
+typedef enum { GP_ROPE_NONE = 0, GP_ROPE_LINEAR = 1, GP_ROPE_BANDS = 2, GP_ROPE_RAMP = 3 } gp_rope_scaling;
+typedef struct gp_rope {
+  int32_t layout;          /* gp_rope_layout */
+  int32_t rotary_dim;      /* a multiple of 16 up to head_dim; 0: no rotation */
+  int32_t scaling;         /* gp_rope_scaling */
+  int32_t original_length; /* BANDS, RAMP: at least 1 */
+  double theta;            /* above 1 */
+  double factor;
+  double low_turns;        /* below high_turns, above 0 */
+  double high_turns;
+  double amplitude;        /* 0: by the rule above */
+} gp_rope;
+
+/* Fill *rope with: HALF, rotary_dim 0, NONE, original_length 8192, theta 10000, factor
+ * 1, low_turns 1, high_turns 0 (which stands for 4 under BANDS and 32 under RAMP),
+ * amplitude 0. */
+gp_status gp_rope_default(gp_rope* rope);
+
+/* gp_append_mapped: the step's new tokens of one layer into the cache, as
+ * gp_append_tokens, but by slot_map and positions and in any of the rotary forms.
+ * q_dev, k_dev, v_dev: device [max_rows] rows of [Hq][d] q_dtype and [Hkv][d]
+ * kv_dtype, whose starts lie q_stride, k_stride and v_stride elements apart (at
+ * least the row, so that all three may be columns of one projection's output);
+ * q_rot_dev: [max_rows][Hq][d], packed, apart from the inputs, or q_dev itself if
+ * that is packed.  q and q_rot both or neither NULL.  All 16-byte aligned, strides
+ * too.  A page written must be the request's alone: the engine does not see the
+ * tables and cannot check.  Accumulated weights are not cleared (an
+ * append that feeds them is gp_append_tokens).  gp_boundary_demand results of all slots
+ * are stale afterwards; a graph's launches do not mark them so: after one, the next
+ * gp_compress_hold needs a new gp_boundary_demand all the same. */
+gp_status gp_append_mapped(gp_ctx* ctx, int32_t layer, const gp_step* step, const gp_rope* rope, const void* q_dev,
+                           int64_t q_stride, const void* k_dev, int64_t k_stride, const void* v_dev, int64_t v_stride,
+                           void* q_rot_dev);
+
+/* gp_block_bounds: bounds of the keys of each block that a row of the step falls
+ * into, over all tokens of the block up to the request's last (older ones are read
+ * again).  bounds_dev: int8 [L][num_pages][Hkv][256 / block][2][d], 16-byte aligned,
+ * scales_dev: fp32 [L][num_pages][Hkv][256 / block]; the caller's, by page, so
+ * that requests share those of a shared prefix.  Per (block, KV head): e is the
+ * least whole number >= -100 with max |k| <= 127 * 2^e (at most 100), the scale is
+ * 2^e, and dimension i has [0][i] = floor(min k_i / 2^e) and [1][i] = ceil(max k_i /
+ * 2^e), held to [-127, 127].  NaN keys are left out (a dimension with no other
+ * counts as 0).  A call that moves keys (Compress & Hold, an eviction) leaves the
+ * bounds of its pages stale: a step with num_cached = 0 and num_new = the tokens
+ * left forms them again (its rows need no queries). */
+gp_status gp_block_bounds(gp_ctx* ctx, int32_t layer, const gp_step* step, int32_t block, int8_t* bounds_dev,
+                          float* scales_dev);
+
+/* gp_select_blocks: the blocks that each row attends to, per KV head.  With the
+ * group's queries as whole numbers Q_g = round(q_g / 2^e) in [-127, 127] (e as above,
+ * of all of the group), a block's score is the sum over g and i of the larger of
+ * Q_gi lo_i and Q_gi hi_i, times its scale: what the group's logits can reach in it.
+ * A row in block b attends to blocks of [0, b]: all of them if they are `top` or
+ * fewer, else the first `sink`, the last `recent` >= 1, and of the others those of
+ * largest score (equal scores: the lower block), `top` >= sink + recent in all.
+ * The arithmetic is exact.  q_rot_dev: [max_rows][Hq][d] q_dtype, 16-byte aligned,
+ * as gp_append_mapped gives it; blocks_dev: int32 [max_rows][Hkv][top], ascending,
+ * then -1. */
+gp_status gp_select_blocks(gp_ctx* ctx, int32_t layer, const gp_step* step, int32_t block, int32_t top, int32_t sink,
+                           int32_t recent, const void* q_rot_dev, const int8_t* bounds_dev, const float* scales_dev,
+                           int32_t* blocks_dev);
+
+/* gp_sparse_attention: attention of each row over the tokens, up to its own, of
+ * the blocks listed for it: z = q . k / sqrt(d), a = softmax(z), out = sum a v.
+ * blocks_dev: int32 [max_rows][Hkv][top]; a list is ascending and ends at the first
+ * entry that is negative, not above the one before it, or past the row's own
+ * block; an empty one gives 0.  q_rot_dev, out_dev: [max_rows][Hq][d] q_dtype,
+ * 16-byte aligned, apart.  Keys and values of the tokens attended to must
+ * be finite; other cache slots may hold any bits. */
+gp_status gp_sparse_attention(gp_ctx* ctx, int32_t layer, const gp_step* step, int32_t block, int32_t top,
+                              const void* q_rot_dev, const int32_t* blocks_dev, void* out_dev);
+
 /* ---- asynchronous compaction (App. E.3: compaction overlapped with decoding)
  * gp_set_compaction_stream: from now on the compaction of gp_compress_hold,
  * gp_shrink, gp_compress_fill, gp_compact_kv and gp_evict_weighted runs on `stream` (a caller
@@ -599,7 +773,12 @@ gp_status gp_set_selection_mode(gp_ctx* ctx, int32_t mode);
 #define GP_KERNEL_WEIGHTS 9        /* the weights of a decode step or a chunk */
 #define GP_KERNEL_EVICT_SELECT 10
 #define GP_KERNEL_EVICT 11
-#define GP_KERNEL_COUNT 12
+#define GP_KERNEL_TABLES 12
+#define GP_KERNEL_MAPPED 13        /* gp_append_mapped */
+#define GP_KERNEL_BOUNDS 14
+#define GP_KERNEL_BLOCK_SELECT 15
+#define GP_KERNEL_SPARSE 16
+#define GP_KERNEL_COUNT 17
 gp_status gp_set_timing(gp_ctx* ctx, int32_t enabled);
 gp_status gp_kernel_time(gp_ctx* ctx, int32_t kernel, double* ms, int64_t* launches);
 gp_status gp_reset_timing(gp_ctx* ctx);

@@ -7,6 +7,6 @@ names.  Every hot-path step runs in the CUDA kernels; there is no CPU path.
 """
 
 from .binding import *  # noqa: F401,F403
-from .binding import EXPORTS, Request, load  # noqa: F401
+from .binding import EXPORTS, Request, Step, load  # noqa: F401
 
-__all__ = ["load", "Request", "EXPORTS"]
+__all__ = ["load", "Request", "Step", "EXPORTS"]

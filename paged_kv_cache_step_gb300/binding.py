@@ -34,9 +34,14 @@ GP_SELECT_AUTO, GP_SELECT_SPECULATIVE, GP_SELECT_IN_COMPACTION = 0, 1, 2
 GP_KERNEL_EMA, GP_KERNEL_PREP, GP_KERNEL_DEMAND, GP_KERNEL_COMPRESS, GP_KERNEL_ATTENTION = 0, 1, 2, 3, 4
 GP_KERNEL_SELECT, GP_KERNEL_ENTROPY = 5, 6
 GP_KERNEL_APPEND, GP_KERNEL_CHUNK, GP_KERNEL_WEIGHTS, GP_KERNEL_EVICT_SELECT, GP_KERNEL_EVICT = 7, 8, 9, 10, 11
+GP_KERNEL_TABLES, GP_KERNEL_MAPPED, GP_KERNEL_BOUNDS, GP_KERNEL_BLOCK_SELECT, GP_KERNEL_SPARSE = 12, 13, 14, 15, 16
+GP_STEP_GIVEN, GP_STEP_NO_PAGES, GP_STEP_NO_ROWS, GP_STEP_INVALID = 0, 1, 2, 3
+GP_ROPE_HALF, GP_ROPE_INTERLEAVED = 0, 1
+GP_ROPE_NONE, GP_ROPE_LINEAR, GP_ROPE_BANDS, GP_ROPE_RAMP = 0, 1, 2, 3
 KERNEL_NAMES = {0: "ema_update", 1: "prep_queries", 2: "boundary_demand", 3: "compress_hold",
                 4: "decode_attention", 5: "select", 6: "entropy", 7: "append_tokens", 8: "chunk_attention",
-                9: "weights", 10: "evict_select", 11: "evict_move"}
+                9: "weights", 10: "evict_select", 11: "evict_move", 12: "build_tables", 13: "append_mapped",
+                14: "block_bounds", 15: "select_blocks", 16: "sparse_attention"}
 
 EXPORTS = [
     "gp_config_default", "gp_create", "gp_destroy", "gp_last_error", "gp_status_string",
@@ -51,6 +56,7 @@ EXPORTS = [
     "gp_set_compaction_stream", "gp_wait_compaction", "gp_decode_attention",
     "gp_synchronize", "gp_debug_set_wait_limit", "gp_debug_fail_next_launch", "gp_set_selection_mode",
     "gp_append_tokens", "gp_decode_attention_weighted", "gp_chunk_attention", "gp_evict_weighted",
+    "gp_build_tables", "gp_rope_default", "gp_append_mapped", "gp_block_bounds", "gp_select_blocks", "gp_sparse_attention",
 ]
 
 
@@ -88,6 +94,12 @@ class GpStats(C.Structure):
     _fields_ = [(n, C.c_int64) for n in ("demand_calls", "demand_requests", "grow", "compress",
                                           "fallback", "forced_grow", "cow_pages", "moved_rows",
                                           "shrink")]
+
+
+class GpRope(C.Structure):
+    _fields_ = [("layout", C.c_int32), ("rotary_dim", C.c_int32), ("scaling", C.c_int32), ("original_length", C.c_int32),
+                ("theta", C.c_double), ("factor", C.c_double), ("low_turns", C.c_double), ("high_turns", C.c_double),
+                ("amplitude", C.c_double)]
 
 
 class GrowPageError(RuntimeError):
@@ -162,6 +174,16 @@ def load(build_if_missing: bool = True):
         "gp_chunk_attention": (I32, [P, I32, I32, P, P, P, P, P, P]),
         "gp_evict_weighted": (I32, [P, I32, C.POINTER(GpRequest), P, P, P]),
     }
+    step = {
+        "gp_build_tables": (I32, [P, P, P, P, P, I32, P, P, P]),
+        "gp_rope_default": (I32, [C.POINTER(GpRope)]),
+        "gp_append_mapped": (I32, [P, I32, P, C.POINTER(GpRope), P, I64, P, I64, P, I64, P]),
+        "gp_block_bounds": (I32, [P, I32, P, I32, P, P]),
+        "gp_select_blocks": (I32, [P, I32, P, I32, I32, I32, I32, P, P, P, P]),
+        "gp_sparse_attention": (I32, [P, I32, P, I32, I32, P, P, P]),
+    }
+    if hasattr(lib, "gp_build_tables"):  # one linked without sparse.cpp has none of them
+        sig.update(step)
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -197,18 +219,21 @@ class _Buffers:
         self.q_row, self.kv_row = cfg.num_q_heads * cfg.head_dim, cfg.num_kv_heads * cfg.head_dim
         self.weights = cfg.num_layers * cfg.max_slots * cfg.num_kv_heads * cfg.max_pages_per_req * cfg.page_size
         self.device = device
-        self.q = self.kv = self.f32 = self.u8 = None  # torch's types, once a tensor is met
+        self.d, self.layers, self.hkv, self.pages = cfg.head_dim, cfg.num_layers, cfg.num_kv_heads, cfg.num_pages
+        self.slots, self.tables = cfg.max_slots, cfg.max_slots * cfg.max_pages_per_req
+        self.q = self.kv = self.f32 = self.u8 = self.i8 = self.i32 = self.i64 = None  # torch's types, once a tensor is met
 
     def know_types(self):
         import torch  # loaded: a tensor of it is being looked at
         self.f32, self.u8 = torch.float32, torch.uint8
+        self.i8, self.i32, self.i64 = torch.int8, torch.int32, torch.int64
         self.q, self.kv = (torch.float32 if x == GP_DTYPE_F32 else torch.bfloat16 for x in self._codes)
 
 
 class _Unknown:
     """_Buffers of a context that gp_create here has not made: nothing is known."""
-    q_row = kv_row = weights = 0
-    device = q = kv = f32 = u8 = None
+    q_row = kv_row = weights = d = layers = hkv = pages = slots = tables = 0
+    device = q = kv = f32 = u8 = i8 = i32 = i64 = None
 
 
 def _held(ctx):
@@ -588,6 +613,114 @@ def gp_evict_weighted(ctx, reqs, num_tokens, keep_tokens, weights_dev):
     st = load().gp_evict_weighted(ctx, len(reqs), arr, _host(nt), _host(nk), _weights(_held(ctx), weights_dev))
     _unmarshal(arr, reqs)
     _check(ctx, st)
+
+
+# gp_step packed field by field: {int32 n, int32 max_rows, nine pointers}
+_STEP_PACK = struct.Struct("=ii9Q")
+
+
+class Step:
+    """The device arrays of a step (gp_step): tensors, checked here once against the
+    context, or addresses, with n and max_rows then given.  The step keeps the
+    tensors alive."""
+
+    def __init__(self, ctx, *, slots, num_cached, num_new, pos, tables, row0, row_req, slot_map, positions, n=None,
+                 max_rows=None):
+        self.n = int(len(slots) if n is None else n)
+        self.max_rows = int(len(row_req) if max_rows is None else max_rows)
+        h, n, rows = _held(ctx), self.n, self.max_rows
+        self.arrays = (slots, num_cached, num_new, pos, tables, row0, row_req, slot_map, positions)
+        if hasattr(tables, "numel") and h.tables and tables.numel() != h.tables:
+            raise GrowPageError(GP_ERR_INVALID, f"block tables of {tables.numel()} entries, where the engine has {h.tables}")
+        self._raw = _STEP_PACK.pack(
+            n, rows, _dense(h, slots, h.i32, n), _dense(h, num_cached, h.i32, n), _dense(h, num_new, h.i32, n),
+            _dense(h, pos, h.i64, n), _dense(h, tables, h.i32, h.tables), _dense(h, row0, h.i32, n + 1),
+            _dense(h, row_req, h.i32, rows), _dense(h, slot_map, h.i64, rows), _dense(h, positions, h.i64, rows))
+
+
+def _strided(held, t, dtype, rows, row):
+    """Address of rows of packed heads and the elements between their starts: a
+    tensor [rows, heads, d] or [rows, heads * d], dense within a row."""
+    if t is None:
+        return 0, 0
+    if not hasattr(t, "stride") or t.dim() < 2 or rows == 0:
+        return _dense(held, t, dtype, 0), row
+    shape, strides = t.shape, t.stride()
+    dense = 1
+    for size, stride in zip(reversed(shape[1:]), reversed(strides[1:])):
+        if size != 1 and stride != dense:
+            raise GrowPageError(GP_ERR_INVALID, f"rows that are not dense: strides {strides}")
+        dense *= size
+    if not t.is_cuda or (held.device is not None and t.get_device() != held.device):
+        raise GrowPageError(GP_ERR_INVALID, f"a buffer on {t.device}, the caches are on device {held.device}")
+    if held is not _Unknown and (t.dtype is not dtype or dense != row or shape[0] < rows):
+        raise GrowPageError(GP_ERR_INVALID, f"{shape[0]} rows of {dense} {t.dtype}, where the call takes {rows} of {row} {dtype}")
+    return t.data_ptr(), strides[0] if shape[0] > 1 else row
+
+
+def gp_rope_default(**overrides) -> GpRope:
+    rope = GpRope()
+    _check(None, load().gp_rope_default(C.byref(rope)))
+    for k, v in overrides.items():
+        if k not in dict(GpRope._fields_):
+            raise TypeError(f"gp_rope has no field {k}")
+        setattr(rope, k, v)
+    return rope
+
+
+def gp_build_tables(ctx, step: Step, held_dev, num_pages_dev, free_dev, taken_in_dev, taken_dev, state_dev, num_free=None):
+    """Rows, block tables, slot map and positions of a step.  held_dev, num_pages_dev:
+    int32 [max_slots]; free_dev: int32 page ids (num_free of them, all by default);
+    taken_in_dev (or None), taken_dev: int32 [1]; state_dev: int32 [n]."""
+    h = _held(ctx)
+    if num_free is None:
+        num_free = 0 if free_dev is None else free_dev.numel()
+    _check(ctx, load().gp_build_tables(ctx, step._raw, _dense(h, held_dev, h.i32, h.slots), _dense(h, num_pages_dev, h.i32, h.slots),
+                                       _dense(h, free_dev, h.i32, num_free), num_free, _dense(h, taken_in_dev, h.i32, 1),
+                                       _dense(h, taken_dev, h.i32, 1), _dense(h, state_dev, h.i32, step.n)))
+
+
+def gp_append_mapped(ctx, layer: int, step: Step, rope: GpRope, q_dev, k_dev, v_dev, q_rot_dev):
+    """The step's tokens of one layer into the cache, in a rotary form.  q_dev, k_dev,
+    v_dev: [max_rows, heads, d], rows any multiple of 16 bytes apart; q_rot_dev
+    packed.  q_dev and q_rot_dev both None: keys and values alone."""
+    h, rows = _held(ctx), step.max_rows
+    q, qs = _strided(h, q_dev, h.q, rows, h.q_row)
+    k, ks = _strided(h, k_dev, h.kv, rows, h.kv_row)
+    v, vs = _strided(h, v_dev, h.kv, rows, h.kv_row)
+    _check(ctx, load().gp_append_mapped(ctx, layer, step._raw, rope, q, qs, k, ks, v, vs,
+                                        _dense(h, q_rot_dev, h.q, rows * h.q_row)))
+
+
+def _bounds(h, block, bounds_dev, scales_dev):
+    blocks = h.layers * h.pages * h.hkv * (256 // block if block > 0 else 0)
+    return _dense(h, bounds_dev, h.i8, blocks * 2 * h.d), _dense(h, scales_dev, h.f32, blocks)
+
+
+def gp_block_bounds(ctx, layer: int, step: Step, block: int, bounds_dev, scales_dev):
+    """Bounds of the blocks that the step's rows fall into: bounds_dev int8
+    [L][num_pages][Hkv][256 / block][2][d], scales_dev fp32, one a block and head."""
+    h = _held(ctx)
+    _check(ctx, load().gp_block_bounds(ctx, layer, step._raw, block, *_bounds(h, block, bounds_dev, scales_dev)))
+
+
+def gp_select_blocks(ctx, layer: int, step: Step, block: int, top: int, sink: int, recent: int, q_rot_dev, bounds_dev, scales_dev,
+                     blocks_dev):
+    """The `top` blocks of each row and KV head: the first `sink`, the last `recent`,
+    and those of largest score; blocks_dev int32 [max_rows][Hkv][top]."""
+    h, rows = _held(ctx), step.max_rows
+    b, s = _bounds(h, block, bounds_dev, scales_dev)
+    _check(ctx, load().gp_select_blocks(ctx, layer, step._raw, block, top, sink, recent, _dense(h, q_rot_dev, h.q, rows * h.q_row),
+                                        b, s, _dense(h, blocks_dev, h.i32, rows * h.hkv * top)))
+
+
+def gp_sparse_attention(ctx, layer: int, step: Step, block: int, top: int, q_rot_dev, blocks_dev, out_dev):
+    """Attention of each row over the blocks listed for it; q_rot_dev and out_dev
+    [max_rows][Hq][d] of q_dtype, blocks_dev as gp_select_blocks gives it."""
+    h, rows = _held(ctx), step.max_rows
+    q = rows * h.q_row
+    _check(ctx, load().gp_sparse_attention(ctx, layer, step._raw, block, top, _dense(h, q_rot_dev, h.q, q),
+                                           _dense(h, blocks_dev, h.i32, rows * h.hkv * top), _dense(h, out_dev, h.q, q)))
 
 
 def gp_compact_kv(ctx, reqs, keep_masks_dev):

@@ -1,0 +1,276 @@
+// Attention of each row over the blocks that are listed for it, on the CUDA cores:
+// fp32 caches or queries, or when forced.
+//
+//   z_i = q . k_i / sqrt(d) over the tokens of the listed blocks up to the row's own,
+//   a = softmax(z),  out = sum a v  (0 when the list is empty).
+// A list is ascending; it ends at the first entry that is negative, not above the
+// one before it or past the row's own block.
+//
+// A cluster of `splits` CTAs a (row, KV head); each takes an even share of the
+// list, and the shares' maxima, sums and outputs are joined through distributed
+// shared memory: no scratch, no second launch, one fixed order.
+// In a CTA a key's row is read by D / 8 lanes, 8 dimensions each; every group of
+// lanes keeps its own running maximum and sum (base 2) over its keys.  All in fp32;
+// one rounding to the query's type at the end.
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "math2.cuh"
+#include "step.cuh"
+
+namespace gp {
+namespace {
+
+constexpr int NT = 256;
+constexpr int NW = NT / 32;
+constexpr int ENTRIES = 64;  // of a share that are looked up at a time
+constexpr float NEG = -1.0e30f;
+
+// Dimension t of the 8 that lane c of a group owns (k_attention.cu's layout: the
+// lanes of a quarter warp read 128 contiguous bytes).
+template <int D, bool F32>
+__device__ __forceinline__ int lane_dim(int c, int t) {
+  if constexpr (F32) return t < 4 ? 4 * c + t : D / 2 + 4 * c + (t - 4);
+  else return 8 * c + t;
+}
+template <int D, bool F32>
+__device__ __forceinline__ void load_row(const unsigned char* row, int c, float (&f)[8]) {
+  if constexpr (F32) {
+    const float4 x = *reinterpret_cast<const float4*>(row + c * 16), y = *reinterpret_cast<const float4*>(row + (c + D / 8) * 16);
+    f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+    f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(row + c * 16);
+    const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+template <int D, int G, bool QF32, bool KF32>
+__global__ void __launch_bounds__(NT) k_sparse(const __grid_constant__ SparseArgs a) {
+  constexpr int LN = D / 8;           // lanes of a group
+  constexpr int GROUPS = NT / LN;
+  constexpr int U = 4;                // keys of a group in flight
+  constexpr int KB = KF32 ? 4 : 2;
+  __shared__ int count_s;
+  __shared__ int64_t at_s[ENTRIES];   // first cache row of an entry's block, -1: none
+  __shared__ int tok_s[ENTRIES];      // its first logical slot
+  __shared__ float acc_s[NW][G][D];
+  __shared__ float m_s[NW][G], l_s[NW][G];
+  __shared__ float part[G][D + 2];    // this CTA's outputs, maxima, sums
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = tid % LN, group = tid / LN;
+  const int C = a.splits, rank = blockIdx.x % C;
+  const int64_t unit = blockIdx.x / C;
+  const int row = (int)(unit / a.Hkv), h = (int)(unit % a.Hkv);
+  const StepRow rw = find_row(a.s, row, tid == 0);
+  if (!rw.live) return;  // (the whole cluster)
+  const int own = rw.at / a.block, per = kStepPage / a.block;
+  const int32_t* list = a.blocks + unit * a.top;
+  if (tid == 0) count_s = a.top;
+  __syncthreads();
+  for (int k = tid; k < a.top; k += NT) {
+    const int b = list[k], before = k ? list[k - 1] : -1;
+    if (b < 0 || b <= before || b > own) atomicMin(&count_s, k);
+  }
+  float q[G][8];
+  const float sc = 1.4426950408889634f / sqrtf((float)D);
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const size_t at = ((size_t)row * a.Hq + h * G + g) * D + lane_dim<D, KF32>(c, t);
+      q[g][t] = sc * (QF32 ? static_cast<const float*>(a.q)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at]));
+    }
+  __syncthreads();
+  const int count = count_s;
+  const int from = (int)((int64_t)count * rank / C), to = (int)((int64_t)count * (rank + 1) / C);
+
+  float m[G], l[G], acc[G][8];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    m[g] = NEG;
+    l[g] = 0.f;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) acc[g][t] = 0.f;
+  }
+  for (int e0 = from; e0 < to; e0 += ENTRIES) {
+    const int n = min(ENTRIES, to - e0);
+    __syncthreads();
+    if (tid < n) {
+      const int b = list[e0 + tid], page = step_page(a.s, rw.slot, b / per);
+      at_s[tid] = page < 0 ? -1 : (((int64_t)a.layer * a.s.num_pages_total + page) * a.Hkv + h) * kStepPage + b % per * a.block;
+      tok_s[tid] = b * a.block;
+    }
+    __syncthreads();
+    const int keys = n * a.block;
+    for (int k0 = group; k0 < keys; k0 += GROUPS * U) {
+      float z[G][U], v[U][8];
+      bool seen[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * GROUPS, e = k / a.block, o = k % a.block;
+        seen[u] = k < keys && at_s[min(e, n - 1)] >= 0 && tok_s[min(e, n - 1)] + o <= rw.at;
+        float kk[8];
+        if (seen[u]) {
+          const size_t at = (size_t)(at_s[e] + o) * D * KB;
+          load_row<D, KF32>(static_cast<const unsigned char*>(a.k_cache) + at, c, kk);
+          load_row<D, KF32>(static_cast<const unsigned char*>(a.v_cache) + at, c, v[u]);
+        } else {
+#pragma unroll
+          for (int t = 0; t < 8; ++t) kk[t] = v[u][t] = 0.f;
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          float s = 0.f;
+#pragma unroll
+          for (int t = 0; t < 8; ++t) s = fmaf(q[g][t], kk[t], s);
+          z[g][u] = s;
+        }
+      }
+      // (the lanes of a group take the same turns; groups of a warp may not)
+      const unsigned mates = LN == 32 ? 0xffffffffu : ((1u << LN) - 1) << (lane / LN * LN);
+#pragma unroll
+      for (int d = LN / 2; d > 0; d /= 2)
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int u = 0; u < U; ++u) z[g][u] += __shfl_xor_sync(mates, z[g][u], d);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float top = m[g];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (seen[u]) top = fmaxf(top, z[g][u]);
+        const float f = ex2f(m[g] - top);
+        m[g] = top;
+        l[g] *= f;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) acc[g][t] *= f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float w = seen[u] ? ex2f(z[g][u] - top) : 0.f;
+          l[g] += w;
+#pragma unroll
+          for (int t = 0; t < 8; ++t) acc[g][t] = fmaf(w, v[u][t], acc[g][t]);
+        }
+      }
+    }
+  }
+  // the groups of a warp, the warps, the CTAs
+  __syncwarp();
+#pragma unroll
+  for (int d = LN; d < 32; d *= 2)
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const float mo = __shfl_xor_sync(0xffffffffu, m[g], d), lo = __shfl_xor_sync(0xffffffffu, l[g], d);
+      const float top = fmaxf(m[g], mo), f = ex2f(m[g] - top), fo = ex2f(mo - top);
+      m[g] = top;
+      l[g] = l[g] * f + lo * fo;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) acc[g][t] = acc[g][t] * f + __shfl_xor_sync(0xffffffffu, acc[g][t], d) * fo;
+    }
+  if (lane < LN) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+      for (int t = 0; t < 8; ++t) acc_s[warp][g][lane_dim<D, KF32>(c, t)] = acc[g][t];
+      if (lane == 0) {
+        m_s[warp][g] = m[g];
+        l_s[warp][g] = l[g];
+      }
+    }
+  }
+  __syncthreads();
+  for (int x = tid; x < G * D; x += NT) {
+    const int g = x / D, d = x % D;
+    float top = NEG;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, m_s[w][g]);
+    float o = 0.f, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float f = ex2f(m_s[w][g] - top);
+      o = fmaf(acc_s[w][g][d], f, o);
+      sum = fmaf(l_s[w][g], f, sum);
+    }
+    part[g][d] = o;
+    if (d == 0) {
+      part[g][D] = top;
+      part[g][D + 1] = sum;
+    }
+  }
+  auto meet = [&] {
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  };
+  if (C > 1) meet();
+  else __syncthreads();
+  auto of = [&](int r, const float* p) {  // *p of CTA r of the cluster
+    if (C == 1) return *p;
+    uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(p)), there;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(r));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
+    return v;
+  };
+  for (int x = rank * NT + tid; x < G * D; x += C * NT) {
+    const int g = x / D, d = x % D;
+    float top = NEG;
+    for (int r = 0; r < C; ++r) top = fmaxf(top, of(r, &part[g][D]));
+    float o = 0.f, sum = 0.f;
+    for (int r = 0; r < C; ++r) {
+      const float f = ex2f(of(r, &part[g][D]) - top);
+      o = fmaf(of(r, &part[g][d]), f, o);
+      sum = fmaf(of(r, &part[g][D + 1]), f, sum);
+    }
+    const float y = sum > 0.f ? o / sum : 0.f;
+    const size_t at = ((size_t)row * a.Hq + h * G + g) * D + d;
+    if (QF32) static_cast<float*>(a.out)[at] = y;
+    else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
+  }
+  if (C > 1) meet();  // no CTA leaves while another reads it
+}
+
+template <int D, int G, bool QF32, bool KF32>
+cudaError_t launch_t(const SparseArgs& a, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.s.max_rows * a.Hkv * a.splits));
+  cfg.blockDim = dim3(NT);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)a.splits;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_sparse<D, G, QF32, KF32>, a);
+}
+template <int D, int G>
+cudaError_t launch_g(const SparseArgs& a, cudaStream_t s) {
+  if (a.q_f32) return a.kv_f32 ? launch_t<D, G, true, true>(a, s) : launch_t<D, G, true, false>(a, s);
+  return a.kv_f32 ? launch_t<D, G, false, true>(a, s) : launch_t<D, G, false, false>(a, s);
+}
+template <int D>
+cudaError_t launch_d(const SparseArgs& a, cudaStream_t s) {
+  switch (a.Hq / a.Hkv) {
+    case 2: return launch_g<D, 2>(a, s);
+    case 4: return launch_g<D, 4>(a, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_sparse(const SparseArgs& a, cudaStream_t s) {
+  if (a.s.n == 0 || a.s.max_rows == 0) return cudaSuccess;
+  if (a.D == 128) return launch_d<128>(a, s);
+  if (a.D == 64) return launch_d<64>(a, s);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace gp

@@ -1,0 +1,83 @@
+// Reading a step's device arrays inside a kernel.  The host has not seen them:
+// every index is held to the sizes of the launch before it is used, and one that
+// is outside sets an error bit and leaves its row out.
+#pragma once
+
+#include <cstdint>
+
+#include "sparse_kernels.h"
+
+namespace gp {
+
+constexpr int kStepPage = 256;
+
+struct StepRow {
+  bool live;
+  int slot;  // of the request
+  int at;    // logical slot of the row: it sees the slots [0, at]
+};
+
+__device__ __forceinline__ StepRow bad_row(const StepArgs& s, int bit, bool report) {
+  if (report) atomicOr(s.err, bit);
+  return {false, 0, 0};
+}
+
+// Row t of request r; `report`: this thread tells of an index outside.
+__device__ __forceinline__ StepRow step_row(const StepArgs& s, int r, int t, bool report) {
+  const int slot = s.slots[r], cached = s.cached[r];
+  if (slot < 0 || slot >= s.M) return bad_row(s, ERR_BAD_SLOT, report);
+  if (t < 0 || cached < 0 || (int64_t)cached + t >= (int64_t)s.maxp * kStepPage) return bad_row(s, ERR_BAD_PAGE, report);
+  return {true, slot, cached + t};
+}
+__device__ __forceinline__ StepRow find_row(const StepArgs& s, int row, bool report) {
+  const int r = s.row_req[row];
+  if (r == -1) return {false, 0, 0};
+  if (r < 0 || r >= s.n) return bad_row(s, ERR_BAD_SLOT, report);
+  return step_row(s, r, row - s.row0[r], report);
+}
+
+// The page of a logical page of `slot`; -1 (and the error bit) if it is none.
+__device__ __forceinline__ int step_page(const StepArgs& s, int slot, int logical) {
+  const int page = s.tables[(size_t)slot * s.maxp + logical];
+  if (page >= 0 && page < s.num_pages_total) return page;
+  atomicOr(s.err, ERR_BAD_PAGE);
+  return -1;
+}
+
+// Pieces of `size` rows of each request, numbered over all of them: request r's
+// are base(r), base(r) + 1, ... with base(r) = row0[r] / size + extra r, so that
+// the launch can be sized without the lengths (at most max_rows / size + extra n
+// pieces; those that no row falls into are left at once).  A whole warp calls it.
+struct StepPiece {
+  int r;     // -1: none
+  int at;    // number within the request
+  int rows;  // of the request
+  int row0;
+};
+__device__ __forceinline__ StepPiece find_piece(const StepArgs& s, int j, int size, int extra) {
+  const int lane = threadIdx.x & 31;
+  int below = 0;  // requests whose first piece is j or before
+  for (int r = lane; r < s.n; r += 32) below += s.row0[r] / size + extra * r <= j;
+  below = __reduce_add_sync(0xffffffffu, below);
+  if (below == 0) return {-1, 0, 0, 0};
+  StepPiece p;
+  p.r = below - 1;
+  p.row0 = s.row0[p.r];
+  const int end = s.row0[below];
+  p.at = j - (p.row0 / size + extra * p.r);
+  p.rows = end - p.row0;
+  if (p.row0 < 0 || end > s.max_rows || p.rows <= 0 || p.at < 0) return {-1, 0, 0, 0};
+  return p;
+}
+
+// The exponent of a scale: the least whole e >= -100 with top <= 127 * 2^e, at
+// most 100 (top >= 0, finite or not).
+__device__ __forceinline__ int scale_exponent(float top) {
+  if (!(top > 0.f)) return -100;
+  const unsigned u = __float_as_uint(top);
+  const int e = (int)(u >> 23) - 133 + ((u & 0x7fffffu) > 0x7e0000u);  // 127 = 0x1.fcp6
+  return min(max(e, -100), 100);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((unsigned)(e + 127) << 23); }
+
+}  // namespace gp
