@@ -114,6 +114,8 @@ struct gp_ctx {
   CUtensorMap vmap;                // V cache the same way (tensor-core attention)
   bool tc_ok = false;              // kmap is valid
   bool attn_tc_ok = false;         // kmap and vmap are valid
+  CUtensorMap block_maps[3][2];    // K and V in boxes of 16, 32 and 64 rows (gp_sparse_attention)
+  bool block_maps_ok[3] = {};      // made at the first call that needs them
   int sms = 152;                   // SMs of the device
   int scan_kernel = GP_SCAN_AUTO;
   int select_mode = GP_SELECT_AUTO;

@@ -1,0 +1,409 @@
+// Attention over listed blocks for one or a few rows of a request (decode steps,
+// drafted tokens), bf16 caches and queries.  The formulas are k_sparse.cu's.
+//
+// Bounded by HBM: K and V of the listed blocks are read once for the 16 / G rows
+// of a piece, whose G heads make the 16 rows of the product's A operand (mma with
+// m = 16: a decode step fills G of them, at no cost: the products take a
+// tenth of the time that the bytes do).  tcgen05 has nothing to add at M = 16.
+//
+// A cluster of `splits` CTAs a (piece, KV head).  Every CTA marks the blocks that
+// the piece's rows list, as bits, and takes an even share of the blocks marked by
+// any; a block's rows are those that list it.  One warp streams the share through a ring of
+// stages of 64 keys, K and V, by TMA (a box is a block of up to 64 tokens, 128-byte
+// swizzle).  Four warps take 16 keys of a stage each:
+//   S = Q K^T   16 x 16, ldmatrix of K
+//   P = 2^(S c - m), c = log2(e) / sqrt(d), in two bf16 parts (2^-16 of a weight is
+//   left; the output's own rounding is 2^-8), the running m and sum l in fp32
+//   O += P V    16 x d, ldmatrix.trans of V, fp32 in registers
+// with a maximum of its own a warp.  Warps and then the CTAs of the cluster are
+// joined in shared memory: no scratch, no second launch, one fixed order.
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "math2.cuh"
+#include "shared_limit.cuh"
+#include "sparse_tc.cuh"
+
+#include <algorithm>
+
+namespace gp {
+namespace {
+
+using namespace tc;
+
+constexpr int WARPS = 4;              // that compute
+constexpr int NT = 32 * (WARPS + 1);  // and one that loads
+constexpr int KEYS = 64;              // of a stage
+constexpr int NST = 3;
+constexpr float NEG = -1.0e30f;
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int D>
+struct Sm {
+  static constexpr int HALF = KEYS * 128;          // 64 dimensions of a stage's keys
+  static constexpr int TILE = D / 64 * HALF;       // K or V of a stage
+  static constexpr int RING = NST * 2 * TILE;
+  static constexpr int PART = RING;                // float [16][D + 2]
+  static constexpr int SEEN = PART + 16 * (D + 2) * 4;
+  // then: unsigned seen[T][words], any[words]; int2 list[entries]
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ SparseArgs a, const __grid_constant__ SparseMaps maps,
+                                                      int words, int entries) {
+  using L = Sm<D>;
+  constexpr int T = 16 / G;  // rows of a piece
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
+  float* part = reinterpret_cast<float*>(sm + L::PART);
+  unsigned* seen = reinterpret_cast<unsigned*>(sm + L::SEEN);
+  int2* list = reinterpret_cast<int2*>(seen + ((T * words + 1) & ~1));  // first key row in the map; block | rows << 16
+  __shared__ __align__(8) uint64_t bars[2 * NST];
+  __shared__ int abort_s, total_s;
+  __shared__ float m_s[WARPS][16], l_s[WARPS][16];
+  volatile int* abort = &abort_s;
+  const uint32_t bar0 = static_cast<uint32_t>(__cvta_generic_to_shared(bars));
+  auto full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
+  auto empty = [&](int s) { return bar0 + 8u * (uint32_t)(NST + s); };
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = a.splits, rank = blockIdx.x % C, unit = blockIdx.x / C, h = unit % a.Hkv;
+
+  const StepPiece p = find_piece(a.s, unit / a.Hkv, T, 1);
+  if (p.r < 0 || p.at * T >= p.rows) return;  // (the whole cluster)
+  const int t0 = p.at * T, m = min(T, p.rows - t0);
+  const StepRow first = step_row(a.s, p.r, t0, tid == 0), last = step_row(a.s, p.r, t0 + m - 1, tid == 0);
+  if (!first.live || !last.live) return;
+  const size_t row0 = (size_t)p.row0 + t0;
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), WARPS);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    abort_s = 0;
+  }
+  for (int i = tid; i < T * words; i += NT) seen[i] = 0u;
+  __syncthreads();
+  for (int x = warp; x < m; x += WARPS + 1)
+    mark_blocks(a.blocks + ((row0 + x) * a.Hkv + h) * a.top, a.top, (first.at + x) / a.block, seen + x * words);
+
+  // this lane's rows of Q: (row / G)-th of the piece, head row % G
+  uint32_t q[D / 16][4];
+  if (warp < WARPS) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int x = (lane >> 2) + 8 * i;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                              ((row0 + x / G) * a.Hq + h * G + x % G) * D) + (lane & 3);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        q[k][i] = x / G < m ? src[8 * k] : 0u;
+        q[k][i + 2] = x / G < m ? src[8 * k + 4] : 0u;
+      }
+    }
+  }
+  __syncthreads();
+  // the marked blocks in order; every warp counts them, the share's are listed
+  const int per = kStepPage / a.block;
+  int total = 0;
+  for (int w0 = 0; w0 < words; w0 += 32) {
+    unsigned any = 0u;
+    for (int x = 0; x < m; ++x) any |= w0 + lane < words ? seen[x * words + w0 + lane] : 0u;
+    total += __popc(any);
+  }
+  total = __reduce_add_sync(0xffffffffu, total);
+  const int from = (int)((int64_t)total * rank / C), to = (int)((int64_t)total * (rank + 1) / C);
+  if (warp == 0) {
+    int at = 0;
+    for (int w0 = 0; w0 < words; w0 += 32) {
+      unsigned any = 0u;
+      for (int x = 0; x < m; ++x) any |= w0 + lane < words ? seen[x * words + w0 + lane] : 0u;
+      const int mine = __popc(any);
+      int upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += v;
+      }
+      int e = at + upto - mine;
+      at += __shfl_sync(0xffffffffu, upto, 31);
+      for (; any; any &= any - 1, ++e)
+        if (e >= from && e < to) list[e - from].y = (w0 + lane) * 32 + __ffs(any) - 1;
+    }
+    if (lane == 0) total_s = to - from;
+  }
+  __syncthreads();
+  const int n = total_s;
+  for (int e = tid; e < n; e += NT) {
+    const int b = list[e].y, page = step_page(a.s, first.slot, b / per);
+    int rows = 0;
+    for (int x = 0; x < m; ++x) rows |= (int)(seen[x * words + (b >> 5)] >> (b & 31) & 1u) << x;
+    if (page < 0) rows = 0;  // reported; the block is left out
+    list[e] = make_int2((int)((((size_t)a.layer * a.s.num_pages_total + max(page, 0)) * a.Hkv + h) * kStepPage + b % per * a.block),
+                        b | rows << 16);
+  }
+  __syncthreads();
+
+  const int box = min(a.block, KEYS), boxes = KEYS / box;  // of a stage
+  const int of_block = a.block / box;                      // boxes of a block
+  const int all = n * of_block;                            // boxes of the share
+  const int stages = (all + boxes - 1) / boxes;
+  bool ok = true;
+  float o[D / 8][4];
+  float mx[2] = {NEG, NEG}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  if (warp == WARPS) {
+    // ---- loads ----
+    int s = 0;
+    for (; s < stages; ++s) {
+      const int slot = s % NST;
+      if (s >= NST) ok = __all_sync(0xffffffffu, wait_phase(empty(slot), (uint32_t)((s / NST - 1) & 1), abort));
+      if (!ok) break;
+      const int have = min(boxes, all - s * boxes);
+      if (lane == 0) mbar_expect_tx(full(slot), (uint32_t)(have * box * D * 4));
+      __syncwarp();
+      if (lane < have) {
+        const int e = s * boxes + lane;
+        const int y = list[e / of_block].x + e % of_block * box;
+        const uint32_t dst = sb + (uint32_t)(slot * 2 * L::TILE + lane * box * 128);
+#pragma unroll
+        for (int d = 0; d < D; d += 64) {
+          tma_load_2d(dst + (uint32_t)(d / 64 * L::HALF), &maps.k, d, y, full(slot));
+          tma_load_2d(dst + (uint32_t)(L::TILE + d / 64 * L::HALF), &maps.v, d, y, full(slot));
+        }
+      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) {
+      atomicOr(a.s.err, ERR_TIMEOUT);
+      *abort = 1;
+    }
+    // every copy issued has landed before the CTA moves on (bounded)
+    for (int x = s > NST ? s - NST : 0; x < s; ++x) drain_phase(full(x % NST), (uint32_t)((x / NST) & 1));
+  } else {
+    // ---- 16 keys a warp ----
+    const float sc = 1.4426950408889634f / sqrtf((float)D);
+    const int xr = lane & 7;
+    const uint32_t krow = (uint32_t)(16 * warp + (lane >> 4) * 8 + xr) * 128u, kc = (uint32_t)(lane >> 3 & 1);
+    const uint32_t vrow = (uint32_t)(16 * warp + (lane >> 3 & 1) * 8 + xr) * 128u, vc = (uint32_t)(lane >> 4);
+    for (int s = 0; s < stages; ++s) {
+      const int slot = s % NST;
+      ok = __all_sync(0xffffffffu, wait_phase(full(slot), (uint32_t)((s / NST) & 1), abort));
+      if (!ok) break;
+      const int e = s * boxes + 16 * warp / box;
+      const int y = e < all ? list[e / of_block].y : 0;
+      if (y >> 16) {  // some row takes this block
+        const uint32_t kt = sb + (uint32_t)(slot * 2 * L::TILE), vt = kt + (uint32_t)L::TILE;
+        // logical slot of the warp's first key
+        const int base = (y & 0xffff) * a.block + e % of_block * box + 16 * warp % box;
+        if (base + 15 > last.at) {  // slots past the piece's last row may hold any bits
+          const int key = lane >> 1;
+          if (base + key > last.at) {
+#pragma unroll
+            for (int d = 0; d < D / 64; ++d)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(sm + (size_t)slot * 2 * L::TILE + L::TILE + d * L::HALF + (16 * warp + key) * 128 +
+                                          ((lane & 1) * 4 + i) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        float z[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t b[4];
+          ldmatrix(b, kt + (uint32_t)(k / 4 * L::HALF) + krow + (((uint32_t)(2 * (k & 3)) + kc) ^ (uint32_t)xr) * 16u);
+          mma_bf16(z[0], q[k][0], q[k][1], q[k][2], q[k][3], b[0], b[1]);
+          mma_bf16(z[1], q[k][0], q[k][1], q[k][2], q[k][3], b[2], b[3]);
+        }
+        uint32_t ph[4], pl[4];
+        float f[2];
+        bool grow = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int x = ((lane >> 2) + 8 * i) / G;  // row of the piece
+          // the last of the 16 keys that it sees
+          const int lim = (y >> (16 + x) & 1) ? first.at + x - base : -1;
+          float top = mx[i];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float& v = z[j >> 1][2 * i + (j & 1)];
+            const int key = (j >> 1) * 8 + 2 * (lane & 3) + (j & 1);
+            v = key <= lim ? v * sc : __int_as_float(0xff800000);
+            top = fmaxf(top, v);
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          f[i] = ex2f(mx[i] - top);
+          grow |= top > mx[i];
+          mx[i] = top;
+          float w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = ex2f(z[j >> 1][2 * i + (j & 1)] - top);
+          l[i] = l[i] * f[i] + ((w[0] + w[1]) + (w[2] + w[3]));
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            ph[i + 2 * j] = pack2(w[2 * j], w[2 * j + 1]);
+            pl[i + 2 * j] = pack2(w[2 * j] - __uint_as_float(ph[i + 2 * j] << 16),
+                                  w[2 * j + 1] - __uint_as_float(ph[i + 2 * j] & 0xffff0000u));
+          }
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            o[i][0] *= f[0];
+            o[i][1] *= f[0];
+            o[i][2] *= f[1];
+            o[i][3] *= f[1];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t b[4];
+          ldmatrix_t(b, vt + (uint32_t)(k / 4 * L::HALF) + vrow + (((uint32_t)(2 * (k & 3)) + vc) ^ (uint32_t)xr) * 16u);
+          mma_bf16(o[2 * k], ph[0], ph[1], ph[2], ph[3], b[0], b[1]);
+          mma_bf16(o[2 * k + 1], ph[0], ph[1], ph[2], ph[3], b[2], b[3]);
+          mma_bf16(o[2 * k], pl[0], pl[1], pl[2], pl[3], b[0], b[1]);
+          mma_bf16(o[2 * k + 1], pl[0], pl[1], pl[2], pl[3], b[2], b[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(slot));
+    }
+    if (!ok && lane == 0) {
+      atomicOr(a.s.err, ERR_TIMEOUT);
+      *abort = 1;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if ((lane & 3) == 0) {
+        m_s[warp][(lane >> 2) + 8 * i] = mx[i];
+        l_s[warp][(lane >> 2) + 8 * i] = l[i];
+      }
+    }
+  }
+  __syncthreads();  // the ring is at rest
+  // ---- the warps' outputs joined ----
+  float* acc = reinterpret_cast<float*>(sm);  // [WARPS][16][D + 4]
+  if (warp < WARPS) {
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<float2*>(acc + ((size_t)warp * 16 + (lane >> 2) + 8 * j) * (D + 4) + 8 * i + 2 * (lane & 3)) =
+            make_float2(o[i][2 * j], o[i][2 * j + 1]);
+  }
+  __syncthreads();
+  const int rows = m * G;
+  for (int x = tid; x < rows * D; x += NT) {
+    const int r = x / D, d = x % D;
+    float top = NEG, y = 0.f, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) top = fmaxf(top, m_s[w][r]);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = ex2f(m_s[w][r] - top);
+      y = fmaf(acc[((size_t)w * 16 + r) * (D + 4) + d], f, y);
+      sum = fmaf(l_s[w][r], f, sum);
+    }
+    part[r * (D + 2) + d] = y;
+    if (d == 0) {
+      part[r * (D + 2) + D] = top;
+      part[r * (D + 2) + D + 1] = sum;
+    }
+  }
+  auto meet = [&] {
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  };
+  if (C > 1) meet();
+  else __syncthreads();
+  auto of = [&](int r, const float* x) {  // *x of CTA r of the cluster
+    if (C == 1) return *x;
+    uint32_t there;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(there)
+                 : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(x))), "r"(r));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
+    return v;
+  };
+  for (int x = 2 * (rank * NT + tid); x < rows * D; x += 2 * C * NT) {
+    const int r = x / D, d = x % D;
+    const float* at = part + r * (D + 2);
+    float top = NEG, y0 = 0.f, y1 = 0.f, sum = 0.f;
+    for (int c = 0; c < C; ++c) top = fmaxf(top, of(c, at + D));
+    for (int c = 0; c < C; ++c) {
+      const float f = ex2f(of(c, at + D) - top);
+      y0 = fmaf(of(c, at + d), f, y0);
+      y1 = fmaf(of(c, at + d + 1), f, y1);
+      sum = fmaf(of(c, at + D + 1), f, sum);
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + ((row0 + r / G) * a.Hq + h * G + r % G) * D + d) =
+        pack2(y0 * inv, y1 * inv);
+  }
+  if (C > 1) meet();  // no CTA leaves while another reads it
+}
+
+template <int D, int G>
+cudaError_t launch_t(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s) {
+  constexpr int T = 16 / G;
+  const int most = a.s.maxp * (kStepPage / a.block), words = (most + 31) / 32;
+  const int entries = (int)((std::min<int64_t>((int64_t)T * a.top, most) + a.splits - 1) / a.splits) + 1;
+  const int smem = 1024 + Sm<D>::SEEN + 4 * ((T * words + 1) & ~1) + 8 * entries;
+  cudaError_t e = allow_shared<&k_sparse_mma<D, G>>(1024 + Sm<D>::SEEN + 4 * T * 128 + 8 * 4098);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((a.s.max_rows / T + a.s.n) * a.Hkv * a.splits));
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)a.splits;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_sparse_mma<D, G>, a, maps, words, entries);
+}
+
+}  // namespace
+
+cudaError_t launch_sparse_mma(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s) {
+  if (a.s.n == 0 || a.s.max_rows == 0) return cudaSuccess;
+  const int G = a.Hq / a.Hkv;
+  if (a.D == 128) return G == 4 ? launch_t<128, 4>(a, maps, s) : launch_t<128, 2>(a, maps, s);
+  if (a.D == 64) return G == 4 ? launch_t<64, 4>(a, maps, s) : launch_t<64, 2>(a, maps, s);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace gp

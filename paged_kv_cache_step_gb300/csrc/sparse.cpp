@@ -98,6 +98,24 @@ StepArgs step_args(gp_ctx* c, const gp_step* s) {
   return a;
 }
 
+// The caches in boxes of a block's rows (64 of a larger block's).
+bool block_maps(gp_ctx* c, int block, SparseMaps* maps) {
+  const gp_config& g = c->cfg;
+  const int i = block == 16 ? 0 : block == 32 ? 1 : 2;
+  if (!c->block_maps_ok[i]) {
+    const cuuint64_t dims[2] = {(cuuint64_t)g.head_dim, (cuuint64_t)g.num_layers * g.num_pages * g.num_kv_heads * kPage};
+    const cuuint64_t strides[1] = {(cuuint64_t)g.head_dim * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)std::min(block, 64)};
+    if (!encode_bf16_map(&c->block_maps[i][0], 2, c->k_cache, dims, strides, box) ||
+        !encode_bf16_map(&c->block_maps[i][1], 2, c->v_cache, dims, strides, box))
+      return false;
+    c->block_maps_ok[i] = true;
+  }
+  maps->k = c->block_maps[i][0];
+  maps->v = c->block_maps[i][1];
+  return true;
+}
+
 // The scaled inverse frequencies of a rotary form (header), fp64.
 void frequencies(const gp_rope& r, double* inv, float* amplitude) {
   const double two_pi = 6.283185307179586476925, rd = r.rotary_dim, L = r.original_length;
@@ -353,11 +371,18 @@ gp_status gp_sparse_attention(gp_ctx* c, int32_t layer, const gp_step* s, int32_
   a.q = q_rot_dev;
   a.blocks = blocks_dev;
   a.out = out_dev;
+  const bool tc = c->attn_tc_ok && c->scan_kernel != GP_SCAN_CUDA_CORE && g.q_dtype == GP_DTYPE_BF16;
+  if (c->scan_kernel == GP_SCAN_TENSOR_CORE && !tc)
+    return fail(c, GP_ERR_UNSUPPORTED, "the tensor-core kernels cannot take this cache or query type");
   // two CTAs an SM while a share keeps 64 tokens or more
   const int64_t units = (int64_t)s->max_rows * g.num_kv_heads, tokens = (int64_t)std::min(top, g.max_pages_per_req * (kPage / block)) * block;
   a.splits = 1;
   while (a.splits < 8 && units * a.splits < 2 * c->sms && tokens >= 128 * a.splits) a.splits *= 2;
-  return launch_step(c, capturing, GP_KERNEL_SPARSE, "sparse_attention", [&] { return launch_sparse(a, c->stream); });
+  if (!tc)
+    return launch_step(c, capturing, GP_KERNEL_SPARSE, "sparse_attention", [&] { return launch_sparse(a, c->stream); });
+  SparseMaps maps;
+  if (!block_maps(c, block, &maps)) return fail(c, GP_ERR_CUDA, "no tensor map of the caches");
+  return launch_step(c, capturing, GP_KERNEL_SPARSE, "sparse_attention", [&] { return launch_sparse_mma(a, maps, c->stream); });
 } catch (const std::exception&) {
   return no_memory(c);
 }

@@ -1,8 +1,10 @@
 // Internal interface between the host side of the calls over a step's device
 // arrays (sparse.cpp) and their kernels (k_tables.cu, k_mapped.cu, k_bounds.cu,
-// k_block_select.cu, k_sparse.cu).  Plain structs of device pointers and sizes;
+// k_block_select.cu, k_sparse.cu, k_sparse_mma.cu).  Plain structs of device pointers and sizes;
 // no torch types.
 #pragma once
+
+#include <cuda.h>
 
 #include "gp_kernels.h"
 
@@ -92,6 +94,12 @@ cudaError_t launch_tables(const TablesArgs& a, cudaStream_t s);
 cudaError_t launch_mapped(const MappedArgs& a, cudaStream_t s);
 cudaError_t launch_bounds(const BoundsArgs& a, cudaStream_t s);
 cudaError_t launch_select_blocks(const SelectBlocksArgs& a, cudaStream_t s);
+// K and V as 2-D tensors of key rows, boxes of 64 dimensions by a block (64 rows of
+// one that is larger).
+struct SparseMaps {
+  CUtensorMap k, v;
+};
 cudaError_t launch_sparse(const SparseArgs& a, cudaStream_t s);
+cudaError_t launch_sparse_mma(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s);  // bf16 caches and queries
 
 }  // namespace gp
