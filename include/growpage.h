@@ -639,8 +639,9 @@ gp_status gp_select_blocks(gp_ctx* ctx, int32_t layer, const gp_step* step, int3
  * blocks_dev: int32 [max_rows][Hkv][top]; a list is ascending and ends at the first
  * entry that is negative, not above the one before it, or past the row's own
  * block; an empty one gives 0.  q_rot_dev, out_dev: [max_rows][Hq][d] q_dtype,
- * 16-byte aligned, apart.  Keys and values of the tokens attended to must
- * be finite; other cache slots may hold any bits. */
+ * 16-byte aligned, apart.  Keys and values of the listed blocks, up to the
+ * request's last token of the step, must be finite; other cache slots may hold any
+ * bits. */
 gp_status gp_sparse_attention(gp_ctx* ctx, int32_t layer, const gp_step* step, int32_t block, int32_t top,
                               const void* q_rot_dev, const int32_t* blocks_dev, void* out_dev);
 

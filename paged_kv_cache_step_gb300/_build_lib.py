@@ -20,7 +20,7 @@ LIB = os.path.join(BUILD, "libgrowpage.so")
 
 SOURCES = ["growpage.cpp", "k_summaries.cu", "k_demand.cu", "k_demand_tc.cu", "k_compress.cu", "k_attention.cu",
            "k_attention_tc.cu", "k_entropy.cu", "noalloc.cu", "weighted.cpp", "k_append.cu", "k_weights.cu", "k_chunk.cu", "k_chunk_tc.cu",
-           "k_evict.cu", "sparse.cpp", "k_tables.cu", "k_mapped.cu", "k_bounds.cu", "k_block_select.cu", "k_sparse.cu", "k_sparse_mma.cu"]
+           "k_evict.cu", "sparse.cpp", "k_tables.cu", "k_mapped.cu", "k_bounds.cu", "k_block_select.cu", "k_sparse.cu", "k_sparse_mma.cu", "k_sparse_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -42,7 +42,7 @@ def _stale(obj: str, src: str) -> bool:
     t = os.path.getmtime(obj)
     deps = [src, os.path.join(CSRC, "gp_kernels.h"), os.path.join(CSRC, "gp_internal.h"),
             os.path.join(CSRC, "demand_common.cuh"), os.path.join(CSRC, "engine.h"),
-            os.path.join(CSRC, "attn_kernels.h"), os.path.join(CSRC, "tc_ptx.cuh"),
+            os.path.join(CSRC, "attn_kernels.h"), os.path.join(CSRC, "tc_ptx.cuh"), os.path.join(CSRC, "tc_rows.cuh"),
             os.path.join(CSRC, "weighted_kernels.h"), os.path.join(CSRC, "chained.cuh"),
             os.path.join(CSRC, "sparse_kernels.h"), os.path.join(CSRC, "step.cuh"), os.path.join(CSRC, "sparse_tc.cuh"),
             os.path.join(CSRC, "math2.cuh"), os.path.join(CSRC, "shared_limit.cuh"),

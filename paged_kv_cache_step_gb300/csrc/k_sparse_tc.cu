@@ -1,0 +1,405 @@
+// Attention over listed blocks for many rows of a request (prompts), on the tensor
+// cores (tcgen05): bf16 caches and queries.  The formulas are k_sparse.cu's.
+//
+// A piece is 128 / G rows of a request; with the G heads of a KV head they make the
+// 128 rows of a product.  The piece goes through the blocks that any of its rows
+// lists, each loaded once; a row takes weight 0 in a block that it does not list, by
+// a bias of its exponent.  Neighbouring rows list much the same blocks, so this
+// reads and multiplies a few times what one row alone needs, where a pass of
+// its own for each row reads all of it from L2 every time.
+//
+// Per stage of 64 keys:
+//   S = Q K^T        128 x 64, Q from TMEM, fp32 in TMEM
+//   P = 2^(S c - m)  in two bf16 parts over S (2^-15 of a weight is left, as
+//                    k_chunk_tc.cu's), a maximum followed only when it grows by
+//                    more than 24: O is then rescaled in TMEM
+//   O += P V         128 x d, both parts, V MN-major as TMA left it
+// A CTA holds 256 of the 512 columns of TMEM (Q d / 2, S and P 64, O d) and half of
+// the shared memory, so that two CTAs share an SM: one's softmax runs beside the
+// other's products, and one's start beside the other's work.
+//   warps 0-3   softmax (thread = row = TMEM lane), then the outputs
+//   warp 4      lists the blocks, then loads K and V (TMA, a box a block of up to 64)
+//   warp 5      issues the products
+// Every wait is bounded: on expiry the CTA records ERR_TIMEOUT, waits for what it
+// has in flight, frees its TMEM and returns.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "math2.cuh"
+#include "shared_limit.cuh"
+#include "sparse_tc.cuh"
+#include "tc_rows.cuh"
+
+namespace gp {
+namespace {
+
+using namespace tc;
+
+constexpr int NT = 192;
+constexpr int KEYS = 64;  // of a stage
+constexpr int TMEM_COLS = 256;
+constexpr float NEG = -1.0e30f;
+constexpr float LAZY = 24.f;  // base-2 growth of a maximum that is not followed
+
+template <int D>
+struct Sm {
+  static constexpr int HALF = KEYS * 128;     // 64 dimensions of a stage's keys
+  static constexpr int TILE = D / 64 * HALF;  // K or V of a stage
+  static constexpr int NST = 384 / D;         // stages: 96 KB
+  static constexpr int RING = NST * 2 * TILE;
+  // then: int page[256]; unsigned seen[T][words]; uint16_t list[blocks]
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ SparseArgs a, const __grid_constant__ SparseMaps maps,
+                                                     int words) {
+  using L = Sm<D>;
+  constexpr int T = 128 / G, NST = L::NST;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
+  int* pages = reinterpret_cast<int*>(sm + L::RING);  // first key row of a page in the map; -1
+  unsigned* seen = reinterpret_cast<unsigned*>(pages + 256);
+  uint16_t* list = reinterpret_cast<uint16_t*>(seen + T * words);
+  __shared__ __align__(8) uint64_t bars[2 * NST + 4];
+  __shared__ int abort_s, count_s;
+  __shared__ uint32_t tmem_s;
+  volatile int* abort = &abort_s;
+  const uint32_t bar0 = static_cast<uint32_t>(__cvta_generic_to_shared(bars));
+  auto full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
+  auto empty = [&](int s) { return bar0 + 8u * (uint32_t)(NST + s); };
+  const uint32_t s_ready = bar0 + 8u * (uint32_t)(2 * NST), p_ready = s_ready + 8u, o_done = s_ready + 16u, mma_done = s_ready + 24u;
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
+  const int h = blockIdx.x % a.Hkv;
+
+  const StepPiece p = find_piece(a.s, blockIdx.x / a.Hkv, T, 1);
+  if (p.r < 0 || p.at * T >= p.rows) return;
+  const int t0 = p.at * T, m_rows = min(T, p.rows - t0);
+  const StepRow first = step_row(a.s, p.r, t0, tid == 0), last = step_row(a.s, p.r, t0 + m_rows - 1, tid == 0);
+  if (!first.live || !last.live) return;
+  const size_t row0 = (size_t)p.row0 + t0;
+  const int per = kStepPage / a.block;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2 * NST + 4; ++i) mbar_init(bar0 + 8u * (uint32_t)i, i == 2 * NST + 1 ? 4u : 1u);  // p_ready: four warps
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    abort_s = 0;
+  }
+  if (warp == 5) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(&tmem_s))),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  for (int i = tid; i < T * words; i += NT) seen[i] = 0u;
+  for (int i = tid; i <= last.at / kStepPage; i += NT) {
+    const int page = a.s.tables[(size_t)first.slot * a.s.maxp + i];
+    pages[i] = page >= 0 && page < a.s.num_pages_total
+                   ? (int)((((size_t)a.layer * a.s.num_pages_total + page) * a.Hkv + h) * kStepPage) : -1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = (uint32_t)uniform((int)tmem_s);
+  const uint32_t tq = tmem + D + 64, ts = tmem + D, to = tmem;  // columns: O, S and P, Q
+  for (int x = warp; x < m_rows; x += NT / 32)
+    mark_blocks(a.blocks + ((row0 + x) * a.Hkv + h) * a.top, a.top, (first.at + x) / a.block, seen + x * words);
+  const int tok = tid / G, sees = first.at + tok;  // of softmax threads
+  const bool valid = warp < 4 && tok < m_rows;
+  const size_t at = ((row0 + tok) * a.Hq + h * G + tid % G) * D;
+  const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+  if (warp < 4) {
+#pragma unroll
+    for (int d = 0; d < D; d += 64) {
+      uint32_t q[32];
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at + d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4 u = valid ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+        q[4 * i] = u.x;
+        q[4 * i + 1] = u.y;
+        q[4 * i + 2] = u.z;
+        q[4 * i + 3] = u.w;
+      }
+      tmem_store32(tq + lanes + (uint32_t)(d / 2), q);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 4) {  // the blocks that any row lists, in order
+    int n = 0;
+    for (int w0 = 0; w0 < words; w0 += 32) {
+      const int w = w0 + lane;
+      unsigned any = 0u;
+      if (w < words)
+        for (int x = 0; x < m_rows; ++x) any |= seen[x * words + w];
+      for (unsigned left = any; left; left &= left - 1) {
+        const int bit = __ffs(left) - 1;
+        if (pages[(w * 32 + bit) / per] >= 0) continue;
+        atomicOr(a.s.err, ERR_BAD_PAGE);  // the block is left out
+        any &= ~(1u << bit);
+      }
+      const int mine = __popc(any);
+      int upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += v;
+      }
+      for (int e = n + upto - mine; any; any &= any - 1) list[e++] = (uint16_t)(w * 32 + __ffs(any) - 1);
+      n += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (lane == 0) count_s = n;
+  }
+  __syncthreads();
+  const int box = min(a.block, KEYS), boxes = KEYS / box, of_block = a.block / box;
+  const int all = uniform(count_s) * of_block;  // boxes
+  const int stages = (all + boxes - 1) / boxes;
+  bool ok = true;
+  auto timed_out = [&] {
+    atomicOr(a.s.err, ERR_TIMEOUT);
+    *abort = 1;
+  };
+
+  if (warp == 4) {
+    // ---- loads ----
+    int s = 0;
+    for (; s < stages; ++s) {
+      const int slot = s % NST;
+      if (s >= NST) ok = __all_sync(0xffffffffu, wait_phase(empty(slot), (uint32_t)((s / NST - 1) & 1), abort));
+      if (!ok) break;
+      const int have = min(boxes, all - s * boxes);
+      if (lane == 0) mbar_expect_tx(full(slot), (uint32_t)(have * box * D * 4));
+      __syncwarp();
+      if (lane < have) {
+        const int e = s * boxes + lane, b = list[e / of_block];
+        const int y = pages[b / per] + b % per * a.block + e % of_block * box;
+        const uint32_t dst = sb + (uint32_t)(slot * 2 * L::TILE + lane * box * 128);
+#pragma unroll
+        for (int d = 0; d < D; d += 64) {
+          tma_load_2d(dst + (uint32_t)(d / 64 * L::HALF), &maps.k, d, y, full(slot));
+          tma_load_2d(dst + (uint32_t)(L::TILE + d / 64 * L::HALF), &maps.v, d, y, full(slot));
+        }
+      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) timed_out();
+    // every copy issued has landed before the CTA moves on (bounded)
+    for (int x = s > NST ? s - NST : 0; x < s; ++x) drain_phase(full(x % NST), (uint32_t)((x / NST) & 1));
+  } else if (warp == 5) {
+    // ---- products ----
+    tc_fence_after();
+    auto wait = [&](uint32_t bar, int phase) {
+      ok = ok && __all_sync(0xffffffffu, wait_phase(bar, (uint32_t)(phase & 1), abort));
+    };
+    auto tile = [&](int s) { return sb + (uint32_t)(s % NST * 2 * L::TILE); };
+    auto score = [&](int s) {
+      wait(full(s % NST), s / NST);
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t k0 = sw128_desc(tile(s));
+#pragma unroll
+      for (int e = 0; e < D / 16; ++e)
+        mma_ts(ts, tq + (uint32_t)(8 * e), k0 + (uint64_t)(((e >> 2) * L::HALF + (e & 3) * 32) >> 4), idesc(KEYS, false), e > 0 ? 1u : 0u);
+      commit(s_ready);
+    };
+    if (stages > 0) score(0);
+    for (int s = 0; s < stages && ok; ++s) {
+      wait(p_ready, s);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t v0 = sw128_mn_desc(tile(s) + (uint32_t)L::TILE, L::HALF);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+          mma_ts(to, ts + (uint32_t)(32 * part + 8 * e), v0 + (uint64_t)(e * 2048 >> 4), idesc(D, true), s == 0 && e == 0 && part == 0 ? 0u : 1u);
+      commit(empty(s % NST));
+      if (s + 1 == stages) commit(o_done);
+      else score(s + 1);  // over P, which the products before it have read
+    }
+    if (!ok && lane == 0) timed_out();
+    // every product issued has completed before TMEM is released (bounded)
+    commit(mma_done);
+    drain_phase(mma_done, 0u);
+    __syncwarp();
+  } else {
+    // ---- softmax: thread = row ----
+    const float sc = 1.4426950408889634f / sqrtf((float)D);
+    const uint32_t my_s = ts + lanes, my_o = to + lanes;
+    const unsigned* mine = seen + min(tok, T - 1) * words;
+    float m = NEG, l = 0.f;
+    for (int s = 0; s < stages; ++s) {
+      // the row's part in each 16 keys of the stage
+      bool in[4];
+      const bool tail = s + 1 == stages;
+      const int end = min(s * boxes + boxes, all);  // past the stage's last box
+      const bool partly = tail || list[(end - 1) / of_block] * a.block + (end - 1) % of_block * box + box - 1 > first.at;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = s * boxes + 16 * i / box;
+        in[i] = false;
+        if (e < all) {
+          const int b = list[e / of_block];
+          in[i] = mine[b >> 5] >> (b & 31) & 1u;
+        }
+      }
+      ok = __all_sync(0xffffffffu, wait_phase(s_ready, (uint32_t)(s & 1), abort));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t r[2][32];
+      tmem_load32(my_s, r[0]);
+      tmem_load32(my_s + 32u, r[1]);
+      tmem_wait_ld();
+      tmem_arrived(r[0]);
+      tmem_arrived(r[1]);
+      if (partly) {
+        // slots that not every row sees, and places that no block filled, which may
+        // hold any bits
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = s * boxes + 16 * i / box;
+          const int base = e < all ? list[e / of_block] * a.block + e % of_block * box + 16 * i % box : 0;
+          const int keep = in[i] ? sees - base : -1;
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if (c > keep) r[i / 2][16 * (i & 1) + c] = 0xff800000u;  // -inf
+        }
+      }
+      float top = NEG;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t* x = r[i / 2] + 16 * (i & 1);
+        float mx = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+#pragma unroll
+        for (int c = 3; c < 15; c += 2) mx = max3(mx, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+        mx = fmaxf(mx, __uint_as_float(x[15]));
+        top = fmaxf(top, in[i] ? sc * mx : NEG);
+      }
+      if (s == 0) {
+        m = fmaxf(m, top);
+      } else {
+        const bool grow = top > m + LAZY;
+        if (__any_sync(0xffffffffu, grow)) {
+          // the products issued before this S have completed: O is at rest
+          const float mn = grow ? top : m, f = ex2f(m - mn);
+          m = mn;
+          l *= f;
+#pragma unroll 1
+          for (int d = 0; d < D; d += 32) {
+            uint32_t o[32];
+            tmem_load32(my_o + (uint32_t)d, o);
+            tmem_wait_ld();
+            tmem_arrived(o);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+            tmem_store32(my_o + (uint32_t)d, o);
+          }
+        }
+      }
+      const float2 sc2 = make_float2(sc, sc);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float bias = in[2 * q + c / 8] ? -m : __int_as_float(0xff800000);
+          float2 z = fma2(make_float2(__uint_as_float(r[q][2 * c]), __uint_as_float(r[q][2 * c + 1])), sc2, make_float2(bias, bias));
+          z.x = ex2f(z.x);
+          z.y = ex2f(z.y);
+          sum[c & 1] = add2(sum[c & 1], z);
+          hi[c] = __byte_perm(__float_as_uint(z.x), __float_as_uint(z.y), 0x7632);  // the upper halves
+          z = less_bf16(z, hi[c]);
+          lo[c] = pack_bf16(z.x, z.y);
+        }
+        tmem_store16(my_s + (uint32_t)(16 * q), hi);
+        tmem_store16(my_s + (uint32_t)(32 + 16 * q), lo);
+      }
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      if (tail) {  // weight 0 times any bits is not 0: those rows of V are cleared
+        const int slot = s % NST, key = tid >> 1;
+        ok = __all_sync(0xffffffffu, wait_phase(full(slot), (uint32_t)((s / NST) & 1), abort));
+        if (!ok) break;
+        const int e = s * boxes + key / box;
+        if (e >= all || list[e / of_block] * a.block + e % of_block * box + key % box > last.at) {
+          unsigned char* v = sm + (size_t)slot * 2 * L::TILE + L::TILE + (size_t)key * 128 + (tid & 1) * 64;
+#pragma unroll
+          for (int d = 0; d < D / 64; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(v + (size_t)d * L::HALF)[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_ready);
+    }
+    if (ok && stages > 0) ok = __all_sync(0xffffffffu, wait_phase(o_done, 0u, abort));
+    if (ok) {
+      tc_fence_after();
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+      for (int d = 0; d < D; d += 32) {
+        uint32_t o[32];
+        if (stages > 0) {
+          tmem_load32(my_o + (uint32_t)d, o);
+          tmem_wait_ld();
+          tmem_arrived(o);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = 0u;
+        }
+        if (valid) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at + d);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              u[k] = pack_bf16(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+            dst[e] = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+        }
+        __syncwarp();
+      }
+    } else if (lane == 0) {
+      timed_out();
+    }
+    tmem_wait_st();  // a loop that was left between a store and its wait
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+  }
+}
+
+template <int D, int G>
+cudaError_t launch_t(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s) {
+  constexpr int T = 128 / G;
+  const int most = a.s.maxp * (kStepPage / a.block), words = (most + 31) / 32;
+  const int smem = 1024 + Sm<D>::RING + 4 * 256 + 4 * T * words + 2 * most;
+  cudaError_t e = allow_shared<&k_sparse_tc<D, G>>(1024 + Sm<D>::RING + 4 * 256 + 4 * T * 128 + 2 * 4096);
+  if (e != cudaSuccess) return e;
+  k_sparse_tc<D, G><<<dim3((unsigned)((a.s.max_rows / T + a.s.n) * a.Hkv)), NT, smem, s>>>(a, maps, words);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_sparse_tc(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s) {
+  if (a.s.n == 0 || a.s.max_rows == 0) return cudaSuccess;
+  const int G = a.Hq / a.Hkv;
+  if (a.D == 128) return G == 4 ? launch_t<128, 4>(a, maps, s) : launch_t<128, 2>(a, maps, s);
+  if (a.D == 64) return G == 4 ? launch_t<64, 4>(a, maps, s) : launch_t<64, 2>(a, maps, s);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace gp

@@ -382,7 +382,9 @@ gp_status gp_sparse_attention(gp_ctx* c, int32_t layer, const gp_step* s, int32_
     return launch_step(c, capturing, GP_KERNEL_SPARSE, "sparse_attention", [&] { return launch_sparse(a, c->stream); });
   SparseMaps maps;
   if (!block_maps(c, block, &maps)) return fail(c, GP_ERR_CUDA, "no tensor map of the caches");
-  return launch_step(c, capturing, GP_KERNEL_SPARSE, "sparse_attention", [&] { return launch_sparse_mma(a, maps, c->stream); });
+  const bool many = s->max_rows >= 16 * s->n;
+  return launch_step(c, capturing, GP_KERNEL_SPARSE, "sparse_attention",
+                     [&] { return many ? launch_sparse_tc(a, maps, c->stream) : launch_sparse_mma(a, maps, c->stream); });
 } catch (const std::exception&) {
   return no_memory(c);
 }

@@ -1,6 +1,6 @@
 // Internal interface between the host side of the calls over a step's device
 // arrays (sparse.cpp) and their kernels (k_tables.cu, k_mapped.cu, k_bounds.cu,
-// k_block_select.cu, k_sparse.cu, k_sparse_mma.cu).  Plain structs of device pointers and sizes;
+// k_block_select.cu, k_sparse.cu, k_sparse_mma.cu, k_sparse_tc.cu).  Plain structs of device pointers and sizes;
 // no torch types.
 #pragma once
 
@@ -100,6 +100,8 @@ struct SparseMaps {
   CUtensorMap k, v;
 };
 cudaError_t launch_sparse(const SparseArgs& a, cudaStream_t s);
-cudaError_t launch_sparse_mma(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s);  // bf16 caches and queries
+// bf16 caches and queries: a few rows of a request at a time, and many
+cudaError_t launch_sparse_mma(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s);
+cudaError_t launch_sparse_tc(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s);
 
 }  // namespace gp
