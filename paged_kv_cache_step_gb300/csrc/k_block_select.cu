@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(NT) k_block_select(const __grid_constant__ Sel
   }
   __syncthreads();
 
-  const int per = kStepPage / a.block;
-  const int some = max(0, last.at / a.block + 1 - a.recent);  // blocks that a row may have to choose from
+  const int lb = log2_of(a.block), lper = kStepPageLog - lb;  // blocks of a page
+  const int some = max(0, (last.at >> lb) + 1 - a.recent);  // blocks that a row may have to choose from
   constexpr int CHUNKS = 2 * D / 64;
   uint32_t bq[CHUNKS][4][2];
 #pragma unroll
@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(NT) k_block_select(const __grid_constant__ Sel
 #pragma unroll
     for (int k = 0; k < 2; ++k) {  // this lane's two blocks
       const int b = min(b0 + (lane >> 2) + 8 * k, some - 1);
-      const int page = max(step_page(a.s, first.slot, b / per), 0);
-      const size_t at = (((size_t)a.layer * a.s.num_pages_total + page) * a.Hkv + h) * per + b % per;
+      const int page = max(step_page(a.s, first.slot, b >> lper), 0);
+      const size_t at = (((((size_t)a.layer * a.s.num_pages_total + page) * a.Hkv) + h) << lper) + (b & ((1 << lper) - 1));
       src[k] = reinterpret_cast<const uint4*>(a.bounds + at * 2 * D) + (lane & 3);
       scale[k] = a.scales[at];
     }
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(NT) k_block_select(const __grid_constant__ Sel
   }
   __syncthreads();
   for (int x = warp; x < m; x += NT / 32) {
-    const int end = (first.at + x) / a.block + 1;  // blocks that the row sees
+    const int end = ((first.at + x) >> lb) + 1;  // blocks that the row sees
     int32_t* out = a.blocks + ((row0 + x) * a.Hkv + h) * a.top;
     if (end <= a.top) {
       for (int k = lane; k < a.top; k += 32) out[k] = k < end ? k : -1;

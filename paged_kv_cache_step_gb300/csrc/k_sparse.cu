@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(NT) k_sparse(const __grid_constant__ SparseArg
   const int row = (int)(unit / a.Hkv), h = (int)(unit % a.Hkv);
   const StepRow rw = find_row(a.s, row, tid == 0);
   if (!rw.live) return;  // (the whole cluster)
-  const int own = rw.at / a.block, per = kStepPage / a.block;
+  const int lb = log2_of(a.block), lper = kStepPageLog - lb, own = rw.at >> lb;
   const int32_t* list = a.blocks + unit * a.top;
   if (tid == 0) count_s = a.top;
   __syncthreads();
@@ -102,18 +102,18 @@ __global__ void __launch_bounds__(NT) k_sparse(const __grid_constant__ SparseArg
     const int n = min(ENTRIES, to - e0);
     __syncthreads();
     if (tid < n) {
-      const int b = list[e0 + tid], page = step_page(a.s, rw.slot, b / per);
-      at_s[tid] = page < 0 ? -1 : (((int64_t)a.layer * a.s.num_pages_total + page) * a.Hkv + h) * kStepPage + b % per * a.block;
-      tok_s[tid] = b * a.block;
+      const int b = list[e0 + tid], page = step_page(a.s, rw.slot, b >> lper);
+      at_s[tid] = page < 0 ? -1 : (((int64_t)a.layer * a.s.num_pages_total + page) * a.Hkv + h) * kStepPage + ((b << lb) & (kStepPage - 1));
+      tok_s[tid] = b << lb;
     }
     __syncthreads();
-    const int keys = n * a.block;
+    const int keys = n << lb;
     for (int k0 = group; k0 < keys; k0 += GROUPS * U) {
       float z[G][U], v[U][8];
       bool seen[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int k = k0 + u * GROUPS, e = k / a.block, o = k % a.block;
+        const int k = k0 + u * GROUPS, e = k >> lb, o = k & (a.block - 1);
         seen[u] = k < keys && at_s[min(e, n - 1)] >= 0 && tok_s[min(e, n - 1)] + o <= rw.at;
         float kk[8];
         if (seen[u]) {

@@ -68,7 +68,7 @@ struct Sm {
   static constexpr int RING = NST * 2 * TILE;
   static constexpr int PART = RING;                // float [16][D + 2]
   static constexpr int SEEN = PART + 16 * (D + 2) * 4;
-  // then: unsigned seen[T][words], any[words]; int2 list[entries]
+  // then: unsigned any[words], seen[T][words]; int2 list[entries]
 };
 
 template <int D, int G>
@@ -80,8 +80,9 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
   float* part = reinterpret_cast<float*>(sm + L::PART);
-  unsigned* seen = reinterpret_cast<unsigned*>(sm + L::SEEN);
-  int2* list = reinterpret_cast<int2*>(seen + ((T * words + 1) & ~1));  // first key row in the map; block | rows << 16
+  unsigned* any_s = reinterpret_cast<unsigned*>(sm + L::SEEN);
+  unsigned* seen = any_s + words;
+  int2* list = reinterpret_cast<int2*>(any_s + (((T + 1) * words + 1) & ~1));  // first key row in the map; block | rows << 16
   __shared__ __align__(8) uint64_t bars[2 * NST];
   __shared__ int abort_s, total_s;
   __shared__ float m_s[WARPS][16], l_s[WARPS][16];
@@ -106,10 +107,10 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     abort_s = 0;
   }
-  for (int i = tid; i < T * words; i += NT) seen[i] = 0u;
+  for (int i = tid; i < (T + 1) * words; i += NT) any_s[i] = 0u;
   __syncthreads();
-  for (int x = warp; x < m; x += WARPS + 1)
-    mark_blocks(a.blocks + ((row0 + x) * a.Hkv + h) * a.top, a.top, (first.at + x) / a.block, seen + x * words);
+  const int lb = log2_of(a.block), lper = kStepPageLog - lb;  // blocks of a page
+  mark_blocks<WARPS + 1, T>(a, row0, m, h, first.at, lb, words, seen, any_s);
 
   // this lane's rows of Q: (row / G)-th of the piece, head row % G
   uint32_t q[D / 16][4];
@@ -128,20 +129,14 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
   }
   __syncthreads();
   // the marked blocks in order; every warp counts them, the share's are listed
-  const int per = kStepPage / a.block;
   int total = 0;
-  for (int w0 = 0; w0 < words; w0 += 32) {
-    unsigned any = 0u;
-    for (int x = 0; x < m; ++x) any |= w0 + lane < words ? seen[x * words + w0 + lane] : 0u;
-    total += __popc(any);
-  }
+  for (int w = lane; w < words; w += 32) total += __popc(any_s[w]);
   total = __reduce_add_sync(0xffffffffu, total);
   const int from = (int)((int64_t)total * rank / C), to = (int)((int64_t)total * (rank + 1) / C);
   if (warp == 0) {
     int at = 0;
     for (int w0 = 0; w0 < words; w0 += 32) {
-      unsigned any = 0u;
-      for (int x = 0; x < m; ++x) any |= w0 + lane < words ? seen[x * words + w0 + lane] : 0u;
+      unsigned any = w0 + lane < words ? any_s[w0 + lane] : 0u;
       const int mine = __popc(any);
       int upto = mine;
 #pragma unroll
@@ -159,19 +154,18 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
   __syncthreads();
   const int n = total_s;
   for (int e = tid; e < n; e += NT) {
-    const int b = list[e].y, page = step_page(a.s, first.slot, b / per);
+    const int b = list[e].y, page = step_page(a.s, first.slot, b >> lper);
     int rows = 0;
     for (int x = 0; x < m; ++x) rows |= (int)(seen[x * words + (b >> 5)] >> (b & 31) & 1u) << x;
     if (page < 0) rows = 0;  // reported; the block is left out
-    list[e] = make_int2((int)((((size_t)a.layer * a.s.num_pages_total + max(page, 0)) * a.Hkv + h) * kStepPage + b % per * a.block),
+    list[e] = make_int2((int)((((size_t)a.layer * a.s.num_pages_total + max(page, 0)) * a.Hkv + h) * kStepPage + ((b << lb) & (kStepPage - 1))),
                         b | rows << 16);
   }
   __syncthreads();
 
-  const int box = min(a.block, KEYS), boxes = KEYS / box;  // of a stage
-  const int of_block = a.block / box;                      // boxes of a block
-  const int all = n * of_block;                            // boxes of the share
-  const int stages = (all + boxes - 1) / boxes;
+  const int lx = min(lb, 6), box = 1 << lx, boxes = KEYS >> lx, lof = lb - lx;  // a box, of a stage, log2 of those of a block
+  const int all = n << lof;                                                    // boxes of the share
+  const int stages = (all + boxes - 1) >> (6 - lx);
   bool ok = true;
   float o[D / 8][4];
   float mx[2] = {NEG, NEG}, l[2] = {0.f, 0.f};
@@ -189,7 +183,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
       __syncwarp();
       if (lane < have) {
         const int e = s * boxes + lane;
-        const int y = list[e / of_block].x + e % of_block * box;
+        const int y = list[e >> lof].x + ((e & ((1 << lof) - 1)) << lx);
         const uint32_t dst = sb + (uint32_t)(slot * 2 * L::TILE + lane * box * 128);
 #pragma unroll
         for (int d = 0; d < D; d += 64) {
@@ -215,12 +209,12 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
       const int slot = s % NST;
       ok = __all_sync(0xffffffffu, wait_phase(full(slot), (uint32_t)((s / NST) & 1), abort));
       if (!ok) break;
-      const int e = s * boxes + 16 * warp / box;
-      const int y = e < all ? list[e / of_block].y : 0;
+      const int e = s * boxes + (16 * warp >> lx);
+      const int y = e < all ? list[e >> lof].y : 0;
       if (y >> 16) {  // some row takes this block
         const uint32_t kt = sb + (uint32_t)(slot * 2 * L::TILE), vt = kt + (uint32_t)L::TILE;
         // logical slot of the warp's first key
-        const int base = (y & 0xffff) * a.block + e % of_block * box + 16 * warp % box;
+        const int base = ((y & 0xffff) << lb) + ((e & ((1 << lof) - 1)) << lx) + (16 * warp & (box - 1));
         if (base + 15 > last.at) {  // slots past the piece's last row may hold any bits
           const int key = lane >> 1;
           if (base + key > last.at) {
@@ -379,8 +373,8 @@ cudaError_t launch_t(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s
   constexpr int T = 16 / G;
   const int most = a.s.maxp * (kStepPage / a.block), words = (most + 31) / 32;
   const int entries = (int)((std::min<int64_t>((int64_t)T * a.top, most) + a.splits - 1) / a.splits) + 1;
-  const int smem = 1024 + Sm<D>::SEEN + 4 * ((T * words + 1) & ~1) + 8 * entries;
-  cudaError_t e = allow_shared<&k_sparse_mma<D, G>>(1024 + Sm<D>::SEEN + 4 * T * 128 + 8 * 4098);
+  const int smem = 1024 + Sm<D>::SEEN + 4 * (((T + 1) * words + 1) & ~1) + 8 * entries;
+  cudaError_t e = allow_shared<&k_sparse_mma<D, G>>(1024 + Sm<D>::SEEN + 4 * (T + 1) * 128 + 8 * 4098);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((a.s.max_rows / T + a.s.n) * a.Hkv * a.splits));

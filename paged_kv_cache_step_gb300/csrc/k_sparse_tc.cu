@@ -9,14 +9,16 @@
 // its own for each row reads all of it from L2 every time.
 //
 // Per stage of 64 keys:
-//   S = Q K^T        128 x 64, Q from TMEM, fp32 in TMEM
+//   S = Q K^T        128 x 64, fp32 in TMEM, double buffered
 //   P = 2^(S c - m)  in two bf16 parts over S (2^-15 of a weight is left, as
 //                    k_chunk_tc.cu's), a maximum followed only when it grows by
 //                    more than 24: O is then rescaled in TMEM
 //   O += P V         128 x d, both parts, V MN-major as TMA left it
-// A CTA holds 256 of the 512 columns of TMEM (Q d / 2, S and P 64, O d) and half of
+// A CTA holds 256 of the 512 columns of TMEM (O d, S and P twice 64) and half of
 // the shared memory, so that two CTAs share an SM: one's softmax runs beside the
-// other's products, and one's start beside the other's work.
+// other's products, and one's start beside the other's work.  The products are
+// issued as S0 S1 O0 S2 O1 S3 ..., so that a CTA's softmax finds the next S done; K and
+// V come through one ring in that order.
 //   warps 0-3   softmax (thread = row = TMEM lane), then the outputs
 //   warp 4      lists the blocks, then loads K and V (TMA, a box a block of up to 64)
 //   warp 5      issues the products
@@ -47,9 +49,11 @@ template <int D>
 struct Sm {
   static constexpr int HALF = KEYS * 128;     // 64 dimensions of a stage's keys
   static constexpr int TILE = D / 64 * HALF;  // K or V of a stage
-  static constexpr int NST = 384 / D;         // stages: 96 KB
-  static constexpr int RING = NST * 2 * TILE;
-  // then: int page[256]; unsigned seen[T][words]; uint16_t list[blocks]
+  static constexpr int NST = 512 / D;         // tiles in flight: 64 KB
+  static constexpr int QHALF = 128 * 128;     // 64 dimensions of the rows of Q
+  static constexpr int Q = NST * TILE;
+  static constexpr int RING = Q + D / 64 * QHALF;
+  // then: int page[256]; unsigned any[words], seen[T][words]; uint16_t list[blocks]
 };
 
 template <int D, int G>
@@ -61,16 +65,19 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
   int* pages = reinterpret_cast<int*>(sm + L::RING);  // first key row of a page in the map; -1
-  unsigned* seen = reinterpret_cast<unsigned*>(pages + 256);
+  unsigned* any_s = reinterpret_cast<unsigned*>(pages + 256);
+  unsigned* seen = any_s + words;
   uint16_t* list = reinterpret_cast<uint16_t*>(seen + T * words);
-  __shared__ __align__(8) uint64_t bars[2 * NST + 4];
-  __shared__ int abort_s, count_s;
+  __shared__ __align__(8) uint64_t bars[2 * NST + 6];
+  __shared__ int abort_s, count_s, bad_s;
   __shared__ uint32_t tmem_s;
   volatile int* abort = &abort_s;
   const uint32_t bar0 = static_cast<uint32_t>(__cvta_generic_to_shared(bars));
   auto full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
   auto empty = [&](int s) { return bar0 + 8u * (uint32_t)(NST + s); };
-  const uint32_t s_ready = bar0 + 8u * (uint32_t)(2 * NST), p_ready = s_ready + 8u, o_done = s_ready + 16u, mma_done = s_ready + 24u;
+  auto s_ready = [&](int s) { return bar0 + 8u * (uint32_t)(2 * NST + (s & 1)); };
+  auto p_ready = [&](int s) { return bar0 + 8u * (uint32_t)(2 * NST + 2 + (s & 1)); };
+  const uint32_t o_done = bar0 + 8u * (uint32_t)(2 * NST + 4), mma_done = o_done + 8u;  // o_done: once a stage
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const int h = blockIdx.x % a.Hkv;
 
@@ -80,12 +87,13 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   const StepRow first = step_row(a.s, p.r, t0, tid == 0), last = step_row(a.s, p.r, t0 + m_rows - 1, tid == 0);
   if (!first.live || !last.live) return;
   const size_t row0 = (size_t)p.row0 + t0;
-  const int per = kStepPage / a.block;
+  const int lb = log2_of(a.block), lper = kStepPageLog - lb;  // blocks of a page
 
   if (tid == 0) {
-    for (int i = 0; i < 2 * NST + 4; ++i) mbar_init(bar0 + 8u * (uint32_t)i, i == 2 * NST + 1 ? 4u : 1u);  // p_ready: four warps
+    for (int i = 0; i < 2 * NST + 6; ++i)  // p_ready: four warps
+      mbar_init(bar0 + 8u * (uint32_t)i, i == 2 * NST + 2 || i == 2 * NST + 3 ? 4u : 1u);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    abort_s = 0;
+    abort_s = bad_s = 0;
   }
   if (warp == 5) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -94,7 +102,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  for (int i = tid; i < T * words; i += NT) seen[i] = 0u;
+  for (int i = tid; i < (T + 1) * words; i += NT) any_s[i] = 0u;
   for (int i = tid; i <= last.at / kStepPage; i += NT) {
     const int page = a.s.tables[(size_t)first.slot * a.s.maxp + i];
     pages[i] = page >= 0 && page < a.s.num_pages_total
@@ -104,42 +112,30 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)tmem_s);
-  const uint32_t tq = tmem + D + 64, ts = tmem + D, to = tmem;  // columns: O, S and P, Q
-  for (int x = warp; x < m_rows; x += NT / 32)
-    mark_blocks(a.blocks + ((row0 + x) * a.Hkv + h) * a.top, a.top, (first.at + x) / a.block, seen + x * words);
+  for (int i = tid; i <= last.at / kStepPage; i += NT)
+    if (pages[i] < 0) bad_s = 1;
+  const uint32_t ts = tmem + D, to = tmem;  // columns: O, S and P of even and of odd stages
+  mark_blocks<NT / 32, T>(a, row0, m_rows, h, first.at, lb, words, seen, any_s);
   const int tok = tid / G, sees = first.at + tok;  // of softmax threads
   const bool valid = warp < 4 && tok < m_rows;
   const size_t at = ((row0 + tok) * a.Hq + h * G + tid % G) * D;
   const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-  if (warp < 4) {
+  if (warp < 4) {  // Q, K-major with the 128-byte swizzle
 #pragma unroll
-    for (int d = 0; d < D; d += 64) {
-      uint32_t q[32];
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at + d);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 u = valid ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-        q[4 * i] = u.x;
-        q[4 * i + 1] = u.y;
-        q[4 * i + 2] = u.z;
-        q[4 * i + 3] = u.w;
-      }
-      tmem_store32(tq + lanes + (uint32_t)(d / 2), q);
-    }
-    tmem_wait_st();
-    tc_fence_before();
+    for (int c = 0; c < D / 8; ++c)
+      *reinterpret_cast<uint4*>(sm + L::Q + c / 8 * L::QHALF + tid * 128 + ((c & 7) ^ (tid & 7)) * 16) =
+          valid ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at)[c] : make_uint4(0u, 0u, 0u, 0u);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   __syncthreads();
   if (warp == 4) {  // the blocks that any row lists, in order
     int n = 0;
     for (int w0 = 0; w0 < words; w0 += 32) {
       const int w = w0 + lane;
-      unsigned any = 0u;
-      if (w < words)
-        for (int x = 0; x < m_rows; ++x) any |= seen[x * words + w];
-      for (unsigned left = any; left; left &= left - 1) {
+      unsigned any = w < words ? any_s[w] : 0u;
+      for (unsigned left = bad_s ? any : 0u; left; left &= left - 1) {
         const int bit = __ffs(left) - 1;
-        if (pages[(w * 32 + bit) / per] >= 0) continue;
+        if (pages[(w * 32 + bit) >> lper] >= 0) continue;
         atomicOr(a.s.err, ERR_BAD_PAGE);  // the block is left out
         any &= ~(1u << bit);
       }
@@ -156,9 +152,11 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
     if (lane == 0) count_s = n;
   }
   __syncthreads();
-  const int box = min(a.block, KEYS), boxes = KEYS / box, of_block = a.block / box;
-  const int all = uniform(count_s) * of_block;  // boxes
-  const int stages = (all + boxes - 1) / boxes;
+  const int lx = min(lb, 6), box = 1 << lx, boxes = KEYS >> lx, lof = lb - lx;  // a box, of a stage, log2 of those of a block
+  const int all = uniform(count_s) << lof;                                     // boxes
+  // first logical slot of box e
+  auto slot_of = [&](int e) { return ((int)list[e >> lof] << lb) + ((e & ((1 << lof) - 1)) << lx); };
+  const int stages = (all + boxes - 1) >> (6 - lx);
   bool ok = true;
   auto timed_out = [&] {
     atomicOr(a.s.err, ERR_TIMEOUT);
@@ -167,60 +165,69 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
 
   if (warp == 4) {
     // ---- loads ----
-    int s = 0;
-    for (; s < stages; ++s) {
-      const int slot = s % NST;
-      if (s >= NST) ok = __all_sync(0xffffffffu, wait_phase(empty(slot), (uint32_t)((s / NST - 1) & 1), abort));
-      if (!ok) break;
+    int c = 0;  // tiles issued
+    auto load = [&](const CUtensorMap* map, int s) {
+      const int slot = c % NST;
+      if (c >= NST) ok = ok && __all_sync(0xffffffffu, wait_phase(empty(slot), (uint32_t)((c / NST - 1) & 1), abort));
+      if (!ok) return;
       const int have = min(boxes, all - s * boxes);
-      if (lane == 0) mbar_expect_tx(full(slot), (uint32_t)(have * box * D * 4));
+      if (lane == 0) mbar_expect_tx(full(slot), (uint32_t)(have * box * D * 2));
       __syncwarp();
       if (lane < have) {
-        const int e = s * boxes + lane, b = list[e / of_block];
-        const int y = pages[b / per] + b % per * a.block + e % of_block * box;
-        const uint32_t dst = sb + (uint32_t)(slot * 2 * L::TILE + lane * box * 128);
+        const int at0 = slot_of(s * boxes + lane), y = pages[at0 >> kStepPageLog] + (at0 & (kStepPage - 1));
+        const uint32_t dst = sb + (uint32_t)(slot * L::TILE + lane * box * 128);
 #pragma unroll
-        for (int d = 0; d < D; d += 64) {
-          tma_load_2d(dst + (uint32_t)(d / 64 * L::HALF), &maps.k, d, y, full(slot));
-          tma_load_2d(dst + (uint32_t)(L::TILE + d / 64 * L::HALF), &maps.v, d, y, full(slot));
-        }
+        for (int d = 0; d < D; d += 64) tma_load_2d(dst + (uint32_t)(d / 64 * L::HALF), map, d, y, full(slot));
       }
       __syncwarp();
+      ++c;
+    };
+    if (stages > 0) load(&maps.k, 0);
+    if (stages > 1) load(&maps.k, 1);
+    for (int s = 0; s < stages && ok; ++s) {
+      load(&maps.v, s);
+      if (s + 2 < stages) load(&maps.k, s + 2);
     }
     if (!ok && lane == 0) timed_out();
     // every copy issued has landed before the CTA moves on (bounded)
-    for (int x = s > NST ? s - NST : 0; x < s; ++x) drain_phase(full(x % NST), (uint32_t)((x / NST) & 1));
+    for (int x = c > NST ? c - NST : 0; x < c; ++x) drain_phase(full(x % NST), (uint32_t)((x / NST) & 1));
   } else if (warp == 5) {
     // ---- products ----
     tc_fence_after();
     auto wait = [&](uint32_t bar, int phase) {
       ok = ok && __all_sync(0xffffffffu, wait_phase(bar, (uint32_t)(phase & 1), abort));
     };
-    auto tile = [&](int s) { return sb + (uint32_t)(s % NST * 2 * L::TILE); };
+    int c = 0;  // tiles used
+    auto tile = [&] { return sb + (uint32_t)(c % NST * L::TILE); };
     auto score = [&](int s) {
-      wait(full(s % NST), s / NST);
+      wait(full(c % NST), c / NST);
       if (!ok) return;
       tc_fence_after();
-      const uint64_t k0 = sw128_desc(tile(s));
+      const uint64_t q0 = sw128_desc(sb + (uint32_t)L::Q), k0 = sw128_desc(tile());
 #pragma unroll
       for (int e = 0; e < D / 16; ++e)
-        mma_ts(ts, tq + (uint32_t)(8 * e), k0 + (uint64_t)(((e >> 2) * L::HALF + (e & 3) * 32) >> 4), idesc(KEYS, false), e > 0 ? 1u : 0u);
-      commit(s_ready);
+        mma_ss(ts + (uint32_t)(64 * (s & 1)), q0 + (uint64_t)(((e >> 2) * L::QHALF + (e & 3) * 32) >> 4),
+               k0 + (uint64_t)(((e >> 2) * L::HALF + (e & 3) * 32) >> 4), idesc(KEYS, false), e > 0 ? 1u : 0u);
+      commit(s_ready(s));
+      commit(empty(c++ % NST));
     };
     if (stages > 0) score(0);
+    if (stages > 1) score(1);
     for (int s = 0; s < stages && ok; ++s) {
-      wait(p_ready, s);
+      wait(full(c % NST), c / NST);
+      wait(p_ready(s), s >> 1);
       if (!ok) break;
       tc_fence_after();
-      const uint64_t v0 = sw128_mn_desc(tile(s) + (uint32_t)L::TILE, L::HALF);
+      const uint64_t v0 = sw128_mn_desc(tile(), L::HALF);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
         for (int part = 0; part < 2; ++part)
-          mma_ts(to, ts + (uint32_t)(32 * part + 8 * e), v0 + (uint64_t)(e * 2048 >> 4), idesc(D, true), s == 0 && e == 0 && part == 0 ? 0u : 1u);
-      commit(empty(s % NST));
-      if (s + 1 == stages) commit(o_done);
-      else score(s + 1);  // over P, which the products before it have read
+          mma_ts(to, ts + (uint32_t)(64 * (s & 1) + 32 * part + 8 * e), v0 + (uint64_t)(e * 2048 >> 4), idesc(D, true),
+                 s == 0 && e == 0 && part == 0 ? 0u : 1u);
+      commit(o_done);
+      commit(empty(c++ % NST));
+      if (s + 2 < stages) score(s + 2);  // over P, which the products before it have read
     }
     if (!ok && lane == 0) timed_out();
     // every product issued has completed before TMEM is released (bounded)
@@ -230,7 +237,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   } else {
     // ---- softmax: thread = row ----
     const float sc = 1.4426950408889634f / sqrtf((float)D);
-    const uint32_t my_s = ts + lanes, my_o = to + lanes;
+    const uint32_t my_o = to + lanes;
     const unsigned* mine = seen + min(tok, T - 1) * words;
     float m = NEG, l = 0.f;
     for (int s = 0; s < stages; ++s) {
@@ -238,17 +245,18 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
       bool in[4];
       const bool tail = s + 1 == stages;
       const int end = min(s * boxes + boxes, all);  // past the stage's last box
-      const bool partly = tail || list[(end - 1) / of_block] * a.block + (end - 1) % of_block * box + box - 1 > first.at;
+      const bool partly = tail || slot_of(end - 1) + box - 1 > first.at;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int e = s * boxes + 16 * i / box;
+        const int e = s * boxes + (16 * i >> lx);
         in[i] = false;
         if (e < all) {
-          const int b = list[e / of_block];
+          const int b = list[e >> lof];
           in[i] = mine[b >> 5] >> (b & 31) & 1u;
         }
       }
-      ok = __all_sync(0xffffffffu, wait_phase(s_ready, (uint32_t)(s & 1), abort));
+      const uint32_t my_s = ts + lanes + (uint32_t)(64 * (s & 1));
+      ok = __all_sync(0xffffffffu, wait_phase(s_ready(s), (uint32_t)(s >> 1 & 1), abort));
       if (!ok) break;
       tc_fence_after();
       uint32_t r[2][32];
@@ -262,8 +270,8 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
         // hold any bits
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int e = s * boxes + 16 * i / box;
-          const int base = e < all ? list[e / of_block] * a.block + e % of_block * box + 16 * i % box : 0;
+          const int e = s * boxes + (16 * i >> lx);
+          const int base = e < all ? slot_of(e) + (16 * i & (box - 1)) : 0;
           const int keep = in[i] ? sees - base : -1;
 #pragma unroll
           for (int c = 0; c < 16; ++c)
@@ -285,7 +293,11 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
       } else {
         const bool grow = top > m + LAZY;
         if (__any_sync(0xffffffffu, grow)) {
-          // the products issued before this S have completed: O is at rest
+          // O is at rest once the products with the last P have completed (those before
+          // it completed before this S)
+          ok = __all_sync(0xffffffffu, wait_phase(o_done, (uint32_t)((s - 1) & 1), abort));
+          if (!ok) break;
+          tc_fence_after();
           const float mn = grow ? top : m, f = ex2f(m - mn);
           m = mn;
           l *= f;
@@ -322,12 +334,12 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
       }
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       if (tail) {  // weight 0 times any bits is not 0: those rows of V are cleared
-        const int slot = s % NST, key = tid >> 1;
-        ok = __all_sync(0xffffffffu, wait_phase(full(slot), (uint32_t)((s / NST) & 1), abort));
+        const int c = 2 * stages - 1, slot = c % NST, key = tid >> 1;  // the last tile
+        ok = __all_sync(0xffffffffu, wait_phase(full(slot), (uint32_t)((c / NST) & 1), abort));
         if (!ok) break;
-        const int e = s * boxes + key / box;
-        if (e >= all || list[e / of_block] * a.block + e % of_block * box + key % box > last.at) {
-          unsigned char* v = sm + (size_t)slot * 2 * L::TILE + L::TILE + (size_t)key * 128 + (tid & 1) * 64;
+        const int e = s * boxes + (key >> lx);
+        if (e >= all || slot_of(e) + (key & (box - 1)) > last.at) {
+          unsigned char* v = sm + (size_t)slot * L::TILE + (size_t)key * 128 + (tid & 1) * 64;
 #pragma unroll
           for (int d = 0; d < D / 64; ++d)
 #pragma unroll
@@ -338,9 +350,9 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_ready);
+      if (lane == 0) mbar_arrive(p_ready(s));
     }
-    if (ok && stages > 0) ok = __all_sync(0xffffffffu, wait_phase(o_done, 0u, abort));
+    if (ok) ok = __all_sync(0xffffffffu, wait_phase(mma_done, 0u, abort));  // (o_done may be two stages behind)
     if (ok) {
       tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -385,8 +397,8 @@ template <int D, int G>
 cudaError_t launch_t(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s) {
   constexpr int T = 128 / G;
   const int most = a.s.maxp * (kStepPage / a.block), words = (most + 31) / 32;
-  const int smem = 1024 + Sm<D>::RING + 4 * 256 + 4 * T * words + 2 * most;
-  cudaError_t e = allow_shared<&k_sparse_tc<D, G>>(1024 + Sm<D>::RING + 4 * 256 + 4 * T * 128 + 2 * 4096);
+  const int smem = 1024 + Sm<D>::RING + 4 * 256 + 4 * (T + 1) * words + 2 * most;
+  cudaError_t e = allow_shared<&k_sparse_tc<D, G>>(1024 + Sm<D>::RING + 4 * 256 + 4 * (T + 1) * 128 + 2 * 4096);
   if (e != cudaSuccess) return e;
   k_sparse_tc<D, G><<<dim3((unsigned)((a.s.max_rows / T + a.s.n) * a.Hkv)), NT, smem, s>>>(a, maps, words);
   return cudaGetLastError();

@@ -10,6 +10,11 @@
 namespace gp {
 
 constexpr int kStepPage = 256;
+constexpr int kStepPageLog = 8;
+
+// log2 of a block's tokens: places and pages of blocks are shifts (a division by a
+// size that the compiler does not know is some thirty instructions).
+__device__ __forceinline__ int log2_of(int block) { return 31 - __clz(block); }
 
 struct StepRow {
   bool live;
