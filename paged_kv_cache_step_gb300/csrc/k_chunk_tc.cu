@@ -82,14 +82,6 @@ constexpr int TMEM_COLS = 512;
 constexpr float NEG = -1.0e30f;
 constexpr float LAZY = 24.f;                 // base-2 growth of a maximum that is not followed
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-
 // Registers of the calling warpgroup (all of its warps call it).  The shares add
 // up to what the block was launched with.
 template <int N>

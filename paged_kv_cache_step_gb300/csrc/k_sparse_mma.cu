@@ -96,6 +96,8 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
   const StepPiece p = find_piece(a.s, unit / a.Hkv, T, 1);
   if (p.r < 0 || p.at * T >= p.rows) return;  // (the whole cluster)
   const int t0 = p.at * T, m = min(T, p.rows - t0);
+  BlockLists<WARPS + 1, T> lists;
+  lists.load(a, (size_t)p.row0 + t0, h, lists.rows_of(m), 0);
   const StepRow first = step_row(a.s, p.r, t0, tid == 0), last = step_row(a.s, p.r, t0 + m - 1, tid == 0);
   if (!first.live || !last.live) return;
   const size_t row0 = (size_t)p.row0 + t0;
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
   for (int i = tid; i < (T + 1) * words; i += NT) any_s[i] = 0u;
   __syncthreads();
   const int lb = log2_of(a.block), lper = kStepPageLog - lb;  // blocks of a page
-  mark_blocks<WARPS + 1, T>(a, row0, m, h, first.at, lb, words, seen, any_s);
+  lists.mark(a, row0, h, m, first.at, lb, words, seen, any_s);
 
   // this lane's rows of Q: (row / G)-th of the piece, head row % G
   uint32_t q[D / 16][4];

@@ -58,7 +58,7 @@ struct Sm {
 
 template <int D, int G>
 __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ SparseArgs a, const __grid_constant__ SparseMaps maps,
-                                                     int words) {
+                                                     const __grid_constant__ CUtensorMap qmap, int words) {
   using L = Sm<D>;
   constexpr int T = 128 / G, NST = L::NST;
   extern __shared__ unsigned char smem_raw[];
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   unsigned* any_s = reinterpret_cast<unsigned*>(pages + 256);
   unsigned* seen = any_s + words;
   uint16_t* list = reinterpret_cast<uint16_t*>(seen + T * words);
-  __shared__ __align__(8) uint64_t bars[2 * NST + 6];
+  __shared__ __align__(8) uint64_t bars[2 * NST + 7];
   __shared__ int abort_s, count_s, bad_s;
   __shared__ uint32_t tmem_s;
   volatile int* abort = &abort_s;
@@ -77,23 +77,30 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   auto empty = [&](int s) { return bar0 + 8u * (uint32_t)(NST + s); };
   auto s_ready = [&](int s) { return bar0 + 8u * (uint32_t)(2 * NST + (s & 1)); };
   auto p_ready = [&](int s) { return bar0 + 8u * (uint32_t)(2 * NST + 2 + (s & 1)); };
-  const uint32_t o_done = bar0 + 8u * (uint32_t)(2 * NST + 4), mma_done = o_done + 8u;  // o_done: once a stage
+  const uint32_t o_done = bar0 + 8u * (uint32_t)(2 * NST + 4), mma_done = o_done + 8u, q_full = o_done + 16u;  // o_done: once a stage
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const int h = blockIdx.x % a.Hkv;
 
   const StepPiece p = find_piece(a.s, blockIdx.x / a.Hkv, T, 1);
   if (p.r < 0 || p.at * T >= p.rows) return;
   const int t0 = p.at * T, m_rows = min(T, p.rows - t0);
+  BlockLists<NT / 32, T> lists;
+  lists.load(a, (size_t)p.row0 + t0, h, lists.rows_of(m_rows), 0);
   const StepRow first = step_row(a.s, p.r, t0, tid == 0), last = step_row(a.s, p.r, t0 + m_rows - 1, tid == 0);
   if (!first.live || !last.live) return;
   const size_t row0 = (size_t)p.row0 + t0;
   const int lb = log2_of(a.block), lper = kStepPageLog - lb;  // blocks of a page
 
   if (tid == 0) {
-    for (int i = 0; i < 2 * NST + 6; ++i)  // p_ready: four warps
+    for (int i = 0; i < 2 * NST + 7; ++i)  // p_ready: four warps
       mbar_init(bar0 + 8u * (uint32_t)i, i == 2 * NST + 2 || i == 2 * NST + 3 ? 4u : 1u);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     abort_s = bad_s = 0;
+    // the G heads of the piece's rows (and of what follows them: a row of the
+    // products that is no row of the piece is never looked at)
+    mbar_expect_tx(q_full, (uint32_t)(D / 64 * L::QHALF));
+    for (int d = 0; d < D; d += 64)
+      tma_load_3d(sb + (uint32_t)(L::Q + d / 64 * L::QHALF), &qmap, d, h * G, (int)row0, q_full);
   }
   if (warp == 5) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -115,18 +122,11 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   for (int i = tid; i <= last.at / kStepPage; i += NT)
     if (pages[i] < 0) bad_s = 1;
   const uint32_t ts = tmem + D, to = tmem;  // columns: O, S and P of even and of odd stages
-  mark_blocks<NT / 32, T>(a, row0, m_rows, h, first.at, lb, words, seen, any_s);
+  lists.mark(a, row0, h, m_rows, first.at, lb, words, seen, any_s);
   const int tok = tid / G, sees = first.at + tok;  // of softmax threads
   const bool valid = warp < 4 && tok < m_rows;
   const size_t at = ((row0 + tok) * a.Hq + h * G + tid % G) * D;
   const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-  if (warp < 4) {  // Q, K-major with the 128-byte swizzle
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c)
-      *reinterpret_cast<uint4*>(sm + L::Q + c / 8 * L::QHALF + tid * 128 + ((c & 7) ^ (tid & 7)) * 16) =
-          valid ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at)[c] : make_uint4(0u, 0u, 0u, 0u);
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  }
   __syncthreads();
   if (warp == 4) {  // the blocks that any row lists, in order
     int n = 0;
@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
     if (!ok && lane == 0) timed_out();
     // every copy issued has landed before the CTA moves on (bounded)
     for (int x = c > NST ? c - NST : 0; x < c; ++x) drain_phase(full(x % NST), (uint32_t)((x / NST) & 1));
+    drain_phase(q_full, 0u);
   } else if (warp == 5) {
     // ---- products ----
     tc_fence_after();
@@ -211,8 +212,9 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
       commit(s_ready(s));
       commit(empty(c++ % NST));
     };
-    if (stages > 0) score(0);
-    if (stages > 1) score(1);
+    wait(q_full, 0);
+    if (stages > 0 && ok) score(0);
+    if (stages > 1 && ok) score(1);
     for (int s = 0; s < stages && ok; ++s) {
       wait(full(c % NST), c / NST);
       wait(p_ready(s), s >> 1);
@@ -394,23 +396,23 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
 }
 
 template <int D, int G>
-cudaError_t launch_t(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s) {
+cudaError_t launch_t(const SparseArgs& a, const SparseMaps& maps, const CUtensorMap& qmap, cudaStream_t s) {
   constexpr int T = 128 / G;
   const int most = a.s.maxp * (kStepPage / a.block), words = (most + 31) / 32;
   const int smem = 1024 + Sm<D>::RING + 4 * 256 + 4 * (T + 1) * words + 2 * most;
   cudaError_t e = allow_shared<&k_sparse_tc<D, G>>(1024 + Sm<D>::RING + 4 * 256 + 4 * (T + 1) * 128 + 2 * 4096);
   if (e != cudaSuccess) return e;
-  k_sparse_tc<D, G><<<dim3((unsigned)((a.s.max_rows / T + a.s.n) * a.Hkv)), NT, smem, s>>>(a, maps, words);
+  k_sparse_tc<D, G><<<dim3((unsigned)((a.s.max_rows / T + a.s.n) * a.Hkv)), NT, smem, s>>>(a, maps, qmap, words);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_sparse_tc(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s) {
+cudaError_t launch_sparse_tc(const SparseArgs& a, const SparseMaps& maps, const CUtensorMap& qmap, cudaStream_t s) {
   if (a.s.n == 0 || a.s.max_rows == 0) return cudaSuccess;
   const int G = a.Hq / a.Hkv;
-  if (a.D == 128) return G == 4 ? launch_t<128, 4>(a, maps, s) : launch_t<128, 2>(a, maps, s);
-  if (a.D == 64) return G == 4 ? launch_t<64, 4>(a, maps, s) : launch_t<64, 2>(a, maps, s);
+  if (a.D == 128) return G == 4 ? launch_t<128, 4>(a, maps, qmap, s) : launch_t<128, 2>(a, maps, qmap, s);
+  if (a.D == 64) return G == 4 ? launch_t<64, 4>(a, maps, qmap, s) : launch_t<64, 2>(a, maps, qmap, s);
   return cudaErrorInvalidValue;
 }
 

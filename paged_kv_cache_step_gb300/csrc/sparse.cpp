@@ -383,8 +383,16 @@ gp_status gp_sparse_attention(gp_ctx* c, int32_t layer, const gp_step* s, int32_
   SparseMaps maps;
   if (!block_maps(c, block, &maps)) return fail(c, GP_ERR_CUDA, "no tensor map of the caches");
   const bool many = s->max_rows >= 16 * s->n;
+  CUtensorMap qmap;
+  if (many) {
+    const cuuint64_t G = (cuuint64_t)(g.num_q_heads / g.num_kv_heads), row = (cuuint64_t)g.head_dim * 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)g.head_dim, (cuuint64_t)g.num_q_heads, (cuuint64_t)s->max_rows};
+    const cuuint64_t strides[2] = {row, row * g.num_q_heads};
+    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(kSparseTcRows / G)};
+    if (!encode_bf16_map(&qmap, 3, q_rot_dev, dims, strides, box)) return fail(c, GP_ERR_CUDA, "no tensor map of the queries");
+  }
   return launch_step(c, capturing, GP_KERNEL_SPARSE, "sparse_attention",
-                     [&] { return many ? launch_sparse_tc(a, maps, c->stream) : launch_sparse_mma(a, maps, c->stream); });
+                     [&] { return many ? launch_sparse_tc(a, maps, qmap, c->stream) : launch_sparse_mma(a, maps, c->stream); });
 } catch (const std::exception&) {
   return no_memory(c);
 }

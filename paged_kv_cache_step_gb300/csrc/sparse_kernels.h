@@ -102,6 +102,7 @@ struct SparseMaps {
 cudaError_t launch_sparse(const SparseArgs& a, cudaStream_t s);
 // bf16 caches and queries: a few rows of a request at a time, and many
 cudaError_t launch_sparse_mma(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s);
-cudaError_t launch_sparse_tc(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s);
+cudaError_t launch_sparse_tc(const SparseArgs& a, const SparseMaps& maps, const CUtensorMap& qmap, cudaStream_t s);
+constexpr int kSparseTcRows = 128;  // qmap's box: 64 dimensions of G heads of 128 / G rows
 
 }  // namespace gp

@@ -25,42 +25,55 @@ __device__ __forceinline__ void drain_phase(uint32_t bar, uint32_t parity) {
   wait_phase(bar, parity, &zero);
 }
 
-// Sets the bits of the blocks listed by the rows of a piece, a row's in seen[x * words]
-// and all of them in any (both cleared before).  A list counts up to its first
-// entry that is negative, not above the one before it or past the row's own block.
-// Every warp of the CTA calls it and takes each WARPS-th row, its loads in flight
-// together.
+// The lists of a piece's rows: every warp of the CTA takes each WARPS-th row, its loads
+// in flight together.  The first 32 entries are loaded ahead, as the rows are known
+// before their places are.
 template <int WARPS, int T>
-__device__ __forceinline__ void mark_blocks(const SparseArgs& a, size_t row0, int m, int h, int first_at, int lb, int words,
-                                            unsigned* seen, unsigned* any) {
-  constexpr int N = (T + WARPS - 1) / WARPS;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int before[N];
-  unsigned live = 0u;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    before[i] = -1;
-    if (warp + i * WARPS < m) live |= 1u << i;
-  }
-  for (int k0 = 0; k0 < a.top && live; k0 += 32) {
-    int b[N];
+struct BlockLists {
+  static constexpr int N = (T + WARPS - 1) / WARPS;
+  int b[N];
+
+  __device__ __forceinline__ void load(const SparseArgs& a, size_t row0, int h, unsigned live, int k0) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int i = 0; i < N; ++i)
       b[i] = (live >> i & 1u) && k0 + lane < a.top ? a.blocks[((row0 + warp + i * WARPS) * a.Hkv + h) * a.top + k0 + lane] : -1;
+  }
+  static __device__ __forceinline__ unsigned rows_of(int m) {  // of this warp, of m in the piece
+    unsigned live = 0u;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int x = warp + i * WARPS;
-      int last = __shfl_up_sync(0xffffffffu, b[i], 1);
-      if (lane == 0) last = before[i];
-      const unsigned ends = __ballot_sync(0xffffffffu, b[i] < 0 || b[i] <= last || b[i] > (first_at + x) >> lb);
-      if (!(ends & ((2u << lane) - 1))) {
-        atomicOr(&seen[x * words + (b[i] >> 5)], 1u << (b[i] & 31));
-        atomicOr(&any[b[i] >> 5], 1u << (b[i] & 31));
+    for (int i = 0; i < N; ++i)
+      if ((int)(threadIdx.x >> 5) + i * WARPS < m) live |= 1u << i;
+    return live;
+  }
+  // Sets the bits of the listed blocks, a row's in seen[x * words] and all of them in
+  // any (both cleared before).  A list counts up to its first entry that is negative,
+  // not above the one before it or past the row's own block.
+  __device__ __forceinline__ void mark(const SparseArgs& a, size_t row0, int h, int m, int first_at, int lb, int words,
+                                       unsigned* seen, unsigned* any) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int before[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) before[i] = -1;
+    unsigned live = rows_of(m);
+    for (int k0 = 0; live; load(a, row0, h, live, k0)) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int x = warp + i * WARPS;
+        int last = __shfl_up_sync(0xffffffffu, b[i], 1);
+        if (lane == 0) last = before[i];
+        const unsigned ends = __ballot_sync(0xffffffffu, b[i] < 0 || b[i] <= last || b[i] > (first_at + x) >> lb);
+        if (!(ends & ((2u << lane) - 1))) {
+          atomicOr(&seen[x * words + (b[i] >> 5)], 1u << (b[i] & 31));
+          atomicOr(&any[b[i] >> 5], 1u << (b[i] & 31));
+        }
+        if (ends) live &= ~(1u << i);
+        before[i] = __shfl_sync(0xffffffffu, b[i], 31);
       }
-      if (ends) live &= ~(1u << i);
-      before[i] = __shfl_sync(0xffffffffu, b[i], 31);
+      k0 += 32;
+      if (k0 >= a.top) break;
     }
   }
-}
+};
 
 }  // namespace gp
