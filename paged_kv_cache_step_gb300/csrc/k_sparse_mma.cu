@@ -68,7 +68,7 @@ struct Sm {
   static constexpr int RING = NST * 2 * TILE;
   static constexpr int PART = RING;                // float [16][D + 2]
   static constexpr int SEEN = PART + 16 * (D + 2) * 4;
-  // then: unsigned any[words], seen[T][words]; int2 list[entries]
+  // then: int page[256]; unsigned any[words], seen[T][words]; int2 list[entries]
 };
 
 template <int D, int G>
@@ -80,7 +80,8 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = static_cast<uint32_t>(__cvta_generic_to_shared(sm));
   float* part = reinterpret_cast<float*>(sm + L::PART);
-  unsigned* any_s = reinterpret_cast<unsigned*>(sm + L::SEEN);
+  int* pages = reinterpret_cast<int*>(sm + L::SEEN);  // first key row of a page in the map; -1
+  unsigned* any_s = reinterpret_cast<unsigned*>(pages + 256);
   unsigned* seen = any_s + words;
   int2* list = reinterpret_cast<int2*>(any_s + (((T + 1) * words + 1) & ~1));  // first key row in the map; block | rows << 16
   __shared__ __align__(8) uint64_t bars[2 * NST];
@@ -110,6 +111,11 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
     abort_s = 0;
   }
   for (int i = tid; i < (T + 1) * words; i += NT) any_s[i] = 0u;
+  for (int i = tid; i <= last.at / kStepPage; i += NT) {
+    const int page = a.s.tables[(size_t)first.slot * a.s.maxp + i];
+    pages[i] = page >= 0 && page < a.s.num_pages_total
+                   ? (int)((((size_t)a.layer * a.s.num_pages_total + page) * a.Hkv + h) * kStepPage) : -1;
+  }
   __syncthreads();
   const int lb = log2_of(a.block), lper = kStepPageLog - lb;  // blocks of a page
   lists.mark(a, row0, h, m, first.at, lb, words, seen, any_s);
@@ -156,17 +162,21 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
   __syncthreads();
   const int n = total_s;
   for (int e = tid; e < n; e += NT) {
-    const int b = list[e].y, page = step_page(a.s, first.slot, b >> lper);
+    const int b = list[e].y, page = pages[b >> lper];
     int rows = 0;
     for (int x = 0; x < m; ++x) rows |= (int)(seen[x * words + (b >> 5)] >> (b & 31) & 1u) << x;
-    if (page < 0) rows = 0;  // reported; the block is left out
-    list[e] = make_int2((int)((((size_t)a.layer * a.s.num_pages_total + max(page, 0)) * a.Hkv + h) * kStepPage + ((b << lb) & (kStepPage - 1))),
-                        b | rows << 16);
+    if (page < 0) {  // the block is left out
+      atomicOr(a.s.err, ERR_BAD_PAGE);
+      rows = 0;
+    }
+    list[e] = make_int2(max(page, 0) + ((b << lb) & (kStepPage - 1)), b | rows << 16);
   }
   __syncthreads();
 
   const int lx = min(lb, 6), box = 1 << lx, boxes = KEYS >> lx, lof = lb - lx;  // a box, of a stage, log2 of those of a block
-  const int all = n << lof;                                                    // boxes of the share
+  int all = n << lof;                                                          // boxes of the share
+  // without those of the last block past the rows
+  while (all > 0 && ((list[(all - 1) >> lof].y & 0xffff) << lb) + (((all - 1) & ((1 << lof) - 1)) << lx) > last.at) --all;
   const int stages = (all + boxes - 1) >> (6 - lx);
   bool ok = true;
   float o[D / 8][4];
@@ -375,11 +385,11 @@ cudaError_t launch_t(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s
   constexpr int T = 16 / G;
   const int most = a.s.maxp * (kStepPage / a.block), words = (most + 31) / 32;
   const int entries = (int)((std::min<int64_t>((int64_t)T * a.top, most) + a.splits - 1) / a.splits) + 1;
-  const int smem = 1024 + Sm<D>::SEEN + 4 * (((T + 1) * words + 1) & ~1) + 8 * entries;
-  cudaError_t e = allow_shared<&k_sparse_mma<D, G>>(1024 + Sm<D>::SEEN + 4 * (T + 1) * 128 + 8 * 4098);
+  const int smem = 1024 + Sm<D>::SEEN + 4 * 256 + 4 * (((T + 1) * words + 1) & ~1) + 8 * entries;
+  cudaError_t e = allow_shared<&k_sparse_mma<D, G>>(1024 + Sm<D>::SEEN + 4 * 256 + 4 * (T + 1) * 128 + 8 * 4098);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((a.s.max_rows / T + a.s.n) * a.Hkv * a.splits));
+  cfg.gridDim = dim3((unsigned)(sparse_pieces(a.s, T) * a.Hkv * a.splits));
   cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;

@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   __shared__ __align__(8) uint64_t bars[2 * NST + 7];
   __shared__ int abort_s, count_s, bad_s;
   __shared__ uint32_t tmem_s;
+  __shared__ float2 ml_s[128];  // a row's maximum and sum
   volatile int* abort = &abort_s;
   const uint32_t bar0 = static_cast<uint32_t>(__cvta_generic_to_shared(bars));
   auto full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
@@ -79,10 +80,10 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   auto p_ready = [&](int s) { return bar0 + 8u * (uint32_t)(2 * NST + 2 + (s & 1)); };
   const uint32_t o_done = bar0 + 8u * (uint32_t)(2 * NST + 4), mma_done = o_done + 8u, q_full = o_done + 16u;  // o_done: once a stage
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
-  const int h = blockIdx.x % a.Hkv;
+  const int C = a.splits, rank = blockIdx.x % C, item = blockIdx.x / C, h = item % a.Hkv;
 
-  const StepPiece p = find_piece(a.s, blockIdx.x / a.Hkv, T, 1);
-  if (p.r < 0 || p.at * T >= p.rows) return;
+  const StepPiece p = find_piece(a.s, item / a.Hkv, T, 1);
+  if (p.r < 0 || p.at * T >= p.rows) return;  // (the whole cluster)
   const int t0 = p.at * T, m_rows = min(T, p.rows - t0);
   BlockLists<NT / 32, T> lists;
   lists.load(a, (size_t)p.row0 + t0, h, lists.rows_of(m_rows), 0);
@@ -153,9 +154,14 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   }
   __syncthreads();
   const int lx = min(lb, 6), box = 1 << lx, boxes = KEYS >> lx, lof = lb - lx;  // a box, of a stage, log2 of those of a block
-  const int all = uniform(count_s) << lof;                                     // boxes
+  // this CTA's share of the list, in boxes
+  const int from = (int)((int64_t)count_s * rank / C);
+  int all = uniform((int)((int64_t)count_s * (rank + 1) / C) - from) << lof;
+  list += from;
   // first logical slot of box e
   auto slot_of = [&](int e) { return ((int)list[e >> lof] << lb) + ((e & ((1 << lof) - 1)) << lx); };
+  while (all > 0 && slot_of(all - 1) > last.at) --all;  // boxes of the last block past the rows
+  all = uniform(all);
   const int stages = (all + boxes - 1) >> (6 - lx);
   bool ok = true;
   auto timed_out = [&] {
@@ -357,7 +363,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
     if (ok) ok = __all_sync(0xffffffffu, wait_phase(mma_done, 0u, abort));  // (o_done may be two stages behind)
     if (ok) {
       tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = C > 1 ? 1.f : l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         uint32_t o[32];
@@ -369,7 +375,13 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
 #pragma unroll
           for (int c = 0; c < 32; ++c) o[c] = 0u;
         }
-        if (valid) {
+        if (C > 1) {
+          float4* dst = reinterpret_cast<float4*>(sm + ((size_t)tid * (D + 4) + d) * 4);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                                 __uint_as_float(o[4 * e + 3]));
+        } else if (valid) {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at + d);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -382,6 +394,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
         }
         __syncwarp();
       }
+      ml_s[tid] = make_float2(m, l);
     } else if (lane == 0) {
       timed_out();
     }
@@ -389,6 +402,44 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   }
   tc_fence_before();
   __syncthreads();
+  if (C > 1) {
+    // ---- the shares joined: a warp a row, each CTA its rows ----
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    auto there = [&](const void* x, int r) {  // *x of CTA r of the cluster
+      uint32_t y;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(x))), "r"(r));
+      return y;
+    };
+    for (int x = rank + C * warp; x < m_rows * G; x += C * (NT / 32)) {
+      float top = NEG, sum = 0.f, y[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) y[i] = 0.f;
+      for (int r = 0; r < C; ++r) {
+        float mr, lr;
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(mr), "=f"(lr) : "r"(there(&ml_s[x], r)) : "memory");
+        const float mn = fmaxf(top, mr), f = ex2f(top - mn), g = ex2f(mr - mn);
+        top = mn;
+        sum = sum * f + lr * g;
+        const uint32_t at0 = there(sm + ((size_t)x * (D + 4) + lane * (D / 32)) * 4, r);
+        float v[D / 32];
+        if constexpr (D == 128) {
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(at0) : "memory");
+        } else {
+          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(at0) : "memory");
+        }
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) y[i] = y[i] * f + v[i] * g;
+      }
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + ((row0 + x / G) * a.Hq + h * G + x % G) * D) +
+                      lane * (D / 64);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) dst[i] = pack_bf16(y[2 * i] * inv, y[2 * i + 1] * inv);
+    }
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // no CTA leaves while another reads it
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  }
   if (warp == 5) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
@@ -402,8 +453,18 @@ cudaError_t launch_t(const SparseArgs& a, const SparseMaps& maps, const CUtensor
   const int smem = 1024 + Sm<D>::RING + 4 * 256 + 4 * (T + 1) * words + 2 * most;
   cudaError_t e = allow_shared<&k_sparse_tc<D, G>>(1024 + Sm<D>::RING + 4 * 256 + 4 * (T + 1) * 128 + 2 * 4096);
   if (e != cudaSuccess) return e;
-  k_sparse_tc<D, G><<<dim3((unsigned)((a.s.max_rows / T + a.s.n) * a.Hkv)), NT, smem, s>>>(a, maps, qmap, words);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(sparse_pieces(a.s, T) * a.Hkv * a.splits));
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)a.splits;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_sparse_tc<D, G>, a, maps, qmap, words);
 }
 
 }  // namespace

@@ -374,18 +374,31 @@ gp_status gp_sparse_attention(gp_ctx* c, int32_t layer, const gp_step* s, int32_
   const bool tc = c->attn_tc_ok && c->scan_kernel != GP_SCAN_CUDA_CORE && g.q_dtype == GP_DTYPE_BF16;
   if (c->scan_kernel == GP_SCAN_TENSOR_CORE && !tc)
     return fail(c, GP_ERR_UNSUPPORTED, "the tensor-core kernels cannot take this cache or query type");
-  // two CTAs an SM while a share keeps 64 tokens or more
-  const int64_t units = (int64_t)s->max_rows * g.num_kv_heads, tokens = (int64_t)std::min(top, g.max_pages_per_req * (kPage / block)) * block;
-  a.splits = 1;
-  while (a.splits < 8 && units * a.splits < 2 * c->sms && tokens >= 128 * a.splits) a.splits *= 2;
-  if (!tc)
+  // Clusters share the blocks of a piece while all of their CTAs find a place at once
+  // (two an SM) and a share keeps 64 tokens.  One long request, 64 blocks of 64: 46, 28, 19 and
+  // 14.7 us at 1, 2, 4 and 8; 16 requests 31, 29, 37 and 52; 64 requests 90, 104, 120 and 175.
+  const int64_t tokens = (int64_t)std::min(top, g.max_pages_per_req * (kPage / block)) * block;
+  auto share = [&](int64_t pieces) {
+    pieces = std::min<int64_t>(pieces, s->max_rows);
+    a.splits = 1;
+    while (a.splits < 8 && (a.splits + 1) * pieces * g.num_kv_heads <= 2 * c->sms && tokens >= 64 * (a.splits + 1)) ++a.splits;
+  };
+  if (!tc) {
+    share(s->max_rows);
     return launch_step(c, capturing, GP_KERNEL_SPARSE, "sparse_attention", [&] { return launch_sparse(a, c->stream); });
+  }
   SparseMaps maps;
   if (!block_maps(c, block, &maps)) return fail(c, GP_ERR_CUDA, "no tensor map of the caches");
-  const bool many = s->max_rows >= 16 * s->n;
+  // A row or two of each request at a time, or pieces of 128 / G rows: those from
+  // where a request has more rows than the small pieces take in one (4 rows of one, 8
+  // and 64 requests with G = 4: 15.2 us on either, 31 and 47, 125 on either; 8 rows: 31 instead
+  // of 47 and 137 instead of 177; 4001 rows: 320 instead of 1094).
+  const int G = g.num_q_heads / g.num_kv_heads;
+  const bool many = s->max_rows > (int64_t)s->n * kSparseMmaRows / G;
+  share(sparse_pieces(a.s, (many ? kSparseTcRows : kSparseMmaRows) / G));
   CUtensorMap qmap;
   if (many) {
-    const cuuint64_t G = (cuuint64_t)(g.num_q_heads / g.num_kv_heads), row = (cuuint64_t)g.head_dim * 2;
+    const cuuint64_t row = (cuuint64_t)g.head_dim * 2;
     const cuuint64_t dims[3] = {(cuuint64_t)g.head_dim, (cuuint64_t)g.num_q_heads, (cuuint64_t)s->max_rows};
     const cuuint64_t strides[2] = {row, row * g.num_q_heads};
     const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(kSparseTcRows / G)};

@@ -87,13 +87,16 @@ struct SparseArgs {
   const void* q;             // [max_rows][Hq][D]
   const int32_t* blocks;     // [max_rows][Hkv][top]
   void* out;                 // [max_rows][Hq][D], q's type
-  int splits;                // CTAs of a cluster that share a row's blocks
+  int splits;                // CTAs of a cluster that share the blocks of a row or piece
 };
 
 cudaError_t launch_tables(const TablesArgs& a, cudaStream_t s);
 cudaError_t launch_mapped(const MappedArgs& a, cudaStream_t s);
 cudaError_t launch_bounds(const BoundsArgs& a, cudaStream_t s);
 cudaError_t launch_select_blocks(const SelectBlocksArgs& a, cudaStream_t s);
+// Pieces of T rows that a launch has room for (step.cuh).
+inline int sparse_pieces(const StepArgs& s, int T) { return s.max_rows / T + s.n; }
+
 // K and V as 2-D tensors of key rows, boxes of 64 dimensions by a block (64 rows of
 // one that is larger).
 struct SparseMaps {
@@ -103,6 +106,7 @@ cudaError_t launch_sparse(const SparseArgs& a, cudaStream_t s);
 // bf16 caches and queries: a few rows of a request at a time, and many
 cudaError_t launch_sparse_mma(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s);
 cudaError_t launch_sparse_tc(const SparseArgs& a, const SparseMaps& maps, const CUtensorMap& qmap, cudaStream_t s);
+constexpr int kSparseMmaRows = 16;  // of the products: 16 / G rows of a request
 constexpr int kSparseTcRows = 128;  // qmap's box: 64 dimensions of G heads of 128 / G rows
 
 }  // namespace gp
