@@ -31,8 +31,8 @@
 namespace gp {
 namespace {
 
-constexpr int NT = 128;
-constexpr int ROWS = 8;  // of a tile: the product's N
+constexpr int NT = 256;
+constexpr int NW = NT / 32;
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -52,112 +52,220 @@ __device__ __forceinline__ unsigned ordered(float f) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// A warp picks `want` of the keys [from, to) of `key` (larger first, equal ones
-// the lower index first) and writes the list: the blocks [0, from), those picked,
-// [to, end), then -1.  Needs 0 <= want < to - from.
-__device__ __forceinline__ void pick(const unsigned* key, int from, int to, int end, int want, int32_t* out, int top) {
+// How many of a warp's keys reach t.
+template <int N>
+__device__ __forceinline__ int reaching(const unsigned (&key)[N], unsigned t) {
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) count += key[i] >= t;
+  return __reduce_add_sync(0xffffffffu, count);
+}
+
+// The threshold that picks `want` >= 1 of a warp's keys, of more: the largest that at
+// least so many reach; `ties`: how many of those that equal it are picked (all
+// that reach it: -1).  Bit by bit from the highest in which the keys differ; two keys
+// that are a part in 250 of their range apart need some ten bits.
+template <typename Count>
+__device__ __forceinline__ unsigned threshold(unsigned low, unsigned high, int want, int& ties, Count&& count) {
+  ties = -1;
+  if (low == high) {
+    ties = want;
+    return low;
+  }
+  const int top = 31 - __clz(low ^ high);
+  unsigned t = high >> top >> 1 << top << 1;  // the bits that all keys share
+  for (int bit = top; bit >= 0; --bit) {
+    const int n = count(t | 1u << bit);
+    if (n >= want) t |= 1u << bit;
+    if (n == want) return t;
+  }
+  ties = want - (t == 0xffffffffu ? 0 : count(t + 1));
+  return t;
+}
+
+// A warp picks `want` of the keys [from, to) (larger first, equal ones the lower index
+// first) and writes the list: the blocks [0, from), those picked, [to, end), then -1.
+// Needs 0 <= want < to - from <= 32 N.
+template <int N>
+__device__ __forceinline__ void pick(const unsigned* keys, int from, int to, int end, int want, int32_t* out, int top) {
   const int lane = threadIdx.x & 31;
-  // the largest threshold that at least `want` keys reach
-  unsigned at_least = 0;
-  if (want > 0)
-    for (int bit = 31; bit >= 0; --bit) {
-      const unsigned t = at_least | (1u << bit);
-      int count = 0;
-      for (int b = from + lane; b < to; b += 32) count += key[b] >= t;
-      count = __reduce_add_sync(0xffffffffu, count);
-      if (count >= want) at_least = t;
-      if (count == want) break;  // exactly these
+  unsigned key[N], low = 0xffffffffu, high = 0u;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int b = from + 32 * i + lane;
+    key[i] = b < to ? keys[b] : 0u;  // (no score is 0: the bits of a NaN)
+    if (b < to) {
+      low = min(low, key[i]);
+      high = max(high, key[i]);
     }
-  int above = 0;
-  for (int b = from + lane; b < to; b += 32) above += key[b] > at_least;
-  above = __reduce_add_sync(0xffffffffu, above);
-  int ties = want - above;  // of the keys that equal it; the first ones
+  }
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  int ties = 0;
+  unsigned t = 0xffffffffu;
+  if (want > 0) t = threshold(low, high, want, ties, [&](unsigned x) { return reaching(key, x); });
   for (int b = lane; b < from; b += 32) out[b] = b;
   int n = from;
-  for (int b0 = from; b0 < to; b0 += 32) {
-    const int b = b0 + lane;
-    const bool more = want > 0 && b < to && key[b] > at_least, same = want > 0 && b < to && key[b] == at_least;
-    const unsigned equal = __ballot_sync(0xffffffffu, same);
-    const bool taken = more || (same && __popc(equal & ((1u << lane) - 1)) < ties);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    bool taken = key[i] > t || (ties < 0 && key[i] == t);
+    if (ties > 0) {
+      const unsigned equal = __ballot_sync(0xffffffffu, key[i] == t);
+      taken = taken || (key[i] == t && __popc(equal & ((1u << lane) - 1)) < ties);
+      ties -= min(ties, __popc(equal));
+    }
     const unsigned kept = __ballot_sync(0xffffffffu, taken);
-    if (taken) out[n + __popc(kept & ((1u << lane) - 1))] = b;
+    if (taken) out[n + __popc(kept & ((1u << lane) - 1))] = from + 32 * i + lane;
     n += __popc(kept);
-    ties -= min(ties, __popc(equal));
   }
   for (int b = to + lane; b < end; b += 32) out[n + b - to] = b;
   n += end - to;
   for (int k = n + lane; k < top; k += 32) out[k] = -1;
 }
 
-template <int D, int G, bool F32>
+// The same for more keys than registers hold.
+__device__ __forceinline__ void pick_many(const unsigned* key, int from, int to, int end, int want, int32_t* out, int top) {
+  const int lane = threadIdx.x & 31;
+  unsigned low = 0xffffffffu, high = 0u;
+  for (int b = from + lane; b < to; b += 32) {
+    low = min(low, key[b]);
+    high = max(high, key[b]);
+  }
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  int ties = 0;
+  unsigned t = 0xffffffffu;
+  if (want > 0)
+    t = threshold(low, high, want, ties, [&](unsigned x) {
+      int count = 0;
+      for (int b = from + lane; b < to; b += 32) count += key[b] >= x;
+      return __reduce_add_sync(0xffffffffu, count);
+    });
+  for (int b = lane; b < from; b += 32) out[b] = b;
+  int n = from;
+  for (int b0 = from; b0 < to; b0 += 32) {
+    const int b = b0 + lane;
+    const unsigned k = b < to ? key[b] : 0u;
+    bool taken = k > t || (ties < 0 && k == t);
+    if (ties > 0) {
+      const unsigned equal = __ballot_sync(0xffffffffu, k == t);
+      taken = taken || (k == t && __popc(equal & ((1u << lane) - 1)) < ties);
+      ties -= min(ties, __popc(equal));
+    }
+    const unsigned kept = __ballot_sync(0xffffffffu, taken);
+    if (taken) out[n + __popc(kept & ((1u << lane) - 1))] = b;
+    n += __popc(kept);
+  }
+  for (int b = to + lane; b < end; b += 32) out[n + b - to] = b;
+  n += end - to;
+  for (int k = n + lane; k < top; k += 32) out[k] = -1;
+}
+
+// ROWS: of a tile, 8 or 16.
+template <int D, int G, bool F32, int ROWS>
 __global__ void __launch_bounds__(NT) k_block_select(const __grid_constant__ SelectBlocksArgs a, int pitch) {
+  constexpr int NN = ROWS / 8;  // products of 8 rows
   extern __shared__ __align__(16) unsigned scores[];  // [ROWS][pitch], ordered bits
   __shared__ __align__(16) __half reach[ROWS][2 * D + 8];  // N, P of the tile's rows
+  __shared__ int pages[256];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.y;
-  const StepPiece p = find_piece(a.s, blockIdx.x, ROWS, 1);
-  if (p.r < 0 || p.at * ROWS >= p.rows) return;
+  const int C = a.splits, rank = blockIdx.x % C, item = blockIdx.x / C, h = item % a.Hkv;
+  const StepPiece p = find_piece(a.s, item / a.Hkv, ROWS, 1);
+  if (p.r < 0 || p.at * ROWS >= p.rows) return;  // (the whole cluster)
   const int t0 = p.at * ROWS, m = min(ROWS, p.rows - t0);  // rows of the tile
-  const StepRow first = step_row(a.s, p.r, t0, tid == 0), last = step_row(a.s, p.r, t0 + m - 1, tid == 0);
-  if (!first.live || !last.live) return;
   const size_t row0 = (size_t)p.row0 + t0;
 
-  // P and N: a warp a row
-  for (int x = warp; x < ROWS; x += NT / 32) {
-    constexpr int E = D / 32;  // dimensions of a lane
-    float q[G][E];
+  // the rows' queries, a warp a row: loaded while their places are looked up
+  constexpr int E = D / 32;  // dimensions of a lane
+  float q[NN][G][E];
+#pragma unroll
+  for (int i = 0; i < NN; ++i) {
+    const int x = warp + NW * i;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const size_t at = ((row0 + x) * a.Hq + h * G + g) * D + E * lane;
+#pragma unroll
+      for (int e = 0; e < E; ++e) q[i][g][e] = 0.f;
+      if (x < m) {
+        if constexpr (F32) {
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const float2 v = *reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at + e);
+            q[i][g][e] = v.x;
+            q[i][g][e + 1] = v.y;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const unsigned v = *reinterpret_cast<const unsigned*>(static_cast<const __nv_bfloat16*>(a.q) + at + e);
+            q[i][g][e] = __uint_as_float(v << 16);
+            q[i][g][e + 1] = __uint_as_float(v & 0xffff0000u);
+          }
+        }
+      }
+    }
+  }
+  const StepRow first = step_row(a.s, p.r, t0, tid == 0), last = step_row(a.s, p.r, t0 + m - 1, tid == 0);
+  if (!first.live || !last.live) return;
+  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int lb = log2_of(a.block), lper = kStepPageLog - lb;  // blocks of a page
+  const int some = max(0, (last.at >> lb) + 1 - a.recent);    // blocks that a row may have to choose from
+  for (int i = tid; i << lper < some; i += NT) pages[i] = max(step_page(a.s, first.slot, i), 0);
+
+#pragma unroll
+  for (int i = 0; i < NN; ++i) {
     float top = 0.f;
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        q[g][i] = 0.f;
-        if (x < m) {
-          const size_t at = ((row0 + x) * a.Hq + h * G + g) * D + lane + 32 * i;
-          q[g][i] = F32 ? static_cast<const float*>(a.q)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at]);
-          if (q[g][i] != q[g][i]) q[g][i] = 0.f;  // NaN asks for nothing
-        }
-        top = fmaxf(top, fabsf(q[g][i]));
+      for (int e = 0; e < E; ++e) {
+        if (q[i][g][e] != q[i][g][e]) q[i][g][e] = 0.f;  // NaN asks for nothing
+        top = fmaxf(top, fabsf(q[i][g][e]));
       }
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     const float down = power_of_two(-scale_exponent(top));
+    float neg[E], pos[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      float neg = 0.f, pos = 0.f;
+    for (int e = 0; e < E; ++e) {
+      neg[e] = pos[e] = 0.f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float v = fminf(fmaxf(rintf(q[g][i] * down), -127.f), 127.f);
-        neg += fminf(v, 0.f);
-        pos += fmaxf(v, 0.f);
+        const float v = fminf(fmaxf(rintf(q[i][g][e] * down), -127.f), 127.f);
+        neg[e] += fminf(v, 0.f);
+        pos[e] += fmaxf(v, 0.f);
       }
-      reach[x][lane + 32 * i] = __float2half_rn(neg);
-      reach[x][D + lane + 32 * i] = __float2half_rn(pos);
+    }
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      *reinterpret_cast<__half2*>(&reach[warp + NW * i][E * lane + e]) = __floats2half2_rn(neg[e], neg[e + 1]);
+      *reinterpret_cast<__half2*>(&reach[warp + NW * i][D + E * lane + e]) = __floats2half2_rn(pos[e], pos[e + 1]);
     }
   }
   __syncthreads();
 
-  const int lb = log2_of(a.block), lper = kStepPageLog - lb;  // blocks of a page
-  const int some = max(0, (last.at >> lb) + 1 - a.recent);  // blocks that a row may have to choose from
   constexpr int CHUNKS = 2 * D / 64;
-  uint32_t bq[CHUNKS][4][2];
+  uint2 bq[NN][CHUNKS][4];
 #pragma unroll
-  for (int c = 0; c < CHUNKS; ++c)
+  for (int i = 0; i < NN; ++i)
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const uint2 v = *reinterpret_cast<const uint2*>(&reach[lane >> 2][64 * c + 16 * (lane & 3) + 4 * s]);
-      bq[c][s][0] = v.x;
-      bq[c][s][1] = v.y;
-    }
-  for (int b0 = 16 * warp; b0 < some; b0 += 16 * (NT / 32)) {
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        bq[i][c][s] = *reinterpret_cast<const uint2*>(&reach[8 * i + (lane >> 2)][64 * c + 16 * (lane & 3) + 4 * s]);
+  uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(scores));  // of the cluster's first CTA
+  if (C > 1) {
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(to));
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // it has started
+  }
+  for (int b0 = 16 * (warp + NW * rank); b0 < some; b0 += 16 * NW * C) {
+    float sum[NN][4];
     float scale[2];
     const uint4* src[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {  // this lane's two blocks
       const int b = min(b0 + (lane >> 2) + 8 * k, some - 1);
-      const int page = max(step_page(a.s, first.slot, b >> lper), 0);
-      const size_t at = (((((size_t)a.layer * a.s.num_pages_total + page) * a.Hkv) + h) << lper) + (b & ((1 << lper) - 1));
+      const size_t at = (((((size_t)a.layer * a.s.num_pages_total + pages[b >> lper]) * a.Hkv) + h) << lper) + (b & ((1 << lper) - 1));
       src[k] = reinterpret_cast<const uint4*>(a.bounds + at * 2 * D) + (lane & 3);
       scale[k] = a.scales[at];
     }
@@ -168,53 +276,83 @@ __global__ void __launch_bounds__(NT) k_block_select(const __grid_constant__ Sel
       w[c][1] = src[1][4 * c];
     }
 #pragma unroll
+    for (int i = 0; i < NN; ++i) sum[i][0] = sum[i][1] = sum[i][2] = sum[i][3] = 0.f;
+#pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
       const unsigned x[4] = {w[c][0].x, w[c][0].y, w[c][0].z, w[c][0].w}, y[4] = {w[c][1].x, w[c][1].y, w[c][1].z, w[c][1].w};
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const uint32_t u = x[s] ^ 0x80808080u, v = y[s] ^ 0x80808080u;
         const uint32_t f[4] = {two_halves(u, 0x4140), two_halves(v, 0x4140), two_halves(u, 0x4342), two_halves(v, 0x4342)};
-        mma_16816(sum, f, bq[c][s][0], bq[c][s][1]);
-      }
-    }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int b = b0 + (lane >> 2) + 8 * k, x = 2 * (lane & 3);
-      if (b < some) {
-        if (x < m) scores[(size_t)x * pitch + b] = ordered(sum[2 * k] * scale[k]);
-        if (x + 1 < m) scores[(size_t)(x + 1) * pitch + b] = ordered(sum[2 * k + 1] * scale[k]);
+        for (int i = 0; i < NN; ++i) mma_16816(sum[i], f, bq[i][c][s].x, bq[i][c][s].y);
       }
     }
+    auto put = [&](int x, int b, float v) {
+      const uint32_t at = to + 4u * (uint32_t)(x * pitch + b);
+      if (C > 1) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(ordered(v)) : "memory");
+      else asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(ordered(v)) : "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < NN; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int b = b0 + (lane >> 2) + 8 * k, x = 8 * i + 2 * (lane & 3);
+        if (b < some) {
+          if (x < m) put(x, b, sum[i][2 * k] * scale[k]);
+          if (x + 1 < m) put(x + 1, b, sum[i][2 * k + 1] * scale[k]);
+        }
+      }
   }
-  __syncthreads();
-  for (int x = warp; x < m; x += NT / 32) {
+  if (C > 1) {
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (rank > 0) return;
+  } else {
+    __syncthreads();
+  }
+  for (int x = warp; x < m; x += NW) {
     const int end = ((first.at + x) >> lb) + 1;  // blocks that the row sees
     int32_t* out = a.blocks + ((row0 + x) * a.Hkv + h) * a.top;
+    const unsigned* keys = scores + (size_t)x * pitch;
+    const int to_b = end - a.recent, n = to_b - a.sink, want = a.top - a.sink - a.recent;
     if (end <= a.top) {
       for (int k = lane; k < a.top; k += 32) out[k] = k < end ? k : -1;
+    } else if (n <= 128) {
+      pick<4>(keys, a.sink, to_b, end, want, out, a.top);
+    } else if (n <= 256) {
+      pick<8>(keys, a.sink, to_b, end, want, out, a.top);
+    } else if (n <= 512) {
+      pick<16>(keys, a.sink, to_b, end, want, out, a.top);
     } else {
-      pick(scores + (size_t)x * pitch, a.sink, end - a.recent, end, a.top - a.sink - a.recent, out, a.top);
+      pick_many(keys, a.sink, to_b, end, want, out, a.top);
     }
   }
 }
 
-template <int D, int G, bool F32>
+template <int D, int G, bool F32, int ROWS>
 cudaError_t launch_t(const SelectBlocksArgs& a, cudaStream_t s) {
   const int pitch = a.s.maxp * (kStepPage / a.block);
-  const int smem = ROWS * pitch * 4;
-  cudaError_t e = allow_shared<&k_block_select<D, G, F32>>(ROWS * 4096 * 4);
+  cudaError_t e = allow_shared<&k_block_select<D, G, F32, ROWS>>(ROWS == 8 ? 8 * 4096 * 4 : kSelectShared);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(a.s.max_rows / ROWS + a.s.n), (unsigned)a.Hkv);
-  k_block_select<D, G, F32><<<grid, NT, smem, s>>>(a, pitch);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(sparse_pieces(a.s, ROWS) * a.Hkv * a.splits));
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = (size_t)ROWS * pitch * 4;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)a.splits;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_block_select<D, G, F32, ROWS>, a, pitch);
 }
 template <int D, bool F32>
 cudaError_t launch_g(const SelectBlocksArgs& a, cudaStream_t s) {
-  switch (a.Hq / a.Hkv) {
-    case 2: return launch_t<D, 2, F32>(a, s);
-    case 4: return launch_t<D, 4, F32>(a, s);
-  }
-  return cudaErrorInvalidValue;
+  const bool four = a.Hq / a.Hkv == 4;
+  if (a.rows == 16) return four ? launch_t<D, 4, F32, 16>(a, s) : launch_t<D, 2, F32, 16>(a, s);
+  return four ? launch_t<D, 4, F32, 8>(a, s) : launch_t<D, 2, F32, 8>(a, s);
 }
 
 }  // namespace

@@ -335,6 +335,11 @@ gp_status gp_select_blocks(gp_ctx* c, int32_t layer, const gp_step* s, int32_t b
   a.bounds = bounds_dev;
   a.scales = scales_dev;
   a.blocks = blocks_dev;
+  const int blocks = g.max_pages_per_req * (kPage / block);
+  a.rows = s->max_rows > 8 * (int64_t)s->n && 16 * 4 * blocks <= kSelectShared ? 16 : 8;
+  const int64_t tiles = std::min<int64_t>(sparse_pieces(a.s, a.rows), s->max_rows) * g.num_kv_heads;
+  a.splits = 1;
+  while (a.splits < 8 && (a.splits + 1) * tiles <= 2 * c->sms && blocks >= 128 * (a.splits + 1)) ++a.splits;
   return launch_step(c, capturing, GP_KERNEL_BLOCK_SELECT, "select_blocks", [&] { return launch_select_blocks(a, c->stream); });
 } catch (const std::exception&) {
   return no_memory(c);

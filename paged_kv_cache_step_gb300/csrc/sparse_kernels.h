@@ -76,7 +76,10 @@ struct SelectBlocksArgs {
   const int8_t* bounds;
   const float* scales;
   int32_t* blocks;           // [max_rows][Hkv][top]
+  int rows;                  // of a tile: 8, or 16 while their scores fit kSelectShared
+  int splits;                // CTAs of a cluster that share a tile's blocks
 };
+constexpr int kSelectShared = 64 * 1024;
 
 // ---- attention over listed blocks ---------------------------------------------------
 struct SparseArgs {
