@@ -31,9 +31,6 @@
 namespace gp {
 namespace {
 
-constexpr int NT = 256;
-constexpr int NW = NT / 32;
-
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -161,12 +158,17 @@ __device__ __forceinline__ void pick_many(const unsigned* key, int from, int to,
   for (int k = n + lane; k < top; k += 32) out[k] = -1;
 }
 
-// ROWS: of a tile, 8 or 16.
+// ROWS: of a tile, 8 or 16.  Tiles of 8 rows (decode steps) wait on memory: half as
+// many warps, each with the bounds of 32 blocks in flight, so that a step's tiles
+// are on the GPU together.
 template <int D, int G, bool F32, int ROWS>
-__global__ void __launch_bounds__(NT) k_block_select(const __grid_constant__ SelectBlocksArgs a, int pitch) {
+__global__ void __launch_bounds__(16 * ROWS, ROWS == 8 ? 4 : 3) k_block_select(const __grid_constant__ SelectBlocksArgs a, int pitch) {
+  constexpr int NT = 16 * ROWS, NW = NT / 32;
+  constexpr int AHEAD = ROWS == 8 ? 2 : 1;  // products of 16 blocks whose bounds are loaded together
+  constexpr int QR = ROWS / NW;             // rows of Q a warp
   constexpr int NN = ROWS / 8;  // products of 8 rows
   extern __shared__ __align__(16) unsigned scores[];  // [ROWS][pitch], ordered bits
-  __shared__ __align__(16) __half reach[ROWS][2 * D + 8];  // N, P of the tile's rows
+  __shared__ __align__(16) __half reach[ROWS][2 * D + 4];  // N, P of the tile's rows (520 bytes apart: no bank twice)
   __shared__ int pages[256];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = a.splits, rank = blockIdx.x % C, item = blockIdx.x / C, h = item % a.Hkv;
@@ -177,9 +179,9 @@ __global__ void __launch_bounds__(NT) k_block_select(const __grid_constant__ Sel
 
   // the rows' queries, a warp a row: loaded while their places are looked up
   constexpr int E = D / 32;  // dimensions of a lane
-  float q[NN][G][E];
+  float q[QR][G][E];
 #pragma unroll
-  for (int i = 0; i < NN; ++i) {
+  for (int i = 0; i < QR; ++i) {
     const int x = warp + NW * i;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -213,15 +215,22 @@ __global__ void __launch_bounds__(NT) k_block_select(const __grid_constant__ Sel
   for (int i = tid; i << lper < some; i += NT) pages[i] = max(step_page(a.s, first.slot, i), 0);
 
 #pragma unroll
-  for (int i = 0; i < NN; ++i) {
-    float top = 0.f;
+  for (int i = 0; i < QR; ++i) {
+    float top = 0.f, odd = 0.f;
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        if (q[i][g][e] != q[i][g][e]) q[i][g][e] = 0.f;  // NaN asks for nothing
         top = fmaxf(top, fabsf(q[i][g][e]));
+        odd = fmaf(q[i][g][e], 0.f, odd);
       }
+    if (odd != 0.f) {  // NaN asks for nothing
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (q[i][g][e] != q[i][g][e]) q[i][g][e] = 0.f;
+    }
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     const float down = power_of_two(-scale_exponent(top));
@@ -231,10 +240,12 @@ __global__ void __launch_bounds__(NT) k_block_select(const __grid_constant__ Sel
       neg[e] = pos[e] = 0.f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float v = fminf(fmaxf(rintf(q[i][g][e] * down), -127.f), 127.f);
-        neg[e] += fminf(v, 0.f);
+        // to the nearest whole number, ties to even: 1.5 * 2^23 has no room for more
+        const float v = fminf(fmaxf(q[i][g][e] * down, -127.f), 127.f) + 12582912.f - 12582912.f;
+        neg[e] += v;
         pos[e] += fmaxf(v, 0.f);
       }
+      neg[e] -= pos[e];
     }
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
@@ -245,64 +256,63 @@ __global__ void __launch_bounds__(NT) k_block_select(const __grid_constant__ Sel
   __syncthreads();
 
   constexpr int CHUNKS = 2 * D / 64;
-  uint2 bq[NN][CHUNKS][4];
-#pragma unroll
-  for (int i = 0; i < NN; ++i)
-#pragma unroll
-    for (int c = 0; c < CHUNKS; ++c)
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        bq[i][c][s] = *reinterpret_cast<const uint2*>(&reach[8 * i + (lane >> 2)][64 * c + 16 * (lane & 3) + 4 * s]);
+  const __half* mine = &reach[lane >> 2][16 * (lane & 3)];
   uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(scores));  // of the cluster's first CTA
   if (C > 1) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(to));
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // it has started
   }
-  for (int b0 = 16 * (warp + NW * rank); b0 < some; b0 += 16 * NW * C) {
-    float sum[NN][4];
-    float scale[2];
-    const uint4* src[2];
+  auto put = [&](int x, int b, float v) {
+    const uint32_t at = to + 4u * (uint32_t)(x * pitch + b);
+    if (C > 1) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(ordered(v)) : "memory");
+    else asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(ordered(v)) : "memory");
+  };
+  const int stride = 16 * NW * C;
+  for (int b0 = 16 * (warp + NW * rank); b0 < some; b0 += AHEAD * stride) {
+    float scale[AHEAD][2];
+    uint4 w[AHEAD][CHUNKS][2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {  // this lane's two blocks
-      const int b = min(b0 + (lane >> 2) + 8 * k, some - 1);
-      const size_t at = (((((size_t)a.layer * a.s.num_pages_total + pages[b >> lper]) * a.Hkv) + h) << lper) + (b & ((1 << lper) - 1));
-      src[k] = reinterpret_cast<const uint4*>(a.bounds + at * 2 * D) + (lane & 3);
-      scale[k] = a.scales[at];
-    }
-    uint4 w[CHUNKS][2];
+    for (int t = 0; t < AHEAD; ++t)
 #pragma unroll
-    for (int c = 0; c < CHUNKS; ++c) {
-      w[c][0] = src[0][4 * c];
-      w[c][1] = src[1][4 * c];
-    }
+      for (int k = 0; k < 2; ++k) {  // this lane's two blocks
+        const int b = min(b0 + t * stride + (lane >> 2) + 8 * k, some - 1);
+        const size_t at = (((((size_t)a.layer * a.s.num_pages_total + pages[b >> lper]) * a.Hkv) + h) << lper) + (b & ((1 << lper) - 1));
+        const uint4* src = reinterpret_cast<const uint4*>(a.bounds + at * 2 * D) + (lane & 3);
 #pragma unroll
-    for (int i = 0; i < NN; ++i) sum[i][0] = sum[i][1] = sum[i][2] = sum[i][3] = 0.f;
-#pragma unroll
-    for (int c = 0; c < CHUNKS; ++c) {
-      const unsigned x[4] = {w[c][0].x, w[c][0].y, w[c][0].z, w[c][0].w}, y[4] = {w[c][1].x, w[c][1].y, w[c][1].z, w[c][1].w};
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const uint32_t u = x[s] ^ 0x80808080u, v = y[s] ^ 0x80808080u;
-        const uint32_t f[4] = {two_halves(u, 0x4140), two_halves(v, 0x4140), two_halves(u, 0x4342), two_halves(v, 0x4342)};
-#pragma unroll
-        for (int i = 0; i < NN; ++i) mma_16816(sum[i], f, bq[i][c][s].x, bq[i][c][s].y);
+        for (int c = 0; c < CHUNKS; ++c) w[t][c][k] = src[4 * c];
+        scale[t][k] = a.scales[at];
       }
-    }
-    auto put = [&](int x, int b, float v) {
-      const uint32_t at = to + 4u * (uint32_t)(x * pitch + b);
-      if (C > 1) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(ordered(v)) : "memory");
-      else asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(ordered(v)) : "memory");
-    };
 #pragma unroll
-    for (int i = 0; i < NN; ++i)
+    for (int t = 0; t < AHEAD; ++t) {
+      float sum[NN][4];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int b = b0 + (lane >> 2) + 8 * k, x = 8 * i + 2 * (lane & 3);
-        if (b < some) {
-          if (x < m) put(x, b, sum[i][2 * k] * scale[k]);
-          if (x + 1 < m) put(x + 1, b, sum[i][2 * k + 1] * scale[k]);
+      for (int i = 0; i < NN; ++i) sum[i][0] = sum[i][1] = sum[i][2] = sum[i][3] = 0.f;
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c) {
+        const uint4 &x4 = w[t][c][0], &y4 = w[t][c][1];
+        const unsigned x[4] = {x4.x, x4.y, x4.z, x4.w}, y[4] = {y4.x, y4.y, y4.z, y4.w};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const uint32_t u = x[s] ^ 0x80808080u, v = y[s] ^ 0x80808080u;
+          const uint32_t f[4] = {two_halves(u, 0x4140), two_halves(v, 0x4140), two_halves(u, 0x4342), two_halves(v, 0x4342)};
+#pragma unroll
+          for (int i = 0; i < NN; ++i) {
+            const uint2 v2 = *reinterpret_cast<const uint2*>(mine + 8 * i * (2 * D + 4) + 64 * c + 4 * s);
+            mma_16816(sum[i], f, v2.x, v2.y);
+          }
         }
       }
+#pragma unroll
+      for (int i = 0; i < NN; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int b = b0 + t * stride + (lane >> 2) + 8 * k, x = 8 * i + 2 * (lane & 3);
+          if (b < some) {
+            if (x < m) put(x, b, sum[i][2 * k] * scale[t][k]);
+            if (x + 1 < m) put(x + 1, b, sum[i][2 * k + 1] * scale[t][k]);
+          }
+        }
+    }
   }
   if (C > 1) {
     asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
@@ -337,7 +347,7 @@ cudaError_t launch_t(const SelectBlocksArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(sparse_pieces(a.s, ROWS) * a.Hkv * a.splits));
-  cfg.blockDim = dim3(NT);
+  cfg.blockDim = dim3(16 * ROWS);
   cfg.dynamicSmemBytes = (size_t)ROWS * pitch * 4;
   cfg.stream = s;
   cudaLaunchAttribute attr{};
