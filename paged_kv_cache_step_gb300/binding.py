@@ -643,6 +643,13 @@ def _strided(held, t, dtype, rows, row):
     tensor [rows, heads, d] or [rows, heads * d], dense within a row."""
     if t is None:
         return 0, 0
+    try:  # heads side by side, in as few looks at the tensor as it takes
+        shape, (apart, head, one) = t.shape, t.stride()
+        if (one == 1 and head == shape[2] and shape[1] * head == row and shape[0] >= rows and t.dtype is dtype
+                and t.get_device() == held.device):
+            return t.data_ptr(), apart if rows > 1 else row
+    except (AttributeError, ValueError):
+        pass
     if not hasattr(t, "stride") or t.dim() < 2 or rows == 0:
         return _dense(held, t, dtype, 0), row
     shape, strides = t.shape, t.stride()
@@ -655,7 +662,7 @@ def _strided(held, t, dtype, rows, row):
         raise GrowPageError(GP_ERR_INVALID, f"a buffer on {t.device}, the caches are on device {held.device}")
     if held is not _Unknown and (t.dtype is not dtype or dense != row or shape[0] < rows):
         raise GrowPageError(GP_ERR_INVALID, f"{shape[0]} rows of {dense} {t.dtype}, where the call takes {rows} of {row} {dtype}")
-    return t.data_ptr(), strides[0] if shape[0] > 1 else row
+    return t.data_ptr(), strides[0] if rows > 1 else row
 
 
 def gp_rope_default(**overrides) -> GpRope:

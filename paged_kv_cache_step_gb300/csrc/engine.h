@@ -116,6 +116,9 @@ struct gp_ctx {
   bool attn_tc_ok = false;         // kmap and vmap are valid
   CUtensorMap block_maps[3][2];    // K and V in boxes of 16, 32 and 64 rows (gp_sparse_attention)
   bool block_maps_ok[3] = {};      // made at the first call that needs them
+  gp_rope rope{};                  // the last rotary form of gp_append_mapped (theta 0: none yet),
+  double rope_inv[64] = {};        // its frequencies and amplitude: 64 powers a call otherwise
+  float rope_amplitude = 1.f;
   int sms = 152;                   // SMs of the device
   int scan_kernel = GP_SCAN_AUTO;
   int select_mode = GP_SELECT_AUTO;

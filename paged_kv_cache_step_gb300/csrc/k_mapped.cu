@@ -12,7 +12,11 @@
 // unit is two pieces of a head that belong together: of rotated halves the
 // pieces p and p + rd / 2, else (interleaved pairs, copied dimensions) two
 // neighbours; so a pair is in one thread and q_rot may be q.  A block a token;
-// its rd / 2 angles serve all heads and are formed while the rows are on their way.
+// its rd / 2 angles serve all heads and are formed while the rows are on their way,
+// which start before the row's place is looked up.  Small blocks keep
+// more loads in flight beside the angles of others: 13 621 rows of 32 + 8 heads, d = 128,
+// interleaved, 56 us with 64 threads, 59 with 192, 73 with 256 and 82 with 384 (a row
+// of 16 + 8 heads, d = 64: 24, 37, - and -); 88 % of the copy rate.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -22,7 +26,7 @@
 namespace gp {
 namespace {
 
-constexpr int NT = 256;
+constexpr int NT = 64;  // and at least half a head
 constexpr int PAGE = 256;
 
 template <bool F32>
@@ -99,20 +103,11 @@ template <int D, bool QF32, bool KF32>
 __global__ void __launch_bounds__(NT) k_mapped(const __grid_constant__ MappedArgs a) {
   constexpr int QE = QF32 ? 4 : 2, KE = KF32 ? 4 : 2, NQ = 16 / QE, NK = 16 / KE;  // bytes of an element, elements of a piece
   constexpr int UQ = D / (2 * NQ), UK = D / (2 * NK);                             // units of a head
-  constexpr int AHEAD = 2;  // units a thread loads before the angles are known
+  constexpr int AHEAD = 3;  // units a thread loads before the angles are known
   __shared__ float cs[D / 2];
   __shared__ float sn[D / 2];
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
-  const int64_t to = a.slot_map[row];
-  if (to == -1) return;
-  if (to < 0 || to >= (int64_t)a.num_pages_total * PAGE) {
-    if (tid == 0) atomicOr(a.err, ERR_BAD_PAGE);
-    return;
-  }
-  const double pos = (double)a.positions[row];
-  const size_t head0 = ((size_t)a.layer * a.num_pages_total + (size_t)(to / PAGE)) * a.Hkv;
-  const size_t in_page = (size_t)(to % PAGE) * D * KE;
   const int nq = a.q ? a.Hq * UQ : 0, nk = nq + a.Hkv * UK, nv = nk + a.Hkv * UK;
   auto load = [&](int u, uint4& u0, uint4& u1) {
     if (u >= nv) return;
@@ -131,6 +126,19 @@ __global__ void __launch_bounds__(NT) k_mapped(const __grid_constant__ MappedArg
     u0 = src[w.p0];
     u1 = src[w.p1];
   };
+  // the rows are on their way before their place is known
+  uint4 u0[AHEAD], u1[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) load(tid + i * NT, u0[i], u1[i]);
+  const int64_t to = a.slot_map[row];
+  const double pos = (double)a.positions[row];
+  if (to == -1) return;
+  if (to < 0 || to >= (int64_t)a.num_pages_total * PAGE) {
+    if (tid == 0) atomicOr(a.err, ERR_BAD_PAGE);
+    return;
+  }
+  const size_t head0 = ((size_t)a.layer * a.num_pages_total + (size_t)(to / PAGE)) * a.Hkv;
+  const size_t in_page = (size_t)(to % PAGE) * D * KE;
   auto store = [&](int u, uint4 u0, uint4 u1) {
     if (u >= nv) return;
     uint4* dst;
@@ -150,9 +158,6 @@ __global__ void __launch_bounds__(NT) k_mapped(const __grid_constant__ MappedArg
     dst[w.p0] = u0;
     dst[w.p1] = u1;
   };
-  uint4 u0[AHEAD], u1[AHEAD];
-#pragma unroll
-  for (int i = 0; i < AHEAD; ++i) load(tid + i * NT, u0[i], u1[i]);
   if (tid < a.rotary_dim / 2) {
     const double ang = pos * a.inv_freq[tid];
     const double k = rint(ang * 0.15915494309189535);  // 1 / (2 pi)

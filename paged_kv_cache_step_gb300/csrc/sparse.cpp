@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <cstring>
 #include <initializer_list>
 
 #include "engine.h"
@@ -271,7 +272,12 @@ gp_status gp_append_mapped(gp_ctx* c, int32_t layer, const gp_step* s, const gp_
   a.rotary_dim = rope->rotary_dim;
   a.interleaved = rope->layout == GP_ROPE_INTERLEAVED;
   a.err = c->err_dev;
-  frequencies(*rope, a.inv_freq, &a.amplitude);
+  if (c->rope.theta == 0. || std::memcmp(&c->rope, rope, sizeof(gp_rope)) != 0) {  // (theta is above 1)
+    frequencies(*rope, c->rope_inv, &c->rope_amplitude);
+    c->rope = *rope;
+  }
+  std::memcpy(a.inv_freq, c->rope_inv, sizeof(a.inv_freq));
+  a.amplitude = c->rope_amplitude;
   st = launch_step(c, capturing, GP_KERNEL_MAPPED, "append_mapped", [&] { return launch_mapped(a, c->stream); });
   if (st != GP_OK) return st;
   for (auto& gen : c->slot_gen) ++gen;  // demand results over the old rows are stale; whose, only the device knows
