@@ -8,7 +8,7 @@
 //
 // A cluster of `splits` CTAs a (piece, KV head).  Every CTA marks the blocks that
 // the piece's rows list, as bits, and takes an even share of the blocks marked by
-// any; a block's rows are those that list it.  One warp streams the share through a ring of
+// any; a block's rows are those that list it.  (Of a single row the list itself.)  One warp streams the share through a ring of
 // stages of 64 keys, K and V, by TMA (a box is a block of up to 64 tokens, 128-byte
 // swizzle).  Four warps take 16 keys of a stage each:
 //   S = Q K^T   16 x 16, ldmatrix of K
@@ -73,7 +73,7 @@ struct Sm {
 
 template <int D, int G>
 __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ SparseArgs a, const __grid_constant__ SparseMaps maps,
-                                                      int words, int entries) {
+                                                      int words) {
   using L = Sm<D>;
   constexpr int T = 16 / G;  // rows of a piece
   extern __shared__ unsigned char smem_raw[];
@@ -94,6 +94,10 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = a.splits, rank = blockIdx.x % C, unit = blockIdx.x / C, h = unit % a.Hkv;
 
+  if (tid == NT - 1) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
+  }
   const StepPiece p = find_piece(a.s, unit / a.Hkv, T, 1);
   if (p.r < 0 || p.at * T >= p.rows) return;  // (the whole cluster)
   const int t0 = p.at * T, m = min(T, p.rows - t0);
@@ -118,8 +122,6 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
   }
   __syncthreads();
   const int lb = log2_of(a.block), lper = kStepPageLog - lb;  // blocks of a page
-  lists.mark(a, row0, h, m, first.at, lb, words, seen, any_s);
-
   // this lane's rows of Q: (row / G)-th of the piece, head row % G
   uint32_t q[D / 16][4];
   if (warp < WARPS) {
@@ -135,36 +137,55 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
       }
     }
   }
-  __syncthreads();
-  // the marked blocks in order; every warp counts them, the share's are listed
-  int total = 0;
-  for (int w = lane; w < words; w += 32) total += __popc(any_s[w]);
-  total = __reduce_add_sync(0xffffffffu, total);
-  const int from = (int)((int64_t)total * rank / C), to = (int)((int64_t)total * (rank + 1) / C);
-  if (warp == 0) {
-    int at = 0;
-    for (int w0 = 0; w0 < words; w0 += 32) {
-      unsigned any = w0 + lane < words ? any_s[w0 + lane] : 0u;
-      const int mine = __popc(any);
-      int upto = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += v;
+  if (m == 1) {
+    // one row: its list is the piece's
+    if (warp == 0) {
+      int n = 0, before = -1;
+      for (int k0 = 0; k0 < a.top;) {
+        const int b = lists.b[0];
+        int last = __shfl_up_sync(0xffffffffu, b, 1);
+        if (lane == 0) last = before;
+        const unsigned ends = __ballot_sync(0xffffffffu, b < 0 || b <= last || b > first.at >> lb);
+        const int some = ends ? __ffs(ends) - 1 : 32;
+        if (lane < some) list[n + lane].y = b;
+        n += some;
+        before = __shfl_sync(0xffffffffu, b, 31);
+        k0 += 32;
+        if (ends || k0 >= a.top) break;
+        lists.load(a, row0, h, 1u, k0);
       }
-      int e = at + upto - mine;
-      at += __shfl_sync(0xffffffffu, upto, 31);
-      for (; any; any &= any - 1, ++e)
-        if (e >= from && e < to) list[e - from].y = (w0 + lane) * 32 + __ffs(any) - 1;
+      if (lane == 0) total_s = n;
     }
-    if (lane == 0) total_s = to - from;
+  } else {
+    lists.mark(a, row0, h, m, first.at, lb, words, seen, any_s);
+    __syncthreads();
+    if (warp == 0) {  // the marked blocks in order
+      int at = 0;
+      for (int w0 = 0; w0 < words; w0 += 32) {
+        unsigned any = w0 + lane < words ? any_s[w0 + lane] : 0u;
+        const int mine = __popc(any);
+        int upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+          const int v = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane >= d) upto += v;
+        }
+        int e = at + upto - mine;
+        at += __shfl_sync(0xffffffffu, upto, 31);
+        for (; any; any &= any - 1) list[e++].y = (w0 + lane) * 32 + __ffs(any) - 1;
+      }
+      if (lane == 0) total_s = at;
+    }
   }
   __syncthreads();
-  const int n = total_s;
+  // this CTA's share
+  const int from = (int)((int64_t)total_s * rank / C), n = (int)((int64_t)total_s * (rank + 1) / C) - from;
+  list += from;
   for (int e = tid; e < n; e += NT) {
     const int b = list[e].y, page = pages[b >> lper];
-    int rows = 0;
-    for (int x = 0; x < m; ++x) rows |= (int)(seen[x * words + (b >> 5)] >> (b & 31) & 1u) << x;
+    int rows = m == 1;
+    if (m > 1)
+      for (int x = 0; x < m; ++x) rows |= (int)(seen[x * words + (b >> 5)] >> (b & 31) & 1u) << x;
     if (page < 0) {  // the block is left out
       atomicOr(a.s.err, ERR_BAD_PAGE);
       rows = 0;
@@ -384,10 +405,11 @@ template <int D, int G>
 cudaError_t launch_t(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s) {
   constexpr int T = 16 / G;
   const int most = a.s.maxp * (kStepPage / a.block), words = (most + 31) / 32;
-  const int entries = (int)((std::min<int64_t>((int64_t)T * a.top, most) + a.splits - 1) / a.splits) + 1;
+  const int entries = (int)std::min<int64_t>((int64_t)T * a.top, most);
   const int smem = 1024 + Sm<D>::SEEN + 4 * 256 + 4 * (((T + 1) * words + 1) & ~1) + 8 * entries;
-  cudaError_t e = allow_shared<&k_sparse_mma<D, G>>(1024 + Sm<D>::SEEN + 4 * 256 + 4 * (T + 1) * 128 + 8 * 4098);
+  cudaError_t e = allow_shared<&k_sparse_mma<D, G>>(1024 + Sm<D>::SEEN + 4 * 256 + 4 * (T + 1) * 128 + 8 * 4096);
   if (e != cudaSuccess) return e;
+  if (a.splits > 8 && (e = allow_large_clusters<&k_sparse_mma<D, G>>()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(sparse_pieces(a.s, T) * a.Hkv * a.splits));
   cfg.blockDim = dim3(NT);
@@ -399,7 +421,7 @@ cudaError_t launch_t(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_sparse_mma<D, G>, a, maps, words, entries);
+  return cudaLaunchKernelEx(&cfg, k_sparse_mma<D, G>, a, maps, words);
 }
 
 }  // namespace

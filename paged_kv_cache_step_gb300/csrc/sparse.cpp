@@ -389,13 +389,13 @@ gp_status gp_sparse_attention(gp_ctx* c, int32_t layer, const gp_step* s, int32_
   // (two an SM) and a share keeps 64 tokens.  One long request, 64 blocks of 64: 46, 28, 19 and
   // 14.7 us at 1, 2, 4 and 8; 16 requests 31, 29, 37 and 52; 64 requests 90, 104, 120 and 175.
   const int64_t tokens = (int64_t)std::min(top, g.max_pages_per_req * (kPage / block)) * block;
-  auto share = [&](int64_t pieces) {
+  auto share = [&](int64_t pieces, int most) {
     pieces = std::min<int64_t>(pieces, s->max_rows);
     a.splits = 1;
-    while (a.splits < 8 && (a.splits + 1) * pieces * g.num_kv_heads <= 2 * c->sms && tokens >= 64 * (a.splits + 1)) ++a.splits;
+    while (a.splits < most && (a.splits + 1) * pieces * g.num_kv_heads <= 2 * c->sms && tokens >= 64 * (a.splits + 1)) ++a.splits;
   };
   if (!tc) {
-    share(s->max_rows);
+    share(s->max_rows, 8);
     return launch_step(c, capturing, GP_KERNEL_SPARSE, "sparse_attention", [&] { return launch_sparse(a, c->stream); });
   }
   SparseMaps maps;
@@ -406,7 +406,7 @@ gp_status gp_sparse_attention(gp_ctx* c, int32_t layer, const gp_step* s, int32_
   // of 47 and 137 instead of 177; 4001 rows: 320 instead of 1094).
   const int G = g.num_q_heads / g.num_kv_heads;
   const bool many = s->max_rows > (int64_t)s->n * kSparseMmaRows / G;
-  share(sparse_pieces(a.s, (many ? kSparseTcRows : kSparseMmaRows) / G));
+  share(sparse_pieces(a.s, (many ? kSparseTcRows : kSparseMmaRows) / G), many ? 8 : 16);
   CUtensorMap qmap;
   if (many) {
     const cuuint64_t row = (cuuint64_t)g.head_dim * 2;
