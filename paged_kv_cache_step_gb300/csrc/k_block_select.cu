@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(16 * ROWS, ROWS == 8 ? 4 : 3) k_block_select(c
   __shared__ int pages[256];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = a.splits, rank = blockIdx.x % C, item = blockIdx.x / C, h = item % a.Hkv;
-  const StepPiece p = find_piece(a.s, item / a.Hkv, ROWS, 1);
+  const StepPiece p = find_piece(a.s, item / a.Hkv, log2_const(ROWS), 1);
   if (p.r < 0 || p.at * ROWS >= p.rows) return;  // (the whole cluster)
   const int t0 = p.at * ROWS, m = min(ROWS, p.rows - t0);  // rows of the tile
   const size_t row0 = (size_t)p.row0 + t0;

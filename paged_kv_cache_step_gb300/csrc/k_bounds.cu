@@ -32,18 +32,18 @@ __global__ void __launch_bounds__(NT) k_bounds(const __grid_constant__ BoundsArg
   constexpr int PIECES = D / N;    // of a row
   __shared__ float lo_s[NT * N], hi_s[NT * N];
   const int tid = threadIdx.x, unit = tid / threads, t = tid % threads;
-  const int h = blockIdx.y * heads + unit;
-  const StepPiece p = find_piece(a.s, blockIdx.x, a.block, 2);
+  const int h = blockIdx.y * heads + unit, lb = log2_of(a.block);
+  const StepPiece p = find_piece(a.s, blockIdx.x, lb, 2);
   if (p.r < 0) return;
   const StepRow first = step_row(a.s, p.r, 0, tid == 0);  // the request's first and last row
   const StepRow last = step_row(a.s, p.r, p.rows - 1, tid == 0);
   if (!first.live || !last.live) return;
-  const int b = first.at / a.block + p.at;
-  if (b > last.at / a.block) return;
-  const int page = step_page(a.s, first.slot, b * a.block / kStepPage);
+  const int b = (first.at >> lb) + p.at;
+  if (b > last.at >> lb) return;
+  const int page = step_page(a.s, first.slot, b >> (kStepPageLog - lb));
   if (page < 0) return;
   const bool mine = h < a.Hkv;
-  const int per = kStepPage / a.block, sub = b % per, tokens = min(a.block, last.at + 1 - b * a.block);
+  const int per = kStepPage >> lb, sub = b & (per - 1), tokens = min(a.block, last.at + 1 - (b << lb));
   const size_t head = ((size_t)a.layer * a.s.num_pages_total + page) * a.Hkv + h;
   float lo[N], hi[N];
 #pragma unroll

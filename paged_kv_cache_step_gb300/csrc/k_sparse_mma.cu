@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
   }
-  const StepPiece p = find_piece(a.s, unit / a.Hkv, T, 1);
+  const StepPiece p = find_piece(a.s, unit / a.Hkv, log2_const(T), 1);
   if (p.r < 0 || p.at * T >= p.rows) return;  // (the whole cluster)
   const int t0 = p.at * T, m = min(T, p.rows - t0);
   BlockLists<WARPS + 1, T> lists;

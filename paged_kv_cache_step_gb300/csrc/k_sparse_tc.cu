@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const int C = a.splits, rank = blockIdx.x % C, item = blockIdx.x / C, h = item % a.Hkv;
 
-  const StepPiece p = find_piece(a.s, item / a.Hkv, T, 1);
+  const StepPiece p = find_piece(a.s, item / a.Hkv, log2_const(T), 1);
   if (p.r < 0 || p.at * T >= p.rows) return;  // (the whole cluster)
   const int t0 = p.at * T, m_rows = min(T, p.rows - t0);
   BlockLists<NT / 32, T> lists;

@@ -25,6 +25,7 @@ namespace gp {
 namespace {
 
 constexpr int PAGE = 256;
+constexpr int AT_ONCE = 4;
 enum { GIVEN = 0, NO_PAGES = 1, NO_ROWS = 2, INVALID = 3 };  // gp_step_state
 
 // Inclusive sum over the block's threads; every thread also gets the total.
@@ -49,12 +50,14 @@ __device__ __forceinline__ int block_sum(int v, int* part, int& total) {
   return v;
 }
 
-__global__ void __launch_bounds__(1024) k_tables(const __grid_constant__ TablesArgs a) {
+__global__ void __launch_bounds__(1024, 1) k_tables(const __grid_constant__ TablesArgs a) {
   extern __shared__ int sm[];
   int* row0 = sm;               // [n + 1]
   int* first = row0 + a.n + 1;  // [n] pages given before
   int* held = first + a.n;      // [n]
-  unsigned* seen = reinterpret_cast<unsigned*>(held + a.n);  // a bit a slot
+  int* cached = held + a.n;     // [n]
+  int* slots = cached + a.n;    // [n]
+  unsigned* seen = reinterpret_cast<unsigned*>(slots + a.n);  // a bit a slot
   const int words = (a.M + 31) / 32;
   unsigned* twice = seen + words;
   __shared__ int part[32];
@@ -77,9 +80,11 @@ __global__ void __launch_bounds__(1024) k_tables(const __grid_constant__ TablesA
   int rows_wanted = 0, pages_wanted = 0, rows = 0, pages = 0;  // of the requests before this round's
   for (int r0 = 0; r0 < a.n; r0 += nt) {
     const int r = r0 + tid;
-    int have = 0, fresh = 0, need = 0, state = INVALID;
+    int have = 0, fresh = 0, need = 0, state = INVALID, s = 0, c = 0;
     if (r < a.n) {
-      const int s = a.slots[r], c = a.cached[r], m = a.fresh[r];
+      s = a.slots[r];
+      c = a.cached[r];
+      const int m = a.fresh[r];
       if (s >= 0 && s < a.M && !(twice[s >> 5] >> (s & 31) & 1)) {
         have = a.held[s];
         if (c >= 0 && m >= 0 && (int64_t)c + m <= (int64_t)a.maxp * PAGE && have <= a.maxp && have >= (c + PAGE - 1) / PAGE) {
@@ -106,6 +111,8 @@ __global__ void __launch_bounds__(1024) k_tables(const __grid_constant__ TablesA
       row0[r] = row_end - fresh;
       first[r] = page_end - take;
       held[r] = have;
+      cached[r] = c;
+      slots[r] = s;
       if (r == a.n - 1) row0[a.n] = row_end;
     }
     // kept for the writes below: the state of this round's request
@@ -123,7 +130,7 @@ __global__ void __launch_bounds__(1024) k_tables(const __grid_constant__ TablesA
   for (int r = me; r < a.n; r += stride) {
     a.row0[r] = row0[r];
     const int taken = (r + 1 < a.n ? first[r + 1] : pages) - first[r];
-    const int s = a.slots[r];
+    const int s = slots[r];
     if (s >= 0 && s < a.M && !(twice[s >> 5] >> (s & 31) & 1)) {
       a.num_pages[s] = held[r] + taken;
       for (int j = 0; j < taken; ++j) a.tables[(size_t)s * a.maxp + held[r] + j] = a.free_pages[before + first[r] + j];
@@ -133,27 +140,48 @@ __global__ void __launch_bounds__(1024) k_tables(const __grid_constant__ TablesA
     a.row0[a.n] = row0[a.n];
     *a.taken = before + pages;
   }
+  // A warp takes 32 AT_ONCE rows that follow each other, of few requests as a rule: it
+  // looks up the first row's request, and a row of another its own.
+  // (The entries of the tables that are read here are not those written above.)
   const int live = row0[a.n];
-  for (int row = me; row < a.max_rows; row += stride) {
-    if (row >= live) {
-      a.row_req[row] = -1;
-      a.slot_map[row] = -1;
-      a.positions[row] = 0;
-      continue;
-    }
-    int lo = 0, hi = a.n;  // row0[lo] <= row < row0[hi]
+  auto request_of = [&](int row, int lo) {  // row0[lo] <= row
+    int hi = a.n;                           // row0[request] <= row < row0[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (row0[mid] <= row) lo = mid;
       else hi = mid;
     }
-    const int t = row - row0[lo], at = a.cached[lo] + t, j = at / PAGE;
-    const int page = j < held[lo] ? a.tables[(size_t)a.slots[lo] * a.maxp + j] : a.free_pages[before + first[lo] + j - held[lo]];
-    const bool ok = page >= 0 && page < a.num_pages_total;
-    if (!ok) atomicOr(a.err, ERR_BAD_PAGE);
-    a.row_req[row] = lo;
-    a.slot_map[row] = ok ? (int64_t)page * PAGE + at % PAGE : -1;
-    a.positions[row] = a.pos[lo] + t;
+    return lo;
+  };
+  for (int w0 = me / 32 * (32 * AT_ONCE); w0 < a.max_rows; w0 += stride * AT_ONCE) {
+    const int base = w0 < live ? request_of(w0, 0) : 0, r0 = w0 + (tid & 31);
+    int req[AT_ONCE], at[AT_ONCE], page[AT_ONCE];
+    int64_t pos[AT_ONCE];
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int row = r0 + 32 * i;
+      req[i] = -1;
+      at[i] = page[i] = 0;
+      pos[i] = 0;
+      if (row < live) {
+        const int lo = row < row0[base + 1] ? base : request_of(row, base + 1);
+        req[i] = lo;
+        at[i] = cached[lo] + row - row0[lo];
+        const int j = at[i] / PAGE;
+        page[i] = j < held[lo] ? __ldg(a.tables + (size_t)slots[lo] * a.maxp + j) : __ldg(a.free_pages + before + first[lo] + j - held[lo]);
+        pos[i] = __ldg(a.pos + lo) + (row - row0[lo]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int row = r0 + 32 * i;
+      if (row >= a.max_rows) break;
+      const bool ok = page[i] >= 0 && page[i] < a.num_pages_total;
+      if (!ok) atomicOr(a.err, ERR_BAD_PAGE);
+      a.row_req[row] = req[i];
+      a.slot_map[row] = req[i] >= 0 && ok ? (int64_t)page[i] * PAGE + at[i] % PAGE : -1;
+      a.positions[row] = pos[i];
+    }
   }
 }
 
@@ -161,11 +189,14 @@ __global__ void __launch_bounds__(1024) k_tables(const __grid_constant__ TablesA
 
 cudaError_t launch_tables(const TablesArgs& a, cudaStream_t s) {
   const bool small = a.n <= 256 && a.max_rows <= 512;
-  const size_t smem = sizeof(int) * ((size_t)3 * a.n + 1 + 2 * ((size_t)(a.M + 31) / 32));
-  cudaError_t e = allow_shared<&k_tables>(sizeof(int) * (3 * kStepMaxRequests + 1 + 2 * kStepMaxSlots / 32));
+  const size_t smem = sizeof(int) * ((size_t)5 * a.n + 1 + 2 * ((size_t)(a.M + 31) / 32));
+  cudaError_t e = allow_shared<&k_tables>(sizeof(int) * (5 * kStepMaxRequests + 1 + 2 * kStepMaxSlots / 32));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(small ? 1 : 8);
+  // 42 000 rows of 300 requests: 45, 26, 15, 10.3 and 7.5 us with 1, 2, 4, 8 and 16 blocks
+  const bool large = a.max_rows > 16384;
+  if (large && (e = allow_large_clusters<&k_tables>()) != cudaSuccess) return e;
+  cfg.gridDim = dim3(small ? 1 : large ? 16 : 8);
   cfg.blockDim = dim3(small ? 256 : 1024);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

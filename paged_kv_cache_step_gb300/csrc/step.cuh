@@ -14,6 +14,7 @@ constexpr int kStepPageLog = 8;
 
 // log2 of a block's tokens: places and pages of blocks are shifts (a division by a
 // size that the compiler does not know is some thirty instructions).
+__host__ __device__ constexpr int log2_const(int n) { return n > 1 ? 1 + log2_const(n / 2) : 0; }
 __device__ __forceinline__ int log2_of(int block) { return 31 - __clz(block); }
 
 struct StepRow {
@@ -49,9 +50,9 @@ __device__ __forceinline__ int step_page(const StepArgs& s, int slot, int logica
   return -1;
 }
 
-// Pieces of `size` rows of each request, numbered over all of them: request r's
-// are base(r), base(r) + 1, ... with base(r) = row0[r] / size + extra r, so that
-// the launch can be sized without the lengths (at most max_rows / size + extra n
+// Pieces of 2^log rows of each request, numbered over all of them: request r's
+// are base(r), base(r) + 1, ... with base(r) = (row0[r] >> log) + extra r, so that
+// the launch can be sized without the lengths (at most (max_rows >> log) + extra n
 // pieces; those that no row falls into are left at once).  A whole warp calls it.
 struct StepPiece {
   int r;     // -1: none
@@ -59,17 +60,17 @@ struct StepPiece {
   int rows;  // of the request
   int row0;
 };
-__device__ __forceinline__ StepPiece find_piece(const StepArgs& s, int j, int size, int extra) {
+__device__ __forceinline__ StepPiece find_piece(const StepArgs& s, int j, int log, int extra) {
   const int lane = threadIdx.x & 31;
   int below = 0;  // requests whose first piece is j or before
-  for (int r = lane; r < s.n; r += 32) below += s.row0[r] / size + extra * r <= j;
+  for (int r = lane; r < s.n; r += 32) below += (s.row0[r] >> log) + extra * r <= j;
   below = __reduce_add_sync(0xffffffffu, below);
   if (below == 0) return {-1, 0, 0, 0};
   StepPiece p;
   p.r = below - 1;
   p.row0 = s.row0[p.r];
   const int end = s.row0[below];
-  p.at = j - (p.row0 / size + extra * p.r);
+  p.at = j - ((p.row0 >> log) + extra * p.r);
   p.rows = end - p.row0;
   if (p.row0 < 0 || end > s.max_rows || p.rows <= 0 || p.at < 0) return {-1, 0, 0, 0};
   return p;
