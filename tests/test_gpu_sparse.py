@@ -671,6 +671,90 @@ def test_sparse_attention_of_chunks(shape, new):
                 e.close()
 
 
+@pytest.mark.parametrize("block,top", [(16, 70), (32, 33), (64, 8), (128, 5), (256, 2)])
+@pytest.mark.parametrize("shape", ["bf16_g4_d128", "bf16_g2_d128", "bf16_g4_d64", "bf16_g2_d64"])
+def test_sparse_attention_of_few_rows(shape, block, top):
+    """One row a request, and as many as a small piece takes: the kernel of decode steps."""
+    for new in ([1] * 9, [4, 1, 3, 2, 4, 0, 1, 4, 4] if "g4" in shape else [8, 1, 7, 2, 8, 0, 5, 8, 8]):
+        e = Engine([0, 255, 256, 7, 1000, 2511, 31, 1023, 4090], new, pad=0, seed=block + len(shape), **SHAPES[shape])
+        try:
+            e.fill()
+            check_attention(e, block, top, seed=block)
+        finally:
+            e.close()
+
+
+@pytest.mark.parametrize("block,top", [(16, 70), (32, 33), (64, 8), (128, 5), (256, 2)])
+@pytest.mark.parametrize("shape", ["bf16_g4_d128", "bf16_g2_d128", "bf16_g4_d64", "bf16_g2_d64"])
+def test_sparse_attention_of_many_rows(shape, block, top):
+    """Whole pieces of 128 / G rows, one row more and one less, beside requests of a row or
+    none, with rows behind the last one."""
+    n = 32 if "g4" in shape else 64
+    e = Engine([0, 700, 255, 3000, 7, 100], [n, n + 1, 1, n - 1, 0, 2 * n], pad=5, seed=block + len(shape), **SHAPES[shape])
+    try:
+        e.fill()
+        check_attention(e, block, top, seed=block)
+    finally:
+        e.close()
+
+
+@pytest.mark.parametrize("new", [1, 4, 60])
+def test_rows_without_blocks(new):
+    """Empty lists only, in every kernel: zeros, whatever the caches hold."""
+    for kernel in (gp.GP_SCAN_TENSOR_CORE, gp.GP_SCAN_CUDA_CORE):
+        e = Engine([300, 0], [new, new], seed=new, kernel=kernel)
+        try:
+            q = e.randn(2 * new, 8, 128).bfloat16()
+            out = torch.full_like(q, math.nan)
+            gp.gp_sparse_attention(e.ctx, e.layer, e.step, 64, 3, q, torch.full((2 * new, 2, 3), -1, dtype=torch.int32, **CUDA), out)
+            gp.gp_synchronize(e.ctx)
+            assert not out.any()
+        finally:
+            e.close()
+
+
+@pytest.mark.parametrize("new", [4, 70])
+def test_queries_of_other_rows_do_not_matter(new):
+    """NaN in the queries of one request, and behind the last row, stays there."""
+    e = Engine([500, 300], [new, new], pad=40, seed=3)
+    e.block = 32
+    try:
+        e.fill()
+        lists = random_lists(e, 5, 1)
+        blocks = np.full((e.max_rows, 2, 5), -1)
+        for row, x in enumerate(lists):
+            for h in range(2):
+                blocks[row, h, :len(x[h])] = x[h]
+        q = e.randn(e.max_rows, 8, 128).bfloat16()
+        want, tol = attention_reference(e, q, lists)
+        q[new:] = math.nan
+        out = torch.zeros_like(q)
+        gp.gp_sparse_attention(e.ctx, e.layer, e.step, 32, 5, q, i32(blocks), out)
+        gp.gp_synchronize(e.ctx)
+        assert torch.all((out[:new].double() - want[:new]).abs() <= tol[:new])
+        assert not out[2 * new:].any()
+    finally:
+        e.close()
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_sparse_attention_at_random(seed):
+    rng = np.random.default_rng(seed)
+    for _ in range(3):
+        n = int(rng.integers(1, 9))
+        shape = list(SHAPES)[rng.integers(len(SHAPES))]
+        cached = (rng.random(n) ** 3 * 5000).astype(int)
+        new = (rng.random(n) ** 3 * rng.choice([3, 12, 150])).astype(int)
+        new[rng.integers(n)] += 1
+        block = int(rng.choice([16, 32, 64, 128, 256]))
+        e = Engine(cached.tolist(), new.tolist(), pad=int(rng.integers(0, 9)), seed=seed, **SHAPES[shape])
+        try:
+            e.fill()
+            check_attention(e, block, int(rng.integers(1, 1 + 2048 // block)), seed=seed)
+        finally:
+            e.close()
+
+
 @pytest.mark.parametrize("shape", ["bf16_g4_d128", "f32_g4_d128"])
 def test_lists_end_where_they_stop_ascending(shape):
     """At an entry that is negative, not above the one before it, or past the row's own block."""
@@ -779,6 +863,29 @@ def test_bad_device_data_is_reported_and_left_out():
     def page(e):
         e.arrays["tables"][int(e.slots[2]), 0] = e.pool
     run(page, [4, 5])
+
+
+@pytest.mark.parametrize("new", [2, 50])
+def test_a_bad_page_is_left_out(new):
+    """Blocks on a page outside the pool count for nothing, in each kernel; the rest does."""
+    for kernel in (gp.GP_SCAN_TENSOR_CORE, gp.GP_SCAN_CUDA_CORE):
+        e = Engine([700], [new], L=1, layer=0, seed=8, kernel=kernel)
+        e.block = 64
+        try:
+            e.fill()
+            q = e.randn(new, 8, 128).bfloat16()
+            blocks = i32([[[0, 2, 5, 6, 9]] * 2] * new)
+            want, tol = attention_reference(e, q, [[np.array([0, 2, 9])] * 2] * new)
+            for bad in (-1, e.pool, 2 ** 31 - 1, -2 ** 31):
+                e.arrays["tables"][int(e.slots[0]), 1] = bad  # blocks 4 to 7
+                out = torch.full_like(q, 7.0)
+                gp.gp_sparse_attention(e.ctx, 0, e.step, 64, 5, q, blocks, out)
+                with pytest.raises(gp.GrowPageError) as err:
+                    gp.gp_synchronize(e.ctx)
+                assert err.value.status == gp.GP_ERR_INVALID
+                assert torch.all((out.double() - want).abs() <= tol)
+        finally:
+            e.close()
 
 
 # ---- together ------------------------------------------------------------------------------
@@ -917,6 +1024,80 @@ def test_a_run_of_steps_eager_and_replayed():
     eager, replayed = run_serving(False), run_serving(True)
     for a, b in zip(eager, replayed):
         assert torch.equal(bits(a), bits(b))
+
+
+def test_a_captured_prompt():
+    """Prompts in a graph: the larger kernels and their tensor maps, replayed over other contents."""
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        e = Engine([300, 0], [400, 90], L=1, layer=0, seed=11, stream=stream)
+        e.block = 32
+        e.fill()
+        q = e.randn(490, 8, 128).bfloat16()
+        blocks = torch.full((490, 2, 6), -1, dtype=torch.int32, **CUDA)
+        bounds, scales = bounds_arrays(e, 32)
+        out = torch.zeros_like(q)
+
+        def calls():
+            gp.gp_block_bounds(e.ctx, 0, e.step, 32, bounds, scales)
+            gp.gp_select_blocks(e.ctx, 0, e.step, 32, 6, 0, 1, q, bounds, scales, blocks)
+            gp.gp_sparse_attention(e.ctx, 0, e.step, 32, 6, q, blocks, out)
+
+        e.cached, e.new = [0, 0], [700, 90]  # the bounds of every block
+        calls()
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            calls()
+        for _ in range(2):
+            q.copy_(e.randn(490, 8, 128))
+            e.fill()
+            graph.replay()
+            gp.gp_synchronize(e.ctx)
+            e.cached, e.new = [300, 0], [400, 90]
+            lists = [[h[h >= 0] for h in row] for row in blocks.cpu().numpy()]
+            want, tol = attention_reference(e, q, lists)
+            assert torch.all((out.double() - want).abs() <= tol)
+            first = out.clone()
+            calls()
+            gp.gp_synchronize(e.ctx)
+            assert torch.equal(bits(first), bits(out))
+        del graph
+        e.close()
+
+
+def test_two_engines_at_once():
+    """Two contexts on two streams, the same calls at the same time: nothing shared."""
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    engines, outs = [], []
+    for i, st in enumerate(streams):
+        with torch.cuda.stream(st):
+            e = Engine([2000, 30], [300, 1], L=1, layer=0, seed=20 + i, stream=st)
+            e.fill()
+            e.block = 64
+            lists = random_lists(e, 8, i)
+            blocks = np.full((301, 2, 8), -1)
+            for row, x in enumerate(lists):
+                for h in range(2):
+                    blocks[row, h, :len(x[h])] = x[h]
+            q = e.randn(301, 8, 128).bfloat16()
+            engines.append((e, q, i32(blocks), lists))
+    torch.cuda.synchronize()
+    for i, st in enumerate(streams):
+        with torch.cuda.stream(st):
+            outs.append([torch.zeros_like(engines[i][1]) for _ in range(10)])
+    torch.cuda.synchronize()
+    for k in range(10):
+        for i in range(2):
+            e, q, blocks, _ = engines[i]
+            gp.gp_sparse_attention(e.ctx, 0, e.step, 64, 8, q, blocks, outs[i][k])
+    for i in range(2):
+        e, q, blocks, lists = engines[i]
+        gp.gp_synchronize(e.ctx)
+        want, tol = attention_reference(e, q, lists)
+        for out in outs[i]:
+            assert torch.all((out.double() - want).abs() <= tol) and torch.equal(bits(out), bits(outs[i][0]))
+        e.close()
 
 
 def test_bounds_after_an_eviction():
