@@ -487,9 +487,10 @@ gp_status gp_evict_weighted(gp_ctx* ctx, int32_t n, gp_request* reqs, const int3
  * They share these rules.  Addresses, sizes and options are checked before
  * anything happens (GP_ERR_INVALID, nothing changed); the device current at
  * gp_create must be current (GP_ERR_INVALID).  What the device arrays hold is
- * checked by the kernels: a row whose request, slot, length or page is outside
- * the engine's sizes is left out (its outputs stay as they were) and
- * reported by the next synchronising call as GP_ERR_INVALID.  Block sizes are
+ * checked by the kernels: a row whose request, slot, length or place is outside
+ * the engine's sizes is left out (its outputs stay as they were), a page of a
+ * table that is outside the pool counts for nothing (to gp_select_blocks: for any
+ * page), and both are reported by the next synchronising call as GP_ERR_INVALID.  Block sizes are
  * 16, 32, 64, 128 or 256 tokens.  Rows behind the step's last one
  * (row_req and slot_map of -1) are left as they were.
  * All run on the engine stream, asynchronously.  Those that read or write K/V
@@ -501,7 +502,8 @@ gp_status gp_evict_weighted(gp_ctx* ctx, int32_t n, gp_request* reqs, const int3
  * gp_step: the arrays of one step, device memory of the caller, 4-byte (64-bit
  * ones 8-byte) aligned and apart from one another.  The first four are inputs of
  * gp_build_tables; tables is read and extended by it; the last four are what it
- * writes and the others read.  A caller may fill those by other means.
+ * writes.  gp_append_mapped reads slot_map and positions, the other three calls slots,
+ * num_cached, tables, row0 and row_req.  A caller may fill them by other means.
  *   n          requests, at most max_slots and 4096
  *   max_rows   rows that the step's buffers have room for (new tokens of all
  *              requests together)
@@ -730,8 +732,8 @@ gp_status gp_debug_fail_next_launch(gp_ctx* ctx, int32_t kernel);
 
 /* Which kernels do the cache-wide contractions: the scan of
  * gp_boundary_demand and the scores and weighted values of
- * gp_decode_attention(_weighted) and gp_chunk_attention (which takes bf16
- * queries and caches on the tensor cores).  AUTO (default): the tensor-core (tcgen05) kernels
+ * gp_decode_attention(_weighted), gp_chunk_attention and gp_sparse_attention (which
+ * two take bf16 queries and caches on the tensor cores).  AUTO (default): the tensor-core (tcgen05) kernels
  * where they apply -- the scan for bf16 caches (every request length up to
  * the 256-page block-table limit), attention for bf16 caches with d = 128
  * and 2 or 4 query heads per KV head -- and the CUDA-core (fp32 FMA)
