@@ -159,23 +159,8 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
   } else {
     lists.mark(a, row0, h, m, first.at, lb, words, seen, any_s);
     __syncthreads();
-    if (warp == 0) {  // the marked blocks in order
-      int at = 0;
-      for (int w0 = 0; w0 < words; w0 += 32) {
-        unsigned any = w0 + lane < words ? any_s[w0 + lane] : 0u;
-        const int mine = __popc(any);
-        int upto = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-          const int v = __shfl_up_sync(0xffffffffu, upto, d);
-          if (lane >= d) upto += v;
-        }
-        int e = at + upto - mine;
-        at += __shfl_sync(0xffffffffu, upto, 31);
-        for (; any; any &= any - 1) list[e++].y = (w0 + lane) * 32 + __ffs(any) - 1;
-      }
-      if (lane == 0) total_s = at;
-    }
+    const int n = list_blocks<WARPS + 1>(any_s, words, [&](int e, int b) { list[e].y = b; });  // in order
+    if (tid == 0) total_s = n;
   }
   __syncthreads();
   // this CTA's share

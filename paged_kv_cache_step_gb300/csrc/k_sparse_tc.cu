@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   unsigned* seen = any_s + words;
   uint16_t* list = reinterpret_cast<uint16_t*>(seen + T * words);
   __shared__ __align__(8) uint64_t bars[2 * NST + 7];
-  __shared__ int abort_s, count_s, bad_s;
+  __shared__ int abort_s, bad_s;
   __shared__ uint32_t tmem_s;
   __shared__ float2 ml_s[128];  // a row's maximum and sum
   volatile int* abort = &abort_s;
@@ -129,34 +129,25 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   const size_t at = ((row0 + tok) * a.Hq + h * G + tid % G) * D;
   const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
   __syncthreads();
-  if (warp == 4) {  // the blocks that any row lists, in order
-    int n = 0;
-    for (int w0 = 0; w0 < words; w0 += 32) {
-      const int w = w0 + lane;
-      unsigned any = w < words ? any_s[w] : 0u;
-      for (unsigned left = bad_s ? any : 0u; left; left &= left - 1) {
-        const int bit = __ffs(left) - 1;
-        if (pages[(w * 32 + bit) >> lper] >= 0) continue;
-        atomicOr(a.s.err, ERR_BAD_PAGE);  // the block is left out
-        any &= ~(1u << bit);
+  if (bad_s) {  // blocks on a page outside the pool are left out
+    if (warp == 0)
+      for (int w = 0; w < words; ++w) {
+        const bool out = (any_s[w] >> lane & 1u) && pages[(w * 32 + lane) >> lper] < 0;
+        const unsigned drop = __ballot_sync(0xffffffffu, out);
+        if (lane == 0 && drop) {
+          atomicOr(a.s.err, ERR_BAD_PAGE);
+          any_s[w] &= ~drop;
+        }
       }
-      const int mine = __popc(any);
-      int upto = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += v;
-      }
-      for (int e = n + upto - mine; any; any &= any - 1) list[e++] = (uint16_t)(w * 32 + __ffs(any) - 1);
-      n += __shfl_sync(0xffffffffu, upto, 31);
-    }
-    if (lane == 0) count_s = n;
+    __syncthreads();
   }
+  // the blocks that any row lists, in order
+  const int count = list_blocks<NT / 32>(any_s, words, [&](int e, int b) { list[e] = (uint16_t)b; });
   __syncthreads();
   const int lx = min(lb, 6), box = 1 << lx, boxes = KEYS >> lx, lof = lb - lx;  // a box, of a stage, log2 of those of a block
   // this CTA's share of the list, in boxes
-  const int from = (int)((int64_t)count_s * rank / C);
-  int all = uniform((int)((int64_t)count_s * (rank + 1) / C) - from) << lof;
+  const int from = (int)((int64_t)count * rank / C);
+  int all = uniform((int)((int64_t)count * (rank + 1) / C) - from) << lof;
   list += from;
   // first logical slot of box e
   auto slot_of = [&](int e) { return ((int)list[e >> lof] << lb) + ((e & ((1 << lof) - 1)) << lx); };

@@ -76,4 +76,29 @@ struct BlockLists {
   }
 };
 
+// Puts the marked blocks in order: put(place, block).  Every warp of the CTA calls it,
+// takes each WARPS-th word (a lane a bit) and gets the count.
+template <int WARPS, typename Put>
+__device__ __forceinline__ int list_blocks(const unsigned* any, int words, Put&& put) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int total = 0;
+  for (int w0 = 0; w0 < words; w0 += 32) {
+    const unsigned mine = w0 + lane < words ? any[w0 + lane] : 0u;
+    int upto = __popc(mine);
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += v;
+    }
+    const int before = total + upto - __popc(mine);
+    total += __shfl_sync(0xffffffffu, upto, 31);
+    for (int w = warp; w < 32 && w0 + w < words; w += WARPS) {
+      const unsigned bits = __shfl_sync(0xffffffffu, mine, w);
+      const int at = __shfl_sync(0xffffffffu, before, w);
+      if (bits >> lane & 1u) put(at + __popc(bits & ((1u << lane) - 1)), (w0 + w) * 32 + lane);
+    }
+  }
+  return total;
+}
+
 }  // namespace gp
