@@ -492,7 +492,8 @@ gp_status gp_evict_weighted(gp_ctx* ctx, int32_t n, gp_request* reqs, const int3
  * table that is outside the pool counts for nothing (to gp_select_blocks: for any
  * page), and both are reported by the next synchronising call as GP_ERR_INVALID.  Block sizes are
  * 16, 32, 64, 128 or 256 tokens.  Rows behind the step's last one
- * (row_req and slot_map of -1) are left as they were.
+ * (row_req and slot_map of -1) are left as they were.  max_rows times the KV heads
+ * is below 2^27 (GP_ERR_UNSUPPORTED).  gp_set_timing does not time captured launches.
  * All run on the engine stream, asynchronously.  Those that read or write K/V
  * (gp_append_mapped, gp_block_bounds, gp_sparse_attention) wait there for a
  * compaction pending on the side stream, whatever its pages; a call that is

@@ -133,7 +133,7 @@ void frequencies(const gp_rope& r, double* inv, float* amplitude) {
     if (r.scaling == GP_ROPE_LINEAR) part = 1.;
     if (r.scaling == GP_ROPE_BANDS) part = 1. - std::fmin(1., std::fmax(0., (L * f / two_pi - r.low_turns) / (high - r.low_turns)));
     if (r.scaling == GP_ROPE_RAMP) part = std::fmin(1., std::fmax(0., (i - from) / std::fmax(to - from, 0.001)));
-    inv[i] = f * (1. - part) + f / r.factor * part;
+    inv[i] = part > 0. ? f * (1. - part) + f / r.factor * part : f;  // (the factor counts for nothing under NONE)
   }
   *amplitude = (float)(r.amplitude != 0. ? r.amplitude : r.scaling == GP_ROPE_RAMP ? 0.1 * std::log(r.factor) + 1. : 1.);
 }

@@ -20,6 +20,9 @@ first run):
 """
 
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -291,7 +294,7 @@ def frequencies(rd, layout, scaling, theta, factor, original, low, high):
             pair = lambda t: rd * math.log(original / (2 * math.pi * t)) / (2 * math.log(theta))
             a, b = max(0, math.floor(pair(high))), min(rd - 1, math.ceil(pair(low)))
             part = min(1.0, max(0.0, (i - a) / max(b - a, 0.001)))
-        out.append((1 - part) * f + part * f / factor)
+        out.append((1 - part) * f + part * f / factor if part else f)
     return np.array(out)
 
 
@@ -314,7 +317,8 @@ FORMS = [dict(), dict(layout=gp.GP_ROPE_INTERLEAVED), dict(rotary_dim=16), dict(
          dict(scaling=gp.GP_ROPE_BANDS, factor=8.0, theta=5e5),
          dict(scaling=gp.GP_ROPE_BANDS, factor=2.0, low_turns=2.0, high_turns=9.0, original_length=4096, rotary_dim=32),
          dict(scaling=gp.GP_ROPE_RAMP, factor=32.0, theta=1e6), dict(scaling=gp.GP_ROPE_RAMP, factor=4.0, amplitude=1.0, rotary_dim=32),
-         dict(scaling=gp.GP_ROPE_RAMP, factor=4.0, original_length=1, layout=gp.GP_ROPE_INTERLEAVED), dict(amplitude=0.5, theta=100.0)]
+         dict(scaling=gp.GP_ROPE_RAMP, factor=4.0, original_length=1, layout=gp.GP_ROPE_INTERLEAVED), dict(amplitude=0.5, theta=100.0),
+         dict(factor=0.0, original_length=0, low_turns=math.nan)]
 
 
 def check_append(e, form, packed="columns"):
@@ -1064,6 +1068,36 @@ def test_a_captured_prompt():
             assert torch.equal(bits(first), bits(out))
         del graph
         e.close()
+
+
+FIRST_CAPTURE = """
+import math, sys
+sys.path[:0] = [%r, %r]
+import torch
+import test_gpu_sparse as t
+stream = torch.cuda.Stream()
+with torch.cuda.stream(stream):
+    s = t.Serving([300, 1], stream=stream)
+    b = s.buffers(310)
+    s.new.copy_(t.i32([300, 1]))
+    b["qkv"].copy_(torch.randn(b["qkv"].shape, device="cuda", generator=s.gen))
+    stream.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        s.pass_(b)
+    graph.replay()
+    t.gp.gp_synchronize(s.ctx)
+    t.check_serving(s, b, [300, 1], [0, 0])
+    del graph
+print("captured first")
+"""
+
+
+def test_the_first_calls_of_a_process_are_captured():
+    """Nothing has to run before a capture: kernels and settings are made during it."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    got = subprocess.run([sys.executable, "-c", FIRST_CAPTURE % (os.path.dirname(here), here)], capture_output=True, text=True, timeout=200)
+    assert got.returncode == 0 and "captured first" in got.stdout, got.stdout + got.stderr
 
 
 def test_two_engines_at_once():
