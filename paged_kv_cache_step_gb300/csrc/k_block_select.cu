@@ -18,8 +18,15 @@
 // block's row, four K steps' worth (K is summed over, so its order is free as
 // long as P and N follow it), made fp16 by placing each byte under the exponent of
 // 1024 and subtracting.  A tile of up to 8 rows of a request shares them.
-// Scores stay in shared memory; a warp picks a row's blocks: the threshold by
-// halving the range of the ordered bits, then one ordered pass.
+// Scores stay in shared memory; a warp picks a row's blocks with their keys in
+// registers: the threshold bit by bit from the highest that differs, then one ordered
+// pass.  Few tiles are shared by a cluster, whose scores go to its first CTA.
+//
+// Measured (32 + 8 heads, d = 128, blocks of 64, 32 of them): a decode step of 64 requests of
+// 4 to 128 pages 13.5 us in a graph, where reading the bounds takes 4.5: latency; 4001 rows behind
+// 12 007 tokens 64 us, 68 % of the issue slots.  On the way: tiles of 8 rows, keys read from shared
+// memory for every bit 141 us; in registers, tiles of 16 80 us; the products' row operand from
+// shared memory, so that three CTAs fit on an SM, 64 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -13,8 +13,10 @@
 // block of 64 tokens and head, which keeps the call free of a read-modify-write
 // and makes it the one that rebuilds after an eviction too.
 //
-// `threads` threads a (block, head), each with 16 bytes of every so-manieth token:
-// eight loads a thread where the block has that many.
+// A power of two of threads a (block, head), 16 bytes of a token each, eight loads in
+// flight where the block has that many.  Measured: 64 blocks of 64 tokens with 8 heads 8 us
+// (five dependent reads, from row0 to the keys), 13 621 tokens in blocks of 32 11 us, where
+// reading the keys takes 4.3 at the copy rate.
 #include <cuda_bf16.h>
 
 #include <cstdint>

@@ -9,7 +9,8 @@
 //   row i of request r: logical slot t = cached_r + i, page table[t / 256] or, for
 //   t / 256 >= held_r, free[taken + (pages given before) + t / 256 - held_r]
 //
-// Bounded by latency: a step of 64 requests reads and writes 5 KB.  One launch:
+// Bounded by latency: a step of 64 requests reads and writes 5 KB and takes 4 us in a
+// graph; 42 000 rows of 300 requests 8 us.  One launch:
 // every block of a cluster scans all requests for itself (4 bytes x 5 a request),
 // the cluster meets once, so that no output is written before every input is
 // read (num_pages may be held, taken taken_in), and then shares the rows.
