@@ -10,7 +10,9 @@
 // list, and the shares' maxima, sums and outputs are joined through distributed
 // shared memory: no scratch, no second launch, one fixed order.
 // In a CTA a key's row is read by D / 8 lanes, 8 dimensions each; every group of
-// lanes keeps its own running maximum and sum (base 2) over its keys.  All in fp32;
+// lanes keeps its own running maximum and sum (base 2) over its keys.  The logits of
+// four keys are summed over the lanes by halves, so that a lane ends with one or two of
+// them and weighs those alone (15 exchanges for 16 logits instead of 64).  All in fp32;
 // one rounding to the query's type at the end.  Six requests of 3 to 5 rows, d = 64, fp32, 24 blocks
 // of 16: 6.8 us in a graph.
 #include <cuda_bf16.h>
@@ -27,6 +29,7 @@ constexpr int NT = 256;
 constexpr int NW = NT / 32;
 constexpr int ENTRIES = 64;  // of a share that are looked up at a time
 constexpr float NEG = -1.0e30f;
+constexpr float LAZY = 16.f;
 
 // Dimension t of the 8 that lane c of a group owns (k_attention.cu's layout: the
 // lanes of a quarter warp read 128 contiguous bytes).
@@ -91,14 +94,17 @@ __global__ void __launch_bounds__(NT) k_sparse(const __grid_constant__ SparseArg
   const int count = count_s;
   const int from = (int)((int64_t)count * rank / C), to = (int)((int64_t)count * (rank + 1) / C);
 
-  float m[G], l[G], acc[G][8];
+  // The G U logits of a turn are summed over the lanes of the group by halves, after
+  // which lane c holds OWN of them, those from FIRST(c) = g U + u on; it keeps the
+  // maximum and its part of the sum of their head.
+  constexpr int NV = G * U, OWN = NV > LN ? NV / LN : 1, TWINS = LN > NV ? LN / NV : 1;  // TWINS lanes hold the same
+  const unsigned mates = ((1u << (LN - 1) << 1) - 1) << (lane / LN * LN);
+  const int first = c / TWINS * OWN;
+  float m_own = NEG, l_own = 0.f, acc[G][8];
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    m[g] = NEG;
-    l[g] = 0.f;
+  for (int g = 0; g < G; ++g)
 #pragma unroll
     for (int t = 0; t < 8; ++t) acc[g][t] = 0.f;
-  }
   for (int e0 = from; e0 < to; e0 += ENTRIES) {
     const int n = min(ENTRIES, to - e0);
     __syncthreads();
@@ -110,60 +116,93 @@ __global__ void __launch_bounds__(NT) k_sparse(const __grid_constant__ SparseArg
     __syncthreads();
     const int keys = n << lb;
     for (int k0 = group; k0 < keys; k0 += GROUPS * U) {
-      float z[G][U], v[U][8];
-      bool seen[U];
+      float z[NV], v[U][8];
+      unsigned seen = 0u;  // a bit a key
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int k = k0 + u * GROUPS, e = k >> lb, o = k & (a.block - 1);
-        seen[u] = k < keys && at_s[min(e, n - 1)] >= 0 && tok_s[min(e, n - 1)] + o <= rw.at;
+        const int k = k0 + u * GROUPS, e = min(k >> lb, n - 1), o = k & (a.block - 1);
+        const bool see = k < keys && at_s[e] >= 0 && tok_s[e] + o <= rw.at;
         float kk[8];
-        if (seen[u]) {
+        if (see) {
           const size_t at = (size_t)(at_s[e] + o) * D * KB;
           load_row<D, KF32>(static_cast<const unsigned char*>(a.k_cache) + at, c, kk);
           load_row<D, KF32>(static_cast<const unsigned char*>(a.v_cache) + at, c, v[u]);
+          seen |= 1u << u;
         } else {
 #pragma unroll
           for (int t = 0; t < 8; ++t) kk[t] = v[u][t] = 0.f;
         }
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          float s = 0.f;
+          float x = 0.f;
 #pragma unroll
-          for (int t = 0; t < 8; ++t) s = fmaf(q[g][t], kk[t], s);
-          z[g][u] = s;
+          for (int t = 0; t < 8; ++t) x = fmaf(q[g][t], kk[t], x);
+          z[g * U + u] = x;
         }
       }
       // (the lanes of a group take the same turns; groups of a warp may not)
-      const unsigned mates = LN == 32 ? 0xffffffffu : ((1u << LN) - 1) << (lane / LN * LN);
+      int have = NV;
 #pragma unroll
-      for (int d = LN / 2; d > 0; d /= 2)
+      for (int d = LN / 2; d > 0; d /= 2) {
+        if (have > 1) {
+          have /= 2;
+          const bool upper = (c & d) != 0;
 #pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-          for (int u = 0; u < U; ++u) z[g][u] += __shfl_xor_sync(mates, z[g][u], d);
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        float top = m[g];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (seen[u]) top = fmaxf(top, z[g][u]);
-        const float f = ex2f(m[g] - top);
-        m[g] = top;
-        l[g] *= f;
-#pragma unroll
-        for (int t = 0; t < 8; ++t) acc[g][t] *= f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float w = seen[u] ? ex2f(z[g][u] - top) : 0.f;
-          l[g] += w;
-#pragma unroll
-          for (int t = 0; t < 8; ++t) acc[g][t] = fmaf(w, v[u][t], acc[g][t]);
+          for (int i = 0; i < NV / 2; ++i)
+            if (i < have) {
+              const float keep = upper ? z[i + have] : z[i], send = upper ? z[i] : z[i + have];
+              z[i] = keep + __shfl_xor_sync(mates, send, d);
+            }
+        } else {
+          z[0] += __shfl_xor_sync(mates, z[0], d);
         }
       }
+      float top = NEG;
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) {
+        if (!(seen >> ((first + i) % U) & 1u)) z[i] = __int_as_float(0xff800000);  // -inf
+        top = fmaxf(top, z[i]);
+      }
+#pragma unroll
+      for (int d = TWINS; d < U / OWN * TWINS; d *= 2) top = fmaxf(top, __shfl_xor_sync(mates, top, d));
+      const bool grow = top > m_own + LAZY;
+      if (__any_sync(mates, grow)) {  // a maximum is followed only when it grows by more than 16
+        const float f = grow ? ex2f(m_own - top) : 1.f;
+        if (grow) m_own = top;
+        l_own *= f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float fg = __shfl_sync(mates, f, g * U / OWN * TWINS, LN);
+#pragma unroll
+          for (int t = 0; t < 8; ++t) acc[g][t] *= fg;
+        }
+      }
+      float w[OWN];
+#pragma unroll
+      for (int i = 0; i < OWN; ++i) {
+        w[i] = ex2f(z[i] - m_own);
+        l_own += w[i];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float x = __shfl_sync(mates, w[(g * U + u) % OWN], (g * U + u) / OWN * TWINS, LN);
+#pragma unroll
+          for (int t = 0; t < 8; ++t) acc[g][t] = fmaf(x, v[u][t], acc[g][t]);
+        }
     }
   }
-  // the groups of a warp, the warps, the CTAs
   __syncwarp();
+#pragma unroll
+  for (int d = TWINS; d < U / OWN * TWINS; d *= 2) l_own += __shfl_xor_sync(0xffffffffu, l_own, d);
+  float m[G], l[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    m[g] = __shfl_sync(0xffffffffu, m_own, g * U / OWN * TWINS, LN);
+    l[g] = __shfl_sync(0xffffffffu, l_own, g * U / OWN * TWINS, LN);
+  }
+  // the groups of a warp, the warps, the CTAs
 #pragma unroll
   for (int d = LN; d < 32; d *= 2)
 #pragma unroll
