@@ -10,12 +10,13 @@
 //   t / 256 >= held_r, free[taken + (pages given before) + t / 256 - held_r]
 //
 // Bounded by latency: a step of 64 requests reads and writes 5 KB and takes 4 us in a
-// graph; 42 000 rows of 300 requests 8 us.  One launch:
+// graph.  One launch:
 // every block of a cluster scans all requests for itself (4 bytes x 5 a request),
 // the cluster meets once, so that no output is written before every input is
 // read (num_pages may be held, taken taken_in), and then shares the rows.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "chained.cuh"
@@ -26,7 +27,7 @@ namespace gp {
 namespace {
 
 constexpr int PAGE = 256;
-constexpr int AT_ONCE = 4;
+constexpr int AT_ONCE = 2;
 enum { GIVEN = 0, NO_PAGES = 1, NO_ROWS = 2, INVALID = 3 };  // gp_step_state
 
 // Inclusive sum over the block's threads; every thread also gets the total.
@@ -63,9 +64,7 @@ __global__ void __launch_bounds__(1024, 1) k_tables(const __grid_constant__ Tabl
   unsigned* twice = seen + words;
   __shared__ int part[32];
   const int tid = threadIdx.x, nt = blockDim.x;
-  unsigned rank, ranks;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const unsigned rank = blockIdx.x, ranks = gridDim.x;  // (of one cluster, unless the buffers are apart)
   const bool leader = rank == 0;
 
   for (int i = tid; i < 2 * words; i += nt) seen[i] = 0;
@@ -120,8 +119,8 @@ __global__ void __launch_bounds__(1024, 1) k_tables(const __grid_constant__ Tabl
     if (r < a.n && leader) a.state[r] = state;
   }
   if (a.n == 0 && tid == 0) row0[0] = 0;
-  // every block of the cluster has read the inputs
-  if (ranks > 1) {
+  // every block has read what another may write
+  if (ranks > 1 && !a.apart) {
     asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   } else {
@@ -189,21 +188,23 @@ __global__ void __launch_bounds__(1024, 1) k_tables(const __grid_constant__ Tabl
 }  // namespace
 
 cudaError_t launch_tables(const TablesArgs& a, cudaStream_t s) {
-  const bool small = a.n <= 256 && a.max_rows <= 512;
+  // Buffers of their own for what is read and written need no meeting: blocks of 512
+  // threads, one for 1024 rows.  Else a cluster, which 16 blocks are the most of.
+  // 42 000 rows of 300 requests: 45, 26, 15, 10.3 and 7.5 us with 1, 2, 4, 8 and 16 blocks
+  // of 1024 threads in a cluster, 5.1 us with 43 blocks apart.
+  const bool small = a.n <= 256 && a.max_rows <= 512, large = !small && !a.apart && a.max_rows > 16384;
   const size_t smem = sizeof(int) * ((size_t)5 * a.n + 1 + 2 * ((size_t)(a.M + 31) / 32));
   cudaError_t e = allow_shared<&k_tables>(sizeof(int) * (5 * kStepMaxRequests + 1 + 2 * kStepMaxSlots / 32));
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  // 42 000 rows of 300 requests: 45, 26, 15, 10.3 and 7.5 us with 1, 2, 4, 8 and 16 blocks
-  const bool large = a.max_rows > 16384;
   if (large && (e = allow_large_clusters<&k_tables>()) != cudaSuccess) return e;
-  cfg.gridDim = dim3(small ? 1 : large ? 16 : 8);
-  cfg.blockDim = dim3(small ? 256 : 1024);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(small ? 1 : a.apart ? (unsigned)std::min((a.max_rows + 1023) / 1024 + 1, 128) : large ? 16 : 8);
+  cfg.blockDim = dim3(small ? 256 : a.apart ? 512 : 1024);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cfg.gridDim.x;
+  attr.val.clusterDim.x = a.apart ? 1 : cfg.gridDim.x;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;

@@ -208,6 +208,7 @@ gp_status gp_build_tables(gp_ctx* c, const gp_step* s, const int32_t* held_dev, 
   a.slot_map = s->slot_map;
   a.positions = s->positions;
   a.err = c->err_dev;
+  a.apart = num_pages_dev != held_dev && taken_dev != taken_in_dev;
   return launch_step(c, capturing, GP_KERNEL_TABLES, "build_tables", [&] { return launch_tables(a, c->stream); });
 } catch (const std::exception&) {
   return no_memory(c);

@@ -39,6 +39,7 @@ struct TablesArgs {
   int32_t *tables, *num_pages, *row0, *row_req, *state, *taken;
   int64_t *slot_map, *positions;
   int* err;
+  bool apart;                // num_pages is not held, taken not taken_in
 };
 
 // ---- rotary forms, through the slot map ----------------------------------------
