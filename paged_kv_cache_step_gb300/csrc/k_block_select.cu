@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(16 * ROWS, ROWS == 8 ? 4 : 3) k_block_select(c
   __shared__ int pages[256];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = a.splits, rank = blockIdx.x % C, item = blockIdx.x / C, h = item % a.Hkv;
+  begin_step();
   const StepPiece p = find_piece(a.s, item / a.Hkv, log2_const(ROWS), 1);
   if (p.r < 0 || p.at * ROWS >= p.rows) return;  // (the whole cluster)
   const int t0 = p.at * ROWS, m = min(ROWS, p.rows - t0);  // rows of the tile
@@ -352,18 +353,7 @@ cudaError_t launch_t(const SelectBlocksArgs& a, cudaStream_t s) {
   const int pitch = a.s.maxp * (kStepPage / a.block);
   cudaError_t e = allow_shared<&k_block_select<D, G, F32, ROWS>>(ROWS == 8 ? 8 * 4096 * 4 : kSelectShared);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(sparse_pieces(a.s, ROWS) * a.Hkv * a.splits));
-  cfg.blockDim = dim3(16 * ROWS);
-  cfg.dynamicSmemBytes = (size_t)ROWS * pitch * 4;
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)a.splits;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_block_select<D, G, F32, ROWS>, a, pitch);
+  return launch_step_kernel(k_block_select<D, G, F32, ROWS>, dim3((unsigned)(sparse_pieces(a.s, ROWS) * a.Hkv * a.splits)), 16 * ROWS, (size_t)ROWS * pitch * 4, a.splits, s, a, pitch);
 }
 template <int D, bool F32>
 cudaError_t launch_g(const SelectBlocksArgs& a, cudaStream_t s) {

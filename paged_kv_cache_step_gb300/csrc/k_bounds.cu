@@ -35,6 +35,7 @@ __global__ void __launch_bounds__(NT) k_bounds(const __grid_constant__ BoundsArg
   __shared__ float lo_s[NT * N], hi_s[NT * N];
   const int tid = threadIdx.x, unit = tid / threads, t = tid % threads;
   const int h = blockIdx.y * heads + unit, lb = log2_of(a.block);
+  begin_step();
   const StepPiece p = find_piece(a.s, blockIdx.x, lb, 2);
   if (p.r < 0) return;
   const StepRow first = step_row(a.s, p.r, 0, tid == 0);  // the request's first and last row
@@ -129,8 +130,7 @@ cudaError_t launch_t(const BoundsArgs& a, cudaStream_t s) {
   while (threads < NT && threads * 8 < a.block * PIECES) threads *= 2;
   const int heads = NT / threads;
   const dim3 grid((unsigned)(a.s.max_rows / a.block + 2 * a.s.n), (unsigned)((a.Hkv + heads - 1) / heads));
-  k_bounds<D, F32><<<grid, NT, 0, s>>>(a, threads, heads);
-  return cudaGetLastError();
+  return launch_step_kernel(k_bounds<D, F32>, grid, NT, 0, 1, s, a, threads, heads);
 }
 
 }  // namespace

@@ -15,13 +15,14 @@
 // its rd / 2 angles serve all heads and are formed while the rows are on their way,
 // which start before the row's place is looked up.  Small blocks keep
 // more loads in flight beside the angles of others: 13 621 rows of 32 + 8 heads, d = 128,
-// interleaved, 56 us with 64 threads, 59 with 192, 73 with 256 and 82 with 384 (a row
-// of 16 + 8 heads, d = 64: 24, 37, - and -); 88 % of the copy rate.
+// interleaved, 56 us with 64 threads, 59 with 192, 73 with 256 and 82 with 384, by
+// themselves (a row of 16 + 8 heads, d = 64: 24 and 37 with 64 and 192); among others, their
+// starts overlapped, 52 us, 95 % of the copy rate.
 #include <cuda_bf16.h>
 
 #include <cstdint>
 
-#include "sparse_kernels.h"
+#include "step.cuh"
 
 namespace gp {
 namespace {
@@ -126,6 +127,7 @@ __global__ void __launch_bounds__(NT) k_mapped(const __grid_constant__ MappedArg
     u0 = src[w.p0];
     u1 = src[w.p1];
   };
+  begin_step();
   // the rows are on their way before their place is known
   uint4 u0[AHEAD], u1[AHEAD];
 #pragma unroll
@@ -180,14 +182,9 @@ __global__ void __launch_bounds__(NT) k_mapped(const __grid_constant__ MappedArg
 template <int D>
 cudaError_t launch_d(const MappedArgs& a, cudaStream_t s) {
   const dim3 grid((unsigned)a.rows);
-  if (a.q_f32) {
-    if (a.kv_f32) k_mapped<D, true, true><<<grid, NT, 0, s>>>(a);
-    else k_mapped<D, true, false><<<grid, NT, 0, s>>>(a);
-  } else {
-    if (a.kv_f32) k_mapped<D, false, true><<<grid, NT, 0, s>>>(a);
-    else k_mapped<D, false, false><<<grid, NT, 0, s>>>(a);
-  }
-  return cudaGetLastError();
+  auto launch = [&](auto kernel) { return launch_step_kernel(kernel, grid, NT, 0, 1, s, a); };
+  if (a.q_f32) return a.kv_f32 ? launch(k_mapped<D, true, true>) : launch(k_mapped<D, true, false>);
+  return a.kv_f32 ? launch(k_mapped<D, false, true>) : launch(k_mapped<D, false, false>);
 }
 
 }  // namespace

@@ -14,7 +14,7 @@
 // four keys are summed over the lanes by halves, so that a lane ends with one or two of
 // them and weighs those alone (15 exchanges for 16 logits instead of 64).  All in fp32;
 // one rounding to the query's type at the end.  Six requests of 3 to 5 rows, d = 64, fp32, 24 blocks
-// of 16: 6.8 us in a graph.  64 requests of 2048 listed tokens,
+// of 16: 6.2 us in a graph.  64 requests of 2048 listed tokens,
 // 32 + 8 heads, d = 128, fp32: 240 us, 66 % of the copy rate; with registers for one CTA an SM
 // (147 instead of 128) 402 us: the loads of two hide each other's sums.
 #include <cuda_bf16.h>
@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse(const __grid_constant__ Sparse
   const int C = a.splits, rank = blockIdx.x % C;
   const int64_t unit = blockIdx.x / C;
   const int row = (int)(unit / a.Hkv), h = (int)(unit % a.Hkv);
+  begin_step();
   const StepRow rw = find_row(a.s, row, tid == 0);
   if (!rw.live) return;  // (the whole cluster)
   const int lb = log2_of(a.block), lper = kStepPageLog - lb, own = rw.at >> lb;
@@ -280,17 +281,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse(const __grid_constant__ Sparse
 
 template <int D, int G, bool QF32, bool KF32>
 cudaError_t launch_t(const SparseArgs& a, cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.s.max_rows * a.Hkv * a.splits));
-  cfg.blockDim = dim3(NT);
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)a.splits;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_sparse<D, G, QF32, KF32>, a);
+  return launch_step_kernel(k_sparse<D, G, QF32, KF32>, dim3((unsigned)(a.s.max_rows * a.Hkv * a.splits)), NT, 0, a.splits, s, a);
 }
 template <int D, int G>
 cudaError_t launch_g(const SparseArgs& a, cudaStream_t s) {

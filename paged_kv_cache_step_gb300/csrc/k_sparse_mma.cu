@@ -19,7 +19,7 @@
 // joined in shared memory: no scratch, no second launch, one fixed order.
 //
 // Measured (32 + 8 heads, d = 128, 32 blocks of 64): a decode step of 64 requests 88 us, 89 % of the
-// copy rate (433 us on the CUDA cores); one request with 64 blocks 14.3 us, 8 of them from
+// copy rate (433 us on the CUDA cores); one request with 64 blocks 12.1 us, 8 of them from
 // start to end of a CTA.  A stage takes a CTA alone 1200 clocks, two on an SM 2300: memory.
 #include <cuda_bf16.h>
 
@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
   }
+  begin_step();
   const StepPiece p = find_piece(a.s, unit / a.Hkv, log2_const(T), 1);
   if (p.r < 0 || p.at * T >= p.rows) return;  // (the whole cluster)
   const int t0 = p.at * T, m = min(T, p.rows - t0);
@@ -399,18 +400,7 @@ cudaError_t launch_t(const SparseArgs& a, const SparseMaps& maps, cudaStream_t s
   cudaError_t e = allow_shared<&k_sparse_mma<D, G>>(1024 + Sm<D>::SEEN + 4 * 256 + 4 * (T + 1) * 128 + 8 * 4096);
   if (e != cudaSuccess) return e;
   if (a.splits > 8 && (e = allow_large_clusters<&k_sparse_mma<D, G>>()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(sparse_pieces(a.s, T) * a.Hkv * a.splits));
-  cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)a.splits;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_sparse_mma<D, G>, a, maps, words);
+  return launch_step_kernel(k_sparse_mma<D, G>, dim3((unsigned)(sparse_pieces(a.s, T) * a.Hkv * a.splits)), NT, (size_t)smem, a.splits, s, a, maps, words);
 }
 
 }  // namespace

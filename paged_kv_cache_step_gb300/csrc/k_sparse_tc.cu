@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const int C = a.splits, rank = blockIdx.x % C, item = blockIdx.x / C, h = item % a.Hkv;
 
+  begin_step();
   const StepPiece p = find_piece(a.s, item / a.Hkv, log2_const(T), 1);
   if (p.r < 0 || p.at * T >= p.rows) return;  // (the whole cluster)
   const int t0 = p.at * T, m_rows = min(T, p.rows - t0);
@@ -449,18 +450,7 @@ cudaError_t launch_t(const SparseArgs& a, const SparseMaps& maps, const CUtensor
   const int smem = 1024 + Sm<D>::RING + 4 * 256 + 4 * (T + 1) * words + 2 * most;
   cudaError_t e = allow_shared<&k_sparse_tc<D, G>>(1024 + Sm<D>::RING + 4 * 256 + 4 * (T + 1) * 128 + 2 * 4096);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(sparse_pieces(a.s, T) * a.Hkv * a.splits));
-  cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)a.splits;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_sparse_tc<D, G>, a, maps, qmap, words);
+  return launch_step_kernel(k_sparse_tc<D, G>, dim3((unsigned)(sparse_pieces(a.s, T) * a.Hkv * a.splits)), NT, (size_t)smem, a.splits, s, a, maps, qmap, words);
 }
 
 }  // namespace

@@ -19,9 +19,8 @@
 #include <algorithm>
 #include <cstdint>
 
-#include "chained.cuh"
 #include "shared_limit.cuh"
-#include "sparse_kernels.h"
+#include "step.cuh"
 
 namespace gp {
 namespace {
@@ -68,6 +67,7 @@ __global__ void __launch_bounds__(1024, 1) k_tables(const __grid_constant__ Tabl
   const bool leader = rank == 0;
 
   for (int i = tid; i < 2 * words; i += nt) seen[i] = 0;
+  begin_step();
   __syncthreads();
   for (int r = tid; r < a.n; r += nt) {  // a slot that is listed twice is no one's
     const int s = a.slots[r];
@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(1024, 1) k_tables(const __grid_constant__ Tabl
         req[i] = lo;
         at[i] = cached[lo] + row - row0[lo];
         const int j = at[i] / PAGE;
-        page[i] = j < held[lo] ? __ldg(a.tables + (size_t)slots[lo] * a.maxp + j) : __ldg(a.free_pages + before + first[lo] + j - held[lo]);
-        pos[i] = __ldg(a.pos + lo) + (row - row0[lo]);
+        page[i] = j < held[lo] ? a.tables[(size_t)slots[lo] * a.maxp + j] : a.free_pages[before + first[lo] + j - held[lo]];
+        pos[i] = a.pos[lo] + (row - row0[lo]);
       }
     }
 #pragma unroll
@@ -197,18 +197,8 @@ cudaError_t launch_tables(const TablesArgs& a, cudaStream_t s) {
   cudaError_t e = allow_shared<&k_tables>(sizeof(int) * (5 * kStepMaxRequests + 1 + 2 * kStepMaxSlots / 32));
   if (e != cudaSuccess) return e;
   if (large && (e = allow_large_clusters<&k_tables>()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(small ? 1 : a.apart ? (unsigned)std::min((a.max_rows + 1023) / 1024 + 1, 128) : large ? 16 : 8);
-  cfg.blockDim = dim3(small ? 256 : a.apart ? 512 : 1024);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = a.apart ? 1 : cfg.gridDim.x;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_tables, a);
+  const int blocks = small ? 1 : a.apart ? std::min((a.max_rows + 1023) / 1024 + 1, 128) : large ? 16 : 8;
+  return launch_step_kernel(k_tables, dim3((unsigned)blocks), small ? 256 : a.apart ? 512 : 1024, smem, a.apart ? 1 : blocks, s, a);
 }
 
 }  // namespace gp

@@ -4,7 +4,9 @@
 #pragma once
 
 #include <cstdint>
+#include <utility>
 
+#include "chained.cuh"
 #include "sparse_kernels.h"
 
 namespace gp {
@@ -16,6 +18,32 @@ constexpr int kStepPageLog = 8;
 // size that the compiler does not know is some thirty instructions).
 __host__ __device__ constexpr int log2_const(int n) { return n > 1 ? 1 + log2_const(n / 2) : 0; }
 __device__ __forceinline__ int log2_of(int block) { return 31 - __clz(block); }
+
+// A call's launch.  The calls of a step follow one another on the engine stream with
+// little to do each: the next one's blocks are placed while the last ones of this one
+// still run, and wait on the device for its end before they touch anything (every kernel
+// calls begin_step first; all it reads after that, by ordinary loads or TMA).
+template <typename... P, typename... A>
+cudaError_t launch_step_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+__device__ __forceinline__ void begin_step() {
+  let_next_in();
+  wait_for_previous();
+}
 
 struct StepRow {
   bool live;
