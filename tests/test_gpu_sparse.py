@@ -1190,6 +1190,83 @@ def test_capture_and_side_stream():
         e.close()
 
 
+def test_calls_wait_for_a_long_eviction():
+    """Calls whose launches overlap those before them still wait for the side stream: an
+    eviction of many pages and layers, at once followed by bounds and attention."""
+    stream, side = torch.cuda.Stream(), torch.cuda.Stream()
+    T, keep, L = 60 * PAGE, 40 * PAGE, 24
+    with torch.cuda.stream(stream):
+        e = Engine([T - 1], [1], L=L, layer=L - 1, hq=16, hkv=8, seed=30, cap=60, stream=stream)
+        for layer in range(L):
+            e.layer = layer
+            e.fill()
+        e.block = 64
+        for _ in range(e.pool):
+            gp.gp_page_alloc(e.ctx)
+        [gp.gp_slot_acquire(e.ctx) for _ in range(e.M)]
+        req = gp.Request(int(e.slots[0]), e.tables_host[e.slots[0], :60], T, 60)
+        w = torch.rand(L, e.M, 8, 60 * PAGE, device="cuda", generator=e.gen)
+        q, out = e.randn(1, 16, 128).bfloat16(), torch.zeros(1, 16, 128, dtype=torch.bfloat16, **CUDA)
+        blocks = i32(np.tile(np.arange(0, 640, 5), (1, 8, 1)))
+        gp.gp_set_compaction_stream(e.ctx, side)
+        bounds, scales = bounds_arrays(e, 64)
+        lengths = i32([keep - 1])
+        stream.synchronize()
+        for _ in range(3):  # kernels ahead of the wait, for the launches behind it to overlap
+            gp.gp_sparse_attention(e.ctx, e.layer, e.step, 64, 128, q, blocks, out)
+        gp.gp_evict_weighted(e.ctx, [req], [T], [keep], w)
+        e.arrays["num_cached"].copy_(lengths)
+        gp.gp_block_bounds(e.ctx, e.layer, e.step, 64, bounds, scales)
+        gp.gp_sparse_attention(e.ctx, e.layer, e.step, 64, 128, q, blocks, out)
+        gp.gp_synchronize(e.ctx)
+        e.cached = [keep - 1]
+        check_bounds(e, 64, bounds, scales)
+        want, tol = attention_reference(e, q, [[np.arange(0, 640, 5)] * 8])
+        assert torch.all((out.double() - want).abs() <= tol)
+        e.close()
+
+
+def test_captured_behind_copies_and_other_streams():
+    """In a graph, calls behind a copy, and behind another stream's work that an event joins."""
+    stream, other = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        e = Engine([300], [50], L=1, layer=0, seed=31, stream=stream)
+        e.fill()
+        e.block = 32
+        lists = random_lists(e, 5, 3)
+        blocks = np.full((50, 2, 5), -1)
+        for row, x in enumerate(lists):
+            for h in range(2):
+                blocks[row, h, :len(x[h])] = x[h]
+        blocks = i32(blocks)
+        src, q, half = e.randn(50, 8, 128).bfloat16(), torch.zeros(50, 8, 128, dtype=torch.bfloat16, **CUDA), e.randn(50, 8, 128).bfloat16()
+        out, out2 = torch.zeros_like(q), torch.zeros_like(q)
+        gp.gp_sparse_attention(e.ctx, 0, e.step, 32, 5, q, blocks, out)
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            q.copy_(src)
+            gp.gp_sparse_attention(e.ctx, 0, e.step, 32, 5, q, blocks, out)
+            other.wait_stream(stream)
+            with torch.cuda.stream(other):
+                for _ in range(20):
+                    half.mul_(0.5)
+                    half.mul_(2.0)
+                half.add_(1.0)
+            stream.wait_stream(other)
+            gp.gp_sparse_attention(e.ctx, 0, e.step, 32, 5, half, blocks, out2)
+        base = half.clone()
+        graph.replay()
+        gp.gp_synchronize(e.ctx)
+        want, tol = attention_reference(e, src, lists)
+        assert torch.all((out.double() - want).abs() <= tol)
+        assert torch.equal(half, base + 1.0)
+        want, tol = attention_reference(e, half, lists)
+        assert torch.all((out2.double() - want).abs() <= tol)
+        del graph
+        e.close()
+
+
 def test_kernel_times_are_counted():
     e = Engine([100], [3], L=1, layer=0)
     try:
