@@ -24,9 +24,9 @@
 //
 // Measured (32 + 8 heads, d = 128, blocks of 64, 32 of them): a decode step of 64 requests of
 // 4 to 128 pages 13.5 us in a graph, where reading the bounds takes 4.5: latency; 4001 rows behind
-// 12 007 tokens 64 us, 68 % of the issue slots.  On the way: tiles of 8 rows, keys read from shared
+// 12 007 tokens 57 us, bounded by instruction issue.  On the way: tiles of 8 rows, keys read from shared
 // memory for every bit 141 us; in registers, tiles of 16 80 us; the products' row operand from
-// shared memory, so that three CTAs fit on an SM, 64 us.
+// shared memory, so that three CTAs fit on an SM, 64 us; four, at 64 registers a thread, 57 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -169,7 +169,7 @@ __device__ __forceinline__ void pick_many(const unsigned* key, int from, int to,
 // many warps, each with the bounds of 32 blocks in flight, so that a step's tiles
 // are on the GPU together.
 template <int D, int G, bool F32, int ROWS>
-__global__ void __launch_bounds__(16 * ROWS, ROWS == 8 ? 4 : 3) k_block_select(const __grid_constant__ SelectBlocksArgs a, int pitch) {
+__global__ void __launch_bounds__(16 * ROWS, 4) k_block_select(const __grid_constant__ SelectBlocksArgs a, int pitch) {
   constexpr int NT = 16 * ROWS, NW = NT / 32;
   constexpr int AHEAD = ROWS == 8 ? 2 : 1;  // products of 16 blocks whose bounds are loaded together
   constexpr int QR = ROWS / NW;             // rows of Q a warp
