@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(16 * ROWS, 4) k_block_select(const __grid_cons
       }
     }
   }
-  const StepRow first = step_row(a.s, p.r, t0, tid == 0), last = step_row(a.s, p.r, t0 + m - 1, tid == 0);
+  const StepRow first = step_row(a.s, p.slot, p.cached, t0, tid == 0), last = step_row(a.s, p.slot, p.cached, t0 + m - 1, tid == 0);
   if (!first.live || !last.live) return;
   if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int lb = log2_of(a.block), lper = kStepPageLog - lb;  // blocks of a page

@@ -38,8 +38,8 @@ __global__ void __launch_bounds__(NT) k_bounds(const __grid_constant__ BoundsArg
   begin_step();
   const StepPiece p = find_piece(a.s, blockIdx.x, lb, 2);
   if (p.r < 0) return;
-  const StepRow first = step_row(a.s, p.r, 0, tid == 0);  // the request's first and last row
-  const StepRow last = step_row(a.s, p.r, p.rows - 1, tid == 0);
+  const StepRow first = step_row(a.s, p.slot, p.cached, 0, tid == 0);  // the request's first and last row
+  const StepRow last = step_row(a.s, p.slot, p.cached, p.rows - 1, tid == 0);
   if (!first.live || !last.live) return;
   const int b = (first.at >> lb) + p.at;
   if (b > last.at >> lb) return;

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
   const int t0 = p.at * T, m = min(T, p.rows - t0);
   BlockLists<WARPS + 1, T> lists;
   lists.load(a, (size_t)p.row0 + t0, h, lists.rows_of(m), 0);
-  const StepRow first = step_row(a.s, p.r, t0, tid == 0), last = step_row(a.s, p.r, t0 + m - 1, tid == 0);
+  const StepRow first = step_row(a.s, p.slot, p.cached, t0, tid == 0), last = step_row(a.s, p.slot, p.cached, t0 + m - 1, tid == 0);
   if (!first.live || !last.live) return;
   const size_t row0 = (size_t)p.row0 + t0;
   if (tid == 0) {

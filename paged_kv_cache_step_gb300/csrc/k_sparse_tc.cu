@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   const int t0 = p.at * T, m_rows = min(T, p.rows - t0);
   BlockLists<NT / 32, T> lists;
   lists.load(a, (size_t)p.row0 + t0, h, lists.rows_of(m_rows), 0);
-  const StepRow first = step_row(a.s, p.r, t0, tid == 0), last = step_row(a.s, p.r, t0 + m_rows - 1, tid == 0);
+  const StepRow first = step_row(a.s, p.slot, p.cached, t0, tid == 0), last = step_row(a.s, p.slot, p.cached, t0 + m_rows - 1, tid == 0);
   if (!first.live || !last.live) return;
   const size_t row0 = (size_t)p.row0 + t0;
   const int lb = log2_of(a.block), lper = kStepPageLog - lb;  // blocks of a page

@@ -56,9 +56,8 @@ __device__ __forceinline__ StepRow bad_row(const StepArgs& s, int bit, bool repo
   return {false, 0, 0};
 }
 
-// Row t of request r; `report`: this thread tells of an index outside.
-__device__ __forceinline__ StepRow step_row(const StepArgs& s, int r, int t, bool report) {
-  const int slot = s.slots[r], cached = s.cached[r];
+// Row t of a request; `report`: this thread tells of an index outside.
+__device__ __forceinline__ StepRow step_row(const StepArgs& s, int slot, int cached, int t, bool report) {
   if (slot < 0 || slot >= s.M) return bad_row(s, ERR_BAD_SLOT, report);
   if (t < 0 || cached < 0 || (int64_t)cached + t >= (int64_t)s.maxp * kStepPage) return bad_row(s, ERR_BAD_PAGE, report);
   return {true, slot, cached + t};
@@ -67,7 +66,7 @@ __device__ __forceinline__ StepRow find_row(const StepArgs& s, int row, bool rep
   const int r = s.row_req[row];
   if (r == -1) return {false, 0, 0};
   if (r < 0 || r >= s.n) return bad_row(s, ERR_BAD_SLOT, report);
-  return step_row(s, r, row - s.row0[r], report);
+  return step_row(s, s.slots[r], s.cached[r], row - s.row0[r], report);
 }
 
 // The page of a logical page of `slot`; -1 (and the error bit) if it is none.
@@ -87,20 +86,50 @@ struct StepPiece {
   int at;    // number within the request
   int rows;  // of the request
   int row0;
+  int slot, cached;
 };
 __device__ __forceinline__ StepPiece find_piece(const StepArgs& s, int j, int log, int extra) {
   const int lane = threadIdx.x & 31;
-  int below = 0;  // requests whose first piece is j or before
-  for (int r = lane; r < s.n; r += 32) below += (s.row0[r] >> log) + extra * r <= j;
-  below = __reduce_add_sync(0xffffffffu, below);
-  if (below == 0) return {-1, 0, 0, 0};
   StepPiece p;
-  p.r = below - 1;
-  p.row0 = s.row0[p.r];
-  const int end = s.row0[below];
+  int end;
+  if (s.n <= 64) {  // everything of every request at once: one trip to memory instead of two
+    int v[2][4];
+    unsigned below = 0u;  // requests whose first piece is j or before
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = lane + 32 * i;
+      v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0;
+      if (r < s.n) {
+        v[i][0] = s.row0[r];
+        v[i][1] = s.row0[r + 1];
+        v[i][2] = s.slots[r];
+        v[i][3] = s.cached[r];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      below += __popc(__ballot_sync(0xffffffffu, lane + 32 * i < s.n && (v[i][0] >> log) + extra * (lane + 32 * i) <= j));
+    p.r = (int)below - 1;
+    const bool upper = p.r >= 32;
+    p.row0 = __shfl_sync(0xffffffffu, upper ? v[1][0] : v[0][0], p.r & 31);
+    end = __shfl_sync(0xffffffffu, upper ? v[1][1] : v[0][1], p.r & 31);
+    p.slot = __shfl_sync(0xffffffffu, upper ? v[1][2] : v[0][2], p.r & 31);
+    p.cached = __shfl_sync(0xffffffffu, upper ? v[1][3] : v[0][3], p.r & 31);
+    if (p.r < 0) return {-1, 0, 0, 0, 0, 0};
+  } else {
+    int below = 0;
+    for (int r = lane; r < s.n; r += 32) below += (s.row0[r] >> log) + extra * r <= j;
+    below = __reduce_add_sync(0xffffffffu, below);
+    if (below == 0) return {-1, 0, 0, 0, 0, 0};
+    p.r = below - 1;
+    p.row0 = s.row0[p.r];
+    end = s.row0[below];
+    p.slot = s.slots[p.r];
+    p.cached = s.cached[p.r];
+  }
   p.at = j - ((p.row0 >> log) + extra * p.r);
   p.rows = end - p.row0;
-  if (p.row0 < 0 || end > s.max_rows || p.rows <= 0 || p.at < 0) return {-1, 0, 0, 0};
+  if (p.row0 < 0 || end > s.max_rows || p.rows <= 0 || p.at < 0) return {-1, 0, 0, 0, 0, 0};
   return p;
 }
 

@@ -803,6 +803,23 @@ def test_long_and_many():
             e.close()
 
 
+@pytest.mark.parametrize("n", [63, 64, 65, 97, 300])
+def test_many_requests(n):
+    """At and over the 64 requests that a warp looks at together."""
+    rng = np.random.default_rng(n)
+    e = Engine(rng.integers(0, 500, n).tolist(), rng.integers(0, 6, n).tolist(), L=1, layer=0, hq=4, hkv=2, d=64, pad=3, seed=n)
+    try:
+        e.fill()
+        bounds, scales = bounds_arrays(e, 32)
+        gp.gp_block_bounds(e.ctx, 0, e.step, 32, bounds, scales)
+        gp.gp_synchronize(e.ctx)
+        check_bounds(e, 32, bounds, scales)
+        check_select(e, 32, 6, 1, 2, seed=n)
+        check_attention(e, 32, 6, seed=n)
+    finally:
+        e.close()
+
+
 def test_cache_offsets_beyond_32_bits():
     """Pages at the far end of caches of 4.6e9 elements."""
     e = Engine([700, 300], [20, 1], L=1, layer=0, hq=16, hkv=8, pool=17_600, seed=7)
