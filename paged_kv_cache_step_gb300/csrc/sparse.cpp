@@ -89,8 +89,6 @@ StepArgs step_args(gp_ctx* c, const gp_step* s) {
   a.cached = s->num_cached;
   a.row0 = s->row0;
   a.row_req = s->row_req;
-  a.slot_map = s->slot_map;
-  a.positions = s->positions;
   a.tables = s->tables;
   a.M = c->cfg.max_slots;
   a.maxp = c->cfg.max_pages_per_req;

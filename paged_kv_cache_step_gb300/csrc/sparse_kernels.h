@@ -18,8 +18,6 @@ struct StepArgs {
   const int32_t* cached;     // [n]
   const int32_t* row0;       // [n + 1]
   const int32_t* row_req;    // [max_rows], -1: no row
-  const int64_t* slot_map;   // [max_rows], -1: no row
-  const int64_t* positions;  // [max_rows]
   const int32_t* tables;     // [M][maxp]
   int M, maxp;
   int num_pages_total;

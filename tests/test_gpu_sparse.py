@@ -1243,6 +1243,43 @@ def test_calls_wait_for_a_long_eviction():
         e.close()
 
 
+@pytest.mark.parametrize("kernel", [gp.GP_SCAN_TENSOR_CORE, gp.GP_SCAN_CUDA_CORE])
+def test_calls_behind_chunk_attention(kernel):
+    """Attention whose queries are what chunk attention has just written, and appends to the
+    pages that it has just read, with and without its other kernels in between."""
+    e = Engine([3000], [300], L=1, layer=0, seed=32, cap=13, kernel=kernel)
+    try:
+        e.fill()
+        for _ in range(e.pool):
+            gp.gp_page_alloc(e.ctx)
+        [gp.gp_slot_acquire(e.ctx) for _ in range(e.M)]
+        req = gp.Request(int(e.slots[0]), e.tables_host[e.slots[0], :13], 3300, 13)
+        q = e.randn(300, 8, 128).bfloat16()
+        blocks = i32(np.tile(np.arange(0, 46, 3), (300, 2, 1)))
+        k, v = e.randn(300, 2, 128).bfloat16(), e.randn(300, 2, 128).bfloat16()
+        k0, v0 = e.k.clone(), e.v.clone()
+        rope = gp.gp_rope_default()
+        for weights in (None, torch.zeros(1, e.M, 2, 13 * PAGE, **CUDA)):
+            results = []
+            for sync in (True, False, False):
+                e.k.copy_(k0)
+                e.v.copy_(v0)
+                mid, out = torch.zeros_like(q), torch.zeros_like(q)
+                torch.cuda.synchronize()
+                gp.gp_chunk_attention(e.ctx, 0, [req], [3000], [300], q, mid, weights)
+                if sync:
+                    torch.cuda.synchronize()
+                gp.gp_sparse_attention(e.ctx, 0, e.step, 64, 16, mid, blocks, out)
+                gp.gp_append_mapped(e.ctx, 0, e.step, rope, None, k, v, None)
+                gp.gp_synchronize(e.ctx)
+                results.append((mid, out, e.k.clone(), e.v.clone()))
+            for other in results[1:]:
+                assert all(torch.equal(bits(a), bits(b)) for a, b in zip(results[0], other))
+            assert results[0][1].abs().sum() > 0
+    finally:
+        e.close()
+
+
 def test_captured_behind_copies_and_other_streams():
     """In a graph, calls behind a copy, and behind another stream's work that an event joins."""
     stream, other = torch.cuda.Stream(), torch.cuda.Stream()
