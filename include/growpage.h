@@ -641,7 +641,7 @@ gp_status gp_select_blocks(gp_ctx* ctx, int32_t layer, const gp_step* step, int3
  * the blocks listed for it: z = q . k / sqrt(d), a = softmax(z), out = sum a v.
  * blocks_dev: int32 [max_rows][Hkv][top]; a list is ascending and ends at the first
  * entry that is negative, not above the one before it, or past the row's own
- * block; an empty one gives 0.  q_rot_dev, out_dev: [max_rows][Hq][d] q_dtype,
+ * block; an empty one gives 0, a query with NaN or an infinite logit NaN.  q_rot_dev, out_dev: [max_rows][Hq][d] q_dtype,
  * 16-byte aligned, apart.  Keys and values of the listed blocks, up to the
  * request's last token of the step, must be finite; other cache slots may hold any
  * bits. */

@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse(const __grid_constant__ Sparse
       o = fmaf(of(r, &part[g][d]), f, o);
       sum = fmaf(of(r, &part[g][D + 1]), f, sum);
     }
-    const float y = sum > 0.f ? o / sum : 0.f;
+    const float y = sum == 0.f ? 0.f : o / sum;  // (an empty list; NaN stays NaN)
     const size_t at = ((size_t)row * a.Hq + h * G + g) * D + d;
     if (QF32) static_cast<float*>(a.out)[at] = y;
     else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);

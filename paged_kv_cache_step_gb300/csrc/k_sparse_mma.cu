@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
       y1 = fmaf(of(c, at + d + 1), f, y1);
       sum = fmaf(of(c, at + D + 1), f, sum);
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + ((row0 + r / G) * a.Hq + h * G + r % G) * D + d) =
         pack2(y0 * inv, y1 * inv);
   }

@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
     if (ok) ok = __all_sync(0xffffffffu, wait_phase(mma_done, 0u, abort));  // (o_done may be two stages behind)
     if (ok) {
       tc_fence_after();
-      const float inv = C > 1 ? 1.f : l > 0.f ? 1.f / l : 0.f;
+      const float inv = C > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         uint32_t o[32];
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) y[i] = y[i] * f + v[i] * g;
       }
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
       uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + ((row0 + x / G) * a.Hq + h * G + x % G) * D) +
                       lane * (D / 64);
 #pragma unroll
