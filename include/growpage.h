@@ -487,13 +487,17 @@ gp_status gp_evict_weighted(gp_ctx* ctx, int32_t n, gp_request* reqs, const int3
  * They share these rules.  Addresses, sizes and options are checked before
  * anything happens (GP_ERR_INVALID, nothing changed); the device current at
  * gp_create must be current (GP_ERR_INVALID).  What the device arrays hold is
- * checked by the kernels: a row whose request, slot, length or place is outside
- * the engine's sizes is left out (its outputs stay as they were), a page of a
- * table that is outside the pool counts for nothing (to gp_select_blocks: for any
- * page), and both are reported by the next synchronising call as GP_ERR_INVALID.  Block sizes are
- * 16, 32, 64, 128 or 256 tokens.  Rows behind the step's last one
- * (row_req and slot_map of -1) are left as they were.  max_rows times the KV heads
- * is below 2^27 (GP_ERR_UNSUPPORTED).  gp_set_timing does not time captured launches.
+ * checked by the kernels.  A row whose request, slot or place is outside the
+ * engine's sizes is left out: its outputs stay as they were, the other rows of its
+ * request take part.  To gp_append_mapped that is a slot_map outside the pool; to the
+ * last three calls a row takes part if row_req names its request and row0 agrees,
+ * row0[r] <= row < row0[r + 1], and if its own token has a place in the table.  A page
+ * of a table that is outside the pool counts for nothing (to gp_select_blocks: for any
+ * page).  Both are reported by the next synchronising call as GP_ERR_INVALID.  Rows
+ * whose row_req (slot_map) is -1 and those behind the step's last one, from row0[n] on, are
+ * left as they were without a report.  row0 must ascend; where it does not, which
+ * rows take part is not defined.  Block sizes are 16, 32, 64, 128 or 256 tokens.
+ * max_rows times the KV heads is below 2^27 (GP_ERR_UNSUPPORTED).  gp_set_timing does not time captured launches.
  * All run on the engine stream, asynchronously.  Those that read or write K/V
  * (gp_append_mapped, gp_block_bounds, gp_sparse_attention) wait there for a
  * compaction pending on the side stream, whatever its pages; a call that is

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(16 * ROWS, 4) k_block_select(const __grid_cons
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = a.splits, rank = blockIdx.x % C, item = blockIdx.x / C, h = item % a.Hkv;
   begin_step();
-  const StepPiece p = find_piece(a.s, item / a.Hkv, log2_const(ROWS), 1);
+  const StepPiece p = find_piece(a.s, item / a.Hkv, log2_const(ROWS), 1, tid == 0);
   if (p.r < 0 || p.at * ROWS >= p.rows) return;  // (the whole cluster)
   const int t0 = p.at * ROWS, m = min(ROWS, p.rows - t0);  // rows of the tile
   const size_t row0 = (size_t)p.row0 + t0;
@@ -188,9 +188,11 @@ __global__ void __launch_bounds__(16 * ROWS, 4) k_block_select(const __grid_cons
   // the rows' queries, a warp a row: loaded while their places are looked up
   constexpr int E = D / 32;  // dimensions of a lane
   float q[QR][G][E];
+  int named[QR];
 #pragma unroll
   for (int i = 0; i < QR; ++i) {
     const int x = warp + NW * i;
+    named[i] = x < m ? a.s.row_req[row0 + x] : -1;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const size_t at = ((row0 + x) * a.Hq + h * G + g) * D + E * lane;
@@ -215,12 +217,11 @@ __global__ void __launch_bounds__(16 * ROWS, 4) k_block_select(const __grid_cons
       }
     }
   }
-  const StepRow first = step_row(a.s, p.slot, p.cached, t0, tid == 0), last = step_row(a.s, p.slot, p.cached, t0 + m - 1, tid == 0);
-  if (!first.live || !last.live) return;
+  const int first = p.cached + t0, last = first + m - 1;  // the rows' slots
   if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int lb = log2_of(a.block), lper = kStepPageLog - lb;  // blocks of a page
-  const int some = max(0, (last.at >> lb) + 1 - a.recent);    // blocks that a row may have to choose from
-  for (int i = tid; i << lper < some; i += NT) pages[i] = max(step_page(a.s, first.slot, i), 0);
+  const int some = max(0, (last >> lb) + 1 - a.recent);    // blocks that a row may have to choose from
+  for (int i = tid; i << lper < some; i += NT) pages[i] = max(step_page(a.s, p.slot, i), 0);
 
 #pragma unroll
   for (int i = 0; i < QR; ++i) {
@@ -329,8 +330,13 @@ __global__ void __launch_bounds__(16 * ROWS, 4) k_block_select(const __grid_cons
   } else {
     __syncthreads();
   }
-  for (int x = warp; x < m; x += NW) {
-    const int end = ((first.at + x) >> lb) + 1;  // blocks that the row sees
+  unsigned live = 0u;
+#pragma unroll
+  for (int i = 0; i < QR; ++i) live |= (unsigned)row_named(a.s, named[i], p.r) << i;
+#pragma unroll 1
+  for (int i = 0; i < QR; ++i) {
+    if (!(live >> i & 1u)) continue;
+    const int x = warp + NW * i, end = ((first + x) >> lb) + 1;  // blocks that the row sees
     int32_t* out = a.blocks + ((row0 + x) * a.Hkv + h) * a.top;
     const unsigned* keys = scores + (size_t)x * pitch;
     const int to_b = end - a.recent, n = to_b - a.sink, want = a.top - a.sink - a.recent;

@@ -36,17 +36,17 @@ __global__ void __launch_bounds__(NT) k_bounds(const __grid_constant__ BoundsArg
   const int tid = threadIdx.x, unit = tid / threads, t = tid % threads;
   const int h = blockIdx.y * heads + unit, lb = log2_of(a.block);
   begin_step();
-  const StepPiece p = find_piece(a.s, blockIdx.x, lb, 2);
+  const StepPiece p = find_piece(a.s, blockIdx.x, lb, 2, tid == 0);
   if (p.r < 0) return;
-  const StepRow first = step_row(a.s, p.slot, p.cached, 0, tid == 0);  // the request's first and last row
-  const StepRow last = step_row(a.s, p.slot, p.cached, p.rows - 1, tid == 0);
-  if (!first.live || !last.live) return;
-  const int b = (first.at >> lb) + p.at;
-  if (b > last.at >> lb) return;
-  const int page = step_page(a.s, first.slot, b >> (kStepPageLog - lb));
+  const int last = p.cached + p.rows - 1;  // the request's last slot
+  const int b = (p.cached >> lb) + p.at;
+  if (b > last >> lb) return;
+  const int t0 = max((b << lb) - p.cached, 0), rows = min(((b + 1) << lb) - p.cached, p.rows) - t0;  // of the block, up to NT
+  const int named = tid < rows ? a.s.row_req[p.row0 + t0 + tid] : -1;
+  const int page = step_page(a.s, p.slot, b >> (kStepPageLog - lb));
   if (page < 0) return;
   const bool mine = h < a.Hkv;
-  const int per = kStepPage >> lb, sub = b & (per - 1), tokens = min(a.block, last.at + 1 - (b << lb));
+  const int per = kStepPage >> lb, sub = b & (per - 1), tokens = min(a.block, last + 1 - (b << lb));
   const size_t head = ((size_t)a.layer * a.s.num_pages_total + page) * a.Hkv + h;
   float lo[N], hi[N];
 #pragma unroll
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(NT) k_bounds(const __grid_constant__ BoundsArg
     lo_s[i * NT + tid] = lo[i];
     hi_s[i * NT + tid] = hi[i];
   }
-  __syncthreads();
+  if (!__syncthreads_or(row_named(a.s, named, p.r))) return;  // no row falls into the block
   constexpr int FIRST = PIECES < 32 ? 32 : PIECES;  // threads of a unit that end with a piece
   const bool ends = t < FIRST && t < PIECES;
   float top = 0.f;

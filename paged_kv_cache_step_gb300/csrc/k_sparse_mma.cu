@@ -103,14 +103,14 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
   }
   begin_step();
-  const StepPiece p = find_piece(a.s, unit / a.Hkv, log2_const(T), 1);
+  const StepPiece p = find_piece(a.s, unit / a.Hkv, log2_const(T), 1, tid == 0);
   if (p.r < 0 || p.at * T >= p.rows) return;  // (the whole cluster)
   const int t0 = p.at * T, m = min(T, p.rows - t0);
   BlockLists<WARPS + 1, T> lists;
   lists.load(a, (size_t)p.row0 + t0, h, lists.rows_of(m), 0);
-  const StepRow first = step_row(a.s, p.slot, p.cached, t0, tid == 0), last = step_row(a.s, p.slot, p.cached, t0 + m - 1, tid == 0);
-  if (!first.live || !last.live) return;
+  const int first_at = p.cached + t0, last_at = first_at + m - 1;  // the rows' slots
   const size_t row0 = (size_t)p.row0 + t0;
+  const int named = lane < m ? a.s.row_req[row0 + lane] : -1;
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(full(i), 1);
@@ -120,12 +120,14 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
     abort_s = 0;
   }
   for (int i = tid; i < (T + 1) * words; i += NT) any_s[i] = 0u;
-  for (int i = tid; i <= last.at / kStepPage; i += NT) {
-    const int page = a.s.tables[(size_t)first.slot * a.s.maxp + i];
+  for (int i = tid; i <= last_at / kStepPage; i += NT) {
+    const int page = a.s.tables[(size_t)p.slot * a.s.maxp + i];
     pages[i] = page >= 0 && page < a.s.num_pages_total
                    ? (int)((((size_t)a.layer * a.s.num_pages_total + page) * a.Hkv + h) * kStepPage) : -1;
   }
   __syncthreads();
+  const unsigned live = __ballot_sync(0xffffffffu, row_named(a.s, named, p.r));  // the same in every warp
+  if (!live) return;  // (the whole cluster)
   const int lb = log2_of(a.block), lper = kStepPageLog - lb;  // blocks of a page
   // this lane's rows of Q: (row / G)-th of the piece, head row % G
   uint32_t q[D / 16][4];
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
         const int b = lists.b[0];
         int last = __shfl_up_sync(0xffffffffu, b, 1);
         if (lane == 0) last = before;
-        const unsigned ends = __ballot_sync(0xffffffffu, b < 0 || b <= last || b > first.at >> lb);
+        const unsigned ends = __ballot_sync(0xffffffffu, b < 0 || b <= last || b > first_at >> lb);
         const int some = ends ? __ffs(ends) - 1 : 32;
         if (lane < some) list[n + lane].y = b;
         n += some;
@@ -162,7 +164,10 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
       if (lane == 0) total_s = n;
     }
   } else {
-    lists.mark(a, row0, h, m, first.at, lb, words, seen, any_s);
+    unsigned mine = 0u;
+#pragma unroll
+    for (int i = 0; i < lists.N; ++i) mine |= (live >> (warp + i * (WARPS + 1)) & 1u) << i;
+    lists.mark(a, row0, h, mine, first_at, lb, words, seen, any_s);
     __syncthreads();
     const int n = list_blocks<WARPS + 1>(any_s, words, [&](int e, int b) { list[e].y = b; });  // in order
     if (tid == 0) total_s = n;
@@ -187,7 +192,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
   const int lx = min(lb, 6), box = 1 << lx, boxes = KEYS >> lx, lof = lb - lx;  // a box, of a stage, log2 of those of a block
   int all = n << lof;                                                          // boxes of the share
   // without those of the last block past the rows
-  while (all > 0 && ((list[(all - 1) >> lof].y & 0xffff) << lb) + (((all - 1) & ((1 << lof) - 1)) << lx) > last.at) --all;
+  while (all > 0 && ((list[(all - 1) >> lof].y & 0xffff) << lb) + (((all - 1) & ((1 << lof) - 1)) << lx) > last_at) --all;
   const int stages = (all + boxes - 1) >> (6 - lx);
   bool ok = true;
   float o[D / 8][4];
@@ -238,9 +243,9 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
         const uint32_t kt = sb + (uint32_t)(slot * 2 * L::TILE), vt = kt + (uint32_t)L::TILE;
         // logical slot of the warp's first key
         const int base = ((y & 0xffff) << lb) + ((e & ((1 << lof) - 1)) << lx) + (16 * warp & (box - 1));
-        if (base + 15 > last.at) {  // slots past the piece's last row may hold any bits
+        if (base + 15 > last_at) {  // slots past the piece's last row may hold any bits
           const int key = lane >> 1;
-          if (base + key > last.at) {
+          if (base + key > last_at) {
 #pragma unroll
             for (int d = 0; d < D / 64; ++d)
 #pragma unroll
@@ -266,7 +271,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
         for (int i = 0; i < 2; ++i) {
           const int x = ((lane >> 2) + 8 * i) / G;  // row of the piece
           // the last of the 16 keys that it sees
-          const int lim = (y >> (16 + x) & 1) ? first.at + x - base : -1;
+          const int lim = (y >> (16 + x) & 1) ? first_at + x - base : -1;
           float top = mx[i];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -375,6 +380,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
   };
   for (int x = 2 * (rank * NT + tid); x < rows * D; x += 2 * C * NT) {
     const int r = x / D, d = x % D;
+    if (!(live >> (r / G) & 1u)) continue;
     const float* at = part + r * (D + 2);
     float top = NEG, y0 = 0.f, y1 = 0.f, sum = 0.f;
     for (int c = 0; c < C; ++c) top = fmaxf(top, of(c, at + D));

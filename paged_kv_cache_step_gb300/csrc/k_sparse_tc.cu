@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   __shared__ int abort_s, bad_s;
   __shared__ uint32_t tmem_s;
   __shared__ float2 ml_s[128];  // a row's maximum and sum
+  __shared__ bool live_s[T];    // the row takes part
   volatile int* abort = &abort_s;
   const uint32_t bar0 = static_cast<uint32_t>(__cvta_generic_to_shared(bars));
   auto full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
@@ -88,14 +89,14 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   const int C = a.splits, rank = blockIdx.x % C, item = blockIdx.x / C, h = item % a.Hkv;
 
   begin_step();
-  const StepPiece p = find_piece(a.s, item / a.Hkv, log2_const(T), 1);
+  const StepPiece p = find_piece(a.s, item / a.Hkv, log2_const(T), 1, tid == 0);
   if (p.r < 0 || p.at * T >= p.rows) return;  // (the whole cluster)
   const int t0 = p.at * T, m_rows = min(T, p.rows - t0);
   BlockLists<NT / 32, T> lists;
   lists.load(a, (size_t)p.row0 + t0, h, lists.rows_of(m_rows), 0);
-  const StepRow first = step_row(a.s, p.slot, p.cached, t0, tid == 0), last = step_row(a.s, p.slot, p.cached, t0 + m_rows - 1, tid == 0);
-  if (!first.live || !last.live) return;
+  const int first_at = p.cached + t0, last_at = first_at + m_rows - 1;  // the rows' slots
   const size_t row0 = (size_t)p.row0 + t0;
+  const int named = tid < m_rows ? a.s.row_req[row0 + tid] : -1;
   const int lb = log2_of(a.block), lper = kStepPageLog - lb;  // blocks of a page
 
   if (tid == 0) {
@@ -117,21 +118,24 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   for (int i = tid; i < (T + 1) * words; i += NT) any_s[i] = 0u;
-  for (int i = tid; i <= last.at / kStepPage; i += NT) {
-    const int page = a.s.tables[(size_t)first.slot * a.s.maxp + i];
+  for (int i = tid; i <= last_at / kStepPage; i += NT) {
+    const int page = a.s.tables[(size_t)p.slot * a.s.maxp + i];
     pages[i] = page >= 0 && page < a.s.num_pages_total
                    ? (int)((((size_t)a.layer * a.s.num_pages_total + page) * a.Hkv + h) * kStepPage) : -1;
   }
+  if (tid < T) live_s[tid] = row_named(a.s, named, p.r);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)tmem_s);
-  for (int i = tid; i <= last.at / kStepPage; i += NT)
+  for (int i = tid; i <= last_at / kStepPage; i += NT)
     if (pages[i] < 0) bad_s = 1;
   const uint32_t ts = tmem + D, to = tmem;  // columns: O, S and P of even and of odd stages
-  lists.mark(a, row0, h, m_rows, first.at, lb, words, seen, any_s);
-  const int tok = tid / G, sees = first.at + tok;  // of softmax threads
-  const bool valid = warp < 4 && tok < m_rows;
+  const int owned = warp + lane * (NT / 32);  // row `lane` of this warp's lists
+  lists.mark(a, row0, h, __ballot_sync(0xffffffffu, lane < lists.N && owned < T && live_s[min(owned, T - 1)]), first_at, lb, words,
+             seen, any_s);
+  const int tok = tid / G, sees = first_at + tok;  // of softmax threads
+  const bool valid = warp < 4 && live_s[min(tok, T - 1)];
   const size_t at = ((row0 + tok) * a.Hq + h * G + tid % G) * D;
   const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
   __syncthreads();
@@ -157,7 +161,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   list += from;
   // first logical slot of box e
   auto slot_of = [&](int e) { return ((int)list[e >> lof] << lb) + ((e & ((1 << lof) - 1)) << lx); };
-  while (all > 0 && slot_of(all - 1) > last.at) --all;  // boxes of the last block past the rows
+  while (all > 0 && slot_of(all - 1) > last_at) --all;  // boxes of the last block past the rows
   all = uniform(all);
   const int stages = (all + boxes - 1) >> (6 - lx);
   bool ok = true;
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
       bool in[4];
       const bool tail = s + 1 == stages;
       const int end = min(s * boxes + boxes, all);  // past the stage's last box
-      const bool partly = tail || slot_of(end - 1) + box - 1 > first.at;
+      const bool partly = tail || slot_of(end - 1) + box - 1 > first_at;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int e = s * boxes + (16 * i >> lx);
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
         ok = __all_sync(0xffffffffu, wait_phase(full(slot), (uint32_t)((c / NST) & 1), abort));
         if (!ok) break;
         const int e = s * boxes + (key >> lx);
-        if (e >= all || slot_of(e) + (key & (box - 1)) > last.at) {
+        if (e >= all || slot_of(e) + (key & (box - 1)) > last_at) {
           unsigned char* v = sm + (size_t)slot * L::TILE + (size_t)key * 128 + (tid & 1) * 64;
 #pragma unroll
           for (int d = 0; d < D / 64; ++d)
@@ -409,6 +413,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
       return y;
     };
     for (int x = rank + C * warp; x < m_rows * G; x += C * (NT / 32)) {
+      if (!live_s[x / G]) continue;
       float top = NEG, sum = 0.f, y[D / 32];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) y[i] = 0.f;

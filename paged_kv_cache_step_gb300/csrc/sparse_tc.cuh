@@ -46,16 +46,18 @@ struct BlockLists {
       if ((int)(threadIdx.x >> 5) + i * WARPS < m) live |= 1u << i;
     return live;
   }
-  // Sets the bits of the listed blocks, a row's in seen[x * words] and all of them in
-  // any (both cleared before).  A list counts up to its first entry that is negative,
+  // Sets the bits of the blocks that this warp's `live` rows list, a row's in seen[x * words]
+  // and all of them in any (both cleared before).  A list counts up to its first entry that is negative,
   // not above the one before it or past the row's own block.
-  __device__ __forceinline__ void mark(const SparseArgs& a, size_t row0, int h, int m, int first_at, int lb, int words,
+  __device__ __forceinline__ void mark(const SparseArgs& a, size_t row0, int h, unsigned live, int first_at, int lb, int words,
                                        unsigned* seen, unsigned* any) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int before[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) before[i] = -1;
-    unsigned live = rows_of(m);
+    for (int i = 0; i < N; ++i) {
+      before[i] = -1;
+      if (!(live >> i & 1u)) b[i] = -1;
+    }
     for (int k0 = 0; live; load(a, row0, h, live, k0)) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {

@@ -45,28 +45,47 @@ __device__ __forceinline__ void begin_step() {
   wait_for_previous();
 }
 
+// One rule for the rows of every kernel: row i is request r's if row_req[i] names r and row0
+// has it there, row0[r] <= i < row0[r + 1].  It takes part if r's slot is the engine's and
+// its own place, cached + i - row0[r], is in the tables; if not, it alone is left out and
+// an error bit set.  Rows that row_req gives to none, or behind row0[n], are left out as they are.
+__device__ __forceinline__ bool row_named(const StepArgs& s, int named, int r) {
+  if (named != r && named != -1) atomicOr(s.err, ERR_BAD_SLOT);
+  return named == r;
+}
+// How many of the request's rows [row0, end) take part: the first ones.
+__device__ __forceinline__ int rows_placed(const StepArgs& s, int row0, int end, int slot, int cached, bool report) {
+  int bad = 0, rows = 0;
+  if (row0 < 0 || end < row0 || end > s.max_rows) {
+    bad = ERR_BAD_SLOT;
+  } else if (end > row0) {
+    const int room = cached < 0 ? 0 : max(s.maxp * kStepPage - cached, 0);
+    rows = slot < 0 || slot >= s.M ? 0 : min(end - row0, room);
+    bad = slot < 0 || slot >= s.M ? ERR_BAD_SLOT : rows < end - row0 ? ERR_BAD_PAGE : 0;
+  }
+  if (bad && report) atomicOr(s.err, bad);
+  return rows;
+}
+
+// A single row: its request's slot and its logical slot there (it sees the slots [0, at]).
 struct StepRow {
   bool live;
-  int slot;  // of the request
-  int at;    // logical slot of the row: it sees the slots [0, at]
+  int slot;
+  int at;
 };
-
-__device__ __forceinline__ StepRow bad_row(const StepArgs& s, int bit, bool report) {
-  if (report) atomicOr(s.err, bit);
-  return {false, 0, 0};
-}
-
-// Row t of a request; `report`: this thread tells of an index outside.
-__device__ __forceinline__ StepRow step_row(const StepArgs& s, int slot, int cached, int t, bool report) {
-  if (slot < 0 || slot >= s.M) return bad_row(s, ERR_BAD_SLOT, report);
-  if (t < 0 || cached < 0 || (int64_t)cached + t >= (int64_t)s.maxp * kStepPage) return bad_row(s, ERR_BAD_PAGE, report);
-  return {true, slot, cached + t};
-}
 __device__ __forceinline__ StepRow find_row(const StepArgs& s, int row, bool report) {
-  const int r = s.row_req[row];
-  if (r == -1) return {false, 0, 0};
-  if (r < 0 || r >= s.n) return bad_row(s, ERR_BAD_SLOT, report);
-  return step_row(s, s.slots[r], s.cached[r], row - s.row0[r], report);
+  const int r = s.row_req[row], rows = s.row0[s.n];
+  if (r == -1 || row >= rows) return {false, 0, 0};
+  if (r < 0 || r >= s.n) {
+    if (report) atomicOr(s.err, ERR_BAD_SLOT);
+    return {false, 0, 0};
+  }
+  const int row0 = s.row0[r], end = s.row0[r + 1], slot = s.slots[r], cached = s.cached[r];
+  if (row < row0 || row >= end) {
+    if (report) atomicOr(s.err, ERR_BAD_SLOT);
+    return {false, 0, 0};
+  }
+  return {row - row0 < rows_placed(s, row0, end, slot, cached, report), slot, cached + (row - row0)};
 }
 
 // The page of a logical page of `slot`; -1 (and the error bit) if it is none.
@@ -80,15 +99,16 @@ __device__ __forceinline__ int step_page(const StepArgs& s, int slot, int logica
 // Pieces of 2^log rows of each request, numbered over all of them: request r's
 // are base(r), base(r) + 1, ... with base(r) = (row0[r] >> log) + extra r, so that
 // the launch can be sized without the lengths (at most (max_rows >> log) + extra n
-// pieces; those that no row falls into are left at once).  A whole warp calls it.
+// pieces; those that no row falls into are left at once).  A whole warp calls it;
+// `report`: this thread tells of rows that cannot take part.
 struct StepPiece {
   int r;     // -1: none
   int at;    // number within the request
-  int rows;  // of the request
+  int rows;  // of the request, that take part
   int row0;
   int slot, cached;
 };
-__device__ __forceinline__ StepPiece find_piece(const StepArgs& s, int j, int log, int extra) {
+__device__ __forceinline__ StepPiece find_piece(const StepArgs& s, int j, int log, int extra, bool report) {
   const int lane = threadIdx.x & 31;
   StepPiece p;
   int end;
@@ -128,8 +148,8 @@ __device__ __forceinline__ StepPiece find_piece(const StepArgs& s, int j, int lo
     p.cached = s.cached[p.r];
   }
   p.at = j - ((p.row0 >> log) + extra * p.r);
-  p.rows = end - p.row0;
-  if (p.row0 < 0 || end > s.max_rows || p.rows <= 0 || p.at < 0) return {-1, 0, 0, 0, 0, 0};
+  p.rows = rows_placed(s, p.row0, end, p.slot, p.cached, report);
+  if (p.rows == 0 || p.at < 0) return {-1, 0, 0, 0, 0, 0};
   return p;
 }
 

@@ -1,5 +1,5 @@
 """What earlier tests of the calls over a step's device arrays do not show: not-a-number
-queries, in every kernel."""
+queries, and one rule for the rows that are left out, in every kernel."""
 
 import math
 
@@ -8,7 +8,8 @@ import pytest
 import torch
 
 import paged_kv_cache_step_gb300 as gp
-from test_gpu_sparse import DT, SHAPES, Engine, attention_reference, i32, kernels
+from test_gpu_sparse import CUDA, DT, PAGE, SHAPES, Engine, attention_reference, bounds_arrays, bounds_reference, i32, kernels, \
+    random_lists, select_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -55,5 +56,116 @@ def test_a_query_that_is_not_a_number_gives_none(shape, new):
                 gp.gp_sparse_attention(e.ctx, e.layer, e.step, 64, 40, q, blocks, out)
                 gp.gp_synchronize(e.ctx)
                 assert out[0, 0].isnan().all()
+            finally:
+                e.close()
+
+
+def told(e, reported):
+    """The next call that synchronises reports bad device data, or nothing."""
+    if reported:
+        with pytest.raises(gp.GrowPageError) as err:
+            gp.gp_synchronize(e.ctx)
+        assert err.value.status == gp.GP_ERR_INVALID
+    gp.gp_synchronize(e.ctx)
+
+
+def check_rows(e, dead, reported, spoil):
+    """Bounds, selected blocks and attention of a spoiled step: rows of `dead` are left
+    out, every other is right, and each call is reported by itself."""
+    block, per, layer = 64, PAGE // 64, e.layer
+    e.block = block
+    live = [i for i in range(e.rows) if i not in dead]
+    rest = [i for i in range(e.max_rows) if i not in live]
+    lists = random_lists(e, 6, 1)
+    q, blocks = e.randn(e.max_rows, e.hq, e.d).to(DT[e.qt]), np.full((e.max_rows, e.hkv, 6), -1)
+    blocks[e.rows:] = np.arange(6)
+    for row, x in enumerate(lists):
+        for h in range(e.hkv):
+            blocks[row, h, :len(x[h])] = x[h]
+    rng = np.random.default_rng(2)
+    shape = (e.L, e.pool, e.hkv, per)
+    held = np.sort(rng.integers(-127, 128, (*shape, 2, e.d)), -2)
+    scales = 2.0 ** rng.integers(-6, 3, shape)
+    want, tol = attention_reference(e, q, lists)
+    chosen = select_reference(e, q, held, scales, block, 5, 1, 2)
+    want_b, want_s = bounds_arrays(e, block)
+    for r in range(len(e.new)):
+        mine = [t for t in range(e.new[r]) if e.row0[r] + t in live]
+        rows = e.rows_of(e.k, r, e.cached[r] + e.new[r])
+        for b in {(e.cached[r] + t) // block for t in mine}:
+            x = bounds_reference(rows[b * block:(b + 1) * block])
+            page = int(e.tables_host[e.slots[r], b // per])
+            want_b[layer, page, :, b % per] = torch.as_tensor(x[0].astype(np.int8), **CUDA)
+            want_s[layer, page, :, b % per] = torch.as_tensor(x[1], **CUDA).float()
+    spoil(e)
+    got_b, got_s = bounds_arrays(e, block)
+    gp.gp_block_bounds(e.ctx, layer, e.step, block, got_b, got_s)
+    told(e, reported)
+    assert torch.equal(got_b, want_b) and torch.equal(got_s, want_s)
+    got = torch.full((e.max_rows, e.hkv, 5), -5, dtype=torch.int32, **CUDA)
+    gp.gp_select_blocks(e.ctx, layer, e.step, block, 5, 1, 2, q, torch.as_tensor(held.astype(np.int8), **CUDA),
+                        torch.as_tensor(scales.astype(np.float32), **CUDA), got)
+    told(e, reported)
+    assert np.array_equal(got[live].cpu().numpy(), chosen[live]) and (got[rest] == -5).all()
+    out = torch.full((e.max_rows, e.hq, e.d), 7.0, dtype=DT[e.qt], **CUDA)
+    gp.gp_sparse_attention(e.ctx, layer, e.step, block, 6, q, i32(blocks), out)
+    told(e, reported)
+    assert torch.all((out[live].double() - want[live]).abs() <= tol[live]) and (out[rest] == 7.0).all()
+
+
+def put(name, at, value):
+    return lambda e: e.arrays[name].__setitem__(at, value)
+
+
+# three requests of `new` rows each, the second of which, or its second row, is spoiled:
+# what is spoiled, how, which rows are left out, whether that is reported
+SPOILED = [("row_req", "row", -1, "row", False), ("row_req", "row", 3, "row", True), ("row_req", "row", -2, "row", True),
+           ("row_req", "row", 2 ** 31 - 1, "row", True), ("row_req", "row", 0, "row", True), ("row_req", "row", 2, "row", True),
+           ("slots", 1, -1, "request", True), ("slots", 1, 6, "request", True), ("num_cached", 1, -400, "request", True),
+           ("num_cached", 1, 2 ** 31 - 1, "request", True), ("row0", 3, 2 ** 31 - 1, "last", True)]
+
+
+@pytest.mark.parametrize("new", [2, 50])
+@pytest.mark.parametrize("shape", ["bf16_g4_d128", "bf16_g2_d64", "f32_g2_d64"])
+@pytest.mark.parametrize("name,at,value,dead,reported", SPOILED)
+def test_rows_that_are_left_out(name, at, value, dead, reported, shape, new):
+    """The same rows in the bounds, the selection and each attention kernel."""
+    for kernel in kernels(shape):
+        e = Engine([700, 300, 40], [new] * 3, pad=2, seed=new, kernel=kernel, **SHAPES[shape])
+        try:
+            e.fill()
+            rows = {"row": [new + 1], "request": range(new, 2 * new), "last": range(2 * new, 3 * new)}[dead]
+            check_rows(e, rows, reported, put(name, new + 1 if at == "row" else at, value))
+        finally:
+            e.close()
+
+
+@pytest.mark.parametrize("fit,past", [(1, 1), (1, 2), (3, 1), (40, 30), (64, 1), (63, 65), (129, 3)])
+@pytest.mark.parametrize("shape", ["bf16_g4_d128", "bf16_g2_d64", "f32_g2_d64"])
+def test_rows_past_the_end_of_the_table(shape, fit, past):
+    """A request whose first `fit` rows have a place in its table and whose last `past` have
+    none: those alone are left out, and reported."""
+    def spoil(e):
+        e.arrays["row0"][2] = 5 + fit + past
+        e.arrays["row_req"][5 + fit:5 + fit + past] = 1
+
+    for kernel in kernels(shape):
+        e = Engine([300, 4 * PAGE - fit], [5, fit], pad=past + 2, cap=4, seed=fit, kernel=kernel, **SHAPES[shape])
+        try:
+            e.fill()
+            check_rows(e, (), True, spoil)
+        finally:
+            e.close()
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_rows_behind_the_last_are_not_looked_at(new):
+    """Whatever row_req holds there, in every kernel."""
+    for kernel in (gp.GP_SCAN_TENSOR_CORE, gp.GP_SCAN_CUDA_CORE):
+        for value in (0, 1, 2, -5):
+            e = Engine([300, 70], [new, new], pad=20, seed=4, kernel=kernel)
+            try:
+                e.fill()
+                check_rows(e, (), False, put("row_req", slice(2 * new, None), value))
             finally:
                 e.close()
