@@ -722,12 +722,14 @@ gp_status gp_debug_attention_plan(gp_ctx* ctx, int32_t n, const int32_t* num_tok
  * gp_debug_set_wait_limit: the limit, in SM clock cycles, of the bounded copy
  * waits of later launches of `kernel` (GP_KERNEL_COMPRESS: the compaction;
  * GP_KERNEL_SELECT: the speculative selection; GP_KERNEL_EVICT: the eviction's
- * waits for rows still to be read; GP_KERNEL_CHUNK, GP_KERNEL_WEIGHTS: the
- * waits inside the tensor-core chunk attention and its weights); 0 makes each
- * such wait give up at once (of the last two, those for a free buffer), a
+ * waits for rows still to be read; GP_KERNEL_CHUNK, GP_KERNEL_WEIGHTS,
+ * GP_KERNEL_SPARSE: the waits inside the tensor-core chunk attention, its weights and
+ * the tensor-core kernels of gp_sparse_attention); 0 makes each
+ * such wait give up at once (of the last three, those for a free buffer), a
  * negative value restores the default of 2^31 (about one second).  A wait that gives up makes its CTA wait for the copies it already
  * issued (always with the default limit), record a timeout and return;
- * gp_synchronize then reports GP_ERR_TIMEOUT.  Other kernels:
+ * gp_synchronize then reports GP_ERR_TIMEOUT.  (gp_sparse_attention leaves a row and head
+ * whose blocks were not all attended to as it was.)  Other kernels:
  * GP_ERR_UNSUPPORTED.  Host only; for tests of the timeout path.
  * gp_debug_fail_next_launch: the next launch of `kernel` (GP_KERNEL_*) fails
  * without running, as a failed launch would (GP_ERR_CUDA); -1 clears it.

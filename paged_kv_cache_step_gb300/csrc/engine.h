@@ -153,6 +153,7 @@ struct gp_ctx {
   long long wait_limit_evict = gp::kDefaultWaitLimit;
   long long wait_limit_chunk = gp::kDefaultWaitLimit;
   long long wait_limit_weights = gp::kDefaultWaitLimit;
+  long long wait_limit_sparse = gp::kDefaultWaitLimit;
   int inject_fail = -1;
 };
 

@@ -1176,6 +1176,8 @@ gp_status gp_debug_set_wait_limit(gp_ctx* c, int32_t kernel, int64_t cycles) {
     c->wait_limit_chunk = v;
   } else if (kernel == GP_KERNEL_WEIGHTS) {
     c->wait_limit_weights = v;
+  } else if (kernel == GP_KERNEL_SPARSE) {
+    c->wait_limit_sparse = v;
   } else {
     return fail(c, GP_ERR_UNSUPPORTED, "kernel %d has no settable wait limit", kernel);
   }

@@ -204,7 +204,8 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
     int s = 0;
     for (; s < stages; ++s) {
       const int slot = s % NST;
-      if (s >= NST) ok = __all_sync(0xffffffffu, wait_phase(empty(slot), (uint32_t)((s / NST - 1) & 1), abort));
+      if (s >= NST)
+        ok = a.wait_limit != 0 && __all_sync(0xffffffffu, wait_phase(empty(slot), (uint32_t)((s / NST - 1) & 1), abort, a.wait_limit));
       if (!ok) break;
       const int have = min(boxes, all - s * boxes);
       if (lane == 0) mbar_expect_tx(full(slot), (uint32_t)(have * box * D * 4));
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
     const uint32_t vrow = (uint32_t)(16 * warp + (lane >> 3 & 1) * 8 + xr) * 128u, vc = (uint32_t)(lane >> 4);
     for (int s = 0; s < stages; ++s) {
       const int slot = s % NST;
-      ok = __all_sync(0xffffffffu, wait_phase(full(slot), (uint32_t)((s / NST) & 1), abort));
+      ok = __all_sync(0xffffffffu, wait_phase(full(slot), (uint32_t)((s / NST) & 1), abort, a.wait_limit));
       if (!ok) break;
       const int e = s * boxes + (16 * warp >> lx);
       const int y = e < all ? list[e >> lof].y : 0;
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
     part[r * (D + 2) + d] = y;
     if (d == 0) {
       part[r * (D + 2) + D] = top;
-      part[r * (D + 2) + D + 1] = sum;
+      part[r * (D + 2) + D + 1] = abort_s ? -1.f : sum;  // (a sum is never negative)
     }
   }
   auto meet = [&] {
@@ -383,13 +384,16 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_mma(const __grid_constant__ Sp
     if (!(live >> (r / G) & 1u)) continue;
     const float* at = part + r * (D + 2);
     float top = NEG, y0 = 0.f, y1 = 0.f, sum = 0.f;
+    bool whole = true;
     for (int c = 0; c < C; ++c) top = fmaxf(top, of(c, at + D));
     for (int c = 0; c < C; ++c) {
-      const float f = ex2f(of(c, at + D) - top);
+      const float f = ex2f(of(c, at + D) - top), lc = of(c, at + D + 1);
       y0 = fmaf(of(c, at + d), f, y0);
       y1 = fmaf(of(c, at + d + 1), f, y1);
-      sum = fmaf(of(c, at + D + 1), f, sum);
+      sum = fmaf(lc, f, sum);
+      whole = whole && !(lc < 0.f);
     }
+    if (!whole) continue;  // a CTA gave up: the row stays as it was
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + ((row0 + r / G) * a.Hq + h * G + r % G) * D + d) =
         pack2(y0 * inv, y1 * inv);

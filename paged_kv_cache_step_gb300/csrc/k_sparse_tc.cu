@@ -28,7 +28,7 @@
 // for 473 GFLOP, 75 % of the measured bf16 rate; row by row in k_sparse_mma.cu 1094 us.  A CTA alone
 // takes 1300 clocks a stage, its start 8500 (lists, pages), its outputs 3000.
 // Every wait is bounded: on expiry the CTA records ERR_TIMEOUT, waits for what it
-// has in flight, frees its TMEM and returns.
+// has in flight, frees its TMEM and returns; rows that it has part in stay as they were.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -175,7 +175,9 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
     int c = 0;  // tiles issued
     auto load = [&](const CUtensorMap* map, int s) {
       const int slot = c % NST;
-      if (c >= NST) ok = ok && __all_sync(0xffffffffu, wait_phase(empty(slot), (uint32_t)((c / NST - 1) & 1), abort));
+      if (c >= NST)
+        ok = ok && a.wait_limit != 0 &&
+             __all_sync(0xffffffffu, wait_phase(empty(slot), (uint32_t)((c / NST - 1) & 1), abort, a.wait_limit));
       if (!ok) return;
       const int have = min(boxes, all - s * boxes);
       if (lane == 0) mbar_expect_tx(full(slot), (uint32_t)(have * box * D * 2));
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
     // ---- products ----
     tc_fence_after();
     auto wait = [&](uint32_t bar, int phase) {
-      ok = ok && __all_sync(0xffffffffu, wait_phase(bar, (uint32_t)(phase & 1), abort));
+      ok = ok && __all_sync(0xffffffffu, wait_phase(bar, (uint32_t)(phase & 1), abort, a.wait_limit));
     };
     int c = 0;  // tiles used
     auto tile = [&] { return sb + (uint32_t)(c % NST * L::TILE); };
@@ -238,7 +240,11 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
       commit(empty(c++ % NST));
       if (s + 2 < stages) score(s + 2);  // over P, which the products before it have read
     }
-    if (!ok && lane == 0) timed_out();
+    if (!ok) {
+      if (lane == 0) timed_out();
+      __threadfence_block();  // the others see it before mma_done
+      __syncwarp();
+    }
     // every product issued has completed before TMEM is released (bounded)
     commit(mma_done);
     drain_phase(mma_done, 0u);
@@ -265,7 +271,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
         }
       }
       const uint32_t my_s = ts + lanes + (uint32_t)(64 * (s & 1));
-      ok = __all_sync(0xffffffffu, wait_phase(s_ready(s), (uint32_t)(s >> 1 & 1), abort));
+      ok = __all_sync(0xffffffffu, wait_phase(s_ready(s), (uint32_t)(s >> 1 & 1), abort, a.wait_limit));
       if (!ok) break;
       tc_fence_after();
       uint32_t r[2][32];
@@ -304,7 +310,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
         if (__any_sync(0xffffffffu, grow)) {
           // O is at rest once the products with the last P have completed (those before
           // it completed before this S)
-          ok = __all_sync(0xffffffffu, wait_phase(o_done, (uint32_t)((s - 1) & 1), abort));
+          ok = __all_sync(0xffffffffu, wait_phase(o_done, (uint32_t)((s - 1) & 1), abort, a.wait_limit));
           if (!ok) break;
           tc_fence_after();
           const float mn = grow ? top : m, f = ex2f(m - mn);
@@ -344,7 +350,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       if (tail) {  // weight 0 times any bits is not 0: those rows of V are cleared
         const int c = 2 * stages - 1, slot = c % NST, key = tid >> 1;  // the last tile
-        ok = __all_sync(0xffffffffu, wait_phase(full(slot), (uint32_t)((c / NST) & 1), abort));
+        ok = __all_sync(0xffffffffu, wait_phase(full(slot), (uint32_t)((c / NST) & 1), abort, a.wait_limit));
         if (!ok) break;
         const int e = s * boxes + (key >> lx);
         if (e >= all || slot_of(e) + (key & (box - 1)) > last_at) {
@@ -361,7 +367,8 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
       __syncwarp();
       if (lane == 0) mbar_arrive(p_ready(s));
     }
-    if (ok) ok = __all_sync(0xffffffffu, wait_phase(mma_done, 0u, abort));  // (o_done may be two stages behind)
+    // (o_done may be two stages behind; products that were given up are done too)
+    if (ok) ok = __all_sync(0xffffffffu, wait_phase(mma_done, 0u, abort, a.wait_limit) && !*abort);
     if (ok) {
       tc_fence_after();
       const float inv = C > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
@@ -405,6 +412,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
   __syncthreads();
   if (C > 1) {
     // ---- the shares joined: a warp a row, each CTA its rows ----
+    if (abort_s && tid < 128) ml_s[tid] = make_float2(NEG, -1.f);  // (a sum is never negative)
     asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     auto there = [&](const void* x, int r) {  // *x of CTA r of the cluster
@@ -415,6 +423,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
     for (int x = rank + C * warp; x < m_rows * G; x += C * (NT / 32)) {
       if (!live_s[x / G]) continue;
       float top = NEG, sum = 0.f, y[D / 32];
+      bool whole = true;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) y[i] = 0.f;
       for (int r = 0; r < C; ++r) {
@@ -423,6 +432,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
         const float mn = fmaxf(top, mr), f = ex2f(top - mn), g = ex2f(mr - mn);
         top = mn;
         sum = sum * f + lr * g;
+        whole = whole && !(lr < 0.f);
         const uint32_t at0 = there(sm + ((size_t)x * (D + 4) + lane * (D / 32)) * 4, r);
         float v[D / 32];
         if constexpr (D == 128) {
@@ -433,6 +443,7 @@ __global__ void __launch_bounds__(NT, 2) k_sparse_tc(const __grid_constant__ Spa
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) y[i] = y[i] * f + v[i] * g;
       }
+      if (!whole) continue;  // a CTA gave up
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + ((row0 + x / G) * a.Hq + h * G + x % G) * D) +
                       lane * (D / 64);

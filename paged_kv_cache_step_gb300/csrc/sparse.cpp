@@ -385,6 +385,7 @@ gp_status gp_sparse_attention(gp_ctx* c, int32_t layer, const gp_step* s, int32_
   a.q = q_rot_dev;
   a.blocks = blocks_dev;
   a.out = out_dev;
+  a.wait_limit = c->wait_limit_sparse;
   const bool tc = c->attn_tc_ok && c->scan_kernel != GP_SCAN_CUDA_CORE && g.q_dtype == GP_DTYPE_BF16;
   if (c->scan_kernel == GP_SCAN_TENSOR_CORE && !tc)
     return fail(c, GP_ERR_UNSUPPORTED, "the tensor-core kernels cannot take this cache or query type");

@@ -90,6 +90,7 @@ struct SparseArgs {
   const int32_t* blocks;     // [max_rows][Hkv][top]
   void* out;                 // [max_rows][Hq][D], q's type
   int splits;                // CTAs of a cluster that share the blocks of a row or piece
+  long long wait_limit;      // clock cycles a wait may take before the CTA gives up
 };
 
 cudaError_t launch_tables(const TablesArgs& a, cudaStream_t s);

@@ -10,19 +10,20 @@
 namespace gp {
 
 // Bounded wait for a phase of an mbarrier; gives up when the limit passes or *abort
-// is set.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const volatile int* abort) {
+// is set.  (A try may itself wait for a while; a limit of 0 is looked at by the warp that
+// loads, before it tries for a free buffer.)
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const volatile int* abort, long long limit) {
   if (tc::mbar_try(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
-    if (*abort || clock64() - t0 > kDefaultWaitLimit) return false;
+    if (*abort || clock64() - t0 > limit) return false;
     if (tc::mbar_try(bar, parity)) return true;
   }
 }
 // The same for what a role has in flight before it ends: whatever *abort says.
 __device__ __forceinline__ void drain_phase(uint32_t bar, uint32_t parity) {
   const int zero = 0;
-  wait_phase(bar, parity, &zero);
+  wait_phase(bar, parity, &zero, kDefaultWaitLimit);
 }
 
 // The lists of a piece's rows: every warp of the CTA takes each WARPS-th row, its loads

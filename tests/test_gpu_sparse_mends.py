@@ -1,5 +1,6 @@
 """What earlier tests of the calls over a step's device arrays do not show: not-a-number
-queries, and one rule for the rows that are left out, in every kernel."""
+queries, one rule for the rows that are left out, and waits that run out, in every
+kernel.  The engine, the formulas in 64 bits and the tolerances are test_gpu_sparse.py's."""
 
 import math
 
@@ -169,3 +170,41 @@ def test_rows_behind_the_last_are_not_looked_at(new):
                 check_rows(e, (), False, put("row_req", slice(2 * new, None), value))
             finally:
                 e.close()
+
+
+# One request or many: with and without clusters; a row each, or pieces of 128 / G rows.
+# Every share is longer than the ring of buffers.
+@pytest.mark.parametrize("cached,new,top", [([60_000], [1], 400), ([9000] * 80, [1] * 80, 40), ([12_000], [40], 150), ([4000] * 40, [70] * 40, 20)])
+@pytest.mark.parametrize("shape", ["bf16_g4_d128", "bf16_g2_d64"])
+def test_waits_that_give_up_are_reported(shape, cached, new, top):
+    """Without patience every CTA stops with copies and products in flight; with a little
+    some may.  A row and head is right or as it was, and the next call is right."""
+    s = SHAPES[shape]
+    e = Engine(cached, new, L=1, layer=0, seed=top, **dict(s, hq=4 * s["hq"] // s["hkv"], hkv=4) if len(new) > 1 else s)
+    e.block = 64
+    try:
+        e.fill()
+        rng = np.random.default_rng(top)
+        lists = [[np.sort(rng.permutation((e.cached[r] + t) // 64 + 1)[:top]) for _ in range(e.hkv)]
+                 for r in range(len(new)) for t in range(new[r])]
+        blocks = packed(e, lists, top)
+        q = e.randn(e.rows, e.hq, e.d).bfloat16()
+        want, tol = attention_reference(e, q, lists)
+        gave_up = 0
+        for limit in (0, 1, 300, 3000, 30_000, 0, -1):
+            gp.gp_debug_set_wait_limit(e.ctx, gp.GP_KERNEL_SPARSE, limit)
+            out = torch.full_like(q, 7.0)
+            gp.gp_sparse_attention(e.ctx, 0, e.step, 64, top, q, blocks, out)
+            try:
+                gp.gp_synchronize(e.ctx)
+                assert limit != 0
+            except gp.GrowPageError as err:
+                assert err.status == gp.GP_ERR_TIMEOUT and limit >= 0
+            right = ((out.double() - want).abs() <= tol).all(-1)
+            left = (out == 7.0).all(-1)
+            assert torch.all(right | left)
+            assert limit >= 0 or right.all()
+            gave_up += int(left.any())
+        assert gave_up >= 2
+    finally:
+        e.close()
