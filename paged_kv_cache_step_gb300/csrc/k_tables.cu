@@ -85,9 +85,9 @@ __global__ void __launch_bounds__(1024, 1) k_tables(const __grid_constant__ Tabl
       s = a.slots[r];
       c = a.cached[r];
       const int m = a.fresh[r];
-      if (s >= 0 && s < a.M && !(twice[s >> 5] >> (s & 31) & 1)) {
+      if (s >= 0 && s < a.M) {
         have = a.held[s];
-        if (c >= 0 && m >= 0 && (int64_t)c + m <= (int64_t)a.maxp * PAGE && have <= a.maxp && have >= (c + PAGE - 1) / PAGE) {
+        if (!(twice[s >> 5] >> (s & 31) & 1) && c >= 0 && m >= 0 && (int64_t)c + m <= (int64_t)a.maxp * PAGE && have <= a.maxp && have >= (c + PAGE - 1) / PAGE) {
           state = GIVEN;
           fresh = m;
           need = (c + m + PAGE - 1) / PAGE;
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(1024, 1) k_tables(const __grid_constant__ Tabl
     a.row0[r] = row0[r];
     const int taken = (r + 1 < a.n ? first[r + 1] : pages) - first[r];
     const int s = slots[r];
-    if (s >= 0 && s < a.M && !(twice[s >> 5] >> (s & 31) & 1)) {
+    if (s >= 0 && s < a.M) {  // (one that is listed twice keeps its pages: the same number twice)
       a.num_pages[s] = held[r] + taken;
       for (int j = 0; j < taken; ++j) a.tables[(size_t)s * a.maxp + held[r] + j] = a.free_pages[before + first[r] + j];
     }

@@ -9,8 +9,8 @@ import pytest
 import torch
 
 import paged_kv_cache_step_gb300 as gp
-from test_gpu_sparse import CUDA, DT, PAGE, SHAPES, Engine, attention_reference, bounds_arrays, bounds_reference, i32, kernels, \
-    random_lists, select_reference
+from test_gpu_sparse import (CUDA, DT, PAGE, SHAPES, Engine, Tables, attention_reference, bounds_arrays, bounds_reference, i32,
+                             kernels, random_lists, select_reference)
 
 pytestmark = pytest.mark.gpu
 
@@ -208,3 +208,19 @@ def test_waits_that_give_up_are_reported(shape, cached, new, top):
         assert gave_up >= 2
     finally:
         e.close()
+
+
+@pytest.mark.parametrize("n", [4, 300])
+def test_pages_of_a_slot_that_is_listed_twice(n):
+    """num_pages_dev, a buffer of its own, gets the pages of every listed slot, of refused ones too."""
+    slots = np.arange(n)
+    slots[[1, n - 1]] = 0, 2  # slots 0 and 2 twice
+    held = np.arange(n + 3) % 3 + 1
+    t = Tables([5] * n, [1] * n, 2 * n, 5, slots=slots, M=n + 3, held=held, seed=n)
+    gp.gp_synchronize(t.ctx)
+    t.num_pages = torch.full_like(t.held, -9)
+    t.taken.zero_()
+    gp.gp_build_tables(t.ctx, gp.Step(t.ctx, **t.a), t.held, t.num_pages, t.free, None, t.taken, t.state)
+    t.want["num_pages"] = np.where(np.isin(np.arange(n + 3), slots), held, -9)
+    assert (t.want["state"][[0, 1, 2, n - 1]] == gp.GP_STEP_INVALID).all()
+    t.check()
