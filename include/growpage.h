@@ -539,7 +539,7 @@ typedef struct gp_step {
 typedef enum {
   GP_STEP_GIVEN = 0,    /* its rows are in the step */
   GP_STEP_NO_PAGES = 1, /* the free list has too few pages */
-  GP_STEP_NO_ROWS = 2,  /* its rows do not fit behind those before it */
+  GP_STEP_NO_ROWS = 2,  /* its rows do not fit behind those that the valid requests before it ask for */
   GP_STEP_INVALID = 3   /* slot out of range or listed twice, a negative length, more tokens
                            than max_pages_per_req pages, or cached ones without a page */
 } gp_step_state;
@@ -548,9 +548,12 @@ typedef enum {
  * Request i with slot s holds held[s] pages; it needs ceil((num_cached[i] +
  * num_new[i]) / 256) and takes the ones missing from free_dev, behind those taken
  * by the requests before it.  A request whose rows or pages do not fit
- * has no row in this step, takes no page and keeps its table; those after it are
- * still given what fits.  (Pages: once the list is too short for a request, no
- * later one takes any.)  free_dev: int32 [num_free], pages that the caller took with
+ * has no row in this step, takes no page and keeps its table.  Both are given in
+ * order, and none is passed over.  Rows: the new tokens of all valid requests are added
+ * up, those of refused ones among them, and from where the sum passes max_rows no
+ * request with new tokens has a row.  Pages: from where the missing ones of the requests
+ * whose rows fit pass the list, no request takes any; later ones that need none still
+ * have their rows.  free_dev: int32 [num_free], pages that the caller took with
  * gp_page_alloc, each listed once, of which the first taken_in[0] (NULL: none) are
  * used up; taken_dev: int32 [1] gets the count after the call, and may be
  * taken_in.  held_dev: int32 [max_slots]; num_pages_dev: int32 [max_slots] gets the

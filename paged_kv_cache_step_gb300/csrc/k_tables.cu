@@ -3,8 +3,8 @@
 //
 //   need_r  = ceil((cached_r + new_r) / 256) pages, take_r = max(0, need_r - held_r)
 //   a request is given its rows and pages if it is valid, its rows fit the
-//   buffers behind those of the requests before it, and the free list holds its
-//   pages behind theirs; else it has no row in this step and keeps its table
+//   buffers behind those that the valid requests before it ask for (given or not: a
+//   plain running sum), and the free list holds its pages behind theirs; else it has no row in this step and keeps its table
 //   row0  = running sum of the given rows
 //   row i of request r: logical slot t = cached_r + i, page table[t / 256] or, for
 //   t / 256 >= held_r, free[taken + (pages given before) + t / 256 - held_r]

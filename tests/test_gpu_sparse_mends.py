@@ -224,3 +224,38 @@ def test_pages_of_a_slot_that_is_listed_twice(n):
     t.want["num_pages"] = np.where(np.isin(np.arange(n + 3), slots), held, -9)
     assert (t.want["state"][[0, 1, 2, n - 1]] == gp.GP_STEP_INVALID).all()
     t.check()
+
+
+@pytest.mark.parametrize("new,rows,free,states", [
+    ([3, 300, 1, 0], 4, 9, [0, 2, 2, 0]),    # 303 rows asked for before the third: it has none, though one is left
+    ([3, 300, 1, 0], 304, 9, [0, 0, 0, 0]),
+    ([300, 3, 1], 304, 1, [1, 1, 1]),        # two pages missing, one left: no later request takes it
+    ([300, 3, 1], 303, 9, [0, 0, 2]),
+    ([300, 200, 1], 400, 1, [1, 2, 2])])     # rows of a request refused for its pages count
+def test_rows_and_pages_are_given_in_order(new, rows, free, states):
+    t = Tables([0] * len(new), new, rows, free, held=[0] * (len(new) + 3), seed=1)
+    gp.gp_synchronize(t.ctx)
+    assert t.state.tolist() == states
+    t.check()
+
+
+def test_pages_go_back_to_the_pool():
+    """What the table on the device names comes back through the host: a request's entries, one
+    gp_page_unref each."""
+    e = Engine([0, 0], [700, 20], L=1, layer=0, cap=4, spare=3)
+    try:
+        pages = [gp.gp_page_alloc(e.ctx) for _ in range(e.pool)]
+        held, taken, state = (torch.zeros(k, dtype=torch.int32, **CUDA) for k in (e.M, 1, 2))
+        gp.gp_build_tables(e.ctx, e.step, held, held, i32(pages), taken, taken, state)
+        gp.gp_synchronize(e.ctx)
+        assert gp.gp_free_page_count(e.ctx) == 0
+        tables, counts = e.arrays["tables"].cpu().numpy(), held.cpu().numpy()
+        for s in e.slots:
+            for page in tables[s, :counts[s]]:
+                gp.gp_page_unref(e.ctx, int(page))
+        assert gp.gp_free_page_count(e.ctx) == 4 and taken.tolist() == [4]
+        for page in pages[4:]:
+            gp.gp_page_unref(e.ctx, page)
+        assert gp.gp_free_page_count(e.ctx) == e.pool
+    finally:
+        e.close()
