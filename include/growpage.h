@@ -511,7 +511,11 @@ gp_status gp_evict_weighted(gp_ctx* ctx, int32_t n, gp_request* reqs, const int3
  * num_cached, tables, row0 and row_req.  A caller may fill them by other means.
  *   n          requests, at most max_slots and 4096
  *   max_rows   rows that the step's buffers have room for (new tokens of all
- *              requests together)
+ *              requests together).  The host knows no other count: launches are
+ *              sized by it, and gp_select_blocks (above 8 rows a request) and
+ *              gp_sparse_attention (above 16 Hkv / Hq) take the kernels for prompts
+ *              by it.  A step of single tokens is faster with room for its rows alone:
+ *              a gp_step of its own, over the same arrays
  *   slots      int32 [n], the requests' slots (gp_slot_acquire), listed once
  *   num_cached int32 [n], tokens in the cache before the step
  *   num_new    int32 [n], tokens of the step
@@ -559,7 +563,12 @@ typedef enum {
  * taken_in.  held_dev: int32 [max_slots]; num_pages_dev: int32 [max_slots] gets the
  * pages of the listed slots after the call, and may be held_dev: a call repeated
  * over the same lengths then takes nothing.  state_dev: int32 [n], gp_step_state,
- * apart from the inputs. */
+ * apart from the inputs.
+ * Which pages a request was given, only its row of tables tells.  When it ends, or
+ * before a call that takes a host table (Compress & Hold, an eviction), the caller copies
+ * that row back, num_pages_dev[slot] entries of it: one gp_page_unref each, or the
+ * gp_request's block_table, whose row on the device is written again after a call that
+ * changes it. */
 gp_status gp_build_tables(gp_ctx* ctx, const gp_step* step, const int32_t* held_dev, int32_t* num_pages_dev,
                           const int32_t* free_dev, int32_t num_free, const int32_t* taken_in_dev, int32_t* taken_dev,
                           int32_t* state_dev);

@@ -14,9 +14,10 @@
 // and makes it the one that rebuilds after an eviction too.
 //
 // A power of two of threads a (block, head), 16 bytes of a token each, eight loads in
-// flight where the block has that many.  Measured: 64 blocks of 64 tokens with 8 heads 8 us
-// (five dependent reads, from row0 to the keys), 13 621 tokens in blocks of 32 11 us, where
-// reading the keys takes 4.3 at the copy rate.
+// flight where the block has that many.  Measured: 64 blocks of 64 tokens with 8 heads 8.1 us
+// (four dependent reads, from row0 to the keys; 5.2 us with the keys in L2), 13 734 tokens in
+// blocks of 32 11 us (7.2 us), where reading the keys takes 4.3 at the copy rate: every CTA goes
+// through that chain for one block, with nothing else in flight.
 #include <cuda_bf16.h>
 
 #include <cstdint>

@@ -16,7 +16,7 @@
 // one rounding to the query's type at the end.  Six requests of 3 to 5 rows, d = 64, fp32, 24 blocks
 // of 16: 6.2 us in a graph.  64 requests of 2048 listed tokens,
 // 32 + 8 heads, d = 128, fp32: 240 us, 66 % of the copy rate; with registers for one CTA an SM
-// (147 instead of 128) 402 us: the loads of two hide each other's sums.
+// (147; of 128, G = 4 spills 24 bytes a thread) 402 us: the loads of two hide each other's sums.
 #include <cuda_bf16.h>
 
 #include <cstdint>

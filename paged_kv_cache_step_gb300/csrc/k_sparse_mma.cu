@@ -20,7 +20,9 @@
 //
 // Measured (32 + 8 heads, d = 128, 32 blocks of 64): a decode step of 64 requests 88 us, 89 % of the
 // copy rate (433 us on the CUDA cores); one request with 64 blocks 12.1 us, 8 of them from
-// start to end of a CTA.  A stage takes a CTA alone 1200 clocks, two on an SM 2300: memory.
+// start to end of a CTA.  Two CTAs share an SM while a launch takes up to 115 KB of
+// shared memory (d = 128: 110 KB with blocks of 64; 121 KB with G = 2, 256 pages and blocks
+// of 16, where one fits).  A stage takes a CTA alone 1200 clocks, two on an SM 2300: memory.
 #include <cuda_bf16.h>
 
 #include <cstdint>

@@ -15,7 +15,8 @@
 //                    more than 24: O is then rescaled in TMEM
 //   O += P V         128 x d, both parts, V MN-major as TMA left it
 // A CTA holds 256 of the 512 columns of TMEM (O d, S and P twice 64) and half of
-// the shared memory, so that two CTAs share an SM: one's softmax runs beside the
+// the shared memory (101 to 115 KB with blocks of 64 and more, d = 128; 125 KB with 256
+// pages in blocks of 16, G = 4, where one CTA fits), so that two CTAs share an SM: one's softmax runs beside the
 // other's products, and one's start beside the other's work.  The products are
 // issued as S0 S1 O0 S2 O1 S3 ..., so that a CTA's softmax finds the next S done; K and
 // V come through one ring in that order.

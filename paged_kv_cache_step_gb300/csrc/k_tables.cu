@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(1024, 1) k_tables(const __grid_constant__ Tabl
 cudaError_t launch_tables(const TablesArgs& a, cudaStream_t s) {
   // Buffers of their own for what is read and written need no meeting: blocks of 512
   // threads, one for 1024 rows.  Else a cluster, which 16 blocks are the most of.
-  // 42 000 rows of 300 requests: 45, 26, 15, 10.3 and 7.5 us with 1, 2, 4, 8 and 16 blocks
+  // 43 943 rows of 300 requests: 45, 26, 15, 10.3 and 7.5 us with 1, 2, 4, 8 and 16 blocks
   // of 1024 threads in a cluster, 5.1 us with 43 blocks apart.
   const bool small = a.n <= 256 && a.max_rows <= 512, large = !small && !a.apart && a.max_rows > 16384;
   const size_t smem = sizeof(int) * ((size_t)5 * a.n + 1 + 2 * ((size_t)(a.M + 31) / 32));

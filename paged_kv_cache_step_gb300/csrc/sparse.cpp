@@ -345,7 +345,8 @@ gp_status gp_select_blocks(gp_ctx* c, int32_t layer, const gp_step* s, int32_t b
   const int64_t tiles = std::min<int64_t>(sparse_pieces(a.s, a.rows), s->max_rows) * g.num_kv_heads;
   a.splits = 1;
   // Clusters share the blocks of tiles of 8 rows while all of their CTAs find a place at once
-  // (four an SM) and each has 64 blocks.  Decode steps of 4, 16, 32 and 64 requests of up to 125
+  // (four an SM: scores of up to 1600 blocks a row; of 4096, 256 pages in blocks of 16, one)
+  // and each has 64 blocks.  Decode steps of 4, 16, 32 and 64 requests of up to 125
   // pages: 11.5, 12.4, 13.0 and 14.5 us without, 8.7, 9.5, 11.3 and 17.8 us shared by 4, 4, 2 and 2.
   // Tiles of 16 rows have work enough for a CTA: 300 rows 10.8 us, shared by two 13.8.
   while (a.rows == 8 && a.splits < 8 && (a.splits + 1) * tiles <= 4 * c->sms && blocks >= 64 * (a.splits + 1)) ++a.splits;
@@ -390,7 +391,9 @@ gp_status gp_sparse_attention(gp_ctx* c, int32_t layer, const gp_step* s, int32_
   if (c->scan_kernel == GP_SCAN_TENSOR_CORE && !tc)
     return fail(c, GP_ERR_UNSUPPORTED, "the tensor-core kernels cannot take this cache or query type");
   // Clusters share the blocks of a piece while all of their CTAs find a place at once
-  // (two an SM) and a share keeps 64 tokens.  One long request, 64 blocks of 64: 46, 28, 19 and
+  // (two an SM: shared memory has room for two of up to 115 KB, bitmaps and lists by
+  // max_pages_per_req among them; above that, d = 128 with blocks of 16 or 32 and long
+  // tables, one) and a share keeps 64 tokens.  One long request, 64 blocks of 64: 46, 28, 19 and
   // 14.7 us at 1, 2, 4 and 8; 16 requests 31, 29, 37 and 52; 64 requests 90, 104, 120 and 175.
   const int64_t tokens = (int64_t)std::min(top, g.max_pages_per_req * (kPage / block)) * block;
   auto share = [&](int64_t pieces, int most) {
