@@ -646,7 +646,7 @@ gp_status gp_block_bounds(gp_ctx* ctx, int32_t layer, const gp_step* step, int32
  * A row in block b attends to blocks of [0, b]: all of them if they are `top` or
  * fewer, else the first `sink`, the last `recent` >= 1, and of the others those of
  * largest score (equal scores: the lower block), `top` >= sink + recent in all.
- * The arithmetic is exact.  q_rot_dev: [max_rows][Hq][d] q_dtype, 16-byte aligned,
+ * The arithmetic is exact; a NaN in a query counts as 0.  q_rot_dev: [max_rows][Hq][d] q_dtype, 16-byte aligned,
  * as gp_append_mapped gives it; blocks_dev: int32 [max_rows][Hkv][top], ascending,
  * then -1. */
 gp_status gp_select_blocks(gp_ctx* ctx, int32_t layer, const gp_step* step, int32_t block, int32_t top, int32_t sink,

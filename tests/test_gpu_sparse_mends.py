@@ -9,8 +9,8 @@ import pytest
 import torch
 
 import paged_kv_cache_step_gb300 as gp
-from test_gpu_sparse import (CUDA, DT, PAGE, SHAPES, Engine, Tables, attention_reference, bounds_arrays, bounds_reference, i32,
-                             kernels, random_lists, select_reference)
+from test_gpu_sparse import (CUDA, DT, PAGE, SHAPES, Engine, Tables, attention_reference, bits, bounds_arrays, bounds_reference,
+                             i32, kernels, random_lists, select_reference)
 
 pytestmark = pytest.mark.gpu
 
@@ -259,3 +259,74 @@ def test_pages_go_back_to_the_pool():
         assert gp.gp_free_page_count(e.ctx) == e.pool
     finally:
         e.close()
+
+
+def test_two_graphs_of_one_engine_at_once():
+    """Graphs share the caller's buffers alone: two of one engine, of a decode step and of a
+    prompt, replayed on two streams at the same time, give what each gives by itself."""
+    stream, other = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        e = Engine([2000, 900, 30], [300, 1, 1], L=1, layer=0, seed=40, stream=stream)
+        e.fill()
+        small = gp.Step(e.ctx, **dict(e.arrays, row0=i32([0, 0, 1, 2]), row_req=i32([1, 2]), slot_map=e.arrays["slot_map"][300:].clone(),
+                                      positions=e.arrays["positions"][300:].clone()))
+        runs = []
+        for step, rows in ((e.step, 302), (small, 2)):
+            q, out = e.randn(rows, 8, 128).bfloat16(), torch.zeros(rows, 8, 128, dtype=torch.bfloat16, **CUDA)
+            blocks = torch.full((rows, 2, 9), -1, dtype=torch.int32, **CUDA)
+            runs.append((step, q, blocks, out, *bounds_arrays(e, 32)))
+        whole = gp.Step(e.ctx, **dict(e.arrays, num_cached=i32([0, 0, 0]), row0=i32([0, 2300, 3201, 3232]),
+                                      row_req=i32(np.repeat([0, 1, 2], [2300, 901, 31])),
+                                      slot_map=torch.zeros(3232, dtype=torch.int64, **CUDA), positions=torch.zeros(3232, dtype=torch.int64, **CUDA)))
+        for x in runs:
+            gp.gp_block_bounds(e.ctx, 0, whole, 32, x[4], x[5])
+
+        def calls(step, q, blocks, out, bounds, scales):
+            for _ in range(8):
+                gp.gp_block_bounds(e.ctx, 0, step, 32, bounds, scales)
+                gp.gp_select_blocks(e.ctx, 0, step, 32, 9, 1, 2, q, bounds, scales, blocks)
+                gp.gp_sparse_attention(e.ctx, 0, step, 32, 9, q, blocks, out)
+
+        graphs, alone = [], []
+        for x in runs:
+            calls(*x)
+            stream.synchronize()
+            alone.append([t.clone() for t in x[2:]])
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=stream):
+                calls(*x)
+        for x, want in zip(runs, alone):
+            lists = [[h[h >= 0] for h in row] for row in x[2].cpu().numpy()]
+            e.block, first = 32, 302 - len(lists)
+            ref, tol = attention_reference(e, torch.cat([torch.zeros(first, 8, 128, **CUDA).bfloat16(), x[1]]), [[[], []]] * first + lists)
+            assert torch.all((want[1].double() - ref[first:]).abs() <= tol[first:])
+    for _ in range(20):
+        for x in runs:
+            x[2].fill_(-3)
+            x[3].zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            graphs[0].replay()
+        with torch.cuda.stream(other):
+            for _ in range(6):
+                graphs[1].replay()
+        torch.cuda.synchronize()
+        for x, want in zip(runs, alone):
+            assert all(torch.equal(bits(a) if a.is_floating_point() else a, bits(b) if b.is_floating_point() else b)
+                       for a, b in zip(x[2:], want))
+    gp.gp_synchronize(e.ctx)
+    del graphs
+    e.close()
+
+
+@pytest.mark.parametrize("new", [[1] * 9, [1, 300, 1, 0, 5]])
+@pytest.mark.parametrize("shape", ["bf16_g4_d128", "bf16_g2_d64", "f32_g2_d64"])
+def test_room_for_many_more_rows(shape, new):
+    """Buffers of 3000 rows for a step of few: the same rows right, the others as they were."""
+    for kernel in kernels(shape):
+        e = Engine([900, 40, 3000, 255, 256, 7, 0, 513, 64][:len(new)], new, pad=3000, seed=len(new), kernel=kernel, **SHAPES[shape])
+        try:
+            e.fill()
+            check_rows(e, (), False, lambda e: None)
+        finally:
+            e.close()
